@@ -30,6 +30,8 @@ LIB_PATH = os.path.join(HERE, "libstreamkl.so")
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_SCRATCH_LIMIT = range(7)
 BWD_AUTO, BWD_FUSED, BWD_SEPARATE, BWD_DQ_ONLY, BWD_DK_ONLY = 0, 1, 2, 3, 4
 SPLITK_MAX_NQ = 16
+LOGPROBS_MAX_TOP_K = 32
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # streamkl_dtype
 
 
 class Shape(ctypes.Structure):
@@ -68,6 +70,8 @@ SIGNATURES = {
     "streamkl_bwd_mutual": (_I, [_P, _P, _P, _P, Shape, _F, _F, _F, _F, _P, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_bwd_mutual_select": (_I, [Shape, _SZ, _I]),
     "streamkl_bwd_mutual_workspace": (_I, [Shape, _I, ctypes.POINTER(_SZ)]),
+    "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
+    "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_check_device_status": (_I, [_S]),
     "streamkl_debug_wait_timeout": (_I, [_I, _S]),
@@ -391,6 +395,92 @@ def bwd_mutual(q1, k1, q2, k2, lse1, lse2, kl, g, scale=None, causal=False, bwd_
                                      nbytes.value, _stream(dev)),
            "streamkl_bwd_mutual")
     return _back((dq1, dk1, dq2, dk2), host)
+
+
+def _call(name, dev, *args):
+    """Calls a C entry point on `dev`'s current stream, with `dev` the current device while it runs."""
+    f = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(dev))
+    _check(st, name)
+
+
+def _logits_rows(logits, tokens):
+    """Validates logits [..., V] and tokens [...] or [..., T]; returns (device logits as strided [R, V] rows,
+    contiguous int64 device tokens [R, T] or None, T, was_host)."""
+    if logits.dtype not in DTYPES:
+        raise TypeError("logits must be bfloat16, float16 or float32")
+    if logits.dim() < 1 or logits.shape[-1] == 0:
+        raise ValueError("logits must be [..., V] with V > 0")
+    T = 0
+    if tokens is not None:
+        if tokens.dtype not in (torch.int64, torch.int32):
+            raise TypeError("tokens must be int64 or int32")
+        if tokens.shape == logits.shape[:-1]:
+            T = 1
+        elif tokens.dim() == logits.dim() and tokens.shape[:-1] == logits.shape[:-1]:
+            T = tokens.shape[-1]
+        else:
+            raise ValueError(f"tokens {tuple(tokens.shape)} do not fit logits {tuple(logits.shape)}")
+        if tokens.device != logits.device:
+            raise ValueError("inputs on different devices")
+    host = logits.device.type == "cpu"
+    if host:
+        logits = logits.to(torch.device("cuda", torch.cuda.current_device()), non_blocking=True)
+    V = logits.shape[-1]
+    x = logits.reshape(-1, V)
+    if (V > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < V):
+        x = x.contiguous()
+    if T:
+        tokens = tokens.to(device=x.device, dtype=torch.int64, non_blocking=True).contiguous()
+    return x, tokens if T else None, T, host
+
+
+def _row_stride(x):
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def logprobs_fwd(logits, tokens=None, scale=1.0, top_k=0):
+    """Log probabilities of given tokens: (logp, entropy, lse, top_logp, top_index).
+
+    logits: [..., V] bf16, fp16 or fp32, multiplied by scale > 0; tokens: [...] or [..., T], int64 or int32, a
+    negative one is no token (its logp is 0).  logp has the shape of tokens; entropy and lse are [...];
+    top_logp fp32 and top_index int64 are [..., top_k], the largest logits (equal ones: the lowest index first).
+    """
+    x, tok, T, host = _logits_rows(logits, tokens)
+    if not 0 <= top_k <= min(LOGPROBS_MAX_TOP_K, x.shape[1]):
+        raise ValueError(f"top_k must be between 0 and min({LOGPROBS_MAX_TOP_K}, V)")
+    lead, dev = logits.shape[:-1], x.device
+    logp = torch.empty(tokens.shape if tokens is not None else (*lead, 0), dtype=torch.float32, device=dev)
+    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+    lse = torch.empty(lead, dtype=torch.float32, device=dev)
+    top = torch.empty((*lead, top_k), dtype=torch.float32, device=dev)
+    idx = torch.empty((*lead, top_k), dtype=torch.int64, device=dev)
+    _call("streamkl_logprobs_fwd", dev, _ptr(x), DTYPES[x.dtype], x.shape[0], x.shape[1], _row_stride(x), _ptr(tok), T,
+          scale, top_k, _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(top), _ptr(idx))
+    return _back((logp, entropy, lse, top, idx), host)
+
+
+def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0):
+    """Gradient of the logits, contiguous and of their type, for upstream gradients g_logp (tokens' shape) and
+    g_entropy ([...] or None); lse and entropy are logprobs_fwd's (entropy may be None without g_entropy)."""
+    x, tok, T, host = _logits_rows(logits, tokens)
+    lead, dev = logits.shape[:-1], x.device
+    lse = _rows(lse, dev, lead, "lse")
+    g_entropy = _rows(g_entropy, dev, lead, "g_entropy")
+    if g_entropy is not None and entropy is None:
+        raise ValueError("g_entropy needs the forward's entropy")
+    entropy = _rows(entropy, dev, lead, "entropy") if g_entropy is not None else None
+    g_logp = _rows(g_logp, dev, tokens.shape, "g_logp") if T else None
+    if T and g_logp is None:
+        raise ValueError("tokens need g_logp")
+    out = torch.empty(logits.shape, dtype=x.dtype, device=dev)
+    _call("streamkl_logprobs_bwd", dev, _ptr(x), DTYPES[x.dtype], x.shape[0], x.shape[1], _row_stride(x), _ptr(tok), T,
+          scale, _ptr(lse), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(out), x.shape[1])
+    return _back((out,), host)[0]
 
 
 def check_device_status(device=None) -> int:

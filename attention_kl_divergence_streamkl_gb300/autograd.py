@@ -13,6 +13,7 @@ the reduction of the per-row values to a scalar happens in PyTorch.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -58,3 +59,34 @@ def attention_kl(q1, k1, q2, k2, scale=None, causal=False, reduction="mean", bwd
     if reduction not in ("mean", "sum", "none"):
         raise ValueError("reduction must be 'mean', 'sum' or 'none'")
     return _AttentionKL.apply(q1, k1, q2, k2, scale, causal, reduction, bwd_mode)
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, scale, top_k):
+        logp, entropy, lse, top_logp, top_index = _lib.logprobs_fwd(logits, tokens, scale, top_k)
+        ctx.save_for_backward(logits, tokens, lse, entropy)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(top_logp, top_index)
+        return logp, entropy, top_logp, top_index
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_logp, g_entropy, _top_logp, _top_index):
+        logits, tokens, lse, entropy = ctx.saved_tensors
+        if g_logp is None and g_entropy is None:
+            return None, None, None, None
+        given = tokens if g_logp is not None else None
+        return _lib.logprobs_bwd(logits, given, lse, entropy, g_logp, g_entropy, ctx.scale), None, None, None
+
+
+def token_logprobs(logits, tokens=None, scale=1.0, top_k=0):
+    """(logp, entropy, top_logp, top_index) of each row of logits, differentiable in logp and entropy.
+
+    The output-layer terms of a distillation loss: the log probabilities of the data's tokens (tokens [...]) or of
+    a teacher's alternatives (tokens [..., T], for example the teacher's top_index) under
+    softmax(scale * logits), the rows' entropy, and their own top_k alternatives, which have no gradient (give
+    them as tokens to train on them).  See logprobs_fwd for shapes, types and masked values.
+    """
+    return _TokenLogprobs.apply(logits, tokens, scale, top_k)

@@ -604,6 +604,58 @@ streamkl_status streamkl_bwd_mutual(const void* q1, const void* k1, const void* 
   return from_cuda(e != cudaSuccess ? e : launch_bwd_fused(p, 2, in, dq1, dk1, ws, range_tiles, status, st));
 }
 
+static streamkl_status logprobs_problem(int dtype, long long rows, long long vocab, long long row_stride,
+                                        int num_tokens, int top_k, float scale, LogprobsProblem* p) {
+  if (rows < 0 || vocab <= 0 || num_tokens < 0 || top_k < 0 || row_stride < vocab) return STREAMKL_ERR_INVALID;
+  if (!(scale > 0.f) || isinf(scale)) return STREAMKL_ERR_INVALID;
+  if (dtype != STREAMKL_BF16 && dtype != STREAMKL_FP16 && dtype != STREAMKL_FP32) return STREAMKL_ERR_INVALID;
+  if (top_k > vocab) return STREAMKL_ERR_INVALID;
+  // up to 8 blocks a row in one grid extent; columns and candidate keys are 32-bit
+  if (top_k > STREAMKL_LOGPROBS_MAX_TOP_K || vocab > kMaxRows || rows > 0x7fffffffLL / 8)
+    return STREAMKL_ERR_UNSUPPORTED;
+  *p = LogprobsProblem{rows, row_stride, (int)vocab, num_tokens, top_k, dtype, scale};
+  return STREAMKL_OK;
+}
+
+static bool aligned_to(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+streamkl_status streamkl_logprobs_fwd(const void* logits, int dtype, long long rows, long long vocab,
+                                      long long row_stride, const long long* tokens, int num_tokens, float scale,
+                                      int top_k, float* logp, float* entropy, float* lse, float* top_logp,
+                                      long long* top_index, void* stream) {
+  LogprobsProblem p;
+  streamkl_status v = logprobs_problem(dtype, rows, vocab, row_stride, num_tokens, top_k, scale, &p);
+  if (v != STREAMKL_OK || rows == 0) return v;
+  if (!aligned_to(logits, dtype == STREAMKL_FP32 ? 4 : 2) || !rows_ok(entropy) || !rows_ok(lse))
+    return STREAMKL_ERR_INVALID;
+  if (num_tokens && (!aligned_to(tokens, 8) || !rows_ok(logp))) return STREAMKL_ERR_INVALID;
+  if (top_k && (!rows_ok(top_logp) || !aligned_to(top_index, 8))) return STREAMKL_ERR_INVALID;
+  int sms = 0;
+  if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
+  return from_cuda(launch_logprobs_fwd(p, logits, tokens, logp, entropy, lse, top_logp, top_index, sms,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long rows, long long vocab,
+                                      long long row_stride, const long long* tokens, int num_tokens, float scale,
+                                      const float* lse, const float* entropy, const float* g_logp,
+                                      const float* g_entropy, void* dlogits, long long out_stride, void* stream) {
+  LogprobsProblem p;
+  streamkl_status v = logprobs_problem(dtype, rows, vocab, row_stride, num_tokens, 0, scale, &p);
+  if (v != STREAMKL_OK) return v;
+  if (out_stride < vocab) return STREAMKL_ERR_INVALID;
+  if (rows == 0) return STREAMKL_OK;
+  const uintptr_t size = dtype == STREAMKL_FP32 ? 4 : 2;
+  if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !rows_ok(lse)) return STREAMKL_ERR_INVALID;
+  if (num_tokens && (!aligned_to(tokens, 8) || !rows_ok(g_logp))) return STREAMKL_ERR_INVALID;
+  if (g_entropy && (!rows_ok(g_entropy) || !rows_ok(entropy))) return STREAMKL_ERR_INVALID;
+  if (num_tokens && dlogits == logits) return STREAMKL_ERR_INVALID;  // the tokens' logits are read after the pass
+  int sms = 0;
+  if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
+  return from_cuda(launch_logprobs_bwd(p, logits, tokens, lse, entropy, g_logp, g_entropy, dlogits, out_stride, sms,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
 streamkl_status streamkl_check_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return STREAMKL_ERR_CUDA;
   int h = 0;

@@ -92,6 +92,20 @@ cudaError_t launch_rows_to_bf16(const Problem& p, const float* acc, void* out, c
 // First 128-query tile whose rows see key k0.
 int fused_first_qtile(const Problem& p, long long k0);
 
+// ---- log probabilities of given tokens ---------------------------------------------
+constexpr int kTypeBf16 = 0, kTypeFp16 = 1, kTypeFp32 = 2;  // streamkl_dtype
+struct LogprobsProblem {
+  long long rows, stride;  // stride: elements between rows of the logits
+  int V, T, K, dtype;
+  float scale;
+};
+cudaError_t launch_logprobs_fwd(const LogprobsProblem& p, const void* logits, const long long* tokens, float* logp,
+                                float* entropy, float* lse, float* top_logp, long long* top_index, int num_sms,
+                                cudaStream_t st);
+cudaError_t launch_logprobs_bwd(const LogprobsProblem& p, const void* logits, const long long* tokens,
+                                const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                                void* dlogits, long long out_stride, int num_sms, cudaStream_t st);
+
 // ---- test hook ------------------------------------------------------------------
 cudaError_t launch_wait_timeout_probe(int timeout_us, int* status, cudaStream_t st);
 

@@ -1,0 +1,540 @@
+// Log probabilities of given tokens, entropy and top alternatives of each row
+// of logits, and the gradient of the first two.
+//
+// For a row x = scale * logits (V columns), in log2 units y = x log2(e):
+//     m = max_j y_j,  s = sum_j 2^(y_j - m),  t = sum_j 2^(y_j - m) (y_j - m)
+//     LSE = ln2 (m + log2 s)                      log p_j = x_j - LSE
+//     H   = -sum_j p_j log p_j = ln2 (log2 s - t / s)
+// One pass over the row: every thread keeps (m, s, t) of the columns it reads
+// and moves its m when a 16-byte vector brings a larger value (s and t follow
+// exactly: s' = a s, t' = a (t + s (m - m')), a = 2^(m - m')); the threads'
+// triples merge the same way.  t is centred on m, so the entropy does not lose
+// the digits that sum p x - LSE cancels.  Arguments below -256 are raised to
+// -256: their weight is exactly 0 either way, and 0 * -inf never arises.
+//
+// Top alternatives, also without sorting the row: a thread's largest value is a
+// by-product of the pass.  The K-th largest of these maxima is a lower bound
+// of the K-th largest value, so only the threads whose maximum reaches it are
+// read again (about K of them, from L2), the values that reach it become
+// candidates, and a candidate's place is the number of greater ones.  A value
+// and its column make one 64-bit key (value's order above, column's complement
+// below), so equal values go to the lowest column and the result does not
+// depend on the order in which threads arrive.  Rows with more candidates than
+// the list holds (thousands of equal values) take a second pass in which each
+// warp keeps a sorted list.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace skl {
+namespace {
+
+constexpr int kMaxCand = 512;      // candidate keys a block ranks
+constexpr float kFloor = -256.0f;  // 2^-256 is 0 in fp32
+constexpr int kUnroll = 4;         // 16-byte loads a thread has in flight
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) {
+  return __float2half_rn(x);
+}
+
+template <typename T>
+struct Vec {
+  static constexpr int N = 16 / sizeof(T);
+  union {
+    uint4 u;
+    T e[N];
+  };
+};
+
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Unsigned order of fp32 values (-0 taken as +0), and back.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t column) {
+  return ((uint64_t)order_of(x) << 32) | (0xffffffffu - column);
+}
+
+struct Sums {
+  float m, s, t;
+};
+
+__device__ __forceinline__ void merge(Sums& a, const Sums& b) {
+  if (b.m == kNegInf && b.s == 0.f) return;  // nothing seen (a NaN in b.s goes on)
+  const float m = fmaxf(a.m, b.m);
+  const float z = m == kNegInf ? 0.f : m;
+  const float da = max_nan(a.m - z, kFloor), db = max_nan(b.m - z, kFloor);
+  const float wa = ex2(da), wb = ex2(db);
+  a.t = wa * (a.t + a.s * da) + wb * (b.t + b.s * db);
+  a.s = wa * a.s + wb * b.s;
+  a.m = m;
+}
+
+// Adds n values (n is known at compile time) to a thread's sums and its largest raw value.
+template <int N>
+__device__ __forceinline__ void add_values(Sums& a, float& top, const float (&x)[N], float c) {
+  float vm = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) vm = fmaxf(vm, x[i]);
+  top = fmaxf(top, vm);
+  const float y = vm * c;
+  if (y > a.m) {
+    if (a.m != kNegInf) {
+      const float d = max_nan(a.m - y, kFloor), w = ex2(d);
+      a.t = w * (a.t + a.s * d);
+      a.s *= w;
+    }
+    a.m = y;
+  }
+  const float z = a.m == kNegInf ? 0.f : -a.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = max_nan(fmaf(x[i], c, z), kFloor);
+    const float p = ex2(d);
+    a.s += p;
+    a.t = fmaf(p, d, a.t);
+  }
+}
+
+struct FwdArgs {
+  const void* logits;
+  long long stride;
+  const long long* tokens;
+  float *logp, *entropy, *lse, *top_logp;
+  long long* top_index;
+  int V, T, K, parts;
+  float scale;
+};
+
+// A row, cut for 16-byte loads: `head` columns up to the first 16-byte boundary, `nvec` vectors, then the tail.
+struct Cut {
+  int head, nvec, tail0;
+};
+template <typename T>
+__device__ __forceinline__ Cut cut_row(const T* row, int V) {
+  constexpr int N = Vec<T>::N;
+  const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
+  Cut c;
+  c.head = min(V, off ? N - off : 0);
+  c.nvec = (V - c.head) / N;
+  c.tail0 = c.head + c.nvec * N;
+  return c;
+}
+
+template <int NT>
+struct FwdShared {
+  Sums warp_sums[NT / 32];
+  Sums part_sums[8];
+  uint64_t cand[kMaxCand];
+  uint64_t best[8 * 32];  // each part's top K, gathered in the first part's block
+  unsigned short again[NT];
+  int n_cand, n_again;
+};
+
+// Sorts nothing: the place of a key is the number of greater ones.  Keys are distinct.
+template <int NT>
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int K, uint64_t* out) {
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const uint64_t k = keys[i];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += keys[j] > k;
+    if (place < K) out[place] = k;
+  }
+}
+
+// The block's K largest keys of columns [lo, hi), for any values: each warp reads a contiguous share in order and
+// keeps its K best sorted over its lanes.
+template <typename T, int NT>
+__device__ void warp_lists(const T* row, int lo, int hi, int K, FwdShared<NT>& sh, uint64_t* out) {
+  constexpr int NW = NT / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int share = (hi - lo + NW - 1) / NW;
+  const int w0 = lo + warp * share, w1 = min(hi, w0 + share);
+  uint64_t mine = 0;
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const int j = j0 + lane;
+    const uint64_t key = j < w1 ? key_of(to_float(row[j]), (uint32_t)j) : 0;
+    unsigned todo = __ballot_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, mine, K - 1));
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const uint64_t k = __shfl_sync(0xffffffffu, key, src);
+      const int place = __popc(__ballot_sync(0xffffffffu, mine > k));
+      const uint64_t below = __shfl_up_sync(0xffffffffu, mine, 1);
+      if (lane == place) mine = k;
+      if (lane > place) mine = below;
+    }
+  }
+  __syncthreads();  // every thread has left the candidate list of the first attempt
+  if (lane < K) sh.cand[warp * K + lane] = mine;
+  __syncthreads();
+  // a share with fewer than K columns leaves zero keys: they rank behind every real one
+  for (int i = threadIdx.x; i < NW * K; i += NT) {
+    const uint64_t k = sh.cand[i];
+    if (!k) continue;
+    int place = 0;
+    for (int j = 0; j < NW * K; ++j) place += sh.cand[j] > k;
+    if (place < K) out[place] = k;
+  }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) logprobs_fwd_kernel(const FwdArgs a) {
+  constexpr int N = Vec<T>::N;
+  constexpr int NW = NT / 32;
+  __shared__ FwdShared<NT> sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int part = (int)(blockIdx.x % a.parts);
+  const long long r = blockIdx.x / a.parts;
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  const Cut cut = cut_row(row, a.V);
+  const int v0 = (int)((long long)cut.nvec * part / a.parts), v1 = (int)((long long)cut.nvec * (part + 1) / a.parts);
+  const int nv = v1 - v0;
+  const uint4* vecs = reinterpret_cast<const uint4*>(row + cut.head) + v0;
+  const bool first = part == 0, last = part == a.parts - 1;
+  const float c = a.scale * kLog2e;
+  if (tid == 0) sh.n_cand = sh.n_again = 0;
+  if (a.parts > 1) cg::this_cluster().barrier_arrive();  // this block runs: its shared memory may be written
+
+  Sums sums{kNegInf, 0.f, 0.f};
+  float top = kNegInf;  // this thread's largest value among its vectors
+  int v = tid;
+  for (; v + (kUnroll - 1) * NT < nv; v += kUnroll * NT) {
+    Vec<T> x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) x[u].u = load_stream(vecs + v + u * NT);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = to_float(x[u].e[i]);
+      add_values<N>(sums, top, f, c);
+    }
+  }
+  for (; v < nv; v += NT) {
+    Vec<T> x;
+    x.u = load_stream(vecs + v);
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_float(x.e[i]);
+    add_values<N>(sums, top, f, c);
+  }
+  // the columns outside the vectors: one a thread, and always candidates
+  const uint32_t top_order = tid < nv ? order_of(top) : 0u;
+  __syncthreads();  // the counters are zero
+  for (int side = 0; side < 2; ++side) {
+    const int j = side ? cut.tail0 + tid : tid;
+    if (side ? last && j < a.V : first && j < cut.head) {
+      const float f[1] = {to_float(row[j])};
+      float unused = kNegInf;
+      add_values<1>(sums, unused, f, c);
+      if (a.K) sh.cand[atomicAdd(&sh.n_cand, 1)] = key_of(f[0], (uint32_t)j);  // at most 2 (N - 1) of them
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const Sums b{__shfl_xor_sync(0xffffffffu, sums.m, o), __shfl_xor_sync(0xffffffffu, sums.s, o),
+                 __shfl_xor_sync(0xffffffffu, sums.t, o)};
+    // the same operand order on both sides of the exchange keeps all lanes' sums equal
+    if (lane & o) {
+      Sums q = b;
+      merge(q, sums);
+      sums = q;
+    } else {
+      merge(sums, b);
+    }
+  }
+  if (lane == 0) sh.warp_sums[warp] = sums;
+
+  const int k_here = min(a.K, cut.head * (int)first + nv * N + (a.V - cut.tail0) * (int)last);  // columns can be fewer
+  uint64_t* best = sh.best;
+  if (a.parts > 1) {
+    cg::this_cluster().barrier_wait();
+    best = cg::this_cluster().map_shared_rank(sh.best, 0);
+    if (tid < a.K) best[part * a.K + tid] = 0;  // a part may hold fewer columns than K
+  }
+  if (a.K) {
+    // the largest 16-bit prefix that at least K threads' maxima reach (0 when fewer threads hold vectors)
+    uint32_t thr = 0;
+    const uint32_t prefix = top_order >> 16;
+    for (uint32_t bit = 0x8000u; bit; bit >>= 1)
+      if (__syncthreads_count(prefix >= (thr | bit)) >= a.K) thr |= bit;
+    const uint32_t bound = thr << 16;
+    if (top_order && top_order >= bound) sh.again[atomicAdd(&sh.n_again, 1)] = (unsigned short)tid;
+    __syncthreads();
+    for (int q = warp; q < sh.n_again; q += NW) {
+      const int t = sh.again[q];
+      for (int w = t + lane * NT; w < nv; w += 32 * NT) {
+        Vec<T> x;
+        x.u = __ldg(vecs + w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float f = to_float(x.e[i]);
+          if (order_of(f) >= bound) {
+            const int at = atomicAdd(&sh.n_cand, 1);
+            if (at < kMaxCand) sh.cand[at] = key_of(f, (uint32_t)(cut.head + (v0 + w) * N + i));
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (sh.n_cand <= kMaxCand)
+      rank_keys<NT>(sh.cand, sh.n_cand, k_here, best + part * a.K);
+    else
+      warp_lists<T, NT>(row, first ? 0 : cut.head + v0 * N, last ? a.V : cut.head + v1 * N, k_here, sh,
+                        best + part * a.K);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    Sums all = sh.warp_sums[0];
+    for (int w = 1; w < NW; ++w) merge(all, sh.warp_sums[w]);
+    Sums* to = sh.part_sums;
+    if (a.parts > 1) to = cg::this_cluster().map_shared_rank(sh.part_sums, 0);
+    to[part] = all;
+  }
+  if (a.parts > 1)
+    cg::this_cluster().sync();
+  else
+    __syncthreads();
+  if (part != 0) return;
+
+  Sums all = sh.part_sums[0];
+  for (int q = 1; q < a.parts; ++q) merge(all, sh.part_sums[q]);
+  const bool empty = all.m == kNegInf && all.s == 0.f;  // every logit is -inf
+  const float log2s = log2f(all.s);
+  const float lse = empty ? kNegInf : kLn2 * (all.m + log2s);
+  if (tid == 0) {
+    a.lse[r] = lse;
+    a.entropy[r] = empty ? 0.f : kLn2 * (log2s - all.t / all.s);
+  }
+  auto log_prob = [&](float raw) { return empty ? kNegInf : fmaf(raw, a.scale, -lse); };
+  for (int t = tid; t < a.T; t += NT) {
+    const long long tok = a.tokens[r * a.T + t];
+    float out = 0.f;  // no token
+    if (tok >= a.V) out = __uint_as_float(0x7fffffffu);
+    else if (tok >= 0) out = log_prob(to_float(row[tok]));
+    a.logp[r * a.T + t] = out;
+  }
+  if (a.K) {
+    uint64_t* order = sh.best;
+    if (a.parts > 1) {
+      const int n = a.parts * a.K;
+      for (int i = tid; i < n; i += NT) {
+        const uint64_t k = sh.best[i];
+        if (!k) continue;
+        int place = 0;
+        for (int j = 0; j < n; ++j) place += sh.best[j] > k;
+        if (place < a.K) sh.cand[place] = k;
+      }
+      __syncthreads();
+      order = sh.cand;
+    }
+    if (tid < a.K) {
+      const uint64_t k = order[tid];
+      a.top_index[r * a.K + tid] = (long long)(0xffffffffu - (uint32_t)k);
+      a.top_logp[r * a.K + tid] = log_prob(value_of((uint32_t)(k >> 32)));
+    }
+  }
+}
+
+struct BwdArgs {
+  const void* logits;
+  long long stride, out_stride;
+  const long long* tokens;
+  const float *lse, *entropy, *g_logp, *g_entropy;
+  void* out;
+  int V, T, parts;
+  float scale;
+};
+
+// With A = sum of the row's g over its tokens, B = its g of the entropy, l_j = log p_j:
+//     dx_j = sum_t g_t [j = token_t] - p_j (A + B (l_j + H)),   dlogits_j = scale dx_j
+// The pass writes the second term; then the given tokens' columns, a handful, are written again with the sum of
+// both in fp32, rounded once.  A token that is given twice adds twice: its first place takes the sum of all.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) logprobs_bwd_kernel(const BwdArgs a) {
+  constexpr int N = Vec<T>::N;
+  __shared__ float sum_g[NT / 32];
+  const int tid = threadIdx.x;
+  const int part = (int)(blockIdx.x % a.parts);
+  const long long r = blockIdx.x / a.parts;
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  T* out = static_cast<T*>(a.out) + r * a.out_stride;
+  const long long* tokens = a.tokens + r * a.T;
+  const float* g = a.g_logp + r * a.T;
+  const float lse = a.lse[r];
+  const bool empty = lse == kNegInf;  // every logit is -inf: nothing depends on them
+
+  // A in a fixed order: thread t takes tokens t, t + NT, ...; lanes, then warps
+  float A = 0.f;
+  for (int t = tid; t < a.T; t += NT) {
+    const long long tok = tokens[t];
+    if (tok >= 0 && tok < a.V) A += g[t];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) A += __shfl_xor_sync(0xffffffffu, A, o);
+  if ((tid & 31) == 0) sum_g[tid >> 5] = A;
+  __syncthreads();
+  A = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) A += sum_g[w];
+  const float B = a.g_entropy ? a.g_entropy[r] : 0.f;
+  const float H = a.g_entropy ? a.entropy[r] : 0.f;
+  // dlogits = p (a0 + a1 l2), l2 = log2 p
+  const float a0 = -a.scale * (A + B * H), a1 = -a.scale * B * kLn2;
+  auto grad = [&](float x) {
+    const float l2 = max_nan(fmaf(x, a.scale, -lse) * kLog2e, kFloor);  // one rounding where x is near the LSE
+    return empty ? 0.f : ex2(l2) * fmaf(a1, l2, a0);
+  };
+
+  // vectors where both rows have the same offset from a 16-byte boundary, else single columns
+  const Cut cut = cut_row(row, a.V);
+  const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+  int lo, hi;  // this block's columns
+  if (same) {
+    const int v0 = (int)((long long)cut.nvec * part / a.parts), v1 = (int)((long long)cut.nvec * (part + 1) / a.parts);
+    lo = part == 0 ? 0 : cut.head + v0 * N;
+    hi = part == a.parts - 1 ? a.V : cut.head + v1 * N;
+    const uint4* in = reinterpret_cast<const uint4*>(row + cut.head);
+    uint4* to = reinterpret_cast<uint4*>(out + cut.head);
+    int v = v0 + tid;
+    auto one = [&](uint4 u) {
+      Vec<T> x;
+      x.u = u;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x.e[i] = from_float<T>(grad(to_float(x.e[i])));
+      return x.u;
+    };
+    for (; v + (kUnroll - 1) * NT < v1; v += kUnroll * NT) {
+      uint4 x[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) x[u] = load_stream(in + v + u * NT);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) to[v + u * NT] = one(x[u]);
+    }
+    for (; v < v1; v += NT) to[v] = one(load_stream(in + v));
+    if (part == 0 && tid < cut.head) out[tid] = from_float<T>(grad(to_float(row[tid])));
+    if (part == a.parts - 1 && cut.tail0 + tid < a.V)
+      out[cut.tail0 + tid] = from_float<T>(grad(to_float(row[cut.tail0 + tid])));
+  } else {
+    lo = (int)((long long)a.V * part / a.parts);
+    hi = (int)((long long)a.V * (part + 1) / a.parts);
+    for (int j = lo + tid; j < hi; j += NT) out[j] = from_float<T>(grad(to_float(row[j])));
+  }
+  if (empty) return;
+  __syncthreads();  // the block's columns are written
+  for (int t = tid; t < a.T; t += NT) {
+    const long long tok = tokens[t];
+    if (tok < lo || tok >= hi) continue;
+    float total = 0.f;
+    bool leads = true;
+    for (int u = 0; u < a.T; ++u)
+      if (tokens[u] == tok) {
+        leads = leads && u >= t;
+        total += g[u];
+      }
+    if (leads) out[tok] = from_float<T>(fmaf(a.scale, total, grad(to_float(row[tok]))));
+  }
+}
+
+// Blocks that share a row: as many (a power of two, at most 8, the portable cluster size) as keep the launch within
+// two blocks for each SM, and no part below kMinPartBytes.
+constexpr long long kMinPartBytes = 8192;
+int parts_of(long long rows, long long row_bytes, int num_sms) {
+  int parts = 1;
+  while (parts < 8 && rows * parts * 2 <= 2ll * num_sms && row_bytes / (parts * 2) >= kMinPartBytes) parts *= 2;
+  return parts;
+}
+
+// Threads of a block: 128 for short rows, where 512 would hold no vector.
+constexpr long long kShortRowBytes = 8192;
+
+template <typename T, int NT>
+cudaError_t launch_fwd_nt(const FwdArgs& a, long long rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * a.parts));
+  cfg.blockDim = dim3(NT);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.parts;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, logprobs_fwd_kernel<T, NT>, a);
+}
+
+template <typename T>
+cudaError_t launch_fwd_t(FwdArgs a, long long rows, int num_sms, cudaStream_t st) {
+  const long long bytes = (long long)a.V * sizeof(T);
+  a.parts = parts_of(rows, bytes, num_sms);
+  return bytes <= kShortRowBytes ? launch_fwd_nt<T, 128>(a, rows, st) : launch_fwd_nt<T, 512>(a, rows, st);
+}
+
+template <typename T>
+cudaError_t launch_bwd_t(BwdArgs a, long long rows, int num_sms, cudaStream_t st) {
+  const long long bytes = (long long)a.V * sizeof(T);
+  a.parts = parts_of(rows, bytes, num_sms);
+  if (bytes <= kShortRowBytes)
+    logprobs_bwd_kernel<T, 128><<<(unsigned)(rows * a.parts), 128, 0, st>>>(a);
+  else
+    logprobs_bwd_kernel<T, 512><<<(unsigned)(rows * a.parts), 512, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs_fwd(const LogprobsProblem& p, const void* logits, const long long* tokens, float* logp,
+                                float* entropy, float* lse, float* top_logp, long long* top_index, int num_sms,
+                                cudaStream_t st) {
+  FwdArgs a{logits, p.stride, tokens, logp, entropy, lse, top_logp, top_index, p.V, p.T, p.K, 1, p.scale};
+  if (p.dtype == kTypeBf16) return launch_fwd_t<__nv_bfloat16>(a, p.rows, num_sms, st);
+  if (p.dtype == kTypeFp16) return launch_fwd_t<__half>(a, p.rows, num_sms, st);
+  return launch_fwd_t<float>(a, p.rows, num_sms, st);
+}
+
+cudaError_t launch_logprobs_bwd(const LogprobsProblem& p, const void* logits, const long long* tokens,
+                                const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                                void* dlogits, long long out_stride, int num_sms, cudaStream_t st) {
+  BwdArgs a{logits, p.stride, out_stride, tokens, lse, entropy, g_logp, g_entropy, dlogits, p.V, p.T, 1, p.scale};
+  if (p.dtype == kTypeBf16) return launch_bwd_t<__nv_bfloat16>(a, p.rows, num_sms, st);
+  if (p.dtype == kTypeFp16) return launch_bwd_t<__half>(a, p.rows, num_sms, st);
+  return launch_bwd_t<float>(a, p.rows, num_sms, st);
+}
+
+}  // namespace skl

@@ -299,6 +299,44 @@ int streamkl_bwd_mutual_select(streamkl_shape s, size_t l2_bytes, int num_sms);
 /* Workspace bytes streamkl_bwd_mutual needs in `bwd_mode` on the current device (0 for the mutual kernels). */
 streamkl_status streamkl_bwd_mutual_workspace(streamkl_shape s, int bwd_mode, size_t* bytes);
 
+/*
+ * Log probabilities of given tokens, with entropy and top alternatives: the
+ * output-layer companion of the attention loss (a student scored on the data's
+ * tokens, or on its teacher's most likely ones).
+ *
+ * logits: [rows, vocab] of `dtype`, rows `row_stride` elements apart, aligned to
+ *   an element.  x = scale * logits, scale > 0 (an inverse temperature).
+ * tokens: [rows, num_tokens] 64-bit.  logp[r, t] = x[r, token] - LSE_r.  A
+ *   negative token is no token: its logp is 0 and it has no gradient.  A token
+ *   >= vocab gives NaN and has no gradient; nothing is read for it.
+ * entropy, lse: [rows], H = -sum p log p and log sum e^x.
+ * top_logp, top_index: [rows, top_k], the largest logits in descending order,
+ *   equal ones from the lowest column up (-0 equals +0), with their log
+ *   probabilities.  top_k <= STREAMKL_LOGPROBS_MAX_TOP_K and <= vocab; 0 for none
+ *   (both may be NULL then, as tokens and logp with num_tokens = 0).
+ * A logit of -inf has probability 0.  A row of nothing but -inf has LSE -inf,
+ * entropy 0, log probabilities -inf and a zero gradient.  A +inf or NaN logit
+ * makes its row's values NaN (alternatives are then any columns of the row).
+ *
+ * streamkl_logprobs_bwd writes dlogits [rows, vocab] (rows `out_stride` elements
+ * apart, `dtype`) for upstream gradients g_logp [rows, num_tokens] and, unless
+ * NULL, g_entropy [rows] (entropy is read only then); lse and entropy are the
+ * forward's.  A token given twice in a row adds twice.  The alternatives have no
+ * gradient: to train on some, give them as tokens.  dlogits may be the logits
+ * themselves only where num_tokens is 0.
+ * Sums are fp32.  Results do not depend on the order in which blocks run.
+ */
+typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1, STREAMKL_FP32 = 2 } streamkl_dtype;
+#define STREAMKL_LOGPROBS_MAX_TOP_K 32
+streamkl_status streamkl_logprobs_fwd(const void* logits, int dtype, long long rows, long long vocab,
+                                      long long row_stride, const long long* tokens, int num_tokens, float scale,
+                                      int top_k, float* logp, float* entropy, float* lse, float* top_logp,
+                                      long long* top_index, void* stream);
+streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long rows, long long vocab,
+                                      long long row_stride, const long long* tokens, int num_tokens, float scale,
+                                      const float* lse, const float* entropy, const float* g_logp,
+                                      const float* g_entropy, void* dlogits, long long out_stride, void* stream);
+
 /* Text for a status code (static storage). */
 const char* streamkl_status_string(streamkl_status st);
 
