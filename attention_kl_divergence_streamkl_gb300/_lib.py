@@ -42,6 +42,12 @@ class Shape(ctypes.Structure):
                 ("k_stride_h", ctypes.c_longlong), ("k_stride_n", ctypes.c_longlong)]
 
 
+class AttnShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("HK", ctypes.c_int), ("NQ", ctypes.c_int), ("NK", ctypes.c_int),
+                ("D", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("q_lens", ctypes.c_void_p),
+                ("k_lens", ctypes.c_void_p)] + [(f"{t}_stride_{x}", ctypes.c_longlong) for t in "qkvo" for x in "bhn"]
+
+
 class StreamKLError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -70,6 +76,9 @@ SIGNATURES = {
     "streamkl_bwd_mutual": (_I, [_P, _P, _P, _P, Shape, _F, _F, _F, _F, _P, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_bwd_mutual_select": (_I, [Shape, _SZ, _I]),
     "streamkl_bwd_mutual_workspace": (_I, [Shape, _I, ctypes.POINTER(_SZ)]),
+    "streamkl_attn_fwd_workspace": (_I, [AttnShape, ctypes.POINTER(_SZ)]),
+    "streamkl_attn_fwd_plan": (_I, [AttnShape, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
+    "streamkl_attn_fwd": (_I, [_P, _P, _P, AttnShape, _P, _F, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
     "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
@@ -406,6 +415,88 @@ def _call(name, dev, *args):
         with torch.cuda.device(dev):
             st = f(*args, _stream(dev))
     _check(st, name)
+
+
+def _in_place(t):
+    """A [B, H, N, D] tensor the library can read and its (b, h, n) strides (a contiguous copy where it cannot)."""
+    st = _bhn_strides(t)
+    if st is None:
+        t = t.clone(memory_format=torch.contiguous_format)  # also where only the start is off a 16-byte boundary
+        st = _bhn_strides(t)
+    return t, st
+
+
+def make_attn_shape(B, H, HK, NQ, NK, D, scale=None, causal=False, q_lens=None, k_lens=None, q_strides=(0, 0, 0),
+                    k_strides=(0, 0, 0), v_strides=(0, 0, 0), o_strides=(0, 0, 0)) -> AttnShape:
+    """The C shape of an attention; lens are int32 device tensors (kept alive by the caller) or None."""
+    return AttnShape(int(B), int(H), int(HK), int(NQ), int(NK), int(D), float(scale or 0.0), int(bool(causal)),
+                     _ptr(q_lens), _ptr(k_lens), *q_strides, *k_strides, *v_strides, *o_strides)
+
+
+def _attn_prep(q, k, v, q_lens, k_lens):
+    """Validates an attention's inputs; returns (q, k, v, q_lens, k_lens on the device, their strides, was_host)."""
+    for t in (q, k, v):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("q, k, v must be bfloat16")
+        if t.dim() != 4:
+            raise ValueError("q must be [B, H, N_Q, D], k and v [B, HK, N_K, D]")
+    if k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
+    if k.shape[1] == 0 or q.shape[1] % k.shape[1]:
+        raise ValueError(f"{q.shape[1]} query heads do not divide over {k.shape[1]} key heads")
+    host = q.device.type == "cpu"
+    if any(t.device != q.device for t in (k, v)):
+        raise ValueError("inputs on different devices")
+    if host:
+        dev = torch.device("cuda", torch.cuda.current_device())
+        q, k, v = (t.contiguous().to(dev, non_blocking=True) for t in (q, k, v))
+    lens = []
+    for t, name in ((q_lens, "q_lens"), (k_lens, "k_lens")):
+        if t is not None:
+            if t.dtype != torch.int32 or tuple(t.shape) != (q.shape[0],):
+                raise ValueError(f"{name} must be int32 of shape ({q.shape[0]},)")
+            t = t.to(q.device, non_blocking=True).contiguous()
+        lens.append(t)
+    (q, qs), (k, ks), (v, vs) = _in_place(q), _in_place(k), _in_place(v)
+    return q, k, v, lens[0], lens[1], qs, ks, vs, host
+
+
+def _workspace(name, shape, dev, *args):
+    n = ctypes.c_size_t(0)
+    f = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = f(shape, *args, ctypes.byref(n))
+    else:
+        with torch.cuda.device(dev):
+            st = f(shape, *args, ctypes.byref(n))
+    _check(st, name)
+    return torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None, n.value
+
+
+def attn_fwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
+    """(packed, key splits) of the attention forward on a device with num_sms SMs."""
+    a, b = ctypes.c_int(0), ctypes.c_int(0)
+    _check(lib().streamkl_attn_fwd_plan(make_attn_shape(B, H, HK, NQ, NK, D, None, causal), int(num_sms),
+                                        ctypes.byref(a), ctypes.byref(b)), "streamkl_attn_fwd_plan")
+    return bool(a.value), b.value
+
+
+def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
+    """Attention: (o bf16 with q's layout, lse fp32 [B, H, N_Q]).
+
+    q: [B, H, N_Q, D], k and v: [B, HK, N_K, D] bf16, H a multiple of HK; q_lens, k_lens: int32 [B] lengths of a
+    padded batch's sequences.  Causal masking is aligned at the last query and key of each sequence.  Rows that
+    see no key give 0 and -inf.
+    """
+    q, k, v, q_lens, k_lens, qs, ks, vs, host = _attn_prep(q, k, v, q_lens, k_lens)
+    B, H, NQ, D = q.shape
+    dev = q.device
+    s = make_attn_shape(B, H, k.shape[1], NQ, k.shape[2], D, scale, causal, q_lens, k_lens, qs, ks, vs, qs)
+    ws, nbytes = _workspace("streamkl_attn_fwd_workspace", s, dev)
+    o = _grad_like(q, qs, NQ)
+    lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
+    _call("streamkl_attn_fwd", dev, _ptr(q), _ptr(k), _ptr(v), s, _ptr(o), _ptr(lse), _ptr(ws), nbytes)
+    return _back((o, lse), host)
 
 
 def _logits_rows(logits, tokens):

@@ -259,12 +259,12 @@ bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH,
 }
 
 bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, int B, long long sn, long long sh,
-                     long long sb, int box_rows) {
+                     long long sb, int box_rows, int box_heads) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)sn * 2, (cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
-  const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, 1u, 1u};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, (cuuint32_t)box_heads, 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -604,6 +604,86 @@ streamkl_status streamkl_bwd_mutual(const void* q1, const void* k1, const void* 
   return from_cuda(e != cudaSuccess ? e : launch_bwd_fused(p, 2, in, dq1, dk1, ws, range_tiles, status, st));
 }
 
+static bool aligned_to_or_null(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+static bool aligned_to(const void* p, uintptr_t n) { return p && aligned_to_or_null(p, n); }
+
+static streamkl_status attn_problem(const streamkl_attn_shape& s, AttnProblem* p) {
+  if (s.B <= 0 || s.HK <= 0 || s.H <= 0 || s.H % s.HK || s.NQ < 0 || s.NK < 0 || s.D <= 0) return STREAMKL_ERR_INVALID;
+  if (!(s.scale == s.scale) || isinf(s.scale)) return STREAMKL_ERR_INVALID;
+  if (s.NQ > kMaxRows || s.NK > kMaxRows) return STREAMKL_ERR_UNSUPPORTED;
+  if (s.D != 64 && s.D != 128) return STREAMKL_ERR_UNSUPPORTED;
+  // one-dimensional grids over rows and over tiles of either side
+  if ((long long)s.B * s.H > 0x7fffffffLL || (long long)s.B * s.H * (s.NQ + 128LL) > 0x7fffffffLL ||
+      (long long)s.B * s.H * (s.NK + 128LL) > 0x7fffffffLL * 64)
+    return STREAMKL_ERR_UNSUPPORTED;
+  *p = AttnProblem{};
+  p->B = s.B;
+  p->H = s.H;
+  p->HK = s.HK;
+  p->G = s.H / s.HK;
+  p->NQ = s.NQ;
+  p->NK = s.NK;
+  p->D = s.D;
+  p->causal = s.causal ? 1 : 0;
+  p->scale = s.scale > 0.f ? s.scale : 1.0f / sqrtf((float)s.D);
+  p->c = p->scale * kLog2e;
+  p->q_lens = s.q_lens;
+  p->k_lens = s.k_lens;
+  if (!strides_ok(s.q_stride_b, s.q_stride_h, s.q_stride_n, s.H, s.NQ, s.D, &p->qs_b, &p->qs_h, &p->qs_n) ||
+      !strides_ok(s.k_stride_b, s.k_stride_h, s.k_stride_n, s.HK, s.NK, s.D, &p->ks_b, &p->ks_h, &p->ks_n) ||
+      !strides_ok(s.v_stride_b, s.v_stride_h, s.v_stride_n, s.HK, s.NK, s.D, &p->vs_b, &p->vs_h, &p->vs_n) ||
+      !strides_ok(s.o_stride_b, s.o_stride_h, s.o_stride_n, s.H, s.NQ, s.D, &p->os_b, &p->os_h, &p->os_n))
+    return STREAMKL_ERR_INVALID;
+  p->rows = (long long)s.B * s.H * s.NQ;
+  if (!aligned_to_or_null(s.q_lens, 4) || !aligned_to_or_null(s.k_lens, 4)) return STREAMKL_ERR_INVALID;
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_fwd_workspace(streamkl_attn_shape s, size_t* bytes) {
+  AttnProblem p;
+  streamkl_status v = attn_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!bytes) return STREAMKL_ERR_INVALID;
+  *bytes = 0;
+  if (p.NQ == 0 || p.NK == 0) return STREAMKL_OK;
+  int sms = 0;
+  if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
+  attn_fwd_plan(&p, sms);
+  *bytes = attn_fwd_workspace(p);
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_fwd_plan(streamkl_attn_shape s, int num_sms, int* packed, int* splits) {
+  AttnProblem p;
+  streamkl_status v = attn_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!packed || !splits || num_sms <= 0 || p.NQ == 0) return STREAMKL_ERR_INVALID;
+  attn_fwd_plan(&p, num_sms);
+  *packed = p.packed;
+  *splits = p.splits;
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, streamkl_attn_shape s, void* o,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  AttnProblem p;
+  streamkl_status st = attn_problem(s, &p);
+  if (st != STREAMKL_OK) return st;
+  if (p.NQ == 0) return STREAMKL_OK;
+  if (!o || !aligned16(o) || !rows_ok(lse)) return STREAMKL_ERR_INVALID;
+  if (p.NK > 0) {
+    if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v)) return STREAMKL_ERR_INVALID;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+    attn_fwd_plan(&p, sms);
+    const size_t need = attn_fwd_workspace(p);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return STREAMKL_ERR_WORKSPACE;
+  }
+  int* status = nullptr;
+  if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
+  return from_cuda(launch_attn_fwd(p, q, k, v, o, lse, workspace, status, static_cast<cudaStream_t>(stream)));
+}
+
 static streamkl_status logprobs_problem(int dtype, long long rows, long long vocab, long long row_stride,
                                         int num_tokens, int top_k, float scale, LogprobsProblem* p) {
   if (rows < 0 || vocab <= 0 || num_tokens < 0 || top_k < 0 || row_stride < vocab) return STREAMKL_ERR_INVALID;
@@ -616,8 +696,6 @@ static streamkl_status logprobs_problem(int dtype, long long rows, long long voc
   *p = LogprobsProblem{rows, row_stride, (int)vocab, num_tokens, top_k, dtype, scale};
   return STREAMKL_OK;
 }
-
-static bool aligned_to(const void* p, uintptr_t n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 streamkl_status streamkl_logprobs_fwd(const void* logits, int dtype, long long rows, long long vocab,
                                       long long row_stride, const long long* tokens, int num_tokens, float scale,

@@ -1,0 +1,511 @@
+// Attention forward: O = softmax(scale Q K^T) V and the rows' log-sum-exp, on
+// the 5th-generation tensor cores.
+//
+// One pass over the keys with a running maximum m and sum l per query row, in
+// log2 units x = c (q . k), c = scale log2(e):
+//     p_j = 2^(x_j - m),  l += sum_j p_j,  O += sum_j bf16(p_j) v_j
+//     when m moves to m': l *= 2^(m - m'), O *= 2^(m - m')
+//     at the end O / l and LSE = ln2 (m + log2 l)
+// m is a reference, not the exact maximum: once a row has one, a tile is summed
+// against it without taking its own maximum, and only where a row's sum would
+// pass 2^64 is m moved to the tile's maximum and O, which stays in TMEM, scaled.
+// That is exact because p, l and O share m and bf16 has fp32's exponent range;
+// rounding p to bf16 costs half a bf16 step of each weight, as the product's
+// other operand v has; l sums the unrounded p.
+//
+// A block owns two tiles of 128 rows and streams 128-key tiles of K and V, so
+// each K and V tile loaded from L2 serves 256 rows:
+//   warps 0-3, 4-7  softmax of tile A and of tile B; thread = row (TMEM lane)
+//   warp 8          TMA producer: Q_A, Q_B, then K(j), V(j), K(j+1), ... through a ring
+//   warp 9          TMEM owner and MMA issuer (one thread)
+//   warp 10         clears rows of the V tile that lie past a sequence's key length
+// TMEM: S_A [0,128), S_B [128,256), O_A [256, 256+D), O_B [384, 384+D); P (bf16
+// pairs) overwrites the first 64 columns of its own S and is the A operand of
+// O += P V.  The pipe runs S_A(j+1) behind P V_A(j), then P V_B(j), S_B(j+1):
+// while one tile's softmax works, the other tile's two products run.
+//
+// Few query rows: where all query heads of a key head fit in one tile (G N_Q <=
+// 128) they are packed into it, row g N_Q + n, so that K and V are read once for
+// the whole group.  Few tiles: the keys are split over blocks, each writes its
+// (m, l, O) in fp32 and a second kernel merges them.
+#include "attn.cuh"
+
+namespace skl {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int SOFTMAX_WARPS = 8;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, PATCH_WARP = 10;
+constexpr int THREADS = 12 * 32;
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;  // 256 * 224 + 128 * 56 = 384 * 168 at launch
+constexpr int SLOTS = 5;                            // ring of K and V tiles
+constexpr uint32_t kTmemCols = 512;
+constexpr float kSumLimit = 18446744073709551616.0f;  // 2^64
+constexpr uint32_t kColS = 0, kColO = 256;           // tile t: + 128 t
+
+template <int D>
+struct Smem {
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int OFF_Q = 0;  // Q_A, Q_B
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+  // q_full[2], kv_full[5], kv_empty[5], s_full[2], p_ready[2], o_done[2], to_patch, patched; TMEM slot, abort flag
+  static constexpr int BAR_SLOT = 8 * 20;
+  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
+};
+static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+
+// Sum of 2^(c s - m) over a row's 128 columns; the bf16 pairs of the terms go to pk.
+__device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const uint32_t (&s2)[32],
+                                          const uint32_t (&s3)[32], float c, float m, uint32_t (&pk)[64]) {
+  const float2 cc = make_float2(c, c), nm = make_float2(-m, -m);
+  float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t* s = h == 0 ? s0 : h == 1 ? s1 : h == 2 ? s2 : s3;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float2 x0 = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cc, nm);
+      const float2 x1 = ffma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), cc, nm);
+      const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
+      l0 = fadd2(l0, p0);
+      l1 = fadd2(l1, p1);
+      pk[h * 16 + i / 2] = pack_bf16(p0.x, p0.y);
+      pk[h * 16 + i / 2 + 1] = pack_bf16(p1.x, p1.y);
+    }
+  }
+  l0 = fadd2(l0, l1);
+  return l0.x + l0.y;
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_fwd_kernel(const AttnProblem p, __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse,
+                    float* __restrict__ part_o, float2* __restrict__ part_ml, int* status,
+                    const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv) {
+  using L = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // item: (batch, head or key head, pair of query tiles), the longest causal ones first; then the key split
+  const int split = (int)(blockIdx.x % p.splits);
+  const int item = (int)(blockIdx.x / p.splits);
+  const int qt = p.q_items - 1 - item % p.q_items;
+  const int bh = item / p.q_items;
+  const int heads = p.packed ? p.HK : p.H;
+  const int b = bh / heads, hx = bh % heads;  // hx: key head when packed, else query head
+  const int hk = p.packed ? hx : hx / p.G;
+  const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
+  const int off = kl - ql;
+  const int q0 = qt * 2 * BM;
+  // first key of split s: tiles are dealt out evenly
+  const int tiles_all = (p.NK + BN - 1) / BN;
+  const int kt0 = (int)((long long)tiles_all * split / p.splits);
+  const int kt1 = (int)((long long)tiles_all * (split + 1) / p.splits);
+  // key tiles of query tile t within this split
+  auto key_tiles = [&](int t) {
+    int last;  // last query of the tile
+    if (p.packed) {
+      if (t) return 0;
+      last = ql - 1;
+    } else {
+      const int first = q0 + t * BM;
+      if (first >= ql) return 0;
+      last = min(first + BM, ql) - 1;
+    }
+    const int end = p.causal ? min(kl, last + off + 1) : kl;
+    if (last < 0 || end <= 0) return 0;
+    return max(0, min(kt1, (end + BN - 1) / BN) - kt0);
+  };
+  const int nA = key_tiles(0), nB = key_tiles(1);
+  const int n = max(nA, nB);
+  const bool has_b = !p.packed && q0 + BM < p.NQ;
+  // the V tile that a sequence ends inside: its rows past the end may hold anything, and 0 * NaN is NaN
+  const int patch_i = (kl < p.NK && (kl & (BN - 1))) ? (kl / BN) - kt0 : -1;
+
+  const uint32_t bar = sb + L::OFF_BAR;
+  const uint32_t q_full = bar, kv_full = bar + 16, kv_empty = kv_full + 8 * SLOTS, s_full = kv_empty + 8 * SLOTS,
+                 p_ready = s_full + 16, o_done = p_ready + 16, to_patch = o_done + 16, patched = to_patch + 8;
+  const uint32_t slot = bar + L::BAR_SLOT;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full + 8 * t, 1);
+      mbar_init(s_full + 8 * t, 1);
+      mbar_init(p_ready + 8 * t, SOFTMAX_WARPS / 2);
+      mbar_init(o_done + 8 * t, 1);
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(kv_full + 8 * s, 1);
+      mbar_init(kv_empty + 8 * s, 1);
+    }
+    mbar_init(to_patch, 1);
+    mbar_init(patched, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+
+  if (warp >= SOFTMAX_WARPS) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == PRODUCER_WARP) {
+      if (lane == 0 && n > 0) {
+        const uint32_t q_rows = p.packed ? (uint32_t)(p.G * p.NQ) : (uint32_t)BM;
+        const uint32_t q_bytes = q_rows * D * 2;
+        auto load_q = [&](int t) {
+          mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
+                        p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+        };
+        if (nA > 0) load_q(0);
+        if (nB > 0) load_q(1);
+        int issued = 0;
+        for (int u = 0; u < 2 * n; ++u) {  // K(0), V(0), K(1), ...
+          const int s = u % SLOTS;
+          if (u >= SLOTS && !mbar_wait(kv_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(kv_full + 8 * s, L::TILE);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_KV + s * L::TILE + h * BN * 128, (u & 1) ? &mv : &mk, kv_full + 8 * s, h * 64,
+                        (kt0 + (u >> 1)) * BN, hk, b);
+          issued = u + 1;
+        }
+        // copies that may still be landing
+        if (nA > 0) mbar_drain(q_full, 0, status);
+        if (nB > 0) mbar_drain(q_full + 8, 0, status);
+        for (int u = max(0, issued - SLOTS); u < issued; ++u)
+          mbar_drain(kv_full + 8 * (u % SLOTS), (u / SLOTS) & 1, status);
+      }
+      __syncwarp();
+    } else if (warp == PATCH_WARP) {
+      if (patch_i >= 0 && patch_i < n) {
+        // the MMA thread, which follows the ring's phases, says when the tile is there
+        const int s = (2 * patch_i + 1) % SLOTS;
+        if (mbar_wait_warp(to_patch, 0, status, abort_flag)) {
+          const int from = kl & (BN - 1);
+          for (int i = lane; i < (BN - from) * (D / 8); i += 32) {
+            const int r = from + i / (D / 8);
+            st_shared_zero16(sw128<BN>(sb + L::OFF_KV + s * L::TILE, r, i % (D / 8)));
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(patched);
+        }
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t id_s = idesc_bf16(BM, BN, false, false);
+        constexpr uint32_t id_o = idesc_bf16(BM, D, false, true);
+        const int nt[2] = {nA, nB};
+        bool ok = true;
+        auto issue_s = [&](int t, int i) {  // S_t(i) = Q_t K(i)^T
+          const int u = 2 * i, s = u % SLOTS;
+          if (i == 0 && !mbar_wait(q_full + 8 * t, 0, status, abort_flag)) return false;
+          if (!mbar_wait(kv_full + 8 * s, (u / SLOTS) & 1, status, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t qd = sdesc_sw128(sb + L::OFF_Q + t * L::TILE, 0, 1024);
+          const uint64_t kd = sdesc_sw128(sb + L::OFF_KV + s * L::TILE, 0, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
+            mma_ss(tmem + kColS + 128 * t, sdesc_add(qd, o), sdesc_add(kd, o), id_s, ks > 0);
+          }
+          mma_commit(s_full + 8 * t);
+          if (t == 1 || i >= nB) mma_commit(kv_empty + 8 * s);  // K(i) is read by no later tile
+          return true;
+        };
+        auto issue_o = [&](int t, int i) {  // O_t += P_t(i) V(i)
+          const int u = 2 * i + 1, s = u % SLOTS;
+          if (!mbar_wait(kv_full + 8 * s, (u / SLOTS) & 1, status, abort_flag)) return false;
+          if (i == patch_i) {
+            if (t == 0 || i >= nA) mbar_arrive(to_patch);  // the first of the tiles that read it
+            if (!mbar_wait(patched, 0, status, abort_flag)) return false;
+          }
+          if (!mbar_wait(p_ready + 8 * t, i & 1, status, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t vd = sdesc_sw128(sb + L::OFF_KV + s * L::TILE, BN * 128, 1024);
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks)
+            mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * ks, sdesc_add(vd, ks * 2048), id_o,
+                   i > 0 || ks > 0);
+          mma_commit(o_done + 8 * t);
+          if (t == 1 || i >= nB) mma_commit(kv_empty + 8 * s);
+          return true;
+        };
+        // tile A has the key tiles [0, nA), tile B [0, nB); B is the last to read a tile both have, and where
+        // only A reads it (i >= nB) A is.  Where only B reads it (i >= nA) the same rule holds.
+        for (int t = 0; ok && t < 2; ++t)
+          if (nt[t] > 0) ok = issue_s(t, 0);
+        for (int i = 0; ok && i < n; ++i) {
+          for (int t = 0; ok && t < 2; ++t) {
+            if (i < nt[t]) ok = issue_o(t, i);
+            if (ok && i + 1 < nt[t]) ok = issue_s(t, i + 1);
+          }
+        }
+        if (ok)
+          for (int t = 0; t < 2; ++t)
+            if (nt[t] > 0) mbar_drain(o_done + 8 * t, (nt[t] - 1) & 1, status);
+      }
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const int nt = t ? nB : nA;
+    const int g = p.packed ? r / p.NQ : 0;
+    const int qn = p.packed ? r - g * p.NQ : q0 + t * BM + r;  // query position of this row
+    const int h = p.packed ? hk * p.G + g : hx;
+    const bool real = p.packed ? (t == 0 && g < p.G) : (qn < p.NQ);
+    const int row_end = (real && qn < ql) ? (p.causal ? min(kl, qn + off + 1) : kl) : 0;  // keys this row sees
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t ts = tmem + lanes + kColS + 128 * t, to = tmem + lanes + kColO + 128 * t;
+    const float c = p.c;
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      ok = mbar_wait_warp(s_full + 8 * t, i & 1, status, abort_flag);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+      const int seen = row_end - (kt0 + i) * BN;  // columns this row sees: [0, seen)
+      const bool masked = __any_sync(0xffffffffu, seen < BN);
+      uint32_t s0[32], s1[32], s2[32], s3[32], pk[64];
+      auto load_s = [&]() {
+        tmem_ld32(ts, s0);
+        tmem_ld32(ts + 32, s1);
+        tmem_ld32(ts + 64, s2);
+        tmem_ld32(ts + 96, s3);
+        tmem_ld_wait();
+        reg_fence32(s0);
+        reg_fence32(s1);
+        reg_fence32(s2);
+        reg_fence32(s3);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (k >= seen) s0[k] = __float_as_uint(kNegInf);
+            if (k + 32 >= seen) s1[k] = __float_as_uint(kNegInf);
+            if (k + 64 >= seen) s2[k] = __float_as_uint(kNegInf);
+            if (k + 96 >= seen) s3[k] = __float_as_uint(kNegInf);
+          }
+        }
+      };
+      load_s();
+      float sum = row_exps(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk);
+      // a row without a reference that sees keys here, or whose terms grew too large (inf and NaN included)
+      const bool move = m == kNegInf ? seen > 0 : !(sum < kSumLimit);
+      if (__any_sync(0xffffffffu, move)) {
+        load_s();
+        float mx = kNegInf;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          mx = fmax3(mx, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
+          mx = fmax3(mx, __uint_as_float(s2[k]), __uint_as_float(s3[k]));
+        }
+        const float m2 = move ? fmaxf(m, mx * c) : m;
+        const float w = m == kNegInf ? 0.f : ex2(m - m2);
+        m = m2;
+        l *= w;
+        sum = row_exps(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk);
+        if (i > 0) {
+          ok = mbar_wait_warp(o_done + 8 * t, (i - 1) & 1, status, abort_flag);
+          __syncwarp();
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            tmem_ld32(to + d, s0);
+            tmem_ld_wait();
+            reg_fence32(s0);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s0[k] = __float_as_uint(__uint_as_float(s0[k]) * w);
+            tmem_st32(to + d, s0);
+          }
+        }
+      }
+      l += sum;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_st16(ts + 16 * q, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * q]));
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready + 8 * t);
+    }
+    if (nt > 0 && ok) {
+      ok = mbar_wait_warp(o_done + 8 * t, (nt - 1) & 1, status, abort_flag);
+      __syncwarp();
+    }
+    if (ok && (t == 0 || has_b)) {
+      tc_fence_after();
+      const size_t row = ((size_t)b * p.H + h) * p.NQ + qn;
+      const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees no key: zeros
+      const bool nan = l != l;
+      if (p.splits > 1) {
+        if (real) part_ml[(size_t)split * p.rows + row] = make_float2(m, l);
+      } else if (real) {
+        out_lse[row] = (l > 0.f || nan) ? (m + log2f(l)) * kLn2 : kNegInf;
+      }
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32(to + d, o);
+          tmem_ld_wait();
+          reg_fence32(o);
+        }
+        if (!(l > 0.f) && !nan) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        if (!real) continue;
+        if (p.splits > 1) {
+          float4* dst = reinterpret_cast<float4*>(part_o + ((size_t)split * p.rows + row) * D + d);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                 __uint_as_float(o[4 * k + 3]));
+        } else {
+          const float f = nan ? l : inv;
+          uint4* dst = reinterpret_cast<uint4*>(out + (long long)b * p.os_b + (long long)h * p.os_h +
+                                                (long long)qn * p.os_n + d);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * f, __uint_as_float(o[8 * k + 2 * e + 1]) * f);
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Merges the splits' (m, l, O): one warp per row, a lane takes D / 32 columns.
+template <int D>
+__global__ void __launch_bounds__(256)
+    attn_merge_kernel(const AttnProblem p, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+                      __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse) {
+  constexpr int W = D / 32;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= p.rows) return;
+  float m = kNegInf;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part_ml[(size_t)s * p.rows + row].x);
+  float l = 0.f, o[W];
+#pragma unroll
+  for (int k = 0; k < W; ++k) o[k] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = part_ml[(size_t)s * p.rows + row];
+    if (ml.x == kNegInf && ml.y == 0.f) continue;  // this split has no key for the row
+    const float w = ml.x == m ? 1.f : ex2(ml.x - m);
+    l += w * ml.y;
+    const float* src = part_o + ((size_t)s * p.rows + row) * D + lane * W;
+#pragma unroll
+    for (int k = 0; k < W; ++k) o[k] += w * src[k];
+  }
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  if (lane == 0) out_lse[row] = none ? kNegInf : (m + log2f(l)) * kLn2;
+  const long long bh = row / p.NQ;
+  __nv_bfloat16* dst = out + (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + lane * W;
+#pragma unroll
+  for (int k = 0; k < W; k += 2)
+    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
+                     void* workspace, int* status, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  if (!encode_tile_map(&mq, q, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1) ||
+      !encode_tile_map(&mk, k, p.D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BN) ||
+      !encode_tile_map(&mv, v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BN))
+    return cudaErrorInvalidValue;
+  constexpr int smem = Smem<D>::BYTES > kOneBlockPerSmSmem ? Smem<D>::BYTES : kOneBlockPerSmSmem;
+  cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  float* part_o = static_cast<float*>(workspace);
+  float2* part_ml = p.splits > 1 ? reinterpret_cast<float2*>(part_o + (size_t)p.splits * p.rows * D) : nullptr;
+  auto* out = static_cast<__nv_bfloat16*>(o);
+  const long long blocks = attn_fwd_items(p) * p.splits;
+  attn_fwd_kernel<D><<<(unsigned)blocks, THREADS, smem, st>>>(p, out, lse, part_o, part_ml, status, mq, mk, mv);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
+  attn_merge_kernel<D><<<(unsigned)((p.rows + 7) / 8), 256, 0, st>>>(p, part_o, part_ml, out, lse);
+  return cudaGetLastError();
+}
+
+// No keys at all: O = 0, LSE = -inf.
+__global__ void attn_no_keys_kernel(const AttnProblem p, __nv_bfloat16* out, float* lse) {
+  const long long row = blockIdx.x;
+  const long long bh = row / p.NQ;
+  out[(bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + threadIdx.x] = __float2bfloat16_rn(0.f);
+  if (threadIdx.x == 0) lse[row] = kNegInf;
+}
+
+}  // namespace
+
+long long attn_fwd_items(const AttnProblem& p) {
+  return (long long)p.B * (p.packed ? p.HK : p.H) * p.q_items;
+}
+
+// Blocks of a split have at least this many key tiles: a split costs the second launch and a round trip of its
+// partial through L2, about as much as three or four tiles.
+constexpr int kMinTilesPerSplit = 4;
+void attn_fwd_plan(AttnProblem* p, int num_sms) {
+  p->packed = (long long)p->G * p->NQ <= BM;
+  p->q_items = p->packed ? 1 : (p->NQ + 2 * BM - 1) / (2 * BM);
+  p->rows = (long long)p->B * p->H * p->NQ;
+  const long long items = attn_fwd_items(*p);
+  const int tiles = (p->NK + BN - 1) / BN;
+  // the split count that needs the fewest tile times: waves x tiles of a block; more splits only for a gain
+  int best = 1;
+  double cost = (double)((items + num_sms - 1) / num_sms) * (tiles + 2);
+  for (int s = 2; s <= tiles / kMinTilesPerSplit && items * s <= 4ll * num_sms; ++s) {
+    const double c = (double)((items * s + num_sms - 1) / num_sms) * ((tiles + s - 1) / s + 2) + 3;
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  p->splits = best;
+}
+
+size_t attn_fwd_workspace(const AttnProblem& p) {
+  return p.splits > 1 ? (size_t)p.splits * p.rows * (p.D + 2) * sizeof(float) : 0;
+}
+
+cudaError_t launch_attn_fwd(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
+                            void* workspace, int* status, cudaStream_t st) {
+  if (p.NK == 0) {
+    attn_no_keys_kernel<<<(unsigned)p.rows, p.D, 0, st>>>(p, static_cast<__nv_bfloat16*>(o), lse);
+    return cudaGetLastError();
+  }
+  if (p.D == 64) return launch_d<64>(p, q, k, v, o, lse, workspace, status, st);
+  return launch_d<128>(p, q, k, v, o, lse, workspace, status, st);
+}
+
+}  // namespace skl

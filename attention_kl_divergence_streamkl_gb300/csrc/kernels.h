@@ -25,10 +25,10 @@ __host__ __device__ inline long long row_offset(int bh, int H, long long n, long
 }
 
 // Builds a 4-D TMA map {d, n, h, b} over a bf16 [B, H, N, D] view with the given
-// element strides (d contiguous), a {64, box_rows, 1, 1} box and the 128-byte
+// element strides (d contiguous), a {64, box_rows, box_heads, 1} box and the 128-byte
 // swizzle.  Returns false if the driver rejects it.
 bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, int B, long long sn, long long sh,
-                     long long sb, int box_rows);
+                     long long sb, int box_rows, int box_heads = 1);
 // A 3-D TMA map {d, row, bh} over an fp32 [BH][rows][D] accumulator, a {D, box_rows, 1} box, no swizzle
 // (for bulk reductions into it).
 bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows);
@@ -91,6 +91,26 @@ cudaError_t launch_zero_k_rows(const Problem& p, void* dk, cudaStream_t st);
 cudaError_t launch_rows_to_bf16(const Problem& p, const float* acc, void* out, cudaStream_t st);
 // First 128-query tile whose rows see key k0.
 int fused_first_qtile(const Problem& p, long long k0);
+
+// ---- attention -----------------------------------------------------------------------
+struct AttnProblem {
+  int B, H, HK, G, NQ, NK, D;  // G = H / HK query heads to a key head
+  int causal;                  // row i keeps key j iff j <= i + k_len - q_len
+  float scale, c;              // c = scale * log2(e)
+  const int *q_lens, *k_lens;  // device, [B], or null: every sequence has N_Q queries, N_K keys
+  // element strides along b, h, n of q (and dq), k (dk), v (dv), o (and do)
+  long long qs_b, qs_h, qs_n, ks_b, ks_h, ks_n, vs_b, vs_h, vs_n, os_b, os_h, os_n;
+  long long rows;              // B H N_Q
+  // forward plan (attn_fwd_plan)
+  int packed;   // the query heads of a key head share one tile
+  int q_items;  // blocks along the queries, per (batch, head)
+  int splits;   // blocks along the keys
+};
+void attn_fwd_plan(AttnProblem* p, int num_sms);
+long long attn_fwd_items(const AttnProblem& p);
+size_t attn_fwd_workspace(const AttnProblem& p);  // bytes, 0 without splits
+cudaError_t launch_attn_fwd(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
+                            void* workspace, int* status, cudaStream_t st);
 
 // ---- log probabilities of given tokens ---------------------------------------------
 constexpr int kTypeBf16 = 0, kTypeFp16 = 1, kTypeFp32 = 2;  // streamkl_dtype

@@ -300,6 +300,42 @@ int streamkl_bwd_mutual_select(streamkl_shape s, size_t l2_bytes, int num_sms);
 streamkl_status streamkl_bwd_mutual_workspace(streamkl_shape s, int bwd_mode, size_t* bytes);
 
 /*
+ * Attention: O = softmax(scale Q K^T) V with the rows' log-sum-exp, and its
+ * backward -- what a model whose attention is distilled runs beside the loss
+ * (its LSE is the loss's LSE_t for the same Q and K).
+ *
+ * Q [B, H, N_Q, D]; K, V [B, HK, N_K, D] with H a multiple of HK (query head h
+ * reads key head h / (H / HK)); O like Q; bf16, D 64 or 128.  LSE fp32
+ * [B, H, N_Q].  Strides as in streamkl_shape, each tensor its own (three zeros:
+ * contiguous); O's must not make rows overlap.
+ * q_lens, k_lens: device int32 [B], or NULL for whole sequences: sequence b has
+ * the first q_lens[b] of N_Q queries and k_lens[b] of N_K keys (values are kept
+ * within 0 .. N).  What lies past them is not used, whatever it holds, NaN
+ * included.  causal keeps key j for query i iff j <= i + k_len - q_len.
+ * A row that sees no key -- past its sequence, causal with more queries than
+ * keys, no keys at all -- has O = 0 and LSE = -inf.
+ * Workspace: fp32 partials of the key splits that few query tiles get, 0 bytes
+ * for most shapes; streamkl_attn_fwd_plan gives the choice for any SM count (a
+ * pure host rule): packed != 0 when all query heads of a key head share one
+ * 128-row tile, and the number of key splits.
+ */
+typedef struct {
+  int B, H, HK, NQ, NK, D;
+  float scale;
+  int causal;
+  const int* q_lens;
+  const int* k_lens;
+  long long q_stride_b, q_stride_h, q_stride_n;
+  long long k_stride_b, k_stride_h, k_stride_n;
+  long long v_stride_b, v_stride_h, v_stride_n;
+  long long o_stride_b, o_stride_h, o_stride_n;
+} streamkl_attn_shape;
+streamkl_status streamkl_attn_fwd_workspace(streamkl_attn_shape s, size_t* bytes);
+streamkl_status streamkl_attn_fwd_plan(streamkl_attn_shape s, int num_sms, int* packed, int* splits);
+streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, streamkl_attn_shape s, void* o,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Log probabilities of given tokens, with entropy and top alternatives: the
  * output-layer companion of the attention loss (a student scored on the data's
  * tokens, or on its teacher's most likely ones).

@@ -1,0 +1,93 @@
+"""Attention: what the entry points refuse and how the forward is planned, on the host before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import attention_kl_divergence_streamkl_gb300 as skl
+from attention_kl_divergence_streamkl_gb300 import _lib as K
+from attention_kl_divergence_streamkl_gb300 import build as B
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return K.lib()
+
+
+def ptr(off=0):
+    return ctypes.c_void_p(0x10000000 + off)
+
+
+OK = dict(B=2, H=8, HK=2, NQ=100, NK=100, D=64)
+BAD = [
+    (dict(B=0), K.ERR_INVALID), (dict(H=0), K.ERR_INVALID), (dict(HK=0), K.ERR_INVALID), (dict(HK=3), K.ERR_INVALID),
+    (dict(NQ=-1), K.ERR_INVALID), (dict(NK=-1), K.ERR_INVALID), (dict(D=0), K.ERR_INVALID),
+    (dict(D=96), K.ERR_UNSUPPORTED), (dict(D=256), K.ERR_UNSUPPORTED), (dict(NK=2**31 - 1), K.ERR_UNSUPPORTED),
+    (dict(scale=float("nan")), K.ERR_INVALID), (dict(scale=float("inf")), K.ERR_INVALID),
+    (dict(B=1 << 15, H=1 << 15, HK=1), K.ERR_UNSUPPORTED),
+    (dict(q_strides=(8, 8, 32)), K.ERR_INVALID), (dict(k_strides=(6400, 6401, 64)), K.ERR_INVALID),
+    (dict(v_strides=(-6400, 6400, 64)), K.ERR_INVALID), (dict(o_strides=(6400, 6400, 63)), K.ERR_INVALID),
+]
+
+
+@pytest.mark.parametrize("change,code", BAD)
+def test_fwd_refuses_shapes(lib, change, code):
+    s = K.make_attn_shape(**{**OK, **change})
+    assert lib.streamkl_attn_fwd(ptr(), ptr(), ptr(), s, ptr(), ptr(), None, 0, None) == code
+    assert lib.streamkl_attn_fwd_workspace(s, ctypes.byref(ctypes.c_size_t())) == code
+
+
+def test_fwd_refuses_pointers(lib):
+    s = K.make_attn_shape(**OK)
+    a = [ptr(64 * i) for i in range(5)]
+    for i in range(5):
+        for bad in (None, ptr(64 * i + 2)):
+            b = list(a)
+            b[i] = bad
+            assert lib.streamkl_attn_fwd(*b[:3], s, *b[3:], None, 0, None) == K.ERR_INVALID
+    s.q_lens = 0x1002
+    assert lib.streamkl_attn_fwd(*a[:3], s, *a[3:], None, 0, None) == K.ERR_INVALID
+
+
+def test_no_queries_is_no_work(lib):
+    s = K.make_attn_shape(**{**OK, "NQ": 0})
+    assert lib.streamkl_attn_fwd(None, None, None, s, None, None, None, 0, None) == K.OK
+
+
+@pytest.mark.parametrize("shape,want", [
+    (dict(B=1, H=32, HK=8, NQ=4096, NK=4096, D=128), (False, 1)),   # enough query tiles
+    (dict(B=1, H=8, HK=2, NQ=1, NK=129, D=64), (True, 1)),          # too short to split
+    (dict(B=1, H=8, HK=1, NQ=17, NK=300, D=64), (False, 1)),        # 136 packed rows do not fit one tile
+])
+def test_plan(lib, shape, want):
+    assert skl.attn_fwd_plan(**shape, num_sms=152) == want
+
+
+@pytest.mark.parametrize("NQ,H,HK,B,NK", [(1, 32, 8, 8, 131072), (1, 8, 8, 1, 131072), (4, 32, 8, 1, 4096), (300, 4, 4, 1, 65536)])
+def test_few_tiles_split_the_keys(lib, NQ, H, HK, B, NK):
+    """The launch fills the SMs without leaving a nearly empty last wave, and every split has keys."""
+    packed, splits = skl.attn_fwd_plan(B, H, HK, NQ, NK, 128, 152)
+    assert packed == (H // HK * NQ <= 128)
+    blocks = B * (HK if packed else H * -(-NQ // 256)) * splits
+    assert splits > 1 and -(-NK // 128) // splits >= 4
+    assert blocks / (152 * -(-blocks // 152)) > 0.6 or blocks < 152
+
+
+@pytest.mark.parametrize("q,k,v,lens,error", [
+    ((1, 4, 3, 64), (1, 3, 3, 64), (1, 3, 3, 64), None, ValueError),   # heads do not divide
+    ((1, 4, 3, 64), (1, 2, 3, 64), (1, 2, 4, 64), None, ValueError),   # k and v differ
+    ((1, 4, 3, 64), (2, 2, 3, 64), (2, 2, 3, 64), None, ValueError),   # batches differ
+    ((1, 4, 3, 64), (1, 2, 3, 128), (1, 2, 3, 128), None, ValueError),
+    ((4, 3, 64), (1, 2, 3, 64), (1, 2, 3, 64), None, ValueError),
+])
+def test_binding_refuses(q, k, v, lens, error):
+    q, k, v = (torch.zeros(x, dtype=torch.bfloat16) for x in (q, k, v))
+    with pytest.raises(error):
+        skl.attn_fwd(q, k, v)
+
+
+def test_binding_refuses_types():
+    q = torch.zeros(1, 2, 3, 64)
+    with pytest.raises(TypeError):
+        skl.attn_fwd(q, q, q)
