@@ -79,6 +79,8 @@ SIGNATURES = {
     "streamkl_attn_fwd_workspace": (_I, [AttnShape, ctypes.POINTER(_SZ)]),
     "streamkl_attn_fwd_plan": (_I, [AttnShape, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "streamkl_attn_fwd": (_I, [_P, _P, _P, AttnShape, _P, _F, _P, _SZ, _S]),
+    "streamkl_attn_bwd_workspace": (_I, [AttnShape, ctypes.POINTER(_SZ)]),
+    "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
     "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
@@ -497,6 +499,37 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
     _call("streamkl_attn_fwd", dev, _ptr(q), _ptr(k), _ptr(v), s, _ptr(o), _ptr(lse), _ptr(ws), nbytes)
     return _back((o, lse), host)
+
+
+def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None):
+    """Attention's gradients (dq, dk, dv), bf16 with the layouts of q, k, v.
+
+    o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
+    """
+    for t in (o, do):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("o, do must be bfloat16")
+        if t.shape != q.shape:
+            raise ValueError(f"o, do must be {tuple(q.shape)}")
+        if t.device != q.device:
+            raise ValueError("inputs on different devices")
+    q, k, v, q_lens, k_lens, qs, ks, vs, host = _attn_prep(q, k, v, q_lens, k_lens)
+    B, H, NQ, D = q.shape
+    NK, dev = k.shape[2], q.device
+    if host:
+        o, do = (t.contiguous().to(dev, non_blocking=True) for t in (o, do))
+    (o, os_), (do, ds) = _in_place(o), _in_place(do)
+    if os_ != ds:
+        o, do = (t.clone(memory_format=torch.contiguous_format) for t in (o, do))
+        os_ = _bhn_strides(o)
+    lse = _rows(lse, dev, (B, H, NQ), "lse")
+    dlse = _rows(dlse, dev, (B, H, NQ), "dlse")
+    s = make_attn_shape(B, H, k.shape[1], NQ, NK, D, scale, causal, q_lens, k_lens, qs, ks, vs, os_)
+    ws, nbytes = _workspace("streamkl_attn_bwd_workspace", s, dev)
+    dq, dk, dv = _grad_like(q, qs, NQ), _grad_like(k, ks, NK), _grad_like(v, vs, NK)
+    _call("streamkl_attn_bwd", dev, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dlse), s, _ptr(dq),
+          _ptr(dk), _ptr(dv), _ptr(ws), nbytes)
+    return _back((dq, dk, dv), host)
 
 
 def _logits_rows(logits, tokens):

@@ -61,6 +61,37 @@ def attention_kl(q1, k1, q2, k2, scale=None, causal=False, reduction="mean", bwd
     return _AttentionKL.apply(q1, k1, q2, k2, scale, causal, reduction, bwd_mode)
 
 
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, scale, causal, q_lens, k_lens):
+        o, lse = _lib.attn_fwd(q, k, v, scale, causal, q_lens, k_lens)
+        ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens)
+        ctx.scale, ctx.causal = scale, causal
+        ctx.set_materialize_grads(False)
+        return o, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, dlse):
+        q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
+        if do is None and dlse is None:
+            return (None,) * 7
+        if do is None:
+            do = torch.zeros_like(o)
+        return (*_lib.attn_bwd(q, k, v, o, lse, do, dlse, ctx.scale, ctx.causal, q_lens, k_lens), None, None, None, None)
+
+
+def attention(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, return_lse=False):
+    """softmax(scale Q K^T) V, differentiable: bf16 [B, H, N_Q, D], and with return_lse the rows' log-sum-exp
+    (fp32 [B, H, N_Q], differentiable too).
+
+    The attention of a model that is distilled with attention_kl, which takes the same q and k.  k and v may have
+    fewer heads than q; q_lens, k_lens (int32 [B]) are the lengths of a padded batch's sequences.  See attn_fwd.
+    """
+    o, lse = _Attention.apply(q, k, v, scale, causal, q_lens, k_lens)
+    return (o, lse) if return_lse else o
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, scale, top_k):

@@ -614,7 +614,7 @@ static streamkl_status attn_problem(const streamkl_attn_shape& s, AttnProblem* p
   if (s.D != 64 && s.D != 128) return STREAMKL_ERR_UNSUPPORTED;
   // one-dimensional grids over rows and over tiles of either side
   if ((long long)s.B * s.H > 0x7fffffffLL || (long long)s.B * s.H * (s.NQ + 128LL) > 0x7fffffffLL ||
-      (long long)s.B * s.H * (s.NK + 128LL) > 0x7fffffffLL * 64)
+      (long long)s.B * s.HK * (s.NK + 128LL) > 0x7fffffffLL)
     return STREAMKL_ERR_UNSUPPORTED;
   *p = AttnProblem{};
   p->B = s.B;
@@ -682,6 +682,35 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
   int* status = nullptr;
   if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
   return from_cuda(launch_attn_fwd(p, q, k, v, o, lse, workspace, status, static_cast<cudaStream_t>(stream)));
+}
+
+streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, size_t* bytes) {
+  AttnProblem p;
+  streamkl_status v = attn_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!bytes) return STREAMKL_ERR_INVALID;
+  *bytes = attn_bwd_workspace(p);
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                  const void* go, const float* dlse, streamkl_attn_shape s, void* dq, void* dk,
+                                  void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+  AttnProblem p;
+  streamkl_status st = attn_problem(s, &p);
+  if (st != STREAMKL_OK) return st;
+  if (p.NQ > 0 && (!dq || !aligned16(dq))) return STREAMKL_ERR_INVALID;
+  if (p.NK > 0 && (!dk || !dv || !aligned16(dk) || !aligned16(dv))) return STREAMKL_ERR_INVALID;
+  if (p.NQ > 0 && p.NK > 0) {
+    if (!q || !k || !v || !o || !go || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+        !aligned16(go) || !rows_ok(lse) || !aligned_to_or_null(dlse, 4))
+      return STREAMKL_ERR_INVALID;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < attn_bwd_workspace(p)) return STREAMKL_ERR_WORKSPACE;
+  }
+  int* status = nullptr;
+  if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
+  return from_cuda(launch_attn_bwd(p, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, status,
+                                   static_cast<cudaStream_t>(stream)));
 }
 
 static streamkl_status logprobs_problem(int dtype, long long rows, long long vocab, long long row_stride,

@@ -1,0 +1,782 @@
+// Attention backward: dQ, dK, dV from Q, K, V, O, dO and the saved log-sum-exp,
+// on the 5th-generation tensor cores.
+//
+// The probabilities are rebuilt tile by tile, P = exp(S - LSE), and with
+// dP = dO V^T, delta_i = dO_i . O_i - dLSE_i (which is sum_j P_ij dP_ij, the
+// softmax's coupling, less the gradient of the LSE itself):
+//     dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
+// Two kinds of block, each output written by one block, so no atomics and the
+// same bits on every run:
+//   dK/dV block  128 keys stationary; streams the query tiles of every query
+//                head that reads them: four products a tile pair
+//   dQ block     128 queries stationary; streams the key tiles: three products
+// (seven where one visit of each tile pair would need five; that visit's dQ
+// would go through fp32 reductions in L2, 64 KB a tile pair, which alone take
+// longer than the two products saved).  Both kinds run in one launch, the
+// kind with the longer blocks first: the shorter ones fill the SMs that the
+// longer ones leave.
+//
+// A small kernel first writes, per query row, -LSE log2(e) and delta, 128-row
+// padded so that a tile's 128 values are one bulk copy.  Rows that see no key,
+// and rows past a sequence's length, get -inf and 0: their P is exactly 0.
+#include "attn.cuh"
+
+namespace skl {
+namespace {
+
+constexpr int BT = 128;  // keys and queries of a tile
+constexpr int DS_WARPS = 16;
+constexpr int PRODUCER_WARP = 16, MMA_WARP = 17, PATCH_WARP = 18;
+constexpr int THREADS = 20 * 32;
+constexpr int kRegsDs = 104, kRegsOther = 64;  // 512 * 104 + 128 * 64 = 640 * 96 registers at launch
+constexpr uint32_t kTmemCols = 512;
+
+struct BwdOut {
+  __nv_bfloat16 *dq, *dk, *dv;
+};
+
+// ---------------------------------------------------------------------------
+// Row values: nlse = -LSE log2(e), delta = dO . O - dLSE.  A row takes D / 8
+// lanes of 16 bytes; bound by the read of O and dO.
+template <int D>
+__global__ void __launch_bounds__(256)
+    attn_rows_kernel(const AttnProblem p, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ go,
+                     const float* __restrict__ lse, const float* __restrict__ dlse, float* __restrict__ nlse,
+                     float* __restrict__ delta, int padded) {
+  constexpr int LANES = D / 8, ROWS = 256 / LANES;
+  const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / LANES;  // row of [B H][padded]
+  const int lane = threadIdx.x % LANES;
+  const long long bh = r / padded;
+  const int n = (int)(r % padded);
+  if (bh >= (long long)p.B * p.H) return;  // a whole group of lanes leaves together
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  float sum = 0.f, l = kNegInf;
+  const bool real = n < seq_len(p.q_lens, b, p.NQ);
+  if (real) {
+    const long long at = b * p.os_b + h * p.os_h + n * p.os_n + lane * 8;
+    const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(go + at);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), sum);
+      sum = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), sum);
+    }
+    l = lse[bh * p.NQ + n];
+  }
+  const unsigned group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
+#pragma unroll
+  for (int w = LANES / 2; w; w >>= 1) sum += __shfl_xor_sync(group, sum, w);
+  if (lane == 0) {
+    const bool none = l == kNegInf;
+    nlse[r] = none ? kNegInf : -l * kLog2e;
+    delta[r] = none ? 0.f : dlse ? sum - dlse[bh * p.NQ + n] : sum;
+  }
+}
+
+// One row of an accumulator tile (32 of its columns) as bf16, `f` times the fp32 values.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&a)[32], float f) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(__uint_as_float(a[8 * v + 2 * e]) * f, __uint_as_float(a[8 * v + 2 * e + 1]) * f);
+    reinterpret_cast<uint4*>(dst)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dK/dV block.  The logits are computed transposed, so the TMEM lanes are keys
+// and the columns queries: S^T = K Q^T and dP^T = V dO^T (both operands K-major
+// in shared memory).  P^T and dS^T (bf16 pairs) overwrite their logits and are
+// the A operands of dV += P^T dO and dK += dS^T Q, which read dO and Q
+// MN-major from the tiles that are there already: neither P nor dS passes
+// through shared memory.
+//   TMEM: S^T/P^T [0,128), dP^T/dS^T [128,256), dV [256, 256+D), dK [384, 384+D)
+//   warps 0-15  thread = key, group g = warp / 4 takes queries [32g, 32g+32); its
+//               pairs go to the first 16 of its own 32 columns
+//   warp 16     TMA producer: K, V once; Q(u) with its nlse, dO(u) with its delta
+//   warp 17     TMEM owner and MMA issuer: dV(u), S(u+1), dK(u), dP(u+1): while the
+//               warps turn S(u+1) into P, the pipe runs dK(u) and dP(u+1), and
+//               while they form dS(u+1) it runs dV(u+1) and S(u+2)
+//   warp 18     clears the rows of Q and dO tiles past a sequence's length
+namespace kv {
+constexpr int SLOTS = 2;
+constexpr uint32_t kColS = 0, kColP = 128, kColV = 256, kColK = 384;
+template <int D>
+struct Smem {
+  static constexpr int TILE = BT * D * 2;
+  static constexpr int OFF_K = 0, OFF_V = TILE;
+  static constexpr int OFF_Q = 2 * TILE;                 // Q slots
+  static constexpr int OFF_O = OFF_Q + SLOTS * TILE;     // dO slots
+  static constexpr int OFF_NL = OFF_O + SLOTS * TILE;    // nlse slots, 512 B each
+  static constexpr int OFF_DL = OFF_NL + SLOTS * 512;    // delta slots
+  static constexpr int OFF_BAR = OFF_DL + SLOTS * 512;
+  // kv_full, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, g_done, to_patch, patched
+  static constexpr int BAR_SLOT = 8 * 16;
+  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
+};
+static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+}  // namespace kv
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+template <int D>
+__device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __restrict__ nlse,
+                                         const float* __restrict__ delta, int padded, const BwdOut& out, int* status,
+                                         const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                         const CUtensorMap& mo, const unsigned blk) {
+  using L = kv::Smem<D>;
+  using kv::SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // heads in order (the blocks in flight share one key head's query tiles in L2); within a head the first key
+  // tiles, which see the most queries under a causal mask, first
+  const int n_kt = (p.NK + BT - 1) / BT;
+  const int bhk = (int)(blk / n_kt);
+  const int b = bhk / p.HK, hk = bhk % p.HK;
+  const int k0 = (int)(blk % n_kt) * BT;
+  const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
+  const int off = kl - ql;
+  const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
+  const int n_qt = (k0 < kl && q_begin < ql) ? (ql - q_begin + BT - 1) / BT : 0;
+  const int n = p.G * n_qt;  // tile u: head u / n_qt of the group, query tile u % n_qt
+  const bool ragged = n > 0 && ql < p.NQ && (ql & (BT - 1));  // the last query tile has rows past the sequence
+
+  const uint32_t bar = sb + L::OFF_BAR;
+  const uint32_t kv_full = bar, q_full = bar + 8, q_empty = bar + 24, o_full = bar + 40, o_empty = bar + 56,
+                 s_full = bar + 72, dp_full = bar + 80, p_full = bar + 88, ds_full = bar + 96, g_done = bar + 104,
+                 to_patch = bar + 112, patched = bar + 120, slot = bar + L::BAR_SLOT;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(q_full + 8 * s, 1);
+      mbar_init(q_empty + 8 * s, 1);
+      mbar_init(o_full + 8 * s, 1);
+      mbar_init(o_empty + 8 * s, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, DS_WARPS);
+    mbar_init(ds_full, DS_WARPS);
+    mbar_init(g_done, 1);
+    mbar_init(to_patch, 1);
+    mbar_init(patched, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+
+  if (warp >= DS_WARPS) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == PRODUCER_WARP) {
+      if (lane == 0 && n > 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_4d(sb + L::OFF_K + h * BT * 128, &mk, kv_full, h * 64, k0, hk, b);
+          tma_load_4d(sb + L::OFF_V + h * BT * 128, &mv, kv_full, h * 64, k0, hk, b);
+        }
+        int issued_q = 0, issued_o = 0;
+        for (int u = 0; u < n; ++u) {
+          const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+          const long long row = ((long long)b * p.H + hq) * padded + q0;
+          if (u >= SLOTS && !mbar_wait(q_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + 512);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &mq, q_full + 8 * s, h * 64, q0, hq, b);
+          bulk_load(sb + L::OFF_NL + s * 512, nlse + row, 512, q_full + 8 * s);
+          issued_q = u + 1;
+          if (u >= SLOTS && !mbar_wait(o_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + 512);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &mo, o_full + 8 * s, h * 64, q0, hq, b);
+          bulk_load(sb + L::OFF_DL + s * 512, delta + row, 512, o_full + 8 * s);
+          issued_o = u + 1;
+        }
+        mbar_drain(kv_full, 0, status);
+        for (int u = max(0, issued_q - SLOTS); u < issued_q; ++u)
+          mbar_drain(q_full + 8 * (u % SLOTS), (u / SLOTS) & 1, status);
+        for (int u = max(0, issued_o - SLOTS); u < issued_o; ++u)
+          mbar_drain(o_full + 8 * (u % SLOTS), (u / SLOTS) & 1, status);
+      }
+      __syncwarp();
+    } else if (warp == PATCH_WARP) {
+      // for each head of the group: its last Q tile, then its last dO tile, when the MMA thread has seen them land
+      if (ragged) {
+        for (int e = 0; e < 2 * p.G; ++e) {
+          if (!mbar_wait_warp(to_patch, e & 1, status, abort_flag)) break;
+          const int s = ((e / 2 + 1) * n_qt - 1) % SLOTS, from = ql & (BT - 1);
+          const uint32_t tile = sb + ((e & 1) ? L::OFF_O : L::OFF_Q) + s * L::TILE;
+          for (int i = lane; i < (BT - from) * (D / 8); i += 32)
+            st_shared_zero16(sw128<BT>(tile, from + i / (D / 8), i % (D / 8)));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(patched);
+        }
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
+        constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
+        const uint64_t kd = sdesc_sw128(sb + L::OFF_K, 0, 1024), vd = sdesc_sw128(sb + L::OFF_V, 0, 1024);
+        int patches = 0;
+        auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
+          if (!ragged || (u + 1) % n_qt) return true;
+          mbar_arrive(to_patch);
+          return mbar_wait(patched, patches++ & 1, status, abort_flag);
+        };
+        auto issue_s = [&](int u) {  // S^T(u) = K Q^T
+          const int s = u % SLOTS;
+          if (!mbar_wait(q_full + 8 * s, (u / SLOTS) & 1, status, abort_flag) || !patch(u)) return false;
+          tc_fence_after();
+          const uint64_t qd = sdesc_sw128(sb + L::OFF_Q + s * L::TILE, 0, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
+            mma_ss(tmem + kv::kColS, sdesc_add(kd, o), sdesc_add(qd, o), id_s, ks > 0);
+          }
+          mma_commit(s_full);
+          return true;
+        };
+        auto issue_dp = [&](int u) {  // dP^T(u) = V dO^T
+          const int s = u % SLOTS;
+          if (!mbar_wait(o_full + 8 * s, (u / SLOTS) & 1, status, abort_flag) || !patch(u)) return false;
+          tc_fence_after();
+          const uint64_t od = sdesc_sw128(sb + L::OFF_O + s * L::TILE, 0, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
+            mma_ss(tmem + kv::kColP, sdesc_add(vd, o), sdesc_add(od, o), id_s, ks > 0);
+          }
+          mma_commit(dp_full);
+          return true;
+        };
+        // G += A B: A = pairs in TMEM (16 queries = 8 columns; a group's 32 queries lie in 32 columns' first 16)
+        auto issue_g = [&](uint32_t g_col, uint32_t a_col, uint32_t tile, bool first) {
+          const uint64_t bd = sdesc_sw128(tile, BT * 128, 1024);
+#pragma unroll
+          for (int ks = 0; ks < BT / 16; ++ks)
+            mma_ts(tmem + g_col, tmem + a_col + 32 * (ks >> 1) + 8 * (ks & 1), sdesc_add(bd, ks * 2048), id_g,
+                   !first || ks > 0);
+        };
+        bool ok = mbar_wait(kv_full, 0, status, abort_flag) && issue_s(0) && issue_dp(0);
+        for (int u = 0; ok && u < n; ++u) {
+          const int s = u % SLOTS;
+          if (!mbar_wait(p_full, u & 1, status, abort_flag)) break;
+          tc_fence_after();
+          issue_g(kv::kColV, kv::kColS, sb + L::OFF_O + s * L::TILE, u == 0);  // dV += P^T dO
+          mma_commit(o_empty + 8 * s);
+          if (u + 1 < n && !(ok = issue_s(u + 1))) break;
+          if (!mbar_wait(ds_full, u & 1, status, abort_flag)) break;
+          tc_fence_after();
+          issue_g(kv::kColK, kv::kColP, sb + L::OFF_Q + s * L::TILE, u == 0);  // dK += dS^T Q
+          mma_commit(q_empty + 8 * s);
+          if (u + 1 < n) ok = issue_dp(u + 1);
+        }
+        mma_commit(g_done);
+        mbar_drain(g_done, 0, status);
+      }
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsDs>();
+    const int grp = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const int key = k0 + r;
+    const float c = p.c;
+    const float2 cc = make_float2(c, c);
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t ts = tmem + lanes + kv::kColS + 32 * grp, tp = tmem + lanes + kv::kColP + 32 * grp;
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      const int s = u % SLOTS, ph = (u / SLOTS) & 1;
+      const int q0 = q_begin + (u % n_qt) * BT + 32 * grp;  // first query of this warp's columns
+      const uint32_t nl = sb + L::OFF_NL + s * 512 + grp * 128, dl = sb + L::OFF_DL + s * 512 + grp * 128;
+      ok = mbar_wait_warp(s_full, u & 1, status, abort_flag) && mbar_wait_warp(q_full + 8 * s, ph, status, abort_flag);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t a[32];
+      tmem_ld32(ts, a);
+      tmem_ld_wait();
+      reg_fence32(a);
+      // P = 2^(c S + nlse): 0 for rows without keys and past the sequence, whose nlse is -inf
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 nv = ld_shared_f4(nl + 4 * i);
+        const float2 x0 = ffma2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc, make_float2(nv.x, nv.y));
+        const float2 x1 =
+            ffma2(make_float2(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), cc, make_float2(nv.z, nv.w));
+        a[i] = __float_as_uint(ex2(x0.x));
+        a[i + 1] = __float_as_uint(ex2(x0.y));
+        a[i + 2] = __float_as_uint(ex2(x1.x));
+        a[i + 3] = __float_as_uint(ex2(x1.y));
+      }
+      const int hidden = key >= kl ? 32 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
+      if (__any_sync(0xffffffffu, hidden > 0)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < hidden) a[i] = 0u;
+      }
+      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+      tmem_st16(ts, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag) && mbar_wait_warp(o_full + 8 * s, ph, status, abort_flag);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t d[16];
+        tmem_ld16(tp + 16 * hf, d);
+        tmem_ld_wait();
+        reg_fence16(d);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 dv = ld_shared_f4(dl + 4 * (16 * hf + i));
+          const int j = 16 * hf + i;
+          const float2 e0 = fmul2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
+                                  fsub2(make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), make_float2(dv.x, dv.y)));
+          const float2 e1 = fmul2(make_float2(__uint_as_float(a[j + 2]), __uint_as_float(a[j + 3])),
+                                  fsub2(make_float2(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), make_float2(dv.z, dv.w)));
+          pk[j / 2] = pack_bf16(e0.x, e0.y);
+          pk[j / 2 + 1] = pack_bf16(e1.x, e1.y);
+        }
+      }
+      tmem_st16(tp, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    // ---- out: thread = key row, group g writes d columns [32g, 32g + 32) of both
+    bool got = ok;
+    if (n > 0 && ok) {
+      got = mbar_wait_warp(g_done, 0, status, abort_flag);
+      __syncwarp();
+    }
+    if (got && grp * 32 < D) {
+      tc_fence_after();
+      const long long kat = b * p.ks_b + hk * p.ks_h + (long long)key * p.ks_n + grp * 32;
+      const long long vat = b * p.vs_b + hk * p.vs_h + (long long)key * p.vs_n + grp * 32;
+      uint32_t g[32];
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (n > 0) {
+          tmem_ld32(tmem + lanes + (which ? kv::kColK : kv::kColV) + 32 * grp, g);
+          tmem_ld_wait();
+          reg_fence32(g);
+        }
+        if (n == 0 || key >= kl) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = 0u;
+        }
+        if (key < p.NK) store_row32(which ? out.dk + kat : out.dv + vat, g, which ? p.scale : 1.f);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dQ block.  The TMEM lanes are queries: a thread owns a row and holds its nlse
+// and delta.  S = Q K^T and dP = dO V^T are copied into registers and released
+// at once, so the next tile's products run while dS is formed; dS (bf16 pairs)
+// goes to a double buffer in TMEM, the A operand of dQ += dS K.
+//   TMEM: S [0,128), dP [128,256), dS [256,320) and [320,384), dQ [384, 384+D)
+//   warps 0-15  thread = query, group g = warp / 4 takes keys [32g, 32g+32)
+//   warp 16     TMA producer: Q, dO once; K (held until dQ's product) through three
+//               slots, V through two
+//   warp 17     TMEM owner and MMA issuer: S(j), dP(j), then dQ(j-1)
+//   warp 18     clears the rows of the K tile past a sequence's key length
+namespace qq {
+constexpr int K_SLOTS = 3, V_SLOTS = 2;
+constexpr uint32_t kColS = 0, kColP = 128, kColDS = 256, kColG = 384;
+template <int D>
+struct Smem {
+  static constexpr int TILE = BT * D * 2;
+  static constexpr int OFF_Q = 0, OFF_O = TILE;
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + K_SLOTS * TILE;
+  static constexpr int OFF_BAR = OFF_V + V_SLOTS * TILE;
+  // x_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full, s_free, ds_full[2], ds_free[2], g_done, to_patch,
+  // patched
+  static constexpr int BAR_SLOT = 8 * 20;
+  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
+};
+static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+}  // namespace qq
+
+// dS of 16 columns: a, d = S, dP; `seen` of them are visible.
+template <bool MASKED>
+__device__ __forceinline__ void ds16(const uint32_t (&a)[16], const uint32_t (&d)[16], uint32_t* pk, float c, float nlse,
+                                     float delta, int seen) {
+  const float2 cc = make_float2(c, c), nl = make_float2(nlse, nlse), dl = make_float2(delta, delta);
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float2 x = ffma2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc, nl);
+    float2 e = fmul2(make_float2(ex2(x.x), ex2(x.y)),
+                     fsub2(make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), dl));
+    if (MASKED) {
+      e.x = i < seen ? e.x : 0.f;
+      e.y = i + 1 < seen ? e.y : 0.f;
+    }
+    pk[i / 2] = pack_bf16(e.x, e.y);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void q_block(const AttnProblem& p, const float* __restrict__ nlse,
+                                        const float* __restrict__ delta, int padded, const BwdOut& out, int* status,
+                                        const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                        const CUtensorMap& mo, const unsigned blk) {
+  using L = qq::Smem<D>;
+  using qq::K_SLOTS;
+  using qq::V_SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_qt = (p.NQ + BT - 1) / BT;
+  const int bh = (int)(blk / n_qt);
+  const int b = bh / p.H, h = bh % p.H, hk = h / p.G;
+  const int q0 = (n_qt - 1 - (int)(blk % n_qt)) * BT;  // the last query tiles, which see the most keys, first
+  const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
+  const int off = kl - ql;
+  const int last = min(q0 + BT, ql) - 1;
+  const int end = q0 < ql ? (p.causal ? min(kl, last + off + 1) : kl) : 0;
+  const int n = end > 0 ? (end + BT - 1) / BT : 0;
+  const int patch_j = (kl < p.NK && (kl & (BT - 1))) ? kl / BT : -1;  // the K tile with rows past the sequence
+
+  const uint32_t bar = sb + L::OFF_BAR;
+  const uint32_t x_full = bar, k_full = bar + 8, k_empty = bar + 32, v_full = bar + 56, v_empty = bar + 72,
+                 s_full = bar + 88, s_free = bar + 96, ds_full = bar + 104, ds_free = bar + 120, g_done = bar + 136,
+                 to_patch = bar + 144, patched = bar + 152, slot = bar + L::BAR_SLOT;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+  if (threadIdx.x == 0) {
+    mbar_init(x_full, 1);
+    for (int s = 0; s < K_SLOTS; ++s) {
+      mbar_init(k_full + 8 * s, 1);
+      mbar_init(k_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(v_full + 8 * s, 1);
+      mbar_init(v_empty + 8 * s, 1);
+      mbar_init(ds_full + 8 * s, DS_WARPS);
+      mbar_init(ds_free + 8 * s, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, DS_WARPS);
+    mbar_init(g_done, 1);
+    mbar_init(to_patch, 1);
+    mbar_init(patched, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+
+  if (warp >= DS_WARPS) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == PRODUCER_WARP) {
+      if (lane == 0 && n > 0) {
+        mbar_arrive_expect_tx(x_full, 2 * L::TILE);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) {
+          tma_load_4d(sb + L::OFF_Q + d * BT * 128, &mq, x_full, d * 64, q0, h, b);
+          tma_load_4d(sb + L::OFF_O + d * BT * 128, &mo, x_full, d * 64, q0, h, b);
+        }
+        int issued_k = 0, issued_v = 0;
+        for (int j = 0; j < n; ++j) {
+          const int sk = j % K_SLOTS, sv = j % V_SLOTS;
+          if (j >= K_SLOTS && !mbar_wait(k_empty + 8 * sk, ((j / K_SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(k_full + 8 * sk, L::TILE);
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+            tma_load_4d(sb + L::OFF_K + sk * L::TILE + d * BT * 128, &mk, k_full + 8 * sk, d * 64, j * BT, hk, b);
+          issued_k = j + 1;
+          if (j >= V_SLOTS && !mbar_wait(v_empty + 8 * sv, ((j / V_SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(v_full + 8 * sv, L::TILE);
+#pragma unroll
+          for (int d = 0; d < D / 64; ++d)
+            tma_load_4d(sb + L::OFF_V + sv * L::TILE + d * BT * 128, &mv, v_full + 8 * sv, d * 64, j * BT, hk, b);
+          issued_v = j + 1;
+        }
+        mbar_drain(x_full, 0, status);
+        for (int j = max(0, issued_k - K_SLOTS); j < issued_k; ++j)
+          mbar_drain(k_full + 8 * (j % K_SLOTS), (j / K_SLOTS) & 1, status);
+        for (int j = max(0, issued_v - V_SLOTS); j < issued_v; ++j)
+          mbar_drain(v_full + 8 * (j % V_SLOTS), (j / V_SLOTS) & 1, status);
+      }
+      __syncwarp();
+    } else if (warp == PATCH_WARP) {
+      if (patch_j >= 0 && patch_j < n && mbar_wait_warp(to_patch, 0, status, abort_flag)) {
+        const int from = kl & (BT - 1);
+        for (int i = lane; i < (BT - from) * (D / 8); i += 32)
+          st_shared_zero16(sw128<BT>(sb + L::OFF_K + (patch_j % K_SLOTS) * L::TILE, from + i / (D / 8), i % (D / 8)));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(patched);
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
+        constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
+        const uint64_t qd = sdesc_sw128(sb + L::OFF_Q, 0, 1024), od = sdesc_sw128(sb + L::OFF_O, 0, 1024);
+        bool ok = mbar_wait(x_full, 0, status, abort_flag);
+        for (int j = 0; ok && j <= n; ++j) {
+          if (j < n) {
+            const int sk = j % K_SLOTS, sv = j % V_SLOTS;
+            if (!mbar_wait(k_full + 8 * sk, (j / K_SLOTS) & 1, status, abort_flag)) break;
+            if (j == patch_j) {
+              mbar_arrive(to_patch);
+              if (!mbar_wait(patched, 0, status, abort_flag)) break;
+            }
+            if (!mbar_wait(v_full + 8 * sv, (j / V_SLOTS) & 1, status, abort_flag)) break;
+            if (j >= 1 && !mbar_wait(s_free, (j - 1) & 1, status, abort_flag)) break;
+            tc_fence_after();
+            const uint64_t kd = sdesc_sw128(sb + L::OFF_K + sk * L::TILE, 0, 1024);
+            const uint64_t vd = sdesc_sw128(sb + L::OFF_V + sv * L::TILE, 0, 1024);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
+              mma_ss(tmem + qq::kColS, sdesc_add(qd, o), sdesc_add(kd, o), id_s, ks > 0);
+            }
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
+              mma_ss(tmem + qq::kColP, sdesc_add(od, o), sdesc_add(vd, o), id_s, ks > 0);
+            }
+            mma_commit(s_full);
+            mma_commit(v_empty + 8 * sv);
+          }
+          if (j >= 1) {
+            const int jj = j - 1, bf = jj & 1;
+            if (!mbar_wait(ds_full + 8 * bf, (jj >> 1) & 1, status, abort_flag)) break;
+            tc_fence_after();
+            const uint64_t kd = sdesc_sw128(sb + L::OFF_K + (jj % K_SLOTS) * L::TILE, BT * 128, 1024);
+#pragma unroll
+            for (int ks = 0; ks < BT / 16; ++ks)
+              mma_ts(tmem + qq::kColG, tmem + qq::kColDS + 64 * bf + 8 * ks, sdesc_add(kd, ks * 2048), id_g,
+                     jj > 0 || ks > 0);
+            mma_commit(k_empty + 8 * (jj % K_SLOTS));
+            mma_commit(ds_free + 8 * bf);
+          }
+        }
+        mma_commit(g_done);
+        mbar_drain(g_done, 0, status);
+      }
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsDs>();
+    const int grp = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const int q = q0 + r;
+    const float c = p.c;
+    float nl = kNegInf, dl = 0.f;
+    if (q < p.NQ) {
+      nl = nlse[(size_t)bh * padded + q];
+      dl = delta[(size_t)bh * padded + q];
+    }
+    const int row_end = q < ql ? (p.causal ? min(kl, q + off + 1) : kl) : 0;  // keys this row sees
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t tcol = tmem + lanes + grp * 32;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int bf = j & 1;
+      ok = mbar_wait_warp(s_full, j & 1, status, abort_flag);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+      const int seen = row_end - (j * BT + grp * 32);
+      const bool masked = __any_sync(0xffffffffu, seen < 32);
+      uint32_t pk[16];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t a[16], d[16];
+        tmem_ld16(tcol + qq::kColS + 16 * hf, a);
+        tmem_ld16(tcol + qq::kColP + 16 * hf, d);
+        tmem_ld_wait();
+        reg_fence16(a);
+        reg_fence16(d);
+        if (hf == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+        }
+        if (masked)
+          ds16<true>(a, d, pk + 8 * hf, c, nl, dl, seen - 16 * hf);
+        else
+          ds16<false>(a, d, pk + 8 * hf, c, nl, dl, 16);
+        if (hf == 0)  // first half final before the second half is read
+          asm volatile("" : "+r"(pk[0]), "+r"(pk[1]), "+r"(pk[2]), "+r"(pk[3]), "+r"(pk[4]), "+r"(pk[5]),
+                       "+r"(pk[6]), "+r"(pk[7])::"memory");
+      }
+      reg_fence16(pk);
+      if (j >= 2) {  // this dS buffer's last product is done
+        ok = mbar_wait_warp(ds_free + 8 * bf, ((j >> 1) - 1) & 1, status, abort_flag);
+        __syncwarp();
+        if (!ok) break;
+      }
+      tc_fence_after();
+      tmem_st16(tmem + lanes + qq::kColDS + 64 * bf + 16 * grp, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full + 8 * bf);
+    }
+    bool got = ok;
+    if (n > 0 && ok) {
+      got = mbar_wait_warp(g_done, 0, status, abort_flag);
+      __syncwarp();
+    }
+    if (got && grp * 32 < D) {
+      tc_fence_after();
+      uint32_t g[32];
+      if (n > 0) {
+        tmem_ld32(tmem + lanes + qq::kColG + grp * 32, g);
+        tmem_ld_wait();
+        reg_fence32(g);
+      }
+      if (row_end <= 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) g[i] = 0u;
+      }
+      if (q < p.NQ)
+        store_row32(out.dq + b * p.qs_b + h * p.qs_h + (long long)q * p.qs_n + grp * 32, g, p.scale);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_bwd_kernel(const AttnProblem p, const float* __restrict__ nlse, const float* __restrict__ delta, int padded,
+                    const BwdOut out, int* status, const __grid_constant__ CUtensorMap mq,
+                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                    const __grid_constant__ CUtensorMap mo, const unsigned n_first, const int q_first) {
+  const unsigned x = blockIdx.x;
+  const bool is_q = q_first ? x < n_first : x >= n_first;
+  const unsigned blk = x < n_first ? x : x - n_first;
+  if (is_q)
+    q_block<D>(p, nlse, delta, padded, out, status, mq, mk, mv, mo, blk);
+  else
+    kv_block<D>(p, nlse, delta, padded, out, status, mq, mk, mv, mo, blk);
+}
+
+// Zeros for `rows` rows of each of B H heads (a backward without queries or without keys).
+__global__ void attn_zero_rows_kernel(__nv_bfloat16* dst, int H, int rows, int D, long long sb, long long sh,
+                                      long long sn) {
+  const long long r = blockIdx.x;
+  dst[r / rows / H * sb + r / rows % H * sh + r % rows * sn + threadIdx.x] = __float2bfloat16_rn(0.f);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
+                     int* status, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, mo;
+  if (!encode_tile_map(&mq, in.q, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, BT) ||
+      !encode_tile_map(&mk, in.k, p.D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
+      !encode_tile_map(&mv, in.v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
+      !encode_tile_map(&mo, in.go, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, BT))
+    return cudaErrorInvalidValue;
+  const int padded = (p.NQ + BT - 1) / BT * BT;
+  const long long rows = (long long)p.B * p.H * padded;
+  float* nlse = static_cast<float*>(workspace);
+  float* delta = nlse + rows;
+  constexpr int row_lanes = D / 8, per_block = 256 / row_lanes;
+  attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
+      p, static_cast<const __nv_bfloat16*>(in.o), static_cast<const __nv_bfloat16*>(in.go), in.lse, in.dlse, nlse, delta,
+      padded);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  int smem = kOneBlockPerSmSmem;
+  if (kv::Smem<D>::BYTES > smem) smem = kv::Smem<D>::BYTES;
+  if (qq::Smem<D>::BYTES > smem) smem = qq::Smem<D>::BYTES;
+  auto kern = attn_bwd_kernel<D>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  const long long q_blocks = (long long)p.B * p.H * (padded / BT);
+  const long long kv_blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
+  const BwdOut out{static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv)};
+  // a dQ block walks the keys with three products a tile, a dK/dV block the queries of G heads with four
+  const int q_first = 3ll * p.NK > 4ll * p.G * p.NQ;
+  kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, nlse, delta, padded, out, status, mq, mk, mv, mo,
+                                                                (unsigned)(q_first ? q_blocks : kv_blocks), q_first);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace(const AttnProblem& p) {
+  if (p.NQ == 0 || p.NK == 0) return 0;
+  return (size_t)p.B * p.H * ((p.NQ + BT - 1) / BT * BT) * 2 * sizeof(float);
+}
+
+cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
+                            int* status, cudaStream_t st) {
+  if (p.NQ == 0 || p.NK == 0) {
+    auto* q = static_cast<__nv_bfloat16*>(dq);
+    auto* k = static_cast<__nv_bfloat16*>(dk);
+    auto* v = static_cast<__nv_bfloat16*>(dv);
+    if (p.NQ > 0)
+      attn_zero_rows_kernel<<<(unsigned)((long long)p.B * p.H * p.NQ), p.D, 0, st>>>(q, p.H, p.NQ, p.D, p.qs_b, p.qs_h,
+                                                                                    p.qs_n);
+    if (p.NK > 0) {
+      const unsigned n = (unsigned)((long long)p.B * p.HK * p.NK);
+      attn_zero_rows_kernel<<<n, p.D, 0, st>>>(k, p.HK, p.NK, p.D, p.ks_b, p.ks_h, p.ks_n);
+      attn_zero_rows_kernel<<<n, p.D, 0, st>>>(v, p.HK, p.NK, p.D, p.vs_b, p.vs_h, p.vs_n);
+    }
+    return cudaGetLastError();
+  }
+  if (p.D == 64) return launch_d<64>(p, in, dq, dk, dv, workspace, status, st);
+  return launch_d<128>(p, in, dq, dk, dv, workspace, status, st);
+}
+
+}  // namespace skl

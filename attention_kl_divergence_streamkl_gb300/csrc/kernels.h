@@ -112,6 +112,14 @@ size_t attn_fwd_workspace(const AttnProblem& p);  // bytes, 0 without splits
 cudaError_t launch_attn_fwd(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
                             void* workspace, int* status, cudaStream_t st);
 
+struct AttnBwdIn {
+  const void *q, *k, *v, *o, *go;  // go = dO, with o's strides
+  const float *lse, *dlse;         // dlse may be null
+};
+size_t attn_bwd_workspace(const AttnProblem& p);
+cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
+                            int* status, cudaStream_t st);
+
 // ---- log probabilities of given tokens ---------------------------------------------
 constexpr int kTypeBf16 = 0, kTypeFp16 = 1, kTypeFp32 = 2;  // streamkl_dtype
 struct LogprobsProblem {

@@ -336,6 +336,23 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
                                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Attention backward: with P = exp(scale Q K^T - LSE) rebuilt from the saved LSE,
+ * dP = dO V^T, delta_i = dO_i . O_i - dLSE_i and dS = P (dP - delta):
+ *     dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO  (dK, dV summed over the
+ *     query heads that share a key head)
+ * o, lse: the forward's; go = dLoss/dO with o's strides; dlse = dLoss/dLSE, fp32
+ * [B, H, N_Q], or NULL.  dq, dk, dv: bf16 with the strides of q, k, v (which must
+ * not make rows overlap).  Lengths and causal as in the forward; gradients of
+ * what lies past a sequence are 0, and go, dlse are not used there.  Every output
+ * is written by one block: results are the same on every run.
+ * Workspace: two fp32 values per query row, N_Q rounded up to 128.
+ */
+streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, size_t* bytes);
+streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                  const void* go, const float* dlse, streamkl_attn_shape s, void* dq, void* dk,
+                                  void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Log probabilities of given tokens, with entropy and top alternatives: the
  * output-layer companion of the attention loss (a student scored on the data's
  * tokens, or on its teacher's most likely ones).

@@ -91,3 +91,44 @@ def test_binding_refuses_types():
     q = torch.zeros(1, 2, 3, 64)
     with pytest.raises(TypeError):
         skl.attn_fwd(q, q, q)
+
+
+def bwd_args(s, drop=None, off=None, ws=1 << 30):
+    names = ["q", "k", "v", "o", "lse", "go", "dlse", "s", "dq", "dk", "dv", "ws"]
+    a = {n: ptr(64 * i) for i, n in enumerate(names)}
+    a["s"] = s
+    if drop:
+        a[drop] = None
+    if off:
+        a[off] = ptr(2)
+    return [*a.values(), ws, None]
+
+
+@pytest.mark.parametrize("change,code", BAD)
+def test_bwd_refuses_shapes(lib, change, code):
+    s = K.make_attn_shape(**{**OK, **change})
+    assert lib.streamkl_attn_bwd(*bwd_args(s)) == code
+    assert lib.streamkl_attn_bwd_workspace(s, ctypes.byref(ctypes.c_size_t())) == code
+
+
+def test_bwd_refuses_pointers_and_small_workspaces(lib):
+    s = K.make_attn_shape(**OK)
+    for name in ("q", "k", "v", "o", "lse", "go", "dq", "dk", "dv"):
+        assert lib.streamkl_attn_bwd(*bwd_args(s, drop=name)) == K.ERR_INVALID, name
+        assert lib.streamkl_attn_bwd(*bwd_args(s, off=name)) == K.ERR_INVALID, name
+    assert lib.streamkl_attn_bwd(*bwd_args(s, off="dlse")) == K.ERR_INVALID
+    n = ctypes.c_size_t()
+    assert lib.streamkl_attn_bwd_workspace(s, ctypes.byref(n)) == K.OK
+    assert n.value == 2 * 8 * 128 * 2 * 4
+    assert lib.streamkl_attn_bwd(*bwd_args(s, ws=n.value - 1)) == K.ERR_WORKSPACE
+    assert lib.streamkl_attn_bwd(*bwd_args(s, drop="ws")) == K.ERR_WORKSPACE
+    assert lib.streamkl_attn_bwd(*bwd_args(s, off="ws")) == K.ERR_WORKSPACE
+
+
+def test_bwd_binding_refuses():
+    q = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    lse = torch.zeros(1, 2, 3)
+    with pytest.raises(TypeError):
+        skl.attn_bwd(q, q, q, q, lse, q.float())
+    with pytest.raises(ValueError):
+        skl.attn_bwd(q, q, q, q[:, :, :2], lse, q)
