@@ -19,6 +19,7 @@ the input they belong to.  Other views are copied to a contiguous tensor first.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -408,71 +409,84 @@ def bwd_mutual(q1, k1, q2, k2, lse1, lse2, kl, g, scale=None, causal=False, bwd_
     return _back((dq1, dk1, dq2, dk2), host)
 
 
-def _call(name, dev, *args):
-    """Calls a C entry point on `dev`'s current stream, with `dev` the current device while it runs."""
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, _stream(dev))
+def _call(name, index, *args):
+    """Calls a C entry point on device `index`'s current stream, with that device current while it runs.
+
+    Tensors go in as addresses (plain integers): these calls are made per layer and per token, where the binding's
+    own time counts."""
+    f = getattr(_lib or lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        st = f(*args, stream)
     else:
-        with torch.cuda.device(dev):
-            st = f(*args, _stream(dev))
-    _check(st, name)
+        with torch.cuda.device(index):
+            st = f(*args, stream)
+    if st != OK:
+        raise StreamKLError(st, name)
 
 
-def _in_place(t):
+def _layout(t):
     """A [B, H, N, D] tensor the library can read and its (b, h, n) strides (a contiguous copy where it cannot)."""
+    if t.is_contiguous() and not t.data_ptr() % 16 and t.numel():
+        _, H, N, D = t.shape
+        if D % 8 == 0:
+            return t, (H * N * D, N * D, D)
     st = _bhn_strides(t)
     if st is None:
         t = t.clone(memory_format=torch.contiguous_format)  # also where only the start is off a 16-byte boundary
         st = _bhn_strides(t)
+        if st is None:
+            raise ValueError("the last dimension must be a multiple of 8")
     return t, st
 
 
 def make_attn_shape(B, H, HK, NQ, NK, D, scale=None, causal=False, q_lens=None, k_lens=None, q_strides=(0, 0, 0),
                     k_strides=(0, 0, 0), v_strides=(0, 0, 0), o_strides=(0, 0, 0)) -> AttnShape:
     """The C shape of an attention; lens are int32 device tensors (kept alive by the caller) or None."""
-    return AttnShape(int(B), int(H), int(HK), int(NQ), int(NK), int(D), float(scale or 0.0), int(bool(causal)),
-                     _ptr(q_lens), _ptr(k_lens), *q_strides, *k_strides, *v_strides, *o_strides)
+    return AttnShape(B, H, HK, NQ, NK, D, scale or 0.0, bool(causal), None if q_lens is None else q_lens.data_ptr(),
+                     None if k_lens is None else k_lens.data_ptr(), *q_strides, *k_strides, *v_strides, *o_strides)
 
 
-def _attn_prep(q, k, v, q_lens, k_lens):
-    """Validates an attention's inputs; returns (q, k, v, q_lens, k_lens on the device, their strides, was_host)."""
-    for t in (q, k, v):
-        if t.dtype != torch.bfloat16:
-            raise TypeError("q, k, v must be bfloat16")
-        if t.dim() != 4:
-            raise ValueError("q must be [B, H, N_Q, D], k and v [B, HK, N_K, D]")
-    if k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+def _lens(t, B, device, name):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != (B,):
+        raise ValueError(f"{name} must be int32 of shape ({B},)")
+    return t.to(device, non_blocking=True).contiguous()
+
+
+def _attn_inputs(tensors, q_lens, k_lens):
+    """Validates an attention's tensors (q, k, v, and o, do in the backward).
+
+    Returns (the tensors on the device, their strides, (q_lens, k_lens), (B, H, HK, NQ, NK, D), was_host)."""
+    q, k, v = tensors[:3]
+    for t in tensors:
+        if t.dtype is not torch.bfloat16:
+            raise TypeError("q, k, v, o, do must be bfloat16")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, H, N_Q, D], k and v [B, HK, N_K, D]")
+    B, H, NQ, D = q.shape
+    Bk, HK, NK, Dk = k.shape
+    if k.shape != v.shape or B != Bk or D != Dk:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
-    if k.shape[1] == 0 or q.shape[1] % k.shape[1]:
-        raise ValueError(f"{q.shape[1]} query heads do not divide over {k.shape[1]} key heads")
-    host = q.device.type == "cpu"
-    if any(t.device != q.device for t in (k, v)):
-        raise ValueError("inputs on different devices")
+    for t in tensors[3:]:
+        if t.shape != q.shape:
+            raise ValueError(f"o, do must be {tuple(q.shape)}")
+    if HK == 0 or H % HK:
+        raise ValueError(f"{H} query heads do not divide over {HK} key heads")
+    index = q.get_device()  # -1: host
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError("inputs on different devices")
+    host = index < 0
     if host:
         dev = torch.device("cuda", torch.cuda.current_device())
-        q, k, v = (t.contiguous().to(dev, non_blocking=True) for t in (q, k, v))
-    lens = []
-    for t, name in ((q_lens, "q_lens"), (k_lens, "k_lens")):
-        if t is not None:
-            if t.dtype != torch.int32 or tuple(t.shape) != (q.shape[0],):
-                raise ValueError(f"{name} must be int32 of shape ({q.shape[0]},)")
-            t = t.to(q.device, non_blocking=True).contiguous()
-        lens.append(t)
-    (q, qs), (k, ks), (v, vs) = _in_place(q), _in_place(k), _in_place(v)
-    return q, k, v, lens[0], lens[1], qs, ks, vs, host
-
-
-def _workspace(name, shape, dev, *args):
-    n = ctypes.c_size_t(0)
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = f(shape, *args, ctypes.byref(n))
-    else:
-        with torch.cuda.device(dev):
-            st = f(shape, *args, ctypes.byref(n))
-    _check(st, name)
-    return torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None, n.value
+        tensors = [t.contiguous().to(dev, non_blocking=True) for t in tensors]
+    if q_lens is not None or k_lens is not None:
+        dev = tensors[0].device
+        q_lens, k_lens = _lens(q_lens, B, dev, "q_lens"), _lens(k_lens, B, dev, "k_lens")
+    tensors, strides = zip(*map(_layout, tensors))
+    return tensors, strides, (q_lens, k_lens), (B, H, HK, NQ, NK, D), host
 
 
 def attn_fwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
@@ -483,6 +497,15 @@ def attn_fwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
     return bool(a.value), b.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(name, index, *sizes):
+    """Workspace bytes of an attention of these sizes on device `index` (a pure rule of sizes and the device)."""
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(index):
+        _check(getattr(lib(), name)(make_attn_shape(*sizes), ctypes.byref(n)), name)
+    return n.value
+
+
 def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     """Attention: (o bf16 with q's layout, lse fp32 [B, H, N_Q]).
 
@@ -490,14 +513,16 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     padded batch's sequences.  Causal masking is aligned at the last query and key of each sequence.  Rows that
     see no key give 0 and -inf.
     """
-    q, k, v, q_lens, k_lens, qs, ks, vs, host = _attn_prep(q, k, v, q_lens, k_lens)
-    B, H, NQ, D = q.shape
-    dev = q.device
-    s = make_attn_shape(B, H, k.shape[1], NQ, k.shape[2], D, scale, causal, q_lens, k_lens, qs, ks, vs, qs)
-    ws, nbytes = _workspace("streamkl_attn_fwd_workspace", s, dev)
-    o = _grad_like(q, qs, NQ)
+    (q, k, v), (qs, ks, vs), lens, sizes, host = _attn_inputs((q, k, v), q_lens, k_lens)
+    B, H, _, NQ, _, D = sizes
+    dev, index = q.device, q.get_device()
+    s = make_attn_shape(*sizes, scale, causal, *lens, qs, ks, vs, qs)
+    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", index, *sizes)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    o = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
-    _call("streamkl_attn_fwd", dev, _ptr(q), _ptr(k), _ptr(v), s, _ptr(o), _ptr(lse), _ptr(ws), nbytes)
+    _call("streamkl_attn_fwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), s, o.data_ptr(), lse.data_ptr(),
+          ws.data_ptr() if nbytes else None, nbytes)
     return _back((o, lse), host)
 
 
@@ -506,61 +531,58 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
     """
-    for t in (o, do):
-        if t.dtype != torch.bfloat16:
-            raise TypeError("o, do must be bfloat16")
-        if t.shape != q.shape:
-            raise ValueError(f"o, do must be {tuple(q.shape)}")
-        if t.device != q.device:
-            raise ValueError("inputs on different devices")
-    q, k, v, q_lens, k_lens, qs, ks, vs, host = _attn_prep(q, k, v, q_lens, k_lens)
-    B, H, NQ, D = q.shape
-    NK, dev = k.shape[2], q.device
-    if host:
-        o, do = (t.contiguous().to(dev, non_blocking=True) for t in (o, do))
-    (o, os_), (do, ds) = _in_place(o), _in_place(do)
-    if os_ != ds:
+    (q, k, v, o, do), (qs, ks, vs, os_, ds), lens, sizes, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
+    B, H, HK, NQ, NK, D = sizes
+    dev, index = q.device, q.get_device()
+    if os_ != ds:  # the library reads both with one set of strides
         o, do = (t.clone(memory_format=torch.contiguous_format) for t in (o, do))
-        os_ = _bhn_strides(o)
+        os_ = (H * NQ * D, NQ * D, D)
     lse = _rows(lse, dev, (B, H, NQ), "lse")
     dlse = _rows(dlse, dev, (B, H, NQ), "dlse")
-    s = make_attn_shape(B, H, k.shape[1], NQ, NK, D, scale, causal, q_lens, k_lens, qs, ks, vs, os_)
-    ws, nbytes = _workspace("streamkl_attn_bwd_workspace", s, dev)
-    dq, dk, dv = _grad_like(q, qs, NQ), _grad_like(k, ks, NK), _grad_like(v, vs, NK)
-    _call("streamkl_attn_bwd", dev, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dlse), s, _ptr(dq),
-          _ptr(dk), _ptr(dv), _ptr(ws), nbytes)
+    s = make_attn_shape(*sizes, scale, causal, *lens, qs, ks, vs, os_)
+    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", index, *sizes)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    dq = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
+    dk = torch.empty_strided((B, HK, NK, D), (*ks, 1), dtype=torch.bfloat16, device=dev)
+    dv = torch.empty_strided((B, HK, NK, D), (*vs, 1), dtype=torch.bfloat16, device=dev)
+    _call("streamkl_attn_bwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          do.data_ptr(), None if dlse is None else dlse.data_ptr(), s, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          ws.data_ptr() if nbytes else None, nbytes)
     return _back((dq, dk, dv), host)
 
 
 def _logits_rows(logits, tokens):
     """Validates logits [..., V] and tokens [...] or [..., T]; returns (device logits as strided [R, V] rows,
-    contiguous int64 device tokens [R, T] or None, T, was_host)."""
+    contiguous int64 device tokens or None, T, was_host)."""
     if logits.dtype not in DTYPES:
         raise TypeError("logits must be bfloat16, float16 or float32")
     if logits.dim() < 1 or logits.shape[-1] == 0:
         raise ValueError("logits must be [..., V] with V > 0")
     T = 0
     if tokens is not None:
-        if tokens.dtype not in (torch.int64, torch.int32):
+        if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
             raise TypeError("tokens must be int64 or int32")
-        if tokens.shape == logits.shape[:-1]:
+        lead = logits.shape[:-1]
+        if tokens.shape == lead:
             T = 1
-        elif tokens.dim() == logits.dim() and tokens.shape[:-1] == logits.shape[:-1]:
+        elif tokens.dim() == logits.dim() and tokens.shape[:-1] == lead:
             T = tokens.shape[-1]
         else:
             raise ValueError(f"tokens {tuple(tokens.shape)} do not fit logits {tuple(logits.shape)}")
-        if tokens.device != logits.device:
+        if tokens.get_device() != logits.get_device():
             raise ValueError("inputs on different devices")
-    host = logits.device.type == "cpu"
+    host = not logits.is_cuda
     if host:
         logits = logits.to(torch.device("cuda", torch.cuda.current_device()), non_blocking=True)
     V = logits.shape[-1]
-    x = logits.reshape(-1, V)
-    if (V > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < V):
+    x = logits if logits.dim() == 2 else logits.reshape(-1, V)
+    if not x.is_contiguous() and ((V > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < V)):
         x = x.contiguous()
-    if T:
-        tokens = tokens.to(device=x.device, dtype=torch.int64, non_blocking=True).contiguous()
-    return x, tokens if T else None, T, host
+    if not T:
+        return x, None, 0, host
+    if host or tokens.dtype is not torch.int64:
+        tokens = tokens.to(device=x.device, dtype=torch.int64, non_blocking=True)
+    return x, tokens.contiguous(), T, host
 
 
 def _row_stride(x):
@@ -575,7 +597,8 @@ def logprobs_fwd(logits, tokens=None, scale=1.0, top_k=0):
     top_logp fp32 and top_index int64 are [..., top_k], the largest logits (equal ones: the lowest index first).
     """
     x, tok, T, host = _logits_rows(logits, tokens)
-    if not 0 <= top_k <= min(LOGPROBS_MAX_TOP_K, x.shape[1]):
+    R, V = x.shape
+    if not 0 <= top_k <= min(LOGPROBS_MAX_TOP_K, V):
         raise ValueError(f"top_k must be between 0 and min({LOGPROBS_MAX_TOP_K}, V)")
     lead, dev = logits.shape[:-1], x.device
     logp = torch.empty(tokens.shape if tokens is not None else (*lead, 0), dtype=torch.float32, device=dev)
@@ -583,8 +606,9 @@ def logprobs_fwd(logits, tokens=None, scale=1.0, top_k=0):
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     top = torch.empty((*lead, top_k), dtype=torch.float32, device=dev)
     idx = torch.empty((*lead, top_k), dtype=torch.int64, device=dev)
-    _call("streamkl_logprobs_fwd", dev, _ptr(x), DTYPES[x.dtype], x.shape[0], x.shape[1], _row_stride(x), _ptr(tok), T,
-          scale, top_k, _ptr(logp), _ptr(entropy), _ptr(lse), _ptr(top), _ptr(idx))
+    _call("streamkl_logprobs_fwd", x.get_device(), x.data_ptr(), DTYPES[x.dtype], R, V, _row_stride(x),
+          tok.data_ptr() if T else None, T, scale, top_k, logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+          top.data_ptr(), idx.data_ptr())
     return _back((logp, entropy, lse, top, idx), host)
 
 
@@ -592,18 +616,21 @@ def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0
     """Gradient of the logits, contiguous and of their type, for upstream gradients g_logp (tokens' shape) and
     g_entropy ([...] or None); lse and entropy are logprobs_fwd's (entropy may be None without g_entropy)."""
     x, tok, T, host = _logits_rows(logits, tokens)
+    R, V = x.shape
     lead, dev = logits.shape[:-1], x.device
     lse = _rows(lse, dev, lead, "lse")
-    g_entropy = _rows(g_entropy, dev, lead, "g_entropy")
-    if g_entropy is not None and entropy is None:
-        raise ValueError("g_entropy needs the forward's entropy")
-    entropy = _rows(entropy, dev, lead, "entropy") if g_entropy is not None else None
+    ent = None
+    if g_entropy is not None:
+        if entropy is None:
+            raise ValueError("g_entropy needs the forward's entropy")
+        g_entropy, ent = _rows(g_entropy, dev, lead, "g_entropy"), _rows(entropy, dev, lead, "entropy")
     g_logp = _rows(g_logp, dev, tokens.shape, "g_logp") if T else None
     if T and g_logp is None:
         raise ValueError("tokens need g_logp")
     out = torch.empty(logits.shape, dtype=x.dtype, device=dev)
-    _call("streamkl_logprobs_bwd", dev, _ptr(x), DTYPES[x.dtype], x.shape[0], x.shape[1], _row_stride(x), _ptr(tok), T,
-          scale, _ptr(lse), _ptr(entropy), _ptr(g_logp), _ptr(g_entropy), _ptr(out), x.shape[1])
+    _call("streamkl_logprobs_bwd", x.get_device(), x.data_ptr(), DTYPES[x.dtype], R, V, _row_stride(x),
+          tok.data_ptr() if T else None, T, scale, lse.data_ptr(), None if ent is None else ent.data_ptr(),
+          g_logp.data_ptr() if T else None, None if ent is None else g_entropy.data_ptr(), out.data_ptr(), V)
     return _back((out,), host)[0]
 
 

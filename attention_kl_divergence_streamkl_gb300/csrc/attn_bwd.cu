@@ -239,7 +239,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
         constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
         const uint64_t kd = sdesc_sw128(sb + L::OFF_K, 0, 1024), vd = sdesc_sw128(sb + L::OFF_V, 0, 1024);
@@ -560,7 +560,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const float* __res
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
         constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
         const uint64_t qd = sdesc_sw128(sb + L::OFF_Q, 0, 1024), od = sdesc_sw128(sb + L::OFF_O, 0, 1024);

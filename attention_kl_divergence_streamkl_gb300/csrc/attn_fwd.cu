@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BM, BN, false, false);
         constexpr uint32_t id_o = idesc_bf16(BM, D, false, true);
         const int nt[2] = {nA, nB};
