@@ -16,9 +16,12 @@
 // kind with the longer blocks first: the shorter ones fill the SMs that the
 // longer ones leave.
 //
-// A small kernel first writes, per query row, -LSE log2(e) and delta, 128-row
-// padded so that a tile's 128 values are one bulk copy.  Rows that see no key,
-// and rows past a sequence's length, get -inf and 0: their P is exactly 0.
+// A small kernel first writes, per query row, -LSE / scale and -delta, each as
+// three bf16 that add up to its 24 bits, in 16 bytes and 128-row padded: a
+// tile's 128 rows are one bulk copy and lie in shared memory as the 16-wide
+// K step that adds the row's value to a product (the other operand's step is
+// ones).  Rows that see no key, and rows past a sequence's length, get -1e30
+// and 0: their P is exactly 0.
 #include "attn.cuh"
 
 namespace skl {
@@ -36,40 +39,94 @@ struct BwdOut {
 };
 
 // ---------------------------------------------------------------------------
-// Row values: nlse = -LSE log2(e), delta = dO . O - dLSE.  A row takes D / 8
+// Row values: -LSE / scale and -delta, delta = dO . O - dLSE.  A row takes D / 8
 // lanes of 16 bytes; bound by the read of O and dO.
+//
+// O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|.  Among many keys that averages out of the
+// gradients; a row that sees few of them passes it on whole.  For rows of at most 32 keys (the first rows under a causal
+// mask, short sequences) delta is computed as sum_j P_ij dP_ij instead, a key to a lane.
+constexpr float kNoRow = -1.0e30f;
+
+__device__ __forceinline__ uint4 three_bf16(float x) {
+  const float hi = __bfloat162float(__float2bfloat16_rn(x));
+  const float mid = __bfloat162float(__float2bfloat16_rn(x - hi));
+  return make_uint4(pack_bf16(hi, mid), pack_bf16(x - hi - mid, 0.f), 0u, 0u);
+}
+__device__ __forceinline__ float from_three_bf16(uint2 v) {
+  return __uint_as_float(v.x << 16) + (__uint_as_float(v.x & 0xffff0000u) + __uint_as_float(v.y << 16));
+}
+// Sum of the products of 8 bf16 pairs.
+__device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), sum);
+    sum = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), sum);
+  }
+  return sum;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256)
-    attn_rows_kernel(const AttnProblem p, const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ go,
-                     const float* __restrict__ lse, const float* __restrict__ dlse, float* __restrict__ nlse,
-                     float* __restrict__ delta, int padded) {
+    attn_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
+                     int padded) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
   const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / LANES;  // row of [B H][padded]
   const int lane = threadIdx.x % LANES;
-  const long long bh = r / padded;
+  const bool inside = r < (long long)p.B * p.H * padded;
+  const long long bh = inside ? r / padded : 0;
   const int n = (int)(r % padded);
-  if (bh >= (long long)p.B * p.H) return;  // a whole group of lanes leaves together
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
-  float sum = 0.f, l = kNegInf;
-  const bool real = n < seq_len(p.q_lens, b, p.NQ);
-  if (real) {
-    const long long at = b * p.os_b + h * p.os_h + n * p.os_n + lane * 8;
-    const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(go + at);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), sum);
-      sum = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), sum);
-    }
-    l = lse[bh * p.NQ + n];
+  const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
+  const bool real = inside && n < ql;
+  const int seen = real ? (p.causal ? min(kl, n + kl - ql + 1) : kl) : 0;  // keys this row sees (none: <= 0)
+  const long long at = b * p.os_b + h * p.os_h + n * p.os_n;
+  const auto* go = static_cast<const __nv_bfloat16*>(in.go) + at;
+  float sum = 0.f, l = 0.f;
+  if (seen > 0) {
+    const auto* o = static_cast<const __nv_bfloat16*>(in.o) + at;
+    sum = dot8(reinterpret_cast<const uint4*>(o)[lane], reinterpret_cast<const uint4*>(go)[lane], 0.f);
+    l = in.lse[bh * p.NQ + n];
   }
-  const unsigned group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
 #pragma unroll
-  for (int w = LANES / 2; w; w >>= 1) sum += __shfl_xor_sync(group, sum, w);
-  if (lane == 0) {
-    const bool none = l == kNegInf;
-    nlse[r] = none ? kNegInf : -l * kLog2e;
-    delta[r] = none ? 0.f : dlse ? sum - dlse[bh * p.NQ + n] : sum;
+  for (int w = LANES / 2; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+  const int key = threadIdx.x & 31;
+  if (__any_sync(0xffffffffu, seen > 0 && seen <= 32)) {
+    // the warp's rows one after the other; every lane takes one key of the row
+    for (int g = 0; g < 32 / LANES; ++g) {
+      const int src = g * LANES;
+      const int keys = __shfl_sync(0xffffffffu, seen, src);
+      const float lg = __shfl_sync(0xffffffffu, l, src);
+      const int bg = __shfl_sync(0xffffffffu, b, src), hg = __shfl_sync(0xffffffffu, h, src),
+                ng = __shfl_sync(0xffffffffu, n, src);
+      if (keys <= 0 || keys > 32) continue;
+      float s = 0.f, t = 0.f;
+      if (key < keys) {
+        const auto* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.q) + bg * p.qs_b +
+                                                        hg * p.qs_h + ng * p.qs_n);
+        const auto* gr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.go) + bg * p.os_b +
+                                                        hg * p.os_h + ng * p.os_n);
+        const auto* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.k) + bg * p.ks_b +
+                                                        hg / p.G * p.ks_h + key * p.ks_n);
+        const auto* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.v) + bg * p.vs_b +
+                                                        hg / p.G * p.vs_h + key * p.vs_n);
+#pragma unroll 4
+        for (int d = 0; d < D / 8; ++d) {
+          s = dot8(qr[d], kr[d], s);
+          t = dot8(gr[d], vr[d], t);
+        }
+        t *= ex2(fmaf(s, p.c, -lg * kLog2e));
+      }
+#pragma unroll
+      for (int w = 16; w; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+      if (key / LANES == g) sum = t;
+    }
+  }
+  if (inside && lane == 0) {
+    const bool none = seen <= 0 || l == kNegInf;
+    const float delta = in.dlse && !none ? sum - in.dlse[bh * p.NQ + n] : sum;
+    row_s[r] = three_bf16(none ? kNoRow : -l / p.scale);
+    row_d[r] = three_bf16(none ? 0.f : -delta);
   }
 }
 
@@ -91,11 +148,14 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
 // in shared memory).  P^T and dS^T (bf16 pairs) overwrite their logits and are
 // the A operands of dV += P^T dO and dK += dS^T Q, which read dO and Q
 // MN-major from the tiles that are there already: neither P nor dS passes
-// through shared memory.
+// through shared memory.  The queries' LSE and delta belong to columns here; a
+// ninth K step of each product adds them (64 cycles), where reading them from
+// shared memory, 16 bytes to a lane, kept the load pipe busy for 1024 cycles a
+// tile pair.
 //   TMEM: S^T/P^T [0,128), dP^T/dS^T [128,256), dV [256, 256+D), dK [384, 384+D)
 //   warps 0-15  thread = key, group g = warp / 4 takes queries [32g, 32g+32); its
 //               pairs go to the first 16 of its own 32 columns
-//   warp 16     TMA producer: K, V once; Q(u) with its nlse, dO(u) with its delta
+//   warp 16     TMA producer: K, V once; Q(u) and dO(u) with their rows' values
 //   warp 17     TMEM owner and MMA issuer: dV(u), S(u+1), dK(u), dP(u+1): while the
 //               warps turn S(u+1) into P, the pipe runs dK(u) and dP(u+1), and
 //               while they form dS(u+1) it runs dV(u+1) and S(u+2)
@@ -109,9 +169,13 @@ struct Smem {
   static constexpr int OFF_K = 0, OFF_V = TILE;
   static constexpr int OFF_Q = 2 * TILE;                 // Q slots
   static constexpr int OFF_O = OFF_Q + SLOTS * TILE;     // dO slots
-  static constexpr int OFF_NL = OFF_O + SLOTS * TILE;    // nlse slots, 512 B each
-  static constexpr int OFF_DL = OFF_NL + SLOTS * 512;    // delta slots
-  static constexpr int OFF_BAR = OFF_DL + SLOTS * 512;
+  // K steps without swizzle: 128 rows of 16 bytes are 16 core matrices of 8 rows for k = 0 .. 7; k = 8 .. 15 is ZERO
+  static constexpr int STEP = 128 * 16;
+  static constexpr int OFF_RS = OFF_O + SLOTS * TILE;    // -LSE / scale of the Q slots
+  static constexpr int OFF_RD = OFF_RS + SLOTS * STEP;   // -delta of the dO slots
+  static constexpr int OFF_ONES = OFF_RD + SLOTS * STEP; // 1, 1, 1, 0, ...
+  static constexpr int OFF_ZERO = OFF_ONES + STEP;
+  static constexpr int OFF_BAR = OFF_ZERO + STEP;
   // kv_full, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, g_done, to_patch, patched
   static constexpr int BAR_SLOT = 8 * 16;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
@@ -125,15 +189,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
+// Descriptor of a K-major K step without swizzle: 8-row core matrices 128 bytes apart, the second half of K at `zero`.
+__device__ __forceinline__ uint64_t sdesc_step(uint32_t addr, uint32_t zero) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(((zero - addr) >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
 }
 
 template <int D>
-__device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __restrict__ nlse,
-                                         const float* __restrict__ delta, int padded, const BwdOut& out, int* status,
+__device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __restrict__ row_s,
+                                         const uint4* __restrict__ row_d, int padded, const BwdOut& out, int* status,
                                          const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                          const CUtensorMap& mo, const unsigned blk) {
   using L = kv::Smem<D>;
@@ -178,6 +242,11 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x < 128) {
+    st_shared16(sb + L::OFF_ONES + threadIdx.x * 16, make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u));
+    st_shared16(sb + L::OFF_ZERO + threadIdx.x * 16, make_uint4(0u, 0u, 0u, 0u));
+    fence_async_smem();
+  }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
     tmem_relinquish();
@@ -202,18 +271,18 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
           const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
           const long long row = ((long long)b * p.H + hq) * padded + q0;
           if (u >= SLOTS && !mbar_wait(q_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + 512);
+          mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
             tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &mq, q_full + 8 * s, h * 64, q0, hq, b);
-          bulk_load(sb + L::OFF_NL + s * 512, nlse + row, 512, q_full + 8 * s);
+          bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + row, L::STEP, q_full + 8 * s);
           issued_q = u + 1;
           if (u >= SLOTS && !mbar_wait(o_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + 512);
+          mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
             tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &mo, o_full + 8 * s, h * 64, q0, hq, b);
-          bulk_load(sb + L::OFF_DL + s * 512, delta + row, 512, o_full + 8 * s);
+          bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + row, L::STEP, o_full + 8 * s);
           issued_o = u + 1;
         }
         mbar_drain(kv_full, 0, status);
@@ -243,13 +312,14 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
         constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
         constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
         const uint64_t kd = sdesc_sw128(sb + L::OFF_K, 0, 1024), vd = sdesc_sw128(sb + L::OFF_V, 0, 1024);
+        const uint64_t ones = sdesc_step(sb + L::OFF_ONES, sb + L::OFF_ZERO);
         int patches = 0;
         auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
           if (!ragged || (u + 1) % n_qt) return true;
           mbar_arrive(to_patch);
           return mbar_wait(patched, patches++ & 1, status, abort_flag);
         };
-        auto issue_s = [&](int u) {  // S^T(u) = K Q^T
+        auto issue_s = [&](int u) {  // S^T(u) = K Q^T - LSE / scale
           const int s = u % SLOTS;
           if (!mbar_wait(q_full + 8 * s, (u / SLOTS) & 1, status, abort_flag) || !patch(u)) return false;
           tc_fence_after();
@@ -259,10 +329,11 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
             const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
             mma_ss(tmem + kv::kColS, sdesc_add(kd, o), sdesc_add(qd, o), id_s, ks > 0);
           }
+          mma_ss(tmem + kv::kColS, ones, sdesc_step(sb + L::OFF_RS + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
           mma_commit(s_full);
           return true;
         };
-        auto issue_dp = [&](int u) {  // dP^T(u) = V dO^T
+        auto issue_dp = [&](int u) {  // dP^T(u) = V dO^T - delta
           const int s = u % SLOTS;
           if (!mbar_wait(o_full + 8 * s, (u / SLOTS) & 1, status, abort_flag) || !patch(u)) return false;
           tc_fence_after();
@@ -272,6 +343,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
             const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
             mma_ss(tmem + kv::kColP, sdesc_add(vd, o), sdesc_add(od, o), id_s, ks > 0);
           }
+          mma_ss(tmem + kv::kColP, ones, sdesc_step(sb + L::OFF_RD + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
           mma_commit(dp_full);
           return true;
         };
@@ -313,10 +385,8 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
     const uint32_t ts = tmem + lanes + kv::kColS + 32 * grp, tp = tmem + lanes + kv::kColP + 32 * grp;
     bool ok = true;
     for (int u = 0; u < n; ++u) {
-      const int s = u % SLOTS, ph = (u / SLOTS) & 1;
       const int q0 = q_begin + (u % n_qt) * BT + 32 * grp;  // first query of this warp's columns
-      const uint32_t nl = sb + L::OFF_NL + s * 512 + grp * 128, dl = sb + L::OFF_DL + s * 512 + grp * 128;
-      ok = mbar_wait_warp(s_full, u & 1, status, abort_flag) && mbar_wait_warp(q_full + 8 * s, ph, status, abort_flag);
+      ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
@@ -324,17 +394,12 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
       tmem_ld32(ts, a);
       tmem_ld_wait();
       reg_fence32(a);
-      // P = 2^(c S + nlse): 0 for rows without keys and past the sequence, whose nlse is -inf
+      // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float4 nv = ld_shared_f4(nl + 4 * i);
-        const float2 x0 = ffma2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc, make_float2(nv.x, nv.y));
-        const float2 x1 =
-            ffma2(make_float2(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), cc, make_float2(nv.z, nv.w));
-        a[i] = __float_as_uint(ex2(x0.x));
-        a[i + 1] = __float_as_uint(ex2(x0.y));
-        a[i + 2] = __float_as_uint(ex2(x1.x));
-        a[i + 3] = __float_as_uint(ex2(x1.y));
+      for (int i = 0; i < 32; i += 2) {
+        const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc);
+        a[i] = __float_as_uint(ex2(x.x));
+        a[i + 1] = __float_as_uint(ex2(x.y));
       }
       const int hidden = key >= kl ? 32 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
       if (__any_sync(0xffffffffu, hidden > 0)) {
@@ -350,27 +415,19 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
-      ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag) && mbar_wait_warp(o_full + 8 * s, ph, status, abort_flag);
+      ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
+      uint32_t d[32];
+      tmem_ld32(tp, d);
+      tmem_ld_wait();
+      reg_fence32(d);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t d[16];
-        tmem_ld16(tp + 16 * hf, d);
-        tmem_ld_wait();
-        reg_fence16(d);
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 dv = ld_shared_f4(dl + 4 * (16 * hf + i));
-          const int j = 16 * hf + i;
-          const float2 e0 = fmul2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
-                                  fsub2(make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), make_float2(dv.x, dv.y)));
-          const float2 e1 = fmul2(make_float2(__uint_as_float(a[j + 2]), __uint_as_float(a[j + 3])),
-                                  fsub2(make_float2(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])), make_float2(dv.z, dv.w)));
-          pk[j / 2] = pack_bf16(e0.x, e0.y);
-          pk[j / 2 + 1] = pack_bf16(e1.x, e1.y);
-        }
+      for (int i = 0; i < 32; i += 2) {
+        const float2 e = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])),
+                               make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+        pk[i / 2] = pack_bf16(e.x, e.y);
       }
       tmem_st16(tp, pk);
       tmem_st_wait();
@@ -415,7 +472,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const float* __re
 // ---------------------------------------------------------------------------
 // dQ block.  The TMEM lanes are queries: a thread owns a row and holds its nlse
 // and delta.  S = Q K^T and dP = dO V^T are copied into registers and released
-// at once, so the next tile's products run while dS is formed; dS (bf16 pairs)
+// at once, before anything is computed, so the next tile's products run meanwhile; dS (bf16 pairs)
 // goes to a double buffer in TMEM, the A operand of dQ += dS K.
 //   TMEM: S [0,128), dP [128,256), dS [256,320) and [320,384), dQ [384, 384+D)
 //   warps 0-15  thread = query, group g = warp / 4 takes keys [32g, 32g+32)
@@ -441,13 +498,13 @@ struct Smem {
 static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
 }  // namespace qq
 
-// dS of 16 columns: a, d = S, dP; `seen` of them are visible.
+// dS of 32 columns: a, d = S, dP; `seen` of them are visible.
 template <bool MASKED>
-__device__ __forceinline__ void ds16(const uint32_t (&a)[16], const uint32_t (&d)[16], uint32_t* pk, float c, float nlse,
-                                     float delta, int seen) {
+__device__ __forceinline__ void ds32(const uint32_t (&a)[32], const uint32_t (&d)[32], uint32_t (&pk)[16], float c,
+                                     float nlse, float delta, int seen) {
   const float2 cc = make_float2(c, c), nl = make_float2(nlse, nlse), dl = make_float2(delta, delta);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
+  for (int i = 0; i < 32; i += 2) {
     const float2 x = ffma2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc, nl);
     float2 e = fmul2(make_float2(ex2(x.x), ex2(x.y)),
                      fsub2(make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), dl));
@@ -460,8 +517,8 @@ __device__ __forceinline__ void ds16(const uint32_t (&a)[16], const uint32_t (&d
 }
 
 template <int D>
-__device__ __forceinline__ void q_block(const AttnProblem& p, const float* __restrict__ nlse,
-                                        const float* __restrict__ delta, int padded, const BwdOut& out, int* status,
+__device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __restrict__ row_s,
+                                        const uint4* __restrict__ row_d, int padded, const BwdOut& out, int* status,
                                         const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                         const CUtensorMap& mo, const unsigned blk) {
   using L = qq::Smem<D>;
@@ -615,11 +672,9 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const float* __res
     const int r = wq * 32 + lane;
     const int q = q0 + r;
     const float c = p.c;
-    float nl = kNegInf, dl = 0.f;
-    if (q < p.NQ) {
-      nl = nlse[(size_t)bh * padded + q];
-      dl = delta[(size_t)bh * padded + q];
-    }
+    // the padding's rows are there too: -1e30 and 0
+    const float nl = c * from_three_bf16(*reinterpret_cast<const uint2*>(row_s + (size_t)bh * padded + q));
+    const float dl = -from_three_bf16(*reinterpret_cast<const uint2*>(row_d + (size_t)bh * padded + q));
     const int row_end = q < ql ? (p.causal ? min(kl, q + off + 1) : kl) : 0;  // keys this row sees
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t tcol = tmem + lanes + grp * 32;
@@ -632,29 +687,19 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const float* __res
       tc_fence_after();
       const int seen = row_end - (j * BT + grp * 32);
       const bool masked = __any_sync(0xffffffffu, seen < 32);
-      uint32_t pk[16];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t a[16], d[16];
-        tmem_ld16(tcol + qq::kColS + 16 * hf, a);
-        tmem_ld16(tcol + qq::kColP + 16 * hf, d);
-        tmem_ld_wait();
-        reg_fence16(a);
-        reg_fence16(d);
-        if (hf == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
-        }
-        if (masked)
-          ds16<true>(a, d, pk + 8 * hf, c, nl, dl, seen - 16 * hf);
-        else
-          ds16<false>(a, d, pk + 8 * hf, c, nl, dl, 16);
-        if (hf == 0)  // first half final before the second half is read
-          asm volatile("" : "+r"(pk[0]), "+r"(pk[1]), "+r"(pk[2]), "+r"(pk[3]), "+r"(pk[4]), "+r"(pk[5]),
-                       "+r"(pk[6]), "+r"(pk[7])::"memory");
-      }
-      reg_fence16(pk);
+      uint32_t a[32], d[32], pk[16];
+      tmem_ld32(tcol + qq::kColS, a);
+      tmem_ld32(tcol + qq::kColP, d);
+      tmem_ld_wait();
+      reg_fence32(a);
+      reg_fence32(d);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free);
+      if (masked)
+        ds32<true>(a, d, pk, c, nl, dl, seen);
+      else
+        ds32<false>(a, d, pk, c, nl, dl, 32);
       if (j >= 2) {  // this dS buffer's last product is done
         ok = mbar_wait_warp(ds_free + 8 * bf, ((j >> 1) - 1) & 1, status, abort_flag);
         __syncwarp();
@@ -698,7 +743,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const float* __res
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    attn_bwd_kernel(const AttnProblem p, const float* __restrict__ nlse, const float* __restrict__ delta, int padded,
+    attn_bwd_kernel(const AttnProblem p, const uint4* __restrict__ row_s, const uint4* __restrict__ row_d, int padded,
                     const BwdOut out, int* status, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                     const __grid_constant__ CUtensorMap mo, const unsigned n_first, const int q_first) {
@@ -706,9 +751,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const bool is_q = q_first ? x < n_first : x >= n_first;
   const unsigned blk = x < n_first ? x : x - n_first;
   if (is_q)
-    q_block<D>(p, nlse, delta, padded, out, status, mq, mk, mv, mo, blk);
+    q_block<D>(p, row_s, row_d, padded, out, status, mq, mk, mv, mo, blk);
   else
-    kv_block<D>(p, nlse, delta, padded, out, status, mq, mk, mv, mo, blk);
+    kv_block<D>(p, row_s, row_d, padded, out, status, mq, mk, mv, mo, blk);
 }
 
 // Zeros for `rows` rows of each of B H heads (a backward without queries or without keys).
@@ -729,12 +774,10 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
     return cudaErrorInvalidValue;
   const int padded = (p.NQ + BT - 1) / BT * BT;
   const long long rows = (long long)p.B * p.H * padded;
-  float* nlse = static_cast<float*>(workspace);
-  float* delta = nlse + rows;
+  uint4* row_s = static_cast<uint4*>(workspace);
+  uint4* row_d = row_s + rows;
   constexpr int row_lanes = D / 8, per_block = 256 / row_lanes;
-  attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
-      p, static_cast<const __nv_bfloat16*>(in.o), static_cast<const __nv_bfloat16*>(in.go), in.lse, in.dlse, nlse, delta,
-      padded);
+  attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(p, in, row_s, row_d, padded);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   int smem = kOneBlockPerSmSmem;
@@ -747,7 +790,7 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
   const BwdOut out{static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv)};
   // a dQ block walks the keys with three products a tile, a dK/dV block the queries of G heads with four
   const int q_first = 3ll * p.NK > 4ll * p.G * p.NQ;
-  kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, nlse, delta, padded, out, status, mq, mk, mv, mo,
+  kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, row_s, row_d, padded, out, status, mq, mk, mv, mo,
                                                                 (unsigned)(q_first ? q_blocks : kv_blocks), q_first);
   return cudaGetLastError();
 }
@@ -756,7 +799,7 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
 
 size_t attn_bwd_workspace(const AttnProblem& p) {
   if (p.NQ == 0 || p.NK == 0) return 0;
-  return (size_t)p.B * p.H * ((p.NQ + BT - 1) / BT * BT) * 2 * sizeof(float);
+  return (size_t)p.B * p.H * ((p.NQ + BT - 1) / BT * BT) * 2 * sizeof(uint4);
 }
 
 cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,

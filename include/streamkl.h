@@ -345,7 +345,7 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
  * not make rows overlap).  Lengths and causal as in the forward; gradients of
  * what lies past a sequence are 0, and go, dlse are not used there.  Every output
  * is written by one block: results are the same on every run.
- * Workspace: two fp32 values per query row, N_Q rounded up to 128.
+ * Workspace: 32 bytes per query row, N_Q rounded up to 128.
  */
 streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, size_t* bytes);
 streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,

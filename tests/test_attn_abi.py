@@ -119,7 +119,7 @@ def test_bwd_refuses_pointers_and_small_workspaces(lib):
     assert lib.streamkl_attn_bwd(*bwd_args(s, off="dlse")) == K.ERR_INVALID
     n = ctypes.c_size_t()
     assert lib.streamkl_attn_bwd_workspace(s, ctypes.byref(n)) == K.OK
-    assert n.value == 2 * 8 * 128 * 2 * 4
+    assert n.value == 2 * 8 * 128 * 32
     assert lib.streamkl_attn_bwd(*bwd_args(s, ws=n.value - 1)) == K.ERR_WORKSPACE
     assert lib.streamkl_attn_bwd(*bwd_args(s, drop="ws")) == K.ERR_WORKSPACE
     assert lib.streamkl_attn_bwd(*bwd_args(s, off="ws")) == K.ERR_WORKSPACE
