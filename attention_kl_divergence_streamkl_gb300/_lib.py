@@ -427,10 +427,11 @@ def _call(name, index, *args):
 
 def _layout(t):
     """A [B, H, N, D] tensor the library can read and its (b, h, n) strides (a contiguous copy where it cannot)."""
-    if t.is_contiguous() and not t.data_ptr() % 16 and t.numel():
-        _, H, N, D = t.shape
-        if D % 8 == 0:
-            return t, (H * N * D, N * D, D)
+    B, H, N, D = t.shape
+    sb, sh, sn, sd = st = t.stride()
+    if sd == 1 and not (t.data_ptr() & 15 or (sb | sh | sn) & 7) and (
+            D <= sn and sn * N <= sh and sh * H <= sb or D <= sh and sh * H <= sn and sn * N <= sb) and sb < 1 << 38:
+        return t, st[:3]  # heads by rows or rows by heads, the usual orders
     st = _bhn_strides(t)
     if st is None:
         t = t.clone(memory_format=torch.contiguous_format)  # also where only the start is off a 16-byte boundary
@@ -447,46 +448,45 @@ def make_attn_shape(B, H, HK, NQ, NK, D, scale=None, causal=False, q_lens=None, 
                      None if k_lens is None else k_lens.data_ptr(), *q_strides, *k_strides, *v_strides, *o_strides)
 
 
-def _lens(t, B, device, name):
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or tuple(t.shape) != (B,):
+def _lens(t, B, dev, name):
+    if t.dtype is not torch.int32 or t.shape != (B,):
         raise ValueError(f"{name} must be int32 of shape ({B},)")
-    return t.to(device, non_blocking=True).contiguous()
+    if t.device != dev:
+        t = t.to(dev, non_blocking=True)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _attn_inputs(tensors, q_lens, k_lens):
     """Validates an attention's tensors (q, k, v, and o, do in the backward).
 
-    Returns (the tensors on the device, their strides, (q_lens, k_lens), (B, H, HK, NQ, NK, D), was_host)."""
+    Returns (the tensors on the device, q_lens, k_lens, (B, H, HK, NQ, NK, D), device, was_host)."""
     q, k, v = tensors[:3]
+    shape, key_shape, dev = q.shape, k.shape, q.device
     for t in tensors:
         if t.dtype is not torch.bfloat16:
             raise TypeError("q, k, v, o, do must be bfloat16")
-    if q.dim() != 4 or k.dim() != 4:
+        if t.device != dev:
+            raise ValueError("inputs on different devices")
+    if len(shape) != 4 or len(key_shape) != 4:
         raise ValueError("q must be [B, H, N_Q, D], k and v [B, HK, N_K, D]")
-    B, H, NQ, D = q.shape
-    Bk, HK, NK, Dk = k.shape
-    if k.shape != v.shape or B != Bk or D != Dk:
+    B, H, NQ, D = shape
+    Bk, HK, NK, Dk = key_shape
+    if key_shape != v.shape or B != Bk or D != Dk:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
     for t in tensors[3:]:
-        if t.shape != q.shape:
-            raise ValueError(f"o, do must be {tuple(q.shape)}")
+        if t.shape != shape:
+            raise ValueError(f"o, do must be {tuple(shape)}")
     if HK == 0 or H % HK:
         raise ValueError(f"{H} query heads do not divide over {HK} key heads")
-    index = q.get_device()  # -1: host
-    for t in tensors:
-        if t.get_device() != index:
-            raise ValueError("inputs on different devices")
-    host = index < 0
+    host = dev.type == "cpu"
     if host:
         dev = torch.device("cuda", torch.cuda.current_device())
         tensors = [t.contiguous().to(dev, non_blocking=True) for t in tensors]
-    if q_lens is not None or k_lens is not None:
-        dev = tensors[0].device
-        q_lens, k_lens = _lens(q_lens, B, dev, "q_lens"), _lens(k_lens, B, dev, "k_lens")
-    tensors, strides = zip(*map(_layout, tensors))
-    return tensors, strides, (q_lens, k_lens), (B, H, HK, NQ, NK, D), host
+    if q_lens is not None:
+        q_lens = _lens(q_lens, B, dev, "q_lens")
+    if k_lens is not None:
+        k_lens = _lens(k_lens, B, dev, "k_lens")
+    return tensors, q_lens, k_lens, (B, H, HK, NQ, NK, D), dev, host
 
 
 def attn_fwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
@@ -513,17 +513,17 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     padded batch's sequences.  Causal masking is aligned at the last query and key of each sequence.  Rows that
     see no key give 0 and -inf.
     """
-    (q, k, v), (qs, ks, vs), lens, sizes, host = _attn_inputs((q, k, v), q_lens, k_lens)
+    (q, k, v), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v), q_lens, k_lens)
+    (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
     B, H, _, NQ, _, D = sizes
-    dev, index = q.device, q.get_device()
-    s = make_attn_shape(*sizes, scale, causal, *lens, qs, ks, vs, qs)
-    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", index, *sizes)
+    s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, qs)
+    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", dev.index, *sizes)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     o = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
-    _call("streamkl_attn_fwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), s, o.data_ptr(), lse.data_ptr(),
+    _call("streamkl_attn_fwd", dev.index, q.data_ptr(), k.data_ptr(), v.data_ptr(), s, o.data_ptr(), lse.data_ptr(),
           ws.data_ptr() if nbytes else None, nbytes)
-    return _back((o, lse), host)
+    return _back((o, lse), True) if host else (o, lse)
 
 
 def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None):
@@ -531,58 +531,59 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
     """
-    (q, k, v, o, do), (qs, ks, vs, os_, ds), lens, sizes, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
+    (q, k, v, o, do), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
+    (q, qs), (k, ks), (v, vs), (o, os_), (do, ds) = _layout(q), _layout(k), _layout(v), _layout(o), _layout(do)
     B, H, HK, NQ, NK, D = sizes
-    dev, index = q.device, q.get_device()
     if os_ != ds:  # the library reads both with one set of strides
         o, do = (t.clone(memory_format=torch.contiguous_format) for t in (o, do))
         os_ = (H * NQ * D, NQ * D, D)
     lse = _rows(lse, dev, (B, H, NQ), "lse")
     dlse = _rows(dlse, dev, (B, H, NQ), "dlse")
-    s = make_attn_shape(*sizes, scale, causal, *lens, qs, ks, vs, os_)
-    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", index, *sizes)
+    s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, os_)
+    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", dev.index, *sizes)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     dq = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     dk = torch.empty_strided((B, HK, NK, D), (*ks, 1), dtype=torch.bfloat16, device=dev)
     dv = torch.empty_strided((B, HK, NK, D), (*vs, 1), dtype=torch.bfloat16, device=dev)
-    _call("streamkl_attn_bwd", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+    _call("streamkl_attn_bwd", dev.index, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
           do.data_ptr(), None if dlse is None else dlse.data_ptr(), s, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
           ws.data_ptr() if nbytes else None, nbytes)
-    return _back((dq, dk, dv), host)
+    return _back((dq, dk, dv), True) if host else (dq, dk, dv)
 
 
 def _logits_rows(logits, tokens):
     """Validates logits [..., V] and tokens [...] or [..., T]; returns (device logits as strided [R, V] rows,
-    contiguous int64 device tokens or None, T, was_host)."""
+    contiguous int64 device tokens or None, T, the leading shape, device, was_host)."""
+    shape, dev = logits.shape, logits.device
     if logits.dtype not in DTYPES:
         raise TypeError("logits must be bfloat16, float16 or float32")
-    if logits.dim() < 1 or logits.shape[-1] == 0:
+    if len(shape) < 1 or shape[-1] == 0:
         raise ValueError("logits must be [..., V] with V > 0")
-    T = 0
+    V, lead, T = shape[-1], shape[:-1], 0
     if tokens is not None:
         if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
             raise TypeError("tokens must be int64 or int32")
-        lead = logits.shape[:-1]
-        if tokens.shape == lead:
+        given = tokens.shape
+        if given == lead:
             T = 1
-        elif tokens.dim() == logits.dim() and tokens.shape[:-1] == lead:
-            T = tokens.shape[-1]
+        elif len(given) == len(shape) and given[:-1] == lead:
+            T = given[-1]
         else:
-            raise ValueError(f"tokens {tuple(tokens.shape)} do not fit logits {tuple(logits.shape)}")
-        if tokens.get_device() != logits.get_device():
+            raise ValueError(f"tokens {tuple(given)} do not fit logits {tuple(shape)}")
+        if tokens.device != dev:
             raise ValueError("inputs on different devices")
-    host = not logits.is_cuda
+    host = dev.type == "cpu"
     if host:
-        logits = logits.to(torch.device("cuda", torch.cuda.current_device()), non_blocking=True)
-    V = logits.shape[-1]
-    x = logits if logits.dim() == 2 else logits.reshape(-1, V)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        logits = logits.to(dev, non_blocking=True)
+    x = logits if len(shape) == 2 else logits.reshape(-1, V)
     if not x.is_contiguous() and ((V > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < V)):
         x = x.contiguous()
     if not T:
-        return x, None, 0, host
+        return x, None, 0, lead, dev, host
     if host or tokens.dtype is not torch.int64:
-        tokens = tokens.to(device=x.device, dtype=torch.int64, non_blocking=True)
-    return x, tokens.contiguous(), T, host
+        tokens = tokens.to(device=dev, dtype=torch.int64, non_blocking=True)
+    return x, tokens if tokens.is_contiguous() else tokens.contiguous(), T, lead, dev, host
 
 
 def _row_stride(x):
@@ -596,28 +597,26 @@ def logprobs_fwd(logits, tokens=None, scale=1.0, top_k=0):
     negative one is no token (its logp is 0).  logp has the shape of tokens; entropy and lse are [...];
     top_logp fp32 and top_index int64 are [..., top_k], the largest logits (equal ones: the lowest index first).
     """
-    x, tok, T, host = _logits_rows(logits, tokens)
+    x, tok, T, lead, dev, host = _logits_rows(logits, tokens)
     R, V = x.shape
     if not 0 <= top_k <= min(LOGPROBS_MAX_TOP_K, V):
         raise ValueError(f"top_k must be between 0 and min({LOGPROBS_MAX_TOP_K}, V)")
-    lead, dev = logits.shape[:-1], x.device
     logp = torch.empty(tokens.shape if tokens is not None else (*lead, 0), dtype=torch.float32, device=dev)
     entropy = torch.empty(lead, dtype=torch.float32, device=dev)
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     top = torch.empty((*lead, top_k), dtype=torch.float32, device=dev)
     idx = torch.empty((*lead, top_k), dtype=torch.int64, device=dev)
-    _call("streamkl_logprobs_fwd", x.get_device(), x.data_ptr(), DTYPES[x.dtype], R, V, _row_stride(x),
+    _call("streamkl_logprobs_fwd", dev.index, x.data_ptr(), DTYPES[x.dtype], R, V, _row_stride(x),
           tok.data_ptr() if T else None, T, scale, top_k, logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
           top.data_ptr(), idx.data_ptr())
-    return _back((logp, entropy, lse, top, idx), host)
+    return _back((logp, entropy, lse, top, idx), True) if host else (logp, entropy, lse, top, idx)
 
 
 def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0):
     """Gradient of the logits, contiguous and of their type, for upstream gradients g_logp (tokens' shape) and
     g_entropy ([...] or None); lse and entropy are logprobs_fwd's (entropy may be None without g_entropy)."""
-    x, tok, T, host = _logits_rows(logits, tokens)
+    x, tok, T, lead, dev, host = _logits_rows(logits, tokens)
     R, V = x.shape
-    lead, dev = logits.shape[:-1], x.device
     lse = _rows(lse, dev, lead, "lse")
     ent = None
     if g_entropy is not None:
@@ -628,10 +627,10 @@ def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0
     if T and g_logp is None:
         raise ValueError("tokens need g_logp")
     out = torch.empty(logits.shape, dtype=x.dtype, device=dev)
-    _call("streamkl_logprobs_bwd", x.get_device(), x.data_ptr(), DTYPES[x.dtype], R, V, _row_stride(x),
+    _call("streamkl_logprobs_bwd", dev.index, x.data_ptr(), DTYPES[x.dtype], R, V, _row_stride(x),
           tok.data_ptr() if T else None, T, scale, lse.data_ptr(), None if ent is None else ent.data_ptr(),
           g_logp.data_ptr() if T else None, None if ent is None else g_entropy.data_ptr(), out.data_ptr(), V)
-    return _back((out,), host)[0]
+    return _back((out,), True)[0] if host else out
 
 
 def check_device_status(device=None) -> int:

@@ -709,7 +709,9 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
   }
   int* status = nullptr;
   if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
-  return from_cuda(launch_attn_bwd(p, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, status,
+  int sms = 0;
+  if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+  return from_cuda(launch_attn_bwd(p, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, sms, status,
                                    static_cast<cudaStream_t>(stream)));
 }
 

@@ -44,4 +44,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
   tmem_st16(taddr + 16, *reinterpret_cast<const uint32_t(*)[16]>(&r[16]));
 }
 
+// ---- a tile out: fp32 rows in registers -> bf16 in a swizzled tile in shared memory -> one TMA store.  Written from
+// registers a thread's row would scatter over 32 lines to a store: 2000 cycles a 128 x 128 tile against 300.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// 32 columns from `col` of row r, `f` times, into the tile at `tile`.
+__device__ __forceinline__ void stage_row32(uint32_t tile, int r, int col, const uint32_t (&a)[32], float f) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(__uint_as_float(a[8 * v + 2 * e]) * f, __uint_as_float(a[8 * v + 2 * e + 1]) * f);
+    st_shared16(sw128<128>(tile, r, col / 8 + v), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+// Stores the tile (D / 64 halves of 128-byte rows); one thread, after a fence and a barrier of the writers.
+template <int D>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t tile, int y, int z, int w) {
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h) tma_store_4d(map, tile + h * 128 * 128, h * 64, y, z, w);
+  bulk_commit();
+  bulk_wait_read();
+}
+
 }  // namespace skl

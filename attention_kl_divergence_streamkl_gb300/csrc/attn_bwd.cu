@@ -34,8 +34,8 @@ constexpr int THREADS = 20 * 32;
 constexpr int kRegsDs = 104, kRegsOther = 64;  // 512 * 104 + 128 * 64 = 640 * 96 registers at launch
 constexpr uint32_t kTmemCols = 512;
 
-struct BwdOut {
-  __nv_bfloat16 *dq, *dk, *dv;
+struct BwdMaps {  // of the inputs, and of the outputs
+  CUtensorMap q, k, v, go, dq, dk, dv;
 };
 
 // ---------------------------------------------------------------------------
@@ -130,18 +130,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One row of an accumulator tile (32 of its columns) as bf16, `f` times the fp32 values.
-__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (&a)[32], float f) {
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack_bf16(__uint_as_float(a[8 * v + 2 * e]) * f, __uint_as_float(a[8 * v + 2 * e + 1]) * f);
-    reinterpret_cast<uint4*>(dst)[v] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
 // ---------------------------------------------------------------------------
 // dK/dV block.  The logits are computed transposed, so the TMEM lanes are keys
 // and the columns queries: S^T = K Q^T and dP^T = V dO^T (both operands K-major
@@ -197,9 +185,8 @@ __device__ __forceinline__ uint64_t sdesc_step(uint32_t addr, uint32_t zero) {
 
 template <int D>
 __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __restrict__ row_s,
-                                         const uint4* __restrict__ row_d, int padded, const BwdOut& out, int* status,
-                                         const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                         const CUtensorMap& mo, const unsigned blk) {
+                                         const uint4* __restrict__ row_d, int padded, int* status, const BwdMaps& maps,
+                                         const unsigned blk, const int longest_first) {
   using L = kv::Smem<D>;
   using kv::SLOTS;
   extern __shared__ uint8_t smem_raw[];
@@ -207,11 +194,11 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // heads in order (the blocks in flight share one key head's query tiles in L2); within a head the first key
-  // tiles, which see the most queries under a causal mask, first
-  const int n_kt = (p.NK + BT - 1) / BT;
-  const int bhk = (int)(blk / n_kt);
+  // tiles, which see the most queries under a causal mask, first.  A small grid: the first key tiles of all heads first
+  const int n_kt = (p.NK + BT - 1) / BT, heads = p.B * p.HK;
+  const int bhk = longest_first ? (int)(blk % heads) : (int)(blk / n_kt);
   const int b = bhk / p.HK, hk = bhk % p.HK;
-  const int k0 = (int)(blk % n_kt) * BT;
+  const int k0 = (longest_first ? (int)(blk / heads) : (int)(blk % n_kt)) * BT;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
@@ -263,8 +250,8 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
         mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-          tma_load_4d(sb + L::OFF_K + h * BT * 128, &mk, kv_full, h * 64, k0, hk, b);
-          tma_load_4d(sb + L::OFF_V + h * BT * 128, &mv, kv_full, h * 64, k0, hk, b);
+          tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
+          tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
         }
         int issued_q = 0, issued_o = 0;
         for (int u = 0; u < n; ++u) {
@@ -274,14 +261,14 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
           mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &mq, q_full + 8 * s, h * 64, q0, hq, b);
+            tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &maps.q, q_full + 8 * s, h * 64, q0, hq, b);
           bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + row, L::STEP, q_full + 8 * s);
           issued_q = u + 1;
           if (u >= SLOTS && !mbar_wait(o_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
           mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &mo, o_full + 8 * s, h * 64, q0, hq, b);
+            tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &maps.go, o_full + 8 * s, h * 64, q0, hq, b);
           bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + row, L::STEP, o_full + 8 * s);
           issued_o = u + 1;
         }
@@ -441,10 +428,9 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       got = mbar_wait_warp(g_done, 0, status, abort_flag);
       __syncwarp();
     }
+    // dV through the first Q slot, dK through the first dO slot: every product that read them is done
     if (got && grp * 32 < D) {
       tc_fence_after();
-      const long long kat = b * p.ks_b + hk * p.ks_h + (long long)key * p.ks_n + grp * 32;
-      const long long vat = b * p.vs_b + hk * p.vs_h + (long long)key * p.vs_n + grp * 32;
       uint32_t g[32];
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
@@ -457,8 +443,14 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = 0u;
         }
-        if (key < p.NK) store_row32(which ? out.dk + kat : out.dv + vat, g, which ? p.scale : 1.f);
+        stage_row32(sb + (which ? L::OFF_O : L::OFF_Q), r, 32 * grp, g, which ? p.scale : 1.f);
       }
+      fence_async_smem();
+    }
+    // every warp comes here; one that gave up makes none of them store
+    if (!named_bar_any(1, DS_WARPS * 32, !got) && threadIdx.x == 0) {
+      store_tile<D>(&maps.dv, sb + L::OFF_Q, k0, hk, b);
+      store_tile<D>(&maps.dk, sb + L::OFF_O, k0, hk, b);
     }
   }
   tc_fence_before();
@@ -518,9 +510,8 @@ __device__ __forceinline__ void ds32(const uint32_t (&a)[32], const uint32_t (&d
 
 template <int D>
 __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __restrict__ row_s,
-                                        const uint4* __restrict__ row_d, int padded, const BwdOut& out, int* status,
-                                        const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                                        const CUtensorMap& mo, const unsigned blk) {
+                                        const uint4* __restrict__ row_d, int padded, int* status, const BwdMaps& maps,
+                                        const unsigned blk, const int longest_first) {
   using L = qq::Smem<D>;
   using qq::K_SLOTS;
   using qq::V_SLOTS;
@@ -529,9 +520,11 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = (p.NQ + BT - 1) / BT;
-  const int bh = (int)(blk / n_qt);
+  const int heads = p.B * p.H;
+  const int bh = longest_first ? (int)(blk % heads) : (int)(blk / n_qt);
   const int b = bh / p.H, h = bh % p.H, hk = h / p.G;
-  const int q0 = (n_qt - 1 - (int)(blk % n_qt)) * BT;  // the last query tiles, which see the most keys, first
+  // the last query tiles, which see the most keys, first
+  const int q0 = (n_qt - 1 - (longest_first ? (int)(blk / heads) : (int)(blk % n_qt))) * BT;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int last = min(q0 + BT, ql) - 1;
@@ -580,8 +573,8 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
         mbar_arrive_expect_tx(x_full, 2 * L::TILE);
 #pragma unroll
         for (int d = 0; d < D / 64; ++d) {
-          tma_load_4d(sb + L::OFF_Q + d * BT * 128, &mq, x_full, d * 64, q0, h, b);
-          tma_load_4d(sb + L::OFF_O + d * BT * 128, &mo, x_full, d * 64, q0, h, b);
+          tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
+          tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
         }
         int issued_k = 0, issued_v = 0;
         for (int j = 0; j < n; ++j) {
@@ -590,13 +583,13 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
           mbar_arrive_expect_tx(k_full + 8 * sk, L::TILE);
 #pragma unroll
           for (int d = 0; d < D / 64; ++d)
-            tma_load_4d(sb + L::OFF_K + sk * L::TILE + d * BT * 128, &mk, k_full + 8 * sk, d * 64, j * BT, hk, b);
+            tma_load_4d(sb + L::OFF_K + sk * L::TILE + d * BT * 128, &maps.k, k_full + 8 * sk, d * 64, j * BT, hk, b);
           issued_k = j + 1;
           if (j >= V_SLOTS && !mbar_wait(v_empty + 8 * sv, ((j / V_SLOTS) - 1) & 1, status, abort_flag)) break;
           mbar_arrive_expect_tx(v_full + 8 * sv, L::TILE);
 #pragma unroll
           for (int d = 0; d < D / 64; ++d)
-            tma_load_4d(sb + L::OFF_V + sv * L::TILE + d * BT * 128, &mv, v_full + 8 * sv, d * 64, j * BT, hk, b);
+            tma_load_4d(sb + L::OFF_V + sv * L::TILE + d * BT * 128, &maps.v, v_full + 8 * sv, d * 64, j * BT, hk, b);
           issued_v = j + 1;
         }
         mbar_drain(x_full, 0, status);
@@ -729,9 +722,12 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
 #pragma unroll
         for (int i = 0; i < 32; ++i) g[i] = 0u;
       }
-      if (q < p.NQ)
-        store_row32(out.dq + b * p.qs_b + h * p.qs_h + (long long)q * p.qs_n + grp * 32, g, p.scale);
+      stage_row32(sb + L::OFF_K, r, 32 * grp, g, p.scale);  // through the first K slot: its products are done
+      fence_async_smem();
     }
+    // every warp comes here; one that gave up makes none of them store
+    if (!named_bar_any(1, DS_WARPS * 32, !got) && threadIdx.x == 0)
+      store_tile<D>(&maps.dq, sb + L::OFF_K, q0, h, b);
   }
   tc_fence_before();
   __syncthreads();
@@ -744,16 +740,15 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_bwd_kernel(const AttnProblem p, const uint4* __restrict__ row_s, const uint4* __restrict__ row_d, int padded,
-                    const BwdOut out, int* status, const __grid_constant__ CUtensorMap mq,
-                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                    const __grid_constant__ CUtensorMap mo, const unsigned n_first, const int q_first) {
+                    int* status, const __grid_constant__ BwdMaps maps, const unsigned n_first, const int q_first,
+                    const int longest_first) {
   const unsigned x = blockIdx.x;
   const bool is_q = q_first ? x < n_first : x >= n_first;
   const unsigned blk = x < n_first ? x : x - n_first;
   if (is_q)
-    q_block<D>(p, row_s, row_d, padded, out, status, mq, mk, mv, mo, blk);
+    q_block<D>(p, row_s, row_d, padded, status, maps, blk, longest_first);
   else
-    kv_block<D>(p, row_s, row_d, padded, out, status, mq, mk, mv, mo, blk);
+    kv_block<D>(p, row_s, row_d, padded, status, maps, blk, longest_first);
 }
 
 // Zeros for `rows` rows of each of B H heads (a backward without queries or without keys).
@@ -763,14 +758,23 @@ __global__ void attn_zero_rows_kernel(__nv_bfloat16* dst, int H, int rows, int D
   dst[r / rows / H * sb + r / rows % H * sh + r % rows * sn + threadIdx.x] = __float2bfloat16_rn(0.f);
 }
 
+// In a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for).
+constexpr int kSmallGrid = 6;
+
 template <int D>
 cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
-                     int* status, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mo;
-  if (!encode_tile_map(&mq, in.q, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, BT) ||
-      !encode_tile_map(&mk, in.k, p.D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
-      !encode_tile_map(&mv, in.v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
-      !encode_tile_map(&mo, in.go, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, BT))
+                     int num_sms, int* status, cudaStream_t st) {
+  BwdMaps m;
+  auto q_map = [&](CUtensorMap* map, const void* x, long long sn, long long sh, long long sb) {
+    return encode_tile_map(map, x, p.D, p.NQ, p.H, p.B, sn, sh, sb, BT);
+  };
+  auto k_map = [&](CUtensorMap* map, const void* x, long long sn, long long sh, long long sb) {
+    return encode_tile_map(map, x, p.D, p.NK, p.HK, p.B, sn, sh, sb, BT);
+  };
+  if (!q_map(&m.q, in.q, p.qs_n, p.qs_h, p.qs_b) || !k_map(&m.k, in.k, p.ks_n, p.ks_h, p.ks_b) ||
+      !k_map(&m.v, in.v, p.vs_n, p.vs_h, p.vs_b) || !q_map(&m.go, in.go, p.os_n, p.os_h, p.os_b) ||
+      !q_map(&m.dq, dq, p.qs_n, p.qs_h, p.qs_b) || !k_map(&m.dk, dk, p.ks_n, p.ks_h, p.ks_b) ||
+      !k_map(&m.dv, dv, p.vs_n, p.vs_h, p.vs_b))
     return cudaErrorInvalidValue;
   const int padded = (p.NQ + BT - 1) / BT * BT;
   const long long rows = (long long)p.B * p.H * padded;
@@ -787,11 +791,11 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
   const long long q_blocks = (long long)p.B * p.H * (padded / BT);
   const long long kv_blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
-  const BwdOut out{static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv)};
   // a dQ block walks the keys with three products a tile, a dK/dV block the queries of G heads with four
   const int q_first = 3ll * p.NK > 4ll * p.G * p.NQ;
-  kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, row_s, row_d, padded, out, status, mq, mk, mv, mo,
-                                                                (unsigned)(q_first ? q_blocks : kv_blocks), q_first);
+  kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, row_s, row_d, padded, status, m,
+                                                                (unsigned)(q_first ? q_blocks : kv_blocks), q_first,
+                                                                q_blocks + kv_blocks <= kSmallGrid * num_sms);
   return cudaGetLastError();
 }
 
@@ -803,7 +807,7 @@ size_t attn_bwd_workspace(const AttnProblem& p) {
 }
 
 cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
-                            int* status, cudaStream_t st) {
+                            int num_sms, int* status, cudaStream_t st) {
   if (p.NQ == 0 || p.NK == 0) {
     auto* q = static_cast<__nv_bfloat16*>(dq);
     auto* k = static_cast<__nv_bfloat16*>(dk);
@@ -818,8 +822,8 @@ cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq,
     }
     return cudaGetLastError();
   }
-  if (p.D == 64) return launch_d<64>(p, in, dq, dk, dv, workspace, status, st);
-  return launch_d<128>(p, in, dq, dk, dv, workspace, status, st);
+  if (p.D == 64) return launch_d<64>(p, in, dq, dk, dv, workspace, num_sms, status, st);
+  return launch_d<128>(p, in, dq, dk, dv, workspace, num_sms, status, st);
 }
 
 }  // namespace skl

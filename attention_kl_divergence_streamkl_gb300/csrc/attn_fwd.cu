@@ -80,10 +80,10 @@ __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    attn_fwd_kernel(const AttnProblem p, __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse,
+    attn_fwd_kernel(const AttnProblem p, float* __restrict__ out_lse,
                     float* __restrict__ part_o, float2* __restrict__ part_ml, int* status,
                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv) {
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
   using L = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -93,9 +93,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   // item: (batch, head or key head, pair of query tiles), the longest causal ones first; then the key split
   const int split = (int)(blockIdx.x % p.splits);
   const int item = (int)(blockIdx.x / p.splits);
-  const int qt = p.q_items - 1 - item % p.q_items;
-  const int bh = item / p.q_items;
   const int heads = p.packed ? p.HK : p.H;
+  const int qt = p.q_items - 1 - (p.longest_first ? item / (p.B * heads) : item % p.q_items);
+  const int bh = p.longest_first ? item % (p.B * heads) : item / p.q_items;
   const int b = bh / heads, hx = bh % heads;  // hx: key head when packed, else query head
   const int hk = p.packed ? hx : hx / p.G;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
@@ -351,49 +351,43 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = mbar_wait_warp(o_done + 8 * t, (nt - 1) & 1, status, abort_flag);
       __syncwarp();
     }
-    if (ok && (t == 0 || has_b)) {
-      tc_fence_after();
+    if (t == 0 || has_b) {
       const size_t row = ((size_t)b * p.H + h) * p.NQ + qn;
-      const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees no key: zeros
       const bool nan = l != l;
-      if (p.splits > 1) {
-        if (real) part_ml[(size_t)split * p.rows + row] = make_float2(m, l);
-      } else if (real) {
-        out_lse[row] = (l > 0.f || nan) ? (m + log2f(l)) * kLn2 : kNegInf;
-      }
+      const float f = nan ? l : l > 0.f ? 1.f / l : 0.f;  // a row that sees no key: zeros
+      if (ok) {
+        tc_fence_after();
+        if (real && p.splits > 1)
+          part_ml[(size_t)split * p.rows + row] = make_float2(m, l);
+        else if (real)
+          out_lse[row] = (l > 0.f || nan) ? (m + log2f(l)) * kLn2 : kNegInf;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        uint32_t o[32];
-        if (nt > 0) {
-          tmem_ld32(to + d, o);
-          tmem_ld_wait();
-          reg_fence32(o);
-        }
-        if (!(l > 0.f) && !nan) {
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          if (nt > 0) {
+            tmem_ld32(to + d, o);
+            tmem_ld_wait();
+            reg_fence32(o);
+          }
+          if (!(l > 0.f) && !nan) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        }
-        if (!real) continue;
-        if (p.splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(part_o + ((size_t)split * p.rows + row) * D + d);
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          }
+          if (p.splits == 1) {
+            stage_row32(sb + L::OFF_Q + t * L::TILE, r, d, o, f);  // Q's products are done
+          } else if (real) {
+            float4* dst = reinterpret_cast<float4*>(part_o + ((size_t)split * p.rows + row) * D + d);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                                 __uint_as_float(o[4 * k + 3]));
-        } else {
-          const float f = nan ? l : inv;
-          uint4* dst = reinterpret_cast<uint4*>(out + (long long)b * p.os_b + (long long)h * p.os_h +
-                                                (long long)qn * p.os_n + d);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16(__uint_as_float(o[8 * k + 2 * e]) * f, __uint_as_float(o[8 * k + 2 * e + 1]) * f);
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                   __uint_as_float(o[4 * k + 3]));
           }
         }
+        fence_async_smem();
       }
+      // every warp of the tile comes here; one that gave up makes none of them store
+      if (!named_bar_any(1 + t, SOFTMAX_WARPS / 2 * 32, !ok) && p.splits == 1 && r == 0)
+        store_tile<D>(&mo, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
     }
   }
   tc_fence_before();
@@ -440,10 +434,11 @@ __global__ void __launch_bounds__(256)
 template <int D>
 cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
                      void* workspace, int* status, cudaStream_t st) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   if (!encode_tile_map(&mq, q, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1) ||
       !encode_tile_map(&mk, k, p.D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BN) ||
-      !encode_tile_map(&mv, v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BN))
+      !encode_tile_map(&mv, v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BN) ||
+      !encode_tile_map(&mo, o, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1))
     return cudaErrorInvalidValue;
   constexpr int smem = Smem<D>::BYTES > kOneBlockPerSmSmem ? Smem<D>::BYTES : kOneBlockPerSmSmem;
   cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -452,7 +447,7 @@ cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const v
   float2* part_ml = p.splits > 1 ? reinterpret_cast<float2*>(part_o + (size_t)p.splits * p.rows * D) : nullptr;
   auto* out = static_cast<__nv_bfloat16*>(o);
   const long long blocks = attn_fwd_items(p) * p.splits;
-  attn_fwd_kernel<D><<<(unsigned)blocks, THREADS, smem, st>>>(p, out, lse, part_o, part_ml, status, mq, mk, mv);
+  attn_fwd_kernel<D><<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
   attn_merge_kernel<D><<<(unsigned)((p.rows + 7) / 8), 256, 0, st>>>(p, part_o, part_ml, out, lse);
   return cudaGetLastError();
@@ -475,6 +470,7 @@ long long attn_fwd_items(const AttnProblem& p) {
 // Blocks of a split have at least this many key tiles: a split costs the second launch and a round trip of its
 // partial through L2, about as much as three or four tiles.
 constexpr int kMinTilesPerSplit = 4;
+constexpr int kSmallGrid = 6;
 void attn_fwd_plan(AttnProblem* p, int num_sms) {
   p->packed = (long long)p->G * p->NQ <= BM;
   p->q_items = p->packed ? 1 : (p->NQ + 2 * BM - 1) / (2 * BM);
@@ -492,6 +488,8 @@ void attn_fwd_plan(AttnProblem* p, int num_sms) {
     }
   }
   p->splits = best;
+  // in a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for)
+  p->longest_first = items * best <= kSmallGrid * num_sms;
 }
 
 size_t attn_fwd_workspace(const AttnProblem& p) {

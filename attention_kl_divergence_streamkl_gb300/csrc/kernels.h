@@ -105,6 +105,7 @@ struct AttnProblem {
   int packed;   // the query heads of a key head share one tile
   int q_items;  // blocks along the queries, per (batch, head)
   int splits;   // blocks along the keys
+  int longest_first;  // the last query tiles of all heads first, not head by head
 };
 void attn_fwd_plan(AttnProblem* p, int num_sms);
 long long attn_fwd_items(const AttnProblem& p);
@@ -118,7 +119,7 @@ struct AttnBwdIn {
 };
 size_t attn_bwd_workspace(const AttnProblem& p);
 cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
-                            int* status, cudaStream_t st);
+                            int num_sms, int* status, cudaStream_t st);
 
 // ---- log probabilities of given tokens ---------------------------------------------
 constexpr int kTypeBf16 = 0, kTypeFp16 = 1, kTypeFp32 = 2;  // streamkl_dtype

@@ -34,7 +34,9 @@ def check(q, k, v, do, dlse=None, **kw):
 @pytest.mark.parametrize("B,H,HK,NQ,NK", [
     (1, 1, 1, 1, 1), (1, 1, 1, 2, 2), (2, 2, 1, 1, 2), (1, 4, 2, 3, 127), (1, 3, 3, 128, 128), (1, 2, 2, 129, 129),
     (2, 6, 2, 255, 300), (1, 2, 1, 256, 256), (1, 2, 2, 257, 511), (1, 8, 1, 16, 1000), (1, 1, 1, 600, 640),
-    (1, 1, 1, 300, 100), (1, 6, 3, 500, 70), (1, 2, 2, 1000, 1000)])
+    (1, 1, 1, 300, 100), (1, 6, 3, 500, 70), (1, 2, 2, 1000, 1000),
+    # long streams of few tiles
+    (1, 2, 1, 100, 4200), (1, 8, 1, 1200, 90), (2, 1, 1, 2100, 2200)])
 def test_backward(B, H, HK, NQ, NK, causal, D):
     q, k, v, do = A.tensors(B, H, HK, NQ, NK, D, B + NQ + NK)
     check(q, k, v, do, causal=causal)
