@@ -80,8 +80,9 @@ SIGNATURES = {
     "streamkl_attn_fwd_workspace": (_I, [AttnShape, ctypes.POINTER(_SZ)]),
     "streamkl_attn_fwd_plan": (_I, [AttnShape, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "streamkl_attn_fwd": (_I, [_P, _P, _P, AttnShape, _P, _F, _P, _SZ, _S]),
-    "streamkl_attn_bwd_workspace": (_I, [AttnShape, ctypes.POINTER(_SZ)]),
-    "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _P, _SZ, _S]),
+    "streamkl_attn_bwd_select": (_I, [AttnShape, _I]),
+    "streamkl_attn_bwd_workspace": (_I, [AttnShape, _I, ctypes.POINTER(_SZ)]),
+    "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
     "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
@@ -498,11 +499,11 @@ def attn_fwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
 
 
 @functools.lru_cache(maxsize=1024)
-def _attn_workspace(name, index, *sizes):
+def _attn_workspace(name, index, sizes, *mode):
     """Workspace bytes of an attention of these sizes on device `index` (a pure rule of sizes and the device)."""
     n = ctypes.c_size_t(0)
     with torch.cuda.device(index):
-        _check(getattr(lib(), name)(make_attn_shape(*sizes), ctypes.byref(n)), name)
+        _check(getattr(lib(), name)(make_attn_shape(*sizes), *mode, ctypes.byref(n)), name)
     return n.value
 
 
@@ -517,7 +518,7 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
     B, H, _, NQ, _, D = sizes
     s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, qs)
-    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", dev.index, *sizes)
+    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", dev.index, sizes)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     o = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
@@ -526,10 +527,17 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     return _back((o, lse), True) if host else (o, lse)
 
 
-def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None):
+def attn_bwd_select(B, H, HK, NQ, NK, D, num_sms, causal=False) -> int:
+    """The path BWD_AUTO takes in attn_bwd on a device with num_sms SMs."""
+    return lib().streamkl_attn_bwd_select(make_attn_shape(B, H, HK, NQ, NK, D, None, causal), int(num_sms))
+
+
+def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None, bwd_mode=BWD_AUTO):
     """Attention's gradients (dq, dk, dv), bf16 with the layouts of q, k, v.
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
+    bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED visits each tile pair once and adds dq up in no
+    fixed order; BWD_AUTO picks by shape.
     """
     (q, k, v, o, do), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
     (q, qs), (k, ks), (v, vs), (o, os_), (do, ds) = _layout(q), _layout(k), _layout(v), _layout(o), _layout(do)
@@ -540,14 +548,14 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
     lse = _rows(lse, dev, (B, H, NQ), "lse")
     dlse = _rows(dlse, dev, (B, H, NQ), "dlse")
     s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, os_)
-    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", dev.index, *sizes)
+    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", dev.index, sizes, bwd_mode)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     dq = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     dk = torch.empty_strided((B, HK, NK, D), (*ks, 1), dtype=torch.bfloat16, device=dev)
     dv = torch.empty_strided((B, HK, NK, D), (*vs, 1), dtype=torch.bfloat16, device=dev)
     _call("streamkl_attn_bwd", dev.index, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
           do.data_ptr(), None if dlse is None else dlse.data_ptr(), s, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-          ws.data_ptr() if nbytes else None, nbytes)
+          bwd_mode, ws.data_ptr() if nbytes else None, nbytes)
     return _back((dq, dk, dv), True) if host else (dq, dk, dv)
 
 

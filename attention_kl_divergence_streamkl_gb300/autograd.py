@@ -63,10 +63,10 @@ def attention_kl(q1, k1, q2, k2, scale=None, causal=False, reduction="mean", bwd
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, scale, causal, q_lens, k_lens):
+    def forward(ctx, q, k, v, scale, causal, q_lens, k_lens, bwd_mode):
         o, lse = _lib.attn_fwd(q, k, v, scale, causal, q_lens, k_lens)
         ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens)
-        ctx.scale, ctx.causal = scale, causal
+        ctx.scale, ctx.causal, ctx.bwd_mode = scale, causal, bwd_mode
         ctx.set_materialize_grads(False)
         return o, lse
 
@@ -75,20 +75,22 @@ class _Attention(torch.autograd.Function):
     def backward(ctx, do, dlse):
         q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
         if do is None and dlse is None:
-            return (None,) * 7
+            return (None,) * 8
         if do is None:
             do = torch.zeros_like(o)
-        return (*_lib.attn_bwd(q, k, v, o, lse, do, dlse, ctx.scale, ctx.causal, q_lens, k_lens), None, None, None, None)
+        return (*_lib.attn_bwd(q, k, v, o, lse, do, dlse, ctx.scale, ctx.causal, q_lens, k_lens, ctx.bwd_mode),
+                None, None, None, None, None)
 
 
-def attention(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, return_lse=False):
+def attention(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, return_lse=False, bwd_mode=_lib.BWD_AUTO):
     """softmax(scale Q K^T) V, differentiable: bf16 [B, H, N_Q, D], and with return_lse the rows' log-sum-exp
     (fp32 [B, H, N_Q], differentiable too).
 
     The attention of a model that is distilled with attention_kl, which takes the same q and k.  k and v may have
-    fewer heads than q; q_lens, k_lens (int32 [B]) are the lengths of a padded batch's sequences.  See attn_fwd.
+    fewer heads than q; q_lens, k_lens (int32 [B]) are the lengths of a padded batch's sequences.  See attn_fwd,
+    and attn_bwd for bwd_mode.
     """
-    o, lse = _Attention.apply(q, k, v, scale, causal, q_lens, k_lens)
+    o, lse = _Attention.apply(q, k, v, scale, causal, q_lens, k_lens, bwd_mode)
     return (o, lse) if return_lse else o
 
 

@@ -246,15 +246,15 @@ __global__ void wait_timeout_probe_kernel(unsigned long long limit_ns, int* stat
 
 }  // namespace
 
-bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows) {
+bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows, int box_cols) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)BH};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 4, (cuuint64_t)rows * D * 4};
-  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)box_rows, 1u};
+  const cuuint32_t box[3] = {(cuuint32_t)(box_cols ? box_cols : D), (cuuint32_t)box_rows, 1u};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            box_cols ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -684,34 +684,51 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
   return from_cuda(launch_attn_fwd(p, q, k, v, o, lse, workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
-streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, size_t* bytes) {
+static bool attn_mode_ok(int mode) {
+  return mode == STREAMKL_BWD_AUTO || mode == STREAMKL_BWD_FUSED || mode == STREAMKL_BWD_SEPARATE;
+}
+
+int streamkl_attn_bwd_select(streamkl_attn_shape s, int num_sms) {
+  AttnProblem p;
+  if (attn_problem(s, &p) != STREAMKL_OK || num_sms <= 0) return 0;
+  return attn_bwd_fused(p, STREAMKL_BWD_AUTO, num_sms) ? STREAMKL_BWD_FUSED : STREAMKL_BWD_SEPARATE;
+}
+
+streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, int bwd_mode, size_t* bytes) {
   AttnProblem p;
   streamkl_status v = attn_problem(s, &p);
   if (v != STREAMKL_OK) return v;
-  if (!bytes) return STREAMKL_ERR_INVALID;
-  *bytes = attn_bwd_workspace(p);
+  if (!bytes || !attn_mode_ok(bwd_mode)) return STREAMKL_ERR_INVALID;
+  int sms = 0;
+  if (bwd_mode == STREAMKL_BWD_AUTO && (v = device_sms(&sms)) != STREAMKL_OK) return v;
+  *bytes = attn_bwd_workspace(p, attn_bwd_fused(p, bwd_mode, sms));
   return STREAMKL_OK;
 }
 
 streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
                                   const void* go, const float* dlse, streamkl_attn_shape s, void* dq, void* dk,
-                                  void* dv, void* workspace, size_t workspace_bytes, void* stream) {
+                                  void* dv, int bwd_mode, void* workspace, size_t workspace_bytes, void* stream) {
   AttnProblem p;
   streamkl_status st = attn_problem(s, &p);
   if (st != STREAMKL_OK) return st;
+  if (!attn_mode_ok(bwd_mode)) return STREAMKL_ERR_INVALID;
   if (p.NQ > 0 && (!dq || !aligned16(dq))) return STREAMKL_ERR_INVALID;
   if (p.NK > 0 && (!dk || !dv || !aligned16(dk) || !aligned16(dv))) return STREAMKL_ERR_INVALID;
+  bool fused = false;
+  int sms = 0;
   if (p.NQ > 0 && p.NK > 0) {
     if (!q || !k || !v || !o || !go || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
         !aligned16(go) || !rows_ok(lse) || !aligned_to_or_null(dlse, 4))
       return STREAMKL_ERR_INVALID;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < attn_bwd_workspace(p)) return STREAMKL_ERR_WORKSPACE;
+    if (!workspace || !aligned16(workspace)) return STREAMKL_ERR_WORKSPACE;
+    if (workspace_bytes < attn_bwd_workspace(p, false)) return STREAMKL_ERR_WORKSPACE;
+    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+    fused = attn_bwd_fused(p, bwd_mode, sms);
+    if (workspace_bytes < attn_bwd_workspace(p, fused)) return STREAMKL_ERR_WORKSPACE;
   }
   int* status = nullptr;
   if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
-  int sms = 0;
-  if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
-  return from_cuda(launch_attn_bwd(p, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, sms, status,
+  return from_cuda(launch_attn_bwd(p, fused, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, sms, status,
                                    static_cast<cudaStream_t>(stream)));
 }
 

@@ -44,6 +44,30 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
   tmem_st16(taddr + 16, *reinterpret_cast<const uint32_t(*)[16]>(&r[16]));
 }
 
+// ---- row values of the backward: -LSE / scale and -delta of a query row, each as three bf16 that add up to its 24
+// bits, in 16 bytes.  128 rows of them are the 16-wide K step that adds the rows' values to a product.
+constexpr float kNoRow = -1.0e30f;  // -LSE / scale of a row that sees no key: its P is exactly 0
+
+__device__ __forceinline__ uint4 three_bf16(float x) {
+  const float hi = __bfloat162float(__float2bfloat16_rn(x));
+  const float mid = __bfloat162float(__float2bfloat16_rn(x - hi));
+  return make_uint4(pack_bf16(hi, mid), pack_bf16(x - hi - mid, 0.f), 0u, 0u);
+}
+__device__ __forceinline__ float from_three_bf16(uint2 v) {
+  return __uint_as_float(v.x << 16) + (__uint_as_float(v.x & 0xffff0000u) + __uint_as_float(v.y << 16));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Descriptor of a K-major K step without swizzle: 8-row core matrices 128 bytes apart, the second half of K at `zero`.
+__device__ __forceinline__ uint64_t sdesc_step(uint32_t addr, uint32_t zero) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(((zero - addr) >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
+}
+
 // ---- a tile out: fp32 rows in registers -> bf16 in a swizzled tile in shared memory -> one TMA store.  Written from
 // registers a thread's row would scatter over 32 lines to a store: 2000 cycles a 128 x 128 tile against 300.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {

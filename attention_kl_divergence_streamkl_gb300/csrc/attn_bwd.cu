@@ -10,11 +10,9 @@
 //   dK/dV block  128 keys stationary; streams the query tiles of every query
 //                head that reads them: four products a tile pair
 //   dQ block     128 queries stationary; streams the key tiles: three products
-// (seven where one visit of each tile pair would need five; that visit's dQ
-// would go through fp32 reductions in L2, 64 KB a tile pair, which alone take
-// longer than the two products saved).  Both kinds run in one launch, the
-// kind with the longer blocks first: the shorter ones fill the SMs that the
-// longer ones leave.
+// (attn_bwd_fused.cu visits each tile pair once, for five, and adds dQ up in
+// L2).  Both kinds run in one launch, the kind with the longer blocks first: the
+// shorter ones fill the SMs that the longer ones leave.
 //
 // A small kernel first writes, per query row, -LSE / scale and -delta, each as
 // three bf16 that add up to its 24 bits, in 16 bytes and 128-row padded: a
@@ -45,16 +43,6 @@ struct BwdMaps {  // of the inputs, and of the outputs
 // O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|.  Among many keys that averages out of the
 // gradients; a row that sees few of them passes it on whole.  For rows of at most 32 keys (the first rows under a causal
 // mask, short sequences) delta is computed as sum_j P_ij dP_ij instead, a key to a lane.
-constexpr float kNoRow = -1.0e30f;
-
-__device__ __forceinline__ uint4 three_bf16(float x) {
-  const float hi = __bfloat162float(__float2bfloat16_rn(x));
-  const float mid = __bfloat162float(__float2bfloat16_rn(x - hi));
-  return make_uint4(pack_bf16(hi, mid), pack_bf16(x - hi - mid, 0.f), 0u, 0u);
-}
-__device__ __forceinline__ float from_three_bf16(uint2 v) {
-  return __uint_as_float(v.x << 16) + (__uint_as_float(v.x & 0xffff0000u) + __uint_as_float(v.y << 16));
-}
 // Sum of the products of 8 bf16 pairs.
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -69,7 +57,7 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
 template <int D>
 __global__ void __launch_bounds__(256)
     attn_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
-                     int padded) {
+                     float4* __restrict__ acc, int padded) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
   const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / LANES;  // row of [B H][padded]
   const int lane = threadIdx.x % LANES;
@@ -82,6 +70,10 @@ __global__ void __launch_bounds__(256)
   const int seen = real ? (p.causal ? min(kl, n + kl - ql + 1) : kl) : 0;  // keys this row sees (none: <= 0)
   const long long at = b * p.os_b + h * p.os_h + n * p.os_n;
   const auto* go = static_cast<const __nv_bfloat16*>(in.go) + at;
+  if (acc && inside) {  // the fused kernel's accumulator starts at zero
+    acc[r * (D / 4) + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    acc[r * (D / 4) + LANES + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   float sum = 0.f, l = 0.f;
   if (seen > 0) {
     const auto* o = static_cast<const __nv_bfloat16*>(in.o) + at;
@@ -170,18 +162,6 @@ struct Smem {
 };
 static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
 }  // namespace kv
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-// Descriptor of a K-major K step without swizzle: 8-row core matrices 128 bytes apart, the second half of K at `zero`.
-__device__ __forceinline__ uint64_t sdesc_step(uint32_t addr, uint32_t zero) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(((zero - addr) >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
-}
 
 template <int D>
 __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __restrict__ row_s,
@@ -762,8 +742,23 @@ __global__ void attn_zero_rows_kernel(__nv_bfloat16* dst, int H, int rows, int D
 constexpr int kSmallGrid = 6;
 
 template <int D>
-cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
+cudaError_t launch_d(const AttnProblem& p, bool fused, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
                      int num_sms, int* status, cudaStream_t st) {
+  const int padded = (p.NQ + BT - 1) / BT * BT;
+  const long long rows = (long long)p.B * p.H * padded;
+  uint4* row_s = static_cast<uint4*>(workspace);
+  uint4* row_d = row_s + rows;
+  float* acc = fused ? reinterpret_cast<float*>(row_d + rows) : nullptr;
+  constexpr int row_lanes = D / 8, per_block = 256 / row_lanes;
+  attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
+      p, in, row_s, row_d, reinterpret_cast<float4*>(acc), padded);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long q_blocks = (long long)p.B * p.H * (padded / BT);
+  const long long kv_blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
+  if (fused)
+    return launch_attn_bwd_fused(p, in, dq, dk, dv, row_s, row_d, acc, padded, kv_blocks <= kSmallGrid * num_sms, status,
+                                 st);
   BwdMaps m;
   auto q_map = [&](CUtensorMap* map, const void* x, long long sn, long long sh, long long sb) {
     return encode_tile_map(map, x, p.D, p.NQ, p.H, p.B, sn, sh, sb, BT);
@@ -776,21 +771,11 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
       !q_map(&m.dq, dq, p.qs_n, p.qs_h, p.qs_b) || !k_map(&m.dk, dk, p.ks_n, p.ks_h, p.ks_b) ||
       !k_map(&m.dv, dv, p.vs_n, p.vs_h, p.vs_b))
     return cudaErrorInvalidValue;
-  const int padded = (p.NQ + BT - 1) / BT * BT;
-  const long long rows = (long long)p.B * p.H * padded;
-  uint4* row_s = static_cast<uint4*>(workspace);
-  uint4* row_d = row_s + rows;
-  constexpr int row_lanes = D / 8, per_block = 256 / row_lanes;
-  attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(p, in, row_s, row_d, padded);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   int smem = kOneBlockPerSmSmem;
   if (kv::Smem<D>::BYTES > smem) smem = kv::Smem<D>::BYTES;
   if (qq::Smem<D>::BYTES > smem) smem = qq::Smem<D>::BYTES;
   auto kern = attn_bwd_kernel<D>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  const long long q_blocks = (long long)p.B * p.H * (padded / BT);
-  const long long kv_blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
   // a dQ block walks the keys with three products a tile, a dK/dV block the queries of G heads with four
   const int q_first = 3ll * p.NK > 4ll * p.G * p.NQ;
   kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, row_s, row_d, padded, status, m,
@@ -801,13 +786,20 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
 
 }  // namespace
 
-size_t attn_bwd_workspace(const AttnProblem& p) {
-  if (p.NQ == 0 || p.NK == 0) return 0;
-  return (size_t)p.B * p.H * ((p.NQ + BT - 1) / BT * BT) * 2 * sizeof(uint4);
+bool attn_bwd_fused(const AttnProblem& p, int mode, int num_sms) {
+  if (p.NQ == 0 || p.NK == 0) return false;
+  if (mode) return mode == 1;  // STREAMKL_BWD_FUSED
+  return (long long)p.B * p.HK * ((p.NK + BT - 1) / BT) >= num_sms;
 }
 
-cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
-                            int num_sms, int* status, cudaStream_t st) {
+size_t attn_bwd_workspace(const AttnProblem& p, bool fused) {
+  if (p.NQ == 0 || p.NK == 0) return 0;
+  const size_t rows = (size_t)p.B * p.H * ((p.NQ + BT - 1) / BT * BT);
+  return rows * (2 * sizeof(uint4) + (fused ? p.D * sizeof(float) : 0));
+}
+
+cudaError_t launch_attn_bwd(const AttnProblem& p, bool fused, const AttnBwdIn& in, void* dq, void* dk, void* dv,
+                            void* workspace, int num_sms, int* status, cudaStream_t st) {
   if (p.NQ == 0 || p.NK == 0) {
     auto* q = static_cast<__nv_bfloat16*>(dq);
     auto* k = static_cast<__nv_bfloat16*>(dk);
@@ -822,8 +814,8 @@ cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq,
     }
     return cudaGetLastError();
   }
-  if (p.D == 64) return launch_d<64>(p, in, dq, dk, dv, workspace, num_sms, status, st);
-  return launch_d<128>(p, in, dq, dk, dv, workspace, num_sms, status, st);
+  if (p.D == 64) return launch_d<64>(p, fused, in, dq, dk, dv, workspace, num_sms, status, st);
+  return launch_d<128>(p, fused, in, dq, dk, dv, workspace, num_sms, status, st);
 }
 
 }  // namespace skl

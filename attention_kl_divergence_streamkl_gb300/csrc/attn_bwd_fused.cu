@@ -1,0 +1,484 @@
+// Attention backward, fused: every tile pair is visited once and gives its share
+// of dK, dV and dQ -- five products a tile pair where the separate blocks
+// (attn_bwd.cu, which states the mathematics) need seven, and one exp instead of
+// two.  Its price: a block owns 128 keys, so dQ is added up over the blocks of
+// a head, in fp32 by bulk reductions into an accumulator that lies in L2 while a
+// head is worked on.  The order of those additions is not fixed: the last bits
+// of dQ can differ between runs (dK and dV do not).
+//
+//   S^T = K Q^T - LSE / scale, dP^T = V dO^T - delta   (lanes = keys; a ninth K step adds the rows' values)
+//   P^T = 2^(c S^T) as bf16 pairs over its logits in TMEM:  dV += P^T dO
+//   dS^T = P^T dP^T as bf16 in shared memory [key][query]:   dK += dS^T Q (K-major A)
+//                                                            dQ = dS K    (the same bytes as an MN-major A)
+// TMEM at D = 128: S/P [0,128), dP and then dQ [128,256), dV [256,384), dK [384,512).  dQ takes dP's columns once
+// the warps hold dP, and four warps empty them into registers at once, so that dP of the next tile can follow; they
+// then stage it 32 columns at a time and issue the reductions.  At D = 64 dQ has columns of its own.
+//   warps 0-7    thread = key, group g = warp / 4 takes queries [64g, 64g + 64)
+//   warps 8-11   dQ: TMEM -> registers -> 4 KB staging tile a warp -> bulk reduction
+//   warp 12      TMA producer: K, V once; Q(u) and dO(u) with their rows' values
+//   warp 13      TMEM owner and MMA issuer: dV(u), S(u+1), dQ(u), dK(u), dP(u+1)
+//   warp 14      clears rows past a sequence's lengths in K, V, Q and dO tiles
+// The five products take 2700 cycles a tile pair at D = 128, the reductions (64 KB a tile pair at the 24 bytes a clock
+// that an SM gets from the L2's adders) about as many.
+#include "attn.cuh"
+
+namespace skl {
+namespace {
+
+constexpr int BT = 128;
+constexpr int DS_WARPS = 8, DQ_WARPS = 4;
+constexpr int PRODUCER_WARP = 12, MMA_WARP = 13, PATCH_WARP = 14;
+constexpr int THREADS = 16 * 32;
+constexpr int kRegsWork = 136, kRegsOther = 104;  // 384 * 136 + 128 * 104 = 512 * 128 registers at launch
+constexpr uint32_t kTmemCols = 512;
+
+struct Maps {
+  CUtensorMap q, k, v, go, dk, dv, acc;  // acc: fp32 [B H][padded rows][D], boxes of 32 x 32
+};
+
+template <int D>
+struct Smem {
+  static constexpr bool ALIAS = D == 128;  // dQ in dP's columns
+  static constexpr int Q_SLOTS = 2, O_SLOTS = D == 128 ? 1 : 2;
+  static constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D, kQ = ALIAS ? kP : 256 + 2 * D;
+  static constexpr int TILE = BT * D * 2;
+  static constexpr int OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE;
+  static constexpr int OFF_O = OFF_Q + Q_SLOTS * TILE;
+  static constexpr int OFF_DS = OFF_O + O_SLOTS * TILE;    // [128 keys][128 queries] bf16, two halves
+  static constexpr int OFF_STAGE = OFF_DS + BT * BT * 2;   // 4 KB for each dQ warp
+  static constexpr int STEP = 128 * 16;                    // rows' values of a tile
+  static constexpr int OFF_RS = OFF_STAGE + DQ_WARPS * 4096;
+  static constexpr int OFF_RD = OFF_RS + Q_SLOTS * STEP;
+  static constexpr int OFF_ONES = OFF_RD + O_SLOTS * STEP;
+  static constexpr int OFF_ZERO = OFF_ONES + STEP;
+  static constexpr int OFF_BAR = OFF_ZERO + STEP;
+  // kv_full, kv_patched, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, ds_free, dq_full,
+  // dq_free, g_done, to_patch, patched; TMEM slot, abort flag
+  static constexpr int BAR_SLOT = 8 * 20;
+  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
+};
+static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_bwd_fused_kernel(const AttnProblem p, const uint4* __restrict__ row_s, const uint4* __restrict__ row_d, int padded,
+                          int* status, const __grid_constant__ Maps maps, const int longest_first) {
+  using L = Smem<D>;
+  constexpr int QS = L::Q_SLOTS, OS = L::O_SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // heads in order (the blocks in flight share one key head's query tiles and dQ rows in L2); within a head the first
+  // key tiles, which see the most queries under a causal mask, first.  A small grid: the first key tiles of all heads
+  const int n_kt = (p.NK + BT - 1) / BT, heads = p.B * p.HK;
+  const int bhk = longest_first ? (int)(blockIdx.x % heads) : (int)(blockIdx.x / n_kt);
+  const int b = bhk / p.HK, hk = bhk % p.HK;
+  const int k0 = (longest_first ? (int)(blockIdx.x / heads) : (int)(blockIdx.x % n_kt)) * BT;
+  const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
+  const int off = kl - ql;
+  const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
+  const int n_qt = (k0 < kl && q_begin < ql) ? (ql - q_begin + BT - 1) / BT : 0;
+  const int n = p.G * n_qt;  // tile u: head u / n_qt of the group, query tile u % n_qt
+  const bool ragged_q = n > 0 && ql < p.NQ && (ql & (BT - 1));  // the last query tile has rows past the sequence
+  const bool ragged_k = n > 0 && kl < p.NK && kl - k0 < BT;     // so has this key tile
+
+  const uint32_t bar = sb + L::OFF_BAR;
+  const uint32_t kv_full = bar, kv_patched = bar + 8, q_full = bar + 16, q_empty = bar + 32, o_full = bar + 48,
+                 o_empty = bar + 64, s_full = bar + 80, dp_full = bar + 88, p_full = bar + 96, ds_full = bar + 104,
+                 ds_free = bar + 112, dq_full = bar + 120, dq_free = bar + 128, g_done = bar + 136, to_patch = bar + 144,
+                 patched = bar + 152, slot = bar + L::BAR_SLOT;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_patched, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(q_full + 8 * s, 1);
+      mbar_init(q_empty + 8 * s, 1);
+      mbar_init(o_full + 8 * s, 1);
+      mbar_init(o_empty + 8 * s, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, DS_WARPS);
+    mbar_init(ds_full, DS_WARPS);
+    mbar_init(ds_free, 1);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_free, DQ_WARPS);
+    mbar_init(g_done, 1);
+    mbar_init(to_patch, 1);
+    mbar_init(patched, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 128) {
+    st_shared16(sb + L::OFF_ONES + threadIdx.x * 16, make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u));
+    st_shared16(sb + L::OFF_ZERO + threadIdx.x * 16, make_uint4(0u, 0u, 0u, 0u));
+    fence_async_smem();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+
+  if (warp >= PRODUCER_WARP) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == PRODUCER_WARP) {
+      if (lane == 0 && n > 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
+          tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
+        }
+        int issued_q = 0, issued_o = 0;
+        for (int u = 0; u < n; ++u) {
+          const int sq = u % QS, so = u % OS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+          const long long row = ((long long)b * p.H + hq) * padded + q0;
+          if (u >= QS && !mbar_wait(q_empty + 8 * sq, ((u / QS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(q_full + 8 * sq, L::TILE + L::STEP);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_Q + sq * L::TILE + h * BT * 128, &maps.q, q_full + 8 * sq, h * 64, q0, hq, b);
+          bulk_load(sb + L::OFF_RS + sq * L::STEP, row_s + row, L::STEP, q_full + 8 * sq);
+          issued_q = u + 1;
+          if (u >= OS && !mbar_wait(o_empty + 8 * so, ((u / OS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(o_full + 8 * so, L::TILE + L::STEP);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_O + so * L::TILE + h * BT * 128, &maps.go, o_full + 8 * so, h * 64, q0, hq, b);
+          bulk_load(sb + L::OFF_RD + so * L::STEP, row_d + row, L::STEP, o_full + 8 * so);
+          issued_o = u + 1;
+        }
+        mbar_drain(kv_full, 0, status);
+        for (int u = max(0, issued_q - QS); u < issued_q; ++u) mbar_drain(q_full + 8 * (u % QS), (u / QS) & 1, status);
+        for (int u = max(0, issued_o - OS); u < issued_o; ++u) mbar_drain(o_full + 8 * (u % OS), (u / OS) & 1, status);
+      }
+      __syncwarp();
+    } else if (warp == PATCH_WARP) {
+      auto clear = [&](uint32_t tile, int from) {
+        for (int i = lane; i < (BT - from) * (D / 8); i += 32)
+          st_shared_zero16(sw128<BT>(tile, from + i / (D / 8), i % (D / 8)));
+      };
+      bool ok = true;
+      if (ragged_k) {
+        ok = mbar_wait_warp(kv_full, 0, status, abort_flag);
+        if (ok) {
+          clear(sb + L::OFF_K, kl - k0);
+          clear(sb + L::OFF_V, kl - k0);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_patched);
+        }
+      }
+      // for each head of the group: its last Q tile, then its last dO tile, when the MMA thread has seen them land
+      for (int e = 0; ok && ragged_q && e < 2 * p.G; ++e) {
+        if (!(ok = mbar_wait_warp(to_patch, e & 1, status, abort_flag))) break;
+        const int u = (e / 2 + 1) * n_qt - 1;
+        clear(sb + ((e & 1) ? L::OFF_O + u % OS * L::TILE : L::OFF_Q + u % QS * L::TILE), ql & (BT - 1));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(patched);
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      if (n > 0 && elect_one()) {
+        constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
+        constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
+        constexpr uint32_t id_q = idesc_bf16(BT, D, true, true);
+        const uint64_t kd = sdesc_sw128(sb + L::OFF_K, 0, 1024), vd = sdesc_sw128(sb + L::OFF_V, 0, 1024);
+        const uint64_t kmn = sdesc_sw128(sb + L::OFF_K, BT * 128, 1024);
+        const uint64_t dsk = sdesc_sw128(sb + L::OFF_DS, 0, 1024), dsmn = sdesc_sw128(sb + L::OFF_DS, BT * 128, 1024);
+        const uint64_t ones = sdesc_step(sb + L::OFF_ONES, sb + L::OFF_ZERO);
+        int patches = 0;
+        auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
+          if (!ragged_q || (u + 1) % n_qt) return true;
+          mbar_arrive(to_patch);
+          return mbar_wait(patched, patches++ & 1, status, abort_flag);
+        };
+        auto issue_s = [&](int u) {  // S^T(u)
+          const int s = u % QS;
+          if (!mbar_wait(q_full + 8 * s, (u / QS) & 1, status, abort_flag) || !patch(u)) return false;
+          tc_fence_after();
+          const uint64_t qd = sdesc_sw128(sb + L::OFF_Q + s * L::TILE, 0, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
+            mma_ss(tmem + L::kS, sdesc_add(kd, o), sdesc_add(qd, o), id_s, ks > 0);
+          }
+          mma_ss(tmem + L::kS, ones, sdesc_step(sb + L::OFF_RS + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
+          mma_commit(s_full);
+          return true;
+        };
+        auto issue_dp = [&](int u) {  // dP^T(u)
+          const int s = u % OS;
+          if (!mbar_wait(o_full + 8 * s, (u / OS) & 1, status, abort_flag) || !patch(u)) return false;
+          tc_fence_after();
+          const uint64_t od = sdesc_sw128(sb + L::OFF_O + s * L::TILE, 0, 1024);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
+            mma_ss(tmem + L::kP, sdesc_add(vd, o), sdesc_add(od, o), id_s, ks > 0);
+          }
+          mma_ss(tmem + L::kP, ones, sdesc_step(sb + L::OFF_RD + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
+          mma_commit(dp_full);
+          return true;
+        };
+        bool ok = mbar_wait(kv_full, 0, status, abort_flag) &&
+                  (!ragged_k || mbar_wait(kv_patched, 0, status, abort_flag)) && issue_s(0) && issue_dp(0);
+        for (int u = 0; ok && u < n; ++u) {
+          const int sq = u % QS, so = u % OS;
+          if (!mbar_wait(p_full, u & 1, status, abort_flag)) break;
+          tc_fence_after();
+          const uint64_t omn = sdesc_sw128(sb + L::OFF_O + so * L::TILE, BT * 128, 1024);
+#pragma unroll
+          for (int ks = 0; ks < BT / 16; ++ks)  // dV += P^T dO; a group's 64 queries lie in the first 32 of its columns
+            mma_ts(tmem + L::kV, tmem + L::kS + 64 * (ks >> 2) + 8 * (ks & 3), sdesc_add(omn, ks * 2048), id_g,
+                   u > 0 || ks > 0);
+          mma_commit(o_empty + 8 * so);
+          if (u + 1 < n && !(ok = issue_s(u + 1))) break;
+          if (!mbar_wait(ds_full, u & 1, status, abort_flag)) break;
+          if (!L::ALIAS && u >= 1 && !mbar_wait(dq_free, (u - 1) & 1, status, abort_flag)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < BT / 16; ++ks)  // dQ = dS K
+            mma_ss(tmem + L::kQ, sdesc_add(dsmn, ks * 2048), sdesc_add(kmn, ks * 2048), id_q, ks > 0);
+          mma_commit(dq_full);
+          const uint64_t qmn = sdesc_sw128(sb + L::OFF_Q + sq * L::TILE, BT * 128, 1024);
+#pragma unroll
+          for (int ks = 0; ks < BT / 16; ++ks)  // dK += dS^T Q
+            mma_ss(tmem + L::kK, sdesc_add(dsk, (ks >> 2) * (BT * 128) + (ks & 3) * 32), sdesc_add(qmn, ks * 2048), id_g,
+                   u > 0 || ks > 0);
+          mma_commit(q_empty + 8 * sq);
+          mma_commit(ds_free);
+          if (u + 1 < n) {
+            if (L::ALIAS && !mbar_wait(dq_free, u & 1, status, abort_flag)) break;
+            ok = issue_dp(u + 1);
+          }
+        }
+        mma_commit(g_done);
+        mbar_drain(g_done, 0, status);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= DS_WARPS) {
+    setmaxnreg_inc<kRegsWork>();
+    // ---------------------------------------------------------------- dQ out
+    const int wq = warp & 3;
+    const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16) + L::kQ;
+    const uint32_t stage = sb + L::OFF_STAGE + (warp - DS_WARPS) * 4096;
+    for (int u = 0; u < n; ++u) {
+      const int hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+      const bool ok = mbar_wait_warp(dq_full, u & 1, status, abort_flag);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t a[D / 32][32];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) tmem_ld32(tq + 32 * c, a[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) reg_fence32(a[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dq_free);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        if (lane == 0) bulk_wait_read();  // the staging tile's last reduction has read it
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          st_shared16(stage + lane * 128 + ((i ^ (lane & 7)) << 4),
+                      make_uint4(a[c][4 * i], a[c][4 * i + 1], a[c][4 * i + 2], a[c][4 * i + 3]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          reduce_add_3d(&maps.acc, stage, 32 * c, q0 + 32 * wq, b * p.H + hq);
+          bulk_commit();
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  } else {
+    setmaxnreg_inc<kRegsWork>();
+    // ---------------------------------------------------------------- P and dS
+    const int grp = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const int key = k0 + r;
+    const float2 cc = make_float2(p.c, p.c);
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t ts = tmem + lanes + L::kS + 64 * grp, tp = tmem + lanes + L::kP + 64 * grp;
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      const int q0 = q_begin + (u % n_qt) * BT + 64 * grp;  // first query of this warp's columns
+      ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t a[2][32];
+      tmem_ld32(ts, a[0]);
+      tmem_ld32(ts + 32, a[1]);
+      tmem_ld_wait();
+      reg_fence32(a[0]);
+      reg_fence32(a[1]);
+      const int hidden = key >= kl ? 64 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
+      const bool masked = __any_sync(0xffffffffu, hidden > 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[16];
+        // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 x = fmul2(make_float2(__uint_as_float(a[h][i]), __uint_as_float(a[h][i + 1])), cc);
+          a[h][i] = __float_as_uint(ex2(x.x));
+          a[h][i + 1] = __float_as_uint(ex2(x.y));
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * h + i < hidden) a[h][i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(a[h][2 * i]), __uint_as_float(a[h][2 * i + 1]));
+        tmem_st16(ts + 16 * h, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag) &&
+           (u == 0 || mbar_wait_warp(ds_free, (u - 1) & 1, status, abort_flag));  // dS of the last tile has been read
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[32];
+        tmem_ld32(tp + 32 * h, d);
+        tmem_ld_wait();
+        reg_fence32(d);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 8 * v + 2 * e;
+            const float2 x = fmul2(make_float2(__uint_as_float(a[h][i]), __uint_as_float(a[h][i + 1])),
+                                   make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+            w[e] = pack_bf16(x.x, x.y);
+          }
+          st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * 8 + h * 4 + v), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
+      tc_fence_before();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    // ---- dV through the first Q slot, dK through the second: every product that read them is done
+    bool got = ok;
+    if (n > 0 && ok) {
+      got = mbar_wait_warp(g_done, 0, status, abort_flag);
+      __syncwarp();
+    }
+    if (got) {
+      tc_fence_after();
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {  // group g takes half of the columns
+          const int col = grp * (D / 2) + 32 * c;
+          uint32_t g[32];
+          if (n > 0) {
+            tmem_ld32(tmem + lanes + (which ? L::kK : L::kV) + col, g);
+            tmem_ld_wait();
+            reg_fence32(g);
+          }
+          if (n == 0 || key >= kl) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) g[i] = 0u;
+          }
+          stage_row32(sb + L::OFF_Q + which * L::TILE, r, col, g, which ? p.scale : 1.f);
+        }
+      }
+      fence_async_smem();
+    }
+    // every warp comes here; one that gave up makes none of them store
+    if (!named_bar_any(1, DS_WARPS * 32, !got) && threadIdx.x == 0) {
+      store_tile<D>(&maps.dv, sb + L::OFF_Q, k0, hk, b);
+      store_tile<D>(&maps.dk, sb + L::OFF_Q + L::TILE, k0, hk, b);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// dQ = scale acc, as bf16 with q's strides; a thread takes 8 columns.
+template <int D>
+__global__ void __launch_bounds__(256) attn_dq_out_kernel(const AttnProblem p, const float* __restrict__ acc, int padded,
+                                                          __nv_bfloat16* __restrict__ dq) {
+  constexpr int LANES = D / 8;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long row = i / LANES;
+  if (row >= p.rows) return;
+  const int lane = (int)(i % LANES);
+  const long long bh = row / p.NQ, n = row % p.NQ;
+  const float4* src = reinterpret_cast<const float4*>(acc + (bh * padded + n) * D + lane * 8);
+  const float4 x = src[0], y = src[1];
+  const float f = p.scale;
+  *reinterpret_cast<uint4*>(dq + bh / p.H * p.qs_b + bh % p.H * p.qs_h + n * p.qs_n + lane * 8) =
+      make_uint4(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f), pack_bf16(y.x * f, y.y * f),
+                 pack_bf16(y.z * f, y.w * f));
+}
+
+template <int D>
+cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, const uint4* row_s,
+                     const uint4* row_d, float* acc, int padded, int longest_first, int* status, cudaStream_t st) {
+  Maps m;
+  if (!encode_tile_map(&m.q, in.q, D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, BT) ||
+      !encode_tile_map(&m.k, in.k, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
+      !encode_tile_map(&m.v, in.v, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
+      !encode_tile_map(&m.go, in.go, D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, BT) ||
+      !encode_tile_map(&m.dk, dk, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
+      !encode_tile_map(&m.dv, dv, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
+      !encode_rows_f32_map(&m.acc, acc, D, padded, p.B * p.H, 32, 32))
+    return cudaErrorInvalidValue;
+  constexpr int smem = Smem<D>::BYTES > kOneBlockPerSmSmem ? Smem<D>::BYTES : kOneBlockPerSmSmem;
+  auto kern = attn_bwd_fused_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
+  kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, row_s, row_d, padded, status, m, longest_first);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  attn_dq_out_kernel<D><<<(unsigned)((p.rows * (D / 8) + 255) / 256), 256, 0, st>>>(p, acc, padded,
+                                                                                    static_cast<__nv_bfloat16*>(dq));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv,
+                                  const void* row_s, const void* row_d, float* acc, int padded, int longest_first,
+                                  int* status, cudaStream_t st) {
+  auto *rs = static_cast<const uint4*>(row_s), *rd = static_cast<const uint4*>(row_d);
+  if (p.D == 64) return launch_d<64>(p, in, dq, dk, dv, rs, rd, acc, padded, longest_first, status, st);
+  return launch_d<128>(p, in, dq, dk, dv, rs, rd, acc, padded, longest_first, status, st);
+}
+
+}  // namespace skl

@@ -37,7 +37,7 @@ constexpr int BM = 128, BN = 128;
 constexpr int SOFTMAX_WARPS = 8;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, PATCH_WARP = 10;
 constexpr int THREADS = 12 * 32;
-constexpr int kRegsSoftmax = 224, kRegsOther = 56;  // 256 * 224 + 128 * 56 = 384 * 168 at launch
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // 256 * 200 + 128 * 104 = 384 * 168 at launch
 constexpr int SLOTS = 5;                            // ring of K and V tiles
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSumLimit = 18446744073709551616.0f;  // 2^64

@@ -31,7 +31,8 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, in
                      long long sb, int box_rows, int box_heads = 1);
 // A 3-D TMA map {d, row, bh} over an fp32 [BH][rows][D] accumulator, a {D, box_rows, 1} box, no swizzle
 // (for bulk reductions into it).
-bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows);
+// With box_cols (32: 128-byte rows) the box is {box_cols, box_rows, 1} with the 128-byte swizzle.
+bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows, int box_cols = 0);
 // The maps of Q1/Q2 and K1/K2 of a problem.
 inline bool encode_q_map(CUtensorMap* map, const void* base, const Problem& p, int box_rows) {
   return encode_tile_map(map, base, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, box_rows);
@@ -117,9 +118,14 @@ struct AttnBwdIn {
   const void *q, *k, *v, *o, *go;  // go = dO, with o's strides
   const float *lse, *dlse;         // dlse may be null
 };
-size_t attn_bwd_workspace(const AttnProblem& p);
-cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
-                            int num_sms, int* status, cudaStream_t st);
+// `fused`: one visit of each tile pair, dQ added up in an fp32 accumulator; else separate dQ and dK/dV blocks.
+bool attn_bwd_fused(const AttnProblem& p, int mode, int num_sms);  // mode: streamkl_bwd_mode
+size_t attn_bwd_workspace(const AttnProblem& p, bool fused);
+cudaError_t launch_attn_bwd(const AttnProblem& p, bool fused, const AttnBwdIn& in, void* dq, void* dk, void* dv,
+                            void* workspace, int num_sms, int* status, cudaStream_t st);
+cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv,
+                                  const void* row_s, const void* row_d, float* acc, int padded, int longest_first,
+                                  int* status, cudaStream_t st);
 
 // ---- log probabilities of given tokens ---------------------------------------------
 constexpr int kTypeBf16 = 0, kTypeFp16 = 1, kTypeFp32 = 2;  // streamkl_dtype

@@ -343,14 +343,23 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
  * o, lse: the forward's; go = dLoss/dO with o's strides; dlse = dLoss/dLSE, fp32
  * [B, H, N_Q], or NULL.  dq, dk, dv: bf16 with the strides of q, k, v (which must
  * not make rows overlap).  Lengths and causal as in the forward; gradients of
- * what lies past a sequence are 0, and go, dlse are not used there.  Every output
- * is written by one block: results are the same on every run.
- * Workspace: 32 bytes per query row, N_Q rounded up to 128.
+ * what lies past a sequence are 0, and go, dlse are not used there.
+ * bwd_mode:
+ *   STREAMKL_BWD_SEPARATE  dQ blocks and dK/dV blocks in one launch, every output
+ *                          written by one block: the same bits on every run.
+ *                          Workspace: 32 bytes per query row, N_Q rounded up to 128.
+ *   STREAMKL_BWD_FUSED     one visit of each tile pair; dQ is added up in fp32 by
+ *                          reductions in L2, in no fixed order, so its last bits can
+ *                          differ between runs.  Workspace: 4 D bytes more per row.
+ *   STREAMKL_BWD_AUTO      as streamkl_attn_bwd_select decides (a pure host rule; 0
+ *                          for an invalid shape): fused where the key tiles alone
+ *                          fill the SMs.
  */
-streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, size_t* bytes);
+int streamkl_attn_bwd_select(streamkl_attn_shape s, int num_sms);
+streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, int bwd_mode, size_t* bytes);
 streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
                                   const void* go, const float* dlse, streamkl_attn_shape s, void* dq, void* dk,
-                                  void* dv, void* workspace, size_t workspace_bytes, void* stream);
+                                  void* dv, int bwd_mode, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Log probabilities of given tokens, with entropy and top alternatives: the

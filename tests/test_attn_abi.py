@@ -93,10 +93,10 @@ def test_binding_refuses_types():
         skl.attn_fwd(q, q, q)
 
 
-def bwd_args(s, drop=None, off=None, ws=1 << 30):
-    names = ["q", "k", "v", "o", "lse", "go", "dlse", "s", "dq", "dk", "dv", "ws"]
+def bwd_args(s, drop=None, off=None, ws=1 << 30, mode=K.BWD_SEPARATE):
+    names = ["q", "k", "v", "o", "lse", "go", "dlse", "s", "dq", "dk", "dv", "mode", "ws"]
     a = {n: ptr(64 * i) for i, n in enumerate(names)}
-    a["s"] = s
+    a["s"], a["mode"] = s, mode
     if drop:
         a[drop] = None
     if off:
@@ -108,7 +108,8 @@ def bwd_args(s, drop=None, off=None, ws=1 << 30):
 def test_bwd_refuses_shapes(lib, change, code):
     s = K.make_attn_shape(**{**OK, **change})
     assert lib.streamkl_attn_bwd(*bwd_args(s)) == code
-    assert lib.streamkl_attn_bwd_workspace(s, ctypes.byref(ctypes.c_size_t())) == code
+    assert lib.streamkl_attn_bwd_workspace(s, K.BWD_SEPARATE, ctypes.byref(ctypes.c_size_t())) == code
+    assert lib.streamkl_attn_bwd_select(s, 152) == 0
 
 
 def test_bwd_refuses_pointers_and_small_workspaces(lib):
@@ -118,8 +119,12 @@ def test_bwd_refuses_pointers_and_small_workspaces(lib):
         assert lib.streamkl_attn_bwd(*bwd_args(s, off=name)) == K.ERR_INVALID, name
     assert lib.streamkl_attn_bwd(*bwd_args(s, off="dlse")) == K.ERR_INVALID
     n = ctypes.c_size_t()
-    assert lib.streamkl_attn_bwd_workspace(s, ctypes.byref(n)) == K.OK
-    assert n.value == 2 * 8 * 128 * 32
+    for mode, size in ((K.BWD_FUSED, 32 + 4 * 64), (K.BWD_SEPARATE, 32)):
+        assert lib.streamkl_attn_bwd_workspace(s, mode, ctypes.byref(n)) == K.OK
+        assert n.value == 2 * 8 * 128 * size
+    for mode in (-1, K.BWD_DQ_ONLY, K.BWD_DK_ONLY, 5):
+        assert lib.streamkl_attn_bwd_workspace(s, mode, ctypes.byref(ctypes.c_size_t())) == K.ERR_INVALID
+        assert lib.streamkl_attn_bwd(*bwd_args(s, mode=mode)) == K.ERR_INVALID
     assert lib.streamkl_attn_bwd(*bwd_args(s, ws=n.value - 1)) == K.ERR_WORKSPACE
     assert lib.streamkl_attn_bwd(*bwd_args(s, drop="ws")) == K.ERR_WORKSPACE
     assert lib.streamkl_attn_bwd(*bwd_args(s, off="ws")) == K.ERR_WORKSPACE
@@ -132,3 +137,9 @@ def test_bwd_binding_refuses():
         skl.attn_bwd(q, q, q, q, lse, q.float())
     with pytest.raises(ValueError):
         skl.attn_bwd(q, q, q, q[:, :, :2], lse, q)
+
+
+def test_bwd_select():
+    """Fused where the key tiles fill the SMs."""
+    assert skl.attn_bwd_select(2, 32, 8, 4096, 4096, 128, 152, True) == K.BWD_FUSED
+    assert skl.attn_bwd_select(1, 8, 8, 1024, 1024, 128, 152) == K.BWD_SEPARATE

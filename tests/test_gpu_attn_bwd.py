@@ -20,13 +20,19 @@ def lens(*n):
     return torch.tensor(n, dtype=torch.int32, device="cuda")
 
 
+MODES = {"separate": skl.BWD_SEPARATE, "fused": skl.BWD_FUSED}
+
+
 def check(q, k, v, do, dlse=None, **kw):
+    """Both paths; returns the separate one's."""
     o, lse = skl.attn_fwd(q, k, v, **kw)
-    got = skl.attn_bwd(q, k, v, o, lse, do, dlse, **kw)
     want, bounds = A.backward(q, k, v, do, dlse, **kw)
-    for name, g, w, b in zip(("dq", "dk", "dv"), got, want, bounds):
-        A.within(g, w, b, name)
-    return got
+    out = {}
+    for mode in MODES:
+        out[mode] = skl.attn_bwd(q, k, v, o, lse, do, dlse, **kw, bwd_mode=MODES[mode])
+        for name, g, w, b in zip(("dq", "dk", "dv"), out[mode], want, bounds):
+            A.within(g, w, b, f"{mode} {name}")
+    return out["separate"]
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -58,14 +64,15 @@ def test_padded_batch_whatever_lies_in_the_padding(NQ, NK, G, causal, D):
         v[b, :, past_k:] = float("inf")
     clean = torch.where(dlse.isnan(), torch.zeros_like(dlse), dlse)
     o, lse = skl.attn_fwd(q, k, v, causal=causal, q_lens=ql, k_lens=kl)
-    got = skl.attn_bwd(q, k, v, o, lse, do, dlse, causal=causal, q_lens=ql, k_lens=kl)
     want, bounds = A.backward(q, k, v, do, clean, causal=causal, q_lens=ql, k_lens=kl)
-    for name, g, w, b in zip(("dq", "dk", "dv"), got, want, bounds):
-        A.within(g, w, b, name)
-    for b in range(6):
-        past_q, past_k = max(min(int(ql[b]), NQ), 0), max(min(int(kl[b]), NK), 0)
-        assert bool((got[0][b, :, past_q:] == 0).all())
-        assert bool((got[1][b, :, past_k:] == 0).all()) and bool((got[2][b, :, past_k:] == 0).all())
+    for mode in MODES:
+        got = skl.attn_bwd(q, k, v, o, lse, do, dlse, causal=causal, q_lens=ql, k_lens=kl, bwd_mode=MODES[mode])
+        for name, g, w, b in zip(("dq", "dk", "dv"), got, want, bounds):
+            A.within(g, w, b, f"{mode} {name}")
+        for b in range(6):
+            past_q, past_k = max(min(int(ql[b]), NQ), 0), max(min(int(kl[b]), NK), 0)
+            assert bool((got[0][b, :, past_q:] == 0).all())
+            assert bool((got[1][b, :, past_k:] == 0).all()) and bool((got[2][b, :, past_k:] == 0).all())
 
 
 def test_gradient_of_the_log_sum_exp():
@@ -108,7 +115,7 @@ def test_views():
 def test_runs_are_bit_identical_alone_together_and_replayed():
     q, k, v, do = A.tensors(1, 8, 2, 700, 900, 128, 15)
     o, lse = skl.attn_fwd(q, k, v, causal=True)
-    call = lambda: skl.attn_bwd(q, k, v, o, lse, do, causal=True)  # noqa: E731
+    call = lambda: skl.attn_bwd(q, k, v, o, lse, do, causal=True, bwd_mode=skl.BWD_SEPARATE)  # noqa: E731
     want = call()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -127,6 +134,33 @@ def test_runs_are_bit_identical_alone_together_and_replayed():
     for got in (other, again, first, second):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_fused_runs_together_and_replayed():
+    """The fused path on two streams at once and in two graphs, each with its own accumulator: dk and dv keep their bits,
+    dq stays within its bound whatever the order of its additions."""
+    q, k, v, do = A.tensors(1, 8, 2, 700, 900, 128, 18)
+    o, lse = skl.attn_fwd(q, k, v, causal=True)
+    call = lambda: skl.attn_bwd(q, k, v, o, lse, do, causal=True, bwd_mode=skl.BWD_FUSED)  # noqa: E731
+    ref = call()
+    want, bounds = A.backward(q, k, v, do, causal=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = call()
+    again = call()
+    torch.cuda.current_stream().wait_stream(side)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        first = call()
+    with torch.cuda.graph(g2):
+        second = call()
+    g1.replay()
+    g2.replay()
+    g1.replay()
+    for got in (ref, other, again, first, second):
+        A.within(got[0], want[0], bounds[0], "dq")
+        assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
 
 
 def test_autograd_against_differences():
@@ -155,7 +189,7 @@ def test_autograd_against_differences():
 def test_autograd_outputs_alone():
     q, k, v, do = A.tensors(1, 2, 2, 40, 50, 64, 17)
     leaves = [t.clone().requires_grad_() for t in (q, k, v)]
-    skl.attention(*leaves).backward(do)
+    skl.attention(*leaves, bwd_mode=skl.BWD_SEPARATE).backward(do)
     for t, w in zip(leaves, check(q, k, v, do)):
         assert torch.equal(t.grad, w)
     for t in leaves:
