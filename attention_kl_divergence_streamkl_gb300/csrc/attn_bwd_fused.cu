@@ -13,11 +13,12 @@
 // TMEM at D = 128: S/P [0,128), dP and then dQ [128,256), dV [256,384), dK [384,512).  dQ takes dP's columns once
 // the warps hold dP, and four warps empty them into registers at once, so that dP of the next tile can follow; they
 // then stage it 32 columns at a time and issue the reductions.  At D = 64 dQ has columns of its own.
-//   warps 0-7    thread = key, group g = warp / 4 takes queries [64g, 64g + 64)
-//   warps 8-11   dQ: TMEM -> registers -> 4 KB staging tile a warp -> bulk reduction
-//   warp 12      TMA producer: K, V once; Q(u) and dO(u) with their rows' values
-//   warp 13      TMEM owner and MMA issuer: dV(u), S(u+1), dQ(u), dK(u), dP(u+1)
-//   warp 14      clears rows past a sequence's lengths in K, V, Q and dO tiles
+//   dS warps     thread = key; 8 of them take 64 queries each (D = 128), or 16 take 32 (D = 64, where their
+//                latency is what bounds a tile pair and registers allow it)
+//   4 dQ warps   TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
+//   then         TMA producer: K, V once; Q(u) and dO(u) with their rows' values
+//                TMEM owner and MMA issuer: dV(u), S(u+1), dQ(u), dK(u), dP(u+1)
+//                a warp that clears rows past a sequence's lengths in K, V, Q and dO tiles
 // The five products take 2700 cycles a tile pair at D = 128, the reductions (64 KB a tile pair at the 24 bytes a clock
 // that an SM gets from the L2's adders) about as many.
 #include "attn.cuh"
@@ -26,28 +27,40 @@ namespace skl {
 namespace {
 
 constexpr int BT = 128;
-constexpr int DS_WARPS = 8, DQ_WARPS = 4;
-constexpr int PRODUCER_WARP = 12, MMA_WARP = 13, PATCH_WARP = 14;
-constexpr int THREADS = 16 * 32;
-constexpr int kRegsWork = 136, kRegsOther = 104;  // 384 * 136 + 128 * 104 = 512 * 128 registers at launch
+constexpr int DQ_WARPS = 4;
 constexpr uint32_t kTmemCols = 512;
 
 struct Maps {
-  CUtensorMap q, k, v, go, dk, dv, acc;  // acc: fp32 [B H][padded rows][D], boxes of 32 x 32
+  CUtensorMap q, k, v, go, dk, dv, acc;  // acc: fp32 [B H][padded rows][D], boxes of a staging chunk
+};
+
+// Warps, in warpgroups, and their registers (the sums are what the launch has).
+template <int D>
+struct Cfg {
+  static constexpr int DS_WARPS = D == 128 ? 8 : 16;
+  static constexpr int COLS = 128 * 4 / DS_WARPS;  // queries of a dS thread
+  static constexpr int PRODUCER_WARP = DS_WARPS + DQ_WARPS, MMA_WARP = PRODUCER_WARP + 1, PATCH_WARP = PRODUCER_WARP + 2;
+  static constexpr int THREADS = 32 * (PRODUCER_WARP + 4);
+  // D = 128: 256 * 136 + 128 * 136 + 128 * 104 = 512 * 128;  D = 64: 512 * 80 + 128 * 96 + 128 * 64 = 768 * 80
+  static constexpr int kRegsDs = D == 128 ? 136 : 80, kRegsDq = D == 128 ? 136 : 96, kRegsOther = D == 128 ? 104 : 64;
 };
 
 template <int D>
 struct Smem {
   static constexpr bool ALIAS = D == 128;  // dQ in dP's columns
+  // a dQ warp's staging ring: chunks of 32 rows x CHUNK columns.  What is on its way to L2 bounds the reductions' rate
+  // (24 bytes a clock with a latency of 1000 to 1500): 24 KB is what D = 128 leaves, in chunks of 2 KB
+  static constexpr int CHUNK = D == 128 ? 16 : 32, RING = D == 128 ? 3 : 4;
+  static constexpr int CHUNK_BYTES = 32 * CHUNK * 4;
   static constexpr int Q_SLOTS = 2, O_SLOTS = D == 128 ? 1 : 2;
   static constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D, kQ = ALIAS ? kP : 256 + 2 * D;
   static constexpr int TILE = BT * D * 2;
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE;
   static constexpr int OFF_O = OFF_Q + Q_SLOTS * TILE;
   static constexpr int OFF_DS = OFF_O + O_SLOTS * TILE;    // [128 keys][128 queries] bf16, two halves
-  static constexpr int OFF_STAGE = OFF_DS + BT * BT * 2;   // 4 KB for each dQ warp
+  static constexpr int OFF_STAGE = OFF_DS + BT * BT * 2;   // the dQ warps' rings
   static constexpr int STEP = 128 * 16;                    // rows' values of a tile
-  static constexpr int OFF_RS = OFF_STAGE + DQ_WARPS * 4096;
+  static constexpr int OFF_RS = OFF_STAGE + DQ_WARPS * RING * CHUNK_BYTES;
   static constexpr int OFF_RD = OFF_RS + Q_SLOTS * STEP;
   static constexpr int OFF_ONES = OFF_RD + O_SLOTS * STEP;
   static constexpr int OFF_ZERO = OFF_ONES + STEP;
@@ -55,7 +68,7 @@ struct Smem {
   // kv_full, kv_patched, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, ds_free, dq_full,
   // dq_free, g_done, to_patch, patched; TMEM slot, abort flag
   static constexpr int BAR_SLOT = 8 * 20;
-  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
+  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16;
 };
 static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
 
@@ -67,13 +80,14 @@ __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t s
 }
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     attn_bwd_fused_kernel(const AttnProblem p, const uint4* __restrict__ row_s, const uint4* __restrict__ row_d, int padded,
                           int* status, const __grid_constant__ Maps maps, const int longest_first) {
   using L = Smem<D>;
-  constexpr int QS = L::Q_SLOTS, OS = L::O_SLOTS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
+  using C = Cfg<D>;
+  constexpr int QS = L::Q_SLOTS, OS = L::O_SLOTS, DS_WARPS = C::DS_WARPS, PRODUCER_WARP = C::PRODUCER_WARP,
+                MMA_WARP = C::MMA_WARP, PATCH_WARP = C::PATCH_WARP;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles' alignment; nothing lies before it
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // heads in order (the blocks in flight share one key head's query tiles and dQ rows in L2); within a head the first
@@ -133,7 +147,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
 
   if (warp >= PRODUCER_WARP) {
-    setmaxnreg_dec<kRegsOther>();
+    setmaxnreg_dec<C::kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (lane == 0 && n > 0) {
         mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
@@ -243,9 +257,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
           const uint64_t omn = sdesc_sw128(sb + L::OFF_O + so * L::TILE, BT * 128, 1024);
 #pragma unroll
-          for (int ks = 0; ks < BT / 16; ++ks)  // dV += P^T dO; a group's 64 queries lie in the first 32 of its columns
-            mma_ts(tmem + L::kV, tmem + L::kS + 64 * (ks >> 2) + 8 * (ks & 3), sdesc_add(omn, ks * 2048), id_g,
-                   u > 0 || ks > 0);
+          for (int ks = 0; ks < BT / 16; ++ks)  // dV += P^T dO; a group's pairs lie in the first half of its columns
+            mma_ts(tmem + L::kV, tmem + L::kS + C::COLS * (ks * 16 / C::COLS) + 8 * (ks % (C::COLS / 16)),
+                   sdesc_add(omn, ks * 2048), id_g, u > 0 || ks > 0);
           mma_commit(o_empty + 8 * so);
           if (u + 1 < n && !(ok = issue_s(u + 1))) break;
           if (!mbar_wait(ds_full, u & 1, status, abort_flag)) break;
@@ -273,11 +287,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     }
   } else if (warp >= DS_WARPS) {
-    setmaxnreg_inc<kRegsWork>();
+    setmaxnreg_inc<C::kRegsDq>();
     // ---------------------------------------------------------------- dQ out
     const int wq = warp & 3;
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16) + L::kQ;
-    const uint32_t stage = sb + L::OFF_STAGE + (warp - DS_WARPS) * 4096;
+    const uint32_t ring = sb + L::OFF_STAGE + (warp - DS_WARPS) * L::RING * L::CHUNK_BYTES;
+    constexpr int LINES = L::CHUNK / 4;  // 16-byte lines of a chunk's row
+    int at = 0;                          // ring position
     for (int u = 0; u < n; ++u) {
       const int hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
       const bool ok = mbar_wait_warp(dq_full, u & 1, status, abort_flag);
@@ -294,17 +310,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(dq_free);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        if (lane == 0) bulk_wait_read();  // the staging tile's last reduction has read it
+      for (int c = 0; c < D / L::CHUNK; ++c) {
+        // the reduction that last used this chunk has read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(L::RING - 1) : "memory");
         __syncwarp();
+        const uint32_t stage = ring + at * L::CHUNK_BYTES;
+        at = at + 1 == L::RING ? 0 : at + 1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          st_shared16(stage + lane * 128 + ((i ^ (lane & 7)) << 4),
-                      make_uint4(a[c][4 * i], a[c][4 * i + 1], a[c][4 * i + 2], a[c][4 * i + 3]));
+        for (int i = 0; i < LINES; ++i) {
+          const uint32_t* v = &a[c * L::CHUNK / 32][c * L::CHUNK % 32 + 4 * i];
+          // the swizzle of 128-byte rows, or of 64-byte rows
+          const int line = L::CHUNK == 32 ? i ^ (lane & 7) : i ^ ((lane >> 1) & 3);
+          st_shared16(stage + lane * (L::CHUNK * 4) + (line << 4), make_uint4(v[0], v[1], v[2], v[3]));
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          reduce_add_3d(&maps.acc, stage, 32 * c, q0 + 32 * wq, b * p.H + hq);
+          reduce_add_3d(&maps.acc, stage, L::CHUNK * c, q0 + 32 * wq, b * p.H + hq);
           bulk_commit();
         }
       }
@@ -312,31 +334,32 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   } else {
-    setmaxnreg_inc<kRegsWork>();
+    setmaxnreg_inc<C::kRegsDs>();
     // ---------------------------------------------------------------- P and dS
+    constexpr int COLS = C::COLS, HALVES = COLS / 32;
     const int grp = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
     const int key = k0 + r;
     const float2 cc = make_float2(p.c, p.c);
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t ts = tmem + lanes + L::kS + 64 * grp, tp = tmem + lanes + L::kP + 64 * grp;
+    const uint32_t ts = tmem + lanes + L::kS + COLS * grp, tp = tmem + lanes + L::kP + COLS * grp;
     bool ok = true;
     for (int u = 0; u < n; ++u) {
-      const int q0 = q_begin + (u % n_qt) * BT + 64 * grp;  // first query of this warp's columns
+      const int q0 = q_begin + (u % n_qt) * BT + COLS * grp;  // first query of this warp's columns
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
-      uint32_t a[2][32];
-      tmem_ld32(ts, a[0]);
-      tmem_ld32(ts + 32, a[1]);
+      uint32_t a[HALVES][32];
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) tmem_ld32(ts + 32 * h, a[h]);
       tmem_ld_wait();
-      reg_fence32(a[0]);
-      reg_fence32(a[1]);
-      const int hidden = key >= kl ? 64 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) reg_fence32(a[h]);
+      const int hidden = key >= kl ? COLS : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
       const bool masked = __any_sync(0xffffffffu, hidden > 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < HALVES; ++h) {
         uint32_t pk[16];
         // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
 #pragma unroll
@@ -364,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < HALVES; ++h) {
         uint32_t d[32];
         tmem_ld32(tp + 32 * h, d);
         tmem_ld_wait();
@@ -379,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                    make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
             w[e] = pack_bf16(x.x, x.y);
           }
-          st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * 8 + h * 4 + v), make_uint4(w[0], w[1], w[2], w[3]));
+          st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * (COLS / 8) + h * 4 + v), make_uint4(w[0], w[1], w[2], w[3]));
         }
       }
       tc_fence_before();
@@ -395,23 +418,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (got) {
       tc_fence_after();
+      // D = 128: each of two groups takes half of the columns of both.  D = 64: groups 0, 1 take dV, 2, 3 take dK
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {  // group g takes half of the columns
-          const int col = grp * (D / 2) + 32 * c;
-          uint32_t g[32];
-          if (n > 0) {
-            tmem_ld32(tmem + lanes + (which ? L::kK : L::kV) + col, g);
-            tmem_ld_wait();
-            reg_fence32(g);
-          }
-          if (n == 0 || key >= kl) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) g[i] = 0u;
-          }
-          stage_row32(sb + L::OFF_Q + which * L::TILE, r, col, g, which ? p.scale : 1.f);
+      for (int i = 0; i < (D == 128 ? 4 : 1); ++i) {
+        const int which = D == 128 ? i / 2 : grp / 2, col = D == 128 ? grp * 64 + (i & 1) * 32 : (grp & 1) * 32;
+        uint32_t g[32];
+        if (n > 0) {
+          tmem_ld32(tmem + lanes + (which ? L::kK : L::kV) + col, g);
+          tmem_ld_wait();
+          reg_fence32(g);
         }
+        if (n == 0 || key >= kl) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) g[k] = 0u;
+        }
+        stage_row32(sb + L::OFF_Q + which * L::TILE, r, col, g, which ? p.scale : 1.f);
       }
       fence_async_smem();
     }
@@ -457,14 +478,14 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
       !encode_tile_map(&m.go, in.go, D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, BT) ||
       !encode_tile_map(&m.dk, dk, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
       !encode_tile_map(&m.dv, dv, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
-      !encode_rows_f32_map(&m.acc, acc, D, padded, p.B * p.H, 32, 32))
+      !encode_rows_f32_map(&m.acc, acc, D, padded, p.B * p.H, 32, Smem<D>::CHUNK))
     return cudaErrorInvalidValue;
   constexpr int smem = Smem<D>::BYTES > kOneBlockPerSmSmem ? Smem<D>::BYTES : kOneBlockPerSmSmem;
   auto kern = attn_bwd_fused_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
-  kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, row_s, row_d, padded, status, m, longest_first);
+  kern<<<(unsigned)blocks, Cfg<D>::THREADS, smem, st>>>(p, row_s, row_d, padded, status, m, longest_first);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   attn_dq_out_kernel<D><<<(unsigned)((p.rows * (D / 8) + 255) / 256), 256, 0, st>>>(p, acc, padded,
                                                                                     static_cast<__nv_bfloat16*>(dq));
