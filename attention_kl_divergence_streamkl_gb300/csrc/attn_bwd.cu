@@ -191,7 +191,24 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
                  s_full = bar + 72, dp_full = bar + 80, p_full = bar + 88, ds_full = bar + 96, g_done = bar + 104,
                  to_patch = bar + 112, patched = bar + 120, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
-  if (threadIdx.x == 0) {
+  // the producer sets the barriers up and issues the first loads while the others get TMEM
+  auto load_q = [&](int u) {
+    const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+    mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+      tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &maps.q, q_full + 8 * s, h * 64, q0, hq, b);
+    bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + ((long long)b * p.H + hq) * padded + q0, L::STEP, q_full + 8 * s);
+  };
+  auto load_o = [&](int u) {
+    const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+    mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+      tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &maps.go, o_full + 8 * s, h * 64, q0, hq, b);
+    bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + ((long long)b * p.H + hq) * padded + q0, L::STEP, o_full + 8 * s);
+  };
+  if (warp == PRODUCER_WARP && lane == 0) {
     mbar_init(kv_full, 1);
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(q_full + 8 * s, 1);
@@ -208,6 +225,15 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     mbar_init(patched, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (n > 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
+      load_q(0);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
+      load_o(0);
+    }
   }
   if (threadIdx.x < 128) {
     st_shared16(sb + L::OFF_ONES + threadIdx.x * 16, make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u));
@@ -227,29 +253,14 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (lane == 0 && n > 0) {
-        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
-          tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
-        }
-        int issued_q = 0, issued_o = 0;
-        for (int u = 0; u < n; ++u) {
-          const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
-          const long long row = ((long long)b * p.H + hq) * padded + q0;
+        int issued_q = 1, issued_o = 1;
+        for (int u = 1; u < n; ++u) {
+          const int s = u % SLOTS;
           if (u >= SLOTS && !mbar_wait(q_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &maps.q, q_full + 8 * s, h * 64, q0, hq, b);
-          bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + row, L::STEP, q_full + 8 * s);
+          load_q(u);
           issued_q = u + 1;
           if (u >= SLOTS && !mbar_wait(o_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &maps.go, o_full + 8 * s, h * 64, q0, hq, b);
-          bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + row, L::STEP, o_full + 8 * s);
+          load_o(u);
           issued_o = u + 1;
         }
         mbar_drain(kv_full, 0, status);
@@ -517,7 +528,22 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
                  s_full = bar + 88, s_free = bar + 96, ds_full = bar + 104, ds_free = bar + 120, g_done = bar + 136,
                  to_patch = bar + 144, patched = bar + 152, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
-  if (threadIdx.x == 0) {
+  // the producer sets the barriers up and issues the first loads while the others get TMEM
+  auto load_k = [&](int j) {
+    const int s = j % K_SLOTS;
+    mbar_arrive_expect_tx(k_full + 8 * s, L::TILE);
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d)
+      tma_load_4d(sb + L::OFF_K + s * L::TILE + d * BT * 128, &maps.k, k_full + 8 * s, d * 64, j * BT, hk, b);
+  };
+  auto load_v = [&](int j) {
+    const int s = j % V_SLOTS;
+    mbar_arrive_expect_tx(v_full + 8 * s, L::TILE);
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d)
+      tma_load_4d(sb + L::OFF_V + s * L::TILE + d * BT * 128, &maps.v, v_full + 8 * s, d * 64, j * BT, hk, b);
+  };
+  if (warp == PRODUCER_WARP && lane == 0) {
     mbar_init(x_full, 1);
     for (int s = 0; s < K_SLOTS; ++s) {
       mbar_init(k_full + 8 * s, 1);
@@ -536,6 +562,15 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
     mbar_init(patched, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (n > 0) {
+      mbar_arrive_expect_tx(x_full, 2 * L::TILE);
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
+      load_k(0);
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
+      load_v(0);
+    }
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -550,26 +585,14 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (lane == 0 && n > 0) {
-        mbar_arrive_expect_tx(x_full, 2 * L::TILE);
-#pragma unroll
-        for (int d = 0; d < D / 64; ++d) {
-          tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
-          tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
-        }
-        int issued_k = 0, issued_v = 0;
-        for (int j = 0; j < n; ++j) {
+        int issued_k = 1, issued_v = 1;
+        for (int j = 1; j < n; ++j) {
           const int sk = j % K_SLOTS, sv = j % V_SLOTS;
           if (j >= K_SLOTS && !mbar_wait(k_empty + 8 * sk, ((j / K_SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(k_full + 8 * sk, L::TILE);
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d)
-            tma_load_4d(sb + L::OFF_K + sk * L::TILE + d * BT * 128, &maps.k, k_full + 8 * sk, d * 64, j * BT, hk, b);
+          load_k(j);
           issued_k = j + 1;
           if (j >= V_SLOTS && !mbar_wait(v_empty + 8 * sv, ((j / V_SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(v_full + 8 * sv, L::TILE);
-#pragma unroll
-          for (int d = 0; d < D / 64; ++d)
-            tma_load_4d(sb + L::OFF_V + sv * L::TILE + d * BT * 128, &maps.v, v_full + 8 * sv, d * 64, j * BT, hk, b);
+          load_v(j);
           issued_v = j + 1;
         }
         mbar_drain(x_full, 0, status);

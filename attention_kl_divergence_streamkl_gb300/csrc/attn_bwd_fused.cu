@@ -12,7 +12,10 @@
 //                                                            dQ = dS K    (the same bytes as an MN-major A)
 // TMEM at D = 128: S/P [0,128), dP and then dQ [128,256), dV [256,384), dK [384,512).  dQ takes dP's columns once
 // the warps hold dP, and four warps empty them into registers at once, so that dP of the next tile can follow; they
-// then stage it 32 columns at a time and issue the reductions.  At D = 64 dQ has columns of its own.
+// then stage it 32 columns at a time and issue the reductions.
+// At D = 64: S/P [0,128), dP/dS [128,256), dV, dK, dQ 64 columns each from 256 on, and K and V as bf16 pairs in the last
+// 64: they are the A operands of S and dP, and dS in TMEM that of dK.  Read from shared memory, operands, dS and the
+// staged dQ come to 324 KB a tile pair, 2500 cycles at 128 bytes a clock; so they are 230 KB.
 //   dS warps     thread = key; 8 of them take 64 queries each (D = 128), or 16 take 32 (D = 64, where their
 //                latency is what bounds a tile pair and registers allow it)
 //   4 dQ warps   TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
@@ -41,8 +44,8 @@ struct Cfg {
   static constexpr int COLS = 128 * 4 / DS_WARPS;  // queries of a dS thread
   static constexpr int PRODUCER_WARP = DS_WARPS + DQ_WARPS, MMA_WARP = PRODUCER_WARP + 1, PATCH_WARP = PRODUCER_WARP + 2;
   static constexpr int THREADS = 32 * (PRODUCER_WARP + 4);
-  // D = 128: 256 * 136 + 128 * 136 + 128 * 104 = 512 * 128;  D = 64: 512 * 80 + 128 * 96 + 128 * 64 = 768 * 80
-  static constexpr int kRegsDs = D == 128 ? 136 : 80, kRegsDq = D == 128 ? 136 : 96, kRegsOther = D == 128 ? 104 : 64;
+  // D = 128: 256 * 136 + 128 * 136 + 128 * 104 = 512 * 128;  D = 64: 512 * 80 + 128 * 88 + 128 * 72 = 768 * 80
+  static constexpr int kRegsDs = D == 128 ? 136 : 80, kRegsDq = D == 128 ? 136 : 88, kRegsOther = D == 128 ? 104 : 72;
 };
 
 template <int D>
@@ -54,6 +57,7 @@ struct Smem {
   static constexpr int CHUNK_BYTES = 32 * CHUNK * 4;
   static constexpr int Q_SLOTS = 2, O_SLOTS = D == 128 ? 1 : 2;
   static constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D, kQ = ALIAS ? kP : 256 + 2 * D;
+  static constexpr uint32_t kTK = 448, kTV = 480;  // D = 64: K and V in TMEM
   static constexpr int TILE = BT * D * 2;
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE;
   static constexpr int OFF_O = OFF_Q + Q_SLOTS * TILE;
@@ -66,8 +70,8 @@ struct Smem {
   static constexpr int OFF_ZERO = OFF_ONES + STEP;
   static constexpr int OFF_BAR = OFF_ZERO + STEP;
   // kv_full, kv_patched, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, ds_free, dq_full,
-  // dq_free, g_done, to_patch, patched; TMEM slot, abort flag
-  static constexpr int BAR_SLOT = 8 * 20;
+  // dq_free, g_done, to_patch, patched, kv_tmem; TMEM slot, abort flag
+  static constexpr int BAR_SLOT = 8 * 21;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16;
 };
 static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
@@ -108,7 +112,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const uint32_t kv_full = bar, kv_patched = bar + 8, q_full = bar + 16, q_empty = bar + 32, o_full = bar + 48,
                  o_empty = bar + 64, s_full = bar + 80, dp_full = bar + 88, p_full = bar + 96, ds_full = bar + 104,
                  ds_free = bar + 112, dq_full = bar + 120, dq_free = bar + 128, g_done = bar + 136, to_patch = bar + 144,
-                 patched = bar + 152, slot = bar + L::BAR_SLOT;
+                 patched = bar + 152, kv_tmem = bar + 160, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -129,6 +133,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     mbar_init(g_done, 1);
     mbar_init(to_patch, 1);
     mbar_init(patched, 1);
+    mbar_init(kv_tmem, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -229,7 +234,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
-            mma_ss(tmem + L::kS, sdesc_add(kd, o), sdesc_add(qd, o), id_s, ks > 0);
+            if (L::ALIAS)
+              mma_ss(tmem + L::kS, sdesc_add(kd, o), sdesc_add(qd, o), id_s, ks > 0);
+            else
+              mma_ts(tmem + L::kS, tmem + L::kTK + 8 * ks, sdesc_add(qd, o), id_s, ks > 0);
           }
           mma_ss(tmem + L::kS, ones, sdesc_step(sb + L::OFF_RS + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
           mma_commit(s_full);
@@ -243,14 +251,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
-            mma_ss(tmem + L::kP, sdesc_add(vd, o), sdesc_add(od, o), id_s, ks > 0);
+            if (L::ALIAS)
+              mma_ss(tmem + L::kP, sdesc_add(vd, o), sdesc_add(od, o), id_s, ks > 0);
+            else
+              mma_ts(tmem + L::kP, tmem + L::kTV + 8 * ks, sdesc_add(od, o), id_s, ks > 0);
           }
           mma_ss(tmem + L::kP, ones, sdesc_step(sb + L::OFF_RD + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
           mma_commit(dp_full);
           return true;
         };
         bool ok = mbar_wait(kv_full, 0, status, abort_flag) &&
-                  (!ragged_k || mbar_wait(kv_patched, 0, status, abort_flag)) && issue_s(0) && issue_dp(0);
+                  (!ragged_k || mbar_wait(kv_patched, 0, status, abort_flag)) &&
+                  (L::ALIAS || mbar_wait(kv_tmem, 0, status, abort_flag)) && issue_s(0) && issue_dp(0);
         for (int u = 0; ok && u < n; ++u) {
           const int sq = u % QS, so = u % OS;
           if (!mbar_wait(p_full, u & 1, status, abort_flag)) break;
@@ -263,22 +275,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           mma_commit(o_empty + 8 * so);
           if (u + 1 < n && !(ok = issue_s(u + 1))) break;
           if (!mbar_wait(ds_full, u & 1, status, abort_flag)) break;
-          if (!L::ALIAS && u >= 1 && !mbar_wait(dq_free, (u - 1) & 1, status, abort_flag)) break;
           tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < BT / 16; ++ks)  // dQ = dS K
-            mma_ss(tmem + L::kQ, sdesc_add(dsmn, ks * 2048), sdesc_add(kmn, ks * 2048), id_q, ks > 0);
-          mma_commit(dq_full);
           const uint64_t qmn = sdesc_sw128(sb + L::OFF_Q + sq * L::TILE, BT * 128, 1024);
+          auto issue_dq = [&]() {  // dQ = dS K
 #pragma unroll
-          for (int ks = 0; ks < BT / 16; ++ks)  // dK += dS^T Q
-            mma_ss(tmem + L::kK, sdesc_add(dsk, (ks >> 2) * (BT * 128) + (ks & 3) * 32), sdesc_add(qmn, ks * 2048), id_g,
-                   u > 0 || ks > 0);
-          mma_commit(q_empty + 8 * sq);
-          mma_commit(ds_free);
-          if (u + 1 < n) {
-            if (L::ALIAS && !mbar_wait(dq_free, u & 1, status, abort_flag)) break;
-            ok = issue_dp(u + 1);
+            for (int ks = 0; ks < BT / 16; ++ks)
+              mma_ss(tmem + L::kQ, sdesc_add(dsmn, ks * 2048), sdesc_add(kmn, ks * 2048), id_q, ks > 0);
+            mma_commit(dq_full);
+          };
+          auto issue_dk = [&]() {  // dK += dS^T Q
+#pragma unroll
+            for (int ks = 0; ks < BT / 16; ++ks) {
+              if (L::ALIAS)
+                mma_ss(tmem + L::kK, sdesc_add(dsk, (ks >> 2) * (BT * 128) + (ks & 3) * 32), sdesc_add(qmn, ks * 2048), id_g,
+                       u > 0 || ks > 0);
+              else
+                mma_ts(tmem + L::kK, tmem + L::kP + C::COLS * (ks * 16 / C::COLS) + 8 * (ks % (C::COLS / 16)),
+                       sdesc_add(qmn, ks * 2048), id_g, u > 0 || ks > 0);
+            }
+            mma_commit(q_empty + 8 * sq);
+          };
+          if (L::ALIAS) {  // dQ first: the dQ warps empty its columns while dK runs, then dP(u+1) takes them
+            issue_dq();
+            issue_dk();
+            mma_commit(ds_free);
+            if (u + 1 < n && (!mbar_wait(dq_free, u & 1, status, abort_flag) || !issue_dp(u + 1))) break;
+          } else {  // dP(u+1), which the dS warps wait for, as soon as dK has read dS
+            issue_dk();
+            if (u + 1 < n && !issue_dp(u + 1)) break;
+            if (u >= 1 && !mbar_wait(dq_free, (u - 1) & 1, status, abort_flag)) break;
+            issue_dq();
+            mma_commit(ds_free);
           }
         }
         mma_commit(g_done);
@@ -344,7 +371,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + L::kS + COLS * grp, tp = tmem + lanes + L::kP + COLS * grp;
     bool ok = true;
-    for (int u = 0; u < n; ++u) {
+    if (!L::ALIAS && n > 0 && grp < 2) {  // K (group 0) and V (group 1) into TMEM: lane = key, a column two of its elements
+      ok = mbar_wait_warp(ragged_k ? kv_patched : kv_full, 0, status, abort_flag) &&
+           mbar_wait_warp(kv_full, 0, status, abort_flag);
+      __syncwarp();
+      if (ok) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = ld_shared16(sw128<BT>(sb + (grp ? L::OFF_V : L::OFF_K), r, i));
+          w[4 * i] = x.x;
+          w[4 * i + 1] = x.y;
+          w[4 * i + 2] = x.z;
+          w[4 * i + 3] = x.w;
+        }
+        tc_fence_after();
+        tmem_st32(tmem + lanes + (grp ? L::kTV : L::kTK), w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_tmem);
+      }
+    }
+    for (int u = 0; ok && u < n; ++u) {
       const int q0 = q_begin + (u % n_qt) * BT + COLS * grp;  // first query of this warp's columns
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
@@ -392,19 +441,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tmem_ld32(tp + 32 * h, d);
         tmem_ld_wait();
         reg_fence32(d);
+        uint32_t pk[16];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = 8 * v + 2 * e;
-            const float2 x = fmul2(make_float2(__uint_as_float(a[h][i]), __uint_as_float(a[h][i + 1])),
-                                   make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
-            w[e] = pack_bf16(x.x, x.y);
-          }
-          st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * (COLS / 8) + h * 4 + v), make_uint4(w[0], w[1], w[2], w[3]));
+        for (int i = 0; i < 32; i += 2) {
+          const float2 x = fmul2(make_float2(__uint_as_float(a[h][i]), __uint_as_float(a[h][i + 1])),
+                                 make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+          pk[i / 2] = pack_bf16(x.x, x.y);
         }
+        if (!L::ALIAS) tmem_st16(tp + 16 * h, pk);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * (COLS / 8) + h * 4 + v),
+                      make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]));
       }
+      if (!L::ALIAS) tmem_st_wait();
       tc_fence_before();
       fence_async_smem();
       __syncwarp();

@@ -132,7 +132,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  if (threadIdx.x == 0) {
+  // the producer sets the barriers up and issues the first loads while the others get TMEM
+  const uint32_t q_bytes = (p.packed ? (uint32_t)(p.G * p.NQ) : (uint32_t)BM) * D * 2;
+  auto load_kv = [&](int u) {  // K(0), V(0), K(1), ...
+    const int s = u % SLOTS;
+    mbar_arrive_expect_tx(kv_full + 8 * s, L::TILE);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+      tma_load_4d(sb + L::OFF_KV + s * L::TILE + h * BN * 128, (u & 1) ? &mv : &mk, kv_full + 8 * s, h * 64,
+                  (kt0 + (u >> 1)) * BN, hk, b);
+  };
+  if (warp == PRODUCER_WARP && lane == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full + 8 * t, 1);
       mbar_init(s_full + 8 * t, 1);
@@ -147,6 +157,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(patched, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    for (int t = 0; t < 2; ++t) {
+      if ((t ? nB : nA) == 0) continue;
+      mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
+                    p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+      if (t == 0 || nA == 0) load_kv(0);
+    }
+    for (int u = 1; u < min(SLOTS, 2 * n); ++u) load_kv(u);
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -161,26 +181,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (lane == 0 && n > 0) {
-        const uint32_t q_rows = p.packed ? (uint32_t)(p.G * p.NQ) : (uint32_t)BM;
-        const uint32_t q_bytes = q_rows * D * 2;
-        auto load_q = [&](int t) {
-          mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
-                        p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
-        };
-        if (nA > 0) load_q(0);
-        if (nB > 0) load_q(1);
-        int issued = 0;
-        for (int u = 0; u < 2 * n; ++u) {  // K(0), V(0), K(1), ...
-          const int s = u % SLOTS;
-          if (u >= SLOTS && !mbar_wait(kv_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(kv_full + 8 * s, L::TILE);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_KV + s * L::TILE + h * BN * 128, (u & 1) ? &mv : &mk, kv_full + 8 * s, h * 64,
-                        (kt0 + (u >> 1)) * BN, hk, b);
+        int issued = min(SLOTS, 2 * n);
+        for (int u = SLOTS; u < 2 * n; ++u) {
+          if (!mbar_wait(kv_empty + 8 * (u % SLOTS), ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
+          load_kv(u);
           issued = u + 1;
         }
         // copies that may still be landing
