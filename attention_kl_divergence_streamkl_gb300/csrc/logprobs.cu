@@ -18,11 +18,14 @@
 // scale still has weight 0), and the fp32 arithmetic on pairs too: 4.5 issue slots
 // a logit against 7 (8192 x 131072 bf16 logits with 8 alternatives: 385 -> FIG us).
 //
-// Top alternatives, also without sorting the row: a thread's largest value is a
-// by-product of the pass.  The K-th largest of these maxima is a lower bound
-// of the K-th largest value, so only the threads whose maximum reaches it are
-// read again (about K of them, from L2), the values that reach it become
-// candidates, and a candidate's place is the number of greater ones.  A value
+// Top alternatives, also without sorting the row: the largest value of each
+// group of four vectors is a by-product of the pass, kept in shared memory, and so is a
+// thread's.  The K-th largest of the threads' maxima is a lower bound of the
+// K-th largest value (any value that at least K of them reach will do, so the search
+// stops at one that few more reach), so only the groups whose maximum reaches it are
+// read again (about K of them), the values that reach it become
+// candidates, and a candidate's place is the number of greater ones.  (Read again thread by
+// thread, without the groups, a row cost 40 KB of DRAM traffic more.)  A value
 // and its column make one 64-bit key (value's order above, column's complement
 // below), so equal values go to the lowest column and the result does not
 // depend on the order in which threads arrive.  Rows with more candidates than
@@ -109,6 +112,24 @@ __device__ __forceinline__ void merge(Sums& a, const Sums& b) {
   a.t = wa * (a.t + a.s * da) + wb * (b.t + b.s * db);
   a.s = wa * a.s + wb * b.s;
   a.m = m;
+}
+
+// The sums of the warp's first N lanes, on all of them.  The same operand order on both sides of an exchange keeps the
+// lanes' results equal.
+template <int N>
+__device__ __forceinline__ void merge_lanes(Sums& a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = N / 2; o; o >>= 1) {
+    Sums b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+           __shfl_xor_sync(0xffffffffu, a.t, o)};
+    if (lane & o) {
+      const Sums c = a;
+      a = b;
+      b = c;
+    }
+    merge(a, b);
+  }
 }
 
 // Adds n values (n is known at compile time) to a thread's sums and its largest raw value.
@@ -244,9 +265,13 @@ __device__ __forceinline__ Cut cut_row(const T* row, int V) {
   return c;
 }
 
+constexpr int kGroups = 16;  // maxima that a thread keeps; group g of a long row goes with g mod 16
+
 template <int NT>
 struct FwdShared {
+  float group_max[kGroups][NT];
   Sums warp_sums[NT / 32];
+  uint32_t warp_lo[NT / 32], warp_hi[NT / 32];
   Sums part_sums[8];
   uint64_t cand[kMaxCand];
   uint64_t best[8 * 32];  // each part's top K, gathered in the first part's block
@@ -302,7 +327,7 @@ __device__ void warp_lists(const T* row, int lo, int hi, int K, FwdShared<NT>& s
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT) logprobs_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int NW = NT / 32;
   __shared__ FwdShared<NT> sh;
@@ -323,18 +348,32 @@ __global__ void __launch_bounds__(NT) logprobs_fwd_kernel(const FwdArgs a) {
 
   Sums sums{kNegInf, 0.f, 0.f};
   float top = kNegInf;  // this thread's largest value among its vectors
-  int v = tid;
+  int v = tid, group = 0;
+  auto keep = [&](float m) {  // a group's maximum
+    top = fmaxf(top, m);
+    if (a.K) {
+      float& slot = sh.group_max[group % kGroups][tid];
+      slot = group < kGroups ? m : fmaxf(slot, m);
+    }
+    ++group;
+  };
   for (; v + (kUnroll - 1) * NT < nv; v += kUnroll * NT) {
     Vec<T> x[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) x[u].u = load_stream(vecs + v + u * NT);
+    float m = kNegInf;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) add_vector<T>(sums, top, x[u], c, packed);
+    for (int u = 0; u < kUnroll; ++u) add_vector<T>(sums, m, x[u], c, packed);
+    keep(m);
   }
-  for (; v < nv; v += NT) {
-    Vec<T> x;
-    x.u = load_stream(vecs + v);
-    add_vector<T>(sums, top, x, c, packed);
+  if (v < nv) {  // the last group is shorter
+    float m = kNegInf;
+    for (; v < nv; v += NT) {
+      Vec<T> x;
+      x.u = load_stream(vecs + v);
+      add_vector<T>(sums, m, x, c, packed);
+    }
+    keep(m);
   }
   // the columns outside the vectors: one a thread, and always candidates
   const uint32_t top_order = tid < nv ? order_of(top) : 0u;
@@ -348,20 +387,14 @@ __global__ void __launch_bounds__(NT) logprobs_fwd_kernel(const FwdArgs a) {
       if (a.K) sh.cand[atomicAdd(&sh.n_cand, 1)] = key_of(f[0], (uint32_t)j);  // at most 2 (N - 1) of them
     }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const Sums b{__shfl_xor_sync(0xffffffffu, sums.m, o), __shfl_xor_sync(0xffffffffu, sums.s, o),
-                 __shfl_xor_sync(0xffffffffu, sums.t, o)};
-    // the same operand order on both sides of the exchange keeps all lanes' sums equal
-    if (lane & o) {
-      Sums q = b;
-      merge(q, sums);
-      sums = q;
-    } else {
-      merge(sums, b);
-    }
+  merge_lanes<32>(sums);
+  const uint32_t prefix = top_order >> 16;  // 16 bits are enough for a lower bound
+  const uint32_t warp_lo = __reduce_min_sync(0xffffffffu, prefix), warp_hi = __reduce_max_sync(0xffffffffu, prefix);
+  if (lane == 0) {
+    sh.warp_sums[warp] = sums;
+    sh.warp_lo[warp] = warp_lo;
+    sh.warp_hi[warp] = warp_hi;
   }
-  if (lane == 0) sh.warp_sums[warp] = sums;
 
   const int k_here = min(a.K, cut.head * (int)first + nv * N + (a.V - cut.tail0) * (int)last);  // columns can be fewer
   uint64_t* best = sh.best;
@@ -371,25 +404,43 @@ __global__ void __launch_bounds__(NT) logprobs_fwd_kernel(const FwdArgs a) {
     if (tid < a.K) best[part * a.K + tid] = 0;  // a part may hold fewer columns than K
   }
   if (a.K) {
-    // the largest 16-bit prefix that at least K threads' maxima reach (0 when fewer threads hold vectors)
-    uint32_t thr = 0;
-    const uint32_t prefix = top_order >> 16;
-    for (uint32_t bit = 0x8000u; bit; bit >>= 1)
-      if (__syncthreads_count(prefix >= (thr | bit)) >= a.K) thr |= bit;
-    const uint32_t bound = thr << 16;
+    __syncthreads();
+    uint32_t lo = sh.warp_lo[0], hi = sh.warp_hi[0];
+    for (int w = 1; w < NW; ++w) {
+      lo = min(lo, sh.warp_lo[w]);
+      hi = max(hi, sh.warp_hi[w]);
+    }
+    // a prefix that at least K threads' maxima reach (0 when fewer threads hold vectors), and not many more; `lo` always
+    // is one where K <= NT, which it is
+    while (lo < hi) {
+      const uint32_t mid = (lo + hi + 1) / 2;
+      const int reach = __syncthreads_count(prefix >= mid);
+      if (reach >= a.K) {
+        lo = mid;
+        if (reach <= a.K + 8) break;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    const uint32_t bound = lo << 16;
     if (top_order && top_order >= bound) sh.again[atomicAdd(&sh.n_again, 1)] = (unsigned short)tid;
     __syncthreads();
     for (int q = warp; q < sh.n_again; q += NW) {
       const int t = sh.again[q];
-      for (int w = t + lane * NT; w < nv; w += 32 * NT) {
-        Vec<T> x;
-        x.u = __ldg(vecs + w);
+      // lane: group lane / 4 (then + 8) of the thread, vector lane % 4 of the group
+      for (int slot = lane / kUnroll; slot < kGroups; slot += 32 / kUnroll) {
+        const int base = t + (slot * kUnroll + lane % kUnroll) * NT;
+        if (t + slot * kUnroll * NT >= nv || order_of(sh.group_max[slot][t]) < bound) continue;
+        for (int w = base; w < nv; w += kGroups * kUnroll * NT) {
+          Vec<T> x;
+          x.u = __ldg(vecs + w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float f = to_float(x.e[i]);
-          if (order_of(f) >= bound) {
-            const int at = atomicAdd(&sh.n_cand, 1);
-            if (at < kMaxCand) sh.cand[at] = key_of(f, (uint32_t)(cut.head + (v0 + w) * N + i));
+          for (int i = 0; i < N; ++i) {
+            const float f = to_float(x.e[i]);
+            if (order_of(f) >= bound) {
+              const int at = atomicAdd(&sh.n_cand, 1);
+              if (at < kMaxCand) sh.cand[at] = key_of(f, (uint32_t)(cut.head + (v0 + w) * N + i));
+            }
           }
         }
       }
@@ -402,12 +453,12 @@ __global__ void __launch_bounds__(NT) logprobs_fwd_kernel(const FwdArgs a) {
                         best + part * a.K);
   }
   __syncthreads();
-  if (tid == 0) {
-    Sums all = sh.warp_sums[0];
-    for (int w = 1; w < NW; ++w) merge(all, sh.warp_sums[w]);
+  if (warp == 0) {
+    Sums all = sh.warp_sums[lane % NW];
+    merge_lanes<NW>(all);
     Sums* to = sh.part_sums;
     if (a.parts > 1) to = cg::this_cluster().map_shared_rank(sh.part_sums, 0);
-    to[part] = all;
+    if (lane == 0) to[part] = all;
   }
   if (a.parts > 1)
     cg::this_cluster().sync();
@@ -469,7 +520,7 @@ struct BwdArgs {
 // The pass writes the second term; then the given tokens' columns, a handful, are written again with the sum of
 // both in fp32, rounded once.  A token that is given twice adds twice: its first place takes the sum of all.
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT) logprobs_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ float sum_g[NT / 32];
   const int tid = threadIdx.x;
