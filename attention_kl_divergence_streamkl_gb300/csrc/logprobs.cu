@@ -69,6 +69,7 @@ struct Vec {
   static constexpr int N = 16 / sizeof(T);
   union {
     uint4 u;
+    uint32_t w[4];
     T e[N];
   };
 };
@@ -132,29 +133,21 @@ __device__ __forceinline__ void merge_lanes(Sums& a) {
   }
 }
 
-// Adds n values (n is known at compile time) to a thread's sums and its largest raw value.
-template <int N>
-__device__ __forceinline__ void add_values(Sums& a, float& top, const float (&x)[N], float c) {
-  float vm = x[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) vm = fmaxf(vm, x[i]);
-  top = fmaxf(top, vm);
-  const float y = vm * c;
+// A thread's sums while it reads: two of each, for the two halves of a pair.
+struct Sums2 {
+  float m;
+  float2 s, t;
+};
+
+// Moves m up to y; the sums follow.
+__device__ __forceinline__ void move_max(Sums2& a, float y) {
   if (y > a.m) {
     if (a.m != kNegInf) {
       const float d = max_nan(a.m - y, kFloor), w = ex2(d);
-      a.t = w * (a.t + a.s * d);
-      a.s *= w;
+      a.t = make_float2(w * (a.t.x + a.s.x * d), w * (a.t.y + a.s.y * d));
+      a.s = make_float2(a.s.x * w, a.s.y * w);
     }
     a.m = y;
-  }
-  const float z = a.m == kNegInf ? 0.f : -a.m;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float d = max_nan(fmaf(x[i], c, z), kFloor);
-    const float p = ex2(d);
-    a.s += p;
-    a.t = fmaf(p, d, a.t);
   }
 }
 
@@ -200,44 +193,47 @@ struct Pair<__half> {
   }
 };
 
-// A 16-byte vector of logits.  `packed`: c is large enough for the packed guard.  A vector whose maximum itself lies
-// near the guard's value takes the other way.
-template <typename T>
-__device__ __forceinline__ void add_vector(Sums& a, float& top, const Vec<T>& x, float c, bool packed) {
+// NV 16-byte vectors of logits at once: one maximum, one look at whether m moves.  `packed`: c is large enough for the
+// packed guard.  Vectors whose maximum itself lies near the guard's value take the other way.
+template <typename T, int NV>
+__device__ __forceinline__ void add_vectors(Sums2& a, float& top, const Vec<T> (&x)[NV], float c, bool packed) {
+  float vm;
+  bool pairs = false;
   if constexpr (sizeof(T) == 2) {
-    const uint32_t w[4] = {x.u.x, x.u.y, x.u.z, x.u.w};
-    const float2 m2 = Pair<T>::unpack(Pair<T>::max2(Pair<T>::max2(w[0], w[1]), Pair<T>::max2(w[2], w[3])));
-    const float vm = fmaxf(m2.x, m2.y);
-    if (packed && vm > Pair<T>::kLow * 0.5f) {
-      top = fmaxf(top, vm);
-      const float y = vm * c;
-      if (y > a.m) {
-        if (a.m != kNegInf) {
-          const float d = max_nan(a.m - y, kFloor), f = ex2(d);
-          a.t = f * (a.t + a.s * d);
-          a.s *= f;
-        }
-        a.m = y;
-      }
-      const float2 cc = make_float2(c, c), nm = make_float2(-a.m, -a.m);
-      float2 s = make_float2(0.f, 0.f), t = s;
+    uint32_t m = Pair<T>::max2(x[0].w[0], x[0].w[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 d = ffma2(Pair<T>::unpack(Pair<T>::raise(w[i])), cc, nm);
+    for (int i = 2; i < 4 * NV; ++i) m = Pair<T>::max2(m, x[i / 4].w[i % 4]);
+    const float2 m2 = Pair<T>::unpack(m);
+    vm = fmaxf(m2.x, m2.y);
+    pairs = packed && vm > Pair<T>::kLow * 0.5f;
+  } else {
+    vm = x[0].e[0];
+#pragma unroll
+    for (int i = 1; i < 4 * NV; ++i) vm = fmaxf(vm, x[i / 4].e[i % 4]);
+  }
+  top = fmaxf(top, vm);
+  move_max(a, vm * c);
+  if constexpr (sizeof(T) == 2) {
+    if (pairs) {
+      const float2 cc = make_float2(c, c), nm = make_float2(-a.m, -a.m);
+#pragma unroll
+      for (int i = 0; i < 4 * NV; ++i) {
+        const float2 d = ffma2(Pair<T>::unpack(Pair<T>::raise(x[i / 4].w[i % 4])), cc, nm);
         const float2 e = make_float2(ex2(d.x), ex2(d.y));
-        s = fadd2(s, e);
-        t = ffma2(e, d, t);
+        a.s = fadd2(a.s, e);
+        a.t = ffma2(e, d, a.t);
       }
-      a.s += s.x + s.y;
-      a.t += t.x + t.y;
       return;
     }
   }
-  constexpr int N = Vec<T>::N;
-  float f[N];
+  const float z = a.m == kNegInf ? 0.f : -a.m;
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_float(x.e[i]);
-  add_values<N>(a, top, f, c);
+  for (int i = 0; i < NV * Vec<T>::N; ++i) {
+    const float d = max_nan(fmaf(to_float(x[i / Vec<T>::N].e[i % Vec<T>::N]), c, z), kFloor);
+    const float e = ex2(d);
+    a.s.x += e;
+    a.t.x = fmaf(e, d, a.t.x);
+  }
 }
 
 struct FwdArgs {
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdAr
   if (tid == 0) sh.n_cand = sh.n_again = 0;
   if (a.parts > 1) cg::this_cluster().barrier_arrive();  // this block runs: its shared memory may be written
 
-  Sums sums{kNegInf, 0.f, 0.f};
+  Sums2 acc{kNegInf, make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   float top = kNegInf;  // this thread's largest value among its vectors
   int v = tid, group = 0;
   auto keep = [&](float m) {  // a group's maximum
@@ -362,16 +358,15 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdAr
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) x[u].u = load_stream(vecs + v + u * NT);
     float m = kNegInf;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) add_vector<T>(sums, m, x[u], c, packed);
+    add_vectors<T, kUnroll>(acc, m, x, c, packed);
     keep(m);
   }
   if (v < nv) {  // the last group is shorter
     float m = kNegInf;
     for (; v < nv; v += NT) {
-      Vec<T> x;
-      x.u = load_stream(vecs + v);
-      add_vector<T>(sums, m, x, c, packed);
+      Vec<T> x[1];
+      x[0].u = load_stream(vecs + v);
+      add_vectors<T, 1>(acc, m, x, c, packed);
     }
     keep(m);
   }
@@ -381,12 +376,15 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdAr
   for (int side = 0; side < 2; ++side) {
     const int j = side ? cut.tail0 + tid : tid;
     if (side ? last && j < a.V : first && j < cut.head) {
-      const float f[1] = {to_float(row[j])};
-      float unused = kNegInf;
-      add_values<1>(sums, unused, f, c);
-      if (a.K) sh.cand[atomicAdd(&sh.n_cand, 1)] = key_of(f[0], (uint32_t)j);  // at most 2 (N - 1) of them
+      const float f = to_float(row[j]);
+      move_max(acc, f * c);
+      const float d = max_nan(fmaf(f, c, acc.m == kNegInf ? 0.f : -acc.m), kFloor), e = ex2(d);
+      acc.s.x += e;
+      acc.t.x = fmaf(e, d, acc.t.x);
+      if (a.K) sh.cand[atomicAdd(&sh.n_cand, 1)] = key_of(f, (uint32_t)j);  // at most 2 (N - 1) of them
     }
   }
+  Sums sums{acc.m, acc.s.x + acc.s.y, acc.t.x + acc.t.y};
   merge_lanes<32>(sums);
   const uint32_t prefix = top_order >> 16;  // 16 bits are enough for a lower bound
   const uint32_t warp_lo = __reduce_min_sync(0xffffffffu, prefix), warp_hi = __reduce_max_sync(0xffffffffu, prefix);
