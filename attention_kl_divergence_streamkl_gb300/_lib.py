@@ -80,7 +80,7 @@ SIGNATURES = {
     "streamkl_attn_fwd_workspace": (_I, [AttnShape, ctypes.POINTER(_SZ)]),
     "streamkl_attn_fwd_plan": (_I, [AttnShape, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "streamkl_attn_fwd": (_I, [_P, _P, _P, AttnShape, _P, _F, _P, _SZ, _S]),
-    "streamkl_attn_bwd_select": (_I, [AttnShape, _I]),
+    "streamkl_attn_bwd_plan": (_I, [AttnShape, _I, _I, *[ctypes.POINTER(_I)] * 3, ctypes.POINTER(_SZ)]),
     "streamkl_attn_bwd_workspace": (_I, [AttnShape, _I, ctypes.POINTER(_SZ)]),
     "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
@@ -499,11 +499,11 @@ def attn_fwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
 
 
 @functools.lru_cache(maxsize=1024)
-def _attn_workspace(name, index, sizes, *mode):
+def _attn_workspace(name, index, sizes, causal, *mode):
     """Workspace bytes of an attention of these sizes on device `index` (a pure rule of sizes and the device)."""
     n = ctypes.c_size_t(0)
     with torch.cuda.device(index):
-        _check(getattr(lib(), name)(make_attn_shape(*sizes), *mode, ctypes.byref(n)), name)
+        _check(getattr(lib(), name)(make_attn_shape(*sizes, None, causal), *mode, ctypes.byref(n)), name)
     return n.value
 
 
@@ -518,7 +518,7 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
     B, H, _, NQ, _, D = sizes
     s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, qs)
-    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", dev.index, sizes)
+    nbytes = _attn_workspace("streamkl_attn_fwd_workspace", dev.index, sizes, bool(causal))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     o = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
@@ -527,17 +527,21 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     return _back((o, lse), True) if host else (o, lse)
 
 
-def attn_bwd_select(B, H, HK, NQ, NK, D, num_sms, causal=False) -> int:
-    """The path BWD_AUTO takes in attn_bwd on a device with num_sms SMs."""
-    return lib().streamkl_attn_bwd_select(make_attn_shape(B, H, HK, NQ, NK, D, None, causal), int(num_sms))
+def attn_bwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False, bwd_mode=BWD_AUTO):
+    """(path, parts of a dk/dv tile, parts of a dq tile, workspace bytes) of the attention backward on a device with
+    num_sms SMs; path is BWD_FUSED or BWD_SEPARATE."""
+    path, kv, q, n = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
+    _check(lib().streamkl_attn_bwd_plan(make_attn_shape(B, H, HK, NQ, NK, D, None, causal), int(num_sms), int(bwd_mode),
+                                        *map(ctypes.byref, (path, kv, q, n))), "streamkl_attn_bwd_plan")
+    return path.value, kv.value, q.value, n.value
 
 
 def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None, bwd_mode=BWD_AUTO):
     """Attention's gradients (dq, dk, dv), bf16 with the layouts of q, k, v.
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
-    bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED visits each tile pair once and adds dq up in no
-    fixed order; BWD_AUTO picks by shape.
+    bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED (D = 64) visits each tile pair once and adds dq up
+    in no fixed order; BWD_AUTO picks by shape.
     """
     (q, k, v, o, do), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
     (q, qs), (k, ks), (v, vs), (o, os_), (do, ds) = _layout(q), _layout(k), _layout(v), _layout(o), _layout(do)
@@ -548,7 +552,7 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
     lse = _rows(lse, dev, (B, H, NQ), "lse")
     dlse = _rows(dlse, dev, (B, H, NQ), "dlse")
     s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, os_)
-    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", dev.index, sizes, bwd_mode)
+    nbytes = _attn_workspace("streamkl_attn_bwd_workspace", dev.index, sizes, bool(causal), bwd_mode)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     dq = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     dk = torch.empty_strided((B, HK, NK, D), (*ks, 1), dtype=torch.bfloat16, device=dev)

@@ -690,21 +690,25 @@ static bool attn_mode_ok(int mode) {
   return mode == STREAMKL_BWD_AUTO || mode == STREAMKL_BWD_FUSED || mode == STREAMKL_BWD_SEPARATE;
 }
 
-int streamkl_attn_bwd_select(streamkl_attn_shape s, int num_sms) {
-  AttnProblem p;
-  if (attn_problem(s, &p) != STREAMKL_OK || num_sms <= 0) return 0;
-  return attn_bwd_fused(p, STREAMKL_BWD_AUTO, num_sms) ? STREAMKL_BWD_FUSED : STREAMKL_BWD_SEPARATE;
-}
-
-streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, int bwd_mode, size_t* bytes) {
+streamkl_status streamkl_attn_bwd_plan(streamkl_attn_shape s, int num_sms, int bwd_mode, int* path, int* kv_parts,
+                                       int* q_parts, size_t* workspace_bytes) {
   AttnProblem p;
   streamkl_status v = attn_problem(s, &p);
   if (v != STREAMKL_OK) return v;
-  if (!bytes || !attn_mode_ok(bwd_mode)) return STREAMKL_ERR_INVALID;
-  int sms = 0;
-  if (bwd_mode == STREAMKL_BWD_AUTO && (v = device_sms(&sms)) != STREAMKL_OK) return v;
-  *bytes = attn_bwd_workspace(p, attn_bwd_fused(p, bwd_mode, sms));
+  if (!attn_mode_ok(bwd_mode) || !path || !kv_parts || !q_parts || !workspace_bytes) return STREAMKL_ERR_INVALID;
+  if (bwd_mode == STREAMKL_BWD_FUSED && !attn_bwd_has_fused(p)) return STREAMKL_ERR_UNSUPPORTED;
+  if (num_sms <= 0 && (v = device_sms(&num_sms)) != STREAMKL_OK) return v;
+  const AttnBwdPlan g = attn_bwd_plan(p, bwd_mode, num_sms);
+  *path = g.fused ? STREAMKL_BWD_FUSED : STREAMKL_BWD_SEPARATE;
+  *kv_parts = g.kv_parts;
+  *q_parts = g.q_parts;
+  *workspace_bytes = attn_bwd_scratch(p, g, nullptr).bytes;
   return STREAMKL_OK;
+}
+
+streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, int bwd_mode, size_t* bytes) {
+  int path, kv_parts, q_parts;
+  return streamkl_attn_bwd_plan(s, 0, bwd_mode, &path, &kv_parts, &q_parts, bytes);
 }
 
 streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -714,23 +718,24 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
   streamkl_status st = attn_problem(s, &p);
   if (st != STREAMKL_OK) return st;
   if (!attn_mode_ok(bwd_mode)) return STREAMKL_ERR_INVALID;
+  if (bwd_mode == STREAMKL_BWD_FUSED && !attn_bwd_has_fused(p)) return STREAMKL_ERR_UNSUPPORTED;
   if (p.NQ > 0 && (!dq || !aligned16(dq))) return STREAMKL_ERR_INVALID;
   if (p.NK > 0 && (!dk || !dv || !aligned16(dk) || !aligned16(dv))) return STREAMKL_ERR_INVALID;
-  bool fused = false;
-  int sms = 0;
+  AttnBwdPlan plan{};
   if (p.NQ > 0 && p.NK > 0) {
     if (!q || !k || !v || !o || !go || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
         !aligned16(go) || !rows_ok(lse) || !aligned_to_or_null(dlse, 4))
       return STREAMKL_ERR_INVALID;
-    if (!workspace || !aligned16(workspace)) return STREAMKL_ERR_WORKSPACE;
-    if (workspace_bytes < attn_bwd_workspace(p, false)) return STREAMKL_ERR_WORKSPACE;
+    // no plan needs less than the rows' values
+    if (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)p.rows * 32) return STREAMKL_ERR_WORKSPACE;
+    int sms = 0;
     if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
-    fused = attn_bwd_fused(p, bwd_mode, sms);
-    if (workspace_bytes < attn_bwd_workspace(p, fused)) return STREAMKL_ERR_WORKSPACE;
+    plan = attn_bwd_plan(p, bwd_mode, sms);
+    if (workspace_bytes < attn_bwd_scratch(p, plan, workspace).bytes) return STREAMKL_ERR_WORKSPACE;
   }
   int* status = nullptr;
   if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
-  return from_cuda(launch_attn_bwd(p, fused, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, sms, status,
+  return from_cuda(launch_attn_bwd(p, plan, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, status,
                                    static_cast<cudaStream_t>(stream)));
 }
 

@@ -74,6 +74,66 @@ __device__ __forceinline__ uint64_t sdesc_step(uint32_t addr, uint32_t zero) {
          ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
 }
 
+// ---- parts: where a kind of block has fewer or longer tiles than the SMs can share evenly, a tile's stream is dealt out
+// over `parts` blocks.  Each leaves its fp32 accumulators in the workspace, and the one that counts up to `parts` adds
+// them all in the parts' order, so the sum does not depend on who that is.
+struct TilePart {
+  int tile, rank, parts;
+  // The first of the stream's `n` elements that part `rank + next` takes.
+  // (n is below 2^24, parts at most 8.)
+  __device__ __forceinline__ int from(int n, int next = 0) const {
+    return (int)((unsigned)n * (unsigned)(rank + next) / (unsigned)parts);
+  }
+};
+// Block x of a kind whose tiles [0, whole) are one block each and the later ones `parts`.
+__device__ __forceinline__ TilePart tile_part(unsigned x, unsigned whole, int parts) {
+  if (x < whole) return TilePart{(int)x, 0, 1};
+  return TilePart{(int)(whole + (x - whole) / parts), (int)((x - whole) % parts), parts};
+}
+// A part is [COLS / 4][128 rows] float4: a warp, whose lanes are rows, writes and reads whole lines.
+template <int COLS>
+__device__ __forceinline__ void part_put(float4* tile, int rank, int r, int col, const uint32_t (&a)[32]) {
+  float4* dst = tile + (size_t)rank * (COLS / 4 * 128) + col / 4 * 128 + r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    __stcg(dst + i * 128, make_float4(__uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]),
+                                      __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3])));
+}
+template <int COLS>
+__device__ __forceinline__ void part_sum(const float4* tile, int parts, int r, int col, uint32_t (&a)[32]) {
+  float s[32] = {};
+#pragma unroll 1
+  for (int q = 0; q < parts; ++q) {
+    const float4* src = tile + (size_t)q * (COLS / 4 * 128) + col / 4 * 128 + r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = __ldcg(src + i * 128);
+      s[4 * i] += v.x;
+      s[4 * i + 1] += v.y;
+      s[4 * i + 2] += v.z;
+      s[4 * i + 3] += v.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a[i] = __float_as_uint(s[i]);
+}
+// True on the block whose part is the last to be written; `threads` (the first of the block, by whole warps) call it once
+// their writes are issued.  The counter is left at zero.
+__device__ __forceinline__ bool part_last(unsigned* counter, int parts, int threads, volatile int* flag) {
+  __threadfence();
+  __syncwarp();
+  named_bar_sync(2, threads);
+  if (threadIdx.x == 0) {
+    const unsigned before = atomicAdd(counter, 1u);
+    if (before + 1 == (unsigned)parts) *counter = 0;
+    *flag = before + 1 == (unsigned)parts;
+    __threadfence();
+  }
+  __syncwarp();  // the barrier wants whole warps
+  named_bar_sync(2, threads);
+  return *flag;
+}
+
 // ---- a tile out: fp32 rows in registers -> bf16 in a swizzled tile in shared memory -> one TMA store.  Written from
 // registers a thread's row would scatter over 32 lines to a store: 2000 cycles a 128 x 128 tile against 300.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {

@@ -12,7 +12,8 @@
 //   dQ block     128 queries stationary; streams the key tiles: three products
 // (attn_bwd_fused.cu visits each tile pair once, for five, and adds dQ up in
 // L2).  Both kinds run in one launch, the kind with the longer blocks first: the
-// shorter ones fill the SMs that the longer ones leave.
+// shorter ones fill the SMs that the longer ones leave.  Tiles whose streams are
+// long for the number of SMs are dealt out over several blocks (attn_bwd_plan).
 //
 // A small kernel first writes, per query row, -LSE / scale and -delta, each as
 // three bf16 that add up to its 24 bits, in 16 bytes and 128-row padded: a
@@ -57,8 +58,9 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
 template <int D>
 __global__ void __launch_bounds__(256)
     attn_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
-                     float4* __restrict__ acc, int padded) {
+                     float4* __restrict__ acc, unsigned* __restrict__ counters, unsigned n_counters, int padded) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
+  for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
   const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / LANES;  // row of [B H][padded]
   const int lane = threadIdx.x % LANES;
   const bool inside = r < (long long)p.B * p.H * padded;
@@ -166,7 +168,8 @@ static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
 template <int D>
 __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __restrict__ row_s,
                                          const uint4* __restrict__ row_d, int padded, int* status, const BwdMaps& maps,
-                                         const unsigned blk, const int longest_first) {
+                                         const AttnBwdPlan& plan, const unsigned blk, float4* __restrict__ part_acc,
+                                         unsigned* __restrict__ counters) {
   using L = kv::Smem<D>;
   using kv::SLOTS;
   extern __shared__ uint8_t smem_raw[];
@@ -175,15 +178,17 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // heads in order (the blocks in flight share one key head's query tiles in L2); within a head the first key
   // tiles, which see the most queries under a causal mask, first.  A small grid: the first key tiles of all heads first
+  const TilePart part = tile_part(blk, plan.kv_whole, plan.kv_parts);
   const int n_kt = (p.NK + BT - 1) / BT, heads = p.B * p.HK;
-  const int bhk = longest_first ? (int)(blk % heads) : (int)(blk / n_kt);
+  const int bhk = plan.longest_first ? part.tile % heads : part.tile / n_kt;
   const int b = bhk / p.HK, hk = bhk % p.HK;
-  const int k0 = (longest_first ? (int)(blk / heads) : (int)(blk % n_kt)) * BT;
+  const int k0 = (plan.longest_first ? part.tile / heads : part.tile % n_kt) * BT;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
   const int n_qt = (k0 < kl && q_begin < ql) ? (ql - q_begin + BT - 1) / BT : 0;
-  const int n = p.G * n_qt;  // tile u: head u / n_qt of the group, query tile u % n_qt
+  // tile u: head u / n_qt of the group, query tile u % n_qt; this block takes the tiles [u0, u0 + n)
+  const int u0 = part.from(p.G * n_qt), n = part.from(p.G * n_qt, 1) - u0;
   const bool ragged = n > 0 && ql < p.NQ && (ql & (BT - 1));  // the last query tile has rows past the sequence
 
   const uint32_t bar = sb + L::OFF_BAR;
@@ -191,9 +196,10 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
                  s_full = bar + 72, dp_full = bar + 80, p_full = bar + 88, ds_full = bar + 96, g_done = bar + 104,
                  to_patch = bar + 112, patched = bar + 120, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+  volatile int* part_flag = abort_flag + 1;
   // the producer sets the barriers up and issues the first loads while the others get TMEM
   auto load_q = [&](int u) {
-    const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+    const int s = u % SLOTS, hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
     mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
@@ -201,39 +207,42 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + ((long long)b * p.H + hq) * padded + q0, L::STEP, q_full + 8 * s);
   };
   auto load_o = [&](int u) {
-    const int s = u % SLOTS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+    const int s = u % SLOTS, hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
     mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
       tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &maps.go, o_full + 8 * s, h * 64, q0, hq, b);
     bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + ((long long)b * p.H + hq) * padded + q0, L::STEP, o_full + 8 * s);
   };
-  if (warp == PRODUCER_WARP && lane == 0) {
-    mbar_init(kv_full, 1);
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(q_full + 8 * s, 1);
-      mbar_init(q_empty + 8 * s, 1);
-      mbar_init(o_full + 8 * s, 1);
-      mbar_init(o_empty + 8 * s, 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(p_full, DS_WARPS);
-    mbar_init(ds_full, DS_WARPS);
-    mbar_init(g_done, 1);
-    mbar_init(to_patch, 1);
-    mbar_init(patched, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    if (n > 0) {
-      mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+  if (warp == PRODUCER_WARP) {
+    if (elect_one()) {
+      mbar_init(kv_full, 1);
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(q_full + 8 * s, 1);
+        mbar_init(q_empty + 8 * s, 1);
+        mbar_init(o_full + 8 * s, 1);
+        mbar_init(o_empty + 8 * s, 1);
+      }
+      mbar_init(s_full, 1);
+      mbar_init(dp_full, 1);
+      mbar_init(p_full, DS_WARPS);
+      mbar_init(ds_full, DS_WARPS);
+      mbar_init(g_done, 1);
+      mbar_init(to_patch, 1);
+      mbar_init(patched, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      if (n > 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
-      load_q(0);
+        for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
+        load_q(0);
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
-      load_o(0);
+        for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
+        load_o(0);
+      }
     }
+    __syncwarp();  // the warp's other lanes wait for the one that issues
   }
   if (threadIdx.x < 128) {
     st_shared16(sb + L::OFF_ONES + threadIdx.x * 16, make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u));
@@ -252,7 +261,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
   if (warp >= DS_WARPS) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         int issued_q = 1, issued_o = 1;
         for (int u = 1; u < n; ++u) {
           const int s = u % SLOTS;
@@ -271,11 +280,12 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       }
       __syncwarp();
     } else if (warp == PATCH_WARP) {
-      // for each head of the group: its last Q tile, then its last dO tile, when the MMA thread has seen them land
+      // for each head's last tile: its Q, then its dO, when the MMA thread has seen them land
       if (ragged) {
-        for (int e = 0; e < 2 * p.G; ++e) {
+        const int first = n_qt - 1 - u0 % n_qt;  // the first of this block's tiles that is a head's last
+        for (int e = 0; first + e / 2 * n_qt < n; ++e) {
           if (!mbar_wait_warp(to_patch, e & 1, status, abort_flag)) break;
-          const int s = ((e / 2 + 1) * n_qt - 1) % SLOTS, from = ql & (BT - 1);
+          const int s = (first + e / 2 * n_qt) % SLOTS, from = ql & (BT - 1);
           const uint32_t tile = sb + ((e & 1) ? L::OFF_O : L::OFF_Q) + s * L::TILE;
           for (int i = lane; i < (BT - from) * (D / 8); i += 32)
             st_shared_zero16(sw128<BT>(tile, from + i / (D / 8), i % (D / 8)));
@@ -293,7 +303,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
         const uint64_t ones = sdesc_step(sb + L::OFF_ONES, sb + L::OFF_ZERO);
         int patches = 0;
         auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
-          if (!ragged || (u + 1) % n_qt) return true;
+          if (!ragged || (u0 + u + 1) % n_qt) return true;
           mbar_arrive(to_patch);
           return mbar_wait(patched, patches++ & 1, status, abort_flag);
         };
@@ -363,7 +373,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     const uint32_t ts = tmem + lanes + kv::kColS + 32 * grp, tp = tmem + lanes + kv::kColP + 32 * grp;
     bool ok = true;
     for (int u = 0; u < n; ++u) {
-      const int q0 = q_begin + (u % n_qt) * BT + 32 * grp;  // first query of this warp's columns
+      const int q0 = q_begin + ((u0 + u) % n_qt) * BT + 32 * grp;  // first query of this warp's columns
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
@@ -419,18 +429,40 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       got = mbar_wait_warp(g_done, 0, status, abort_flag);
       __syncwarp();
     }
-    // dV through the first Q slot, dK through the first dO slot: every product that read them is done
-    if (got && grp * 32 < D) {
+    // dV through the first Q slot, dK through the first dO slot: every product that read them is done.  A part's
+    // accumulators of both are one tile of 2 D columns
+    float4* mine = part_acc + (size_t)(part.tile - plan.kv_whole) * part.parts * (2 * D / 4 * BT);
+    const bool cols = grp * 32 < D;
+    bool last = true;
+    if (part.parts > 1) {
+      if (got && cols) {
+        tc_fence_after();
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          uint32_t g[32] = {};
+          if (n > 0) {
+            tmem_ld32(tmem + lanes + (which ? kv::kColK : kv::kColV) + 32 * grp, g);
+            tmem_ld_wait();
+            reg_fence32(g);
+          }
+          part_put<2 * D>(mine, part.rank, r, which * D + 32 * grp, g);
+        }
+      }
+      last = part_last(counters + (part.tile - plan.kv_whole), part.parts, DS_WARPS * 32, part_flag);
+    }
+    if (got && last && cols) {
       tc_fence_after();
-      uint32_t g[32];
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        if (n > 0) {
+        uint32_t g[32] = {};
+        if (part.parts > 1) {
+          part_sum<2 * D>(mine, part.parts, r, which * D + 32 * grp, g);
+        } else if (n > 0) {
           tmem_ld32(tmem + lanes + (which ? kv::kColK : kv::kColV) + 32 * grp, g);
           tmem_ld_wait();
           reg_fence32(g);
         }
-        if (n == 0 || key >= kl) {
+        if (key >= kl) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = 0u;
         }
@@ -439,9 +471,12 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       fence_async_smem();
     }
     // every warp comes here; one that gave up makes none of them store
-    if (!named_bar_any(1, DS_WARPS * 32, !got) && threadIdx.x == 0) {
-      store_tile<D>(&maps.dv, sb + L::OFF_Q, k0, hk, b);
-      store_tile<D>(&maps.dk, sb + L::OFF_O, k0, hk, b);
+    if (!named_bar_any(1, DS_WARPS * 32, !got) && last && warp == 0) {
+      if (elect_one()) {
+        store_tile<D>(&maps.dv, sb + L::OFF_Q, k0, hk, b);
+        store_tile<D>(&maps.dk, sb + L::OFF_O, k0, hk, b);
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
@@ -502,7 +537,8 @@ __device__ __forceinline__ void ds32(const uint32_t (&a)[32], const uint32_t (&d
 template <int D>
 __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __restrict__ row_s,
                                         const uint4* __restrict__ row_d, int padded, int* status, const BwdMaps& maps,
-                                        const unsigned blk, const int longest_first) {
+                                        const AttnBwdPlan& plan, const unsigned blk, float4* __restrict__ part_acc,
+                                        unsigned* __restrict__ counters) {
   using L = qq::Smem<D>;
   using qq::K_SLOTS;
   using qq::V_SLOTS;
@@ -511,66 +547,72 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = (p.NQ + BT - 1) / BT;
+  const TilePart part = tile_part(blk, plan.q_whole, plan.q_parts);
   const int heads = p.B * p.H;
-  const int bh = longest_first ? (int)(blk % heads) : (int)(blk / n_qt);
+  const int bh = plan.longest_first ? part.tile % heads : part.tile / n_qt;
   const int b = bh / p.H, h = bh % p.H, hk = h / p.G;
   // the last query tiles, which see the most keys, first
-  const int q0 = (n_qt - 1 - (longest_first ? (int)(blk / heads) : (int)(blk % n_qt))) * BT;
+  const int q0 = (n_qt - 1 - (plan.longest_first ? part.tile / heads : part.tile % n_qt)) * BT;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int last = min(q0 + BT, ql) - 1;
   const int end = q0 < ql ? (p.causal ? min(kl, last + off + 1) : kl) : 0;
-  const int n = end > 0 ? (end + BT - 1) / BT : 0;
-  const int patch_j = (kl < p.NK && (kl & (BT - 1))) ? kl / BT : -1;  // the K tile with rows past the sequence
+  const int tiles = end > 0 ? (end + BT - 1) / BT : 0;
+  const int j0 = part.from(tiles), n = part.from(tiles, 1) - j0;  // this block takes the key tiles [j0, j0 + n)
+  const int patch_j = (kl < p.NK && (kl & (BT - 1))) ? kl / BT - j0 : -1;  // the K tile with rows past the sequence
 
   const uint32_t bar = sb + L::OFF_BAR;
   const uint32_t x_full = bar, k_full = bar + 8, k_empty = bar + 32, v_full = bar + 56, v_empty = bar + 72,
                  s_full = bar + 88, s_free = bar + 96, ds_full = bar + 104, ds_free = bar + 120, g_done = bar + 136,
                  to_patch = bar + 144, patched = bar + 152, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+  volatile int* part_flag = abort_flag + 1;
   // the producer sets the barriers up and issues the first loads while the others get TMEM
   auto load_k = [&](int j) {
     const int s = j % K_SLOTS;
     mbar_arrive_expect_tx(k_full + 8 * s, L::TILE);
 #pragma unroll
     for (int d = 0; d < D / 64; ++d)
-      tma_load_4d(sb + L::OFF_K + s * L::TILE + d * BT * 128, &maps.k, k_full + 8 * s, d * 64, j * BT, hk, b);
+      tma_load_4d(sb + L::OFF_K + s * L::TILE + d * BT * 128, &maps.k, k_full + 8 * s, d * 64, (j0 + j) * BT, hk, b);
   };
   auto load_v = [&](int j) {
     const int s = j % V_SLOTS;
     mbar_arrive_expect_tx(v_full + 8 * s, L::TILE);
 #pragma unroll
     for (int d = 0; d < D / 64; ++d)
-      tma_load_4d(sb + L::OFF_V + s * L::TILE + d * BT * 128, &maps.v, v_full + 8 * s, d * 64, j * BT, hk, b);
+      tma_load_4d(sb + L::OFF_V + s * L::TILE + d * BT * 128, &maps.v, v_full + 8 * s, d * 64, (j0 + j) * BT, hk, b);
   };
-  if (warp == PRODUCER_WARP && lane == 0) {
-    mbar_init(x_full, 1);
-    for (int s = 0; s < K_SLOTS; ++s) {
-      mbar_init(k_full + 8 * s, 1);
-      mbar_init(k_empty + 8 * s, 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(v_full + 8 * s, 1);
-      mbar_init(v_empty + 8 * s, 1);
-      mbar_init(ds_full + 8 * s, DS_WARPS);
-      mbar_init(ds_free + 8 * s, 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, DS_WARPS);
-    mbar_init(g_done, 1);
-    mbar_init(to_patch, 1);
-    mbar_init(patched, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    if (n > 0) {
-      mbar_arrive_expect_tx(x_full, 2 * L::TILE);
+  if (warp == PRODUCER_WARP) {
+    if (elect_one()) {
+      mbar_init(x_full, 1);
+      for (int s = 0; s < K_SLOTS; ++s) {
+        mbar_init(k_full + 8 * s, 1);
+        mbar_init(k_empty + 8 * s, 1);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(v_full + 8 * s, 1);
+        mbar_init(v_empty + 8 * s, 1);
+        mbar_init(ds_full + 8 * s, DS_WARPS);
+        mbar_init(ds_free + 8 * s, 1);
+      }
+      mbar_init(s_full, 1);
+      mbar_init(s_free, DS_WARPS);
+      mbar_init(g_done, 1);
+      mbar_init(to_patch, 1);
+      mbar_init(patched, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      if (n > 0) {
+        mbar_arrive_expect_tx(x_full, 2 * L::TILE);
 #pragma unroll
-      for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
-      load_k(0);
+        for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
+        load_k(0);
 #pragma unroll
-      for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
-      load_v(0);
+        for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
+        load_v(0);
+      }
     }
+    __syncwarp();  // the warp's other lanes wait for the one that issues
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -584,7 +626,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
   if (warp >= DS_WARPS) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         int issued_k = 1, issued_v = 1;
         for (int j = 1; j < n; ++j) {
           const int sk = j % K_SLOTS, sv = j % V_SLOTS;
@@ -681,7 +723,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
-      const int seen = row_end - (j * BT + grp * 32);
+      const int seen = row_end - ((j0 + j) * BT + grp * 32);
       const bool masked = __any_sync(0xffffffffu, seen < 32);
       uint32_t a[32], d[32], pk[16];
       tmem_ld32(tcol + qq::kColS, a);
@@ -713,14 +755,22 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
       got = mbar_wait_warp(g_done, 0, status, abort_flag);
       __syncwarp();
     }
-    if (got && grp * 32 < D) {
+    const bool cols = grp * 32 < D;
+    uint32_t g[32] = {};
+    if (got && cols && n > 0) {
       tc_fence_after();
-      uint32_t g[32];
-      if (n > 0) {
-        tmem_ld32(tmem + lanes + qq::kColG + grp * 32, g);
-        tmem_ld_wait();
-        reg_fence32(g);
-      }
+      tmem_ld32(tmem + lanes + qq::kColG + grp * 32, g);
+      tmem_ld_wait();
+      reg_fence32(g);
+    }
+    bool last = true;
+    if (part.parts > 1) {
+      float4* mine = part_acc + (size_t)(part.tile - plan.q_whole) * part.parts * (D / 4 * BT);
+      if (cols) part_put<D>(mine, part.rank, r, grp * 32, g);
+      last = part_last(counters + (part.tile - plan.q_whole), part.parts, DS_WARPS * 32, part_flag);
+      if (last && cols) part_sum<D>(mine, part.parts, r, grp * 32, g);
+    }
+    if (got && last && cols) {
       if (row_end <= 0) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) g[i] = 0u;
@@ -729,8 +779,10 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
       fence_async_smem();
     }
     // every warp comes here; one that gave up makes none of them store
-    if (!named_bar_any(1, DS_WARPS * 32, !got) && threadIdx.x == 0)
-      store_tile<D>(&maps.dq, sb + L::OFF_K, q0, h, b);
+    if (!named_bar_any(1, DS_WARPS * 32, !got) && last && warp == 0) {
+      if (elect_one()) store_tile<D>(&maps.dq, sb + L::OFF_K, q0, h, b);
+      __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -743,15 +795,16 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_bwd_kernel(const AttnProblem p, const uint4* __restrict__ row_s, const uint4* __restrict__ row_d, int padded,
-                    int* status, const __grid_constant__ BwdMaps maps, const unsigned n_first, const int q_first,
-                    const int longest_first) {
-  const unsigned x = blockIdx.x;
-  const bool is_q = q_first ? x < n_first : x >= n_first;
-  const unsigned blk = x < n_first ? x : x - n_first;
+                    int* status, const __grid_constant__ BwdMaps maps, const AttnBwdPlan plan,
+                    float4* __restrict__ kv_parts, unsigned* __restrict__ kv_counters, float4* __restrict__ q_parts,
+                    unsigned* __restrict__ q_counters) {
+  const unsigned x = blockIdx.x, first = plan.q_first ? plan.q_blocks : plan.kv_blocks;
+  const bool is_q = plan.q_first ? x < first : x >= first;
+  const unsigned blk = x < first ? x : x - first;
   if (is_q)
-    q_block<D>(p, row_s, row_d, padded, status, maps, blk, longest_first);
+    q_block<D>(p, row_s, row_d, padded, status, maps, plan, blk, q_parts, q_counters);
   else
-    kv_block<D>(p, row_s, row_d, padded, status, maps, blk, longest_first);
+    kv_block<D>(p, row_s, row_d, padded, status, maps, plan, blk, kv_parts, kv_counters);
 }
 
 // Zeros for `rows` rows of each of B H heads (a backward without queries or without keys).
@@ -761,27 +814,18 @@ __global__ void attn_zero_rows_kernel(__nv_bfloat16* dst, int H, int rows, int D
   dst[r / rows / H * sb + r / rows % H * sh + r % rows * sn + threadIdx.x] = __float2bfloat16_rn(0.f);
 }
 
-// In a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for).
-constexpr int kSmallGrid = 6;
-
 template <int D>
-cudaError_t launch_d(const AttnProblem& p, bool fused, const AttnBwdIn& in, void* dq, void* dk, void* dv, void* workspace,
-                     int num_sms, int* status, cudaStream_t st) {
-  const int padded = (p.NQ + BT - 1) / BT * BT;
-  const long long rows = (long long)p.B * p.H * padded;
-  uint4* row_s = static_cast<uint4*>(workspace);
-  uint4* row_d = row_s + rows;
-  float* acc = fused ? reinterpret_cast<float*>(row_d + rows) : nullptr;
+cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk, void* dv,
+                     void* workspace, int* status, cudaStream_t st) {
+  const AttnBwdScratch w = attn_bwd_scratch(p, plan, workspace);
+  const long long rows = (long long)p.B * p.H * w.padded;
+  auto *row_s = static_cast<uint4*>(w.row_s), *row_d = static_cast<uint4*>(w.row_d);
   constexpr int row_lanes = D / 8, per_block = 256 / row_lanes;
   attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
-      p, in, row_s, row_d, reinterpret_cast<float4*>(acc), padded);
+      p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc), w.kv_counters, w.n_counters, w.padded);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const long long q_blocks = (long long)p.B * p.H * (padded / BT);
-  const long long kv_blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
-  if (fused)
-    return launch_attn_bwd_fused(p, in, dq, dk, dv, row_s, row_d, acc, padded, kv_blocks <= kSmallGrid * num_sms, status,
-                                 st);
+  if (plan.fused) return launch_attn_bwd_fused(p, plan, in, dq, dk, dv, w, status, st);
   BwdMaps m;
   auto q_map = [&](CUtensorMap* map, const void* x, long long sn, long long sh, long long sb) {
     return encode_tile_map(map, x, p.D, p.NQ, p.H, p.B, sn, sh, sb, BT);
@@ -799,30 +843,111 @@ cudaError_t launch_d(const AttnProblem& p, bool fused, const AttnBwdIn& in, void
   if (qq::Smem<D>::BYTES > smem) smem = qq::Smem<D>::BYTES;
   auto kern = attn_bwd_kernel<D>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  // a dQ block walks the keys with three products a tile, a dK/dV block the queries of G heads with four
-  const int q_first = 3ll * p.NK > 4ll * p.G * p.NQ;
-  kern<<<(unsigned)(q_blocks + kv_blocks), THREADS, smem, st>>>(p, row_s, row_d, padded, status, m,
-                                                                (unsigned)(q_first ? q_blocks : kv_blocks), q_first,
-                                                                q_blocks + kv_blocks <= kSmallGrid * num_sms);
+  kern<<<plan.q_blocks + plan.kv_blocks, THREADS, smem, st>>>(
+      p, row_s, row_d, w.padded, status, m, plan, static_cast<float4*>(w.kv_parts), w.kv_counters,
+      static_cast<float4*>(w.q_parts), w.q_counters);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-bool attn_bwd_fused(const AttnProblem& p, int mode, int num_sms) {
-  if (p.NQ == 0 || p.NK == 0) return false;
-  if (mode) return mode == 1;  // STREAMKL_BWD_FUSED
-  return (long long)p.B * p.HK * ((p.NK + BT - 1) / BT) >= num_sms;
+bool attn_bwd_has_fused(const AttnProblem& p) { return p.D == 64; }
+
+// The plan.  Lengths are in products of a tile pair: a dK/dV block does four for each query tile of its G heads, a dQ
+// block three for each key tile, a fused one five; setting a block up, filling its pipeline and storing its tile take as
+// long as about kBlockCost more.
+//   separate  of the ways to deal both kinds' tiles out over 1 to 8 parts each, one whose larger of the longest block and
+//             the SMs' share of all is clearly smallest; a part's trip through the workspace costs kPartCost more.
+//             Measured, us without and with parts: B1 H4 HK1 N4096 D128 causal 186 / 68, B1 H16 HK4 N2048 D64 causal 89 /
+//             60, B1 H8 HK1 N512 D128 53 / 30; where the rule leaves them whole: B1 H32 HK8 N2048 D128 causal 119 / 133,
+//             B1 H32 N_Q128 N_K64K D128 866 / 910.
+//   fused     the tiles of the last, incomplete wave are dealt out so that it fills the SMs (non-causal: a causal grid's
+//             short blocks fill the end by themselves).
+// In a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for).
+constexpr int kBlockCost = 16, kPartCost = 8;
+constexpr int kMaxParts = 8;
+constexpr int kMinPartTiles = 4;
+constexpr int kSmallGrid = 6;
+
+AttnBwdPlan attn_bwd_plan(const AttnProblem& p, int mode, int num_sms) {
+  const int nq = (p.NQ + BT - 1) / BT, nk = (p.NK + BT - 1) / BT;
+  AttnBwdPlan g{};
+  g.kv_tiles = (unsigned)((long long)p.B * p.HK * nk);
+  g.q_tiles = (unsigned)((long long)p.B * p.H * nq);
+  g.kv_parts = g.q_parts = 1;
+  if (nq == 0 || nk == 0) return g;
+  const long long stream = (long long)p.G * nq;  // tiles a dK/dV block streams
+  // STREAMKL_BWD_AUTO, 0: fused where it exists and its blocks fill the SMs
+  g.fused = attn_bwd_has_fused(p) && (mode == 1 || (mode == 0 && g.kv_tiles >= (unsigned)num_sms));
+  if (g.fused) {
+    g.q_tiles = 0;
+    const unsigned tail = g.kv_tiles % num_sms;
+    g.kv_whole = g.kv_tiles;
+    if (tail && (!p.causal || g.kv_tiles < (unsigned)num_sms)) {
+      long long parts = num_sms / tail;
+      if (parts > kMaxParts) parts = kMaxParts;
+      if (parts > stream / kMinPartTiles) parts = stream / kMinPartTiles;
+      if (parts > 1) {
+        g.kv_whole = g.kv_tiles - tail;
+        g.kv_parts = (int)parts;
+      }
+    }
+  } else {
+    const double mean = p.causal ? 0.5 : 1.0;
+    double best = 0;
+    int best_kv = 1, best_q = 1;
+    for (int a = 1; a <= kMaxParts; ++a) {
+      if (a > 1 && stream / a < kMinPartTiles) break;
+      for (int b = 1; b <= kMaxParts; ++b) {
+        if (b > 1 && nk / b < kMinPartTiles) break;
+        const double kv = 4.0 * stream / a, q = 3.0 * nk / b;
+        const double kv_cost = kBlockCost + (a > 1 ? kPartCost : 0), q_cost = kBlockCost + (b > 1 ? kPartCost : 0);
+        const double longest = kv + kv_cost > q + q_cost ? kv + kv_cost : q + q_cost;
+        const double all = (g.kv_tiles * a * (mean * kv + kv_cost) + g.q_tiles * b * (mean * q + q_cost)) / num_sms;
+        const double cost = longest > all ? longest : all;
+        if (best == 0 || cost < best * 0.85) {  // more parts only for a clear gain
+          best = cost;
+          best_kv = a;
+          best_q = b;
+        }
+      }
+    }
+    g.kv_parts = best_kv;
+    g.q_parts = best_q;
+    g.kv_whole = best_kv > 1 ? 0 : g.kv_tiles;
+    g.q_whole = best_q > 1 ? 0 : g.q_tiles;
+  }
+  g.kv_blocks = g.kv_whole + (g.kv_tiles - g.kv_whole) * g.kv_parts;
+  g.q_blocks = g.q_whole + (g.q_tiles - g.q_whole) * g.q_parts;
+  g.longest_first = (long long)g.kv_blocks + g.q_blocks <= (long long)kSmallGrid * num_sms;
+  g.q_first = 3.0 * nk / g.q_parts > 4.0 * stream / g.kv_parts;
+  return g;
 }
 
-size_t attn_bwd_workspace(const AttnProblem& p, bool fused) {
-  if (p.NQ == 0 || p.NK == 0) return 0;
-  const size_t rows = (size_t)p.B * p.H * ((p.NQ + BT - 1) / BT * BT);
-  return rows * (2 * sizeof(uint4) + (fused ? p.D * sizeof(float) : 0));
+AttnBwdScratch attn_bwd_scratch(const AttnProblem& p, const AttnBwdPlan& plan, void* workspace) {
+  AttnBwdScratch w{};
+  w.padded = (p.NQ + BT - 1) / BT * BT;
+  if (p.NQ == 0 || p.NK == 0) return w;
+  const size_t rows = (size_t)p.B * p.H * w.padded;
+  const size_t kv_split = plan.kv_tiles - plan.kv_whole, q_split = plan.q_tiles - plan.q_whole;
+  auto take = [&](size_t bytes) {
+    void* at = static_cast<char*>(workspace) + w.bytes;
+    w.bytes += (bytes + 15) / 16 * 16;
+    return at;
+  };
+  w.row_s = take(rows * 16);
+  w.row_d = take(rows * 16);
+  if (plan.fused) w.acc = static_cast<float*>(take(rows * p.D * sizeof(float)));
+  w.kv_parts = take(kv_split * plan.kv_parts * 2 * p.D * BT * sizeof(float));
+  w.q_parts = take(q_split * plan.q_parts * p.D * BT * sizeof(float));
+  w.n_counters = (unsigned)(kv_split + q_split);
+  w.kv_counters = static_cast<unsigned*>(take(w.n_counters * sizeof(unsigned)));
+  w.q_counters = w.kv_counters + kv_split;
+  return w;
 }
 
-cudaError_t launch_attn_bwd(const AttnProblem& p, bool fused, const AttnBwdIn& in, void* dq, void* dk, void* dv,
-                            void* workspace, int num_sms, int* status, cudaStream_t st) {
+cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk,
+                            void* dv, void* workspace, int* status, cudaStream_t st) {
   if (p.NQ == 0 || p.NK == 0) {
     auto* q = static_cast<__nv_bfloat16*>(dq);
     auto* k = static_cast<__nv_bfloat16*>(dk);
@@ -837,8 +962,8 @@ cudaError_t launch_attn_bwd(const AttnProblem& p, bool fused, const AttnBwdIn& i
     }
     return cudaGetLastError();
   }
-  if (p.D == 64) return launch_d<64>(p, fused, in, dq, dk, dv, workspace, num_sms, status, st);
-  return launch_d<128>(p, fused, in, dq, dk, dv, workspace, num_sms, status, st);
+  if (p.D == 64) return launch_d<64>(p, plan, in, dq, dk, dv, workspace, status, st);
+  return launch_d<128>(p, plan, in, dq, dk, dv, workspace, status, st);
 }
 
 }  // namespace skl

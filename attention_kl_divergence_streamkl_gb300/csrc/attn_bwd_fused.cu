@@ -1,80 +1,67 @@
-// Attention backward, fused: every tile pair is visited once and gives its share
-// of dK, dV and dQ -- five products a tile pair where the separate blocks
-// (attn_bwd.cu, which states the mathematics) need seven, and one exp instead of
-// two.  Its price: a block owns 128 keys, so dQ is added up over the blocks of
-// a head, in fp32 by bulk reductions into an accumulator that lies in L2 while a
-// head is worked on.  The order of those additions is not fixed: the last bits
-// of dQ can differ between runs (dK and dV do not).
+// Attention backward, fused, for D = 64: every tile pair is visited once and
+// gives its share of dK, dV and dQ -- five products a tile pair where the separate
+// blocks (attn_bwd.cu, which states the mathematics) need seven, and one exp
+// instead of two.  Its price: a block owns 128 keys, so dQ is added up over the
+// blocks of a head, in fp32 by bulk reductions into an accumulator that lies in L2
+// while a head is worked on.  The order of those additions is not fixed: the last
+// bits of dQ can differ between runs (dK and dV do not).
 //
-//   S^T = K Q^T - LSE / scale, dP^T = V dO^T - delta   (lanes = keys; a ninth K step adds the rows' values)
+//   S^T = K Q^T - LSE / scale, dP^T = V dO^T - delta   (lanes = keys; a K step more adds the rows' values)
 //   P^T = 2^(c S^T) as bf16 pairs over its logits in TMEM:  dV += P^T dO
-//   dS^T = P^T dP^T as bf16 in shared memory [key][query]:   dK += dS^T Q (K-major A)
-//                                                            dQ = dS K    (the same bytes as an MN-major A)
-// TMEM at D = 128: S/P [0,128), dP and then dQ [128,256), dV [256,384), dK [384,512).  dQ takes dP's columns once
-// the warps hold dP, and four warps empty them into registers at once, so that dP of the next tile can follow; they
-// then stage it 32 columns at a time and issue the reductions.
-// At D = 64: S/P [0,128), dP/dS [128,256), dV, dK, dQ 64 columns each from 256 on, and K and V as bf16 pairs in the last
-// 64: they are the A operands of S and dP, and dS in TMEM that of dK.  Read from shared memory, operands, dS and the
-// staged dQ come to 324 KB a tile pair, 2500 cycles at 128 bytes a clock; so they are 230 KB.
-//   dS warps     thread = key; 8 of them take 64 queries each (D = 128), or 16 take 32 (D = 64, where their
-//                latency is what bounds a tile pair and registers allow it)
-//   4 dQ warps   TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
-//   then         TMA producer: K, V once; Q(u) and dO(u) with their rows' values
-//                TMEM owner and MMA issuer: dV(u), S(u+1), dQ(u), dK(u), dP(u+1)
-//                a warp that clears rows past a sequence's lengths in K, V, Q and dO tiles
-// The five products take 2700 cycles a tile pair at D = 128, the reductions (64 KB a tile pair at the 24 bytes a clock
-// that an SM gets from the L2's adders) about as many.
+//   dS^T = P^T dP^T as bf16 pairs over dP in TMEM:          dK += dS^T Q
+//          and in shared memory [key][query]:               dQ = dS K (MN-major A)
+// TMEM: S/P [0,128), dP/dS [128,256), dV, dK, dQ 64 columns each from 256 on, and K and V as bf16 pairs in the last 64,
+// the A operands of S and dP.  Shared-memory traffic is what bounds a tile pair: with every operand read from there it
+// was 324 KB, 2500 of 2800 cycles at 128 bytes a clock; so it is 230 KB.
+//   warps 0-15   thread = key, group g = warp / 4 takes queries [32g, 32g + 32)
+//   warps 16-19  dQ: TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
+//   warp 20      TMA producer: K, V once; Q(u) and dO(u) with their rows' values
+//   warp 21      TMEM owner and MMA issuer: dV(u), S(u+1), dK(u), dP(u+1), dQ(u)
+//   warp 22      clears rows past a sequence's lengths in K, V, Q and dO tiles
+// At D = 128 the same kernel (built, measured, not kept) has 532 KB of shared-memory traffic a tile pair, dQ's staging
+// and reductions 128 KB of it: 4450 cycles against 4460 for the separate blocks' two visits (B2 H32 HK8 N4096 causal
+// 0.69 against 0.68 ms).  At D = 64: 8 heads, N8192, non-causal 0.39 against 0.44 ms.
 #include "attn.cuh"
 
 namespace skl {
 namespace {
 
 constexpr int BT = 128;
-constexpr int DQ_WARPS = 4;
+constexpr int D = 64;
+constexpr int DS_WARPS = 16, DQ_WARPS = 4;
+constexpr int PRODUCER_WARP = 20, MMA_WARP = 21, PATCH_WARP = 22;
+constexpr int THREADS = 24 * 32;
+constexpr int kRegsDs = 80, kRegsDq = 88, kRegsOther = 72;  // 512 * 80 + 128 * 88 + 128 * 72 = 768 * 80 at launch
 constexpr uint32_t kTmemCols = 512;
 
 struct Maps {
   CUtensorMap q, k, v, go, dk, dv, acc;  // acc: fp32 [B H][padded rows][D], boxes of a staging chunk
 };
 
-// Warps, in warpgroups, and their registers (the sums are what the launch has).
-template <int D>
-struct Cfg {
-  static constexpr int DS_WARPS = D == 128 ? 8 : 16;
-  static constexpr int COLS = 128 * 4 / DS_WARPS;  // queries of a dS thread
-  static constexpr int PRODUCER_WARP = DS_WARPS + DQ_WARPS, MMA_WARP = PRODUCER_WARP + 1, PATCH_WARP = PRODUCER_WARP + 2;
-  static constexpr int THREADS = 32 * (PRODUCER_WARP + 4);
-  // D = 128: 256 * 136 + 128 * 136 + 128 * 104 = 512 * 128;  D = 64: 512 * 80 + 128 * 88 + 128 * 72 = 768 * 80
-  static constexpr int kRegsDs = D == 128 ? 136 : 80, kRegsDq = D == 128 ? 136 : 88, kRegsOther = D == 128 ? 104 : 72;
-};
+constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 320, kQ = 384, kTK = 448, kTV = 480;  // TMEM columns
+constexpr int SLOTS = 2;                                                                 // of Q and of dO tiles
+// A dQ warp's staging ring: chunks of 32 rows x 32 columns.  What is on its way to L2 bounds the reductions' rate (24
+// bytes a clock with a latency of 1000 to 1500).
+constexpr int RING = 4, CHUNK_BYTES = 32 * 32 * 4;
 
-template <int D>
 struct Smem {
-  static constexpr bool ALIAS = D == 128;  // dQ in dP's columns
-  // a dQ warp's staging ring: chunks of 32 rows x CHUNK columns.  What is on its way to L2 bounds the reductions' rate
-  // (24 bytes a clock with a latency of 1000 to 1500): 24 KB is what D = 128 leaves, in chunks of 2 KB
-  static constexpr int CHUNK = D == 128 ? 16 : 32, RING = D == 128 ? 3 : 4;
-  static constexpr int CHUNK_BYTES = 32 * CHUNK * 4;
-  static constexpr int Q_SLOTS = 2, O_SLOTS = D == 128 ? 1 : 2;
-  static constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D, kQ = ALIAS ? kP : 256 + 2 * D;
-  static constexpr uint32_t kTK = 448, kTV = 480;  // D = 64: K and V in TMEM
   static constexpr int TILE = BT * D * 2;
   static constexpr int OFF_K = 0, OFF_V = TILE, OFF_Q = 2 * TILE;
-  static constexpr int OFF_O = OFF_Q + Q_SLOTS * TILE;
-  static constexpr int OFF_DS = OFF_O + O_SLOTS * TILE;    // [128 keys][128 queries] bf16, two halves
+  static constexpr int OFF_O = OFF_Q + SLOTS * TILE;
+  static constexpr int OFF_DS = OFF_O + SLOTS * TILE;      // [128 keys][128 queries] bf16, two halves
   static constexpr int OFF_STAGE = OFF_DS + BT * BT * 2;   // the dQ warps' rings
   static constexpr int STEP = 128 * 16;                    // rows' values of a tile
   static constexpr int OFF_RS = OFF_STAGE + DQ_WARPS * RING * CHUNK_BYTES;
-  static constexpr int OFF_RD = OFF_RS + Q_SLOTS * STEP;
-  static constexpr int OFF_ONES = OFF_RD + O_SLOTS * STEP;
+  static constexpr int OFF_RD = OFF_RS + SLOTS * STEP;
+  static constexpr int OFF_ONES = OFF_RD + SLOTS * STEP;
   static constexpr int OFF_ZERO = OFF_ONES + STEP;
   static constexpr int OFF_BAR = OFF_ZERO + STEP;
   // kv_full, kv_patched, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, ds_free, dq_full,
-  // dq_free, g_done, to_patch, patched, kv_tmem; TMEM slot, abort flag
+  // dq_free, g_done, to_patch, patched, kv_tmem; TMEM slot, abort flag, part flag
   static constexpr int BAR_SLOT = 8 * 21;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16;
 };
-static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+static_assert(Smem::BYTES <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -83,28 +70,27 @@ __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t s
                : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     attn_bwd_fused_kernel(const AttnProblem p, const uint4* __restrict__ row_s, const uint4* __restrict__ row_d, int padded,
-                          int* status, const __grid_constant__ Maps maps, const int longest_first) {
-  using L = Smem<D>;
-  using C = Cfg<D>;
-  constexpr int QS = L::Q_SLOTS, OS = L::O_SLOTS, DS_WARPS = C::DS_WARPS, PRODUCER_WARP = C::PRODUCER_WARP,
-                MMA_WARP = C::MMA_WARP, PATCH_WARP = C::PATCH_WARP;
+                          int* status, const __grid_constant__ Maps maps, const AttnBwdPlan plan, float4* __restrict__ part_acc,
+                          unsigned* __restrict__ counters) {
+  using L = Smem;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles' alignment; nothing lies before it
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // heads in order (the blocks in flight share one key head's query tiles and dQ rows in L2); within a head the first
   // key tiles, which see the most queries under a causal mask, first.  A small grid: the first key tiles of all heads
+  const TilePart part = tile_part(blockIdx.x, plan.kv_whole, plan.kv_parts);
   const int n_kt = (p.NK + BT - 1) / BT, heads = p.B * p.HK;
-  const int bhk = longest_first ? (int)(blockIdx.x % heads) : (int)(blockIdx.x / n_kt);
+  const int bhk = plan.longest_first ? part.tile % heads : part.tile / n_kt;
   const int b = bhk / p.HK, hk = bhk % p.HK;
-  const int k0 = (longest_first ? (int)(blockIdx.x / heads) : (int)(blockIdx.x % n_kt)) * BT;
+  const int k0 = (plan.longest_first ? part.tile / heads : part.tile % n_kt) * BT;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
   const int n_qt = (k0 < kl && q_begin < ql) ? (ql - q_begin + BT - 1) / BT : 0;
-  const int n = p.G * n_qt;  // tile u: head u / n_qt of the group, query tile u % n_qt
+  // tile u: head u / n_qt of the group, query tile u % n_qt; this block takes the tiles [u0, u0 + n)
+  const int u0 = part.from(p.G * n_qt), n = part.from(p.G * n_qt, 1) - u0;
   const bool ragged_q = n > 0 && ql < p.NQ && (ql & (BT - 1));  // the last query tile has rows past the sequence
   const bool ragged_k = n > 0 && kl < p.NK && kl - k0 < BT;     // so has this key tile
 
@@ -114,6 +100,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                  ds_free = bar + 112, dq_full = bar + 120, dq_free = bar + 128, g_done = bar + 136, to_patch = bar + 144,
                  patched = bar + 152, kv_tmem = bar + 160, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
+  volatile int* part_flag = abort_flag + 1;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     mbar_init(kv_patched, 1);
@@ -152,9 +139,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
 
   if (warp >= PRODUCER_WARP) {
-    setmaxnreg_dec<C::kRegsOther>();
+    setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -163,26 +150,26 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         int issued_q = 0, issued_o = 0;
         for (int u = 0; u < n; ++u) {
-          const int sq = u % QS, so = u % OS, hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+          const int s = u % SLOTS, hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
           const long long row = ((long long)b * p.H + hq) * padded + q0;
-          if (u >= QS && !mbar_wait(q_empty + 8 * sq, ((u / QS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(q_full + 8 * sq, L::TILE + L::STEP);
+          if (u >= SLOTS && !mbar_wait(q_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_Q + sq * L::TILE + h * BT * 128, &maps.q, q_full + 8 * sq, h * 64, q0, hq, b);
-          bulk_load(sb + L::OFF_RS + sq * L::STEP, row_s + row, L::STEP, q_full + 8 * sq);
+            tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &maps.q, q_full + 8 * s, h * 64, q0, hq, b);
+          bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + row, L::STEP, q_full + 8 * s);
           issued_q = u + 1;
-          if (u >= OS && !mbar_wait(o_empty + 8 * so, ((u / OS) - 1) & 1, status, abort_flag)) break;
-          mbar_arrive_expect_tx(o_full + 8 * so, L::TILE + L::STEP);
+          if (u >= SLOTS && !mbar_wait(o_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
+          mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sb + L::OFF_O + so * L::TILE + h * BT * 128, &maps.go, o_full + 8 * so, h * 64, q0, hq, b);
-          bulk_load(sb + L::OFF_RD + so * L::STEP, row_d + row, L::STEP, o_full + 8 * so);
+            tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &maps.go, o_full + 8 * s, h * 64, q0, hq, b);
+          bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + row, L::STEP, o_full + 8 * s);
           issued_o = u + 1;
         }
         mbar_drain(kv_full, 0, status);
-        for (int u = max(0, issued_q - QS); u < issued_q; ++u) mbar_drain(q_full + 8 * (u % QS), (u / QS) & 1, status);
-        for (int u = max(0, issued_o - OS); u < issued_o; ++u) mbar_drain(o_full + 8 * (u % OS), (u / OS) & 1, status);
+        for (int u = max(0, issued_q - SLOTS); u < issued_q; ++u) mbar_drain(q_full + 8 * (u % SLOTS), (u / SLOTS) & 1, status);
+        for (int u = max(0, issued_o - SLOTS); u < issued_o; ++u) mbar_drain(o_full + 8 * (u % SLOTS), (u / SLOTS) & 1, status);
       }
       __syncwarp();
     } else if (warp == PATCH_WARP) {
@@ -201,11 +188,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           if (lane == 0) mbar_arrive(kv_patched);
         }
       }
-      // for each head of the group: its last Q tile, then its last dO tile, when the MMA thread has seen them land
-      for (int e = 0; ok && ragged_q && e < 2 * p.G; ++e) {
+      // for each head's last tile: its Q, then its dO, when the MMA thread has seen them land
+      const int first = n > 0 ? n_qt - 1 - u0 % n_qt : 0;  // the first of this block's tiles that is a head's last
+      for (int e = 0; ok && ragged_q && first + e / 2 * n_qt < n; ++e) {
         if (!(ok = mbar_wait_warp(to_patch, e & 1, status, abort_flag))) break;
-        const int u = (e / 2 + 1) * n_qt - 1;
-        clear(sb + ((e & 1) ? L::OFF_O + u % OS * L::TILE : L::OFF_Q + u % QS * L::TILE), ql & (BT - 1));
+        const int u = first + e / 2 * n_qt;
+        clear(sb + ((e & 1) ? L::OFF_O + u % SLOTS * L::TILE : L::OFF_Q + u % SLOTS * L::TILE), ql & (BT - 1));
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(patched);
@@ -216,97 +204,72 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         constexpr uint32_t id_s = idesc_bf16(BT, BT, false, false);
         constexpr uint32_t id_g = idesc_bf16(BT, D, false, true);
         constexpr uint32_t id_q = idesc_bf16(BT, D, true, true);
-        const uint64_t kd = sdesc_sw128(sb + L::OFF_K, 0, 1024), vd = sdesc_sw128(sb + L::OFF_V, 0, 1024);
         const uint64_t kmn = sdesc_sw128(sb + L::OFF_K, BT * 128, 1024);
-        const uint64_t dsk = sdesc_sw128(sb + L::OFF_DS, 0, 1024), dsmn = sdesc_sw128(sb + L::OFF_DS, BT * 128, 1024);
+        const uint64_t dsmn = sdesc_sw128(sb + L::OFF_DS, BT * 128, 1024);
         const uint64_t ones = sdesc_step(sb + L::OFF_ONES, sb + L::OFF_ZERO);
         int patches = 0;
         auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
-          if (!ragged_q || (u + 1) % n_qt) return true;
+          if (!ragged_q || (u0 + u + 1) % n_qt) return true;
           mbar_arrive(to_patch);
           return mbar_wait(patched, patches++ & 1, status, abort_flag);
         };
         auto issue_s = [&](int u) {  // S^T(u)
-          const int s = u % QS;
-          if (!mbar_wait(q_full + 8 * s, (u / QS) & 1, status, abort_flag) || !patch(u)) return false;
+          const int s = u % SLOTS;
+          if (!mbar_wait(q_full + 8 * s, (u / SLOTS) & 1, status, abort_flag) || !patch(u)) return false;
           tc_fence_after();
           const uint64_t qd = sdesc_sw128(sb + L::OFF_Q + s * L::TILE, 0, 1024);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
-            if (L::ALIAS)
-              mma_ss(tmem + L::kS, sdesc_add(kd, o), sdesc_add(qd, o), id_s, ks > 0);
-            else
-              mma_ts(tmem + L::kS, tmem + L::kTK + 8 * ks, sdesc_add(qd, o), id_s, ks > 0);
+            mma_ts(tmem + kS, tmem + kTK + 8 * ks, sdesc_add(qd, o), id_s, ks > 0);
           }
-          mma_ss(tmem + L::kS, ones, sdesc_step(sb + L::OFF_RS + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
+          mma_ss(tmem + kS, ones, sdesc_step(sb + L::OFF_RS + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
           mma_commit(s_full);
           return true;
         };
         auto issue_dp = [&](int u) {  // dP^T(u)
-          const int s = u % OS;
-          if (!mbar_wait(o_full + 8 * s, (u / OS) & 1, status, abort_flag) || !patch(u)) return false;
+          const int s = u % SLOTS;
+          if (!mbar_wait(o_full + 8 * s, (u / SLOTS) & 1, status, abort_flag) || !patch(u)) return false;
           tc_fence_after();
           const uint64_t od = sdesc_sw128(sb + L::OFF_O + s * L::TILE, 0, 1024);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = (ks >> 2) * (BT * 128) + (ks & 3) * 32;
-            if (L::ALIAS)
-              mma_ss(tmem + L::kP, sdesc_add(vd, o), sdesc_add(od, o), id_s, ks > 0);
-            else
-              mma_ts(tmem + L::kP, tmem + L::kTV + 8 * ks, sdesc_add(od, o), id_s, ks > 0);
+            mma_ts(tmem + kP, tmem + kTV + 8 * ks, sdesc_add(od, o), id_s, ks > 0);
           }
-          mma_ss(tmem + L::kP, ones, sdesc_step(sb + L::OFF_RD + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
+          mma_ss(tmem + kP, ones, sdesc_step(sb + L::OFF_RD + s * L::STEP, sb + L::OFF_ZERO), id_s, true);
           mma_commit(dp_full);
           return true;
         };
         bool ok = mbar_wait(kv_full, 0, status, abort_flag) &&
                   (!ragged_k || mbar_wait(kv_patched, 0, status, abort_flag)) &&
-                  (L::ALIAS || mbar_wait(kv_tmem, 0, status, abort_flag)) && issue_s(0) && issue_dp(0);
+                  mbar_wait(kv_tmem, 0, status, abort_flag) && issue_s(0) && issue_dp(0);
         for (int u = 0; ok && u < n; ++u) {
-          const int sq = u % QS, so = u % OS;
+          const int s = u % SLOTS;
           if (!mbar_wait(p_full, u & 1, status, abort_flag)) break;
           tc_fence_after();
-          const uint64_t omn = sdesc_sw128(sb + L::OFF_O + so * L::TILE, BT * 128, 1024);
+          const uint64_t omn = sdesc_sw128(sb + L::OFF_O + s * L::TILE, BT * 128, 1024);
 #pragma unroll
-          for (int ks = 0; ks < BT / 16; ++ks)  // dV += P^T dO; a group's pairs lie in the first half of its columns
-            mma_ts(tmem + L::kV, tmem + L::kS + C::COLS * (ks * 16 / C::COLS) + 8 * (ks % (C::COLS / 16)),
-                   sdesc_add(omn, ks * 2048), id_g, u > 0 || ks > 0);
-          mma_commit(o_empty + 8 * so);
+          for (int ks = 0; ks < BT / 16; ++ks)  // dV += P^T dO; a group's 32 queries lie in 32 columns' first 16
+            mma_ts(tmem + kV, tmem + kS + 32 * (ks >> 1) + 8 * (ks & 1), sdesc_add(omn, ks * 2048), id_g, u > 0 || ks > 0);
+          mma_commit(o_empty + 8 * s);
           if (u + 1 < n && !(ok = issue_s(u + 1))) break;
           if (!mbar_wait(ds_full, u & 1, status, abort_flag)) break;
           tc_fence_after();
-          const uint64_t qmn = sdesc_sw128(sb + L::OFF_Q + sq * L::TILE, BT * 128, 1024);
-          auto issue_dq = [&]() {  // dQ = dS K
+          const uint64_t qmn = sdesc_sw128(sb + L::OFF_Q + s * L::TILE, BT * 128, 1024);
 #pragma unroll
-            for (int ks = 0; ks < BT / 16; ++ks)
-              mma_ss(tmem + L::kQ, sdesc_add(dsmn, ks * 2048), sdesc_add(kmn, ks * 2048), id_q, ks > 0);
-            mma_commit(dq_full);
-          };
-          auto issue_dk = [&]() {  // dK += dS^T Q
+          for (int ks = 0; ks < BT / 16; ++ks)  // dK += dS^T Q
+            mma_ts(tmem + kK, tmem + kP + 32 * (ks >> 1) + 8 * (ks & 1), sdesc_add(qmn, ks * 2048), id_g, u > 0 || ks > 0);
+          mma_commit(q_empty + 8 * s);
+          // dP(u+1), which the dS warps wait for, as soon as dK has read dS
+          if (u + 1 < n && !issue_dp(u + 1)) break;
+          if (u >= 1 && !mbar_wait(dq_free, (u - 1) & 1, status, abort_flag)) break;
+          tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < BT / 16; ++ks) {
-              if (L::ALIAS)
-                mma_ss(tmem + L::kK, sdesc_add(dsk, (ks >> 2) * (BT * 128) + (ks & 3) * 32), sdesc_add(qmn, ks * 2048), id_g,
-                       u > 0 || ks > 0);
-              else
-                mma_ts(tmem + L::kK, tmem + L::kP + C::COLS * (ks * 16 / C::COLS) + 8 * (ks % (C::COLS / 16)),
-                       sdesc_add(qmn, ks * 2048), id_g, u > 0 || ks > 0);
-            }
-            mma_commit(q_empty + 8 * sq);
-          };
-          if (L::ALIAS) {  // dQ first: the dQ warps empty its columns while dK runs, then dP(u+1) takes them
-            issue_dq();
-            issue_dk();
-            mma_commit(ds_free);
-            if (u + 1 < n && (!mbar_wait(dq_free, u & 1, status, abort_flag) || !issue_dp(u + 1))) break;
-          } else {  // dP(u+1), which the dS warps wait for, as soon as dK has read dS
-            issue_dk();
-            if (u + 1 < n && !issue_dp(u + 1)) break;
-            if (u >= 1 && !mbar_wait(dq_free, (u - 1) & 1, status, abort_flag)) break;
-            issue_dq();
-            mma_commit(ds_free);
-          }
+          for (int ks = 0; ks < BT / 16; ++ks)  // dQ = dS K
+            mma_ss(tmem + kQ, sdesc_add(dsmn, ks * 2048), sdesc_add(kmn, ks * 2048), id_q, ks > 0);
+          mma_commit(dq_full);
+          mma_commit(ds_free);
         }
         mma_commit(g_done);
         mbar_drain(g_done, 0, status);
@@ -314,15 +277,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       __syncwarp();
     }
   } else if (warp >= DS_WARPS) {
-    setmaxnreg_inc<C::kRegsDq>();
+    setmaxnreg_inc<kRegsDq>();
     // ---------------------------------------------------------------- dQ out
     const int wq = warp & 3;
-    const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16) + L::kQ;
-    const uint32_t ring = sb + L::OFF_STAGE + (warp - DS_WARPS) * L::RING * L::CHUNK_BYTES;
-    constexpr int LINES = L::CHUNK / 4;  // 16-byte lines of a chunk's row
+    const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16) + kQ;
+    const uint32_t ring = sb + L::OFF_STAGE + (warp - DS_WARPS) * RING * CHUNK_BYTES;
     int at = 0;                          // ring position
     for (int u = 0; u < n; ++u) {
-      const int hq = hk * p.G + u / n_qt, q0 = q_begin + (u % n_qt) * BT;
+      const int hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
       const bool ok = mbar_wait_warp(dq_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
@@ -337,43 +299,40 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(dq_free);
 #pragma unroll
-      for (int c = 0; c < D / L::CHUNK; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         // the reduction that last used this chunk has read it
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(L::RING - 1) : "memory");
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(RING - 1) : "memory");
         __syncwarp();
-        const uint32_t stage = ring + at * L::CHUNK_BYTES;
-        at = at + 1 == L::RING ? 0 : at + 1;
+        const uint32_t stage = ring + at * CHUNK_BYTES;
+        at = (at + 1) % RING;
 #pragma unroll
-        for (int i = 0; i < LINES; ++i) {
-          const uint32_t* v = &a[c * L::CHUNK / 32][c * L::CHUNK % 32 + 4 * i];
-          // the swizzle of 128-byte rows, or of 64-byte rows
-          const int line = L::CHUNK == 32 ? i ^ (lane & 7) : i ^ ((lane >> 1) & 3);
-          st_shared16(stage + lane * (L::CHUNK * 4) + (line << 4), make_uint4(v[0], v[1], v[2], v[3]));
-        }
+        for (int i = 0; i < 8; ++i)
+          st_shared16(stage + lane * 128 + ((i ^ (lane & 7)) << 4),
+                      make_uint4(a[c][4 * i], a[c][4 * i + 1], a[c][4 * i + 2], a[c][4 * i + 3]));
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          reduce_add_3d(&maps.acc, stage, L::CHUNK * c, q0 + 32 * wq, b * p.H + hq);
+        if (elect_one()) {  // the same lane every time: bulk groups are a thread's own
+          reduce_add_3d(&maps.acc, stage, 32 * c, q0 + 32 * wq, b * p.H + hq);
           bulk_commit();
         }
+        __syncwarp();
       }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   } else {
-    setmaxnreg_inc<C::kRegsDs>();
+    setmaxnreg_inc<kRegsDs>();
     // ---------------------------------------------------------------- P and dS
-    constexpr int COLS = C::COLS, HALVES = COLS / 32;
     const int grp = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
     const int key = k0 + r;
     const float2 cc = make_float2(p.c, p.c);
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t ts = tmem + lanes + L::kS + COLS * grp, tp = tmem + lanes + L::kP + COLS * grp;
+    const uint32_t ts = tmem + lanes + kS + 32 * grp, tp = tmem + lanes + kP + 32 * grp;
     bool ok = true;
-    if (!L::ALIAS && n > 0 && grp < 2) {  // K (group 0) and V (group 1) into TMEM: lane = key, a column two of its elements
-      ok = mbar_wait_warp(ragged_k ? kv_patched : kv_full, 0, status, abort_flag) &&
-           mbar_wait_warp(kv_full, 0, status, abort_flag);
+    if (n > 0 && grp < 2) {  // K (group 0) and V (group 1) into TMEM: lane = key, a column two of its elements
+      ok = mbar_wait_warp(kv_full, 0, status, abort_flag) &&
+           (!ragged_k || mbar_wait_warp(kv_patched, 0, status, abort_flag));
       __syncwarp();
       if (ok) {
         uint32_t w[32];
@@ -386,7 +345,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           w[4 * i + 3] = x.w;
         }
         tc_fence_after();
-        tmem_st32(tmem + lanes + (grp ? L::kTV : L::kTK), w);
+        tmem_st32(tmem + lanes + (grp ? kTV : kTK), w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -394,38 +353,31 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
     }
     for (int u = 0; ok && u < n; ++u) {
-      const int q0 = q_begin + (u % n_qt) * BT + COLS * grp;  // first query of this warp's columns
+      const int q0 = q_begin + ((u0 + u) % n_qt) * BT + 32 * grp;  // first query of this warp's columns
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
-      uint32_t a[HALVES][32];
-#pragma unroll
-      for (int h = 0; h < HALVES; ++h) tmem_ld32(ts + 32 * h, a[h]);
+      uint32_t a[32], pk[16];
+      tmem_ld32(ts, a);
       tmem_ld_wait();
+      reg_fence32(a);
+      // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h) reg_fence32(a[h]);
-      const int hidden = key >= kl ? COLS : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
-      const bool masked = __any_sync(0xffffffffu, hidden > 0);
-#pragma unroll
-      for (int h = 0; h < HALVES; ++h) {
-        uint32_t pk[16];
-        // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 x = fmul2(make_float2(__uint_as_float(a[h][i]), __uint_as_float(a[h][i + 1])), cc);
-          a[h][i] = __float_as_uint(ex2(x.x));
-          a[h][i + 1] = __float_as_uint(ex2(x.y));
-        }
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * h + i < hidden) a[h][i] = 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(a[h][2 * i]), __uint_as_float(a[h][2 * i + 1]));
-        tmem_st16(ts + 16 * h, pk);
+      for (int i = 0; i < 32; i += 2) {
+        const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc);
+        a[i] = __float_as_uint(ex2(x.x));
+        a[i + 1] = __float_as_uint(ex2(x.y));
       }
+      const int hidden = key >= kl ? 32 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
+      if (__any_sync(0xffffffffu, hidden > 0)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < hidden) a[i] = 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+      tmem_st16(ts, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -435,61 +387,62 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
+      uint32_t d[32];
+      tmem_ld32(tp, d);
+      tmem_ld_wait();
+      reg_fence32(d);
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h) {
-        uint32_t d[32];
-        tmem_ld32(tp + 32 * h, d);
-        tmem_ld_wait();
-        reg_fence32(d);
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 x = fmul2(make_float2(__uint_as_float(a[h][i]), __uint_as_float(a[h][i + 1])),
-                                 make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
-          pk[i / 2] = pack_bf16(x.x, x.y);
-        }
-        if (!L::ALIAS) tmem_st16(tp + 16 * h, pk);
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * (COLS / 8) + h * 4 + v),
-                      make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]));
+      for (int i = 0; i < 32; i += 2) {
+        const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])),
+                               make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+        pk[i / 2] = pack_bf16(x.x, x.y);
       }
-      if (!L::ALIAS) tmem_st_wait();
+      tmem_st16(tp, pk);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * 4 + v),
+                    make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]));
+      tmem_st_wait();
       tc_fence_before();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
-    // ---- dV through the first Q slot, dK through the second: every product that read them is done
+    // ---- dV (groups 0, 1) through the first Q slot, dK (2, 3) through the second: every product that read them is done
     bool got = ok;
     if (n > 0 && ok) {
       got = mbar_wait_warp(g_done, 0, status, abort_flag);
       __syncwarp();
     }
-    if (got) {
+    const int which = grp / 2, col = (grp & 1) * 32;
+    uint32_t g[32];
+    if (got && n > 0) {
       tc_fence_after();
-      // D = 128: each of two groups takes half of the columns of both.  D = 64: groups 0, 1 take dV, 2, 3 take dK
-#pragma unroll
-      for (int i = 0; i < (D == 128 ? 4 : 1); ++i) {
-        const int which = D == 128 ? i / 2 : grp / 2, col = D == 128 ? grp * 64 + (i & 1) * 32 : (grp & 1) * 32;
-        uint32_t g[32];
-        if (n > 0) {
-          tmem_ld32(tmem + lanes + (which ? L::kK : L::kV) + col, g);
-          tmem_ld_wait();
-          reg_fence32(g);
-        }
-        if (n == 0 || key >= kl) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) g[k] = 0u;
-        }
-        stage_row32(sb + L::OFF_Q + which * L::TILE, r, col, g, which ? p.scale : 1.f);
-      }
-      fence_async_smem();
+      tmem_ld32(tmem + lanes + (which ? kK : kV) + col, g);
+      tmem_ld_wait();
+      reg_fence32(g);
     }
+    if (n == 0 || key >= kl) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) g[i] = 0u;
+    }
+    bool last = true;
+    if (part.parts > 1) {
+      // both tensors' accumulators of a part are one tile of 2 D columns
+      float4* mine = part_acc + (size_t)(part.tile - plan.kv_whole) * part.parts * (2 * D / 4 * BT);
+      part_put<2 * D>(mine, part.rank, r, which * D + col, g);
+      last = part_last(counters + (part.tile - plan.kv_whole), part.parts, DS_WARPS * 32, part_flag);
+      if (last) part_sum<2 * D>(mine, part.parts, r, which * D + col, g);
+    }
+    if (got && last) stage_row32(sb + L::OFF_Q + which * L::TILE, r, col, g, which ? p.scale : 1.f);
+    fence_async_smem();
     // every warp comes here; one that gave up makes none of them store
-    if (!named_bar_any(1, DS_WARPS * 32, !got) && threadIdx.x == 0) {
-      store_tile<D>(&maps.dv, sb + L::OFF_Q, k0, hk, b);
-      store_tile<D>(&maps.dk, sb + L::OFF_Q + L::TILE, k0, hk, b);
+    if (!named_bar_any(1, DS_WARPS * 32, !got) && last && warp == 0) {
+      if (elect_one()) {
+        store_tile<D>(&maps.dv, sb + L::OFF_Q, k0, hk, b);
+        store_tile<D>(&maps.dk, sb + L::OFF_Q + L::TILE, k0, hk, b);
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
@@ -501,7 +454,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 }
 
 // dQ = scale acc, as bf16 with q's strides; a thread takes 8 columns.
-template <int D>
 __global__ void __launch_bounds__(256) attn_dq_out_kernel(const AttnProblem p, const float* __restrict__ acc, int padded,
                                                           __nv_bfloat16* __restrict__ dq) {
   constexpr int LANES = D / 8;
@@ -518,9 +470,10 @@ __global__ void __launch_bounds__(256) attn_dq_out_kernel(const AttnProblem p, c
                  pack_bf16(y.z * f, y.w * f));
 }
 
-template <int D>
-cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv, const uint4* row_s,
-                     const uint4* row_d, float* acc, int padded, int longest_first, int* status, cudaStream_t st) {
+}  // namespace
+
+cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk,
+                                  void* dv, const AttnBwdScratch& w, int* status, cudaStream_t st) {
   Maps m;
   if (!encode_tile_map(&m.q, in.q, D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, BT) ||
       !encode_tile_map(&m.k, in.k, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
@@ -528,28 +481,18 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* 
       !encode_tile_map(&m.go, in.go, D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, BT) ||
       !encode_tile_map(&m.dk, dk, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
       !encode_tile_map(&m.dv, dv, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
-      !encode_rows_f32_map(&m.acc, acc, D, padded, p.B * p.H, 32, Smem<D>::CHUNK))
+      !encode_rows_f32_map(&m.acc, w.acc, D, w.padded, p.B * p.H, 32, 32))
     return cudaErrorInvalidValue;
-  constexpr int smem = Smem<D>::BYTES > kOneBlockPerSmSmem ? Smem<D>::BYTES : kOneBlockPerSmSmem;
-  auto kern = attn_bwd_fused_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = Smem::BYTES > kOneBlockPerSmSmem ? Smem::BYTES : kOneBlockPerSmSmem;
+  cudaError_t e = cudaFuncSetAttribute(attn_bwd_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long blocks = (long long)p.B * p.HK * ((p.NK + BT - 1) / BT);
-  kern<<<(unsigned)blocks, Cfg<D>::THREADS, smem, st>>>(p, row_s, row_d, padded, status, m, longest_first);
+  attn_bwd_fused_kernel<<<plan.kv_blocks, THREADS, smem, st>>>(p, static_cast<const uint4*>(w.row_s),
+                                                              static_cast<const uint4*>(w.row_d), w.padded, status, m, plan,
+                                                              static_cast<float4*>(w.kv_parts), w.kv_counters);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  attn_dq_out_kernel<D><<<(unsigned)((p.rows * (D / 8) + 255) / 256), 256, 0, st>>>(p, acc, padded,
-                                                                                    static_cast<__nv_bfloat16*>(dq));
+  attn_dq_out_kernel<<<(unsigned)((p.rows * (D / 8) + 255) / 256), 256, 0, st>>>(p, w.acc, w.padded,
+                                                                               static_cast<__nv_bfloat16*>(dq));
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv,
-                                  const void* row_s, const void* row_d, float* acc, int padded, int longest_first,
-                                  int* status, cudaStream_t st) {
-  auto *rs = static_cast<const uint4*>(row_s), *rd = static_cast<const uint4*>(row_d);
-  if (p.D == 64) return launch_d<64>(p, in, dq, dk, dv, rs, rd, acc, padded, longest_first, status, st);
-  return launch_d<128>(p, in, dq, dk, dv, rs, rd, acc, padded, longest_first, status, st);
 }
 
 }  // namespace skl

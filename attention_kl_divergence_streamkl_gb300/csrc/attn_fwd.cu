@@ -142,31 +142,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       tma_load_4d(sb + L::OFF_KV + s * L::TILE + h * BN * 128, (u & 1) ? &mv : &mk, kv_full + 8 * s, h * 64,
                   (kt0 + (u >> 1)) * BN, hk, b);
   };
-  if (warp == PRODUCER_WARP && lane == 0) {
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full + 8 * t, 1);
-      mbar_init(s_full + 8 * t, 1);
-      mbar_init(p_ready + 8 * t, SOFTMAX_WARPS / 2);
-      mbar_init(o_done + 8 * t, 1);
-    }
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(kv_full + 8 * s, 1);
-      mbar_init(kv_empty + 8 * s, 1);
-    }
-    mbar_init(to_patch, 1);
-    mbar_init(patched, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    for (int t = 0; t < 2; ++t) {
-      if ((t ? nB : nA) == 0) continue;
-      mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
+  if (warp == PRODUCER_WARP) {
+    if (elect_one()) {
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(q_full + 8 * t, 1);
+        mbar_init(s_full + 8 * t, 1);
+        mbar_init(p_ready + 8 * t, SOFTMAX_WARPS / 2);
+        mbar_init(o_done + 8 * t, 1);
+      }
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(kv_full + 8 * s, 1);
+        mbar_init(kv_empty + 8 * s, 1);
+      }
+      mbar_init(to_patch, 1);
+      mbar_init(patched, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      for (int t = 0; t < 2; ++t) {
+        if ((t ? nB : nA) == 0) continue;
+        mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
-                    p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
-      if (t == 0 || nA == 0) load_kv(0);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
+                      p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+        if (t == 0 || nA == 0) load_kv(0);
+      }
+      for (int u = 1; u < min(SLOTS, 2 * n); ++u) load_kv(u);
     }
-    for (int u = 1; u < min(SLOTS, 2 * n); ++u) load_kv(u);
+    __syncwarp();  // the warp's other lanes wait for the one that issues
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp >= SOFTMAX_WARPS) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         int issued = min(SLOTS, 2 * n);
         for (int u = SLOTS; u < 2 * n; ++u) {
           if (!mbar_wait(kv_empty + 8 * (u % SLOTS), ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
@@ -246,8 +249,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int ks = 0; ks < BN / 16; ++ks)
             mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * ks, sdesc_add(vd, ks * 2048), id_o,
                    i > 0 || ks > 0);
-          mma_commit(o_done + 8 * t);
           if (t == 1 || i >= nB) mma_commit(kv_empty + 8 * s);
+          mma_commit(o_done + 8 * t);  // last: the block leaves once it has arrived
           return true;
         };
         // tile A has the key tiles [0, nA), tile B [0, nB); B is the last to read a tile both have, and where
@@ -390,8 +393,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_async_smem();
       }
       // every warp of the tile comes here; one that gave up makes none of them store
-      if (!named_bar_any(1 + t, SOFTMAX_WARPS / 2 * 32, !ok) && p.splits == 1 && r == 0)
-        store_tile<D>(&mo, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+      if (!named_bar_any(1 + t, SOFTMAX_WARPS / 2 * 32, !ok) && p.splits == 1 && wq == 0) {
+        if (elect_one())
+          store_tile<D>(&mo, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+        __syncwarp();
+      }
     }
   }
   tc_fence_before();

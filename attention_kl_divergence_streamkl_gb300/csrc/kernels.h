@@ -118,14 +118,33 @@ struct AttnBwdIn {
   const void *q, *k, *v, *o, *go;  // go = dO, with o's strides
   const float *lse, *dlse;         // dlse may be null
 };
-// `fused`: one visit of each tile pair, dQ added up in an fp32 accumulator; else separate dQ and dK/dV blocks.
-bool attn_bwd_fused(const AttnProblem& p, int mode, int num_sms);  // mode: streamkl_bwd_mode
-size_t attn_bwd_workspace(const AttnProblem& p, bool fused);
-cudaError_t launch_attn_bwd(const AttnProblem& p, bool fused, const AttnBwdIn& in, void* dq, void* dk, void* dv,
-                            void* workspace, int num_sms, int* status, cudaStream_t st);
-cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdIn& in, void* dq, void* dk, void* dv,
-                                  const void* row_s, const void* row_d, float* acc, int padded, int longest_first,
-                                  int* status, cudaStream_t st);
+// How a backward runs on a device (a pure rule of sizes).  Tiles [0, whole) of a kind are one block each, the later ones
+// `parts` blocks.  Fused: one visit of each tile pair by the kv blocks, dQ added up in an fp32 accumulator.
+struct AttnBwdPlan {
+  bool fused;
+  unsigned kv_tiles, kv_whole, kv_blocks;
+  unsigned q_tiles, q_whole, q_blocks;  // dQ blocks; none when fused
+  int kv_parts, q_parts;
+  int q_first;        // which kind comes first in the grid
+  int longest_first;  // the longest tiles of all heads first, not head by head
+};
+// Where things lie in the workspace.
+struct AttnBwdScratch {
+  int padded;             // N_Q rounded up to 128
+  void *row_s, *row_d;    // 16 bytes per row of [B H][padded]
+  float* acc;             // fused: [B H][padded][D]
+  void *kv_parts, *q_parts;
+  unsigned *kv_counters, *q_counters;
+  unsigned n_counters;    // of both, one after the other
+  size_t bytes;
+};
+bool attn_bwd_has_fused(const AttnProblem& p);
+AttnBwdPlan attn_bwd_plan(const AttnProblem& p, int mode, int num_sms);  // mode: streamkl_bwd_mode
+AttnBwdScratch attn_bwd_scratch(const AttnProblem& p, const AttnBwdPlan& plan, void* workspace);
+cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk,
+                            void* dv, void* workspace, int* status, cudaStream_t st);
+cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk,
+                                  void* dv, const AttnBwdScratch& w, int* status, cudaStream_t st);
 
 // ---- log probabilities of given tokens ---------------------------------------------
 constexpr int kTypeBf16 = 0, kTypeFp16 = 1, kTypeFp32 = 2;  // streamkl_dtype

@@ -345,17 +345,24 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
  * not make rows overlap).  Lengths and causal as in the forward; gradients of
  * what lies past a sequence are 0, and go, dlse are not used there.
  * bwd_mode:
- *   STREAMKL_BWD_SEPARATE  dQ blocks and dK/dV blocks in one launch, every output
- *                          written by one block: the same bits on every run.
- *                          Workspace: 32 bytes per query row, N_Q rounded up to 128.
- *   STREAMKL_BWD_FUSED     one visit of each tile pair; dQ is added up in fp32 by
- *                          reductions in L2, in no fixed order, so its last bits can
- *                          differ between runs.  Workspace: 4 D bytes more per row.
- *   STREAMKL_BWD_AUTO      as streamkl_attn_bwd_select decides (a pure host rule; 0
- *                          for an invalid shape): fused where the key tiles alone
- *                          fill the SMs.
+ *   STREAMKL_BWD_SEPARATE  dQ blocks and dK/dV blocks in one launch; what several
+ *                          blocks add up is added in a fixed order: the same bits on
+ *                          every run.  Workspace: 32 bytes per query row (N_Q
+ *                          rounded up to 128), and the fp32 accumulators of tiles
+ *                          that are dealt out over several blocks.
+ *   STREAMKL_BWD_FUSED     D = 64 only (else STREAMKL_ERR_UNSUPPORTED): one visit of
+ *                          each tile pair; dQ is added up in fp32 by reductions in
+ *                          L2, in no fixed order, so its last bits can differ between
+ *                          runs (dK and dV do not).  Workspace: 4 D bytes more per row.
+ *   STREAMKL_BWD_AUTO      fused for D = 64 where the key tiles alone fill the SMs,
+ *                          else separate.
+ * streamkl_attn_bwd_plan gives the path, the parts that dK/dV tiles and dQ tiles are
+ * dealt out over (1: one block each; the fused path deals out only its last wave)
+ * and the workspace for any SM count (num_sms <= 0: the current device); with
+ * num_sms > 0 it is a pure host rule.
  */
-int streamkl_attn_bwd_select(streamkl_attn_shape s, int num_sms);
+streamkl_status streamkl_attn_bwd_plan(streamkl_attn_shape s, int num_sms, int bwd_mode, int* path, int* kv_parts,
+                                       int* q_parts, size_t* workspace_bytes);
 streamkl_status streamkl_attn_bwd_workspace(streamkl_attn_shape s, int bwd_mode, size_t* bytes);
 streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse,
                                   const void* go, const float* dlse, streamkl_attn_shape s, void* dq, void* dk,

@@ -108,8 +108,9 @@ def bwd_args(s, drop=None, off=None, ws=1 << 30, mode=K.BWD_SEPARATE):
 def test_bwd_refuses_shapes(lib, change, code):
     s = K.make_attn_shape(**{**OK, **change})
     assert lib.streamkl_attn_bwd(*bwd_args(s)) == code
-    assert lib.streamkl_attn_bwd_workspace(s, K.BWD_SEPARATE, ctypes.byref(ctypes.c_size_t())) == code
-    assert lib.streamkl_attn_bwd_select(s, 152) == 0
+    out = [ctypes.byref(ctypes.c_int()) for _ in range(3)] + [ctypes.byref(ctypes.c_size_t())]
+    assert lib.streamkl_attn_bwd_plan(s, 152, K.BWD_AUTO, *out) == code
+    assert lib.streamkl_attn_bwd_workspace(s, K.BWD_AUTO, out[-1]) == code
 
 
 def test_bwd_refuses_pointers_and_small_workspaces(lib):
@@ -118,14 +119,14 @@ def test_bwd_refuses_pointers_and_small_workspaces(lib):
         assert lib.streamkl_attn_bwd(*bwd_args(s, drop=name)) == K.ERR_INVALID, name
         assert lib.streamkl_attn_bwd(*bwd_args(s, off=name)) == K.ERR_INVALID, name
     assert lib.streamkl_attn_bwd(*bwd_args(s, off="dlse")) == K.ERR_INVALID
-    n = ctypes.c_size_t()
-    for mode, size in ((K.BWD_FUSED, 32 + 4 * 64), (K.BWD_SEPARATE, 32)):
-        assert lib.streamkl_attn_bwd_workspace(s, mode, ctypes.byref(n)) == K.OK
-        assert n.value == 2 * 8 * 128 * size
     for mode in (-1, K.BWD_DQ_ONLY, K.BWD_DK_ONLY, 5):
-        assert lib.streamkl_attn_bwd_workspace(s, mode, ctypes.byref(ctypes.c_size_t())) == K.ERR_INVALID
         assert lib.streamkl_attn_bwd(*bwd_args(s, mode=mode)) == K.ERR_INVALID
-    assert lib.streamkl_attn_bwd(*bwd_args(s, ws=n.value - 1)) == K.ERR_WORKSPACE
+        with pytest.raises(skl.StreamKLError):
+            skl.attn_bwd_plan(**OK, num_sms=152, bwd_mode=mode)
+    wide = K.make_attn_shape(**{**OK, "D": 128})
+    assert lib.streamkl_attn_bwd(*bwd_args(wide, mode=K.BWD_FUSED)) == K.ERR_UNSUPPORTED
+    for ws in (0, 2 * 8 * 100 * 32 - 1):
+        assert lib.streamkl_attn_bwd(*bwd_args(s, ws=ws)) == K.ERR_WORKSPACE
     assert lib.streamkl_attn_bwd(*bwd_args(s, drop="ws")) == K.ERR_WORKSPACE
     assert lib.streamkl_attn_bwd(*bwd_args(s, off="ws")) == K.ERR_WORKSPACE
 
@@ -139,7 +140,22 @@ def test_bwd_binding_refuses():
         skl.attn_bwd(q, q, q, q[:, :, :2], lse, q)
 
 
-def test_bwd_select():
-    """Fused where the key tiles fill the SMs."""
-    assert skl.attn_bwd_select(2, 32, 8, 4096, 4096, 128, 152, True) == K.BWD_FUSED
-    assert skl.attn_bwd_select(1, 8, 8, 1024, 1024, 128, 152) == K.BWD_SEPARATE
+def test_bwd_plan(lib):
+    """The path, the parts and the workspace: 32 bytes a row (queries rounded up to 128), 4 D more when fused, and 3 D
+    fp32 accumulators of 128 rows for a part of both kinds."""
+    rows = 2 * 8 * 128
+    assert skl.attn_bwd_plan(**OK, num_sms=152) == (K.BWD_SEPARATE, 1, 1, rows * 32)
+    assert skl.attn_bwd_plan(**OK, num_sms=152, bwd_mode=K.BWD_FUSED)[3] == rows * (32 + 4 * 64)
+    # D = 64, key tiles fill the SMs: fused; its last wave of 512 - 3 * 152 = 56 tiles in two parts each
+    path, kv, q, ws = skl.attn_bwd_plan(1, 8, 8, 8192, 8192, 64, 152)
+    assert (path, kv, q) == (K.BWD_FUSED, 2, 1)
+    assert ws == 8 * 8192 * (32 + 256) + 56 * 2 * 128 * 128 * 4 + 56 * 4
+    # causal: its own short blocks fill the end
+    assert skl.attn_bwd_plan(1, 8, 8, 8192, 8192, 64, 152, True)[:2] == (K.BWD_FUSED, 1)
+    assert skl.attn_bwd_plan(1, 8, 8, 8192, 8192, 64, 152, bwd_mode=K.BWD_SEPARATE)[0] == K.BWD_SEPARATE
+    # many blocks: none is dealt out
+    assert skl.attn_bwd_plan(2, 32, 8, 4096, 4096, 128, 152, True)[:3] == (K.BWD_SEPARATE, 1, 1)
+    # 64 key tiles, each read by four heads of 16 tiles, leave most SMs idle
+    assert skl.attn_bwd_plan(1, 16, 4, 2048, 2048, 128, 152, True)[1:3] == (2, 1)
+    # so do 4 query tiles over 512 key tiles
+    assert skl.attn_bwd_plan(1, 4, 4, 128, 65536, 128, 152)[2] > 1
