@@ -1,10 +1,13 @@
-"""ctypes binding of libstreamkl (argument marshalling only).
+"""Python binding of libstreamkl (argument marshalling only), through ctypes.
 
 Every step of the computation runs in the CUDA kernels of ``libstreamkl.so``;
 this module only checks tensor metadata, allocates outputs and workspaces
 through PyTorch's CUDA allocator, and passes raw pointers and the current CUDA
 stream to the C entry points of the same names.  There is no CPU fallback: if
-the library is missing, every call raises.
+the library is missing, every call raises.  The entry points that a model calls
+per layer and per token (attn_fwd, attn_bwd, logprobs_fwd, logprobs_bwd) go to
+the native caller first (csrc/calls.cpp, _calls.so), which does the same for
+tensors that need no copy in a third of the time, and come back here for the rest.
 
 Inputs given as CPU tensors are copied to the current CUDA device on the
 current stream (non-blocking from pinned memory) and the results are copied
@@ -92,6 +95,7 @@ SIGNATURES = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
+_calls = None
 
 
 def lib() -> ctypes.CDLL:
@@ -108,6 +112,20 @@ def lib() -> ctypes.CDLL:
             f.argtypes = args
         _lib = L
     return _lib
+
+
+def calls():
+    """The native caller of the per-layer entry points (csrc/calls.cpp); raises if it has not been built."""
+    global _calls
+    if _calls is None:
+        lib()
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise RuntimeError("_calls.so is missing or does not load: build it with "
+                               f"attention_kl_divergence_streamkl_gb300.build.build() ({e})") from e
+        _calls = module
+    return _calls
 
 
 def status_string(status: int) -> str:
@@ -514,6 +532,9 @@ def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
     padded batch's sequences.  Causal masking is aligned at the last query and key of each sequence.  Rows that
     see no key give 0 and -inf.
     """
+    got = (_calls or calls()).attn_fwd(q, k, v, scale, causal, q_lens, k_lens)
+    if got is not None:
+        return got
     (q, k, v), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v), q_lens, k_lens)
     (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
     B, H, _, NQ, _, D = sizes
@@ -543,6 +564,9 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
     bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED (D = 64) visits each tile pair once and adds dq up
     in no fixed order; BWD_AUTO picks by shape.
     """
+    got = (_calls or calls()).attn_bwd(q, k, v, o, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode)
+    if got is not None:
+        return got
     (q, k, v, o, do), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
     (q, qs), (k, ks), (v, vs), (o, os_), (do, ds) = _layout(q), _layout(k), _layout(v), _layout(o), _layout(do)
     B, H, HK, NQ, NK, D = sizes
@@ -609,6 +633,9 @@ def logprobs_fwd(logits, tokens=None, scale=1.0, top_k=0):
     negative one is no token (its logp is 0).  logp has the shape of tokens; entropy and lse are [...];
     top_logp fp32 and top_index int64 are [..., top_k], the largest logits (equal ones: the lowest index first).
     """
+    got = (_calls or calls()).logprobs_fwd(logits, tokens, scale, top_k)
+    if got is not None:
+        return got
     x, tok, T, lead, dev, host = _logits_rows(logits, tokens)
     R, V = x.shape
     if not 0 <= top_k <= min(LOGPROBS_MAX_TOP_K, V):
@@ -627,6 +654,9 @@ def logprobs_fwd(logits, tokens=None, scale=1.0, top_k=0):
 def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0):
     """Gradient of the logits, contiguous and of their type, for upstream gradients g_logp (tokens' shape) and
     g_entropy ([...] or None); lse and entropy are logprobs_fwd's (entropy may be None without g_entropy)."""
+    got = (_calls or calls()).logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy, scale)
+    if got is not None:
+        return got
     x, tok, T, lead, dev, host = _logits_rows(logits, tokens)
     R, V = x.shape
     lse = _rows(lse, dev, lead, "lse")
