@@ -74,6 +74,25 @@ __device__ __forceinline__ uint64_t sdesc_step(uint32_t addr, uint32_t zero) {
          ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
 }
 
+// P = 2^(c (S - LSE / scale)) of 32 columns (0 for rows without keys and past the sequence), as fp32 over the logits and as
+// bf16 pairs; the first `hidden` columns do not see the thread's key.  A copy of its own for the tiles without a mask: there
+// the conversions run between the exponentials.
+template <bool MASKED>
+__device__ __forceinline__ void p32(uint32_t (&a)[32], uint32_t (&pk)[16], float2 cc, int hidden) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc);
+    float2 e = make_float2(ex2(x.x), ex2(x.y));
+    if (MASKED) {
+      e.x = i < hidden ? 0.f : e.x;
+      e.y = i + 1 < hidden ? 0.f : e.y;
+    }
+    a[i] = __float_as_uint(e.x);
+    a[i + 1] = __float_as_uint(e.y);
+    pk[i / 2] = pack_bf16(e.x, e.y);
+  }
+}
+
 // ---- parts: where a kind of block has fewer or longer tiles than the SMs can share evenly, a tile's stream is dealt out
 // over `parts` blocks.  Each leaves its fp32 accumulators in the workspace, and the one that counts up to `parts` adds
 // them all in the parts' order, so the sum does not depend on who that is.

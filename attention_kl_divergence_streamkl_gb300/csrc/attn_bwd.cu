@@ -372,32 +372,22 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t ts = tmem + lanes + kv::kColS + 32 * grp, tp = tmem + lanes + kv::kColP + 32 * grp;
     bool ok = true;
+    const int q_last = q_begin + (n_qt - 1) * BT + 32 * grp;
+    int q0 = q_begin + (n > 0 ? u0 % n_qt : 0) * BT + 32 * grp;  // first query of this warp's columns
     for (int u = 0; u < n; ++u) {
-      const int q0 = q_begin + ((u0 + u) % n_qt) * BT + 32 * grp;  // first query of this warp's columns
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
-      uint32_t a[32];
+      uint32_t a[32], pk[16];
       tmem_ld32(ts, a);
       tmem_ld_wait();
       reg_fence32(a);
-      // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc);
-        a[i] = __float_as_uint(ex2(x.x));
-        a[i + 1] = __float_as_uint(ex2(x.y));
-      }
       const int hidden = key >= kl ? 32 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
-      if (__any_sync(0xffffffffu, hidden > 0)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < hidden) a[i] = 0u;
-      }
-      uint32_t pk[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+      if (__any_sync(0xffffffffu, hidden > 0))
+        p32<true>(a, pk, cc, hidden);
+      else
+        p32<false>(a, pk, cc, 0);
       tmem_st16(ts, pk);
       tmem_st_wait();
       tc_fence_before();
@@ -422,6 +412,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
+      q0 = q0 == q_last ? q_last - (n_qt - 1) * BT : q0 + BT;
     }
     // ---- out: thread = key row, group g writes d columns [32g, 32g + 32) of both
     bool got = ok;

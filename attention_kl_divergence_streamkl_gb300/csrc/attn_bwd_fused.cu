@@ -12,15 +12,19 @@
 //          and in shared memory [key][query]:               dQ = dS K (MN-major A)
 // TMEM: S/P [0,128), dP/dS [128,256), dV, dK, dQ 64 columns each from 256 on, and K and V as bf16 pairs in the last 64,
 // the A operands of S and dP.  Shared-memory traffic is what bounds a tile pair: with every operand read from there it
-// was 324 KB, 2500 of 2800 cycles at 128 bytes a clock; so it is 230 KB.
+// was 350 KB, so it is 260, 2000 cycles at 128 bytes a clock, of about 2550 that a tile pair takes (the products alone
+// 1350).  It comes in two halves, between the two barriers of the P and dS warps; dQ is computed before dP, and so
+// staged and reduced while the first half's products leave room (the other way round 1290 us where it is now 1192:
+// 32 heads, 8 key heads, N8192, non-causal).
 //   warps 0-15   thread = key, group g = warp / 4 takes queries [32g, 32g + 32)
 //   warps 16-19  dQ: TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
 //   warp 20      TMA producer: K, V once; Q(u) and dO(u) with their rows' values
-//   warp 21      TMEM owner and MMA issuer: dV(u), S(u+1), dK(u), dP(u+1), dQ(u)
+//   warp 21      TMEM owner and MMA issuer: dV(u), S(u+1), dK(u), dQ(u), dP(u+1)
 //   warp 22      clears rows past a sequence's lengths in K, V, Q and dO tiles
 // At D = 128 the same kernel (built, measured, not kept) has 532 KB of shared-memory traffic a tile pair, dQ's staging
 // and reductions 128 KB of it: 4450 cycles against 4460 for the separate blocks' two visits (B2 H32 HK8 N4096 causal
-// 0.69 against 0.68 ms).  At D = 64: 8 heads, N8192, non-causal 0.39 against 0.44 ms.
+// 0.69 against 0.68 ms).  At D = 64: 8 heads, N8192, non-causal 0.32 against 0.44 ms;
+// with red.add from registers instead of staging and bulk reductions 0.39.
 #include "attn.cuh"
 
 namespace skl {
@@ -56,9 +60,9 @@ struct Smem {
   static constexpr int OFF_ONES = OFF_RD + SLOTS * STEP;
   static constexpr int OFF_ZERO = OFF_ONES + STEP;
   static constexpr int OFF_BAR = OFF_ZERO + STEP;
-  // kv_full, kv_patched, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, ds_free, dq_full,
+  // kv_full, kv_patched, q_full[2], q_empty[2], o_full[2], o_empty[2], s_full, dp_full, p_full, ds_full, dq_full,
   // dq_free, g_done, to_patch, patched, kv_tmem; TMEM slot, abort flag, part flag
-  static constexpr int BAR_SLOT = 8 * 21;
+  static constexpr int BAR_SLOT = 8 * 20;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16;
 };
 static_assert(Smem::BYTES <= 227 * 1024, "shared memory");
@@ -97,8 +101,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t bar = sb + L::OFF_BAR;
   const uint32_t kv_full = bar, kv_patched = bar + 8, q_full = bar + 16, q_empty = bar + 32, o_full = bar + 48,
                  o_empty = bar + 64, s_full = bar + 80, dp_full = bar + 88, p_full = bar + 96, ds_full = bar + 104,
-                 ds_free = bar + 112, dq_full = bar + 120, dq_free = bar + 128, g_done = bar + 136, to_patch = bar + 144,
-                 patched = bar + 152, kv_tmem = bar + 160, slot = bar + L::BAR_SLOT;
+                 dq_full = bar + 112, dq_free = bar + 120, g_done = bar + 128, to_patch = bar + 136, patched = bar + 144,
+                 kv_tmem = bar + 152, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
   volatile int* part_flag = abort_flag + 1;
   if (threadIdx.x == 0) {
@@ -114,7 +118,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(dp_full, 1);
     mbar_init(p_full, DS_WARPS);
     mbar_init(ds_full, DS_WARPS);
-    mbar_init(ds_free, 1);
     mbar_init(dq_full, 1);
     mbar_init(dq_free, DQ_WARPS);
     mbar_init(g_done, 1);
@@ -261,15 +264,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int ks = 0; ks < BT / 16; ++ks)  // dK += dS^T Q
             mma_ts(tmem + kK, tmem + kP + 32 * (ks >> 1) + 8 * (ks & 1), sdesc_add(qmn, ks * 2048), id_g, u > 0 || ks > 0);
           mma_commit(q_empty + 8 * s);
-          // dP(u+1), which the dS warps wait for, as soon as dK has read dS
-          if (u + 1 < n && !issue_dp(u + 1)) break;
           if (u >= 1 && !mbar_wait(dq_free, (u - 1) & 1, status, abort_flag)) break;
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < BT / 16; ++ks)  // dQ = dS K
             mma_ss(tmem + kQ, sdesc_add(dsmn, ks * 2048), sdesc_add(kmn, ks * 2048), id_q, ks > 0);
           mma_commit(dq_full);
-          mma_commit(ds_free);
+          // last, when dK has read dS from dP's columns; dQ before it, so that its way out is over before dV and S run
+          if (u + 1 < n && !issue_dp(u + 1)) break;
         }
         mma_commit(g_done);
         mbar_drain(g_done, 0, status);
@@ -283,8 +285,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16) + kQ;
     const uint32_t ring = sb + L::OFF_STAGE + (warp - DS_WARPS) * RING * CHUNK_BYTES;
     int at = 0;                          // ring position
+    int hq = hk * p.G + (n > 0 ? u0 / n_qt : 0), q0 = q_begin + (n > 0 ? u0 % n_qt : 0) * BT;
     for (int u = 0; u < n; ++u) {
-      const int hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
       const bool ok = mbar_wait_warp(dq_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
@@ -316,6 +318,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           bulk_commit();
         }
         __syncwarp();
+      }
+      q0 += BT;
+      if (q0 == q_begin + n_qt * BT) {
+        q0 = q_begin;
+        ++hq;
       }
     }
     if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -352,8 +359,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(kv_tmem);
       }
     }
+    const int q_last = q_begin + (n_qt - 1) * BT + 32 * grp;
+    int q0 = q_begin + (n > 0 ? u0 % n_qt : 0) * BT + 32 * grp;  // first query of this warp's columns
     for (int u = 0; ok && u < n; ++u) {
-      const int q0 = q_begin + ((u0 + u) % n_qt) * BT + 32 * grp;  // first query of this warp's columns
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
@@ -362,28 +370,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_ld32(ts, a);
       tmem_ld_wait();
       reg_fence32(a);
-      // P = 2^(c (S - LSE / scale)): 0 for rows without keys and past the sequence
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), cc);
-        a[i] = __float_as_uint(ex2(x.x));
-        a[i + 1] = __float_as_uint(ex2(x.y));
-      }
       const int hidden = key >= kl ? 32 : p.causal ? key - off - q0 : 0;  // the first columns that do not see this key
-      if (__any_sync(0xffffffffu, hidden > 0)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < hidden) a[i] = 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+      if (__any_sync(0xffffffffu, hidden > 0))
+        p32<true>(a, pk, cc, hidden);
+      else
+        p32<false>(a, pk, cc, 0);
       tmem_st16(ts, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
-      ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag) &&
-           (u == 0 || mbar_wait_warp(ds_free, (u - 1) & 1, status, abort_flag));  // dS of the last tile has been read
+      ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag);  // dQ(u-1), issued before dP(u), has read dS too
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
@@ -392,21 +389,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_ld_wait();
       reg_fence32(d);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])),
-                               make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
-        pk[i / 2] = pack_bf16(x.x, x.y);
-      }
-      tmem_st16(tp, pk);
+      for (int v = 0; v < 4; ++v) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+        for (int i = 8 * v; i < 8 * v + 8; i += 2) {
+          const float2 x = fmul2(make_float2(__uint_as_float(a[i]), __uint_as_float(a[i + 1])),
+                                 make_float2(__uint_as_float(d[i]), __uint_as_float(d[i + 1])));
+          pk[i / 2] = pack_bf16(x.x, x.y);
+        }
         st_shared16(sw128<BT>(sb + L::OFF_DS, r, grp * 4 + v),
                     make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]));
+      }
+      tmem_st16(tp, pk);
       tmem_st_wait();
       tc_fence_before();
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
+      q0 = q0 == q_last ? q_last - (n_qt - 1) * BT : q0 + BT;
     }
     // ---- dV (groups 0, 1) through the first Q slot, dK (2, 3) through the second: every product that read them is done
     bool got = ok;
