@@ -43,7 +43,8 @@ struct BwdMaps {  // of the inputs, and of the outputs
 //
 // O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|.  Among many keys that averages out of the
 // gradients; a row that sees few of them passes it on whole.  For rows of at most 32 keys (the first rows under a causal
-// mask, short sequences) delta is computed as sum_j P_ij dP_ij instead, a key to a lane.
+// mask, short sequences) delta is computed as sum_j P_ij dP_ij instead, by the row's own lanes (a key to a lane reads 32
+// lines with every instruction: 25 us for 1500 such rows).
 // Sum of the products of 8 bf16 pairs.
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -55,72 +56,127 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
   return sum;
 }
 
+// The totals of N values over LANES lanes: on return lane l holds in v[0] the total of value lane_index<N>(l).
+template <int N>
+__device__ __forceinline__ int lane_index(int lane) {
+  int i = 0;
+#pragma unroll
+  for (int o = 1; o < N; o *= 2) i = 2 * i + ((lane & o) != 0);
+  return i;
+}
+template <int LANES, int N>
+__device__ __forceinline__ void lane_totals(float (&v)[N], int lane) {
+  static_assert(N <= LANES, "a lane for each value");
+#pragma unroll
+  for (int o = 1, n = N / 2; n; o *= 2, n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool upper = lane & o;
+      const float other = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + n], o);
+      v[i] = (upper ? v[i + n] : v[i]) + other;
+    }
+#pragma unroll
+  for (int o = N; o < LANES; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+}
+
+constexpr int kRowsEach = 4;  // rows of a thread, all loaded before the first is used; a quarter of the head apart, so
+                              // that the rows that see few keys, which lie together, spread over many threads
+constexpr int kExactKeys = 32, kKeysAtOnce = 4;
+
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     attn_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
                      float4* __restrict__ acc, unsigned* __restrict__ counters, unsigned n_counters, int padded) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
+  static_assert(BT % (ROWS * kRowsEach) == 0, "a block's rows are one head's");
   for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
-  const long long r = (long long)blockIdx.x * ROWS + threadIdx.x / LANES;  // row of [B H][padded]
+  const int step = padded / kRowsEach;
+  const unsigned per_head = (unsigned)step / ROWS;
+  const int bh = (int)(blockIdx.x / per_head);
+  const int b = bh / p.H, h = bh % p.H;
+  const int n0 = (int)(blockIdx.x % per_head) * ROWS + threadIdx.x / LANES;  // rows n0, n0 + step, ...
   const int lane = threadIdx.x % LANES;
-  const bool inside = r < (long long)p.B * p.H * padded;
-  const long long bh = inside ? r / padded : 0;
-  const int n = (int)(r % padded);
-  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
-  const bool real = inside && n < ql;
-  const int seen = real ? (p.causal ? min(kl, n + kl - ql + 1) : kl) : 0;  // keys this row sees (none: <= 0)
-  const long long at = b * p.os_b + h * p.os_h + n * p.os_n;
-  const auto* go = static_cast<const __nv_bfloat16*>(in.go) + at;
-  if (acc && inside) {  // the fused kernel's accumulator starts at zero
-    acc[r * (D / 4) + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    acc[r * (D / 4) + LANES + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  float sum = 0.f, l = 0.f;
-  if (seen > 0) {
-    const auto* o = static_cast<const __nv_bfloat16*>(in.o) + at;
-    sum = dot8(reinterpret_cast<const uint4*>(o)[lane], reinterpret_cast<const uint4*>(go)[lane], 0.f);
-    l = in.lse[bh * p.NQ + n];
-  }
+  auto seen = [&](int n) { return n < ql ? (p.causal ? min(kl, n + kl - ql + 1) : kl) : 0; };  // keys a row sees, or <= 0
+  const long long r0 = (long long)bh * padded + n0;  // row of [B H][padded]
+  const auto* o = static_cast<const __nv_bfloat16*>(in.o) + b * p.os_b + h * p.os_h + lane * 8;
+  const auto* go = static_cast<const __nv_bfloat16*>(in.go) + b * p.os_b + h * p.os_h + lane * 8;
+  const float* lse = in.lse + (long long)bh * p.NQ;
+  const float* dlse = in.dlse ? in.dlse + (long long)bh * p.NQ : nullptr;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 x[kRowsEach], y[kRowsEach];
+  bool few = false;
 #pragma unroll
-  for (int w = LANES / 2; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-  const int key = threadIdx.x & 31;
-  if (__any_sync(0xffffffffu, seen > 0 && seen <= 32)) {
-    // the warp's rows one after the other; every lane takes one key of the row
-    for (int g = 0; g < 32 / LANES; ++g) {
-      const int src = g * LANES;
-      const int keys = __shfl_sync(0xffffffffu, seen, src);
-      const float lg = __shfl_sync(0xffffffffu, l, src);
-      const int bg = __shfl_sync(0xffffffffu, b, src), hg = __shfl_sync(0xffffffffu, h, src),
-                ng = __shfl_sync(0xffffffffu, n, src);
-      if (keys <= 0 || keys > 32) continue;
-      float s = 0.f, t = 0.f;
-      if (key < keys) {
-        const auto* qr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.q) + bg * p.qs_b +
-                                                        hg * p.qs_h + ng * p.qs_n);
-        const auto* gr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.go) + bg * p.os_b +
-                                                        hg * p.os_h + ng * p.os_n);
-        const auto* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.k) + bg * p.ks_b +
-                                                        hg / p.G * p.ks_h + key * p.ks_n);
-        const auto* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.v) + bg * p.vs_b +
-                                                        hg / p.G * p.vs_h + key * p.vs_n);
-#pragma unroll 4
-        for (int d = 0; d < D / 8; ++d) {
-          s = dot8(qr[d], kr[d], s);
-          t = dot8(gr[d], vr[d], t);
-        }
-        t *= ex2(fmaf(s, p.c, -lg * kLog2e));
-      }
-#pragma unroll
-      for (int w = 16; w; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
-      if (key / LANES == g) sum = t;
+  for (int u = 0; u < kRowsEach; ++u) {
+    const int n = n0 + u * step, keys = seen(n);
+    x[u] = y[u] = none;
+    few = few || (keys > 0 && keys <= kExactKeys);
+    if (keys > 0) {
+      x[u] = *reinterpret_cast<const uint4*>(o + n * p.os_n);
+      y[u] = *reinterpret_cast<const uint4*>(go + n * p.os_n);
     }
   }
-  if (inside && lane == 0) {
-    const bool none = seen <= 0 || l == kNegInf;
-    const float delta = in.dlse && !none ? sum - in.dlse[bh * p.NQ + n] : sum;
-    row_s[r] = three_bf16(none ? kNoRow : -l / p.scale);
-    row_d[r] = three_bf16(none ? 0.f : -delta);
+  // lanes 0 to 3 write the values of a row each
+  const int own = lane_index<kRowsEach>(lane), n_own = n0 + own * step;
+  const bool sees_own = lane < kRowsEach && seen(n_own) > 0;
+  const float l_own = sees_own ? lse[n_own] : kNegInf, g_own = sees_own && dlse ? dlse[n_own] : 0.f;
+  if (acc) {  // the fused kernel's accumulator starts at zero
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) {
+      acc[(r0 + u * step) * (D / 4) + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+      acc[(r0 + u * step) * (D / 4) + LANES + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  float sums[kRowsEach];
+#pragma unroll
+  for (int u = 0; u < kRowsEach; ++u) sums[u] = dot8(x[u], y[u], 0.f);
+  lane_totals<LANES>(sums, lane);
+  if (lane < kRowsEach) {
+    row_s[r0 + own * step] = three_bf16(l_own == kNegInf ? kNoRow : -l_own * (1.f / p.scale));
+    row_d[r0 + own * step] = three_bf16(l_own == kNegInf ? 0.f : g_own - sums[0]);
+  }
+  if (!__syncthreads_or(few)) return;
+  // the head's first keys, which all such rows see, through shared memory
+  __shared__ uint4 first_k[kExactKeys][LANES], first_v[kExactKeys][LANES];
+  const auto* q = static_cast<const __nv_bfloat16*>(in.q) + b * p.qs_b + h * p.qs_h + lane * 8;
+  const auto* k = static_cast<const __nv_bfloat16*>(in.k) + b * p.ks_b + h / p.G * p.ks_h + lane * 8;
+  const auto* v = static_cast<const __nv_bfloat16*>(in.v) + b * p.vs_b + h / p.G * p.vs_h + lane * 8;
+#pragma unroll
+  for (int i = 0; i < kExactKeys / ROWS; ++i) {
+    const int j = i * ROWS + threadIdx.x / LANES;
+    first_k[j][lane] = j < kl ? *reinterpret_cast<const uint4*>(k + j * p.ks_n) : none;
+    first_v[j][lane] = j < kl ? *reinterpret_cast<const uint4*>(v + j * p.vs_n) : none;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int u = 0; u < kRowsEach; ++u) {
+    const int n = n0 + u * step, sees = seen(n);
+    const int keys = sees <= kExactKeys ? max(sees, 0) : 0;
+    const int most = __reduce_max_sync(0xffffffffu, keys);
+    if (most == 0) continue;
+    uint4 qr = none, gr = none;
+    float lr = kNegInf;
+    if (keys) {
+      qr = *reinterpret_cast<const uint4*>(q + n * p.qs_n);
+      gr = *reinterpret_cast<const uint4*>(go + n * p.os_n);
+      lr = lse[n];
+    }
+    float sum = 0.f;
+    for (int j0 = 0; j0 < most; j0 += kKeysAtOnce) {
+      float t[2 * kKeysAtOnce];
+#pragma unroll
+      for (int j = 0; j < kKeysAtOnce; ++j) {
+        t[2 * j] = dot8(qr, first_k[j0 + j][lane], 0.f);
+        t[2 * j + 1] = dot8(gr, first_v[j0 + j][lane], 0.f);
+      }
+      // a lane and the one kKeysAtOnce further hold a key's q . k and dO . v
+      lane_totals<LANES>(t, lane);
+      const float d = __shfl_xor_sync(0xffffffffu, t[0], kKeysAtOnce);
+      if (j0 + lane_index<kKeysAtOnce>(lane) < keys) sum = fmaf(d, ex2(fmaf(t[0], p.c, -lr * kLog2e)), sum);
+    }
+#pragma unroll
+    for (int w = 1; w < kKeysAtOnce; w *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    if (keys && lane == 0) row_d[r0 + u * step] = three_bf16(lr == kNegInf ? 0.f : (dlse ? dlse[n] : 0.f) - sum);
   }
 }
 
@@ -811,8 +867,8 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBw
   const AttnBwdScratch w = attn_bwd_scratch(p, plan, workspace);
   const long long rows = (long long)p.B * p.H * w.padded;
   auto *row_s = static_cast<uint4*>(w.row_s), *row_d = static_cast<uint4*>(w.row_d);
-  constexpr int row_lanes = D / 8, per_block = 256 / row_lanes;
-  attn_rows_kernel<D><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
+  constexpr int per_block = 256 / (D / 8) * kRowsEach;
+  attn_rows_kernel<D><<<(unsigned)(rows / per_block), 256, 0, st>>>(
       p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc), w.kv_counters, w.n_counters, w.padded);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
