@@ -101,13 +101,15 @@ struct TilePart {
   // The first of the stream's `n` elements that part `rank + next` takes.
   // (n is below 2^24, parts at most 8.)
   __device__ __forceinline__ int from(int n, int next = 0) const {
+    if (parts == 1) return next ? n : 0;
     return (int)((unsigned)n * (unsigned)(rank + next) / (unsigned)parts);
   }
 };
-// Block x of a kind whose tiles [0, whole) are one block each and the later ones `parts`.
-__device__ __forceinline__ TilePart tile_part(unsigned x, unsigned whole, int parts) {
+// Block x of a kind whose tiles [0, whole) are one block each and the later ones `by.d`.
+__device__ __forceinline__ TilePart tile_part(unsigned x, unsigned whole, const FastDiv& by) {
   if (x < whole) return TilePart{(int)x, 0, 1};
-  return TilePart{(int)(whole + (x - whole) / parts), (int)((x - whole) % parts), parts};
+  const unsigned t = by.div(x - whole);
+  return TilePart{(int)(whole + t), (int)(x - whole - t * by.d), (int)by.d};
 }
 // A part is [COLS / 4][128 rows] float4: a warp, whose lanes are rows, writes and reads whole lines.
 template <int COLS>

@@ -234,17 +234,17 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // heads in order (the blocks in flight share one key head's query tiles in L2); within a head the first key
   // tiles, which see the most queries under a causal mask, first.  A small grid: the first key tiles of all heads first
-  const TilePart part = tile_part(blk, plan.kv_whole, plan.kv_parts);
-  const int n_kt = (p.NK + BT - 1) / BT, heads = p.B * p.HK;
-  const int bhk = plan.longest_first ? part.tile % heads : part.tile / n_kt;
-  const int b = bhk / p.HK, hk = bhk % p.HK;
-  const int k0 = (plan.longest_first ? part.tile / heads : part.tile % n_kt) * BT;
+  const TilePart part = tile_part(blk, plan.kv_whole, plan.by_kv_parts);
+  const int x = (int)plan.by_kv_tile.div(part.tile), y = part.tile - x * (int)plan.by_kv_tile.d;
+  const int bhk = plan.longest_first ? y : x, k0 = (plan.longest_first ? x : y) * BT;
+  const int b = (int)plan.by_key_heads.div(bhk), hk = bhk - b * p.HK;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
   const int n_qt = (k0 < kl && q_begin < ql) ? (ql - q_begin + BT - 1) / BT : 0;
   // tile u: head u / n_qt of the group, query tile u % n_qt; this block takes the tiles [u0, u0 + n)
   const int u0 = part.from(p.G * n_qt), n = part.from(p.G * n_qt, 1) - u0;
+  const int head0 = u0 > 0 ? u0 / n_qt : 0, qt0 = u0 - head0 * n_qt;  // of the first
   const bool ragged = n > 0 && ql < p.NQ && (ql & (BT - 1));  // the last query tile has rows past the sequence
 
   const uint32_t bar = sb + L::OFF_BAR;
@@ -254,16 +254,16 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
   volatile int* part_flag = abort_flag + 1;
   // the producer sets the barriers up and issues the first loads while the others get TMEM
-  auto load_q = [&](int u) {
-    const int s = u % SLOTS, hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
+  auto load_q = [&](int u, int hq, int q0) {
+    const int s = u % SLOTS;
     mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
       tma_load_4d(sb + L::OFF_Q + s * L::TILE + h * BT * 128, &maps.q, q_full + 8 * s, h * 64, q0, hq, b);
     bulk_load(sb + L::OFF_RS + s * L::STEP, row_s + ((long long)b * p.H + hq) * padded + q0, L::STEP, q_full + 8 * s);
   };
-  auto load_o = [&](int u) {
-    const int s = u % SLOTS, hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
+  auto load_o = [&](int u, int hq, int q0) {
+    const int s = u % SLOTS;
     mbar_arrive_expect_tx(o_full + 8 * s, L::TILE + L::STEP);
 #pragma unroll
     for (int h = 0; h < D / 64; ++h)
@@ -292,10 +292,10 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
         mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
-        load_q(0);
+        load_q(0, hk * p.G + head0, q_begin + qt0 * BT);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
-        load_o(0);
+        load_o(0, hk * p.G + head0, q_begin + qt0 * BT);
       }
     }
     __syncwarp();  // the warp's other lanes wait for the one that issues
@@ -318,14 +318,18 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (n > 0 && elect_one()) {
-        int issued_q = 1, issued_o = 1;
+        int issued_q = 1, issued_o = 1, hq = hk * p.G + head0, qt = qt0;
         for (int u = 1; u < n; ++u) {
           const int s = u % SLOTS;
+          if (++qt == n_qt) {
+            qt = 0;
+            ++hq;
+          }
           if (u >= SLOTS && !mbar_wait(q_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          load_q(u);
+          load_q(u, hq, q_begin + qt * BT);
           issued_q = u + 1;
           if (u >= SLOTS && !mbar_wait(o_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
-          load_o(u);
+          load_o(u, hq, q_begin + qt * BT);
           issued_o = u + 1;
         }
         mbar_drain(kv_full, 0, status);
@@ -338,7 +342,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     } else if (warp == PATCH_WARP) {
       // for each head's last tile: its Q, then its dO, when the MMA thread has seen them land
       if (ragged) {
-        const int first = n_qt - 1 - u0 % n_qt;  // the first of this block's tiles that is a head's last
+        const int first = n_qt - 1 - qt0;  // the first of this block's tiles that is a head's last
         for (int e = 0; first + e / 2 * n_qt < n; ++e) {
           if (!mbar_wait_warp(to_patch, e & 1, status, abort_flag)) break;
           const int s = (first + e / 2 * n_qt) % SLOTS, from = ql & (BT - 1);
@@ -359,7 +363,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
         const uint64_t ones = sdesc_step(sb + L::OFF_ONES, sb + L::OFF_ZERO);
         int patches = 0;
         auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
-          if (!ragged || (u0 + u + 1) % n_qt) return true;
+          if (!ragged || (qt0 + u + 1) % n_qt) return true;
           mbar_arrive(to_patch);
           return mbar_wait(patched, patches++ & 1, status, abort_flag);
         };
@@ -429,7 +433,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     const uint32_t ts = tmem + lanes + kv::kColS + 32 * grp, tp = tmem + lanes + kv::kColP + 32 * grp;
     bool ok = true;
     const int q_last = q_begin + (n_qt - 1) * BT + 32 * grp;
-    int q0 = q_begin + (n > 0 ? u0 % n_qt : 0) * BT + 32 * grp;  // first query of this warp's columns
+    int q0 = q_begin + qt0 * BT + 32 * grp;  // first query of this warp's columns
     for (int u = 0; u < n; ++u) {
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();
@@ -594,12 +598,11 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = (p.NQ + BT - 1) / BT;
-  const TilePart part = tile_part(blk, plan.q_whole, plan.q_parts);
-  const int heads = p.B * p.H;
-  const int bh = plan.longest_first ? part.tile % heads : part.tile / n_qt;
-  const int b = bh / p.H, h = bh % p.H, hk = h / p.G;
-  // the last query tiles, which see the most keys, first
-  const int q0 = (n_qt - 1 - (plan.longest_first ? part.tile / heads : part.tile % n_qt)) * BT;
+  const TilePart part = tile_part(blk, plan.q_whole, plan.by_q_parts);
+  const int x = (int)plan.by_q_tile.div(part.tile), y = part.tile - x * (int)plan.by_q_tile.d;
+  const int bh = plan.longest_first ? y : x;
+  const int b = (int)plan.by_heads.div(bh), h = bh - b * p.H, hk = (int)plan.by_group.div(h);
+  const int q0 = (n_qt - 1 - (plan.longest_first ? x : y)) * BT;  // the last query tiles, which see the most keys, first
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int last = min(q0 + BT, ql) - 1;
@@ -968,6 +971,13 @@ AttnBwdPlan attn_bwd_plan(const AttnProblem& p, int mode, int num_sms) {
   g.q_blocks = g.q_whole + (g.q_tiles - g.q_whole) * g.q_parts;
   g.longest_first = (long long)g.kv_blocks + g.q_blocks <= (long long)kSmallGrid * num_sms;
   g.q_first = 3.0 * nk / g.q_parts > 4.0 * stream / g.kv_parts;
+  g.by_kv_parts = FastDiv((unsigned)g.kv_parts);
+  g.by_q_parts = FastDiv((unsigned)g.q_parts);
+  g.by_kv_tile = FastDiv((unsigned)(g.longest_first ? p.B * p.HK : nk));
+  g.by_q_tile = FastDiv((unsigned)(g.longest_first ? p.B * p.H : nq));
+  g.by_key_heads = FastDiv((unsigned)p.HK);
+  g.by_heads = FastDiv((unsigned)p.H);
+  g.by_group = FastDiv((unsigned)p.G);
   return g;
 }
 

@@ -84,17 +84,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // heads in order (the blocks in flight share one key head's query tiles and dQ rows in L2); within a head the first
   // key tiles, which see the most queries under a causal mask, first.  A small grid: the first key tiles of all heads
-  const TilePart part = tile_part(blockIdx.x, plan.kv_whole, plan.kv_parts);
-  const int n_kt = (p.NK + BT - 1) / BT, heads = p.B * p.HK;
-  const int bhk = plan.longest_first ? part.tile % heads : part.tile / n_kt;
-  const int b = bhk / p.HK, hk = bhk % p.HK;
-  const int k0 = (plan.longest_first ? part.tile / heads : part.tile % n_kt) * BT;
+  const TilePart part = tile_part(blockIdx.x, plan.kv_whole, plan.by_kv_parts);
+  const int x = (int)plan.by_kv_tile.div(part.tile), y = part.tile - x * (int)plan.by_kv_tile.d;
+  const int bhk = plan.longest_first ? y : x, k0 = (plan.longest_first ? x : y) * BT;
+  const int b = (int)plan.by_key_heads.div(bhk), hk = bhk - b * p.HK;
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
   const int q_begin = p.causal ? max(0, k0 - off) / BT * BT : 0;
   const int n_qt = (k0 < kl && q_begin < ql) ? (ql - q_begin + BT - 1) / BT : 0;
   // tile u: head u / n_qt of the group, query tile u % n_qt; this block takes the tiles [u0, u0 + n)
   const int u0 = part.from(p.G * n_qt), n = part.from(p.G * n_qt, 1) - u0;
+  const int head0 = u0 > 0 ? u0 / n_qt : 0, qt0 = u0 - head0 * n_qt;  // of the first
   const bool ragged_q = n > 0 && ql < p.NQ && (ql & (BT - 1));  // the last query tile has rows past the sequence
   const bool ragged_k = n > 0 && kl < p.NK && kl - k0 < BT;     // so has this key tile
 
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
           tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
         }
-        int issued_q = 0, issued_o = 0;
+        int issued_q = 0, issued_o = 0, hq = hk * p.G + head0, qt = qt0;
         for (int u = 0; u < n; ++u) {
-          const int s = u % SLOTS, hq = hk * p.G + (u0 + u) / n_qt, q0 = q_begin + ((u0 + u) % n_qt) * BT;
+          const int s = u % SLOTS, q0 = q_begin + qt * BT;
           const long long row = ((long long)b * p.H + hq) * padded + q0;
           if (u >= SLOTS && !mbar_wait(q_empty + 8 * s, ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
           mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
@@ -169,6 +169,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             tma_load_4d(sb + L::OFF_O + s * L::TILE + h * BT * 128, &maps.go, o_full + 8 * s, h * 64, q0, hq, b);
           bulk_load(sb + L::OFF_RD + s * L::STEP, row_d + row, L::STEP, o_full + 8 * s);
           issued_o = u + 1;
+          if (++qt == n_qt) {
+            qt = 0;
+            ++hq;
+          }
         }
         mbar_drain(kv_full, 0, status);
         for (int u = max(0, issued_q - SLOTS); u < issued_q; ++u) mbar_drain(q_full + 8 * (u % SLOTS), (u / SLOTS) & 1, status);
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       // for each head's last tile: its Q, then its dO, when the MMA thread has seen them land
-      const int first = n > 0 ? n_qt - 1 - u0 % n_qt : 0;  // the first of this block's tiles that is a head's last
+      const int first = n_qt - 1 - qt0;  // the first of this block's tiles that is a head's last
       for (int e = 0; ok && ragged_q && first + e / 2 * n_qt < n; ++e) {
         if (!(ok = mbar_wait_warp(to_patch, e & 1, status, abort_flag))) break;
         const int u = first + e / 2 * n_qt;
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t ones = sdesc_step(sb + L::OFF_ONES, sb + L::OFF_ZERO);
         int patches = 0;
         auto patch = [&](int u) {  // the head's last tile: wait until its rows past the sequence are cleared
-          if (!ragged_q || (u0 + u + 1) % n_qt) return true;
+          if (!ragged_q || (qt0 + u + 1) % n_qt) return true;
           mbar_arrive(to_patch);
           return mbar_wait(patched, patches++ & 1, status, abort_flag);
         };
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tq = tmem + ((uint32_t)(wq * 32) << 16) + kQ;
     const uint32_t ring = sb + L::OFF_STAGE + (warp - DS_WARPS) * RING * CHUNK_BYTES;
     int at = 0;                          // ring position
-    int hq = hk * p.G + (n > 0 ? u0 / n_qt : 0), q0 = q_begin + (n > 0 ? u0 % n_qt : 0) * BT;
+    int hq = hk * p.G + head0, q0 = q_begin + qt0 * BT;
     for (int u = 0; u < n; ++u) {
       const bool ok = mbar_wait_warp(dq_full, u & 1, status, abort_flag);
       __syncwarp();
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     const int q_last = q_begin + (n_qt - 1) * BT + 32 * grp;
-    int q0 = q_begin + (n > 0 ? u0 % n_qt : 0) * BT + 32 * grp;  // first query of this warp's columns
+    int q0 = q_begin + qt0 * BT + 32 * grp;  // first query of this warp's columns
     for (int u = 0; ok && u < n; ++u) {
       ok = mbar_wait_warp(s_full, u & 1, status, abort_flag);
       __syncwarp();

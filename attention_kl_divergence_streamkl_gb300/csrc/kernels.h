@@ -94,6 +94,20 @@ cudaError_t launch_rows_to_bf16(const Problem& p, const float* acc, void* out, c
 int fused_first_qtile(const Problem& p, long long k0);
 
 // ---- attention -----------------------------------------------------------------------
+// Division of n < 2^31 by a number that the host knows, by multiplication (Granlund and Montgomery): with s = ceil(log2 d)
+// and mul = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, mul) + n) >> s.
+struct FastDiv {
+  unsigned d = 1, mul = 1, shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(unsigned by) : d(by), shift(0) {
+    while ((1ull << shift) < by) ++shift;
+    mul = (unsigned)((((1ull << shift) - by) << 32) / by + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
+
 struct AttnProblem {
   int B, H, HK, G, NQ, NK, D;  // G = H / HK query heads to a key head
   int causal;                  // row i keeps key j iff j <= i + k_len - q_len
@@ -107,6 +121,7 @@ struct AttnProblem {
   int q_items;  // blocks along the queries, per (batch, head)
   int splits;   // blocks along the keys
   int longest_first;  // the last query tiles of all heads first, not head by head
+  FastDiv by_splits, by_items, by_heads, by_group;  // by_items: what an item's number is first divided by
 };
 void attn_fwd_plan(AttnProblem* p, int num_sms);
 long long attn_fwd_items(const AttnProblem& p);
@@ -127,6 +142,8 @@ struct AttnBwdPlan {
   int kv_parts, q_parts;
   int q_first;        // which kind comes first in the grid
   int longest_first;  // the longest tiles of all heads first, not head by head
+  // of a block's number by parts, of a tile's by what it is first divided by, of a (batch, head) by heads, of a head by G
+  FastDiv by_kv_parts, by_q_parts, by_kv_tile, by_q_tile, by_key_heads, by_heads, by_group;
 };
 // Where things lie in the workspace.
 struct AttnBwdScratch {
