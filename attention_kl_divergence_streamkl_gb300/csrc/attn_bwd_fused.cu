@@ -35,7 +35,9 @@ constexpr int D = 64;
 constexpr int DS_WARPS = 16, DQ_WARPS = 4;
 constexpr int PRODUCER_WARP = 20, MMA_WARP = 21, PATCH_WARP = 22;
 constexpr int THREADS = 24 * 32;
-constexpr int kRegsDs = 80, kRegsDq = 88, kRegsOther = 72;  // 512 * 80 + 128 * 88 + 128 * 72 = 768 * 80 at launch
+// 512 * 80 + 128 * 88 + 128 * 72 = 768 * 80 registers at launch; the P and dS warps keep their 80 (an inc to the count that a
+// warp has already is not described)
+constexpr int kRegsDq = 88, kRegsOther = 72;
 constexpr uint32_t kTmemCols = 512;
 
 struct Maps {
@@ -332,7 +334,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   } else {
-    setmaxnreg_inc<kRegsDs>();
     // ---------------------------------------------------------------- P and dS
     const int grp = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
