@@ -914,7 +914,7 @@ bool attn_bwd_has_fused(const AttnProblem& p) { return p.D == 64; }
 //   fused     the tiles of the last, incomplete wave are dealt out so that it fills the SMs (non-causal: a causal grid's
 //             short blocks fill the end by themselves).
 // In a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for).
-constexpr int kBlockCost = 16, kPartCost = 8;
+constexpr int kBlockCost = 12, kPartCost = 4;
 constexpr int kMaxParts = 8;
 constexpr int kMinPartTiles = 4;
 constexpr int kSmallGrid = 6;

@@ -16,7 +16,8 @@
 // take in DRAM time, so for 16-bit types a vector's maximum and its guard against
 // -inf work on packed pairs (raised to -1e30, or fp16's lowest, where that times
 // scale still has weight 0), and the fp32 arithmetic on pairs too: 4.5 issue slots
-// a logit against 7 (8192 x 131072 bf16 logits with 8 alternatives: 385 -> FIG us).
+// a logit against 7.  8192 x 131072 bf16 logits with 8 alternatives take 320 us, 6.7 TB/s; 8 such rows 7.6 us, most of it the
+// alternatives' chain of barriers (4.0 us without them).
 //
 // Top alternatives, also without sorting the row: the largest value of each
 // group of four vectors is a by-product of the pass, kept in shared memory, and so is a
@@ -45,6 +46,9 @@ namespace {
 constexpr int kMaxCand = 512;      // candidate keys a block ranks
 constexpr float kFloor = -256.0f;  // 2^-256 is 0 in fp32
 constexpr int kUnroll = 4;         // 16-byte loads a thread has in flight
+// The forward's threads on an SM: 40 registers each.  With 2048 and 32 the loop that reads spills (4096 x 131072 bf16, no
+// alternatives: 167 against 161 us).
+constexpr int kThreadsPerSm = 1536;
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -104,32 +108,19 @@ struct Sums {
   float m, s, t;
 };
 
-__device__ __forceinline__ void merge(Sums& a, const Sums& b) {
-  if (b.m == kNegInf && b.s == 0.f) return;  // nothing seen (a NaN in b.s goes on)
-  const float m = fmaxf(a.m, b.m);
-  const float z = m == kNegInf ? 0.f : m;
-  const float da = max_nan(a.m - z, kFloor), db = max_nan(b.m - z, kFloor);
-  const float wa = ex2(da), wb = ex2(db);
-  a.t = wa * (a.t + a.s * da) + wb * (b.t + b.s * db);
-  a.s = wa * a.s + wb * b.s;
-  a.m = m;
-}
-
-// The sums of the warp's first N lanes, on all of them.  The same operand order on both sides of an exchange keeps the
-// lanes' results equal.
+// The sums of N lanes (of the warp's first N, which the others repeat), on all of them: one common maximum, then plain
+// sums, equal on both sides of every exchange.
 template <int N>
 __device__ __forceinline__ void merge_lanes(Sums& a) {
-  const int lane = threadIdx.x & 31;
+  const float m = value_of(__reduce_max_sync(0xffffffffu, order_of(a.m)));
+  const float d = max_nan(a.m - (m == kNegInf ? 0.f : m), kFloor), w = ex2(d);
+  a.m = m;
+  a.t = w * (a.t + a.s * d);
+  a.s *= w;
 #pragma unroll
   for (int o = N / 2; o; o >>= 1) {
-    Sums b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-           __shfl_xor_sync(0xffffffffu, a.t, o)};
-    if (lane & o) {
-      const Sums c = a;
-      a = b;
-      b = c;
-    }
-    merge(a, b);
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
   }
 }
 
@@ -242,7 +233,7 @@ struct FwdArgs {
   const long long* tokens;
   float *logp, *entropy, *lse, *top_logp;
   long long* top_index;
-  int V, T, K, parts;
+  int V, T, K, parts, log_parts;
   float scale;
 };
 
@@ -286,6 +277,27 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int K, ui
   }
 }
 
+// The same for `lists` (at most eight) sorted lists of K keys, one after the other; 0 is no key.  A lane searches a list.
+template <int NT>
+__device__ __forceinline__ void rank_lists(const uint64_t* keys, int lists, int K, uint64_t* out) {
+  const int q = threadIdx.x % 8;
+  for (int i0 = 0; i0 < lists * K; i0 += NT / 8) {
+    const int i = i0 + threadIdx.x / 8;
+    const uint64_t k = i < lists * K ? keys[i] : 0;
+    int place = 0, end = q < lists ? K : 0;
+    while (place < end) {
+      const int mid = (place + end) / 2;
+      if (keys[q * K + mid] > k)
+        place = mid + 1;
+      else
+        end = mid;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (k && q == 0 && place < K) out[place] = k;
+  }
+}
+
 // The block's K largest keys of columns [lo, hi), for any values: each warp reads a contiguous share in order and
 // keeps its K best sorted over its lanes.
 template <typename T, int NT>
@@ -323,16 +335,16 @@ __device__ void warp_lists(const T* row, int lo, int hi, int K, FwdShared<NT>& s
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(NT, kThreadsPerSm / NT) logprobs_fwd_kernel(const FwdArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int NW = NT / 32;
   __shared__ FwdShared<NT> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int part = (int)(blockIdx.x % a.parts);
-  const long long r = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x & (a.parts - 1u));
+  const long long r = blockIdx.x >> a.log_parts;
   const T* row = static_cast<const T*>(a.logits) + r * a.stride;
   const Cut cut = cut_row(row, a.V);
-  const int v0 = (int)((long long)cut.nvec * part / a.parts), v1 = (int)((long long)cut.nvec * (part + 1) / a.parts);
+  const int v0 = (int)((long long)cut.nvec * part >> a.log_parts), v1 = (int)((long long)cut.nvec * (part + 1) >> a.log_parts);
   const int nv = v1 - v0;
   const uint4* vecs = reinterpret_cast<const uint4*>(row + cut.head) + v0;
   const bool first = part == 0, last = part == a.parts - 1;
@@ -383,6 +395,12 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdAr
       acc.t.x = fmaf(e, d, acc.t.x);
       if (a.K) sh.cand[atomicAdd(&sh.n_cand, 1)] = key_of(f, (uint32_t)j);  // at most 2 (N - 1) of them
     }
+  }
+  long long tok0 = -1;  // this thread's first given token and its logit, on their way meanwhile
+  float raw0 = 0.f;
+  if (first && tid < a.T) {
+    tok0 = a.tokens[r * a.T + tid];
+    if (tok0 >= 0 && tok0 < a.V) raw0 = to_float(row[tok0]);
   }
   Sums sums{acc.m, acc.s.x + acc.s.y, acc.t.x + acc.t.y};
   merge_lanes<32>(sums);
@@ -464,8 +482,8 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdAr
     __syncthreads();
   if (part != 0) return;
 
-  Sums all = sh.part_sums[0];
-  for (int q = 1; q < a.parts; ++q) merge(all, sh.part_sums[q]);
+  Sums all = lane % 8 < a.parts ? sh.part_sums[lane % 8] : Sums{kNegInf, 0.f, 0.f};
+  merge_lanes<8>(all);
   const bool empty = all.m == kNegInf && all.s == 0.f;  // every logit is -inf
   const float log2s = log2f(all.s);
   const float lse = empty ? kNegInf : kLn2 * (all.m + log2s);
@@ -475,23 +493,16 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_fwd_kernel(const FwdAr
   }
   auto log_prob = [&](float raw) { return empty ? kNegInf : fmaf(raw, a.scale, -lse); };
   for (int t = tid; t < a.T; t += NT) {
-    const long long tok = a.tokens[r * a.T + t];
+    const long long tok = t == tid ? tok0 : a.tokens[r * a.T + t];
     float out = 0.f;  // no token
     if (tok >= a.V) out = __uint_as_float(0x7fffffffu);
-    else if (tok >= 0) out = log_prob(to_float(row[tok]));
+    else if (tok >= 0) out = log_prob(t == tid ? raw0 : to_float(row[tok]));
     a.logp[r * a.T + t] = out;
   }
   if (a.K) {
     uint64_t* order = sh.best;
     if (a.parts > 1) {
-      const int n = a.parts * a.K;
-      for (int i = tid; i < n; i += NT) {
-        const uint64_t k = sh.best[i];
-        if (!k) continue;
-        int place = 0;
-        for (int j = 0; j < n; ++j) place += sh.best[j] > k;
-        if (place < a.K) sh.cand[place] = k;
-      }
+      rank_lists<NT>(sh.best, a.parts, a.K, sh.cand);
       __syncthreads();
       order = sh.cand;
     }
@@ -509,7 +520,7 @@ struct BwdArgs {
   const long long* tokens;
   const float *lse, *entropy, *g_logp, *g_entropy;
   void* out;
-  int V, T, parts;
+  int V, T, parts, log_parts;
   float scale;
 };
 
@@ -522,8 +533,8 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdAr
   constexpr int N = Vec<T>::N;
   __shared__ float sum_g[NT / 32];
   const int tid = threadIdx.x;
-  const int part = (int)(blockIdx.x % a.parts);
-  const long long r = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x & (a.parts - 1u));
+  const long long r = blockIdx.x >> a.log_parts;
   const T* row = static_cast<const T*>(a.logits) + r * a.stride;
   T* out = static_cast<T*>(a.out) + r * a.out_stride;
   const long long* tokens = a.tokens + r * a.T;
@@ -558,7 +569,7 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdAr
   const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
   int lo, hi;  // this block's columns
   if (same) {
-    const int v0 = (int)((long long)cut.nvec * part / a.parts), v1 = (int)((long long)cut.nvec * (part + 1) / a.parts);
+    const int v0 = (int)((long long)cut.nvec * part >> a.log_parts), v1 = (int)((long long)cut.nvec * (part + 1) >> a.log_parts);
     lo = part == 0 ? 0 : cut.head + v0 * N;
     hi = part == a.parts - 1 ? a.V : cut.head + v1 * N;
     const uint4* in = reinterpret_cast<const uint4*>(row + cut.head);
@@ -583,8 +594,8 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdAr
     if (part == a.parts - 1 && cut.tail0 + tid < a.V)
       out[cut.tail0 + tid] = from_float<T>(grad(to_float(row[cut.tail0 + tid])));
   } else {
-    lo = (int)((long long)a.V * part / a.parts);
-    hi = (int)((long long)a.V * (part + 1) / a.parts);
+    lo = (int)((long long)a.V * part >> a.log_parts);
+    hi = (int)((long long)a.V * (part + 1) >> a.log_parts);
     for (int j = lo + tid; j < hi; j += NT) out[j] = from_float<T>(grad(to_float(row[j])));
   }
   if (empty) return;
@@ -606,14 +617,20 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdAr
 // Blocks that share a row: as many (a power of two, at most 8, the portable cluster size) as keep the launch within
 // two blocks for each SM, and no part below kMinPartBytes.
 constexpr long long kMinPartBytes = 8192;
-int parts_of(long long rows, long long row_bytes, int num_sms) {
-  int parts = 1;
-  while (parts < 8 && rows * parts * 2 <= 2ll * num_sms && row_bytes / (parts * 2) >= kMinPartBytes) parts *= 2;
-  return parts;
+int log_parts_of(long long rows, long long row_bytes, int num_sms) {
+  int n = 0;
+  while (n < 3 && (rows << (n + 1)) <= 2ll * num_sms && (row_bytes >> (n + 1)) >= kMinPartBytes) ++n;
+  return n;
 }
 
-// Threads of a block: 128 for short rows, where 512 would hold no vector.
-constexpr long long kShortRowBytes = 8192;
+// Threads of a block: 128 for short rows, where 512 would hold no vector.  The forward's longer rows: 512 where all blocks
+// are resident at once, so that a row is read soon; fewer where they are not, since a block that ends then makes room in
+// smaller pieces, and the blocks' searches for the alternatives overlap with more blocks' reading: 128 up to
+// kFwdMidRowBytes, 256 above, where a thread of 128 would have too many groups.  In us with 512 / 256 / 128 threads:
+// 8192 x 32000 bf16, 8 alternatives, 163 / 120 / 109; 5000 x 64000, 5: - / 118 / 110; 4096 x 131072, 8: 180 / 172 / 188;
+// 333 x 50021 fp32, 16: 17.1 / 19.6 / -.  The gradient: 256 up to kBwdMidRowBytes (8192 x 32000 169 -> 164), 512 above
+// (5000 x 64000 198 against 204).
+constexpr long long kShortRowBytes = 8192, kFwdMidRowBytes = 144 * 1024, kBwdMidRowBytes = 96 * 1024;
 
 template <typename T, int NT>
 cudaError_t launch_fwd_nt(const FwdArgs& a, long long rows, cudaStream_t st) {
@@ -633,16 +650,23 @@ cudaError_t launch_fwd_nt(const FwdArgs& a, long long rows, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_fwd_t(FwdArgs a, long long rows, int num_sms, cudaStream_t st) {
   const long long bytes = (long long)a.V * sizeof(T);
-  a.parts = parts_of(rows, bytes, num_sms);
-  return bytes <= kShortRowBytes ? launch_fwd_nt<T, 128>(a, rows, st) : launch_fwd_nt<T, 512>(a, rows, st);
+  a.log_parts = log_parts_of(rows, bytes, num_sms);
+  a.parts = 1 << a.log_parts;
+  if (bytes <= kShortRowBytes) return launch_fwd_nt<T, 128>(a, rows, st);
+  if (rows * a.parts > (long long)num_sms * (kThreadsPerSm / 512))
+    return bytes <= kFwdMidRowBytes ? launch_fwd_nt<T, 128>(a, rows, st) : launch_fwd_nt<T, 256>(a, rows, st);
+  return launch_fwd_nt<T, 512>(a, rows, st);
 }
 
 template <typename T>
 cudaError_t launch_bwd_t(BwdArgs a, long long rows, int num_sms, cudaStream_t st) {
   const long long bytes = (long long)a.V * sizeof(T);
-  a.parts = parts_of(rows, bytes, num_sms);
+  a.log_parts = log_parts_of(rows, bytes, num_sms);
+  a.parts = 1 << a.log_parts;
   if (bytes <= kShortRowBytes)
     logprobs_bwd_kernel<T, 128><<<(unsigned)(rows * a.parts), 128, 0, st>>>(a);
+  else if (bytes <= kBwdMidRowBytes)
+    logprobs_bwd_kernel<T, 256><<<(unsigned)(rows * a.parts), 256, 0, st>>>(a);
   else
     logprobs_bwd_kernel<T, 512><<<(unsigned)(rows * a.parts), 512, 0, st>>>(a);
   return cudaGetLastError();
@@ -653,7 +677,7 @@ cudaError_t launch_bwd_t(BwdArgs a, long long rows, int num_sms, cudaStream_t st
 cudaError_t launch_logprobs_fwd(const LogprobsProblem& p, const void* logits, const long long* tokens, float* logp,
                                 float* entropy, float* lse, float* top_logp, long long* top_index, int num_sms,
                                 cudaStream_t st) {
-  FwdArgs a{logits, p.stride, tokens, logp, entropy, lse, top_logp, top_index, p.V, p.T, p.K, 1, p.scale};
+  FwdArgs a{logits, p.stride, tokens, logp, entropy, lse, top_logp, top_index, p.V, p.T, p.K, 1, 0, p.scale};
   if (p.dtype == kTypeBf16) return launch_fwd_t<__nv_bfloat16>(a, p.rows, num_sms, st);
   if (p.dtype == kTypeFp16) return launch_fwd_t<__half>(a, p.rows, num_sms, st);
   return launch_fwd_t<float>(a, p.rows, num_sms, st);
@@ -662,7 +686,7 @@ cudaError_t launch_logprobs_fwd(const LogprobsProblem& p, const void* logits, co
 cudaError_t launch_logprobs_bwd(const LogprobsProblem& p, const void* logits, const long long* tokens,
                                 const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
                                 void* dlogits, long long out_stride, int num_sms, cudaStream_t st) {
-  BwdArgs a{logits, p.stride, out_stride, tokens, lse, entropy, g_logp, g_entropy, dlogits, p.V, p.T, 1, p.scale};
+  BwdArgs a{logits, p.stride, out_stride, tokens, lse, entropy, g_logp, g_entropy, dlogits, p.V, p.T, 1, 0, p.scale};
   if (p.dtype == kTypeBf16) return launch_bwd_t<__nv_bfloat16>(a, p.rows, num_sms, st);
   if (p.dtype == kTypeFp16) return launch_bwd_t<__half>(a, p.rows, num_sms, st);
   return launch_bwd_t<float>(a, p.rows, num_sms, st);
