@@ -38,20 +38,21 @@ constexpr int SOFTMAX_WARPS = 8;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, PATCH_WARP = 10;
 constexpr int THREADS = 12 * 32;
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // 256 * 200 + 128 * 104 = 384 * 168 at launch
-constexpr int SLOTS = 5;                            // ring of K and V tiles
 constexpr uint32_t kTmemCols = 512;
 constexpr int kFreshTiles = 16;  // see attn_fwd_kernel's FRESH
 constexpr float kSumLimit = 18446744073709551616.0f;  // 2^64
-constexpr uint32_t kColS = 0, kColO = 256;           // tile t: + 128 t
 
 template <int D>
 struct Smem {
+  static constexpr int SLOTS = D == 64 ? 8 : 5;  // ring of K and V tiles
+  static constexpr int S_BUFS = D == 64 ? 3 : 2;
   static constexpr int TILE = 128 * D * 2;
   static constexpr int OFF_Q = 0;  // Q_A, Q_B
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
-  // q_full[2], kv_full[5], kv_empty[5], s_full[2], p_ready[2], o_done[2], to_patch, patched; TMEM slot, abort flag
-  static constexpr int BAR_SLOT = 8 * 20;
+  // q_full[2], kv_full[SLOTS], kv_empty[SLOTS], s_full[S_BUFS], p_ready[S_BUFS], o_done[S_BUFS], to_patch, patched; TMEM
+  // slot, abort flag
+  static constexpr int BAR_SLOT = 8 * (4 + 2 * SLOTS + 3 * S_BUFS);
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
 };
 static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
@@ -89,6 +90,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
   using L = Smem<D>;
+  constexpr int SLOTS = L::SLOTS, S_BUFS = L::S_BUFS;
+  constexpr uint32_t kColO = 128 * S_BUFS;  // O_B follows O_A; S buffer i at 128 i
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
@@ -131,13 +134,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
   const int nA = key_tiles(0), nB = key_tiles(1);
   const int n = max(nA, nB);
+  // A pair's three barriers (S there, P there, its product done) go with its S buffer: nobody can be two uses behind or
+  // ahead of one, as the phases' parities require.
+  // The tile pairs in the order in which they are worked on: A0, B0, A1, B1, ... and then what is left of the longer tile.
+  const int both = min(nA, nB);
+  auto pair_of = [&](int t, int i) { return i < both ? 2 * i + t : both + i; };
+  auto buf_of = [&](int t, int i) { return S_BUFS == 2 ? t : pair_of(t, i) % 3; };       // its S buffer,
+  auto use_of = [&](int t, int i) { return S_BUFS == 2 ? i : pair_of(t, i) / 3; };       // and how often it was used before
   const bool has_b = !p.packed && q0 + BM < p.NQ;
   // the V tile that a sequence ends inside: its rows past the end may hold anything, and 0 * NaN is NaN
   const int patch_i = (kl < p.NK && (kl & (BN - 1))) ? (kl / BN) - kt0 : -1;
 
   const uint32_t bar = sb + L::OFF_BAR;
   const uint32_t q_full = bar, kv_full = bar + 16, kv_empty = kv_full + 8 * SLOTS, s_full = kv_empty + 8 * SLOTS,
-                 p_ready = s_full + 16, o_done = p_ready + 16, to_patch = o_done + 16, patched = to_patch + 8;
+                 p_ready = s_full + 8 * S_BUFS, o_done = p_ready + 8 * S_BUFS, to_patch = o_done + 8 * S_BUFS, patched = to_patch + 8;
   const uint32_t slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
@@ -155,9 +165,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (elect_one()) {
       for (int t = 0; t < 2; ++t) {
         mbar_init(q_full + 8 * t, 1);
-        mbar_init(s_full + 8 * t, 1);
-        mbar_init(p_ready + 8 * t, SOFTMAX_WARPS / 2);
-        mbar_init(o_done + 8 * t, 1);
+      }
+      for (int s = 0; s < S_BUFS; ++s) {
+        mbar_init(s_full + 8 * s, 1);
+        mbar_init(p_ready + 8 * s, SOFTMAX_WARPS / 2);
+        mbar_init(o_done + 8 * s, 1);
       }
       for (int s = 0; s < SLOTS; ++s) {
         mbar_init(kv_full + 8 * s, 1);
@@ -229,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int nt[2] = {nA, nB};
         bool ok = true;
         auto issue_s = [&](int t, int i) {  // S_t(i) = Q_t K(i)^T
-          const int u = 2 * i, s = u % SLOTS;
+          const int u = 2 * i, s = u % SLOTS, buf = buf_of(t, i);
           if (i == 0 && !mbar_wait(q_full + 8 * t, 0, status, abort_flag)) return false;
           if (!mbar_wait(kv_full + 8 * s, (u / SLOTS) & 1, status, abort_flag)) return false;
           tc_fence_after();
@@ -238,9 +250,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-            mma_ss(tmem + kColS + 128 * t, sdesc_add(qd, o), sdesc_add(kd, o), id_s, ks > 0);
+            mma_ss(tmem + 128 * buf, sdesc_add(qd, o), sdesc_add(kd, o), id_s, ks > 0);
           }
-          mma_commit(s_full + 8 * t);
+          mma_commit(s_full + 8 * buf);
           if (t == 1 || i >= nB) mma_commit(kv_empty + 8 * s);  // K(i) is read by no later tile
           return true;
         };
@@ -251,30 +263,42 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (t == 0 || i >= nA) mbar_arrive(to_patch);  // the first of the tiles that read it
             if (!mbar_wait(patched, 0, status, abort_flag)) return false;
           }
-          if (!mbar_wait(p_ready + 8 * t, i & 1, status, abort_flag)) return false;
+          const int buf = buf_of(t, i);
+          if (!mbar_wait(p_ready + 8 * buf, use_of(t, i) & 1, status, abort_flag)) return false;
           tc_fence_after();
           const uint64_t vd = sdesc_sw128(sb + L::OFF_KV + s * L::TILE, BN * 128, 1024);
 #pragma unroll
           for (int ks = 0; ks < BN / 16; ++ks)
-            mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * ks, sdesc_add(vd, ks * 2048), id_o,
-                   i > 0 || ks > 0);
+            mma_ts(tmem + kColO + D * t, tmem + 128 * buf + 8 * ks, sdesc_add(vd, ks * 2048), id_o, i > 0 || ks > 0);
           if (t == 1 || i >= nB) mma_commit(kv_empty + 8 * s);
-          mma_commit(o_done + 8 * t);  // last: the block leaves once it has arrived
+          mma_commit(o_done + 8 * buf);  // last: the block leaves once it has arrived
           return true;
         };
         // tile A has the key tiles [0, nA), tile B [0, nB); B is the last to read a tile both have, and where
         // only A reads it (i >= nB) A is.  Where only B reads it (i >= nA) the same rule holds.
-        for (int t = 0; ok && t < 2; ++t)
-          if (nt[t] > 0) ok = issue_s(t, 0);
-        for (int i = 0; ok && i < n; ++i) {
-          for (int t = 0; ok && t < 2; ++t) {
-            if (i < nt[t]) ok = issue_o(t, i);
-            if (ok && i + 1 < nt[t]) ok = issue_s(t, i + 1);
+        if constexpr (S_BUFS == 3) {
+          // S runs three tile pairs ahead: its buffer is free when the product three pairs before has been issued
+          const int all = nA + nB, longer = nA > nB ? 0 : 1;
+          auto tile_of = [&](int k) { return k < 2 * both ? k & 1 : longer; };
+          auto key_of = [&](int k) { return k < 2 * both ? k >> 1 : k - both; };
+          for (int k = 0; ok && k < min(3, all); ++k) ok = issue_s(tile_of(k), key_of(k));
+          for (int k = 0; ok && k < all; ++k) {
+            ok = issue_o(tile_of(k), key_of(k));
+            if (ok && k + 3 < all) ok = issue_s(tile_of(k + 3), key_of(k + 3));
+          }
+        } else {
+          for (int t = 0; ok && t < 2; ++t)
+            if (nt[t] > 0) ok = issue_s(t, 0);
+          for (int i = 0; ok && i < n; ++i) {
+            for (int t = 0; ok && t < 2; ++t) {
+              if (i < nt[t]) ok = issue_o(t, i);
+              if (ok && i + 1 < nt[t]) ok = issue_s(t, i + 1);
+            }
           }
         }
         if (ok)
           for (int t = 0; t < 2; ++t)
-            if (nt[t] > 0) mbar_drain(o_done + 8 * t, (nt[t] - 1) & 1, status);
+            if (nt[t] > 0) mbar_drain(o_done + 8 * buf_of(t, nt[t] - 1), use_of(t, nt[t] - 1) & 1, status);
       }
       __syncwarp();
     }
@@ -290,12 +314,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool real = p.packed ? (t == 0 && g < p.G) : (qn < p.NQ);
     const int row_end = (real && qn < ql) ? (p.causal ? min(kl, qn + off + 1) : kl) : 0;  // keys this row sees
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t ts = tmem + lanes + kColS + 128 * t, to = tmem + lanes + kColO + 128 * t;
+    const uint32_t to = tmem + lanes + kColO + D * t;
     const float c = p.c;
     float m = kNegInf, l = 0.f;
     bool ok = true, started = false;  // started: some row of the warp has a reference
     for (int i = 0; i < nt; ++i) {
-      ok = mbar_wait_warp(s_full + 8 * t, i & 1, status, abort_flag);
+      const int buf = buf_of(t, i);
+      const uint32_t ts = tmem + lanes + 128 * buf;
+      ok = mbar_wait_warp(s_full + 8 * buf, use_of(t, i) & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
       tc_fence_after();
@@ -345,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (FRESH) started = __any_sync(0xffffffffu, m != kNegInf);
         sum = row_exps(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk);
         if (i > 0) {
-          ok = mbar_wait_warp(o_done + 8 * t, (i - 1) & 1, status, abort_flag);
+          ok = mbar_wait_warp(o_done + 8 * buf_of(t, i - 1), use_of(t, i - 1) & 1, status, abort_flag);
           __syncwarp();
           if (!ok) break;
           tc_fence_after();
@@ -366,10 +392,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready + 8 * t);
+      if (lane == 0) mbar_arrive(p_ready + 8 * buf);
     }
     if (nt > 0 && ok) {
-      ok = mbar_wait_warp(o_done + 8 * t, (nt - 1) & 1, status, abort_flag);
+      ok = mbar_wait_warp(o_done + 8 * buf_of(t, nt - 1), use_of(t, nt - 1) & 1, status, abort_flag);
       __syncwarp();
     }
     if (t == 0 || has_b) {
