@@ -461,37 +461,77 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Merges the splits' (m, l, O): one warp per row, a lane takes D / 32 columns.
+// Merges the splits' (m, l, O), a block to a row: the weights with a thread to a split, then O with a warp to every fourth
+// split, whose first loads are on their way before the weights are known.  Bound by the two trips to L2 (a warp to a row
+// with one split after the other took 16 us for 19 splits, this 4).
+constexpr int kMergeWarps = 4, kMergeAhead = 4;
+constexpr int kMaxSplits = 1024;  // the plan makes at most four blocks an SM
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kMergeWarps * 32)
     attn_merge_kernel(const AttnProblem p, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
                       __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse) {
-  constexpr int W = D / 32;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= p.rows) return;
+  constexpr int W = D / 32;  // columns of a lane
+  struct alignas(W * 4) Cols {
+    float x[W];
+  };
+  __shared__ float weight[kMaxSplits], warp_m[kMergeWarps], warp_l[kMergeWarps];
+  __shared__ Cols sums[kMergeWarps][32];
+  const long long row = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto load = [&](int s) { return *(reinterpret_cast<const Cols*>(part_o + ((size_t)s * p.rows + row) * D) + lane); };
+  Cols first[kMergeAhead];
+#pragma unroll
+  for (int k = 0; k < kMergeAhead; ++k)
+    if (warp + k * kMergeWarps < p.splits) first[k] = load(warp + k * kMergeWarps);
   float m = kNegInf;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part_ml[(size_t)s * p.rows + row].x);
-  float l = 0.f, o[W];
+  for (int s = threadIdx.x; s < p.splits; s += kMergeWarps * 32) m = fmaxf(m, part_ml[(size_t)s * p.rows + row].x);
 #pragma unroll
-  for (int k = 0; k < W; ++k) o[k] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
+  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  if (lane == 0) warp_m[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, warp_m[w]);
+  float l = 0.f;
+  for (int s = threadIdx.x; s < p.splits; s += kMergeWarps * 32) {
     const float2 ml = part_ml[(size_t)s * p.rows + row];
-    if (ml.x == kNegInf && ml.y == 0.f) continue;  // this split has no key for the row
-    const float w = ml.x == m ? 1.f : ex2(ml.x - m);
-    l += w * ml.y;
-    const float* src = part_o + ((size_t)s * p.rows + row) * D + lane * W;
-#pragma unroll
-    for (int k = 0; k < W; ++k) o[k] += w * src[k];
+    const bool none = ml.x == kNegInf && ml.y == 0.f;  // this split has no key for the row
+    const float w = none ? 0.f : ml.x == m ? 1.f : ex2(ml.x - m);
+    weight[s] = w;
+    l += none ? 0.f : w * ml.y;
   }
+#pragma unroll
+  for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  if (lane == 0) warp_l[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) l += warp_l[w];
+  Cols o{};
+  auto add = [&](int s, const Cols& x) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) o.x[i] = fmaf(weight[s], x.x[i], o.x[i]);
+  };
+#pragma unroll
+  for (int k = 0; k < kMergeAhead; ++k)
+    if (warp + k * kMergeWarps < p.splits) add(warp + k * kMergeWarps, first[k]);
+  for (int s = warp + kMergeAhead * kMergeWarps; s < p.splits; s += kMergeWarps) add(s, load(s));
+  sums[warp][lane] = o;
+  __syncthreads();
   const bool none = l == 0.f;
+  if (threadIdx.x == 0) out_lse[row] = none ? kNegInf : (m + log2f(l)) * kLn2;
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    const Cols x = sums[w][lane];
+#pragma unroll
+    for (int i = 0; i < W; ++i) o.x[i] += x.x[i];
+  }
   const float inv = none ? 0.f : 1.f / l;
-  if (lane == 0) out_lse[row] = none ? kNegInf : (m + log2f(l)) * kLn2;
   const long long bh = row / p.NQ;
   __nv_bfloat16* dst = out + (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + lane * W;
 #pragma unroll
   for (int k = 0; k < W; k += 2)
-    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16(o[k] * inv, o[k + 1] * inv);
+    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16(o.x[k] * inv, o.x[k + 1] * inv);
 }
 
 template <int D>
@@ -514,7 +554,7 @@ cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const v
   const long long blocks = attn_fwd_items(p) * p.splits;
   kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  attn_merge_kernel<D><<<(unsigned)((p.rows + 7) / 8), 256, 0, st>>>(p, part_o, part_ml, out, lse);
+  attn_merge_kernel<D><<<(unsigned)p.rows, kMergeWarps * 32, 0, st>>>(p, part_o, part_ml, out, lse);
   return cudaGetLastError();
 }
 
@@ -545,7 +585,7 @@ void attn_fwd_plan(AttnProblem* p, int num_sms) {
   // the split count that needs the fewest tile times: waves x tiles of a block; more splits only for a gain
   int best = 1;
   double cost = (double)((items + num_sms - 1) / num_sms) * (tiles + 2);
-  for (int s = 2; s <= tiles / kMinTilesPerSplit && items * s <= 4ll * num_sms; ++s) {
+  for (int s = 2; s <= tiles / kMinTilesPerSplit && s <= kMaxSplits && items * s <= 4ll * num_sms; ++s) {
     const double c = (double)((items * s + num_sms - 1) / num_sms) * ((tiles + s - 1) / s + 2) + 3;
     if (c < cost) {
       cost = c;
