@@ -572,9 +572,12 @@ long long attn_fwd_items(const AttnProblem& p) {
   return (long long)p.B * (p.packed ? p.HK : p.H) * p.q_items;
 }
 
-// Blocks of a split have at least this many key tiles: a split costs the second launch and a round trip of its
-// partial through L2, about as much as three or four tiles.
-constexpr int kMinTilesPerSplit = 4;
+// In times of a key tile (1.5 us where a block has one tile of rows, and its K and V are new): setting a block up and
+// storing its tile take kBlockCost, the second launch with the partials' round trip through L2 kMergeCost.  Measured, one
+// query and 8 heads of D 128, us by key tiles of a block: 4096 keys 14.6 with 4, 11.6 with 2, 10.7 with 1; 512 keys 11.0 with
+// all 4 and no merge.  A split's partials cost another tile time for each kMergedPerTile values (B1 H8 N512 D128 causal, 4096
+// rows, 11.7 whole, 15.2 with 4 splits).
+constexpr double kBlockCost = 3.0, kMergeCost = 2.5, kMergedPerTile = 1.5e6;
 constexpr int kSmallGrid = 6;
 void attn_fwd_plan(AttnProblem* p, int num_sms) {
   p->packed = (long long)p->G * p->NQ <= BM;
@@ -582,11 +585,12 @@ void attn_fwd_plan(AttnProblem* p, int num_sms) {
   p->rows = (long long)p->B * p->H * p->NQ;
   const long long items = attn_fwd_items(*p);
   const int tiles = (p->NK + BN - 1) / BN;
-  // the split count that needs the fewest tile times: waves x tiles of a block; more splits only for a gain
+  // the split count that needs the fewest tile times: waves of blocks; more splits only for a gain
   int best = 1;
-  double cost = (double)((items + num_sms - 1) / num_sms) * (tiles + 2);
-  for (int s = 2; s <= tiles / kMinTilesPerSplit && s <= kMaxSplits && items * s <= 4ll * num_sms; ++s) {
-    const double c = (double)((items * s + num_sms - 1) / num_sms) * ((tiles + s - 1) / s + 2) + 3;
+  double cost = (double)((items + num_sms - 1) / num_sms) * (tiles + kBlockCost);
+  for (int s = 2; s <= tiles && s <= kMaxSplits && items * s <= 4ll * num_sms; ++s) {
+    const double c = (double)((items * s + num_sms - 1) / num_sms) * ((tiles + s - 1) / s + kBlockCost) + kMergeCost +
+                     (double)p->rows * s * p->D / kMergedPerTile;
     if (c < cost) {
       cost = c;
       best = s;

@@ -70,7 +70,7 @@ def test_few_tiles_split_the_keys(lib, NQ, H, HK, B, NK):
     packed, splits = skl.attn_fwd_plan(B, H, HK, NQ, NK, 128, 152)
     assert packed == (H // HK * NQ <= 128)
     blocks = B * (HK if packed else H * -(-NQ // 256)) * splits
-    assert splits > 1 and -(-NK // 128) // splits >= 4
+    assert splits > 1 and -(-NK // 128) // splits >= 1
     assert blocks / (152 * -(-blocks // 152)) > 0.6 or blocks < 152
 
 
