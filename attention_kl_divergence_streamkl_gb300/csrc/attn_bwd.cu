@@ -21,6 +21,12 @@
 // K step that adds the row's value to a product (the other operand's step is
 // ones).  Rows that see no key, and rows past a sequence's length, get -1e30
 // and 0: their P is exactly 0.
+//
+// Measured at D 128, five products counted: 8 heads, N8192, non-causal 581 us,
+// 1180 TFLOP/s, with the recomputed two 1655, which is near what the power limit
+// leaves a plain matrix product (1750); B2 H32 HK8 N4096 causal 640 us.  Built and
+// not kept: Q and dO of the dQ block as operands in TMEM (64 KB less
+// shared-memory traffic a tile pair, and 3% slower).
 #include "attn.cuh"
 
 namespace skl {
@@ -39,7 +45,8 @@ struct BwdMaps {  // of the inputs, and of the outputs
 
 // ---------------------------------------------------------------------------
 // Row values: -LSE / scale and -delta, delta = dO . O - dLSE.  A row takes D / 8
-// lanes of 16 bytes; bound by the read of O and dO.
+// lanes of 16 bytes; bound by the read of O and dO (262144 rows of D 128: 27 us,
+// 5.1 TB/s).
 //
 // O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|.  Among many keys that averages out of the
 // gradients; a row that sees few of them passes it on whole.  For rows of at most 32 keys (the first rows under a causal
@@ -539,7 +546,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
 }
 
 // ---------------------------------------------------------------------------
-// dQ block.  The TMEM lanes are queries: a thread owns a row and holds its nlse
+// dQ block.  The TMEM lanes are queries: a thread owns a row and holds its LSE
 // and delta.  S = Q K^T and dP = dO V^T are copied into registers and released
 // at once, before anything is computed, so the next tile's products run meanwhile; dS (bf16 pairs)
 // goes to a double buffer in TMEM, the A operand of dQ += dS K.
@@ -908,9 +915,9 @@ bool attn_bwd_has_fused(const AttnProblem& p) { return p.D == 64; }
 // long as about kBlockCost more.
 //   separate  of the ways to deal both kinds' tiles out over 1 to 8 parts each, one whose larger of the longest block and
 //             the SMs' share of all is clearly smallest; a part's trip through the workspace costs kPartCost more.
-//             Measured, us without and with parts: B1 H4 HK1 N4096 D128 causal 186 / 68, B1 H16 HK4 N2048 D64 causal 89 /
-//             60, B1 H8 HK1 N512 D128 53 / 30; where the rule leaves them whole: B1 H32 HK8 N2048 D128 causal 119 / 133,
-//             B1 H32 N_Q128 N_K64K D128 866 / 910.
+//             Measured, us without and with parts: B1 H4 HK1 N4096 D128 causal 176 / 59, B1 H16 HK4 N2048 D64 causal 80 /
+//             51, B1 H8 HK1 N512 D128 51 / 27, B1 H16 HK4 N4096 D128 causal 184 / 177; where the rule leaves them whole
+//             (measured on an earlier build): B1 H32 HK8 N2048 D128 causal 119 / 133, B1 H32 N_Q128 N_K64K D128 866 / 910.
 //   fused     the tiles of the last, incomplete wave are dealt out so that it fills the SMs (non-causal: a causal grid's
 //             short blocks fill the end by themselves).
 // In a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for).

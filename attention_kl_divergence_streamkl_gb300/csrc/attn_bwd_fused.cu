@@ -11,11 +11,11 @@
 //   dS^T = P^T dP^T as bf16 pairs over dP in TMEM:          dK += dS^T Q
 //          and in shared memory [key][query]:               dQ = dS K (MN-major A)
 // TMEM: S/P [0,128), dP/dS [128,256), dV, dK, dQ 64 columns each from 256 on, and K and V as bf16 pairs in the last 64,
-// the A operands of S and dP.  Shared-memory traffic is what bounds a tile pair: with every operand read from there it
-// was 350 KB, so it is 260, 2000 cycles at 128 bytes a clock, of about 2550 that a tile pair takes (the products alone
-// 1350).  It comes in two halves, between the two barriers of the P and dS warps; dQ is computed before dP, and so
-// staged and reduced while the first half's products leave room (the other way round 1290 us where it is now 1192:
-// 32 heads, 8 key heads, N8192, non-causal).
+// the A operands of S and dP: read from shared memory with the other operands they brought a tile pair's traffic there to
+// 350 KB (8 heads, N8192, non-causal: 403 us against 388).  What bounds a tile pair, about 2500 cycles, are the 260 KB that
+// are left, 2000 cycles at 128 bytes a clock; the products alone take 1550.  The traffic comes in two halves, between the
+// two barriers of the P and dS warps; dQ is computed before dP, and so staged and reduced while the first half's products
+// leave room (32 heads, 8 key heads, N8192, non-causal: 1185 us, 1160 TFLOP/s of five products; the other way round 1290).
 //   warps 0-15   thread = key, group g = warp / 4 takes queries [32g, 32g + 32)
 //   warps 16-19  dQ: TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
 //   warp 20      TMA producer: K, V once; Q(u) and dO(u) with their rows' values
@@ -23,8 +23,8 @@
 //   warp 22      clears rows past a sequence's lengths in K, V, Q and dO tiles
 // At D = 128 the same kernel (built, measured, not kept) has 532 KB of shared-memory traffic a tile pair, dQ's staging
 // and reductions 128 KB of it: 4450 cycles against 4460 for the separate blocks' two visits (B2 H32 HK8 N4096 causal
-// 0.69 against 0.68 ms).  At D = 64: 8 heads, N8192, non-causal 0.32 against 0.44 ms;
-// with red.add from registers instead of staging and bulk reductions 0.39.
+// 0.69 against 0.68 ms).  At D = 64: 8 heads, N8192, non-causal 0.31 against 0.43 ms; with red.add from registers instead of
+// staging and bulk reductions 0.39.
 #include "attn.cuh"
 
 namespace skl {

@@ -19,10 +19,20 @@
 //   warp 8          TMA producer: Q_A, Q_B, then K(j), V(j), K(j+1), ... through a ring
 //   warp 9          TMEM owner and MMA issuer (one thread)
 //   warp 10         clears rows of the V tile that lie past a sequence's key length
-// TMEM: S_A [0,128), S_B [128,256), O_A [256, 256+D), O_B [384, 384+D); P (bf16
+// TMEM at D 128: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512); P (bf16
 // pairs) overwrites the first 64 columns of its own S and is the A operand of
 // O += P V.  The pipe runs S_A(j+1) behind P V_A(j), then P V_B(j), S_B(j+1):
 // while one tile's softmax works, the other tile's two products run.
+// At D 64 there is room for three S buffers, [0,384), O_A and O_B behind them: the
+// pairs (A,0), (B,0), (A,1), ... take them in turn and S runs three pairs ahead, so
+// no softmax waits for its next S (one query over 64K keys, B8 H32 HK8: 301 -> 221
+// us; N8192 full, 32 heads: 510 -> 498).
+//
+// Measured: D 128, 32 heads, 8 key heads, N16384 causal 1265 us, 1740 TFLOP/s, what
+// the power limit leaves a plain matrix product (1750); 8 heads, N8192 full 177 us,
+// 1550 (two waves for 256 blocks of 152 SMs).  One query over 131072 keys, B8 H32
+// HK8: 684 us, 6.3 TB/s.  At D 64 the softmax and the one thread that issues the
+// products bound it: N8192 full 498 us, 1105 TFLOP/s.
 //
 // Few query rows: where all query heads of a key head fit in one tile (G N_Q <=
 // 128) they are packed into it, row g N_Q + n, so that K and V are read once for

@@ -528,6 +528,8 @@ struct BwdArgs {
 //     dx_j = sum_t g_t [j = token_t] - p_j (A + B (l_j + H)),   dlogits_j = scale dx_j
 // The pass writes the second term; then the given tokens' columns, a handful, are written again with the sum of
 // both in fp32, rounded once.  A token that is given twice adds twice: its first place takes the sum of all.
+// Bound by DRAM: 4096 x 131072 bf16 324 us, 6.6 TB/s; 333 x 50021 fp16 with 16 tokens 13.8 us, 4.8 TB/s.  (With the first
+// vectors' loads before the sums over the tokens the registers do not suffice: 332 us.)
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdArgs a) {
   constexpr int N = Vec<T>::N;
