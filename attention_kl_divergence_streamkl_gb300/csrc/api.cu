@@ -254,9 +254,7 @@ bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH,
   const cuuint32_t box[3] = {(cuuint32_t)(box_cols ? box_cols : D), (cuuint32_t)box_rows, 1u};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_cols == 32   ? CU_TENSOR_MAP_SWIZZLE_128B
-            : box_cols == 16 ? CU_TENSOR_MAP_SWIZZLE_64B
-                             : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -782,7 +780,8 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
   if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !rows_ok(lse)) return STREAMKL_ERR_INVALID;
   if (num_tokens && (!aligned_to(tokens, 8) || !rows_ok(g_logp))) return STREAMKL_ERR_INVALID;
   if (g_entropy && (!rows_ok(g_entropy) || !rows_ok(entropy))) return STREAMKL_ERR_INVALID;
-  if (num_tokens && dlogits == logits) return STREAMKL_ERR_INVALID;  // the tokens' logits are read after the pass
+  // in place: the tokens' logits are read after the pass, and a row must lie on itself
+  if (dlogits == logits && (num_tokens || (rows > 1 && out_stride != row_stride))) return STREAMKL_ERR_INVALID;
   int sms = 0;
   if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
   return from_cuda(launch_logprobs_bwd(p, logits, tokens, lse, entropy, g_logp, g_entropy, dlogits, out_stride, sms,

@@ -31,7 +31,7 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, in
                      long long sb, int box_rows, int box_heads = 1);
 // A 3-D TMA map {d, row, bh} over an fp32 [BH][rows][D] accumulator, a {D, box_rows, 1} box, no swizzle
 // (for bulk reductions into it).
-// With box_cols 32 or 16 the box is {box_cols, box_rows, 1} with the swizzle of its 128- or 64-byte rows.
+// With box_cols 32 the box is {32, box_rows, 1} with the swizzle of its 128-byte rows.
 bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows, int box_cols = 0);
 // The maps of Q1/Q2 and K1/K2 of a problem.
 inline bool encode_q_map(CUtensorMap* map, const void* base, const Problem& p, int box_rows) {

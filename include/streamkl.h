@@ -315,7 +315,7 @@ streamkl_status streamkl_bwd_mutual_workspace(streamkl_shape s, int bwd_mode, si
  * A row that sees no key -- past its sequence, causal with more queries than
  * keys, no keys at all -- has O = 0 and LSE = -inf.
  * Workspace: fp32 partials of the key splits that few query tiles get, 0 bytes
- * for most shapes; streamkl_attn_fwd_plan gives the choice for any SM count (a
+ * where the query tiles fill the SMs; streamkl_attn_fwd_plan gives the choice for any SM count (a
  * pure host rule): packed != 0 when all query heads of a key head share one
  * 128-row tile, and the number of key splits.
  */
@@ -392,7 +392,7 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
  * NULL, g_entropy [rows] (entropy is read only then); lse and entropy are the
  * forward's.  A token given twice in a row adds twice.  The alternatives have no
  * gradient: to train on some, give them as tokens.  dlogits may be the logits
- * themselves only where num_tokens is 0.
+ * themselves, with the same stride, only where num_tokens is 0.
  * Sums are fp32.  Results do not depend on the order in which blocks run.
  */
 typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1, STREAMKL_FP32 = 2 } streamkl_dtype;

@@ -43,6 +43,7 @@ def test_fwd_refuses(lib, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(out_stride=99), K.ERR_INVALID), (dict(out=None), K.ERR_INVALID), (dict(out=ptr(1)), K.ERR_INVALID),
     (dict(out=ptr()), K.ERR_INVALID),  # onto the logits, with tokens
+    (dict(out=ptr(), out_stride=104, T=0), K.ERR_INVALID),  # onto the logits, rows on other rows
     (dict(lse=None), K.ERR_INVALID), (dict(g=None), K.ERR_INVALID), (dict(tokens=None), K.ERR_INVALID),
     (dict(entropy=None), K.ERR_INVALID), (dict(scale=0.0), K.ERR_INVALID), (dict(rows=2**31), K.ERR_UNSUPPORTED),
 ])
