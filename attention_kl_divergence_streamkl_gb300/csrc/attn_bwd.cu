@@ -225,7 +225,7 @@ struct Smem {
   static constexpr int BAR_SLOT = 8 * 16;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
 };
-static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+static_assert(Smem<128>::BYTES <= kWholeSmSmem, "shared memory");
 }  // namespace kv
 
 template <int D>
@@ -260,7 +260,6 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
                  to_patch = bar + 112, patched = bar + 120, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
   volatile int* part_flag = abort_flag + 1;
-  // the producer sets the barriers up and issues the first loads while the others get TMEM
   auto load_q = [&](int u, int hq, int q0) {
     const int s = u % SLOTS;
     mbar_arrive_expect_tx(q_full + 8 * s, L::TILE + L::STEP);
@@ -295,17 +294,9 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       mbar_init(patched, 1);
       *abort_flag = 0;
       fence_mbar_init();
-      if (n > 0) {
-        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
-        load_q(0, hk * p.G + head0, q_begin + qt0 * BT);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
-        load_o(0, hk * p.G + head0, q_begin + qt0 * BT);
-      }
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    __syncwarp();  // the warp's other lanes wait for the one that issues
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (threadIdx.x < 128) {
     st_shared16(sb + L::OFF_ONES + threadIdx.x * 16, make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u));
@@ -319,12 +310,20 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= DS_WARPS) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (n > 0 && elect_one()) {
+        mbar_arrive_expect_tx(kv_full, 2 * L::TILE);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_K + h * BT * 128, &maps.k, kv_full, h * 64, k0, hk, b);
+        load_q(0, hk * p.G + head0, q_begin + qt0 * BT);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) tma_load_4d(sb + L::OFF_V + h * BT * 128, &maps.v, kv_full, h * 64, k0, hk, b);
+        load_o(0, hk * p.G + head0, q_begin + qt0 * BT);
         int issued_q = 1, issued_o = 1, hq = hk * p.G + head0, qt = qt0;
         for (int u = 1; u < n; ++u) {
           const int s = u % SLOTS;
@@ -358,7 +357,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
             st_shared_zero16(sw128<BT>(tile, from + i / (D / 8), i % (D / 8)));
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(patched);
+          arrive_one(patched);
         }
       }
       __syncwarp();
@@ -459,7 +458,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      arrive_one(p_full);
       ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag);
       __syncwarp();
       if (!ok) break;
@@ -478,7 +477,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      arrive_one(ds_full);
       q0 = q0 == q_last ? q_last - (n_qt - 1) * BT : q0 + BT;
     }
     // ---- out: thread = key row, group g writes d columns [32g, 32g + 32) of both
@@ -498,6 +497,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           uint32_t g[32] = {};
+          __syncwarp();
           if (n > 0) {
             tmem_ld32(tmem + lanes + (which ? kv::kColK : kv::kColV) + 32 * grp, g);
             tmem_ld_wait();
@@ -513,6 +513,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         uint32_t g[32] = {};
+        __syncwarp();  // rows differ in what they do below; the load wants the whole warp
         if (part.parts > 1) {
           part_sum<2 * D>(mine, part.parts, r, which * D + 32 * grp, g);
         } else if (n > 0) {
@@ -571,7 +572,7 @@ struct Smem {
   static constexpr int BAR_SLOT = 8 * 20;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
 };
-static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+static_assert(Smem<128>::BYTES <= kWholeSmSmem, "shared memory");
 }  // namespace qq
 
 // dS of 32 columns: a, d = S, dP; `seen` of them are visible.
@@ -624,7 +625,6 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
                  to_patch = bar + 144, patched = bar + 152, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
   volatile int* part_flag = abort_flag + 1;
-  // the producer sets the barriers up and issues the first loads while the others get TMEM
   auto load_k = [&](int j) {
     const int s = j % K_SLOTS;
     mbar_arrive_expect_tx(k_full + 8 * s, L::TILE);
@@ -659,17 +659,9 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
       mbar_init(patched, 1);
       *abort_flag = 0;
       fence_mbar_init();
-      if (n > 0) {
-        mbar_arrive_expect_tx(x_full, 2 * L::TILE);
-#pragma unroll
-        for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
-        load_k(0);
-#pragma unroll
-        for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
-        load_v(0);
-      }
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    __syncwarp();  // the warp's other lanes wait for the one that issues
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -678,12 +670,20 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= DS_WARPS) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (n > 0 && elect_one()) {
+        mbar_arrive_expect_tx(x_full, 2 * L::TILE);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_Q + d * BT * 128, &maps.q, x_full, d * 64, q0, h, b);
+        load_k(0);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) tma_load_4d(sb + L::OFF_O + d * BT * 128, &maps.go, x_full, d * 64, q0, h, b);
+        load_v(0);
         int issued_k = 1, issued_v = 1;
         for (int j = 1; j < n; ++j) {
           const int sk = j % K_SLOTS, sv = j % V_SLOTS;
@@ -708,7 +708,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
           st_shared_zero16(sw128<BT>(sb + L::OFF_K + (patch_j % K_SLOTS) * L::TILE, from + i / (D / 8), i % (D / 8)));
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(patched);
+        arrive_one(patched);
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
@@ -790,7 +790,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
       reg_fence32(d);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_free);
+      arrive_one(s_free);
       if (masked)
         ds32<true>(a, d, pk, c, nl, dl, seen);
       else
@@ -805,7 +805,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full + 8 * bf);
+      arrive_one(ds_full + 8 * bf);
     }
     bool got = ok;
     if (n > 0 && ok) {
@@ -895,9 +895,7 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBw
       !q_map(&m.dq, dq, p.qs_n, p.qs_h, p.qs_b) || !k_map(&m.dk, dk, p.ks_n, p.ks_h, p.ks_b) ||
       !k_map(&m.dv, dv, p.vs_n, p.vs_h, p.vs_b))
     return cudaErrorInvalidValue;
-  int smem = kOneBlockPerSmSmem;
-  if (kv::Smem<D>::BYTES > smem) smem = kv::Smem<D>::BYTES;
-  if (qq::Smem<D>::BYTES > smem) smem = qq::Smem<D>::BYTES;
+  constexpr int smem = kWholeSmSmem;
   auto kern = attn_bwd_kernel<D>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
   kern<<<plan.q_blocks + plan.kv_blocks, THREADS, smem, st>>>(

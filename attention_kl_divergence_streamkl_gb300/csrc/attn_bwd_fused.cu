@@ -67,7 +67,7 @@ struct Smem {
   static constexpr int BAR_SLOT = 8 * 20;
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16;
 };
-static_assert(Smem::BYTES <= 227 * 1024, "shared memory");
+static_assert(Smem::BYTES <= kWholeSmSmem, "shared memory");
 
 __device__ __forceinline__ void reduce_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -107,27 +107,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                  kv_tmem = bar + 152, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
   volatile int* part_flag = abort_flag + 1;
-  if (threadIdx.x == 0) {
-    mbar_init(kv_full, 1);
-    mbar_init(kv_patched, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(q_full + 8 * s, 1);
-      mbar_init(q_empty + 8 * s, 1);
-      mbar_init(o_full + 8 * s, 1);
-      mbar_init(o_empty + 8 * s, 1);
+  if (warp == PRODUCER_WARP) {
+    if (elect_one()) {
+      mbar_init(kv_full, 1);
+      mbar_init(kv_patched, 1);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(q_full + 8 * s, 1);
+        mbar_init(q_empty + 8 * s, 1);
+        mbar_init(o_full + 8 * s, 1);
+        mbar_init(o_empty + 8 * s, 1);
+      }
+      mbar_init(s_full, 1);
+      mbar_init(dp_full, 1);
+      mbar_init(p_full, DS_WARPS);
+      mbar_init(ds_full, DS_WARPS);
+      mbar_init(dq_full, 1);
+      mbar_init(dq_free, DQ_WARPS);
+      mbar_init(g_done, 1);
+      mbar_init(to_patch, 1);
+      mbar_init(patched, 1);
+      mbar_init(kv_tmem, 8);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(p_full, DS_WARPS);
-    mbar_init(ds_full, DS_WARPS);
-    mbar_init(dq_full, 1);
-    mbar_init(dq_free, DQ_WARPS);
-    mbar_init(g_done, 1);
-    mbar_init(to_patch, 1);
-    mbar_init(patched, 1);
-    mbar_init(kv_tmem, 8);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (threadIdx.x < 128) {
     st_shared16(sb + L::OFF_ONES + threadIdx.x * 16, make_uint4(0x3f803f80u, 0x00003f80u, 0u, 0u));
@@ -141,7 +145,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= PRODUCER_WARP) {
     setmaxnreg_dec<kRegsOther>();
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           clear(sb + L::OFF_V, kl - k0);
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(kv_patched);
+          arrive_one(kv_patched);
         }
       }
       // for each head's last tile: its Q, then its dO, when the MMA thread has seen them land
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         clear(sb + ((e & 1) ? L::OFF_O + u % SLOTS * L::TILE : L::OFF_Q + u % SLOTS * L::TILE), ql & (BT - 1));
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(patched);
+        arrive_one(patched);
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int c = 0; c < D / 32; ++c) reg_fence32(a[c]);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(dq_free);
+      arrive_one(dq_free);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         // the reduction that last used this chunk has read it
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(kv_tmem);
+        arrive_one(kv_tmem);
       }
     }
     const int q_last = q_begin + (n_qt - 1) * BT + 32 * grp;
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      arrive_one(p_full);
       ok = mbar_wait_warp(dp_full, u & 1, status, abort_flag);  // dQ(u-1), issued before dP(u), has read dS too
       __syncwarp();
       if (!ok) break;
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_before();
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      arrive_one(ds_full);
       q0 = q0 == q_last ? q_last - (n_qt - 1) * BT : q0 + BT;
     }
     // ---- dV (groups 0, 1) through the first Q slot, dK (2, 3) through the second: every product that read them is done
@@ -487,7 +492,7 @@ cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdPlan& plan,
       !encode_tile_map(&m.dv, dv, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
       !encode_rows_f32_map(&m.acc, w.acc, D, w.padded, p.B * p.H, 32, 32))
     return cudaErrorInvalidValue;
-  constexpr int smem = Smem::BYTES > kOneBlockPerSmSmem ? Smem::BYTES : kOneBlockPerSmSmem;
+  constexpr int smem = kWholeSmSmem;
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   attn_bwd_fused_kernel<<<plan.kv_blocks, THREADS, smem, st>>>(p, static_cast<const uint4*>(w.row_s),

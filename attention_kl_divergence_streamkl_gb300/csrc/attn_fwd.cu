@@ -65,7 +65,7 @@ struct Smem {
   static constexpr int BAR_SLOT = 8 * (4 + 2 * SLOTS + 3 * S_BUFS);
   static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
 };
-static_assert(Smem<128>::BYTES <= 227 * 1024, "shared memory");
+static_assert(Smem<64>::BYTES <= kWholeSmSmem && Smem<128>::BYTES <= kWholeSmSmem, "shared memory");
 
 // Sum of 2^(c s - m) over a row's 128 columns; the bf16 pairs of the terms go to pk.
 __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const uint32_t (&s2)[32],
@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  // the producer sets the barriers up and issues the first loads while the others get TMEM
   const uint32_t q_bytes = (p.packed ? (uint32_t)(p.G * p.NQ) : (uint32_t)BM) * D * 2;
   auto load_kv = [&](int u) {  // K(0), V(0), K(1), ...
     const int s = u % SLOTS;
@@ -189,18 +188,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(patched, 1);
       *abort_flag = 0;
       fence_mbar_init();
-      for (int t = 0; t < 2; ++t) {
-        if ((t ? nB : nA) == 0) continue;
-        mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
-                      p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
-        if (t == 0 || nA == 0) load_kv(0);
-      }
-      for (int u = 1; u < min(SLOTS, 2 * n); ++u) load_kv(u);
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    __syncwarp();  // the warp's other lanes wait for the one that issues
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -209,12 +199,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= SOFTMAX_WARPS) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == PRODUCER_WARP) {
       if (n > 0 && elect_one()) {
+        for (int t = 0; t < 2; ++t) {
+          if ((t ? nB : nA) == 0) continue;
+          mbar_arrive_expect_tx(q_full + 8 * t, q_bytes);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
+                        p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+          if (t == 0 || nA == 0) load_kv(0);
+        }
+        for (int u = 1; u < min(SLOTS, 2 * n); ++u) load_kv(u);
         int issued = min(SLOTS, 2 * n);
         for (int u = SLOTS; u < 2 * n; ++u) {
           if (!mbar_wait(kv_empty + 8 * (u % SLOTS), ((u / SLOTS) - 1) & 1, status, abort_flag)) break;
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(patched);
+          arrive_one(patched);
         }
       }
       __syncwarp();
@@ -387,6 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
 #pragma unroll 1
           for (int d = 0; d < D; d += 32) {
+            __syncwarp();
             tmem_ld32(to + d, s0);
             tmem_ld_wait();
             reg_fence32(s0);
@@ -397,12 +399,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       l += sum;
+      __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_st16(ts + 16 * q, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * q]));
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready + 8 * buf);
+      arrive_one(p_ready + 8 * buf);
     }
     if (nt > 0 && ok) {
       ok = mbar_wait_warp(o_done + 8 * buf_of(t, nt - 1), use_of(t, nt - 1) & 1, status, abort_flag);
@@ -421,6 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t o[32];
+          __syncwarp();  // rows differ in what they do above; the load wants the whole warp
           if (nt > 0) {
             tmem_ld32(to + d, o);
             tmem_ld_wait();
@@ -471,10 +475,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Merges the splits' (m, l, O), a block to a row: the weights with a thread to a split, then O with a warp to every fourth
+// Merges the splits' (m, l, O), a block to a row: the weights with a thread to a split, then O with a warp to every eighth
 // split, whose first loads are on their way before the weights are known.  Bound by the two trips to L2 (a warp to a row
 // with one split after the other took 16 us for 19 splits, this 4).
-constexpr int kMergeWarps = 4, kMergeAhead = 4;
+constexpr int kMergeWarps = 8, kMergeAhead = 2;
 constexpr int kMaxSplits = 1024;  // the plan makes at most four blocks an SM
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
@@ -553,7 +557,7 @@ cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const v
       !encode_tile_map(&mv, v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BN) ||
       !encode_tile_map(&mo, o, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1))
     return cudaErrorInvalidValue;
-  constexpr int smem = Smem<D>::BYTES > kOneBlockPerSmSmem ? Smem<D>::BYTES : kOneBlockPerSmSmem;
+  constexpr int smem = kWholeSmSmem;
   const bool fresh = D == 64 && ((p.NK + BN - 1) / BN + p.splits - 1) / p.splits <= kFreshTiles;
   const auto kern = fresh ? attn_fwd_kernel<D, D == 64> : attn_fwd_kernel<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

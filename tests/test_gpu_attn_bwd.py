@@ -202,3 +202,32 @@ def test_autograd_outputs_alone():
     frozen = q.clone().requires_grad_()
     skl.attention(frozen, k, v).sum().backward()
     assert frozen.grad is not None
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_two_streams_side_by_side(D):
+    """Forward, merge, and both backward paths of two streams at once, kernels of every kind beside one another on the GPU:
+    the bits of the calls made alone."""
+    shapes = [(2, 16, 8, 141, 2123, False), (1, 8, 2, 1, 2694, False), (2, 4, 4, 600, 500, True), (1, 4, 1, 300, 1300, True)]
+    inputs = [A.tensors(B, H, HK, NQ, NK, D, i) for i, (B, H, HK, NQ, NK, _) in enumerate(shapes)]
+
+    def run(i):
+        q, k, v, do = inputs[i]
+        o, lse = skl.attn_fwd(q, k, v, causal=shapes[i][5])
+        out = [o, lse, *skl.attn_bwd(q, k, v, o, lse, do, causal=shapes[i][5], bwd_mode=skl.BWD_SEPARATE)]
+        if D == 64:  # dq's bits depend on the order of the reductions
+            out += skl.attn_bwd(q, k, v, o, lse, do, causal=shapes[i][5], bwd_mode=skl.BWD_FUSED)[1:]
+        return out
+
+    want = [run(i) for i in range(len(shapes))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for round_ in range(60):
+        i, j = round_ % len(shapes), (round_ * 3 + 1) % len(shapes)
+        for _ in range(20):
+            here = run(i)
+            with torch.cuda.stream(side):
+                there = run(j)
+        torch.cuda.synchronize()
+        for got, ref in ((here, want[i]), (there, want[j])):
+            assert all(torch.equal(x, y) for x, y in zip(got, ref))
