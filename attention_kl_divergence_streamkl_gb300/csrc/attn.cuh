@@ -23,29 +23,6 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// True on one lane of a converged warp.  The compiler knows that a single lane follows, so the tensor-core
-// instructions of that branch take their operands from uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
-// A block that owns all 512 TMEM columns has them from column 0 on.  tcgen05.alloc's answer is looked at, by every warp and
-// before setmaxnreg: no load of it is in flight when the warps' registers are dealt out anew, and the addresses that follow
-// are constants.  (Kept in a register it ended, once in 10^4 runs of two streams' kernels side by side, in an
-// illegal-address error; like this 4 10^6 such runs did not.)
-__device__ __forceinline__ void whole_tmem(volatile uint32_t* slot, int* status) {
-  if (*slot != 0) atomicOr(status, kStatusTimeout);
-}
-
-// One arrival for a converged warp; the warp's other lanes wait for the one that arrives.  The instructions on barriers,
-// as those of TMA, may take their operands from the warp's uniform registers, which lanes that ran on would use too.
-__device__ __forceinline__ void arrive_one(uint32_t bar) {
-  if (elect_one()) mbar_arrive(bar);
-  __syncwarp();
-}
-
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }

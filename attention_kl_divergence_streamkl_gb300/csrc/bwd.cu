@@ -149,28 +149,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                  slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(ko_full + 8 * s, 1);
-      mbar_init(ko_empty + 8 * s, 2);
-      mbar_init(kt_full + 8 * s, 1);
-      mbar_init(kt_empty + 8 * s, 1);
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(q_full, 1);
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(ko_full + 8 * s, 1);
+        mbar_init(ko_empty + 8 * s, 2);
+        mbar_init(kt_full + 8 * s, 1);
+        mbar_init(kt_empty + 8 * s, 1);
+      }
+      mbar_init(sa_full, 1);
+      mbar_init(sa_free, DS_WARPS);
+      mbar_init(sb_full, 1);
+      mbar_init(sb_free, DS_WARPS);
+      mbar_init(ds_full, DS_WARPS);
+      mbar_init(ds_free, 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(dk_full + 8 * b, 1);
+        mbar_init(dk_free + 8 * b, DK_WARPS);
+      }
+      mbar_init(all_done, 1);
+      mbar_init(sb_issued, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    mbar_init(sa_full, 1);
-    mbar_init(sa_free, DS_WARPS);
-    mbar_init(sb_full, 1);
-    mbar_init(sb_free, DS_WARPS);
-    mbar_init(ds_full, DS_WARPS);
-    mbar_init(ds_free, 1);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(dk_full + 8 * b, 1);
-      mbar_init(dk_free + 8 * b, DK_WARPS);
-    }
-    mbar_init(all_done, 1);
-    mbar_init(sb_issued, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -179,7 +183,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   // opt side: 2 in setting 1 (dQ2, dK2), 1 in setting 2; "a" is the other side
   constexpr int OFF_QA = SETTING == 1 ? L::OFF_Q1 : L::OFF_Q2, OFF_QB = SETTING == 1 ? L::OFF_Q2 : L::OFF_Q1;
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     setmaxnreg_dec_other();
     if (warp == PRODUCER_WARP) {
       // ------------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(q_full, 2 * L::TQ);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------ TMA producer of K_opt
       // A stream of its own: its slots free only after the gradient MMAs, and the
       // other K tile must not wait behind it.
-      if (lane == 0) {
+      if (elect_one()) {
         const CUtensorMap* mkb = SETTING == 1 ? &mk2 : &mk1;
         int issued = 0;
         for (int j = 0; j < n_kt; ++j) {
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------------------ MMA issuer: logits
       // S_a(j) once the dS warps have read S_b(j - 1) out of the shared region,
       // S_b(j) once they hold S_a(j).
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BQ, BK, false, false);
         const uint64_t qad = sdesc_sw128(sb + OFF_QA, 0, 1024), qbd = sdesc_sw128(sb + OFF_QB, 0, 1024);
         bool ok = mbar_wait(q_full, 0, status, abort_flag);
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // dQ(j), S_b(j + 1), dKp(j): the dS warps, which wait for S_b after copying
       // S_a, find it behind one gradient MMA instead of two (measured: B1 H32 N64K
       // causal 62.3 -> 59.8 ms; holding dQ(j) back as well made it 71.2 ms).
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_dq = idesc_bf16(BQ, D, false, true);
         constexpr uint32_t id_dk = idesc_bf16(128, BK, true, true);
         const uint64_t qod = sdesc_sw128(sb + OFF_QB, D == 128 ? BQ * 128 : 0, 1024);  // Q_opt as MN-major A
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int d = wq * 32 + lane;  // lane of dKp^T = column d
       const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
       const uint32_t stg = sb + L::OFF_STG + half * L::STG;
-      const bool leader = wq == 0 && lane == 0;
+      const bool leader = wq == 0 && elect_one();  // the same lane every time: bulk groups are a thread's own
       for (int j = 0; j < n_kt; ++j) {
         const int b = j & 1;
         const bool got = mbar_wait_warp(dk_full + 8 * b, (j >> 1) & 1, status, abort_flag);
@@ -341,10 +346,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             // dKp MMA of tile j + 2 may overwrite it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dk_free + 8 * b);
+            arrive_one(dk_free + 8 * b);
           }
           // the group's buffer is free once the previous reduction from it has read it
           if (leader) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
           named_bar_sync(2 + half, 128);
           if (d < D) {
 #pragma unroll
@@ -361,9 +367,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
+          __syncwarp();
         }
       }
       if (leader) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      __syncwarp();
     }
   } else {
     setmaxnreg_inc_ds();
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       reg_fence32(held);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sa_free);
+      arrive_one(sa_free);
       const int kg = kbase + j * BK + grp * 32;
       const bool masked = (kg + 31 >= p.NK) || (row >= p.NQ) || (p.causal && kg + 31 > row + p.off);
       const uint32_t vis = masked ? visible_keys<16>(row, kg, p.NQ, p.NK, p.off, p.causal) |
@@ -423,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (h == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(sb_free);
+          arrive_one(sb_free);
         }
         const uint32_t(&ha)[16] = *reinterpret_cast<const uint32_t(*)[16]>(&held[16 * h]);
         if (SETTING == 1) {  // S_b = S2; held = P1
@@ -457,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      arrive_one(ds_full);
     }
     // ---- dQ out: group g writes d columns [32g, 32g + 32)
     const bool done = mbar_wait_warp(all_done, 0, status, abort_flag);

@@ -136,20 +136,24 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
                  slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  if (threadIdx.x == 0) {
-    mbar_init(x_full, 1);
-    mbar_init(s2_issued, 1);
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(y_full + 8 * s, 1);
-      mbar_init(y_empty + 8 * s, 1);
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(x_full, 1);
+      mbar_init(s2_issued, 1);
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(y_full + 8 * s, 1);
+        mbar_init(y_empty + 8 * s, 1);
+      }
+      mbar_init(s_full, 1);
+      mbar_init(s_free, DS_WARPS);
+      mbar_init(ds_full, DS_WARPS);
+      mbar_init(ds_free, 1);
+      mbar_init(g_done, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, DS_WARPS);
-    mbar_init(ds_full, DS_WARPS);
-    mbar_init(ds_free, 1);
-    mbar_init(g_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -158,13 +162,14 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= DS_WARPS) {
     setmaxnreg_dec_other();
     if (warp == PRODUCER_WARP) {
       // ------------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(x_full, 2 * L::TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -192,7 +197,7 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
       // ------------------------------------------------------------------ MMA issuer: logits
       // S1(j) once the dS warps have copied S2(j - 1) out of the region, S2(j) once they hold S1(j);
       // s_free completes twice per key tile: S1(j) copied (2j), S2(j) copied (2j + 1)
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BX, BY, false, false);
         const uint64_t x1d = sdesc_sw128(sb + L::OFF_X1, 0, 1024), x2d = sdesc_sw128(sb + L::OFF_X2, 0, 1024);
         bool ok = mbar_wait(x_full, 0, status, abort_flag);
@@ -218,7 +223,7 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
       // dQ1(j) as soon as dS(j) is in TMEM, so it runs while the dS warps copy S1(j + 1); dQ2(j) once
       // S2(j + 1) is queued, so the logits the dS warps wait for come first (pipe order S1(j + 1),
       // dQ1(j), S2(j + 1), dQ2(j)).
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_g = idesc_bf16(BX, D, false, true);
         bool ok = true;
         for (int j = 0; ok && j < n_yt; ++j) {
@@ -275,7 +280,7 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
       reg_fence32(s1);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_free);
+      arrive_one(s_free);
       const int ylo = j * BY + grp * 32;  // key columns ylo.., query row xidx
       const bool masked = (ylo + 31 >= p.NK) || (xidx >= p.NQ) || (p.causal && ylo + 31 > xidx + p.off);
       ok = mbar_wait_warp(s_full, 1, status, abort_flag);  // S2(j): completion 2j + 1
@@ -293,7 +298,7 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
         if (h == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
+          arrive_one(s_free);
         }
         if (masked)
           make_ds_row_mutual<true, 16>(s1 + 16 * h, s2, pk1 + 8 * h, pk2 + 8 * h, c, p.scale, v.nA, v.nB2, v.nB1,
@@ -316,7 +321,7 @@ __device__ __forceinline__ void dq_mutual_block(const Problem& p, const float* _
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      arrive_one(ds_full);
     }
     // ---- dQ1, dQ2 = scale * accumulators, to bf16: group g writes d columns [32g, 32g + 32)
     const bool got = ok && mbar_wait_warp(g_done, 0, status, abort_flag);
@@ -392,21 +397,25 @@ __device__ __forceinline__ void dk_mutual_block(const Problem& p, const float* _
                  slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  if (threadIdx.x == 0) {
-    mbar_init(k_full, 1);
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(q_full + 8 * s, 1);
-      mbar_init(q_empty + 8 * s, 1);
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(k_full, 1);
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(q_full + 8 * s, 1);
+        mbar_init(q_empty + 8 * s, 1);
+      }
+      mbar_init(sa_full, 1);
+      mbar_init(sa_free, DS_WARPS);
+      mbar_init(sb_full, 1);
+      mbar_init(sb_free, DS_WARPS);
+      mbar_init(ds_full, DS_WARPS);
+      mbar_init(ds_free, 1);
+      mbar_init(g_done, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    mbar_init(sa_full, 1);
-    mbar_init(sa_free, DS_WARPS);
-    mbar_init(sb_full, 1);
-    mbar_init(sb_free, DS_WARPS);
-    mbar_init(ds_full, DS_WARPS);
-    mbar_init(ds_free, 1);
-    mbar_init(g_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -415,13 +424,14 @@ __device__ __forceinline__ void dk_mutual_block(const Problem& p, const float* _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= DS_WARPS) {
     setmaxnreg_dec_other();
     if (warp == PRODUCER_WARP) {
       // ------------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(k_full, 2 * L::TK);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -446,7 +456,7 @@ __device__ __forceinline__ void dk_mutual_block(const Problem& p, const float* _
       __syncwarp();
     } else if (warp == MMA_WARP) {
       // ------------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BQ, BK, false, false);
         constexpr uint32_t id_g = idesc_bf16(BK, D, true, true);
         const uint64_t k1d = sdesc_sw128(sb + L::OFF_K1, 0, 1024), k2d = sdesc_sw128(sb + L::OFF_K2, 0, 1024);
@@ -531,7 +541,7 @@ __device__ __forceinline__ void dk_mutual_block(const Problem& p, const float* _
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      arrive_one(ds_full);
     };
     // S1(j) is copied out before the loop body of tile j: for j >= 1 while dK1(j - 1)'s MMA, which the
     // dS warps wait for before they can store dS2(j - 1), is running
@@ -546,7 +556,7 @@ __device__ __forceinline__ void dk_mutual_block(const Problem& p, const float* _
       reg_fence32(s1);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sa_free);
+      arrive_one(sa_free);
       return true;
     };
     RowVals v = fetch(0);
@@ -570,7 +580,7 @@ __device__ __forceinline__ void dk_mutual_block(const Problem& p, const float* _
         if (h == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(sb_free);
+          arrive_one(sb_free);
         }
         if (masked)
           make_ds_row_mutual<true, 16>(s1 + 16 * h, s2, pk1 + 8 * h, pk2 + 8 * h, c, p.scale, v.nA, v.nB2, v.nB1,

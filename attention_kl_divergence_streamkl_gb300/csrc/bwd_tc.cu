@@ -105,25 +105,29 @@ __device__ __forceinline__ void dq_block(const Problem& p, const float* __restri
                  slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  if (threadIdx.x == 0) {
-    mbar_init(x_full, 1);
-    for (int s = 0; s < YO_SLOTS; ++s) {
-      mbar_init(yo_full + 8 * s, 1);
-      mbar_init(yo_empty + 8 * s, 1);
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(x_full, 1);
+      for (int s = 0; s < YO_SLOTS; ++s) {
+        mbar_init(yo_full + 8 * s, 1);
+        mbar_init(yo_empty + 8 * s, 1);
+      }
+      for (int s = 0; s < YT_SLOTS; ++s) {
+        mbar_init(yt_full + 8 * s, 1);
+        mbar_init(yt_empty + 8 * s, 1);
+      }
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(ds_full + 8 * b, DS_WARPS);
+        mbar_init(ds_free + 8 * b, 1);
+      }
+      mbar_init(s_full, 1);
+      mbar_init(s_free, DS_WARPS);
+      mbar_init(g_done, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    for (int s = 0; s < YT_SLOTS; ++s) {
-      mbar_init(yt_full + 8 * s, 1);
-      mbar_init(yt_empty + 8 * s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(ds_full + 8 * b, DS_WARPS);
-      mbar_init(ds_free + 8 * b, 1);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, DS_WARPS);
-    mbar_init(g_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -132,13 +136,14 @@ __device__ __forceinline__ void dq_block(const Problem& p, const float* __restri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= DS_WARPS) {
     setmaxnreg_dec_other();
     if (warp == PRODUCER_WARP) {
       // ------------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(x_full, 2 * L::TILE);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -175,7 +180,7 @@ __device__ __forceinline__ void dq_block(const Problem& p, const float* __restri
       __syncwarp();
     } else if (warp == MMA_WARP) {
       // ------------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BX, BY, false, false);
         constexpr uint32_t id_g = idesc_bf16(BX, D, false, true);
         const uint64_t x1d = sdesc_sw128(sb + L::OFF_X1, 0, 1024), x2d = sdesc_sw128(sb + L::OFF_X2, 0, 1024);
@@ -261,7 +266,7 @@ __device__ __forceinline__ void dq_block(const Problem& p, const float* __restri
         if (h == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
+          arrive_one(s_free);
         }
         const int y = ylo + 16 * h;
         if (masked)
@@ -285,7 +290,7 @@ __device__ __forceinline__ void dq_block(const Problem& p, const float* __restri
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full + 8 * b);
+      arrive_one(ds_full + 8 * b);
     }
     // ---- G = sum dS Y_opt, scaled, to bf16: group g writes d columns [32g, 32g + 32)
     const bool got = ok && mbar_wait_warp(g_done, 0, status, abort_flag);
@@ -385,23 +390,27 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
                  ds_free = bar + 112, g_done = bar + 120, slot = bar + L::BAR_SLOT;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + L::BAR_SLOT + 4);
 
-  if (threadIdx.x == 0) {
-    mbar_init(k_full, 1);
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(qo_full + 8 * s, 1);
-      mbar_init(qo_empty + 8 * s, 1);
-      mbar_init(qt_full + 8 * s, 1);
-      mbar_init(qt_empty + 8 * s, 1);
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(k_full, 1);
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_init(qo_full + 8 * s, 1);
+        mbar_init(qo_empty + 8 * s, 1);
+        mbar_init(qt_full + 8 * s, 1);
+        mbar_init(qt_empty + 8 * s, 1);
+      }
+      mbar_init(sa_full, 1);
+      mbar_init(sa_free, DS_WARPS);
+      mbar_init(sb_full, 1);
+      mbar_init(sb_free, DS_WARPS);
+      mbar_init(ds_full, DS_WARPS);
+      mbar_init(ds_free, 1);
+      mbar_init(g_done, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    mbar_init(sa_full, 1);
-    mbar_init(sa_free, DS_WARPS);
-    mbar_init(sb_full, 1);
-    mbar_init(sb_free, DS_WARPS);
-    mbar_init(ds_full, DS_WARPS);
-    mbar_init(ds_free, 1);
-    mbar_init(g_done, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(slot, kTmemCols);
@@ -410,13 +419,14 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp >= DS_WARPS) {
     setmaxnreg_dec_other();
     if (warp == PRODUCER_WARP) {
       // ------------------------------------------------------------------ TMA producer
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(k_full, 2 * L::TK);
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -441,7 +451,7 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
       __syncwarp();
     } else if (warp == QOPT_WARP) {
       // ------------------------------------------------------------------ TMA producer of Q_opt
-      if (lane == 0) {
+      if (elect_one()) {
         const CUtensorMap* mqb = SETTING == 1 ? &mq2 : &mq1;
         int issued = 0;
         for (int j = 0; j < n_qt; ++j) {
@@ -459,7 +469,7 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
       __syncwarp();
     } else if (warp == MMA_WARP) {
       // ------------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t id_s = idesc_bf16(BQ, BK, false, false);
         constexpr uint32_t id_g = idesc_bf16(BK, D, true, true);
         const uint64_t kad = sdesc_sw128(sb + L::OFF_KA, 0, 1024), kbd = sdesc_sw128(sb + L::OFF_KB, 0, 1024);
@@ -545,7 +555,7 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
       reg_fence32(held);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sa_free);
+      arrive_one(sa_free);
       const int kg = k0 + grp * 32;
       const bool masked = (kg + 31 >= p.NK) || (q >= p.NQ) || (p.causal && kg + 31 > q + p.off);
       uint32_t pk[16];
@@ -562,7 +572,7 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
         if (h == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(sb_free);
+          arrive_one(sb_free);
         }
         const uint32_t(&ha)[16] = *reinterpret_cast<const uint32_t(*)[16]>(&held[16 * h]);
         auto run = [&](const uint32_t(&s1)[16], const uint32_t(&s2)[16]) {
@@ -596,7 +606,7 @@ __device__ __forceinline__ void dk_block(const Problem& p, const float* __restri
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      arrive_one(ds_full);
       nAr = nA2;
       nBr = nB2;
       Gr = G2;

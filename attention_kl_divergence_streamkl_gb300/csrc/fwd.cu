@@ -192,17 +192,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_slot = bar_q + 80;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_BAR + 84);
 
-  if (threadIdx.x == 0) {
-    mbar_init(bar_q, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, 1);
-      mbar_init(bar_sfull + 8 * s, 1);
-      mbar_init(bar_sfree + 8 * s, SOFTMAX_WARPS);
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(bar_q, 1);
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(bar_full + 8 * s, 1);
+        mbar_init(bar_empty + 8 * s, 1);
+        mbar_init(bar_sfull + 8 * s, 1);
+        mbar_init(bar_sfree + 8 * s, SOFTMAX_WARPS);
+      }
+      mbar_init(bar_qempty, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    mbar_init(bar_qempty, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   if (warp == MMA_WARP) {
     tmem_alloc(tmem_slot, kTmemCols);
@@ -211,10 +215,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + 80);
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + 80), status);
+  constexpr uint32_t tmem = 0;
 
   if (warp == PRODUCER_WARP) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&mq1);
       prefetch_tensormap(&mk1);
       prefetch_tensormap(&mq2);
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == MMA_WARP) {
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_bf16(BM, BN, false, false);
       const uint64_t q1d = sdesc_sw128(sb + L::OFF_Q1, 0, 1024), q2d = sdesc_sw128(sb + L::OFF_Q2, 0, 1024);
       int T = 0, k = 0;
@@ -291,8 +296,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (ok) mma_commit(bar_qempty);  // this item's MMAs done: the producer may load the next Q tiles
       }
-      // the last commit completes once every MMA issued here has finished
-      if (T > 0) mbar_drain(bar_sfull + 8 * ((T - 1) & 1), ((T - 1) >> 1) & 1, status);
+      // the last commit completes once every MMA issued here has finished; no arrival is under way when the block leaves
+      if (ok && k > 0)
+        mbar_drain(bar_qempty, (k - 1) & 1, status);
+      else if (T > 0)
+        mbar_drain(bar_sfull + 8 * ((T - 1) & 1), ((T - 1) >> 1) & 1, status);
     }
     __syncwarp();
   } else {
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         reg_fence32(b1);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sfree + 8 * s);
+        arrive_one(bar_sfree + 8 * s);
         const int key0 = j * BN + grp * 64;
         const bool masked = (key0 + 63 >= p.NK) || (p.causal && key0 + 63 > row_lim);
         if (masked)

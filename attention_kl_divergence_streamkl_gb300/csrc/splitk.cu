@@ -141,18 +141,22 @@ __global__ void __launch_bounds__(THREADS)
                    : "memory");
     }
   }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
-      mbar_init(bar_empty + 8 * s, CONSUMERS);
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(bar_full + 8 * s, 1);
+        mbar_init(bar_empty + 8 * s, CONSUMERS);
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();  // the copies' proxy sees the barriers too
     }
-    *abort_flag = 0;
-    fence_mbar_init();
+    __syncwarp();  // the warp's other lanes wait for the one that sets the barriers up
   }
   __syncthreads();
 
   if (warp == CONSUMERS) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tensormap(&mk1);
       prefetch_tensormap(&mk2);
       int issued = 0;
@@ -172,6 +176,7 @@ __global__ void __launch_bounds__(THREADS)
       for (int it = max(0, issued - STAGES); it < issued; ++it)
         mbar_drain(bar_full + 8 * (it % STAGES), (it / STAGES) & 1, status);
     }
+    __syncwarp();
     return;
   }
 
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+    arrive_one(bar_empty + 8 * s);
 
     const int ka = (t_begin + it) * BN + warp * 16 + g, kb = ka + 8;
 #pragma unroll

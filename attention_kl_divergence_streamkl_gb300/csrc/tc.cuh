@@ -50,10 +50,17 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// A block that owns all 512 TMEM columns has them from column 0 on.  tcgen05.alloc's answer is looked at, by every warp and
+// before the warps' registers are dealt out anew by setmaxnreg: no load of it is in flight then, and the addresses that
+// follow are constants.  (With the answer kept in a register the attention kernels ended, once in 10^4 runs of two streams
+// side by side, in an illegal-address error; like this 4 10^6 such runs did not.  Why is not known.)  Another base
+// is recorded like a wait that ran out.
+__device__ __forceinline__ void whole_tmem(volatile uint32_t* slot, int* status) {
+  if (*slot != 0) atomicOr(status, kStatusTimeout);
+}
+
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// generic-proxy shared-memory writes -> visible to the tensor core (async proxy)
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---- MMA (one thread issues)
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool acc) {
