@@ -308,7 +308,7 @@ __device__ __forceinline__ void kv_block(const AttnProblem& p, const uint4* __re
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  setup_barrier(ql, kl);
   tc_fence_after();
   whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
   constexpr uint32_t tmem = 0;
@@ -668,7 +668,7 @@ __device__ __forceinline__ void q_block(const AttnProblem& p, const uint4* __res
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  setup_barrier(ql, kl);
   tc_fence_after();
   whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
   constexpr uint32_t tmem = 0;

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  setup_barrier(ql, kl);
   tc_fence_after();
   whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
   constexpr uint32_t tmem = 0;

@@ -43,3 +43,14 @@ def test_one_elected_lane_issues(name):
     for m in re.finditer(r"if \((?:lane|threadIdx\.x) == 0\)\s*(\{(?:[^{}]|\{[^{}]*\})*\}|[^;{]*;)", text):
         assert not re.search(r"mbar_|tma_|mma_|bulk|tcgen05", m.group(1)), m.group(0)[:80]
     assert "elect_one()" in text or "arrive_one(" in text
+
+
+@pytest.mark.parametrize("name", [f for f in TENSOR if "seq_len(" in code(f) and "setmaxnreg" in code(f)])
+def test_lengths_have_arrived_before_registers_are_dealt_out(name):
+    """A block that reads its sequence's lengths from memory uses them in the set-up barrier: no load is in flight when
+    setmaxnreg runs."""
+    text = code(name)
+    for m in re.finditer(r"tmem_alloc\(", text):
+        block = text[m.start():]
+        assert "setup_barrier(ql, kl);" in block[:block.index("setmaxnreg")]
+    assert name in ("attn_fwd.cu", "attn_bwd.cu", "attn_bwd_fused.cu")
