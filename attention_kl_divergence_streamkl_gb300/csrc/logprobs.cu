@@ -12,6 +12,11 @@
 // the digits that sum p x - LSE cancels.  Arguments below -256 are raised to
 // -256: their weight is exactly 0 either way, and 0 * -inf never arises.
 //
+// y may leave fp32's range (rows masked with the type's lowest value), and a log
+// probability x - LSE loses the digits that a large LSE has before the point.  So
+// a row whose LSE comes out above 256, or not finite, is summed again from the
+// differences x - m (row_sum), and its log probabilities are scale (x - m) - L.
+//
 // The forward reads a 16-bit logit with about as many instructions as its bytes
 // take in DRAM time, so for 16-bit types a vector's maximum and its guard against
 // -inf work on packed pairs (raised to -1e30, or fp16's lowest, where that times
@@ -34,6 +39,7 @@
 // warp keeps a sorted list.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -167,7 +173,9 @@ struct Pair<__nv_bfloat16> {
 template <>
 struct Pair<__half> {
   static constexpr float kLow = -65504.0f;
-  static constexpr float kMinC = 0.02f;  // 65504 * 0.02 > 1024 binary orders below any fp16 maximum's term
+  // Used where the vectors' maximum is above kLow / 2: what stands for -inf then lies at least 32752 * 0.02 = 655 binary
+  // orders below the row's maximum, and its weight is 0.
+  static constexpr float kMinC = 0.02f;
   static constexpr uint32_t kLowBits = 0xfbfffbffu;
   static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -252,6 +260,66 @@ __device__ __forceinline__ Cut cut_row(const T* row, int V) {
   return c;
 }
 
+// ---- a row from differences of logits
+constexpr float kTrustedLse = 256.0f;  // up to here x - LSE is off by 1.5e-5 at most
+
+// f over v of all threads, in a fixed order.
+template <int NT, typename F>
+__device__ __forceinline__ float block_all(float v, F f, float* shared) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();  // what was there before has been read
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = shared[0];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) v = f(v, shared[w]);
+  return v;
+}
+
+// Every column of a row to f, several loads in flight.
+template <typename T, int NT, typename F>
+__device__ __forceinline__ void each_column(const T* row, int V, F f) {
+  constexpr int N = Vec<T>::N;
+  const Cut cut = cut_row(row, V);
+  const uint4* vecs = reinterpret_cast<const uint4*>(row + cut.head);
+  for (int v = threadIdx.x; v < cut.nvec; v += 2 * NT) {
+    Vec<T> x[2];
+    x[0].u = load_stream(vecs + v);
+    const bool both = v + NT < cut.nvec;
+    if (both) x[1].u = load_stream(vecs + v + NT);
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i)
+      if (i < N || both) f(to_float(x[i / N].e[i % N]));
+  }
+  for (int j = threadIdx.x; j < V - cut.nvec * N; j += NT) f(to_float(row[j < cut.head ? j : j + cut.nvec * N]));
+}
+
+// The row's largest logit m, log2 of s = sum 2^d and t / s with t = sum 2^d d, d = c (x - m); s is 0 where every logit is
+// -inf.  All threads of the block take part, and have read the row when it returns.
+struct RowSum {
+  float m, s, log2s, mean;
+};
+template <typename T, int NT>
+__device__ __forceinline__ RowSum row_sum(const T* row, int V, float c, float* shared) {
+  RowSum a;
+  a.m = kNegInf;
+  each_column<T, NT>(row, V, [&](float x) { a.m = fmaxf(a.m, x); });
+  a.m = block_all<NT>(a.m, [](float x, float y) { return fmaxf(x, y); }, shared);
+  const float m = a.m == kNegInf ? 0.f : a.m;
+  float s = 0.f, t = 0.f;
+  each_column<T, NT>(row, V, [&](float x) {
+    const float d = max_nan((x - m) * c, kFloor), e = ex2(d);
+    s += e;
+    t = fmaf(e, d, t);
+  });
+  a.s = block_all<NT>(s, [](float x, float y) { return x + y; }, shared);
+  t = block_all<NT>(t, [](float x, float y) { return x + y; }, shared);
+  a.log2s = log2f(a.s);
+  a.mean = t / a.s;
+  return a;
+}
+
 constexpr int kGroups = 16;  // maxima that a thread keeps; group g of a long row goes with g mod 16
 
 template <int NT>
@@ -334,8 +402,59 @@ __device__ void warp_lists(const T* row, int lo, int hi, int K, FwdShared<NT>& s
   }
 }
 
+// A row's outputs, from its sums or (FAR) from differences of logits; tok0, raw0: the thread's first given token and its logit.
+template <typename T, int NT, bool FAR>
+__device__ __forceinline__ void write_row(const FwdArgs& a, long long r, const T* row, FwdShared<NT>& sh, Sums all, long long tok0,
+                                          float raw0) {
+  const int tid = threadIdx.x;
+  float log2s = log2f(all.s), mean = all.t / all.s;
+  float lse = kLn2 * (all.m + log2s);
+  float m = 0.f, L = lse;  // log p = scale (x - m) - L
+  bool empty = false;      // every logit is -inf
+  if (FAR) {
+    const RowSum w = row_sum<T, NT>(row, a.V, a.scale * kLog2e, reinterpret_cast<float*>(sh.warp_sums));
+    empty = w.s == 0.f;
+    log2s = w.log2s;
+    mean = w.mean;
+    m = w.m;
+    L = kLn2 * log2s;
+    lse = empty ? kNegInf : fmaf(m, a.scale, L);
+    if (isinf(lse) && !isinf(m)) lse = copysignf(FLT_MAX, lse);  // past fp32's range, but not a row of nothing
+  }
+  if (tid == 0) {
+    a.lse[r] = lse;
+    a.entropy[r] = empty ? 0.f : kLn2 * (log2s - mean);
+  }
+  auto log_prob = [&](float raw) { return empty ? kNegInf : fmaf(FAR ? raw - m : raw, a.scale, -L); };
+  for (int t = tid; t < a.T; t += NT) {
+    const long long tok = !FAR && t == tid ? tok0 : a.tokens[r * a.T + t];
+    float out = 0.f;  // no token
+    if (tok >= a.V) out = __uint_as_float(0x7fffffffu);
+    else if (tok >= 0) out = log_prob(!FAR && t == tid ? raw0 : to_float(row[tok]));
+    a.logp[r * a.T + t] = out;
+  }
+  if (a.K) {
+    uint64_t* order = sh.best;
+    if (a.parts > 1) {
+      rank_lists<NT>(sh.best, a.parts, a.K, sh.cand);
+      __syncthreads();
+      order = sh.cand;
+    }
+    if (tid < a.K) {
+      const uint64_t k = order[tid];
+      a.top_index[r * a.K + tid] = (long long)(0xffffffffu - (uint32_t)k);
+      a.top_logp[r * a.K + tid] = log_prob(value_of((uint32_t)(k >> 32)));
+    }
+  }
+}
+
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT, kThreadsPerSm / NT) logprobs_fwd_kernel(const FwdArgs a) {
+__device__ __noinline__ void write_far_row(const FwdArgs& a, long long r, const T* row, FwdShared<NT>& sh) {
+  write_row<T, NT, true>(a, r, row, sh, Sums{0.f, 1.f, 0.f}, -1, 0.f);
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, kThreadsPerSm / NT) logprobs_fwd_kernel(const __grid_constant__ FwdArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int NW = NT / 32;
   __shared__ FwdShared<NT> sh;
@@ -484,34 +603,10 @@ __global__ void __launch_bounds__(NT, kThreadsPerSm / NT) logprobs_fwd_kernel(co
 
   Sums all = lane % 8 < a.parts ? sh.part_sums[lane % 8] : Sums{kNegInf, 0.f, 0.f};
   merge_lanes<8>(all);
-  const bool empty = all.m == kNegInf && all.s == 0.f;  // every logit is -inf
-  const float log2s = log2f(all.s);
-  const float lse = empty ? kNegInf : kLn2 * (all.m + log2s);
-  if (tid == 0) {
-    a.lse[r] = lse;
-    a.entropy[r] = empty ? 0.f : kLn2 * (log2s - all.t / all.s);
-  }
-  auto log_prob = [&](float raw) { return empty ? kNegInf : fmaf(raw, a.scale, -lse); };
-  for (int t = tid; t < a.T; t += NT) {
-    const long long tok = t == tid ? tok0 : a.tokens[r * a.T + t];
-    float out = 0.f;  // no token
-    if (tok >= a.V) out = __uint_as_float(0x7fffffffu);
-    else if (tok >= 0) out = log_prob(t == tid ? raw0 : to_float(row[tok]));
-    a.logp[r * a.T + t] = out;
-  }
-  if (a.K) {
-    uint64_t* order = sh.best;
-    if (a.parts > 1) {
-      rank_lists<NT>(sh.best, a.parts, a.K, sh.cand);
-      __syncthreads();
-      order = sh.cand;
-    }
-    if (tid < a.K) {
-      const uint64_t k = order[tid];
-      a.top_index[r * a.K + tid] = (long long)(0xffffffffu - (uint32_t)k);
-      a.top_logp[r * a.K + tid] = log_prob(value_of((uint32_t)(k >> 32)));
-    }
-  }
+  if (fabsf(kLn2 * (all.m + log2f(all.s))) <= kTrustedLse)
+    write_row<T, NT, false>(a, r, row, sh, all, tok0, raw0);
+  else
+    write_far_row<T, NT>(a, r, row, sh);
 }
 
 struct BwdArgs {
@@ -528,21 +623,27 @@ struct BwdArgs {
 //     dx_j = sum_t g_t [j = token_t] - p_j (A + B (l_j + H)),   dlogits_j = scale dx_j
 // The pass writes the second term; then the given tokens' columns, a handful, are written again with the sum of
 // both in fp32, rounded once.  A token that is given twice adds twice: its first place takes the sum of all.
+// FAR: l_j = scale (x_j - m) - L, of a row that is summed again; else x_j scale - LSE.  (A copy of its own, inline: a function
+// call cost the ordinary rows 1 to 5%, m and L in their loop 2%.)
 // Bound by DRAM: 4096 x 131072 bf16 324 us, 6.6 TB/s; 333 x 50021 fp16 with 16 tokens 13.8 us, 4.8 TB/s.  (With the first
 // vectors' loads before the sums over the tokens the registers do not suffice: 332 us.)
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdArgs a) {
+template <typename T, int NT, bool FAR>
+__device__ __forceinline__ void write_gradient(const BwdArgs& a, long long r, float* sum_g) {
   constexpr int N = Vec<T>::N;
-  __shared__ float sum_g[NT / 32];
   const int tid = threadIdx.x;
   const int part = (int)(blockIdx.x & (a.parts - 1u));
-  const long long r = blockIdx.x >> a.log_parts;
   const T* row = static_cast<const T*>(a.logits) + r * a.stride;
   T* out = static_cast<T*>(a.out) + r * a.out_stride;
   const long long* tokens = a.tokens + r * a.T;
   const float* g = a.g_logp + r * a.T;
-  const float lse = a.lse[r];
-  const bool empty = lse == kNegInf;  // every logit is -inf: nothing depends on them
+  float m = 0.f, L = a.lse[r];
+  const bool empty = L == kNegInf;  // every logit is -inf: nothing depends on them
+  if (FAR) {
+    const RowSum w = row_sum<T, NT>(row, a.V, a.scale * kLog2e, sum_g);
+    m = w.m;
+    L = kLn2 * w.log2s;
+    __syncthreads();  // sum_g has been read
+  }
 
   // A in a fixed order: thread t takes tokens t, t + NT, ...; lanes, then warps
   float A = 0.f;
@@ -557,12 +658,18 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdAr
   A = 0.f;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) A += sum_g[w];
+  if constexpr (!FAR) {
+    if (fabsf(L) > kTrustedLse && !empty) {  // here and not sooner: the LSE's load runs beside the tokens'
+      write_gradient<T, NT, true>(a, r, sum_g);
+      return;
+    }
+  }
   const float B = a.g_entropy ? a.g_entropy[r] : 0.f;
   const float H = a.g_entropy ? a.entropy[r] : 0.f;
   // dlogits = p (a0 + a1 l2), l2 = log2 p
   const float a0 = -a.scale * (A + B * H), a1 = -a.scale * B * kLn2;
   auto grad = [&](float x) {
-    const float l2 = max_nan(fmaf(x, a.scale, -lse) * kLog2e, kFloor);  // one rounding where x is near the LSE
+    const float l2 = max_nan(fmaf(FAR ? x - m : x, a.scale, -L) * kLog2e, kFloor);  // one rounding where x is near the LSE
     return empty ? 0.f : ex2(l2) * fmaf(a1, l2, a0);
   };
 
@@ -616,6 +723,12 @@ __global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const BwdAr
   }
 }
 
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 2048 / NT) logprobs_bwd_kernel(const __grid_constant__ BwdArgs a) {
+  __shared__ float sum_g[NT / 32];
+  write_gradient<T, NT, false>(a, blockIdx.x >> a.log_parts, sum_g);
+}
+
 // Blocks that share a row: as many (a power of two, at most 8, the portable cluster size) as keep the launch within
 // two blocks for each SM, and no part below kMinPartBytes.
 constexpr long long kMinPartBytes = 8192;
@@ -663,7 +776,8 @@ cudaError_t launch_fwd_t(FwdArgs a, long long rows, int num_sms, cudaStream_t st
 template <typename T>
 cudaError_t launch_bwd_t(BwdArgs a, long long rows, int num_sms, cudaStream_t st) {
   const long long bytes = (long long)a.V * sizeof(T);
-  a.log_parts = log_parts_of(rows, bytes, num_sms);
+  // in place a row has one block, which has read it whole before it writes where it sums it again
+  a.log_parts = a.out == a.logits ? 0 : log_parts_of(rows, bytes, num_sms);
   a.parts = 1 << a.log_parts;
   if (bytes <= kShortRowBytes)
     logprobs_bwd_kernel<T, 128><<<(unsigned)(rows * a.parts), 128, 0, st>>>(a);

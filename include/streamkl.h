@@ -386,13 +386,19 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
  * A logit of -inf has probability 0.  A row of nothing but -inf has LSE -inf,
  * entropy 0, log probabilities -inf and a zero gradient.  A +inf or NaN logit
  * makes its row's values NaN (alternatives are then any columns of the row).
+ * Finite logits are finite numbers, the type's lowest value too: a row masked
+ * whole with it is uniform.  An LSE past fp32's range is given as its end.  A row
+ * whose |LSE| is above 256 is read twice more, for log probabilities that do
+ * not lose the digits which the LSE has before the point.
  *
  * streamkl_logprobs_bwd writes dlogits [rows, vocab] (rows `out_stride` elements
  * apart, `dtype`) for upstream gradients g_logp [rows, num_tokens] and, unless
  * NULL, g_entropy [rows] (entropy is read only then); lse and entropy are the
  * forward's.  A token given twice in a row adds twice.  The alternatives have no
  * gradient: to train on some, give them as tokens.  dlogits may be the logits
- * themselves, with the same stride, only where num_tokens is 0.
+ * themselves, with the same stride, only where num_tokens is 0 (a row is then one
+ * block's work).  A given token is compared with the row's others: num_tokens is
+ * meant for alternatives, tens or hundreds, its square is the cost.
  * Sums are fp32.  Results do not depend on the order in which blocks run.
  */
 typedef enum { STREAMKL_BF16 = 0, STREAMKL_FP16 = 1, STREAMKL_FP32 = 2 } streamkl_dtype;
