@@ -8,10 +8,12 @@
 //     at the end O / l and LSE = ln2 (m + log2 l)
 // m is a reference, not the exact maximum: once a row has one, a tile is summed
 // against it without taking its own maximum, and only where a row's sum would
-// pass 2^64 is m moved to the tile's maximum and O, which stays in TMEM, scaled.
+// pass 2^16 is m moved to the tile's maximum and O, which stays in TMEM, scaled.
 // That is exact because p, l and O share m and bf16 has fp32's exponent range;
 // rounding p to bf16 costs half a bf16 step of each weight, as the product's
-// other operand v has; l sums the unrounded p.
+// other operand v has; l sums the unrounded p.  O holds up to 2^16 |v| a tile before
+// the division, so values up to 2^88 give finite sums at any length (2^23 tiles);
+// 2^16 is seldom passed, a higher limit would narrow the values' range.
 //
 // A block owns two tiles of 128 rows and streams 128-key tiles of K and V, so
 // each K and V tile loaded from L2 serves 256 rows:
@@ -50,7 +52,7 @@ constexpr int THREADS = 12 * 32;
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // 256 * 200 + 128 * 104 = 384 * 168 at launch
 constexpr uint32_t kTmemCols = 512;
 constexpr int kFreshTiles = 16;  // see attn_fwd_kernel's FRESH
-constexpr float kSumLimit = 18446744073709551616.0f;  // 2^64
+constexpr float kSumLimit = 65536.0f;  // 2^16
 
 template <int D>
 struct Smem {

@@ -313,7 +313,8 @@ streamkl_status streamkl_bwd_mutual_workspace(streamkl_shape s, int bwd_mode, si
  * within 0 .. N).  What lies past them is not used, whatever it holds, NaN
  * included.  causal keeps key j for query i iff j <= i + k_len - q_len.
  * A row that sees no key -- past its sequence, causal with more queries than
- * keys, no keys at all -- has O = 0 and LSE = -inf.
+ * keys, no keys at all -- has O = 0 and LSE = -inf.  Values |v| up to 2^88 give finite
+ * results at any length (sums are fp32, before their division).
  * Workspace: fp32 partials of the key splits that few query tiles get, 0 bytes
  * where the query tiles fill the SMs; streamkl_attn_fwd_plan gives the choice for any SM count (a
  * pure host rule): packed != 0 when all query heads of a key head share one
