@@ -562,8 +562,10 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
     bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED (D = 64) visits each tile pair once and adds dq up
-    in no fixed order; BWD_AUTO picks by shape.
+    in no fixed order; BWD_AUTO picks by shape, BWD_SEPARATE where torch.use_deterministic_algorithms asks for the same bits.
     """
+    if bwd_mode == BWD_AUTO and torch.are_deterministic_algorithms_enabled():
+        bwd_mode = BWD_SEPARATE
     got = (_calls or calls()).attn_bwd(q, k, v, o, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode)
     if got is not None:
         return got
