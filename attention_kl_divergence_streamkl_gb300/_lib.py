@@ -35,6 +35,7 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_SCRA
 BWD_AUTO, BWD_FUSED, BWD_SEPARATE, BWD_DQ_ONLY, BWD_DK_ONLY = 0, 1, 2, 3, 4
 SPLITK_MAX_NQ = 16
 LOGPROBS_MAX_TOP_K = 32
+ATTN_EXACT_KEYS = 64  # for rows of up to so many keys the attention backward forms its row sums without o
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # streamkl_dtype
 
 
@@ -49,7 +50,7 @@ class Shape(ctypes.Structure):
 class AttnShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("HK", ctypes.c_int), ("NQ", ctypes.c_int), ("NK", ctypes.c_int),
                 ("D", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int), ("q_lens", ctypes.c_void_p),
-                ("k_lens", ctypes.c_void_p)] + [(f"{t}_stride_{x}", ctypes.c_longlong) for t in "qkvo" for x in "bhn"]
+                ("k_lens", ctypes.c_void_p)] + [(f"{t}_stride_{x}", ctypes.c_longlong) for t in "qkvo" for x in "bhn"] + [("o_rest", ctypes.c_void_p)]
 
 
 class StreamKLError(RuntimeError):
@@ -461,10 +462,11 @@ def _layout(t):
 
 
 def make_attn_shape(B, H, HK, NQ, NK, D, scale=None, causal=False, q_lens=None, k_lens=None, q_strides=(0, 0, 0),
-                    k_strides=(0, 0, 0), v_strides=(0, 0, 0), o_strides=(0, 0, 0)) -> AttnShape:
-    """The C shape of an attention; lens are int32 device tensors (kept alive by the caller) or None."""
+                    k_strides=(0, 0, 0), v_strides=(0, 0, 0), o_strides=(0, 0, 0), o_rest=None) -> AttnShape:
+    """The C shape of an attention; lens are int32 device tensors, o_rest one like o (kept alive by the caller), or None."""
     return AttnShape(B, H, HK, NQ, NK, D, scale or 0.0, bool(causal), None if q_lens is None else q_lens.data_ptr(),
-                     None if k_lens is None else k_lens.data_ptr(), *q_strides, *k_strides, *v_strides, *o_strides)
+                     None if k_lens is None else k_lens.data_ptr(), *q_strides, *k_strides, *v_strides, *o_strides,
+                     None if o_rest is None else o_rest.data_ptr())
 
 
 def _lens(t, B, dev, name):
@@ -476,14 +478,14 @@ def _lens(t, B, dev, name):
 
 
 def _attn_inputs(tensors, q_lens, k_lens):
-    """Validates an attention's tensors (q, k, v, and o, do in the backward).
+    """Validates an attention's tensors (q, k, v, and o, do, o_rest in the backward).
 
     Returns (the tensors on the device, q_lens, k_lens, (B, H, HK, NQ, NK, D), device, was_host)."""
     q, k, v = tensors[:3]
     shape, key_shape, dev = q.shape, k.shape, q.device
     for t in tensors:
         if t.dtype is not torch.bfloat16:
-            raise TypeError("q, k, v, o, do must be bfloat16")
+            raise TypeError("q, k, v, o, do, o_rest must be bfloat16")
         if t.device != dev:
             raise ValueError("inputs on different devices")
     if len(shape) != 4 or len(key_shape) != 4:
@@ -494,7 +496,7 @@ def _attn_inputs(tensors, q_lens, k_lens):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)}")
     for t in tensors[3:]:
         if t.shape != shape:
-            raise ValueError(f"o, do must be {tuple(shape)}")
+            raise ValueError(f"o, do, o_rest must be {tuple(shape)}")
     if HK == 0 or H % HK:
         raise ValueError(f"{H} query heads do not divide over {HK} key heads")
     host = dev.type == "cpu"
@@ -525,27 +527,29 @@ def _attn_workspace(name, index, sizes, causal, *mode):
     return n.value
 
 
-def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None):
+def attn_fwd(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, return_rest=False):
     """Attention: (o bf16 with q's layout, lse fp32 [B, H, N_Q]).
 
     q: [B, H, N_Q, D], k and v: [B, HK, N_K, D] bf16, H a multiple of HK; q_lens, k_lens: int32 [B] lengths of a
     padded batch's sequences.  Causal masking is aligned at the last query and key of each sequence.  Rows that
-    see no key give 0 and -inf.
+    see no key give 0 and -inf.  return_rest adds what rounding o to bf16 left, a bf16 tensor like o, for attn_bwd.
     """
-    got = (_calls or calls()).attn_fwd(q, k, v, scale, causal, q_lens, k_lens)
+    got = (_calls or calls()).attn_fwd(q, k, v, scale, causal, q_lens, k_lens, return_rest)
     if got is not None:
         return got
     (q, k, v), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v), q_lens, k_lens)
     (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
     B, H, _, NQ, _, D = sizes
-    s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, qs)
+    rest = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev) if return_rest else None
+    s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, qs, rest)
     nbytes = _attn_workspace("streamkl_attn_fwd_workspace", dev.index, sizes, bool(causal))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     o = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
     lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
     _call("streamkl_attn_fwd", dev.index, q.data_ptr(), k.data_ptr(), v.data_ptr(), s, o.data_ptr(), lse.data_ptr(),
           ws.data_ptr() if nbytes else None, nbytes)
-    return _back((o, lse), True) if host else (o, lse)
+    out = (o, lse, rest) if return_rest else (o, lse)
+    return _back(out, True) if host else out
 
 
 def attn_bwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False, bwd_mode=BWD_AUTO):
@@ -557,27 +561,34 @@ def attn_bwd_plan(B, H, HK, NQ, NK, D, num_sms, causal=False, bwd_mode=BWD_AUTO)
     return path.value, kv.value, q.value, n.value
 
 
-def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None, bwd_mode=BWD_AUTO):
+def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None, bwd_mode=BWD_AUTO,
+             o_rest=None):
     """Attention's gradients (dq, dk, dv), bf16 with the layouts of q, k, v.
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
+    o_rest: attn_fwd's too (return_rest).  Without it dq and dk carry o's rounding: among more than 64 keys their error grows
+    with the part that v's rows have in common, to several times that of their own rounding (attention gives it).
     bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED (D = 64) visits each tile pair once and adds dq up
     in no fixed order; BWD_AUTO picks by shape, BWD_SEPARATE where torch.use_deterministic_algorithms asks for the same bits.
     """
     if bwd_mode == BWD_AUTO and torch.are_deterministic_algorithms_enabled():
         bwd_mode = BWD_SEPARATE
-    got = (_calls or calls()).attn_bwd(q, k, v, o, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode)
+    got = (_calls or calls()).attn_bwd(q, k, v, o, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode, o_rest)
     if got is not None:
         return got
-    (q, k, v, o, do), q_lens, k_lens, sizes, dev, host = _attn_inputs((q, k, v, o, do), q_lens, k_lens)
-    (q, qs), (k, ks), (v, vs), (o, os_), (do, ds) = _layout(q), _layout(k), _layout(v), _layout(o), _layout(do)
+    (q, k, v, *like_o), q_lens, k_lens, sizes, dev, host = _attn_inputs(
+        (q, k, v, o, do) if o_rest is None else (q, k, v, o, do, o_rest), q_lens, k_lens)
+    (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
+    like_o = [_layout(t) for t in like_o]
     B, H, HK, NQ, NK, D = sizes
-    if os_ != ds:  # the library reads both with one set of strides
-        o, do = (t.clone(memory_format=torch.contiguous_format) for t in (o, do))
+    os_ = like_o[0][1]
+    if any(st != os_ for _, st in like_o):  # the library reads them with one set of strides
+        like_o = [(t.clone(memory_format=torch.contiguous_format), None) for t, _ in like_o]
         os_ = (H * NQ * D, NQ * D, D)
+    o, do, rest = [t for t, _ in like_o] + ([None] if o_rest is None else [])
     lse = _rows(lse, dev, (B, H, NQ), "lse")
     dlse = _rows(dlse, dev, (B, H, NQ), "dlse")
-    s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, os_)
+    s = make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, os_, rest)
     nbytes = _attn_workspace("streamkl_attn_bwd_workspace", dev.index, sizes, bool(causal), bwd_mode)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     dq = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)

@@ -63,9 +63,10 @@ def attention_kl(q1, k1, q2, k2, scale=None, causal=False, reduction="mean", bwd
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, scale, causal, q_lens, k_lens, bwd_mode):
-        o, lse = _lib.attn_fwd(q, k, v, scale, causal, q_lens, k_lens)
-        ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens)
+    def forward(ctx, q, k, v, scale, causal, q_lens, k_lens, bwd_mode, train):
+        # up to 64 keys the backward forms its row sums without o
+        o, lse, *rest = _lib.attn_fwd(q, k, v, scale, causal, q_lens, k_lens, train and k.shape[2] > _lib.ATTN_EXACT_KEYS)
+        ctx.save_for_backward(q, k, v, o, lse, q_lens, k_lens, *rest)
         ctx.scale, ctx.causal, ctx.bwd_mode = scale, causal, bwd_mode
         ctx.set_materialize_grads(False)
         return o, lse
@@ -73,13 +74,13 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do, dlse):
-        q, k, v, o, lse, q_lens, k_lens = ctx.saved_tensors
+        q, k, v, o, lse, q_lens, k_lens, *rest = ctx.saved_tensors
         if do is None and dlse is None:
-            return (None,) * 8
+            return (None,) * 9
         if do is None:
             do = torch.zeros_like(o)
-        return (*_lib.attn_bwd(q, k, v, o, lse, do, dlse, ctx.scale, ctx.causal, q_lens, k_lens, ctx.bwd_mode),
-                None, None, None, None, None)
+        return (*_lib.attn_bwd(q, k, v, o, lse, do, dlse, ctx.scale, ctx.causal, q_lens, k_lens, ctx.bwd_mode, *rest),
+                None, None, None, None, None, None)
 
 
 def attention(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, return_lse=False, bwd_mode=_lib.BWD_AUTO):
@@ -88,9 +89,11 @@ def attention(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, retur
 
     The attention of a model that is distilled with attention_kl, which takes the same q and k.  k and v may have
     fewer heads than q; q_lens, k_lens (int32 [B]) are the lengths of a padded batch's sequences.  See attn_fwd,
-    and attn_bwd for bwd_mode.
+    and attn_bwd for bwd_mode.  Where a gradient will be asked for, what rounding o left (a tensor like o) is kept for
+    the backward beside q, k, v, o and lse.
     """
-    o, lse = _Attention.apply(q, k, v, scale, causal, q_lens, k_lens, bwd_mode)
+    train = torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)
+    o, lse = _Attention.apply(q, k, v, scale, causal, q_lens, k_lens, bwd_mode, train)
     return (o, lse) if return_lse else o
 
 

@@ -635,6 +635,8 @@ static streamkl_status attn_problem(const streamkl_attn_shape& s, AttnProblem* p
       !strides_ok(s.o_stride_b, s.o_stride_h, s.o_stride_n, s.H, s.NQ, s.D, &p->os_b, &p->os_h, &p->os_n))
     return STREAMKL_ERR_INVALID;
   p->rows = (long long)s.B * s.H * s.NQ;
+  p->o_rest = s.o_rest;
+  if (!aligned16(s.o_rest)) return STREAMKL_ERR_INVALID;
   if (!aligned_to_or_null(s.q_lens, 4) || !aligned_to_or_null(s.k_lens, 4)) return STREAMKL_ERR_INVALID;
   return STREAMKL_OK;
 }
@@ -733,7 +735,7 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
   }
   int* status = nullptr;
   if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
-  return from_cuda(launch_attn_bwd(p, plan, AttnBwdIn{q, k, v, o, go, lse, dlse}, dq, dk, dv, workspace, status,
+  return from_cuda(launch_attn_bwd(p, plan, AttnBwdIn{q, k, v, o, go, p.o_rest, lse, dlse}, dq, dk, dv, workspace, status,
                                    static_cast<cudaStream_t>(stream)));
 }
 

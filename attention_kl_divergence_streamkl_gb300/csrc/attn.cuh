@@ -48,6 +48,18 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
   tmem_st16(taddr + 16, *reinterpret_cast<const uint32_t(*)[16]>(&r[16]));
 }
 
+__device__ __forceinline__ float2 from_bf16_pair(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+// a += the pair, by additions that take a bf16.
+__device__ __forceinline__ void add_bf16_pair(float2& a, uint32_t v) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(v));
+}
+// What rounding x to bf16 leaves.
+__device__ __forceinline__ float bf16_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
+
 // ---- row values of the backward: -LSE / scale and -delta of a query row, each as three bf16 that add up to its 24
 // bits, in 16 bytes.  128 rows of them are the 16-wide K step that adds the rows' values to a product.
 constexpr float kNoRow = -1.0e30f;  // -LSE / scale of a row that sees no key: its P is exactly 0

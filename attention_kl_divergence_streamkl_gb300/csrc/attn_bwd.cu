@@ -46,12 +46,18 @@ struct BwdMaps {  // of the inputs, and of the outputs
 // ---------------------------------------------------------------------------
 // Row values: -LSE / scale and -delta, delta = dO . O - dLSE.  A row takes D / 8
 // lanes of 16 bytes; bound by the read of O and dO (262144 rows of D 128: 27 us,
-// 5.1 TB/s).
+// 5.1 TB/s).  Without REST three blocks to an SM: the exact rows want their 80 registers (four, 64: B4
+// H16 N64 D64 10.3 -> 11.7 us of the whole backward).
 //
-// O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|.  Among many keys that averages out of the
-// gradients; a row that sees few of them passes it on whole.  For rows of at most 32 keys (the first rows under a causal
-// mask, short sequences) delta is computed as sum_j P_ij dP_ij instead, by the row's own lanes (a key to a lane reads 32
-// lines with every instruction: 25 us for 1500 such rows).
+// O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|, while what it is subtracted from differs from it by
+// no more than the spread of dO . v over the row's keys: the error of dS grows with the part that the values have in
+// common, and where the weights lie on few keys it does not average out.  Error of dQ against 64 bits, in times of its last
+// rounding's: 1.5 for values and logits of ordinary spread; 2 to 3 with a common vector of the values' size, 4 to 10 with one
+// of three times it, 13 to 31 of ten times; 2.5 with logits four times as wide.  With what the forward's rounding left (REST)
+// delta is exact to 16 bits, and all of these are 1.4 to 1.6.  Without it, for rows of at most 64 keys (the first rows under a
+// causal mask, short sequences), delta is computed as sum_j P_ij dP_ij: 16 such rows are one or two warps', whose S and dP are
+// warp-wide products with the head's first keys in shared memory.  (Latency: B4 H16 N64 8.4 -> 10.3 us, B4 H12 N1001/777
+// causal 46.0, with the rest instead 42.5.)
 // Sum of the products of 8 bf16 pairs.
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -61,6 +67,12 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
     sum = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), sum);
   }
   return sum;
+}
+
+// Brings 16 bytes to the L1 cache: a load that nobody waits for.
+__device__ __forceinline__ void touch(const void* p) {
+  uint32_t a, b, c, d;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
 }
 
 // The totals of N values over LANES lanes: on return lane l holds in v[0] the total of value lane_index<N>(l).
@@ -87,11 +99,11 @@ __device__ __forceinline__ void lane_totals(float (&v)[N], int lane) {
 }
 
 constexpr int kRowsEach = 4;  // rows of a thread, all loaded before the first is used; a quarter of the head apart, so
-                              // that the rows that see few keys, which lie together, spread over many threads
-constexpr int kExactKeys = 32, kKeysAtOnce = 4;
+                              // that the rows that see few keys, which lie together, spread over many blocks
+constexpr int kExactKeys = 64;
 
-template <int D>
-__global__ void __launch_bounds__(256, 4)
+template <int D, bool REST>
+__global__ void __launch_bounds__(256, REST ? 4 : 3)
     attn_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
                      float4* __restrict__ acc, unsigned* __restrict__ counters, unsigned n_counters, int padded) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
@@ -111,14 +123,37 @@ __global__ void __launch_bounds__(256, 4)
   const float* lse = in.lse + (long long)bh * p.NQ;
   const float* dlse = in.dlse ? in.dlse + (long long)bh * p.NQ : nullptr;
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint4 x[kRowsEach], y[kRowsEach];
+  // The head's first keys, which all rows of few keys see, for a block that has any: on their way beside the rows.  Rows of 64
+  // bytes more, so that two of them fill the banks.
+  constexpr int LD = LANES + 4;
+  __shared__ uint4 first_k[REST ? 1 : kExactKeys * LD], first_v[REST ? 1 : kExactKeys * LD];
   bool few = false;
+  if constexpr (!REST) {
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) {  // of the group's rows the first to see a key sees the fewest
+      const int from = (int)(blockIdx.x % per_head) * ROWS + u * step, to = min(from + ROWS, ql) - 1;
+      const int first = p.causal ? max(from, ql - kl) : from;
+      few = few || (first <= to && kl > 0 && seen(first) <= kExactKeys);
+    }
+    if (few) {
+      const auto* k = static_cast<const __nv_bfloat16*>(in.k) + b * p.ks_b + h / p.G * p.ks_h + lane * 8;
+      const auto* v = static_cast<const __nv_bfloat16*>(in.v) + b * p.vs_b + h / p.G * p.vs_h + lane * 8;
+#pragma unroll
+      for (int i = 0; i < kExactKeys / ROWS; ++i) {
+        const int j = i * ROWS + threadIdx.x / LANES;
+        first_k[j * LD + lane] = j < kl ? *reinterpret_cast<const uint4*>(k + j * p.ks_n) : none;
+        first_v[j * LD + lane] = j < kl ? *reinterpret_cast<const uint4*>(v + j * p.vs_n) : none;
+      }
+    }
+  }
+  uint4 x[kRowsEach], y[kRowsEach];
 #pragma unroll
   for (int u = 0; u < kRowsEach; ++u) {
     const int n = n0 + u * step, keys = seen(n);
     x[u] = y[u] = none;
-    few = few || (keys > 0 && keys <= kExactKeys);
     if (keys > 0) {
+      if (!REST && keys <= kExactKeys)
+        touch(static_cast<const __nv_bfloat16*>(in.q) + b * p.qs_b + h * p.qs_h + n * p.qs_n + lane * 8);
       x[u] = *reinterpret_cast<const uint4*>(o + n * p.os_n);
       y[u] = *reinterpret_cast<const uint4*>(go + n * p.os_n);
     }
@@ -137,53 +172,83 @@ __global__ void __launch_bounds__(256, 4)
   float sums[kRowsEach];
 #pragma unroll
   for (int u = 0; u < kRowsEach; ++u) sums[u] = dot8(x[u], y[u], 0.f);
+  if constexpr (REST) {
+    const auto* rest = static_cast<const __nv_bfloat16*>(in.o_rest) + b * p.os_b + h * p.os_h + lane * 8;
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) {
+      const int n = n0 + u * step;
+      x[u] = seen(n) > 0 ? *reinterpret_cast<const uint4*>(rest + n * p.os_n) : none;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) sums[u] += dot8(x[u], y[u], 0.f);
+  }
   lane_totals<LANES>(sums, lane);
   if (lane < kRowsEach) {
     row_s[r0 + own * step] = three_bf16(l_own == kNegInf ? kNoRow : -l_own * (1.f / p.scale));
     row_d[r0 + own * step] = three_bf16(l_own == kNegInf ? 0.f : g_own - sums[0]);
   }
-  if (!__syncthreads_or(few)) return;
-  // the head's first keys, which all such rows see, through shared memory
-  __shared__ uint4 first_k[kExactKeys][LANES], first_v[kExactKeys][LANES];
-  const auto* q = static_cast<const __nv_bfloat16*>(in.q) + b * p.qs_b + h * p.qs_h + lane * 8;
-  const auto* k = static_cast<const __nv_bfloat16*>(in.k) + b * p.ks_b + h / p.G * p.ks_h + lane * 8;
-  const auto* v = static_cast<const __nv_bfloat16*>(in.v) + b * p.vs_b + h / p.G * p.vs_h + lane * 8;
-#pragma unroll
-  for (int i = 0; i < kExactKeys / ROWS; ++i) {
-    const int j = i * ROWS + threadIdx.x / LANES;
-    first_k[j][lane] = j < kl ? *reinterpret_cast<const uint4*>(k + j * p.ks_n) : none;
-    first_v[j][lane] = j < kl ? *reinterpret_cast<const uint4*>(v + j * p.vs_n) : none;
-  }
+  if constexpr (REST) return;
+  if (!few) return;
   __syncthreads();
-#pragma unroll 1
-  for (int u = 0; u < kRowsEach; ++u) {
-    const int n = n0 + u * step, sees = seen(n);
-    const int keys = sees <= kExactKeys ? max(sees, 0) : 0;
-    const int most = __reduce_max_sync(0xffffffffu, keys);
-    if (most == 0) continue;
-    uint4 qr = none, gr = none;
-    float lr = kNegInf;
-    if (keys) {
-      qr = *reinterpret_cast<const uint4*>(q + n * p.qs_n);
-      gr = *reinterpret_cast<const uint4*>(go + n * p.os_n);
-      lr = lse[n];
-    }
-    float sum = 0.f;
-    for (int j0 = 0; j0 < most; j0 += kKeysAtOnce) {
-      float t[2 * kKeysAtOnce];
+  // 16 neighbouring rows to SHARE warps, which take 32 keys in turn.  A thread has rows quad and quad + 8, and of each 32
+  // columns the 8 from 8 sub on, as two steps' pairs of both operands: which columns stand at which place of a step does not
+  // matter to the sum, so both come in 16 bytes.
+  constexpr int TILES = ROWS * kRowsEach / 16, SHARE = 8 / TILES;
+  __shared__ float shares[8][16];
+  const int warp = threadIdx.x >> 5, tile = warp / SHARE, quad = (threadIdx.x & 31) >> 2, sub = threadIdx.x & 3;
+  const int row0 = (int)(blockIdx.x % per_head) * ROWS + tile / (ROWS / 16) * step + tile % (ROWS / 16) * 16 + quad;
+  int keys[2];
+  float nl[2], sum[2] = {0.f, 0.f};
+  const uint4 *q[2], *g[2];  // the rows' queries and gradients
 #pragma unroll
-      for (int j = 0; j < kKeysAtOnce; ++j) {
-        t[2 * j] = dot8(qr, first_k[j0 + j][lane], 0.f);
-        t[2 * j + 1] = dot8(gr, first_v[j0 + j][lane], 0.f);
+  for (int i = 0; i < 2; ++i) {
+    const int n = row0 + 8 * i, sees = seen(n);
+    keys[i] = sees > 0 && sees <= kExactKeys ? sees : 0;
+    const float lr = keys[i] ? lse[n] : 0.f;
+    nl[i] = -lr * kLog2e;
+    if (lr == kNegInf) keys[i] = 0;  // written above
+    const long long qn = b * p.qs_b + h * p.qs_h + n * p.qs_n, on = b * p.os_b + h * p.os_h + n * p.os_n;
+    q[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.q) + qn) + sub;
+    g[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.go) + on) + sub;
+  }
+  const int most = __reduce_max_sync(0xffffffffu, max(keys[0], keys[1]));
+  for (int j0 = warp % SHARE * 32; j0 < most; j0 += SHARE * 32) {
+    float s[4][4] = {}, dp[4][4] = {};
+#pragma unroll 2
+    for (int c = 0; c < D / 32; ++c) {
+      const uint4 q0 = keys[0] ? q[0][4 * c] : none, q1 = keys[1] ? q[1][4 * c] : none;
+      const uint4 g0 = keys[0] ? g[0][4 * c] : none, g1 = keys[1] ? g[1][4 * c] : none;
+      const uint32_t qa[2][4] = {{q0.x, q1.x, q0.y, q1.y}, {q0.z, q1.z, q0.w, q1.w}};
+      const uint32_t ga[2][4] = {{g0.x, g1.x, g0.y, g1.y}, {g0.z, g1.z, g0.w, g1.w}};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 kb = first_k[(j0 + i * 8 + quad) * LD + 4 * c + sub], vb = first_v[(j0 + i * 8 + quad) * LD + 4 * c + sub];
+        mma16816(s[i], qa[0], kb.x, kb.y);
+        mma16816(dp[i], ga[0], vb.x, vb.y);
+        mma16816(s[i], qa[1], kb.z, kb.w);
+        mma16816(dp[i], ga[1], vb.z, vb.w);
       }
-      // a lane and the one kKeysAtOnce further hold a key's q . k and dO . v
-      lane_totals<LANES>(t, lane);
-      const float d = __shfl_xor_sync(0xffffffffu, t[0], kKeysAtOnce);
-      if (j0 + lane_index<kKeysAtOnce>(lane) < keys) sum = fmaf(d, ex2(fmaf(t[0], p.c, -lr * kLog2e)), sum);
     }
 #pragma unroll
-    for (int w = 1; w < kKeysAtOnce; w *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-    if (keys && lane == 0) row_d[r0 + u * step] = three_bf16(lr == kNegInf ? 0.f : (dlse ? dlse[n] : 0.f) - sum);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j0 + i * 8 + 2 * sub + (e & 1) < keys[e >> 1])
+          sum[e >> 1] = fmaf(ex2(fmaf(s[i][e], p.c, nl[e >> 1])), dp[i][e], sum[e >> 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    if (SHARE > 1 && sub == 0) shares[warp][quad + 8 * i] = sum[i];
+  }
+  if (SHARE > 1) __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!keys[i] || sub != 0 || warp % SHARE != 0) continue;
+#pragma unroll
+    for (int w = 1; w < SHARE; ++w) sum[i] += shares[warp + w][quad + 8 * i];
+    row_d[(long long)bh * padded + row0 + 8 * i] = three_bf16((dlse ? dlse[row0 + 8 * i] : 0.f) - sum[i]);
   }
 }
 
@@ -878,8 +943,9 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBw
   const long long rows = (long long)p.B * p.H * w.padded;
   auto *row_s = static_cast<uint4*>(w.row_s), *row_d = static_cast<uint4*>(w.row_d);
   constexpr int per_block = 256 / (D / 8) * kRowsEach;
-  attn_rows_kernel<D><<<(unsigned)(rows / per_block), 256, 0, st>>>(
-      p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc), w.kv_counters, w.n_counters, w.padded);
+  const auto rows_kern = in.o_rest ? attn_rows_kernel<D, true> : attn_rows_kernel<D, false>;
+  rows_kern<<<(unsigned)(rows / per_block), 256, 0, st>>>(p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc),
+                                                         w.kv_counters, w.n_counters, w.padded);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (plan.fused) return launch_attn_bwd_fused(p, plan, in, dq, dk, dv, w, status, st);

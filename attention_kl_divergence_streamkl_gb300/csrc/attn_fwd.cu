@@ -36,6 +36,13 @@
 // HK8: 684 us, 6.3 TB/s.  At D 64 the softmax and the one thread that issues the
 // products bound it: N8192 full 498 us, 1105 TFLOP/s.
 //
+// For a backward pass (o_rest) the forward also leaves O - bf16(O), as bf16: delta
+// = dO . O is subtracted from dP, and O's rounding would stand against no more than
+// the spread of dO . v over the keys.  O is then divided by the sum of the rounded
+// weights: an error of theirs moves O by its share of v - O, not of v.  (Cost, the
+// second sum and the second store: B2 H32 N4096 causal D128 232 -> 263 us, N16384
+// 1338 -> 1460, N8192 32 heads D64 586 -> 614.)
+//
 // Few query rows: where all query heads of a key head fit in one tile (G N_Q <=
 // 128) they are packed into it, row g N_Q + n, so that K and V are read once for
 // the whole group.  Few tiles: the keys are split over blocks, each writes its
@@ -69,11 +76,14 @@ struct Smem {
 };
 static_assert(Smem<64>::BYTES <= kWholeSmSmem && Smem<128>::BYTES <= kWholeSmSmem, "shared memory");
 
-// Sum of 2^(c s - m) over a row's 128 columns; the bf16 pairs of the terms go to pk.
+// Sum of 2^(c s - m) over a row's 128 columns; the bf16 pairs of the terms go to pk, with REST their sum to `rounded`
+// (MIXED: by additions that take a bf16; which is faster depends on what bounds the loop, N8192 32 heads D64 641 -> 614 us,
+// N16384 causal D128 1472 -> 1517).
+template <bool REST, bool MIXED>
 __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const uint32_t (&s2)[32],
-                                          const uint32_t (&s3)[32], float c, float m, uint32_t (&pk)[64]) {
+                                          const uint32_t (&s3)[32], float c, float m, uint32_t (&pk)[64], float& rounded) {
   const float2 cc = make_float2(c, c), nm = make_float2(-m, -m);
-  float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+  float2 l0 = make_float2(0.f, 0.f), l1 = l0, r0 = l0, r1 = l0;
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const uint32_t* s = h == 0 ? s0 : h == 1 ? s1 : h == 2 ? s2 : s3;
@@ -86,7 +96,20 @@ __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32
       l1 = fadd2(l1, p1);
       pk[h * 16 + i / 2] = pack_bf16(p0.x, p0.y);
       pk[h * 16 + i / 2 + 1] = pack_bf16(p1.x, p1.y);
+      if (REST) {
+        if (MIXED) {
+          add_bf16_pair(r0, pk[h * 16 + i / 2]);
+          add_bf16_pair(r1, pk[h * 16 + i / 2 + 1]);
+        } else {
+          r0 = fadd2(r0, from_bf16_pair(pk[h * 16 + i / 2]));
+          r1 = fadd2(r1, from_bf16_pair(pk[h * 16 + i / 2 + 1]));
+        }
+      }
     }
+  }
+  if (REST) {
+    r0 = fadd2(r0, r1);
+    rounded = r0.x + r0.y;
   }
   l0 = fadd2(l0, l1);
   return l0.x + l0.y;
@@ -95,12 +118,14 @@ __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32
 // FRESH: a warp whose rows have no reference yet takes the tile's maximum without summing first, which saves 0.5 us of a
 // block's first tile; in the loop of a long stream the test costs more (D 64: N1024 causal 24.5 -> 23.4 us, one token and
 // 129 keys 7.3 -> 6.8; N8192 518 -> 542).
-template <int D, bool FRESH>
+// REST: the part of O that its rounding leaves is stored too.
+template <int D, bool FRESH, bool REST>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_fwd_kernel(const AttnProblem p, float* __restrict__ out_lse,
                     float* __restrict__ part_o, float2* __restrict__ part_ml, int* status,
                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                    const __grid_constant__ CUtensorMap mrest) {
   using L = Smem<D>;
   constexpr int SLOTS = L::SLOTS, S_BUFS = L::S_BUFS;
   constexpr uint32_t kColO = 128 * S_BUFS;  // O_B follows O_A; S buffer i at 128 i
@@ -329,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const uint32_t to = tmem + lanes + kColO + D * t;
     const float c = p.c;
-    float m = kNegInf, l = 0.f;
+    float m = kNegInf, l = 0.f, lr = 0.f;  // lr (REST): the sum of the rounded weights
     bool ok = true, started = false;  // started: some row of the warp has a reference
     for (int i = 0; i < nt; ++i) {
       const int buf = buf_of(t, i);
@@ -362,11 +387,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       // move: a row without a reference that sees keys here, or whose terms grew too large (inf and NaN included)
-      float sum = 0.f;
+      float sum = 0.f, rounded = 0.f;
       bool move = m == kNegInf && seen > 0;
       if (!FRESH || started || !__any_sync(0xffffffffu, move)) {
         load_s();
-        sum = row_exps(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk);
+        sum = row_exps<REST, D == 64>(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk, rounded);
         move = m == kNegInf ? seen > 0 : !(sum < kSumLimit);
       }
       if (__any_sync(0xffffffffu, move)) {
@@ -381,8 +406,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float w = m == kNegInf ? 0.f : ex2(m - m2);
         m = m2;
         l *= w;
+        if (REST) lr *= w;
         if (FRESH) started = __any_sync(0xffffffffu, m != kNegInf);
-        sum = row_exps(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk);
+        sum = row_exps<REST, D == 64>(s0, s1, s2, s3, c, m == kNegInf ? 0.f : m, pk, rounded);
         if (i > 0) {
           ok = mbar_wait_warp(o_done + 8 * buf_of(t, i - 1), use_of(t, i - 1) & 1, status, abort_flag);
           __syncwarp();
@@ -401,6 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       l += sum;
+      if (REST) lr += rounded;
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_st16(ts + 16 * q, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * q]));
@@ -416,7 +443,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (t == 0 || has_b) {
       const size_t row = ((size_t)b * p.H + h) * p.NQ + qn;
       const bool nan = l != l;
-      const float f = nan ? l : l > 0.f ? 1.f / l : 0.f;  // a row that sees no key: zeros
+      // a row that sees no key: zeros.  The splits' partials are weighed by their l, so theirs are O l / lr
+      const float f = nan ? l : l > 0.f ? (REST && p.splits > 1 ? l : 1.f) / (REST ? lr : l) : 0.f;
       if (ok) {
         tc_fence_after();
         if (real && p.splits > 1)
@@ -442,6 +470,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             // through the warp's share of the Q tile: eight lanes write a row's 128 bytes (a lane that writes its own row
             // scatters every store over 32 lines: 6400 cycles a 128 x 128 tile)
             const uint32_t stage = sb + L::OFF_Q + t * L::TILE + wq * 4096;
+            if (REST) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            }
             __syncwarp();
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -462,10 +494,37 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_async_smem();
       }
       // every warp of the tile comes here; one that gave up makes none of them store
-      if (!named_bar_any(1 + t, SOFTMAX_WARPS / 2 * 32, !ok) && p.splits == 1 && wq == 0) {
+      const bool store = !named_bar_any(1 + t, SOFTMAX_WARPS / 2 * 32, !ok) && p.splits == 1;
+      if (store && wq == 0) {
         if (elect_one())
           store_tile<D>(&mo, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
         __syncwarp();
+      }
+      if (REST && store) {  // the rest through the same tile, once the copy has read it
+        named_bar_sync(1 + t, SOFTMAX_WARPS / 2 * 32);
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          if (nt > 0) {
+            tmem_ld32(to + d, o);
+            tmem_ld_wait();
+            reg_fence32(o);
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float x = l > 0.f || nan ? __uint_as_float(o[k]) * f : 0.f;
+            o[k] = __float_as_uint(bf16_rest(x));
+          }
+          stage_row32(sb + L::OFF_Q + t * L::TILE, r, d, o, 1.f);
+        }
+        fence_async_smem();
+        named_bar_sync(1 + t, SOFTMAX_WARPS / 2 * 32);
+        if (wq == 0) {
+          if (elect_one())
+            store_tile<D>(&mrest, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+          __syncwarp();
+        }
       }
     }
   }
@@ -544,31 +603,39 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
   const float inv = none ? 0.f : 1.f / l;
   const long long bh = row / p.NQ;
-  __nv_bfloat16* dst = out + (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + lane * W;
+  const long long at = (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + lane * W;
 #pragma unroll
-  for (int k = 0; k < W; k += 2)
-    *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16(o.x[k] * inv, o.x[k + 1] * inv);
+  for (int k = 0; k < W; k += 2) *reinterpret_cast<uint32_t*>(out + at + k) = pack_bf16(o.x[k] * inv, o.x[k + 1] * inv);
+  if (p.o_rest) {
+    auto* rest = static_cast<__nv_bfloat16*>(p.o_rest);
+#pragma unroll
+    for (int k = 0; k < W; k += 2)
+      *reinterpret_cast<uint32_t*>(rest + at + k) = pack_bf16(bf16_rest(o.x[k] * inv), bf16_rest(o.x[k + 1] * inv));
+  }
 }
 
 template <int D>
 cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
                      void* workspace, int* status, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mo;
+  CUtensorMap mq, mk, mv, mo, mrest{};
   if (!encode_tile_map(&mq, q, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1) ||
       !encode_tile_map(&mk, k, p.D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BN) ||
       !encode_tile_map(&mv, v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BN) ||
-      !encode_tile_map(&mo, o, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1))
+      !encode_tile_map(&mo, o, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1) ||
+      (p.o_rest && !encode_tile_map(&mrest, p.o_rest, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM,
+                                    p.packed ? p.G : 1)))
     return cudaErrorInvalidValue;
   constexpr int smem = kWholeSmSmem;
   const bool fresh = D == 64 && ((p.NK + BN - 1) / BN + p.splits - 1) / p.splits <= kFreshTiles;
-  const auto kern = fresh ? attn_fwd_kernel<D, D == 64> : attn_fwd_kernel<D, false>;
+  const auto kern = p.o_rest ? (fresh ? attn_fwd_kernel<D, D == 64, true> : attn_fwd_kernel<D, false, true>)
+                             : (fresh ? attn_fwd_kernel<D, D == 64, false> : attn_fwd_kernel<D, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml = p.splits > 1 ? reinterpret_cast<float2*>(part_o + (size_t)p.splits * p.rows * D) : nullptr;
   auto* out = static_cast<__nv_bfloat16*>(o);
   const long long blocks = attn_fwd_items(p) * p.splits;
-  kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo);
+  kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo, mrest);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
   attn_merge_kernel<D><<<(unsigned)p.rows, kMergeWarps * 32, 0, st>>>(p, part_o, part_ml, out, lse);
   return cudaGetLastError();
@@ -578,7 +645,9 @@ cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const v
 __global__ void attn_no_keys_kernel(const AttnProblem p, __nv_bfloat16* out, float* lse) {
   const long long row = blockIdx.x;
   const long long bh = row / p.NQ;
-  out[(bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + threadIdx.x] = __float2bfloat16_rn(0.f);
+  const long long at = (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + threadIdx.x;
+  out[at] = __float2bfloat16_rn(0.f);
+  if (p.o_rest) static_cast<__nv_bfloat16*>(p.o_rest)[at] = __float2bfloat16_rn(0.f);
   if (threadIdx.x == 0) lse[row] = kNegInf;
 }
 

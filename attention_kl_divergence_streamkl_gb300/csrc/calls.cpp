@@ -129,16 +129,21 @@ PyObject* tuple(std::initializer_list<at::Tensor> tensors) {
   return t.release();
 }
 
-// attn_fwd(q, k, v, scale, causal, q_lens, k_lens)
+// attn_fwd(q, k, v, scale, causal, q_lens, k_lens[, return_rest])
 PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Attention a;
-  if (n != 7 || !attention(args, 3, &a)) Py_RETURN_NONE;
-  at::Tensor o, lse;
+  if ((n != 7 && n != 8) || !attention(args, 3, &a) || (n == 8 && !PyBool_Check(args[7]))) Py_RETURN_NONE;
+  const bool with_rest = n == 8 && args[7] == Py_True;
+  at::Tensor o, lse, rest;
   int status;
   {
     NoGil no_gil;
     size_t bytes = 0;
+    if (with_rest) {
+      rest = like(*a.q, a.qs, a.index);
+      a.s.o_rest = data(rest);
+    }
     status = streamkl_attn_fwd_workspace(a.s, &bytes);
     if (status == STREAMKL_OK) {
       const at::Tensor ws = workspace(bytes, a.index);
@@ -149,15 +154,15 @@ PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
   }
   if (status != STREAMKL_OK) Py_RETURN_NONE;
-  return tuple({o, lse});
+  return with_rest ? tuple({o, lse, rest}) : tuple({o, lse});
   END_HANDLE_TH_ERRORS
 }
 
-// attn_bwd(q, k, v, o, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode)
+// attn_bwd(q, k, v, o, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode[, o_rest])
 PyObject* attn_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Attention a;
-  if (n != 12 || !attention(args, 7, &a)) Py_RETURN_NONE;
+  if ((n != 12 && n != 13) || !attention(args, 7, &a)) Py_RETURN_NONE;
   const at::Tensor *o = tensor(args[3]), *go = tensor(args[5]);
   Strides os, gs;
   if (!o || !go || !on_device(*o, a.index) || !on_device(*go, a.index) || o->sizes() != a.q->sizes() ||
@@ -166,6 +171,14 @@ PyObject* attn_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   a.s.o_stride_b = os.b;
   a.s.o_stride_h = os.h;
   a.s.o_stride_n = os.n;
+  if (n == 13 && args[12] != Py_None) {
+    const at::Tensor* rest = tensor(args[12]);
+    Strides rs;
+    if (!rest || !on_device(*rest, a.index) || rest->sizes() != a.q->sizes() || !layout(*rest, &rs) || rs.b != os.b ||
+        rs.h != os.h || rs.n != os.n)
+      Py_RETURN_NONE;
+    a.s.o_rest = const_cast<void*>(rest->const_data_ptr());  // read only
+  }
   const float *lse, *dlse;
   const auto row_sizes = a.q->sizes().slice(0, 3);
   if (args[4] == Py_None || !rows(args[4], row_sizes, a.index, &lse) || !rows(args[6], row_sizes, a.index, &dlse) ||

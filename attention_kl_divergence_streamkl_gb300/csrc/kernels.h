@@ -116,6 +116,7 @@ struct AttnProblem {
   // element strides along b, h, n of q (and dq), k (dk), v (dv), o (and do)
   long long qs_b, qs_h, qs_n, ks_b, ks_h, ks_n, vs_b, vs_h, vs_n, os_b, os_h, os_n;
   long long rows;              // B H N_Q
+  void* o_rest;                // null, or what rounding O to bf16 left, with O's strides: the forward writes it
   // forward plan (attn_fwd_plan)
   int packed;   // the query heads of a key head share one tile
   int q_items;  // blocks along the queries, per (batch, head)
@@ -131,6 +132,7 @@ cudaError_t launch_attn_fwd(const AttnProblem& p, const void* q, const void* k, 
 
 struct AttnBwdIn {
   const void *q, *k, *v, *o, *go;  // go = dO, with o's strides
+  const void* o_rest;              // null, or the forward's
   const float *lse, *dlse;         // dlse may be null
 };
 // How a backward runs on a device (a pure rule of sizes).  Tiles [0, whole) of a kind are one block each, the later ones

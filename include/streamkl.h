@@ -330,6 +330,7 @@ typedef struct {
   long long k_stride_b, k_stride_h, k_stride_n;
   long long v_stride_b, v_stride_h, v_stride_n;
   long long o_stride_b, o_stride_h, o_stride_n;
+  void* o_rest; /* NULL, or bf16 like O: see below */
 } streamkl_attn_shape;
 streamkl_status streamkl_attn_fwd_workspace(streamkl_attn_shape s, size_t* bytes);
 streamkl_status streamkl_attn_fwd_plan(streamkl_attn_shape s, int num_sms, int* packed, int* splits);
@@ -341,6 +342,13 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
  * dP = dO V^T, delta_i = dO_i . O_i - dLSE_i and dS = P (dP - delta):
  *     dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO  (dK, dV summed over the
  *     query heads that share a key head)
+ * s.o_rest (NULL, or [B, H, N_Q, D] bf16 with o's strides): the forward writes what
+ * rounding O to bf16 left to it and divides by the sum of its rounded weights, the
+ * backward reads it.  Without it delta carries O's rounding, and dQ, dK an error that
+ * grows with the part that the values have in common (zero mean 1.5 times, a
+ * common vector of three times their size 4 to 9 times that of the last
+ * rounding); with it 1.4 to 1.6 times.  Rows of at most 64 keys need it not: their delta
+ * is formed from P and dP.
  * o, lse: the forward's; go = dLoss/dO with o's strides; dlse = dLoss/dLSE, fp32
  * [B, H, N_Q], or NULL.  dq, dk, dv: bf16 with the strides of q, k, v (which must
  * not make rows overlap).  Lengths and causal as in the forward; gradients of

@@ -50,7 +50,7 @@ def test_autograd_gives_the_same_bits(deterministic):
     q, k, v, do = A.tensors(4, 20, 20, 300, 500, 64, 1)
     leaves = [t.requires_grad_() for t in (q, k, v)]
     runs = [torch.autograd.grad(skl.attention(*leaves), leaves, do) for _ in range(3)]
-    o, lse = skl.attn_fwd(q, k, v)
-    runs.append(skl.attn_bwd(q, k, v, o, lse, do, bwd_mode=skl.BWD_SEPARATE))
+    o, lse, rest = skl.attn_fwd(q, k, v, return_rest=True)
+    runs.append(skl.attn_bwd(q, k, v, o, lse, do, bwd_mode=skl.BWD_SEPARATE, o_rest=rest))
     for got in runs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got, runs[0]))
