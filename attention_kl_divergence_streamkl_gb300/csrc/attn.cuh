@@ -23,10 +23,14 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// The barrier behind a block's set-up.  Its predicate is computed from the sequence's lengths, so their loads have been
-// waited for, and none is in flight, when setmaxnreg deals the registers out anew.
+// The barrier behind a block's set-up.  A vote on the sequence's lengths before it: their loads have been waited for, and none
+// is in flight, when setmaxnreg deals the registers out anew.  (No length is negative, so the fence never runs; it keeps the
+// vote.)
 __device__ __forceinline__ void setup_barrier(int ql, int kl) {
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %0, 0;\n\tbarrier.cta.red.or.pred q, 0, p;\n\t}" ::"r"(ql | kl) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.lt.s32 p, %0, 0;\n\tvote.sync.any.pred q, p, 0xffffffff;\n\t@q membar.cta;\n\t}" ::"r"(ql | kl)
+      : "memory");
+  __syncthreads();
 }
 
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {

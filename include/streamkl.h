@@ -427,7 +427,9 @@ const char* streamkl_status_string(streamkl_status st);
 /*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns STREAMKL_ERR_TIMEOUT if a bounded wait ran out since
- * the last check, STREAMKL_ERR_CUDA if the sync failed, else STREAMKL_OK.
+ * the last check (or a block that owns its SM's tensor memory was given it from
+ * another column than the first, which is recorded the same way),
+ * STREAMKL_ERR_CUDA if the sync failed, else STREAMKL_OK.
  *
  * The status word is one flag per device for the whole process, shared by
  * every caller, stream and thread that uses the library: a timeout on any

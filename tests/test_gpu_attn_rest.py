@@ -94,7 +94,8 @@ def check(q, k, v, do, dlse=None, **kw):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("B,H,HK,NQ,NK", [(1, 4, 2, 512, 512), (2, 2, 1, 130, 700), (1, 8, 2, 3, 5000), (1, 8, 1, 16, 1000),
-                                          (1, 2, 2, 257, 65), (1, 1, 1, 300, 100), (2, 96, 96, 200, 200)])
+                                          (1, 2, 2, 257, 65), (1, 1, 1, 300, 100), (2, 96, 96, 200, 200),
+                                          (3, 8, 2, 5, 90)])
 def test_forward_and_backward(B, H, HK, NQ, NK, causal, D, common, by):
     check(*make(B, H, HK, NQ, NK, D, common, by), causal=causal)
 
