@@ -22,9 +22,10 @@
 // ones).  Rows that see no key, and rows past a sequence's length, get -1e30
 // and 0: their P is exactly 0.
 //
-// Measured at D 128, five products counted: 8 heads, N8192, non-causal 581 us,
-// 1180 TFLOP/s, with the recomputed two 1655, which is near what the power limit
-// leaves a plain matrix product (1750); B2 H32 HK8 N4096 causal 640 us.  Built and
+// Measured at D 128, five products counted: 8 heads, N8192, non-causal 570 to 595
+// us, 1150 to 1200 TFLOP/s, with the recomputed two 1620 to 1690, which is near what
+// the power limit leaves a plain matrix product (1750); B2 H32 HK8 N4096 causal 625
+// to 680 us.  Built and
 // not kept: Q and dO of the dQ block as operands in TMEM (64 KB less
 // shared-memory traffic a tile pair, and 3% slower).
 #include "attn.cuh"

@@ -15,7 +15,7 @@
 // 350 KB (8 heads, N8192, non-causal: 403 us against 388).  What bounds a tile pair, about 2500 cycles, are the 260 KB that
 // are left, 2000 cycles at 128 bytes a clock; the products alone take 1550.  The traffic comes in two halves, between the
 // two barriers of the P and dS warps; dQ is computed before dP, and so staged and reduced while the first half's products
-// leave room (32 heads, 8 key heads, N8192, non-causal: 1185 us, 1160 TFLOP/s of five products; the other way round 1290).
+// leave room (32 heads, 8 key heads, N8192, non-causal: 1190 to 1220 us, 1140 TFLOP/s of five products; the other way round 1290).
 //   warps 0-15   thread = key, group g = warp / 4 takes queries [32g, 32g + 32)
 //   warps 16-19  dQ: TMEM -> registers -> a ring of staging chunks a warp -> bulk reductions
 //   warp 20      TMA producer: K, V once; Q(u) and dO(u) with their rows' values

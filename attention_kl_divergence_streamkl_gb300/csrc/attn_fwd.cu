@@ -27,14 +27,15 @@
 // while one tile's softmax works, the other tile's two products run.
 // At D 64 there is room for three S buffers, [0,384), O_A and O_B behind them: the
 // pairs (A,0), (B,0), (A,1), ... take them in turn and S runs three pairs ahead, so
-// no softmax waits for its next S (one query over 64K keys, B8 H32 HK8: 301 -> 221
-// us; N8192 full, 32 heads: 510 -> 498).
+// no softmax waits for its next S (one query over 64K keys, B8 H32 HK8: 301 -> 226
+// us when it was built, 218 now; N8192 full, 32 heads: 510 -> 498).
 //
-// Measured: D 128, 32 heads, 8 key heads, N16384 causal 1265 us, 1740 TFLOP/s, what
-// the power limit leaves a plain matrix product (1750); 8 heads, N8192 full 177 us,
-// 1550 (two waves for 256 blocks of 152 SMs).  One query over 131072 keys, B8 H32
-// HK8: 684 us, 6.3 TB/s.  At D 64 the softmax and the one thread that issues the
-// products bound it: N8192 full 498 us, 1105 TFLOP/s.
+// Measured: D 128, 32 heads, 8 key heads, N16384 causal 1270 to 1480 us on different
+// cards, 1490 to 1730 TFLOP/s, near what the power limit leaves a plain matrix
+// product (1750); 8 heads, N8192 full 174 to 188 us, 1460 to 1580 (two waves for 256
+// blocks of 152 SMs).  One query over 131072 keys, B8 H32 HK8: 670 us, 6.4 TB/s.  At
+// D 64 the softmax and the one thread that issues the products bound it: N8192 full,
+// 32 heads, 537 us, 1020 TFLOP/s (498 before the arrivals came from an elected lane).
 //
 // For a backward pass (o_rest) the forward also leaves O - bf16(O), as bf16: delta
 // = dO . O is subtracted from dP, and O's rounding would stand against no more than

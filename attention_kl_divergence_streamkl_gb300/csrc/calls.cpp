@@ -4,9 +4,9 @@
 // of the current device, in a layout the library reads in place) and returns
 // None for everything else: _lib.py then goes through the same call step by
 // step, copies what has to be copied, and reports what is wrong.  A call's host
-// time against the ctypes path's: attention forward 6.7 us against 18, its
-// backward 13 against 26, log probabilities 8 against 21, their gradient 4
-// against 18; the short calls' kernels take 8 to 17 us.
+// time against the ctypes path's: attention forward 7 to 8 us against 24, its
+// backward 13 to 14 against 37, log probabilities 9 to 10 against 24, their gradient
+// 4 to 5 against 18; the short calls' kernels take 6 to 14 us.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
