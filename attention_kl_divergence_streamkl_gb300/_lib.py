@@ -35,7 +35,7 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_SCRA
 BWD_AUTO, BWD_FUSED, BWD_SEPARATE, BWD_DQ_ONLY, BWD_DK_ONLY = 0, 1, 2, 3, 4
 SPLITK_MAX_NQ = 16
 LOGPROBS_MAX_TOP_K = 32
-ATTN_EXACT_KEYS = 64  # for rows of up to so many keys the attention backward forms its row sums without o
+ATTN_EXACT_KEYS = 64  # up to so many keys (N_K) the attention backward forms its row sums without o
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # streamkl_dtype
 
 
@@ -566,7 +566,7 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
     """Attention's gradients (dq, dk, dv), bf16 with the layouts of q, k, v.
 
     o, lse: attn_fwd's for the same inputs; do: dLoss/do like o; dlse: dLoss/dlse fp32 [B, H, N_Q] or None.
-    o_rest: attn_fwd's too (return_rest).  Without it dq and dk carry o's rounding: among more than 64 keys their error grows
+    o_rest: attn_fwd's too (return_rest).  Without it, and with N_K above 64, dq and dk carry o's rounding: their error grows
     with the part that v's rows have in common, to several times that of their own rounding (attention gives it).
     bwd_mode BWD_SEPARATE gives the same bits on every run; BWD_FUSED (D = 64) visits each tile pair once and adds dq up
     in no fixed order; BWD_AUTO picks by shape, BWD_SEPARATE where torch.use_deterministic_algorithms asks for the same bits.

@@ -282,7 +282,7 @@ using namespace skl;
 
 extern "C" {
 
-int streamkl_version(void) { return 100; }
+int streamkl_version(void) { return 200; }
 
 const char* streamkl_status_string(streamkl_status st) {
   switch (st) {

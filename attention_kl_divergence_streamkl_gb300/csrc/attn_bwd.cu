@@ -47,18 +47,19 @@ struct BwdMaps {  // of the inputs, and of the outputs
 // ---------------------------------------------------------------------------
 // Row values: -LSE / scale and -delta, delta = dO . O - dLSE.  A row takes D / 8
 // lanes of 16 bytes; bound by the read of O and dO (262144 rows of D 128: 27 us,
-// 5.1 TB/s).  Without REST three blocks to an SM: the exact rows want their 80 registers (four, 64: B4
-// H16 N64 D64 10.3 -> 11.7 us of the whole backward).
+// 5.1 TB/s).  Three blocks to an SM where all rows are exact, which want the
+// registers: B4 H16 N64 D64 10.0 us for the whole backward, 11.3 with four.
 //
 // O is rounded to bf16, so dO . O is off by up to 2^-8 sum_d |dO_d O_d|, while what it is subtracted from differs from it by
 // no more than the spread of dO . v over the row's keys: the error of dS grows with the part that the values have in
 // common, and where the weights lie on few keys it does not average out.  Error of dQ against 64 bits, in times of its last
 // rounding's: 1.5 for values and logits of ordinary spread; 2 to 3 with a common vector of the values' size, 4 to 10 with one
 // of three times it, 13 to 31 of ten times; 2.5 with logits four times as wide.  With what the forward's rounding left (REST)
-// delta is exact to 16 bits, and all of these are 1.4 to 1.6.  Without it, for rows of at most 64 keys (the first rows under a
-// causal mask, short sequences), delta is computed as sum_j P_ij dP_ij: 16 such rows are one or two warps', whose S and dP are
-// warp-wide products with the head's first keys in shared memory.  (Latency: B4 H16 N64 8.4 -> 10.3 us, B4 H12 N1001/777
-// causal 46.0, with the rest instead 42.5.)
+// delta is exact to 16 bits, and all of these are 1.4 to 1.6.  Without it, for rows of at most 32 keys (the first rows under a
+// causal mask) and where no sequence has more than 64, delta is computed as sum_j P_ij dP_ij: 16 such rows are one or two
+// warps', whose S and dP are warp-wide products with the head's first keys in shared memory.  (Latency: B4 H12 N1001/777
+// causal D128 44.4 us for the whole backward, 42.5 with the rest instead; 45.7 with a key to a group of lanes.  B4 H16 N64
+// D64 10.0, 8.3 with dO . O.)
 // Sum of the products of 8 bf16 pairs.
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -70,6 +71,10 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float sum) {
   return sum;
 }
 
+// 16 bytes of a row to shared memory, on their own (cp.async); zeros where it is not `there`.
+__device__ __forceinline__ void copy_row(void* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
 // Brings 16 bytes to the L1 cache: a load that nobody waits for.
 __device__ __forceinline__ void touch(const void* p) {
   uint32_t a, b, c, d;
@@ -101,13 +106,17 @@ __device__ __forceinline__ void lane_totals(float (&v)[N], int lane) {
 
 constexpr int kRowsEach = 4;  // rows of a thread, all loaded before the first is used; a quarter of the head apart, so
                               // that the rows that see few keys, which lie together, spread over many blocks
-constexpr int kExactKeys = 64;
+// kRowsShort: no sequence has more than kShortKeys keys, and all rows are exact; kRowsLong: rows of at most kExactKeys (more would
+// cost the launches of long sequences, which have few such rows, shared memory and registers).
+constexpr int kExactKeys = 32, kShortKeys = 64;
+enum RowsKind { kRowsLong, kRowsShort, kRowsRest };
 
-template <int D, bool REST>
-__global__ void __launch_bounds__(256, REST ? 4 : 3)
+template <int D, RowsKind KIND>
+__global__ void __launch_bounds__(256, KIND == kRowsShort ? 3 : 4)
     attn_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
                      float4* __restrict__ acc, unsigned* __restrict__ counters, unsigned n_counters, int padded) {
-  constexpr int LANES = D / 8, ROWS = 256 / LANES;
+  constexpr int LANES = D / 8, ROWS = 256 / LANES, KEYS = KIND == kRowsShort ? kShortKeys : kExactKeys;
+  constexpr bool REST = KIND == kRowsRest;
   static_assert(BT % (ROWS * kRowsEach) == 0, "a block's rows are one head's");
   for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
   const int step = padded / kRowsEach;
@@ -127,24 +136,14 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
   // The head's first keys, which all rows of few keys see, for a block that has any: on their way beside the rows.  Rows of 64
   // bytes more, so that two of them fill the banks.
   constexpr int LD = LANES + 4;
-  __shared__ uint4 first_k[REST ? 1 : kExactKeys * LD], first_v[REST ? 1 : kExactKeys * LD];
+  __shared__ uint4 first_k[REST ? 1 : KEYS * LD], first_v[REST ? 1 : KEYS * LD];
   bool few = false;
   if constexpr (!REST) {
 #pragma unroll
     for (int u = 0; u < kRowsEach; ++u) {  // of the group's rows the first to see a key sees the fewest
       const int from = (int)(blockIdx.x % per_head) * ROWS + u * step, to = min(from + ROWS, ql) - 1;
       const int first = p.causal ? max(from, ql - kl) : from;
-      few = few || (first <= to && kl > 0 && seen(first) <= kExactKeys);
-    }
-    if (few) {
-      const auto* k = static_cast<const __nv_bfloat16*>(in.k) + b * p.ks_b + h / p.G * p.ks_h + lane * 8;
-      const auto* v = static_cast<const __nv_bfloat16*>(in.v) + b * p.vs_b + h / p.G * p.vs_h + lane * 8;
-#pragma unroll
-      for (int i = 0; i < kExactKeys / ROWS; ++i) {
-        const int j = i * ROWS + threadIdx.x / LANES;
-        first_k[j * LD + lane] = j < kl ? *reinterpret_cast<const uint4*>(k + j * p.ks_n) : none;
-        first_v[j * LD + lane] = j < kl ? *reinterpret_cast<const uint4*>(v + j * p.vs_n) : none;
-      }
+      few = few || (first <= to && kl > 0 && seen(first) <= KEYS);
     }
   }
   uint4 x[kRowsEach], y[kRowsEach];
@@ -153,10 +152,20 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
     const int n = n0 + u * step, keys = seen(n);
     x[u] = y[u] = none;
     if (keys > 0) {
-      if (!REST && keys <= kExactKeys)
+      if (!REST && keys <= KEYS)
         touch(static_cast<const __nv_bfloat16*>(in.q) + b * p.qs_b + h * p.qs_h + n * p.qs_n + lane * 8);
       x[u] = *reinterpret_cast<const uint4*>(o + n * p.os_n);
       y[u] = *reinterpret_cast<const uint4*>(go + n * p.os_n);
+    }
+  }
+  if (few) {
+    const auto* k = static_cast<const __nv_bfloat16*>(in.k) + b * p.ks_b + h / p.G * p.ks_h + lane * 8;
+    const auto* v = static_cast<const __nv_bfloat16*>(in.v) + b * p.vs_b + h / p.G * p.vs_h + lane * 8;
+#pragma unroll
+    for (int i = 0; i < KEYS / ROWS; ++i) {
+      const int j = i * ROWS + threadIdx.x / LANES;
+      copy_row(&first_k[j * LD + lane], k + (j < kl ? j : 0) * p.ks_n, j < kl);
+      copy_row(&first_v[j * LD + lane], v + (j < kl ? j : 0) * p.vs_n, j < kl);
     }
   }
   // lanes 0 to 3 write the values of a row each
@@ -190,8 +199,9 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
   }
   if constexpr (REST) return;
   if (!few) return;
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  // 16 neighbouring rows to SHARE warps, which take 32 keys in turn.  A thread has rows quad and quad + 8, and of each 32
+  // 16 neighbouring rows to SHARE warps, which take 16 keys in turn.  A thread has rows quad and quad + 8, and of each 32
   // columns the 8 from 8 sub on, as two steps' pairs of both operands: which columns stand at which place of a step does not
   // matter to the sum, so both come in 16 bytes.
   constexpr int TILES = ROWS * kRowsEach / 16, SHARE = 8 / TILES;
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int n = row0 + 8 * i, sees = seen(n);
-    keys[i] = sees > 0 && sees <= kExactKeys ? sees : 0;
+    keys[i] = sees > 0 && sees <= KEYS ? sees : 0;
     const float lr = keys[i] ? lse[n] : 0.f;
     nl[i] = -lr * kLog2e;
     if (lr == kNegInf) keys[i] = 0;  // written above
@@ -213,8 +223,8 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
     g[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.go) + on) + sub;
   }
   const int most = __reduce_max_sync(0xffffffffu, max(keys[0], keys[1]));
-  for (int j0 = warp % SHARE * 32; j0 < most; j0 += SHARE * 32) {
-    float s[4][4] = {}, dp[4][4] = {};
+  for (int j0 = warp % SHARE * 16; j0 < most; j0 += SHARE * 16) {
+    float s[2][4] = {}, dp[2][4] = {};
 #pragma unroll 2
     for (int c = 0; c < D / 32; ++c) {
       const uint4 q0 = keys[0] ? q[0][4 * c] : none, q1 = keys[1] ? q[1][4 * c] : none;
@@ -222,7 +232,7 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
       const uint32_t qa[2][4] = {{q0.x, q1.x, q0.y, q1.y}, {q0.z, q1.z, q0.w, q1.w}};
       const uint32_t ga[2][4] = {{g0.x, g1.x, g0.y, g1.y}, {g0.z, g1.z, g0.w, g1.w}};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const uint4 kb = first_k[(j0 + i * 8 + quad) * LD + 4 * c + sub], vb = first_v[(j0 + i * 8 + quad) * LD + 4 * c + sub];
         mma16816(s[i], qa[0], kb.x, kb.y);
         mma16816(dp[i], ga[0], vb.x, vb.y);
@@ -231,7 +241,7 @@ __global__ void __launch_bounds__(256, REST ? 4 : 3)
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (j0 + i * 8 + 2 * sub + (e & 1) < keys[e >> 1])
@@ -944,7 +954,9 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBw
   const long long rows = (long long)p.B * p.H * w.padded;
   auto *row_s = static_cast<uint4*>(w.row_s), *row_d = static_cast<uint4*>(w.row_d);
   constexpr int per_block = 256 / (D / 8) * kRowsEach;
-  const auto rows_kern = in.o_rest ? attn_rows_kernel<D, true> : attn_rows_kernel<D, false>;
+  const auto rows_kern = in.o_rest            ? attn_rows_kernel<D, kRowsRest>
+                         : p.NK <= kShortKeys ? attn_rows_kernel<D, kRowsShort>
+                                              : attn_rows_kernel<D, kRowsLong>;
   rows_kern<<<(unsigned)(rows / per_block), 256, 0, st>>>(p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc),
                                                          w.kv_counters, w.n_counters, w.padded);
   cudaError_t e = cudaGetLastError();

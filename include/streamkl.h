@@ -347,8 +347,8 @@ streamkl_status streamkl_attn_fwd(const void* q, const void* k, const void* v, s
  * backward reads it.  Without it delta carries O's rounding, and dQ, dK an error that
  * grows with the part that the values have in common (zero mean 1.5 times, a
  * common vector of three times their size 4 to 9 times that of the last
- * rounding); with it 1.4 to 1.6 times.  Rows of at most 64 keys need it not: their delta
- * is formed from P and dP.
+ * rounding); with it 1.4 to 1.6 times.  Rows of at most 32 keys need it not, nor any
+ * where N_K is at most 64: their delta is formed from P and dP.
  * o, lse: the forward's; go = dLoss/dO with o's strides; dlse = dLoss/dLSE, fp32
  * [B, H, N_Q], or NULL.  dq, dk, dv: bf16 with the strides of q, k, v (which must
  * not make rows overlap).  Lengths and causal as in the forward; gradients of
