@@ -53,6 +53,11 @@ class AttnShape(ctypes.Structure):
                 ("k_lens", ctypes.c_void_p)] + [(f"{t}_stride_{x}", ctypes.c_longlong) for t in "qkvo" for x in "bhn"] + [("o_rest", ctypes.c_void_p)]
 
 
+class XentShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("vocab", ctypes.c_longlong), ("channels", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("hidden_stride", ctypes.c_longlong), ("weight_stride", ctypes.c_longlong)]
+
+
 class StreamKLError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -89,6 +94,11 @@ SIGNATURES = {
     "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
     "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
+    "streamkl_vocab_xent_fwd_workspace": (_I, [XentShape, ctypes.POINTER(_SZ)]),
+    "streamkl_vocab_xent_fwd": (_I, [_P, _P, _P, XentShape, _F, _F, _P, _SZ, _S]),
+    "streamkl_vocab_xent_bwd_plan": (_I, [XentShape, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
+    "streamkl_vocab_xent_bwd_workspace": (_I, [XentShape, _I, ctypes.POINTER(_SZ)]),
+    "streamkl_vocab_xent_bwd": (_I, [_P, _P, _P, _F, _F, _F, XentShape, _P, _P, _P, _SZ, _S]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_check_device_status": (_I, [_S]),
     "streamkl_debug_wait_timeout": (_I, [_I, _S]),
@@ -686,6 +696,103 @@ def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0
           tok.data_ptr() if T else None, T, scale, lse.data_ptr(), None if ent is None else ent.data_ptr(),
           g_logp.data_ptr() if T else None, None if ent is None else g_entropy.data_ptr(), out.data_ptr(), V)
     return _back((out,), True)[0] if host else out
+
+
+def make_xent_shape(rows, vocab, channels, dtype=0, scale=1.0, hidden_stride=None, weight_stride=None) -> XentShape:
+    """The C shape of a vocabulary's cross entropy; dtype is a streamkl_dtype, strides default to contiguous rows."""
+    return XentShape(rows, vocab, channels, dtype, scale, channels if hidden_stride is None else hidden_stride,
+                     channels if weight_stride is None else weight_stride)
+
+
+def _matrix(t):
+    """A 2-D matrix that the library reads in place (a contiguous copy where it cannot) and its row stride."""
+    if t.stride(1) != 1 or t.data_ptr() & 15 or (t.shape[0] > 1 and (t.stride(0) % 8 or t.stride(0) < t.shape[1])):
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _xent_inputs(hidden, weight, tokens, scale):
+    """Validates hidden [..., C], weight [V, C] and tokens [...]; returns (hidden as [R, C], weight, contiguous int64
+    tokens, the C shape, the leading shape, device, was_host)."""
+    if hidden.dtype is not torch.bfloat16 and hidden.dtype is not torch.float16:
+        raise TypeError("hidden must be bfloat16 or float16")
+    if weight.dtype is not hidden.dtype:
+        raise TypeError("hidden and weight must have the same type")
+    if hidden.dim() < 1 or weight.dim() != 2 or hidden.shape[-1] != weight.shape[1]:
+        raise ValueError(f"shape mismatch: hidden {tuple(hidden.shape)} weight {tuple(weight.shape)}")
+    V, C = weight.shape
+    if V == 0 or C == 0 or C % 8:
+        raise ValueError("weight must be [V, C] with V > 0 and C a positive multiple of 8")
+    lead, dev = hidden.shape[:-1], hidden.device
+    if tokens.dtype is not torch.int64 and tokens.dtype is not torch.int32:
+        raise TypeError("tokens must be int64 or int32")
+    if tokens.shape != lead:
+        raise ValueError(f"tokens {tuple(tokens.shape)} do not fit hidden {tuple(hidden.shape)}")
+    if weight.device != dev or tokens.device != dev:
+        raise ValueError("inputs on different devices")
+    host = dev.type == "cpu"
+    if host:
+        dev = torch.device("cuda", torch.cuda.current_device())
+        hidden, weight = hidden.to(dev, non_blocking=True), weight.to(dev, non_blocking=True)
+    if host or tokens.dtype is not torch.int64:
+        tokens = tokens.to(device=dev, dtype=torch.int64, non_blocking=True)
+    (x, xs), (w, ws) = _matrix(hidden if hidden.dim() == 2 else hidden.reshape(-1, C)), _matrix(weight)
+    s = make_xent_shape(x.shape[0], V, C, DTYPES[x.dtype], scale, xs, ws)
+    return x, w, tokens if tokens.is_contiguous() else tokens.contiguous(), s, lead, dev, host
+
+
+def vocab_xent_plan(rows, vocab, channels, num_sms, want_dhidden=True):
+    """(pieces of the vocabulary, splits of dhidden's sums, workspace bytes) of the backward on a device with num_sms SMs."""
+    a, b, n = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
+    _check(lib().streamkl_vocab_xent_bwd_plan(make_xent_shape(rows, vocab, channels), int(num_sms), bool(want_dhidden),
+                                              *map(ctypes.byref, (a, b, n))), "streamkl_vocab_xent_bwd_plan")
+    return a.value, b.value, n.value
+
+
+def _xent_workspace(name, dev, *args):
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(dev):
+        _check(getattr(lib(), name)(*args, ctypes.byref(n)), name)
+    return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+
+
+def vocab_xent_fwd(hidden, weight, tokens, scale=1.0):
+    """Cross entropy of the rows softmax(scale hidden weight^T) at given tokens, without the logits in memory:
+    (loss, lse), fp32 like tokens.
+
+    hidden: [..., C], weight: [V, C], both bf16 or both fp16, C a multiple of 8; tokens: [...], int64 or int32, a negative
+    one is no token (its loss is 0), one past the vocabulary gives NaN.
+    """
+    x, w, tok, s, lead, dev, host = _xent_inputs(hidden, weight, tokens, scale)
+    ws, nbytes = _xent_workspace("streamkl_vocab_xent_fwd_workspace", dev, s)
+    loss, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(2))
+    _call("streamkl_vocab_xent_fwd", dev.index, x.data_ptr(), w.data_ptr(), tok.data_ptr(), s, loss.data_ptr(),
+          lse.data_ptr(), ws.data_ptr(), nbytes)
+    return _back((loss, lse), True) if host else (loss, lse)
+
+
+def vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse=None, scale=1.0, want_dhidden=True, want_dweight=True):
+    """Gradients (dhidden, dweight) of vocab_xent_fwd's outputs, contiguous and of the inputs' type, for upstream
+    gradients g_loss and g_lse (fp32 like tokens; g_lse may be None); lse is the forward's.  One that is not wanted is None.
+
+    The same bits on every run.  Hidden states of rows without a gradient have to be finite all the same.
+    """
+    x, w, tok, s, lead, dev, host = _xent_inputs(hidden, weight, tokens, scale)
+    lse, g_loss, g_lse = _rows(lse, dev, lead, "lse"), _rows(g_loss, dev, lead, "g_loss"), _rows(g_lse, dev, lead, "g_lse")
+    if lse is None or g_loss is None:
+        raise ValueError("lse and g_loss are needed")
+    if not want_dhidden and not want_dweight:
+        return None, None
+    ws, nbytes = _xent_workspace("streamkl_vocab_xent_bwd_workspace", dev, s, bool(want_dhidden))
+    dh = torch.empty(hidden.shape, dtype=x.dtype, device=dev) if want_dhidden else None
+    dw = torch.empty(weight.shape, dtype=x.dtype, device=dev) if want_dweight else None
+    _call("streamkl_vocab_xent_bwd", dev.index, x.data_ptr(), w.data_ptr(), tok.data_ptr(), lse.data_ptr(), g_loss.data_ptr(),
+          None if g_lse is None else g_lse.data_ptr(), s, None if dh is None else dh.data_ptr(),
+          None if dw is None else dw.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
+    if not host:
+        return dh, dw
+    got = iter(_back(tuple(t for t in (dh, dw) if t is not None), True))
+    return tuple(None if t is None else next(got) for t in (dh, dw))
 
 
 def check_device_status(device=None) -> int:

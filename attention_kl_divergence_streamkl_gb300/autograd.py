@@ -126,3 +126,36 @@ def token_logprobs(logits, tokens=None, scale=1.0, top_k=0):
     them as tokens to train on them).  See logprobs_fwd for shapes, types and masked values.
     """
     return _TokenLogprobs.apply(logits, tokens, scale, top_k)
+
+
+class _VocabCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, weight, tokens, scale):
+        loss, lse = _lib.vocab_xent_fwd(hidden, weight, tokens, scale)
+        ctx.save_for_backward(hidden, weight, tokens, lse)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g_loss, g_lse):
+        hidden, weight, tokens, lse = ctx.saved_tensors
+        if g_loss is None and g_lse is None:
+            return None, None, None, None
+        if g_loss is None:
+            g_loss = torch.zeros_like(lse)
+        return (*_lib.vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse, ctx.scale, ctx.needs_input_grad[0],
+                                     ctx.needs_input_grad[1]), None, None)
+
+
+def vocab_cross_entropy(hidden, weight, tokens, scale=1.0, return_lse=False):
+    """-log softmax(scale hidden weight^T)[token] of each row, differentiable in hidden and weight: fp32 like tokens, and
+    with return_lse the rows' log-sum-exp, differentiable too (for a penalty on it).
+
+    The loss on the data's tokens beside attention_kl, where the logits themselves are not wanted: they are never in memory
+    (token_logprobs takes logits that are).  hidden [..., C] and weight [V, C] are bf16 or fp16; a negative token is none:
+    its loss is 0.  See vocab_xent_fwd and vocab_xent_bwd.
+    """
+    loss, lse = _VocabCrossEntropy.apply(hidden, weight, tokens, scale)
+    return (loss, lse) if return_lse else loss

@@ -271,6 +271,19 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_matrix_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, int box_rows,
+                       int box_cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_wait_timeout_probe(int timeout_us, int* status, cudaStream_t st) {
   wait_timeout_probe_kernel<<<1, 32, 0, st>>>((unsigned long long)timeout_us * 1000ull, status);
   return cudaGetLastError();
@@ -788,6 +801,85 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
   if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
   return from_cuda(launch_logprobs_bwd(p, logits, tokens, lse, entropy, g_logp, g_entropy, dlogits, out_stride, sms,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+static streamkl_status xent_problem(const streamkl_xent_shape& s, XentProblem* p) {
+  if (s.rows < 0 || s.vocab <= 0 || s.channels <= 0 || s.hidden_stride < s.channels || s.weight_stride < s.channels)
+    return STREAMKL_ERR_INVALID;
+  if (!(s.scale > 0.f) || isinf(s.scale)) return STREAMKL_ERR_INVALID;
+  if (s.dtype != STREAMKL_BF16 && s.dtype != STREAMKL_FP16)
+    return s.dtype == STREAMKL_FP32 ? STREAMKL_ERR_UNSUPPORTED : STREAMKL_ERR_INVALID;
+  // rows of 16-byte granules for TMA; rows, columns and their tiles in 32 bits
+  if (s.channels % 8 || s.hidden_stride % 8 || s.weight_stride % 8) return STREAMKL_ERR_UNSUPPORTED;
+  if (s.rows > kMaxRows || s.vocab > kMaxRows || s.channels > (1 << 20) || s.hidden_stride >= (1ll << 38) ||
+      s.weight_stride >= (1ll << 38) || s.rows * s.channels > (1ll << 40))
+    return STREAMKL_ERR_UNSUPPORTED;
+  *p = XentProblem{s.rows, s.vocab, s.channels, s.dtype == STREAMKL_FP16, s.hidden_stride, s.weight_stride, s.scale};
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_vocab_xent_fwd_workspace(streamkl_xent_shape s, size_t* bytes) {
+  XentProblem p;
+  const streamkl_status v = xent_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!bytes) return STREAMKL_ERR_INVALID;
+  *bytes = p.R ? xent_fwd_workspace(p) : 0;
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, const long long* tokens, streamkl_xent_shape s,
+                                        float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  XentProblem p;
+  streamkl_status v = xent_problem(s, &p);
+  if (v != STREAMKL_OK || p.R == 0) return v;
+  if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(tokens, 8) || !rows_ok(loss) || !rows_ok(lse))
+    return STREAMKL_ERR_INVALID;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < xent_fwd_workspace(p)) return STREAMKL_ERR_WORKSPACE;
+  int sms = 0, *status = nullptr;
+  if ((v = device_sms(&sms)) != STREAMKL_OK || (v = status_ptr(&status)) != STREAMKL_OK) return v;
+  return from_cuda(
+      launch_xent_fwd(p, hidden, weight, tokens, loss, lse, workspace, sms, status, static_cast<cudaStream_t>(stream)));
+}
+
+streamkl_status streamkl_vocab_xent_bwd_plan(streamkl_xent_shape s, int num_sms, int want_dhidden, int* pieces, int* splits,
+                                             size_t* bytes) {
+  XentProblem p;
+  streamkl_status v = xent_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!pieces || !splits || !bytes) return STREAMKL_ERR_INVALID;
+  if (num_sms <= 0 && (v = device_sms(&num_sms)) != STREAMKL_OK) return v;
+  const XentBwdPlan g = xent_bwd_plan(p, want_dhidden != 0, num_sms);
+  *pieces = g.pieces;
+  *splits = g.splits;
+  *bytes = p.R ? g.bytes : 0;
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_vocab_xent_bwd_workspace(streamkl_xent_shape s, int want_dhidden, size_t* bytes) {
+  int pieces, splits;
+  return streamkl_vocab_xent_bwd_plan(s, 0, want_dhidden, &pieces, &splits, bytes);
+}
+
+streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, const long long* tokens, const float* lse,
+                                        const float* g_loss, const float* g_lse, streamkl_xent_shape s, void* dhidden,
+                                        void* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  XentProblem p;
+  streamkl_status v = xent_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if ((!dhidden && !dweight) || !aligned_to_or_null(dhidden, 16) || !aligned_to_or_null(dweight, 16)) return STREAMKL_ERR_INVALID;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.R == 0)  // an empty sum
+    return dweight ? from_cuda(cudaMemsetAsync(dweight, 0, (size_t)p.V * p.C * 2, st)) : STREAMKL_OK;
+  if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(tokens, 8) || !rows_ok(lse) || !rows_ok(g_loss) ||
+      !aligned_to_or_null(g_lse, 4))
+    return STREAMKL_ERR_INVALID;
+  int sms = 0, *status = nullptr;
+  if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
+  const XentBwdPlan g = xent_bwd_plan(p, dhidden != nullptr, sms);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < g.bytes) return STREAMKL_ERR_WORKSPACE;
+  if ((v = status_ptr(&status)) != STREAMKL_OK) return v;
+  return from_cuda(launch_xent_bwd(p, g, XentBwdIn{hidden, weight, tokens, lse, g_loss, g_lse}, dhidden, dweight, workspace,
+                                   sms, status, st));
 }
 
 streamkl_status streamkl_check_device_status(void* stream) {

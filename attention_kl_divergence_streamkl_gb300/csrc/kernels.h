@@ -33,6 +33,10 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, in
 // (for bulk reductions into it).
 // With box_cols 32 the box is {32, box_rows, 1} with the swizzle of its 128-byte rows.
 bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows, int box_cols = 0);
+// A 2-D TMA map {col, row} over a matrix of 2-byte values whose rows lie `stride` elements apart, a {box_cols, box_rows} box
+// with the swizzle of its 128-byte rows.
+bool encode_matrix_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, int box_rows,
+                       int box_cols);
 // The maps of Q1/Q2 and K1/K2 of a problem.
 inline bool encode_q_map(CUtensorMap* map, const void* base, const Problem& p, int box_rows) {
   return encode_tile_map(map, base, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, box_rows);
@@ -178,6 +182,33 @@ cudaError_t launch_logprobs_fwd(const LogprobsProblem& p, const void* logits, co
 cudaError_t launch_logprobs_bwd(const LogprobsProblem& p, const void* logits, const long long* tokens,
                                 const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
                                 void* dlogits, long long out_stride, int num_sms, cudaStream_t st);
+
+// ---- cross entropy over a vocabulary, from hidden states -----------------------------
+struct XentProblem {
+  long long R, V;  // rows of hidden states, the vocabulary
+  int C;           // channels
+  int half;        // fp16, else bf16
+  long long hidden_stride, weight_stride;
+  float scale;
+};
+size_t xent_fwd_workspace(const XentProblem& p);
+cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void* weight, const long long* tokens, float* loss,
+                            float* lse, void* workspace, int num_sms, int* status, cudaStream_t st);
+struct XentBwdPlan {
+  int pieces, splits;   // of the vocabulary; of dh's sums over a piece
+  long long columns;    // of a piece
+  bool direct;          // dh needs no sums between launches
+  size_t off_d, off_acc, bytes;
+};
+XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms);
+struct XentBwdIn {
+  const void *hidden, *weight;
+  const long long* tokens;
+  const float *lse, *g, *g_lse;  // g_lse may be null
+};
+// dhidden, dweight: null where it is not wanted
+cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& plan, const XentBwdIn& in, void* dhidden, void* dweight,
+                            void* workspace, int num_sms, int* status, cudaStream_t st);
 
 // ---- test hook ------------------------------------------------------------------
 cudaError_t launch_wait_timeout_probe(int timeout_us, int* status, cudaStream_t st);

@@ -1,0 +1,704 @@
+// Cross entropy over a vocabulary from hidden states, and its gradients, without the logits in memory:
+//     z = scale h W^T,  loss_r = LSE_r - z_r,t,  LSE_r = log sum_v e^z_rv
+//     d_rv = scale (g_r (p_rv - [v = t_r]) + g'_r p_rv),  p = e^(z - LSE),  dh = d W,  dW = d^T h
+// for upstream gradients g of the losses and g' of the log-sum-exps.
+//
+// All three are matrix products of 2 R C V operations with something done to their tiles, so one product loop serves
+// them: pairs of SMs (cta_group::2) work on 256 x 256 tiles, 64 of the summed index at a time.  Each block of a pair
+// loads 128 rows of either operand, so a byte from L2 feeds twice the products that it would in a 128 x 256 tile of one
+// SM; the accumulators, 256 of the 512 TMEM columns each, take turns, so that the tile's epilogue runs under the next
+// tile's products.
+//   warps 0-7  epilogue: warp w has the rows 32 (w % 4) and the column half w / 4; thread = row
+//   warp 8     TMA producer of the block's own halves
+//   warp 9     TMEM owner; in the even block the MMA issuer (one thread)
+// Forward: a tile leaves each row's maximum and sum of 2^(z - max) over 128 columns, and the given token's logit where
+// it has it; a second kernel joins them in a fixed order.
+// Backward: the vocabulary goes by in pieces.  A piece's d (2 bytes, rows x columns) is written once by the first
+// launch; the second reads it for both gradients: a piece's rows of dW are complete, the sum for dh goes on from piece
+// to piece in fp32.  d is rounded to the inputs' type, as the other operand of the products that it enters is: half a
+// step of each term.  In fp16 it is multiplied by a power of two that brings the largest upstream gradient to 2^14, for
+// p's small values would be lost below 2^-24 otherwise.
+#include "attn.cuh"
+#include "pair.cuh"
+
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+namespace skl {
+namespace {
+
+constexpr int BM = 128, BK = 64;         // rows of either operand in a block, and of the summed index, a stage
+constexpr int TILE = 256;                // a pair's tile: TILE x TILE
+constexpr int EPILOGUE_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9;
+constexpr int THREADS = 10 * 32;
+constexpr int STAGES = 6;
+constexpr int HALF_STAGE = BM * BK * 2;  // one operand
+constexpr uint32_t kTmemCols = 512;
+constexpr int OFF_STAGE = 0, OFF_OUT = STAGES * 2 * HALF_STAGE;  // the epilogue warps' 4 KB each
+constexpr int OFF_BAR = OFF_OUT + EPILOGUE_WARPS * 4096;
+constexpr int BAR_SLOT = 8 * (2 * STAGES + 4);  // full, empty; tile there [2], tile free [2]; TMEM slot, abort flag
+static_assert(OFF_BAR + BAR_SLOT + 16 + 1024 <= kWholeSmSmem, "shared memory");
+
+enum Kind { kForward, kGradLogits, kGradients };
+
+// One matrix product: m_tiles x n_tiles tiles, each over `splits` ranges of the k_chunks 64-wide chunks.
+struct Job {
+  int m_tiles, n_tiles, splits, k_chunks;
+  int m_group;       // forward and d: that many tiles along m share what they read of the other operand
+  int a_mn, b_mn;    // the operand lies with its rows (m or n), not the summed index, along the 128-byte lines
+  int rows, cols;    // of the output
+  __host__ __device__ long long tiles() const { return (long long)m_tiles * n_tiles * splits; }
+};
+struct Tile {
+  int job, m, n, split, k0, k1;
+};
+
+struct XentParams {
+  Job job[2];  // kGradients: dh, dW; else only the first
+  // kGradients: pairs below `more` take one tile of the first job more, and `few` of the second; the others share the rest
+  int more, few;
+  long long R;
+  int V, v0;          // the vocabulary, and the first column of the piece
+  float scale, c;     // c = scale log2(e)
+  const long long* tokens;
+  // forward
+  float2* part;       // [2 tiles along V][part_rows]: maximum (log2 units), sum
+  float* given;       // [R] the token's logit, log2 units
+  long long part_rows;
+  // d
+  const float *lse, *g, *g_lse;
+  // fp16: the power of two on d and its inverse, else null
+  const float* power;
+  int accumulate;     // dh goes to the fp32 sums: 0 stored straight to the output, 1 written, 2 added
+};
+
+struct Maps {
+  CUtensorMap a[2], b[2], out[2], acc;
+};
+
+// The tiles of a pair, in its order.  One job: every pairs-th, the tiles along m first, in groups of m_group.
+// Two: the pair's share of the first job's tiles, then a run of the second's.
+__device__ __forceinline__ Tile job_tile(const Job& j, int job, long long i) {
+  Tile t;
+  t.job = job;
+  const long long per = (long long)j.m_tiles * j.n_tiles;
+  t.split = j.splits == 1 ? 0 : (int)(i / per);
+  long long x = i - t.split * per;
+  if (job == 0 && j.m_group) {
+    const long long group = x / ((long long)j.m_group * j.n_tiles);
+    x -= group * j.m_group * j.n_tiles;
+    const int here = min(j.m_group, j.m_tiles - (int)group * j.m_group);
+    t.n = (int)(x / here);
+    t.m = (int)group * j.m_group + (int)(x - (long long)t.n * here);
+  } else {
+    t.m = (int)(x / j.n_tiles);
+    t.n = (int)(x - (long long)t.m * j.n_tiles);
+  }
+  t.k0 = (int)((long long)j.k_chunks * t.split / j.splits);
+  t.k1 = (int)((long long)j.k_chunks * (t.split + 1) / j.splits);
+  return t;
+}
+struct Walk {
+  long long first, n_first, from, n_all;
+  int pairs;
+  template <Kind KIND>
+  __device__ __forceinline__ static Walk make(const XentParams& p, int pair, int pairs) {
+    Walk w;
+    const long long a = p.job[0].tiles();
+    w.first = pair;
+    w.pairs = pairs;
+    w.n_first = pair < a ? (a - pair + pairs - 1) / pairs : 0;
+    w.from = 0;
+    w.n_all = w.n_first;
+    if (KIND == kGradients) {
+      const long long b = p.job[1].tiles(), few = (long long)p.few * p.more, rest = b - few, others = pairs - p.more;
+      long long to;
+      if (pair < p.more) {
+        w.from = (long long)p.few * pair;
+        to = w.from + p.few;
+      } else {
+        w.from = few + rest * (pair - p.more) / others;
+        to = few + rest * (pair - p.more + 1) / others;
+      }
+      w.n_all += to - w.from;
+    }
+    return w;
+  }
+  __device__ __forceinline__ Tile tile(const XentParams& p, long long i) const {
+    if (i < n_first) return job_tile(p.job[0], 0, first + i * pairs);
+    return job_tile(p.job[1], 1, from + i - n_first);
+  }
+};
+
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (HALF) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return pack_bf16(lo, hi);
+}
+
+// instruction descriptor of a 256 x 256 tile of a pair
+template <bool HALF>
+__device__ __forceinline__ uint32_t pair_idesc(bool a_mn, bool b_mn) {
+  const uint32_t type = HALF ? 0u : 1u;
+  return (1u << 4) | (type << 7) | (type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+}
+
+template <Kind KIND, bool HALF>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    xent_kernel(const XentParams p, int* status, const __grid_constant__ Maps maps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const Walk walk = Walk::make<KIND>(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
+
+  const uint32_t bar = sb + OFF_BAR;
+  const uint32_t full = bar, empty = full + 8 * STAGES, there = empty + 8 * STAGES, free_ = there + 16;
+  const uint32_t slot = bar + BAR_SLOT;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_BAR + BAR_SLOT + 4);
+
+  if (warp == PRODUCER_WARP) {
+    if (elect_one()) {
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(full + 8 * s, 1);   // the even block's: the bytes of both
+        mbar_init(empty + 8 * s, 1);  // both blocks', by one commit
+      }
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(there + 8 * t, 1);
+        mbar_init(free_ + 8 * t, 2 * EPILOGUE_WARPS);  // the even block's: the epilogue warps of both
+      }
+      *abort_flag = 0;
+      fence_mbar_init();
+      fence_async_smem();
+    }
+    __syncwarp();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc_pair(slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both blocks' barriers and TMEM are set up
+  tc_fence_after();
+  whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + BAR_SLOT), status);
+  constexpr uint32_t tmem = 0;
+
+  if (warp == PRODUCER_WARP) {
+    if (elect_one()) {
+      const uint32_t full_even = in_block(full, 0);
+      int s = 0;          // the stage that is filled next
+      uint32_t lap = 0;   // how often the ring has been round
+      bool ok = true;
+      for (long long i = 0; ok && i < walk.n_all; ++i) {
+        const Tile t = walk.tile(p, i);
+        const Job& j = p.job[t.job];
+        const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
+        const int m0 = t.m * TILE + (int)rank * BM, n0 = t.n * TILE + (int)rank * BM;
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (lap && !(ok = mbar_wait(empty + 8 * s, (lap - 1) & 1, status, abort_flag))) break;
+          const uint32_t a = sb + OFF_STAGE + s * 2 * HALF_STAGE, b = a + HALF_STAGE, done = full_even + 8 * s;
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 4 * HALF_STAGE);
+          if (j.a_mn) {
+            tma_load_2d_pair(a, ma, done, m0, k * BK);
+            tma_load_2d_pair(a + HALF_STAGE / 2, ma, done, m0 + 64, k * BK);
+          } else {
+            tma_load_2d_pair(a, ma, done, k * BK, m0);
+          }
+          if (j.b_mn) {
+            tma_load_2d_pair(b, mb, done, n0, k * BK);
+            tma_load_2d_pair(b + HALF_STAGE / 2, mb, done, n0 + 64, k * BK);
+          } else {
+            tma_load_2d_pair(b, mb, done, k * BK, n0);
+          }
+          if (++s == STAGES) {
+            s = 0;
+            ++lap;
+          }
+        }
+      }
+      // the stages in flight have landed once the products that read them are done; after a wait that ran out, the even
+      // block waits for the bytes of both
+      for (int v = 0; v < STAGES; ++v) {
+        if (v >= s && !lap) break;  // never filled
+        const uint32_t parity = (v < s ? lap : lap - 1) & 1;
+        if (ok)
+          mbar_drain(empty + 8 * v, parity, status);
+        else if (rank == 0)
+          mbar_drain(full + 8 * v, parity, status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == MMA_WARP) {
+    if (rank == 0 && elect_one()) {
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (long long i = 0; ok && i < walk.n_all; ++i) {
+        const Tile t = walk.tile(p, i);
+        const Job& j = p.job[t.job];
+        const uint32_t buf = (uint32_t)i & 1;
+        if (i >= 2 && !(ok = mbar_wait(free_ + 8 * buf, (uint32_t)(i / 2 - 1) & 1, status, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t idesc = pair_idesc<HALF>(j.a_mn, j.b_mn);
+        const uint32_t a_step = j.a_mn ? 2048 : 32, b_step = j.b_mn ? 2048 : 32;
+        const uint32_t a_lbo = j.a_mn ? HALF_STAGE / 2 : 0, b_lbo = j.b_mn ? HALF_STAGE / 2 : 0;
+        for (int k = t.k0; k < t.k1; ++k) {
+          if (!(ok = mbar_wait(full + 8 * s, phase, status, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t at = sb + OFF_STAGE + s * 2 * HALF_STAGE;
+          const uint64_t ad = sdesc_sw128(at, a_lbo, 1024), bd = sdesc_sw128(at + HALF_STAGE, b_lbo, 1024);
+#pragma unroll
+          for (int ks = 0; ks < BK / 16; ++ks)
+            mma_pair(tmem + TILE * buf, sdesc_add(ad, ks * a_step), sdesc_add(bd, ks * b_step), idesc, k > t.k0 || ks > 0);
+          mma_commit_pair(empty + 8 * s);
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) mma_commit_pair(there + 8 * buf);
+      }
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t stage = sb + OFF_OUT + warp * 4096;
+    const uint32_t free_even = in_block(free_, 0);
+    const float power = HALF && KIND != kForward ? p.power[KIND == kGradients] : 1.f;
+    for (long long i = 0; i < walk.n_all; ++i) {
+      const Tile t = walk.tile(p, i);
+      const uint32_t buf = (uint32_t)i & 1;
+      const int row0 = t.m * TILE + (int)rank * BM + quarter * 32;  // the warp's first row
+      const int col0 = t.n * TILE + half * 128;                     // and column
+      const int row = row0 + lane;
+      const uint32_t ta = tmem + lanes + TILE * buf + 128 * half;
+      if constexpr (KIND == kForward) {
+        const bool real = row < p.R;
+        const long long token = real ? p.tokens[row] : -1;
+        if (!mbar_wait_warp(there + 8 * buf, (uint32_t)(i / 2) & 1, status, abort_flag)) break;
+        tc_fence_after();
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(ta, s0);
+        tmem_ld32(ta + 32, s1);
+        tmem_ld32(ta + 64, s2);
+        tmem_ld32(ta + 96, s3);
+        tmem_ld_wait();
+        reg_fence32(s0);
+        reg_fence32(s1);
+        reg_fence32(s2);
+        reg_fence32(s3);
+        tc_fence_before();
+        arrive_one_in(free_even + 8 * buf);
+        const int seen = p.V - col0;
+        const long long at = token - col0;
+        if (__any_sync(0xffffffffu, at >= 0 && at < min(128, seen))) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t z = at == k ? s0[k] : at == k + 32 ? s1[k] : at == k + 64 ? s2[k] : s3[k];
+            if (at >= 0 && at < seen && (at & 31) == k && at < 128) p.given[row] = __uint_as_float(z) * p.c;
+          }
+        }
+        if (seen < 128) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (k >= seen) s0[k] = __float_as_uint(kNegInf);
+            if (k + 32 >= seen) s1[k] = __float_as_uint(kNegInf);
+            if (k + 64 >= seen) s2[k] = __float_as_uint(kNegInf);
+            if (k + 96 >= seen) s3[k] = __float_as_uint(kNegInf);
+          }
+        }
+        float mx = kNegInf;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          mx = fmax3(mx, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
+          mx = fmax3(mx, __uint_as_float(s2[k]), __uint_as_float(s3[k]));
+        }
+        const float m = mx * p.c;
+        const float2 cc = make_float2(p.c, p.c), nm = mx == kNegInf ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t* s = h == 0 ? s0 : h == 1 ? s1 : h == 2 ? s2 : s3;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float2 x0 = ffma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
+            const float2 x1 = ffma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc, nm);
+            l0 = fadd2(l0, make_float2(ex2(x0.x), ex2(x0.y)));
+            l1 = fadd2(l1, make_float2(ex2(x1.x), ex2(x1.y)));
+          }
+        }
+        l0 = fadd2(l0, l1);
+        if (real) p.part[(size_t)(2 * t.n + half) * p.part_rows + row] = make_float2(m, l0.x + l0.y);
+      } else if constexpr (KIND == kGradLogits) {
+        const bool real = row < p.R;
+        long long at = -1;
+        float lse2 = 0.f, a = 0.f, g = 0.f;
+        if (real) {
+          const long long token = p.tokens[row];
+          lse2 = p.lse[row] * kLog2e;
+          if (token >= 0 && token < p.V) {
+            g = p.g[row] * p.scale * power;
+            at = token - p.v0 - col0;
+          }
+          a = g + (p.g_lse ? p.g_lse[row] * p.scale * power : 0.f);
+        }
+        const int seen = real ? p.job[0].cols - col0 : 0;  // d is 0 past the piece; what is past the rows is not stored
+        bool ok = mbar_wait_warp(there + 8 * buf, (uint32_t)(i / 2) & 1, status, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t s0[32], s1[32], w[32];
+          tmem_ld32(ta + 64 * q, s0);
+          tmem_ld32(ta + 64 * q + 32, s1);
+          tmem_ld_wait();
+          reg_fence32(s0);
+          reg_fence32(s1);
+          if (q == 1) {
+            tc_fence_before();
+            arrive_one_in(free_even + 8 * buf);
+          }
+          const long long here = at - 64 * q;
+          const bool given = __any_sync(0xffffffffu, here >= 0 && here < 64);
+          const bool edge = __any_sync(0xffffffffu, seen < 64 * (q + 1));
+          const float2 cc = make_float2(p.c, p.c), nl = make_float2(-lse2, -lse2), aa = make_float2(a, a);
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            const uint32_t* s = k < 32 ? s0 : s1;
+            const float2 x = ffma2(make_float2(__uint_as_float(s[k & 31]), __uint_as_float(s[(k & 31) + 1])), cc, nl);
+            float2 d = fmul2(make_float2(ex2(x.x), ex2(x.y)), aa);
+            if (a == 0.f) d = make_float2(0.f, 0.f);  // no gradient is none, whatever the logits are
+            if (given) {
+              if (here == k) d.x -= g;
+              if (here == k + 1) d.y -= g;
+            }
+            if (edge) {
+              if (64 * q + k >= seen) d.x = 0.f;
+              if (64 * q + k + 1 >= seen) d.y = 0.f;
+            }
+            w[k / 2] = pack16<HALF>(d.x, d.y);
+          }
+          if (elect_one()) bulk_wait_read();  // the warp's last store has read its 4 KB
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            st_shared16(stage + lane * 128 + ((k ^ (lane & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+          fence_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+            if (row0 < p.R && col0 + 64 * q < p.job[0].cols) tma_store_2d(&maps.out[0], stage, col0 + 64 * q, row0);
+            bulk_commit();
+          }
+          __syncwarp();
+        }
+      } else {
+        const Job& j = p.job[t.job];
+        const bool sums = t.job == 0 && p.accumulate;
+        if (!mbar_wait_warp(there + 8 * buf, (uint32_t)(i / 2) & 1, status, abort_flag)) break;
+        tc_fence_after();
+        const bool rows_there = row0 < j.rows;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          tmem_ld32(ta + 32 * q, s);
+          tmem_ld_wait();
+          reg_fence32(s);
+          if (q == 3) {
+            tc_fence_before();
+            arrive_one_in(free_even + 8 * buf);
+          }
+          const int col = col0 + 32 * q;
+          if (sums || (q & 1) == 0) {
+            if (elect_one()) bulk_wait_read();
+            __syncwarp();
+          }
+          if (sums) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              st_shared16(stage + lane * 128 + ((k ^ (lane & 7)) << 4), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack16<HALF>(__uint_as_float(s[8 * k + 2 * e]) * power, __uint_as_float(s[8 * k + 2 * e + 1]) * power);
+              st_shared16(stage + lane * 128 + (((4 * (q & 1) + k) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          }
+          if (sums || (q & 1)) {
+            fence_async_smem();
+            __syncwarp();
+            if (elect_one()) {
+              if (sums) {
+                if (rows_there && col < j.cols) {
+                  if (p.accumulate == 1)
+                    tma_store_3d(&maps.acc, stage, col, row0, t.split);
+                  else
+                    tma_add_3d(&maps.acc, stage, col, row0, t.split);
+                }
+              } else if (rows_there && col - 32 < j.cols) {
+                tma_store_2d(&maps.out[t.job], stage, col - 32, row0 + (t.job ? p.v0 : 0));
+              }
+              bulk_commit();
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (KIND != kForward) {
+      if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nothing of this block is read or arrived on any more
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// Joins the tiles' maxima and sums: a warp's lanes are rows, the warps share the tiles.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    xent_join_kernel(long long R, int V, int parts, long long part_rows, const float2* __restrict__ part,
+                     const float* __restrict__ given, const long long* __restrict__ tokens, float* __restrict__ loss,
+                     float* __restrict__ lse) {
+  __shared__ float2 sums[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long row = (long long)blockIdx.x * 32 + lane;
+  const bool real = row < R;
+  float m = kNegInf, l = 0.f;
+  auto join = [&](float2 x) {
+    if (x.x == kNegInf && x.y == 0.f) return;  // nothing but -inf there
+    const float to = fmaxf(m, x.x);
+    l = (m == kNegInf && l == 0.f ? 0.f : l * ex2(m - to)) + (x.x == to ? x.y : x.y * ex2(x.x - to));
+    m = to;
+  };
+  if (real)
+    for (int i = warp; i < parts; i += kJoinWarps) join(part[(size_t)i * part_rows + row]);
+  sums[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  if (warp || !real) return;
+#pragma unroll 1
+  for (int w = 1; w < kJoinWarps; ++w) join(sums[w][lane]);
+  const bool none = m == kNegInf && l == 0.f;
+  const float log_sum = logf(l);
+  lse[row] = none ? kNegInf : fmaf(m, kLn2, log_sum);
+  const long long token = tokens[row];
+  // the differences first: a loss keeps its digits however far from 0 the logits lie
+  loss[row] = token < 0 ? 0.f : token >= V ? __int_as_float(0x7fc00000) : fmaf(m - given[row], kLn2, log_sum);
+}
+
+// fp16: the power of two that brings the largest |scale g| to [2^13, 2^14), and its inverse.
+__global__ void __launch_bounds__(1024) xent_power_kernel(long long R, float scale, const float* __restrict__ g,
+                                                          const float* __restrict__ g_lse, float* __restrict__ power) {
+  __shared__ float warp_max[32];
+  float mx = 0.f;
+  for (long long i = threadIdx.x; i < R; i += 1024) mx = fmaxf(mx, scale * (fabsf(g[i]) + (g_lse ? fabsf(g_lse[i]) : 0.f)));
+#pragma unroll
+  for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = mx;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < 32; ++w) mx = fmaxf(mx, warp_max[w]);
+  int e = 0;
+  if (mx > 0.f && mx < __int_as_float(0x7f800000)) {
+    frexpf(mx, &e);  // mx = f 2^e, f in [1/2, 1)
+    e = min(max(14 - e, -100), 100);
+  }
+  power[0] = ldexpf(1.f, e);
+  power[1] = ldexpf(1.f, -e);
+}
+
+// dh from the splits' fp32 sums, added in their order.
+template <bool HALF>
+__global__ void __launch_bounds__(256)
+    xent_close_kernel(long long n, int splits, const float4* __restrict__ acc, const float* __restrict__ power,
+                      uint2* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four values
+  if (i >= n) return;
+  float4 s = __ldcg(acc + i);
+  for (int k = 1; k < splits; ++k) {
+    const float4 v = __ldcg(acc + k * n + i);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const float f = HALF ? power[1] : 1.f;
+  out[i] = make_uint2(pack16<HALF>(s.x * f, s.y * f), pack16<HALF>(s.z * f, s.w * f));
+}
+
+int tiles_of(long long n, int of) { return (int)((n + of - 1) / of); }
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+// Pairs of the device's SMs, no more than there are tiles.
+int pairs_for(long long tiles, int num_sms) { return (int)std::max<long long>(1, std::min<long long>(tiles, num_sms / 2)); }
+
+// Rows of h that stay in L2 beside the passing tiles of W: the tiles along m go by in groups of so many.
+constexpr double kGroupBytes = 48e6;
+int m_group(const XentProblem& p, int m_tiles) {
+  return std::max(1, std::min(m_tiles, (int)(kGroupBytes / (2.0 * TILE * p.C))));
+}
+
+template <Kind KIND, bool HALF>
+cudaError_t launch(const XentParams& p, const Maps& maps, int pairs, int* status, cudaStream_t st) {
+  const auto kern = xent_kernel<KIND, HALF>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWholeSmSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(2 * pairs), THREADS, kWholeSmSmem, st>>>(p, status, maps);
+  return cudaGetLastError();
+}
+
+// A matrix [rows, cols] of 2-byte values: an operand whose lines run along the summed index (k_major) or along its rows.
+bool operand_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, bool k_major) {
+  return encode_matrix_map(map, base, rows, cols, stride, k_major ? BM : BK, 64);
+}
+
+}  // namespace
+
+// The vocabulary's pieces.  A piece's d lies in memory between the two launches: at most kPieceBytes of it, which is
+// near the L2's size, but at least kPieceColumns, so that the sums of dh, read and written once a piece (8 bytes for
+// 6 V/pieces operations), stay below a few hundredths of the products' time.
+constexpr long long kPieceBytes = 128ll << 20, kPieceColumns = 8192;
+XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms) {
+  XentBwdPlan g{};
+  const long long most = std::max(kPieceColumns, kPieceBytes / (2 * std::max(p.R, 1ll)));
+  g.pieces = (int)((p.V + most - 1) / most);
+  g.columns = (int)up((size_t)((p.V + g.pieces - 1) / g.pieces), TILE);
+  g.pieces = (int)((p.V + g.columns - 1) / g.columns);
+  // few tiles of dh: their long sums are split over blocks, until there is one for every pair or each is 16 chunks long
+  g.splits = 1;
+  if (want_dh) {
+    const long long tiles = (long long)tiles_of(p.R, TILE) * tiles_of(p.C, TILE);
+    const long long chunks = tiles_of(std::min<long long>(g.columns, p.V), BK);
+    g.splits = (int)std::max(1ll, std::min((num_sms / 2) / tiles, chunks / 16));
+  }
+  g.direct = g.pieces == 1 && g.splits == 1;
+  g.off_d = 256;
+  g.off_acc = g.off_d + up((size_t)p.R * std::min<long long>(g.columns, (long long)up(p.V, 8)) * 2, 256);
+  g.bytes = g.off_acc + (want_dh && !g.direct ? (size_t)g.splits * p.R * p.C * 4 : 0);
+  return g;
+}
+
+size_t xent_fwd_workspace(const XentProblem& p) {
+  return up((size_t)p.R * 4, 256) + (size_t)2 * tiles_of(p.V, TILE) * up(p.R, 32) * sizeof(float2);
+}
+
+cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void* weight, const long long* tokens, float* loss,
+                            float* lse, void* workspace, int num_sms, int* status, cudaStream_t st) {
+  Maps maps{};
+  if (!operand_map(&maps.a[0], hidden, p.R, p.C, p.hidden_stride, true) ||
+      !operand_map(&maps.b[0], weight, p.V, p.C, p.weight_stride, true))
+    return cudaErrorInvalidValue;
+  XentParams k{};
+  const int m_tiles = tiles_of(p.R, TILE), n_tiles = tiles_of(p.V, TILE);
+  k.job[0] = Job{m_tiles, n_tiles, 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)p.V};
+  k.R = p.R;
+  k.V = (int)p.V;
+  k.scale = p.scale;
+  k.c = p.scale * kLog2e;
+  k.tokens = tokens;
+  k.given = static_cast<float*>(workspace);
+  k.part_rows = (long long)up(p.R, 32);
+  k.part = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + up((size_t)p.R * 4, 256));
+  const int pairs = pairs_for(k.job[0].tiles(), num_sms);
+  cudaError_t e = p.half ? launch<kForward, true>(k, maps, pairs, status, st) : launch<kForward, false>(k, maps, pairs, status, st);
+  if (e != cudaSuccess) return e;
+  xent_join_kernel<<<(unsigned)tiles_of(p.R, 32), kJoinWarps * 32, 0, st>>>(p.R, (int)p.V, 2 * n_tiles, k.part_rows, k.part,
+                                                                          k.given, tokens, loss, lse);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const XentBwdIn& in, void* dhidden, void* dweight,
+                            void* workspace, int num_sms, int* status, cudaStream_t st) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* power = reinterpret_cast<float*>(ws);
+  uint8_t* d = ws + g.off_d;
+  float* acc = reinterpret_cast<float*>(ws + g.off_acc);
+  cudaError_t e = cudaSuccess;
+  if (p.half) {
+    xent_power_kernel<<<1, 1024, 0, st>>>(p.R, p.scale, in.g, in.g_lse, power);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int m_tiles = tiles_of(p.R, TILE), c_tiles = tiles_of(p.C, TILE);
+  for (int piece = 0; piece < g.pieces; ++piece) {
+    const long long v0 = (long long)piece * g.columns, cols = std::min<long long>(g.columns, p.V - v0);
+    const long long stride = (long long)up(cols, 8);
+    const uint8_t* w = static_cast<const uint8_t*>(in.weight) + v0 * p.weight_stride * 2;
+    XentParams k{};
+    k.R = p.R;
+    k.V = (int)p.V;
+    k.v0 = (int)v0;
+    k.scale = p.scale;
+    k.c = p.scale * kLog2e;
+    k.tokens = in.tokens;
+    k.lse = in.lse;
+    k.g = in.g;
+    k.g_lse = in.g_lse;
+    k.power = p.half ? power : nullptr;
+    {
+      Maps maps{};
+      if (!operand_map(&maps.a[0], in.hidden, p.R, p.C, p.hidden_stride, true) ||
+          !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, true) ||
+          !encode_matrix_map(&maps.out[0], d, p.R, cols, stride, 32, 64))
+        return cudaErrorInvalidValue;
+      k.job[0] = Job{m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)cols};
+      const int pairs = pairs_for(k.job[0].tiles(), num_sms);
+      e = p.half ? launch<kGradLogits, true>(k, maps, pairs, status, st) : launch<kGradLogits, false>(k, maps, pairs, status, st);
+      if (e != cudaSuccess) return e;
+    }
+    Maps maps{};
+    k.job[0] = k.job[1] = Job{};
+    if (dhidden) {
+      if (!operand_map(&maps.a[0], d, p.R, cols, stride, true) || !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, false) ||
+          !encode_matrix_map(&maps.out[0], dhidden, p.R, p.C, p.C, 32, 64) ||
+          (!g.direct && !encode_rows_f32_map(&maps.acc, acc, p.C, (int)p.R, g.splits, 32, 32)))
+        return cudaErrorInvalidValue;
+      // (a last, short piece adds to the first sums only)
+      k.job[0] = Job{m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), 0, 0, 1, (int)p.R, p.C};
+      k.accumulate = g.direct ? 0 : piece == 0 ? 1 : 2;
+    }
+    if (dweight) {
+      if (!operand_map(&maps.a[1], d, p.R, cols, stride, false) ||
+          !operand_map(&maps.b[1], in.hidden, p.R, p.C, p.hidden_stride, false) ||
+          !encode_matrix_map(&maps.out[1], dweight, p.V, p.C, p.C, 32, 64))
+        return cudaErrorInvalidValue;
+      k.job[1] = Job{tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, (int)cols, p.C};
+    }
+    const long long a = k.job[0].tiles(), b = k.job[1].tiles();
+    const int pairs = pairs_for(a + b, num_sms);
+    // the pairs with one tile of dh more get so many tiles of dW that all end together
+    k.more = (int)(a % pairs);
+    const double la = k.job[0].splits ? (double)k.job[0].k_chunks / k.job[0].splits + 2 : 0, lb = k.job[1].k_chunks + 2;
+    const double each = (a * la + b * lb) / pairs, mine = (double)(a / pairs + 1) * la;
+    k.few = k.more ? (int)std::max(0.0, std::min((each - mine) / lb + 0.5, (double)(b / k.more))) : 0;
+    e = p.half ? launch<kGradients, true>(k, maps, pairs, status, st) : launch<kGradients, false>(k, maps, pairs, status, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (dhidden && !g.direct) {
+    const long long n = p.R * p.C / 4;
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    if (p.half)
+      xent_close_kernel<true><<<blocks, 256, 0, st>>>(n, g.splits, reinterpret_cast<float4*>(acc), power, static_cast<uint2*>(dhidden));
+    else
+      xent_close_kernel<false><<<blocks, 256, 0, st>>>(n, g.splits, reinterpret_cast<float4*>(acc), power, static_cast<uint2*>(dhidden));
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace skl

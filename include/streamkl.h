@@ -421,6 +421,48 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
                                       const float* lse, const float* entropy, const float* g_logp,
                                       const float* g_entropy, void* dlogits, long long out_stride, void* stream);
 
+/*
+ * Cross entropy over a vocabulary, from the hidden states, without the logits in
+ * memory: the output layer's loss and its gradients where the logits themselves are
+ * not wanted (with them in memory, streamkl_logprobs_fwd's logp is -loss).
+ *
+ * hidden [rows, channels], weight [vocab, channels]: both of `dtype` (bf16 or fp16),
+ *   rows hidden_stride and weight_stride elements apart, 16-byte aligned; channels and
+ *   strides multiples of 8.  z = scale hidden weight^T, scale > 0.
+ * tokens [rows], 64-bit.  loss_r = LSE_r - z[r, token], lse_r = LSE_r, fp32 [rows].  A
+ *   negative token is no token: its loss is 0 and has no gradient (lse does).  A token
+ *   >= vocab gives NaN and has no gradient.
+ * A +inf or NaN logit makes its row's values NaN, -inf has probability 0.
+ *
+ * streamkl_vocab_xent_bwd: for upstream gradients g_loss [rows] and, unless NULL, g_lse
+ *   [rows] of the two outputs, and the forward's lse:
+ *     d = scale (g_loss (p - [v = token]) + g_lse p),  p = exp(z - lse)
+ *     dhidden = d weight [rows, channels],  dweight = d^T hidden [vocab, channels]
+ *   contiguous, of `dtype`; one of them may be NULL where it is not wanted.  d enters the
+ *   products rounded to `dtype`; sums are fp32, dhidden and dweight are rounded once.  What
+ *   several blocks add up is added in a fixed order: the same bits on every run.  A row whose
+ *   gradients are 0 takes part in dweight's sum with zeros: its hidden states have to be finite.
+ * Workspaces (16-byte aligned): forward, 16 bytes per row and 256 columns; backward, a piece
+ *   of d and fp32 sums of dhidden: streamkl_vocab_xent_bwd_plan gives the number of the
+ *   vocabulary's pieces, the splits of dhidden's sums and the bytes for any SM count
+ *   (num_sms <= 0: the current device; with num_sms > 0 a pure host rule).
+ */
+typedef struct {
+  long long rows, vocab;
+  int channels, dtype;
+  float scale;
+  long long hidden_stride, weight_stride;
+} streamkl_xent_shape;
+streamkl_status streamkl_vocab_xent_fwd_workspace(streamkl_xent_shape s, size_t* bytes);
+streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, const long long* tokens, streamkl_xent_shape s,
+                                        float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+streamkl_status streamkl_vocab_xent_bwd_plan(streamkl_xent_shape s, int num_sms, int want_dhidden, int* pieces, int* splits,
+                                             size_t* bytes);
+streamkl_status streamkl_vocab_xent_bwd_workspace(streamkl_xent_shape s, int want_dhidden, size_t* bytes);
+streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, const long long* tokens, const float* lse,
+                                        const float* g_loss, const float* g_lse, streamkl_xent_shape s, void* dhidden,
+                                        void* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Text for a status code (static storage). */
 const char* streamkl_status_string(streamkl_status st);
 
