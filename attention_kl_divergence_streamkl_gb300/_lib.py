@@ -53,6 +53,13 @@ class AttnShape(ctypes.Structure):
                 ("k_lens", ctypes.c_void_p)] + [(f"{t}_stride_{x}", ctypes.c_longlong) for t in "qkvo" for x in "bhn"] + [("o_rest", ctypes.c_void_p)]
 
 
+class RotaryShape(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_int) for x in ("B", "HQ", "HK", "N", "D", "dim", "dtype", "interleaved")] + [
+        ("amplitude", ctypes.c_float), ("offset", ctypes.c_longlong), ("positions", ctypes.c_void_p),
+        ("positions_bytes", ctypes.c_int), ("positions_stride", ctypes.c_longlong)] + [
+        (f"{t}_stride_{x}", ctypes.c_longlong) for t in ("q", "k", "q_out", "k_out") for x in "bhn"]
+
+
 class XentShape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_longlong), ("vocab", ctypes.c_longlong), ("channels", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("scale", ctypes.c_float), ("hidden_stride", ctypes.c_longlong), ("weight_stride", ctypes.c_longlong)]
@@ -94,6 +101,7 @@ SIGNATURES = {
     "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
     "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
+    "streamkl_rotary": (_I, [_P, _P, RotaryShape, _P, _P, _P, _I, _S]),
     "streamkl_vocab_xent_fwd_workspace": (_I, [XentShape, ctypes.POINTER(_SZ)]),
     "streamkl_vocab_xent_fwd": (_I, [_P, _P, _P, XentShape, _F, _F, _P, _SZ, _S]),
     "streamkl_vocab_xent_bwd_plan": (_I, [XentShape, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
@@ -696,6 +704,96 @@ def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0
           tok.data_ptr() if T else None, T, scale, lse.data_ptr(), None if ent is None else ent.data_ptr(),
           g_logp.data_ptr() if T else None, None if ent is None else g_entropy.data_ptr(), out.data_ptr(), V)
     return _back((out,), True)[0] if host else out
+
+
+def _rotary(tensors, plan, positions, offset, interleaved, inverse, out):
+    """Turns q and k (either may be None) by their positions; see rotary_fwd."""
+    q, k = tensors
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k is needed")
+    B, _, N, D = _rotary_sizes(one)
+    dtype, dev = one.dtype, one.device
+    if dtype not in DTYPES:
+        raise TypeError("q and k must be bfloat16, float16 or float32")
+    if D % 2 or plan.dim > D:
+        raise ValueError(f"{plan.dim} channels do not turn in {D}: D must be even and at least the plan's dim")
+    host = dev.type == "cpu"
+    if host:
+        if out is not None:
+            raise ValueError("out is for device tensors")
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if plan.turns.device != dev:
+        raise ValueError(f"the plan is on {plan.turns.device}, the tensors on {dev}")
+    given, stride, size = None, 0, 0
+    if positions is not None:
+        if offset:
+            raise ValueError("positions or an offset, not both")
+        if positions.dtype is not torch.int64 and positions.dtype is not torch.int32:
+            raise TypeError("positions must be int64 or int32")
+        if positions.shape != (N,) and positions.shape != (B, N):
+            raise ValueError(f"positions {tuple(positions.shape)} must be [{N}] or [{B}, {N}]")
+        given = positions.to(dev, non_blocking=True) if positions.device != dev else positions
+        if N > 1 and given.stride(-1) != 1:
+            given = given.contiguous()
+        size, stride = given.element_size(), given.stride(0) if given.dim() == 2 and B > 1 else 0
+    outs = (None, None) if out is None else tuple(out)
+    if len(outs) != 2:
+        raise ValueError("out must be (q_out, k_out)")
+    ins, outs, strides, ptrs = [], list(outs), [], []
+    for i, (t, o) in enumerate(zip(tensors, list(outs))):
+        if t is None:
+            if o is not None:
+                raise ValueError("an output without its input")
+            ins.append(None)
+            continue
+        if t.dtype != dtype or t.device != one.device:
+            raise ValueError("q and k must have the same type and device")
+        b, h, n, d = _rotary_sizes(t)
+        if (b, n, d) != (B, N, D):
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
+        if host:
+            t = t.to(dev, non_blocking=True)
+        if t.stride(3) != 1:
+            t = t.contiguous()
+        if o is None:
+            outs[i] = torch.empty_like(t) if t.stride(3) == 1 and all(s > 0 for s in t.stride()) else t.new_empty(t.shape)
+        elif o.shape != t.shape or o.dtype != dtype or o.device != dev or o.stride(3) != 1:
+            raise ValueError("an output must have its input's shape, type and device, and contiguous channels")
+        ins.append(t)
+    for t in (*ins, *outs):
+        strides += [0, 0, 0] if t is None else t.stride()[:3]
+        ptrs.append(None if t is None else t.data_ptr())
+    s = RotaryShape(B, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], N, D, plan.dim, DTYPES[dtype],
+                    bool(interleaved), plan.amplitude, int(offset), None if given is None else given.data_ptr(), size, stride,
+                    *strides)
+    _call("streamkl_rotary", dev.index, ptrs[0], ptrs[1], s, plan.turns.data_ptr(), ptrs[2], ptrs[3], bool(inverse))
+    if not host:
+        return tuple(outs)
+    got = iter(_back(tuple(t for t in outs if t is not None), True))
+    return tuple(None if t is None else next(got) for t in outs)
+
+
+def _rotary_sizes(t):
+    if t.dim() != 4:
+        raise ValueError("q and k must be [B, H, N, D]")
+    return t.shape
+
+
+def rotary_fwd(q, k, plan, positions=None, offset=0, interleaved=False, out=None):
+    """Rotary positions: (q, k) with the first plan.dim of D channels turned by each row's position.
+
+    q: [B, HQ, N, D], k: [B, HK, N, D], bf16, fp16 or fp32, either may be None; plan: rotary_plan's, on their device.
+    positions: int64 or int32 [N] or [B, N]; without them row n is at offset + n.  Pairs are the channels i and dim / 2 + i,
+    with interleaved 2 i and 2 i + 1.  out: (q_out, k_out) to write to, for example q and k themselves or a cache's rows
+    (it may overlap nothing else); an entry may be None.
+    """
+    return _rotary((q, k), plan, positions, offset, interleaved, False, out)
+
+
+def rotary_bwd(dq, dk, plan, positions=None, offset=0, interleaved=False, out=None):
+    """The gradients of rotary_fwd's q and k from those of its results: turned back by the same positions."""
+    return _rotary((dq, dk), plan, positions, offset, interleaved, True, out)
 
 
 def make_xent_shape(rows, vocab, channels, dtype=0, scale=1.0, hidden_stride=None, weight_stride=None) -> XentShape:

@@ -159,3 +159,29 @@ def vocab_cross_entropy(hidden, weight, tokens, scale=1.0, return_lse=False):
     """
     loss, lse = _VocabCrossEntropy.apply(hidden, weight, tokens, scale)
     return (loss, lse) if return_lse else loss
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, plan, positions, offset, interleaved):
+        ctx.save_for_backward(positions)
+        ctx.plan, ctx.offset, ctx.interleaved = plan, offset, interleaved
+        ctx.set_materialize_grads(False)
+        return _lib.rotary_fwd(q, k, plan, positions, offset, interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        if dq is None and dk is None:
+            return (None,) * 6
+        positions, = ctx.saved_tensors
+        return (*_lib.rotary_bwd(dq, dk, ctx.plan, positions, ctx.offset, ctx.interleaved), None, None, None, None)
+
+
+def rotary(q, k, plan, positions=None, offset=0, interleaved=False):
+    """(q, k) turned by their positions, differentiable: what attention, differential_attention and attention_kl take.
+
+    q: [B, HQ, N, D], k: [B, HK, N, D]; plan: rotary_plan's; positions int64 or int32 [N] or [B, N], or rows from offset on.
+    See rotary_fwd.
+    """
+    return _Rotary.apply(q, k, plan, positions, offset, interleaved)

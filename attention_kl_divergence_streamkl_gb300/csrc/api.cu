@@ -882,6 +882,81 @@ streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, 
                                    sms, status, st));
 }
 
+// Rows that are written must not share an element: sorted by stride, each covers the extent below it.
+static bool rows_disjoint(const RotaryStrides& s, int B, int H, int N, int D) {
+  long long st[3] = {B > 1 ? s.b : 0, H > 1 ? s.h : 0, N > 1 ? s.n : 0}, n[3] = {B, H, N};
+  long long span = D;
+  for (int round = 0; round < 3; ++round) {
+    int least = -1;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (least < 0 || st[i] < st[least])) least = i;
+    if (least < 0) break;
+    if (st[least] < span) return false;
+    span = st[least] * n[least];
+    n[least] = 1;
+  }
+  return true;
+}
+
+streamkl_status streamkl_rotary(const void* q, const void* k, streamkl_rotary_shape s, const unsigned long long* turns, void* q_out,
+                                void* k_out, int inverse, void* stream) {
+  if (s.B < 0 || s.HQ < 0 || s.HK < 0 || s.N < 0 || s.D <= 0 || s.dim <= 0 || s.dim > s.D || s.dim % 2) return STREAMKL_ERR_INVALID;
+  if (s.dtype != STREAMKL_BF16 && s.dtype != STREAMKL_FP16 && s.dtype != STREAMKL_FP32) return STREAMKL_ERR_INVALID;
+  if (!(s.amplitude == s.amplitude) || isinf(s.amplitude)) return STREAMKL_ERR_INVALID;
+  if (s.positions && s.positions_bytes != 4 && s.positions_bytes != 8) return STREAMKL_ERR_INVALID;
+  if (s.positions && (s.positions_stride < 0 || (reinterpret_cast<uintptr_t>(s.positions) & (s.positions_bytes - 1))))
+    return STREAMKL_ERR_INVALID;
+  if (s.D % 2 || s.D > (1 << 16) || (long long)s.HQ + s.HK > 65535 || (long long)s.B * s.N > 0x7fffffffLL)
+    return STREAMKL_ERR_UNSUPPORTED;
+  const RotaryStrides q_in{s.q_stride_b, s.q_stride_h, s.q_stride_n}, k_in{s.k_stride_b, s.k_stride_h, s.k_stride_n},
+      q_to{s.q_out_stride_b, s.q_out_stride_h, s.q_out_stride_n}, k_to{s.k_out_stride_b, s.k_out_stride_h, s.k_out_stride_n};
+  for (const RotaryStrides& r : {q_in, k_in, q_to, k_to})
+    if (r.b < 0 || r.h < 0 || r.n < 0 || r.b >= (1ll << 40) || r.h >= (1ll << 40) || r.n >= (1ll << 40)) return STREAMKL_ERR_INVALID;
+  if (s.B == 0 || s.N == 0 || s.HQ + s.HK == 0) return STREAMKL_OK;
+  const uintptr_t size = s.dtype == STREAMKL_FP32 ? 4 : 2;
+  if (!aligned_to(turns, 8)) return STREAMKL_ERR_INVALID;
+  if (s.HQ && (!aligned_to(q, size) || !aligned_to(q_out, size) || !rows_disjoint(q_to, s.B, s.HQ, s.N, s.D)))
+    return STREAMKL_ERR_INVALID;
+  if (s.HK && (!aligned_to(k, size) || !aligned_to(k_out, size) || !rows_disjoint(k_to, s.B, s.HK, s.N, s.D)))
+    return STREAMKL_ERR_INVALID;
+  // in place: every row on itself
+  auto moved = [&](const RotaryStrides& a, const RotaryStrides& b, int heads) {
+    return (s.B > 1 && a.b != b.b) || (heads > 1 && a.h != b.h) || (s.N > 1 && a.n != b.n);
+  };
+  if ((s.HQ && q == q_out && moved(q_in, q_to, s.HQ)) || (s.HK && k == k_out && moved(k_in, k_to, s.HK)))
+    return STREAMKL_ERR_INVALID;
+  RotaryProblem p{};
+  p.B = s.B;
+  p.HQ = s.HQ;
+  p.HK = s.HK;
+  p.N = s.N;
+  p.D = s.D;
+  p.dim = s.dim;
+  p.tokens = (unsigned)(s.B * (long long)s.N);
+  p.dtype = s.dtype;
+  p.interleaved = s.interleaved != 0;
+  p.amplitude = s.amplitude;
+  p.sin_sign = inverse ? -s.amplitude : s.amplitude;
+  p.offset = s.offset;
+  p.positions = s.positions;
+  p.positions_stride = s.positions_stride;
+  p.positions_wide = s.positions_bytes == 8;
+  p.turns = turns;
+  p.q_in = s.HQ ? q : nullptr;
+  p.k_in = s.HK ? k : nullptr;
+  p.q_out = s.HQ ? q_out : nullptr;
+  p.k_out = s.HK ? k_out : nullptr;
+  p.q = q_in;
+  p.k = k_in;
+  p.qo = q_to;
+  p.ko = k_to;
+  int sms = 0;
+  const streamkl_status v = device_sms(&sms);
+  if (v != STREAMKL_OK) return v;
+  if (!rotary_plan(&p, sms)) return STREAMKL_ERR_UNSUPPORTED;
+  return from_cuda(launch_rotary(p, static_cast<cudaStream_t>(stream)));
+}
+
 streamkl_status streamkl_check_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return STREAMKL_ERR_CUDA;
   int h = 0;

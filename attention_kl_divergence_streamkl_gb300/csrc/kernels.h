@@ -210,6 +210,33 @@ struct XentBwdIn {
 cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& plan, const XentBwdIn& in, void* dhidden, void* dweight,
                             void* workspace, int num_sms, int* status, cudaStream_t st);
 
+// ---- rotary positions ----------------------------------------------------------------
+struct RotaryStrides {
+  long long b, h, n;  // elements; channels are contiguous
+};
+struct RotaryProblem {
+  int B, HQ, HK, N, D, dim;  // the first dim channels turn
+  unsigned tokens;           // B N
+  int dtype, interleaved;
+  float amplitude, sin_sign;  // cos is multiplied by amplitude, sin by sin_sign: amplitude, or -amplitude for the inverse
+  long long offset;           // position of row 0 where positions is null
+  const void* positions;      // 64-bit, or 32-bit unless positions_wide
+  long long positions_stride;
+  int positions_wide;
+  const unsigned long long* turns;  // [dim / 2], 2^-64 of a turn a position
+  const void *q_in, *k_in;
+  void *q_out, *k_out;
+  RotaryStrides q, k, qo, ko;
+  // plan
+  int vectors;     // 16-byte loads
+  int turning;     // slots of a row that turn
+  int heads_each;  // heads that a thread goes through
+  long long items;
+  FastDiv by_slots, by_rows;
+};
+bool rotary_plan(RotaryProblem* p, int num_sms);  // false: too large for one launch
+cudaError_t launch_rotary(const RotaryProblem& p, cudaStream_t st);
+
 // ---- test hook ------------------------------------------------------------------
 cudaError_t launch_wait_timeout_probe(int timeout_us, int* status, cudaStream_t st);
 

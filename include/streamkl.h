@@ -463,6 +463,40 @@ streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, 
                                         const float* g_loss, const float* g_lse, streamkl_xent_shape s, void* dhidden,
                                         void* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Rotary positions: what turns the queries and keys before an attention, or before
+ * the attention loss, in one launch for both.
+ *
+ * q [B, HQ, N, D], k [B, HK, N, D] of `dtype` (HQ or HK may be 0, and that pointer NULL then),
+ *   D even, channels contiguous, element strides along b, h, n as given, any alignment to an
+ *   element (16-byte granules are faster).  The first `dim` channels (even) turn, the others are
+ *   copied.  Pair i is the channels i and dim / 2 + i, with `interleaved` 2 i and 2 i + 1.
+ * A row at position p: (x, y) -> amplitude (x cos a - y sin a, y cos a + x sin a), a = p turns[i]
+ *   2^-64 of a turn: turns [dim / 2], device, 2^64 f_i / 2 pi mod 2^64 for a frequency of f_i radians
+ *   a position.  The angle is exact to |p| 2^-64 turns for any 64-bit p, negative ones too.
+ *   Arithmetic is fp32, results are rounded once.
+ * positions: device, 32-bit or 64-bit integers (positions_bytes), sequence b's N of them from element
+ *   b positions_stride on (stride 0: the same for all); NULL: row n is at offset + n.
+ * inverse != 0 turns back (-a), with the same amplitude: the gradient's map.
+ * Outputs: strides of their own, rows that do not overlap; q_out may be q and k_out k, with the same
+ *   strides.  Otherwise no output may overlap an input or the other output.
+ */
+typedef struct {
+  int B, HQ, HK, N, D, dim;
+  int dtype, interleaved;
+  float amplitude;
+  long long offset;
+  const void* positions;
+  int positions_bytes;
+  long long positions_stride;
+  long long q_stride_b, q_stride_h, q_stride_n;
+  long long k_stride_b, k_stride_h, k_stride_n;
+  long long q_out_stride_b, q_out_stride_h, q_out_stride_n;
+  long long k_out_stride_b, k_out_stride_h, k_out_stride_n;
+} streamkl_rotary_shape;
+streamkl_status streamkl_rotary(const void* q, const void* k, streamkl_rotary_shape s, const unsigned long long* turns,
+                                void* q_out, void* k_out, int inverse, void* stream);
+
 /* Text for a status code (static storage). */
 const char* streamkl_status_string(streamkl_status st);
 
