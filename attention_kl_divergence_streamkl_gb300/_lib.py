@@ -53,6 +53,11 @@ class AttnShape(ctypes.Structure):
                 ("k_lens", ctypes.c_void_p)] + [(f"{t}_stride_{x}", ctypes.c_longlong) for t in "qkvo" for x in "bhn"] + [("o_rest", ctypes.c_void_p)]
 
 
+class DiffAttnShape(ctypes.Structure):
+    _fields_ = [("maps", AttnShape), ("lam", ctypes.c_void_p)] + [
+        (f"{t}_stride_{x}", ctypes.c_longlong) for t in ("lam", "d") for x in "bhn"]
+
+
 class RotaryShape(ctypes.Structure):
     _fields_ = [(x, ctypes.c_int) for x in ("B", "HQ", "HK", "N", "D", "dim", "dtype", "interleaved")] + [
         ("amplitude", ctypes.c_float), ("offset", ctypes.c_longlong), ("positions", ctypes.c_void_p),
@@ -101,6 +106,11 @@ SIGNATURES = {
     "streamkl_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, AttnShape, _P, _P, _P, _I, _P, _SZ, _S]),
     "streamkl_logprobs_fwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _I, _F, _F, _F, _F, _P, _S]),
     "streamkl_logprobs_bwd": (_I, [_P, _I, _LL, _LL, _LL, _P, _I, ctypes.c_float, _F, _F, _F, _F, _P, _LL, _S]),
+    "streamkl_diff_attn_fwd_plan": (_I, [DiffAttnShape, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
+    "streamkl_diff_attn_fwd_workspace": (_I, [DiffAttnShape, ctypes.POINTER(_SZ)]),
+    "streamkl_diff_attn_fwd": (_I, [_P, _P, _P, DiffAttnShape, _P, _P, _F, _P, _SZ, _S]),
+    "streamkl_diff_attn_bwd_workspace": (_I, [DiffAttnShape, _I, ctypes.POINTER(_SZ)]),
+    "streamkl_diff_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, DiffAttnShape, _P, _P, _P, _F, _I, _P, _SZ, _S]),
     "streamkl_rotary": (_I, [_P, _P, RotaryShape, _P, _P, _P, _I, _S]),
     "streamkl_vocab_xent_fwd_workspace": (_I, [XentShape, ctypes.POINTER(_SZ)]),
     "streamkl_vocab_xent_fwd": (_I, [_P, _P, _P, XentShape, _F, _F, _P, _SZ, _S]),
@@ -618,6 +628,122 @@ def attn_bwd(q, k, v, o, lse, do, dlse=None, scale=None, causal=False, q_lens=No
     return _back((dq, dk, dv), True) if host else (dq, dk, dv)
 
 
+def make_diff_attn_shape(maps, lam=None, lam_strides=(0, 0, 0), d_strides=(0, 0, 0)) -> DiffAttnShape:
+    """The C shape of a difference: make_attn_shape's of both maps, and lam (kept alive by the caller)."""
+    return DiffAttnShape(maps, None if lam is None else lam.data_ptr(), *lam_strides, *d_strides)
+
+
+def diff_attn_plan(B, H, HK, NQ, NK, D, num_sms, causal=False):
+    """(packed, key splits, workspace bytes) of the forward of H differences on a device with num_sms SMs."""
+    a, b, n = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
+    s = make_diff_attn_shape(make_attn_shape(B, 2 * H, HK, NQ, NK, D, None, causal))
+    _check(lib().streamkl_diff_attn_fwd_plan(s, int(num_sms), *map(ctypes.byref, (a, b, n))), "streamkl_diff_attn_fwd_plan")
+    return bool(a.value), b.value, n.value
+
+
+def _diff_inputs(tensors, like_d, lam, q_lens, k_lens):
+    """Validates a difference's tensors (q, k, v, and maps, maps_rest in the backward), what is like its result, and lam."""
+    tensors, q_lens, k_lens, sizes, dev, host = _attn_inputs(tensors, q_lens, k_lens)
+    B, H, HK, NQ, _, D = sizes
+    if H % 2 or H // 2 % HK:
+        raise ValueError(f"{H} query heads are not pairs that divide over {HK} key heads")
+    for i, t in enumerate(like_d):
+        if t.dtype is not torch.bfloat16:
+            raise TypeError("do must be bfloat16")
+        if t.shape != (B, H // 2, NQ, D):
+            raise ValueError(f"do must be {(B, H // 2, NQ, D)}")
+        if (t.device.type == "cpu") != host or (not host and t.device != dev):
+            raise ValueError("inputs on different devices")
+        if host:
+            like_d[i] = t.contiguous().to(dev, non_blocking=True)
+    if lam.dtype is not torch.float32:
+        raise TypeError("lam must be float32")
+    if lam.dim() > 3:
+        raise ValueError(f"lam {tuple(lam.shape)} must broadcast to {(B, H // 2, NQ)}")
+    lam = lam.expand(B, H // 2, NQ)  # raises where it does not
+    if lam.device != dev:
+        if not host:
+            raise ValueError("inputs on different devices")
+        lam = lam.to(dev, non_blocking=True)
+    return tensors, like_d, lam, q_lens, k_lens, sizes, dev, host
+
+
+def diff_attn_fwd(q, k, v, lam, scale=None, causal=False, q_lens=None, k_lens=None, return_maps=False):
+    """Differential attention: (d, lse), d = softmax(scale Q1 K^T) V - lam softmax(scale Q2 K^T) V.
+
+    q: [B, 2 H, N_Q, D] bf16, heads 2 i and 2 i + 1 the maps of difference i; k and v: [B, HK, N_K, D], H a multiple of HK;
+    lam: fp32, any shape that broadcasts to [B, H, N_Q].  d: bf16 [B, H, N_Q, D], stored by heads or by rows as q is; lse: fp32
+    [B, 2 H, N_Q] of both maps.  scale, causal and lengths as in attn_fwd.  return_maps adds what diff_attn_bwd reads: each
+    map's own result and what its rounding left, two bf16 tensors like q.
+    """
+    (q, k, v), _, lam, q_lens, k_lens, sizes, dev, host = _diff_inputs((q, k, v), [], lam, q_lens, k_lens)
+    (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
+    B, H, _, NQ, _, D = sizes
+    maps = rest = None
+    if return_maps:
+        maps, rest = (torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    d = _by_order(B, H // 2, NQ, D, qs, dev)
+    s = make_diff_attn_shape(make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, qs, rest), lam, lam.stride(),
+                             d.stride()[:3])
+    nbytes = _workspace_bytes("streamkl_diff_attn_fwd_workspace", dev, s)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    lse = torch.empty((B, H, NQ), dtype=torch.float32, device=dev)
+    _call("streamkl_diff_attn_fwd", dev.index, q.data_ptr(), k.data_ptr(), v.data_ptr(), s, d.data_ptr(),
+          maps.data_ptr() if return_maps else None, lse.data_ptr(), ws.data_ptr() if nbytes else None, nbytes)
+    out = (d, lse, maps, rest) if return_maps else (d, lse)
+    return _back(out, True) if host else out
+
+
+def _by_order(B, H, N, D, strides, dev):
+    """A dense bf16 [B, H, N, D] tensor, its rows before its heads where `strides` has them so."""
+    if H > 1 and strides[1] < strides[2]:
+        return torch.empty((B, N, H, D), dtype=torch.bfloat16, device=dev).transpose(1, 2)
+    return torch.empty((B, H, N, D), dtype=torch.bfloat16, device=dev)
+
+
+def _workspace_bytes(name, dev, *args):
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(dev):
+        _check(getattr(lib(), name)(*args, ctypes.byref(n)), name)
+    return n.value
+
+
+def diff_attn_bwd(q, k, v, lam, maps, lse, do, dlse=None, scale=None, causal=False, q_lens=None, k_lens=None, bwd_mode=BWD_AUTO,
+                  maps_rest=None):
+    """Differential attention's gradients (dq, dk, dv, dlam): bf16 with the layouts of q, k, v, and fp32 [B, H, N_Q], a value
+    for each row whatever shape lam has.
+
+    maps, lse, maps_rest: diff_attn_fwd's for the same inputs (return_maps); do: dLoss/dd like d; dlse: dLoss/dlse fp32
+    [B, 2 H, N_Q] or None.  bwd_mode as in attn_bwd.
+    """
+    if bwd_mode == BWD_AUTO and torch.are_deterministic_algorithms_enabled():
+        bwd_mode = BWD_SEPARATE
+    if maps_rest is None:
+        raise ValueError("maps_rest is needed: diff_attn_fwd gives it with the maps (return_maps)")
+    (q, k, v, maps, rest), (do,), lam, q_lens, k_lens, sizes, dev, host = _diff_inputs((q, k, v, maps, maps_rest), [do], lam,
+                                                                                     q_lens, k_lens)
+    (q, qs), (k, ks), (v, vs), (do, ds) = _layout(q), _layout(k), _layout(v), _layout(do)
+    (maps, os_), (rest, rs) = _layout(maps), _layout(rest)
+    B, H, HK, NQ, NK, D = sizes
+    if os_ != rs:  # the library reads them with one set of strides
+        maps, rest = (t.clone(memory_format=torch.contiguous_format) for t in (maps, rest))
+        os_ = (H * NQ * D, NQ * D, D)
+    lse, dlse = _rows(lse, dev, (B, H, NQ), "lse"), _rows(dlse, dev, (B, H, NQ), "dlse")
+    if lse is None:
+        raise ValueError("lse is needed")
+    s = make_diff_attn_shape(make_attn_shape(*sizes, scale, causal, q_lens, k_lens, qs, ks, vs, os_, rest), lam, lam.stride(), ds)
+    nbytes = _workspace_bytes("streamkl_diff_attn_bwd_workspace", dev, s, int(bwd_mode))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    dq = torch.empty_strided((B, H, NQ, D), (*qs, 1), dtype=torch.bfloat16, device=dev)
+    dk = torch.empty_strided((B, HK, NK, D), (*ks, 1), dtype=torch.bfloat16, device=dev)
+    dv = torch.empty_strided((B, HK, NK, D), (*vs, 1), dtype=torch.bfloat16, device=dev)
+    dlam = torch.empty((B, H // 2, NQ), dtype=torch.float32, device=dev)
+    _call("streamkl_diff_attn_bwd", dev.index, q.data_ptr(), k.data_ptr(), v.data_ptr(), maps.data_ptr(), lse.data_ptr(),
+          do.data_ptr(), None if dlse is None else dlse.data_ptr(), s, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          dlam.data_ptr(), bwd_mode, ws.data_ptr() if nbytes else None, nbytes)
+    return _back((dq, dk, dv, dlam), True) if host else (dq, dk, dv, dlam)
+
+
 def _logits_rows(logits, tokens):
     """Validates logits [..., V] and tokens [...] or [..., T]; returns (device logits as strided [R, V] rows,
     contiguous int64 device tokens or None, T, the leading shape, device, was_host)."""
@@ -847,13 +973,6 @@ def vocab_xent_plan(rows, vocab, channels, num_sms, want_dhidden=True):
     return a.value, b.value, n.value
 
 
-def _xent_workspace(name, dev, *args):
-    n = ctypes.c_size_t(0)
-    with torch.cuda.device(dev):
-        _check(getattr(lib(), name)(*args, ctypes.byref(n)), name)
-    return torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
-
-
 def vocab_xent_fwd(hidden, weight, tokens, scale=1.0):
     """Cross entropy of the rows softmax(scale hidden weight^T) at given tokens, without the logits in memory:
     (loss, lse), fp32 like tokens.
@@ -862,7 +981,8 @@ def vocab_xent_fwd(hidden, weight, tokens, scale=1.0):
     one is no token (its loss is 0), one past the vocabulary gives NaN.
     """
     x, w, tok, s, lead, dev, host = _xent_inputs(hidden, weight, tokens, scale)
-    ws, nbytes = _xent_workspace("streamkl_vocab_xent_fwd_workspace", dev, s)
+    nbytes = _workspace_bytes("streamkl_vocab_xent_fwd_workspace", dev, s)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     loss, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(2))
     _call("streamkl_vocab_xent_fwd", dev.index, x.data_ptr(), w.data_ptr(), tok.data_ptr(), s, loss.data_ptr(),
           lse.data_ptr(), ws.data_ptr(), nbytes)
@@ -881,7 +1001,8 @@ def vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse=None, scale=1.0, w
         raise ValueError("lse and g_loss are needed")
     if not want_dhidden and not want_dweight:
         return None, None
-    ws, nbytes = _xent_workspace("streamkl_vocab_xent_bwd_workspace", dev, s, bool(want_dhidden))
+    nbytes = _workspace_bytes("streamkl_vocab_xent_bwd_workspace", dev, s, bool(want_dhidden))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     dh = torch.empty(hidden.shape, dtype=x.dtype, device=dev) if want_dhidden else None
     dw = torch.empty(weight.shape, dtype=x.dtype, device=dev) if want_dweight else None
     _call("streamkl_vocab_xent_bwd", dev.index, x.data_ptr(), w.data_ptr(), tok.data_ptr(), lse.data_ptr(), g_loss.data_ptr(),

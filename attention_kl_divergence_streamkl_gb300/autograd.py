@@ -97,6 +97,43 @@ def attention(q, k, v, scale=None, causal=False, q_lens=None, k_lens=None, retur
     return (o, lse) if return_lse else o
 
 
+class _DifferentialAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lam, scale, causal, q_lens, k_lens, bwd_mode, train):
+        d, lse, *maps = _lib.diff_attn_fwd(q, k, v, lam, scale, causal, q_lens, k_lens, train)
+        ctx.save_for_backward(q, k, v, lam, lse, q_lens, k_lens, *maps)
+        ctx.scale, ctx.causal, ctx.bwd_mode = scale, causal, bwd_mode
+        ctx.set_materialize_grads(False)
+        return d, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dd, dlse):
+        q, k, v, lam, lse, q_lens, k_lens, maps, rest = ctx.saved_tensors
+        if dd is None and dlse is None:
+            return (None,) * 10
+        if dd is None:
+            dd = q.new_zeros(q.shape[0], q.shape[1] // 2, *q.shape[2:])
+        *grads, dlam = _lib.diff_attn_bwd(q, k, v, lam, maps, lse, dd, dlse, ctx.scale, ctx.causal, q_lens, k_lens,
+                                          ctx.bwd_mode, rest)
+        return (*grads, dlam.sum_to_size(lam.shape), None, None, None, None, None, None)
+
+
+def differential_attention(q, k, v, lam, scale=None, causal=False, q_lens=None, k_lens=None, return_lse=False,
+                           bwd_mode=_lib.BWD_AUTO):
+    """softmax(scale Q1 K^T) V - lam softmax(scale Q2 K^T) V, differentiable in q, k, v and lam: bf16 [B, H, N_Q, D], and with
+    return_lse both maps' log-sum-exps (fp32 [B, 2 H, N_Q], differentiable too).
+
+    The attention of a model whose heads are differences of two maps: q [B, 2 H, N_Q, D] has heads 2 i and 2 i + 1 for
+    difference i, k and v [B, HK, N_K, D] may have fewer heads; lam fp32 broadcasts to [B, H, N_Q].  Either map is distilled
+    with attention_kl on its heads of q.  See diff_attn_fwd and diff_attn_bwd; where a gradient will be asked for, each map's
+    own result is kept for the backward in two parts like q.
+    """
+    train = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
+    d, lse = _DifferentialAttention.apply(q, k, v, lam, scale, causal, q_lens, k_lens, bwd_mode, train)
+    return (d, lse) if return_lse else d
+
+
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, scale, top_k):

@@ -647,6 +647,9 @@ static streamkl_status attn_problem(const streamkl_attn_shape& s, AttnProblem* p
       !strides_ok(s.v_stride_b, s.v_stride_h, s.v_stride_n, s.HK, s.NK, s.D, &p->vs_b, &p->vs_h, &p->vs_n) ||
       !strides_ok(s.o_stride_b, s.o_stride_h, s.o_stride_n, s.H, s.NQ, s.D, &p->os_b, &p->os_h, &p->os_n))
     return STREAMKL_ERR_INVALID;
+  p->gs_b = p->os_b;
+  p->gs_h = p->os_h;
+  p->gs_n = p->os_n;
   p->rows = (long long)s.B * s.H * s.NQ;
   p->o_rest = s.o_rest;
   if (!aligned16(s.o_rest)) return STREAMKL_ERR_INVALID;
@@ -748,8 +751,109 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
   }
   int* status = nullptr;
   if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
-  return from_cuda(launch_attn_bwd(p, plan, AttnBwdIn{q, k, v, o, go, p.o_rest, lse, dlse}, dq, dk, dv, workspace, status,
+  return from_cuda(launch_attn_bwd(p, plan, AttnBwdIn{q, k, v, o, go, p.o_rest, lse, dlse, nullptr, nullptr}, dq, dk, dv, workspace, status,
                                    static_cast<cudaStream_t>(stream)));
+}
+
+static streamkl_status diff_problem(const streamkl_diff_attn_shape& s, AttnProblem* p) {
+  if (s.maps.H % 2 || s.maps.HK <= 0 || s.maps.H / 2 % s.maps.HK) return STREAMKL_ERR_INVALID;
+  const streamkl_status v = attn_problem(s.maps, p);
+  if (v != STREAMKL_OK) return v;
+  p->diff = 1;
+  p->lam = s.lam;
+  p->ls_b = s.lam_stride_b;
+  p->ls_h = s.lam_stride_h;
+  p->ls_n = s.lam_stride_n;
+  for (long long x : {p->ls_b, p->ls_h, p->ls_n})
+    if (x < 0 || x >= (1ll << 38)) return STREAMKL_ERR_INVALID;
+  if (!aligned_to_or_null(s.lam, 4)) return STREAMKL_ERR_INVALID;
+  if (!strides_ok(s.d_stride_b, s.d_stride_h, s.d_stride_n, s.maps.H / 2, s.maps.NQ, s.maps.D, &p->cs_b, &p->cs_h, &p->cs_n))
+    return STREAMKL_ERR_INVALID;
+  // the gradients that reach the maps lie contiguous in the workspace
+  p->gs_n = p->D;
+  p->gs_h = (long long)p->NQ * p->D;
+  p->gs_b = p->H * p->gs_h;
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_diff_attn_fwd_plan(streamkl_diff_attn_shape s, int num_sms, int* packed, int* splits, size_t* bytes) {
+  AttnProblem p;
+  streamkl_status v = diff_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!packed || !splits || !bytes) return STREAMKL_ERR_INVALID;
+  *packed = *splits = 0;
+  *bytes = 0;
+  if (p.NQ == 0 || p.NK == 0) return STREAMKL_OK;
+  if (num_sms <= 0 && (v = device_sms(&num_sms)) != STREAMKL_OK) return v;
+  attn_fwd_plan(&p, num_sms);
+  *packed = p.packed;
+  *splits = p.splits;
+  *bytes = attn_fwd_workspace(p);
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_diff_attn_fwd_workspace(streamkl_diff_attn_shape s, size_t* bytes) {
+  int packed, splits;
+  return streamkl_diff_attn_fwd_plan(s, 0, &packed, &splits, bytes);
+}
+
+streamkl_status streamkl_diff_attn_fwd(const void* q, const void* k, const void* v, streamkl_diff_attn_shape s, void* d,
+                                       void* maps, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  AttnProblem p;
+  streamkl_status st = diff_problem(s, &p);
+  if (st != STREAMKL_OK || p.NQ == 0) return st;
+  if (!d || !aligned16(d) || !rows_ok(lse) || !aligned16(maps) || !maps != !p.o_rest) return STREAMKL_ERR_INVALID;
+  if (p.NK > 0) {
+    if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v) || !p.lam) return STREAMKL_ERR_INVALID;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+    attn_fwd_plan(&p, sms);
+    const size_t need = attn_fwd_workspace(p);
+    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return STREAMKL_ERR_WORKSPACE;
+  }
+  int* status = nullptr;
+  if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
+  return from_cuda(launch_attn_fwd(p, q, k, v, maps, lse, workspace, status, static_cast<cudaStream_t>(stream), d));
+}
+
+streamkl_status streamkl_diff_attn_bwd_workspace(streamkl_diff_attn_shape s, int bwd_mode, size_t* bytes) {
+  AttnProblem p;
+  streamkl_status v = diff_problem(s, &p);
+  if (v != STREAMKL_OK) return v;
+  if (!attn_mode_ok(bwd_mode) || !bytes) return STREAMKL_ERR_INVALID;
+  if (bwd_mode == STREAMKL_BWD_FUSED && !attn_bwd_has_fused(p)) return STREAMKL_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
+  *bytes = attn_bwd_scratch(p, attn_bwd_plan(p, bwd_mode, sms), nullptr).bytes;
+  return STREAMKL_OK;
+}
+
+streamkl_status streamkl_diff_attn_bwd(const void* q, const void* k, const void* v, const void* maps, const float* lse,
+                                       const void* go, const float* dlse, streamkl_diff_attn_shape s, void* dq, void* dk, void* dv,
+                                       float* dlam, int bwd_mode, void* workspace, size_t workspace_bytes, void* stream) {
+  AttnProblem p;
+  streamkl_status st = diff_problem(s, &p);
+  if (st != STREAMKL_OK) return st;
+  if (!attn_mode_ok(bwd_mode)) return STREAMKL_ERR_INVALID;
+  if (bwd_mode == STREAMKL_BWD_FUSED && !attn_bwd_has_fused(p)) return STREAMKL_ERR_UNSUPPORTED;
+  if (p.NQ > 0 && (!dq || !aligned16(dq) || !rows_ok(dlam))) return STREAMKL_ERR_INVALID;
+  if (p.NK > 0 && (!dk || !dv || !aligned16(dk) || !aligned16(dv))) return STREAMKL_ERR_INVALID;
+  AttnBwdPlan plan{};
+  if (p.NQ > 0 && p.NK > 0) {
+    if (!q || !k || !v || !maps || !p.o_rest || !go || !p.lam || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(maps) || !aligned16(go) || !rows_ok(lse) || !aligned_to_or_null(dlse, 4))
+      return STREAMKL_ERR_INVALID;
+    // no plan needs less than the rows' values
+    if (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)p.rows * 32) return STREAMKL_ERR_WORKSPACE;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != STREAMKL_OK) return st;
+    plan = attn_bwd_plan(p, bwd_mode, sms);
+    if (workspace_bytes < attn_bwd_scratch(p, plan, workspace).bytes) return STREAMKL_ERR_WORKSPACE;
+  }
+  int* status = nullptr;
+  if ((st = status_ptr(&status)) != STREAMKL_OK) return st;
+  return from_cuda(launch_attn_bwd(p, plan, AttnBwdIn{q, k, v, maps, nullptr, p.o_rest, lse, dlse, go, dlam}, dq, dk, dv,
+                                   workspace, status, static_cast<cudaStream_t>(stream)));
 }
 
 static streamkl_status logprobs_problem(int dtype, long long rows, long long vocab, long long row_stride,

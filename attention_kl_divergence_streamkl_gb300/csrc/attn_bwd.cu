@@ -264,6 +264,83 @@ __global__ void __launch_bounds__(256, KIND == kRowsShort ? 3 : 4)
 }
 
 // ---------------------------------------------------------------------------
+// Row values of a difference of two maps, O = O1 - lam O2, for rows of both: what reaches the maps is dO and -lam dO.  The
+// second is rounded to bf16, half a step, as dO itself was where it came from, and goes to the workspace with dO beside it;
+// both deltas are taken from what is stored there and from both parts of the maps' results, dlam = -dO . O2 before the
+// rounding.  Bound by memory: five rows read, two written.
+constexpr int kDiffRowsEach = 2;
+template <int D>
+__global__ void __launch_bounds__(256)
+    attn_diff_rows_kernel(const AttnProblem p, const AttnBwdIn in, uint4* __restrict__ row_s, uint4* __restrict__ row_d,
+                          uint4* __restrict__ go, float4* __restrict__ acc, unsigned* __restrict__ counters,
+                          unsigned n_counters, int padded) {
+  constexpr int LANES = D / 8, ROWS = 256 / LANES;
+  static_assert(BT % (ROWS * kDiffRowsEach) == 0, "a block's rows are one head's");
+  for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
+  const int step = padded / kDiffRowsEach;
+  const unsigned per_head = (unsigned)step / ROWS;
+  const int bp = (int)(blockIdx.x / per_head);
+  const int b = bp / (p.H / 2), pair = bp % (p.H / 2);
+  const int n0 = (int)(blockIdx.x % per_head) * ROWS + threadIdx.x / LANES;
+  const int lane = threadIdx.x % LANES;
+  const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
+  auto seen = [&](int n) { return n < ql && (p.causal ? min(kl, n + kl - ql + 1) : kl) > 0; };
+  const auto* d_out = static_cast<const __nv_bfloat16*>(in.ddiff) + b * p.cs_b + pair * p.cs_h + lane * 8;
+  const long long first = b * p.os_b + 2 * pair * p.os_h + lane * 8;
+  const auto *o = static_cast<const __nv_bfloat16*>(in.o) + first, *rest = static_cast<const __nv_bfloat16*>(in.o_rest) + first;
+  const float* lam = p.lam + b * p.ls_b + pair * p.ls_h;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 g[kDiffRowsEach], x[kDiffRowsEach][2], y[kDiffRowsEach][2];
+  float w[kDiffRowsEach];
+#pragma unroll
+  for (int u = 0; u < kDiffRowsEach; ++u) {
+    const int n = n0 + u * step;
+    const bool there = seen(n);
+    g[u] = there ? *reinterpret_cast<const uint4*>(d_out + n * p.cs_n) : none;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      x[u][t] = there ? *reinterpret_cast<const uint4*>(o + t * p.os_h + n * p.os_n) : none;
+      y[u][t] = there ? *reinterpret_cast<const uint4*>(rest + t * p.os_h + n * p.os_n) : none;
+    }
+    w[u] = there ? -lam[n * p.ls_n] : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kDiffRowsEach; ++u) {
+    const int n = n0 + u * step;
+    const bool there = seen(n);
+    const uint32_t gs[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+    uint32_t hs[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = from_bf16_pair(gs[i]);
+      hs[i] = there ? pack_bf16(v.x * w[u], v.y * w[u]) : 0u;
+    }
+    const uint4 h = make_uint4(hs[0], hs[1], hs[2], hs[3]);
+    float sums[4] = {dot8(x[u][0], g[u], dot8(y[u][0], g[u], 0.f)), dot8(x[u][1], h, dot8(y[u][1], h, 0.f)),
+                     dot8(x[u][1], g[u], dot8(y[u][1], g[u], 0.f)), 0.f};
+    lane_totals<LANES>(sums, lane);
+    const int own = lane_index<4>(lane);  // of the first four lanes: the two maps' deltas, dlam, nothing
+    if (lane < 4 && own < 2) {
+      const long long bh = (long long)b * p.H + 2 * pair + own;
+      const float l = there ? in.lse[bh * p.NQ + n] : kNegInf, dl = there && in.dlse ? in.dlse[bh * p.NQ + n] : 0.f;
+      row_s[bh * padded + n] = three_bf16(l == kNegInf ? kNoRow : -l * (1.f / p.scale));
+      row_d[bh * padded + n] = three_bf16(l == kNegInf ? 0.f : dl - sums[0]);
+    }
+    if (lane < 4 && own == 2 && n < p.NQ) in.dlam[(long long)bp * p.NQ + n] = there ? -sums[0] : 0.f;
+    const long long at = ((long long)b * p.H + 2 * pair) * p.NQ + n;
+    if (n < p.NQ) {
+      go[at * LANES + lane] = g[u];
+      go[(at + p.NQ) * LANES + lane] = h;
+    }
+    if (acc) {  // the fused kernel's accumulator starts at zero
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        acc[((2ll * bp + t / 2) * padded + n) * (D / 4) + (t & 1) * LANES + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // dK/dV block.  The logits are computed transposed, so the TMEM lanes are keys
 // and the columns queries: S^T = K Q^T and dP^T = V dO^T (both operands K-major
 // in shared memory).  P^T and dS^T (bf16 pairs) overwrite their logits and are
@@ -948,7 +1025,7 @@ __global__ void attn_zero_rows_kernel(__nv_bfloat16* dst, int H, int rows, int D
 }
 
 template <int D>
-cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk, void* dv,
+cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, AttnBwdIn in, void* dq, void* dk, void* dv,
                      void* workspace, int* status, cudaStream_t st) {
   const AttnBwdScratch w = attn_bwd_scratch(p, plan, workspace);
   const long long rows = (long long)p.B * p.H * w.padded;
@@ -957,8 +1034,16 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBw
   const auto rows_kern = in.o_rest            ? attn_rows_kernel<D, kRowsRest>
                          : p.NK <= kShortKeys ? attn_rows_kernel<D, kRowsShort>
                                               : attn_rows_kernel<D, kRowsLong>;
-  rows_kern<<<(unsigned)(rows / per_block), 256, 0, st>>>(p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc),
-                                                         w.kv_counters, w.n_counters, w.padded);
+  if (p.diff) {
+    constexpr int each = 256 / (D / 8) * kDiffRowsEach;
+    attn_diff_rows_kernel<D><<<(unsigned)(rows / 2 / each), 256, 0, st>>>(p, in, row_s, row_d, static_cast<uint4*>(w.go),
+                                                                        reinterpret_cast<float4*>(w.acc), w.kv_counters,
+                                                                        w.n_counters, w.padded);
+    in.go = w.go;
+  } else {
+    rows_kern<<<(unsigned)(rows / per_block), 256, 0, st>>>(p, in, row_s, row_d, reinterpret_cast<float4*>(w.acc),
+                                                           w.kv_counters, w.n_counters, w.padded);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (plan.fused) return launch_attn_bwd_fused(p, plan, in, dq, dk, dv, w, status, st);
@@ -970,7 +1055,7 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBw
     return encode_tile_map(map, x, p.D, p.NK, p.HK, p.B, sn, sh, sb, BT);
   };
   if (!q_map(&m.q, in.q, p.qs_n, p.qs_h, p.qs_b) || !k_map(&m.k, in.k, p.ks_n, p.ks_h, p.ks_b) ||
-      !k_map(&m.v, in.v, p.vs_n, p.vs_h, p.vs_b) || !q_map(&m.go, in.go, p.os_n, p.os_h, p.os_b) ||
+      !k_map(&m.v, in.v, p.vs_n, p.vs_h, p.vs_b) || !q_map(&m.go, in.go, p.gs_n, p.gs_h, p.gs_b) ||
       !q_map(&m.dq, dq, p.qs_n, p.qs_h, p.qs_b) || !k_map(&m.dk, dk, p.ks_n, p.ks_h, p.ks_b) ||
       !k_map(&m.dv, dv, p.vs_n, p.vs_h, p.vs_b))
     return cudaErrorInvalidValue;
@@ -1081,6 +1166,7 @@ AttnBwdScratch attn_bwd_scratch(const AttnProblem& p, const AttnBwdPlan& plan, v
   if (plan.fused) w.acc = static_cast<float*>(take(rows * p.D * sizeof(float)));
   w.kv_parts = take(kv_split * plan.kv_parts * 2 * p.D * BT * sizeof(float));
   w.q_parts = take(q_split * plan.q_parts * p.D * BT * sizeof(float));
+  if (p.diff) w.go = take((size_t)p.rows * p.D * 2);
   w.n_counters = (unsigned)(kv_split + q_split);
   w.kv_counters = static_cast<unsigned*>(take(w.n_counters * sizeof(unsigned)));
   w.q_counters = w.kv_counters + kv_split;
@@ -1090,6 +1176,10 @@ AttnBwdScratch attn_bwd_scratch(const AttnProblem& p, const AttnBwdPlan& plan, v
 cudaError_t launch_attn_bwd(const AttnProblem& p, const AttnBwdPlan& plan, const AttnBwdIn& in, void* dq, void* dk,
                             void* dv, void* workspace, int* status, cudaStream_t st) {
   if (p.NQ == 0 || p.NK == 0) {
+    if (p.diff && p.NQ > 0) {
+      const cudaError_t e = cudaMemsetAsync(in.dlam, 0, (size_t)p.rows / 2 * sizeof(float), st);
+      if (e != cudaSuccess) return e;
+    }
     auto* q = static_cast<__nv_bfloat16*>(dq);
     auto* k = static_cast<__nv_bfloat16*>(dk);
     auto* v = static_cast<__nv_bfloat16*>(dv);

@@ -487,7 +487,7 @@ cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdPlan& plan,
   if (!encode_tile_map(&m.q, in.q, D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, BT) ||
       !encode_tile_map(&m.k, in.k, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
       !encode_tile_map(&m.v, in.v, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
-      !encode_tile_map(&m.go, in.go, D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, BT) ||
+      !encode_tile_map(&m.go, in.go, D, p.NQ, p.H, p.B, p.gs_n, p.gs_h, p.gs_b, BT) ||
       !encode_tile_map(&m.dk, dk, D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BT) ||
       !encode_tile_map(&m.dv, dv, D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BT) ||
       !encode_rows_f32_map(&m.acc, w.acc, D, w.padded, p.B * p.H, 32, 32))

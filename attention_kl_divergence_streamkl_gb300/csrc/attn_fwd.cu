@@ -120,13 +120,16 @@ __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32
 // block's first tile; in the loop of a long stream the test costs more (D 64: N1024 causal 24.5 -> 23.4 us, one token and
 // 129 keys 7.3 -> 6.8; N8192 518 -> 542).
 // REST: the part of O that its rounding leaves is stored too.
-template <int D, bool FRESH, bool REST>
+// DIFF: heads 2 i and 2 i + 1 are the two maps of a difference.  A block's tiles are then the same 128 rows of both, so that
+// they share K and V and the difference is formed at the end, in fp32, from both accumulators (the second's through shared
+// memory); where heads are packed both maps' rows lie in the tile.  Without REST only the difference leaves the SM.
+template <int D, bool FRESH, bool REST, bool DIFF>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_fwd_kernel(const AttnProblem p, float* __restrict__ out_lse,
                     float* __restrict__ part_o, float2* __restrict__ part_ml, int* status,
                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
-                    const __grid_constant__ CUtensorMap mrest) {
+                    const __grid_constant__ CUtensorMap mrest, const __grid_constant__ CUtensorMap mdiff) {
   using L = Smem<D>;
   constexpr int SLOTS = L::SLOTS, S_BUFS = L::S_BUFS;
   constexpr uint32_t kColO = 128 * S_BUFS;  // O_B follows O_A; S buffer i at 128 i
@@ -149,12 +152,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   const unsigned x = p.by_items.div(item), y = item - x * p.by_items.d;
   const int qt = p.q_items - 1 - (int)(p.longest_first ? x : y), bh = (int)(p.longest_first ? y : x);
-  const int heads = p.packed ? p.HK : p.H;
-  const int b = (int)p.by_heads.div(bh), hx = bh - b * heads;  // hx: key head when packed, else query head
+  const int heads = p.packed ? p.HK : DIFF ? p.H / 2 : p.H;
+  const int b = (int)p.by_heads.div(bh), hx = bh - b * heads;  // hx: key head when packed, else query head (or pair of heads)
   const int hk = p.packed ? hx : (int)p.by_group.div(hx);
   const int ql = seq_len(p.q_lens, b, p.NQ), kl = seq_len(p.k_lens, b, p.NK);
   const int off = kl - ql;
-  const int q0 = qt * 2 * BM;
+  const int q0 = DIFF ? qt * BM : qt * 2 * BM;
+  auto first_row = [&](int t) { return DIFF ? q0 : q0 + t * BM; };   // of tile t, unless packed
+  auto head_of = [&](int t) { return DIFF ? 2 * hx + t : hx; };
   // key tiles of query tile t within this split
   auto key_tiles = [&](int t) {
     int last;  // last query of the tile
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (t) return 0;
       last = ql - 1;
     } else {
-      const int first = q0 + t * BM;
+      const int first = first_row(t);
       if (first >= ql) return 0;
       last = min(first + BM, ql) - 1;
     }
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto pair_of = [&](int t, int i) { return i < both ? 2 * i + t : both + i; };
   auto buf_of = [&](int t, int i) { return S_BUFS == 2 ? t : pair_of(t, i) % 3; };       // its S buffer,
   auto use_of = [&](int t, int i) { return S_BUFS == 2 ? i : pair_of(t, i) / 3; };       // and how often it was used before
-  const bool has_b = !p.packed && q0 + BM < p.NQ;
+  const bool has_b = !p.packed && (DIFF || q0 + BM < p.NQ);
   // the V tile that a sequence ends inside: its rows past the end may hold anything, and 0 * NaN is NaN
   const int patch_i = (kl < p.NK && (kl & (BN - 1))) ? (kl / BN) - kt0 : -1;
 
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
             tma_load_4d(sb + L::OFF_Q + t * L::TILE + h * BM * 128, &mq, q_full + 8 * t, h * 64,
-                        p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+                        p.packed ? 0 : first_row(t), p.packed ? hk * p.G : head_of(t), b);
           if (t == 0 || nA == 0) load_kv(0);
         }
         for (int u = 1; u < min(SLOTS, 2 * n); ++u) load_kv(u);
@@ -348,8 +353,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int r = wq * 32 + lane;
     const int nt = t ? nB : nA;
     const int g = p.packed ? r / p.NQ : 0;
-    const int qn = p.packed ? r - g * p.NQ : q0 + t * BM + r;  // query position of this row
-    const int h = p.packed ? hk * p.G + g : hx;
+    const int qn = p.packed ? r - g * p.NQ : first_row(t) + r;  // query position of this row
+    const int h = p.packed ? hk * p.G + g : head_of(t);
     const bool real = p.packed ? (t == 0 && g < p.G) : (qn < p.NQ);
     const int row_end = (real && qn < ql) ? (p.causal ? min(kl, qn + off + 1) : kl) : 0;  // keys this row sees
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
@@ -466,7 +471,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int k = 0; k < 32; ++k) o[k] = 0;
           }
           if (p.splits == 1) {
-            stage_row32(sb + L::OFF_Q + t * L::TILE, r, d, o, f);  // Q's products are done
+            if (!DIFF || REST)
+              stage_row32(sb + L::OFF_Q + t * L::TILE, r, d, o, f);  // Q's products are done
           } else {
             // through the warp's share of the Q tile: eight lanes write a row's 128 bytes (a lane that writes its own row
             // scatters every store over 32 lines: 6400 cycles a 128 x 128 tile)
@@ -496,9 +502,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // every warp of the tile comes here; one that gave up makes none of them store
       const bool store = !named_bar_any(1 + t, SOFTMAX_WARPS / 2 * 32, !ok) && p.splits == 1;
-      if (store && wq == 0) {
+      if (store && wq == 0 && (!DIFF || REST)) {
         if (elect_one())
-          store_tile<D>(&mo, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+          store_tile<D>(&mo, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : first_row(t), p.packed ? hk * p.G : head_of(t), b);
         __syncwarp();
       }
       if (REST && store) {  // the rest through the same tile, once the copy has read it
@@ -523,8 +529,72 @@ __global__ void __launch_bounds__(THREADS, 1)
         named_bar_sync(1 + t, SOFTMAX_WARPS / 2 * 32);
         if (wq == 0) {
           if (elect_one())
-            store_tile<D>(&mrest, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : q0 + t * BM, p.packed ? hk * p.G : hx, b);
+            store_tile<D>(&mrest, sb + L::OFF_Q + t * L::TILE, p.packed ? 0 : first_row(t), p.packed ? hk * p.G : head_of(t), b);
           __syncwarp();
+        }
+      }
+      if constexpr (DIFF) {
+        // the second map's rows go through the ring's memory, whose tiles have all been used
+        const int threads = p.packed ? SOFTMAX_WARPS / 2 * 32 : SOFTMAX_WARPS * 32;
+        if (p.splits == 1 && !named_bar_any(3, threads, !ok)) {
+          const bool none = !(l > 0.f) && !nan;
+          const bool second = p.packed ? g & 1 : t;
+          const uint32_t ring = sb + L::OFF_KV;
+          auto at = [&](int y, int v) { return ring + (uint32_t)(y * (D * 4) + ((v ^ (y & 7)) << 4)); };  // 16 bytes v of row y
+          auto load = [&](int d, uint32_t (&o)[32]) {
+            __syncwarp();
+            if (nt > 0) {
+              tmem_ld32(to + d, o);
+              tmem_ld_wait();
+              reg_fence32(o);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
+          };
+          if (p.packed || t == 1) {
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              load(d, o);
+              if (second && real) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  st_shared16(at(r, d / 4 + k), make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+              }
+            }
+          }
+          __syncwarp();
+          named_bar_sync(3, threads);
+          if (t == 0) {
+            const bool mine = !second && real;
+            // (a row without keys is 0, whatever stands beside it)
+            const float lam = mine && !none ? p.lam[(long long)b * p.ls_b + (long long)(h / 2) * p.ls_h + (long long)qn * p.ls_n] : 0.f;
+            const int other = p.packed ? r + p.NQ : r, out_row = p.packed ? g / 2 * p.NQ + qn : r;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              load(d, o);
+              if (mine) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint4 x = ld_shared16(at(other, d / 4 + k));
+                  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    o[4 * k + e] = __float_as_uint(fmaf(-lam, __uint_as_float(xs[e]), __uint_as_float(o[4 * k + e])));
+                }
+                stage_row32(sb + L::OFF_Q, out_row, d, o, 1.f);
+              }
+            }
+            fence_async_smem();
+            __syncwarp();
+            named_bar_sync(1, SOFTMAX_WARPS / 2 * 32);
+            if (wq == 0) {
+              if (elect_one())
+                store_tile<D>(&mdiff, sb + L::OFF_Q, p.packed ? 0 : q0, p.packed ? hk * (p.G / 2) : hx, b);
+              __syncwarp();
+            }
+          }
         }
       }
     }
@@ -542,25 +612,31 @@ __global__ void __launch_bounds__(THREADS, 1)
 // with one split after the other took 16 us for 19 splits, this 4).
 constexpr int kMergeWarps = 8, kMergeAhead = 2;
 constexpr int kMaxSplits = 1024;  // the plan makes at most four blocks an SM
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32)
+// DIFF: a block has a row of both maps, eight warps to each, and writes their difference too (and `out`, unless null).
+template <int D, bool DIFF>
+__global__ void __launch_bounds__(kMergeWarps * 32 * (DIFF ? 2 : 1))
     attn_merge_kernel(const AttnProblem p, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                      __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse) {
+                      __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse, __nv_bfloat16* __restrict__ diff) {
   constexpr int W = D / 32;  // columns of a lane
+  constexpr int MAPS = DIFF ? 2 : 1;
   struct alignas(W * 4) Cols {
     float x[W];
   };
-  __shared__ float weight[kMaxSplits], warp_m[kMergeWarps], warp_l[kMergeWarps];
-  __shared__ Cols sums[kMergeWarps][32];
-  const long long row = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float weights[MAPS][kMaxSplits], warps_m[MAPS][kMergeWarps], warps_l[MAPS][kMergeWarps];
+  __shared__ Cols all_sums[MAPS][kMergeWarps][32];
+  const int map = DIFF ? threadIdx.x / (kMergeWarps * 32) : 0, thread = threadIdx.x - map * (kMergeWarps * 32);
+  const int lane = thread & 31, warp = thread >> 5;
+  const long long n = DIFF ? blockIdx.x % p.NQ : 0;
+  const long long row = DIFF ? (2 * (blockIdx.x / (long long)p.NQ) + map) * p.NQ + n : blockIdx.x;
+  float *weight = weights[map], *warp_m = warps_m[map], *warp_l = warps_l[map];
+  Cols(*sums)[32] = all_sums[map];
   auto load = [&](int s) { return *(reinterpret_cast<const Cols*>(part_o + ((size_t)s * p.rows + row) * D) + lane); };
   Cols first[kMergeAhead];
 #pragma unroll
   for (int k = 0; k < kMergeAhead; ++k)
     if (warp + k * kMergeWarps < p.splits) first[k] = load(warp + k * kMergeWarps);
   float m = kNegInf;
-  for (int s = threadIdx.x; s < p.splits; s += kMergeWarps * 32) m = fmaxf(m, part_ml[(size_t)s * p.rows + row].x);
+  for (int s = thread; s < p.splits; s += kMergeWarps * 32) m = fmaxf(m, part_ml[(size_t)s * p.rows + row].x);
 #pragma unroll
   for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
   if (lane == 0) warp_m[warp] = m;
@@ -568,7 +644,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, warp_m[w]);
   float l = 0.f;
-  for (int s = threadIdx.x; s < p.splits; s += kMergeWarps * 32) {
+  for (int s = thread; s < p.splits; s += kMergeWarps * 32) {
     const float2 ml = part_ml[(size_t)s * p.rows + row];
     const bool none = ml.x == kNegInf && ml.y == 0.f;  // this split has no key for the row
     const float w = none ? 0.f : ml.x == m ? 1.f : ex2(ml.x - m);
@@ -594,16 +670,40 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   sums[warp][lane] = o;
   __syncthreads();
   const bool none = l == 0.f;
-  if (threadIdx.x == 0) out_lse[row] = none ? kNegInf : (m + log2f(l)) * kLn2;
-  if (warp != 0) return;
+  if (thread == 0) out_lse[row] = none ? kNegInf : (m + log2f(l)) * kLn2;
+  if (!DIFF && warp != 0) return;
+  if (warp == 0) {
 #pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) {
-    const Cols x = sums[w][lane];
+    for (int w = 1; w < kMergeWarps; ++w) {
+      const Cols x = sums[w][lane];
 #pragma unroll
-    for (int i = 0; i < W; ++i) o.x[i] += x.x[i];
+      for (int i = 0; i < W; ++i) o.x[i] += x.x[i];
+    }
   }
   const float inv = none ? 0.f : 1.f / l;
   const long long bh = row / p.NQ;
+  if constexpr (DIFF) {
+    if (map == 1 && warp == 0) {
+      Cols x{};
+#pragma unroll
+      for (int i = 0; i < W; ++i) x.x[i] = o.x[i] * inv;
+      all_sums[1][0][lane] = x;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    if (map == 0) {
+      const long long b = bh / p.H, h = bh % p.H / 2;
+      const float lam = none ? 0.f : p.lam[b * p.ls_b + h * p.ls_h + n * p.ls_n];  // a row without keys is 0
+      const Cols y = all_sums[1][0][lane];
+      float d[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) d[i] = none ? 0.f : fmaf(-lam, y.x[i], o.x[i] * inv);
+#pragma unroll
+      for (int k = 0; k < W; k += 2)
+        *reinterpret_cast<uint32_t*>(diff + b * p.cs_b + h * p.cs_h + n * p.cs_n + lane * W + k) = pack_bf16(d[k], d[k + 1]);
+    }
+    if (!out) return;
+  }
   const long long at = (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + lane * W;
 #pragma unroll
   for (int k = 0; k < W; k += 2) *reinterpret_cast<uint32_t*>(out + at + k) = pack_bf16(o.x[k] * inv, o.x[k + 1] * inv);
@@ -615,39 +715,43 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
 }
 
-template <int D>
-cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
+template <int D, bool DIFF>
+cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse, void* diff,
                      void* workspace, int* status, cudaStream_t st) {
-  CUtensorMap mq, mk, mv, mo, mrest{};
+  CUtensorMap mq, mk, mv, mo{}, mrest{}, mdiff{};
   if (!encode_tile_map(&mq, q, p.D, p.NQ, p.H, p.B, p.qs_n, p.qs_h, p.qs_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1) ||
       !encode_tile_map(&mk, k, p.D, p.NK, p.HK, p.B, p.ks_n, p.ks_h, p.ks_b, BN) ||
       !encode_tile_map(&mv, v, p.D, p.NK, p.HK, p.B, p.vs_n, p.vs_h, p.vs_b, BN) ||
-      !encode_tile_map(&mo, o, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1) ||
+      (o && !encode_tile_map(&mo, o, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM, p.packed ? p.G : 1)) ||
+      (DIFF && !encode_tile_map(&mdiff, diff, p.D, p.NQ, p.H / 2, p.B, p.cs_n, p.cs_h, p.cs_b, p.packed ? p.NQ : BM,
+                                p.packed ? p.G / 2 : 1)) ||
       (p.o_rest && !encode_tile_map(&mrest, p.o_rest, p.D, p.NQ, p.H, p.B, p.os_n, p.os_h, p.os_b, p.packed ? p.NQ : BM,
                                     p.packed ? p.G : 1)))
     return cudaErrorInvalidValue;
   constexpr int smem = kWholeSmSmem;
   const bool fresh = D == 64 && ((p.NK + BN - 1) / BN + p.splits - 1) / p.splits <= kFreshTiles;
-  const auto kern = p.o_rest ? (fresh ? attn_fwd_kernel<D, D == 64, true> : attn_fwd_kernel<D, false, true>)
-                             : (fresh ? attn_fwd_kernel<D, D == 64, false> : attn_fwd_kernel<D, false, false>);
+  const auto kern = p.o_rest ? (fresh ? attn_fwd_kernel<D, D == 64, true, DIFF> : attn_fwd_kernel<D, false, true, DIFF>)
+                             : (fresh ? attn_fwd_kernel<D, D == 64, false, DIFF> : attn_fwd_kernel<D, false, false, DIFF>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   float* part_o = static_cast<float*>(workspace);
   float2* part_ml = p.splits > 1 ? reinterpret_cast<float2*>(part_o + (size_t)p.splits * p.rows * D) : nullptr;
   auto* out = static_cast<__nv_bfloat16*>(o);
   const long long blocks = attn_fwd_items(p) * p.splits;
-  kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo, mrest);
+  kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo, mrest, mdiff);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  attn_merge_kernel<D><<<(unsigned)p.rows, kMergeWarps * 32, 0, st>>>(p, part_o, part_ml, out, lse);
+  attn_merge_kernel<D, DIFF><<<(unsigned)(DIFF ? p.rows / 2 : p.rows), kMergeWarps * 32 * (DIFF ? 2 : 1), 0, st>>>(
+      p, part_o, part_ml, out, lse, static_cast<__nv_bfloat16*>(diff));
   return cudaGetLastError();
 }
 
 // No keys at all: O = 0, LSE = -inf.
-__global__ void attn_no_keys_kernel(const AttnProblem p, __nv_bfloat16* out, float* lse) {
+__global__ void attn_no_keys_kernel(const AttnProblem p, __nv_bfloat16* out, float* lse, __nv_bfloat16* diff) {
   const long long row = blockIdx.x;
-  const long long bh = row / p.NQ;
-  const long long at = (bh / p.H) * p.os_b + (bh % p.H) * p.os_h + (row % p.NQ) * p.os_n + threadIdx.x;
-  out[at] = __float2bfloat16_rn(0.f);
+  const long long bh = row / p.NQ, b = bh / p.H, h = bh % p.H;
+  const long long at = b * p.os_b + h * p.os_h + (row % p.NQ) * p.os_n + threadIdx.x;
+  if (out) out[at] = __float2bfloat16_rn(0.f);
+  if (diff && h % 2 == 0) diff[b * p.cs_b + h / 2 * p.cs_h + (row % p.NQ) * p.cs_n + threadIdx.x] = __float2bfloat16_rn(0.f);
   if (p.o_rest) static_cast<__nv_bfloat16*>(p.o_rest)[at] = __float2bfloat16_rn(0.f);
   if (threadIdx.x == 0) lse[row] = kNegInf;
 }
@@ -655,7 +759,7 @@ __global__ void attn_no_keys_kernel(const AttnProblem p, __nv_bfloat16* out, flo
 }  // namespace
 
 long long attn_fwd_items(const AttnProblem& p) {
-  return (long long)p.B * (p.packed ? p.HK : p.H) * p.q_items;
+  return (long long)p.B * (p.packed ? p.HK : p.diff ? p.H / 2 : p.H) * p.q_items;
 }
 
 // In times of a key tile (1.5 us where a block has one tile of rows, and its K and V are new): setting a block up and
@@ -667,7 +771,8 @@ constexpr double kBlockCost = 3.0, kMergeCost = 2.5, kMergedPerTile = 1.5e6;
 constexpr int kSmallGrid = 6;
 void attn_fwd_plan(AttnProblem* p, int num_sms) {
   p->packed = (long long)p->G * p->NQ <= BM;
-  p->q_items = p->packed ? 1 : (p->NQ + 2 * BM - 1) / (2 * BM);
+  const int rows = p->diff ? BM : 2 * BM;  // of a block's two tiles
+  p->q_items = p->packed ? 1 : (p->NQ + rows - 1) / rows;
   p->rows = (long long)p->B * p->H * p->NQ;
   const long long items = attn_fwd_items(*p);
   const int tiles = (p->NK + BN - 1) / BN;
@@ -685,11 +790,11 @@ void attn_fwd_plan(AttnProblem* p, int num_sms) {
   p->splits = best;
   // in a grid of few waves the order of lengths counts for more than the L2 (whose reuse a head-major order is for)
   p->longest_first = items * best <= kSmallGrid * num_sms;
-  const unsigned heads = p->packed ? p->HK : p->H;
+  const unsigned heads = p->packed ? p->HK : p->diff ? p->H / 2 : p->H;
   p->by_splits = FastDiv((unsigned)p->splits);
   p->by_items = FastDiv(p->longest_first ? p->B * heads : (unsigned)p->q_items);
   p->by_heads = FastDiv(heads);
-  p->by_group = FastDiv((unsigned)p->G);
+  p->by_group = FastDiv((unsigned)(p->diff ? p->G / 2 : p->G));
 }
 
 size_t attn_fwd_workspace(const AttnProblem& p) {
@@ -697,13 +802,18 @@ size_t attn_fwd_workspace(const AttnProblem& p) {
 }
 
 cudaError_t launch_attn_fwd(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
-                            void* workspace, int* status, cudaStream_t st) {
+                            void* workspace, int* status, cudaStream_t st, void* diff) {
   if (p.NK == 0) {
-    attn_no_keys_kernel<<<(unsigned)p.rows, p.D, 0, st>>>(p, static_cast<__nv_bfloat16*>(o), lse);
+    attn_no_keys_kernel<<<(unsigned)p.rows, p.D, 0, st>>>(p, static_cast<__nv_bfloat16*>(o), lse,
+                                                         static_cast<__nv_bfloat16*>(diff));
     return cudaGetLastError();
   }
-  if (p.D == 64) return launch_d<64>(p, q, k, v, o, lse, workspace, status, st);
-  return launch_d<128>(p, q, k, v, o, lse, workspace, status, st);
+  if (p.diff) {
+    if (p.D == 64) return launch_d<64, true>(p, q, k, v, o, lse, diff, workspace, status, st);
+    return launch_d<128, true>(p, q, k, v, o, lse, diff, workspace, status, st);
+  }
+  if (p.D == 64) return launch_d<64, false>(p, q, k, v, o, lse, nullptr, workspace, status, st);
+  return launch_d<128, false>(p, q, k, v, o, lse, nullptr, workspace, status, st);
 }
 
 }  // namespace skl

@@ -119,6 +119,12 @@ struct AttnProblem {
   const int *q_lens, *k_lens;  // device, [B], or null: every sequence has N_Q queries, N_K keys
   // element strides along b, h, n of q (and dq), k (dk), v (dv), o (and do)
   long long qs_b, qs_h, qs_n, ks_b, ks_h, ks_n, vs_b, vs_h, vs_n, os_b, os_h, os_n;
+  long long gs_b, gs_h, gs_n;  // of do, in the backward's products
+  // a difference of two maps: heads 2 i and 2 i + 1 of q, o, lse and their gradients are its maps
+  int diff;
+  const float* lam;            // the second map's weight, fp32 by (b, pair of heads, n) with strides that may be 0
+  long long ls_b, ls_h, ls_n;
+  long long cs_b, cs_h, cs_n;  // strides of the difference, [B, H / 2, N_Q, D], and of its gradient
   long long rows;              // B H N_Q
   void* o_rest;                // null, or what rounding O to bf16 left, with O's strides: the forward writes it
   // forward plan (attn_fwd_plan)
@@ -131,13 +137,16 @@ struct AttnProblem {
 void attn_fwd_plan(AttnProblem* p, int num_sms);
 long long attn_fwd_items(const AttnProblem& p);
 size_t attn_fwd_workspace(const AttnProblem& p);  // bytes, 0 without splits
+// diff: the difference's result, where p.diff (o, each map's own, is then null unless p.o_rest is wanted too)
 cudaError_t launch_attn_fwd(const AttnProblem& p, const void* q, const void* k, const void* v, void* o, float* lse,
-                            void* workspace, int* status, cudaStream_t st);
+                            void* workspace, int* status, cudaStream_t st, void* diff = nullptr);
 
 struct AttnBwdIn {
   const void *q, *k, *v, *o, *go;  // go = dO, with o's strides
   const void* o_rest;              // null, or the forward's
   const float *lse, *dlse;         // dlse may be null
+  const void* ddiff;               // a difference's gradient (go is then null), and where that of its weights goes
+  float* dlam;
 };
 // How a backward runs on a device (a pure rule of sizes).  Tiles [0, whole) of a kind are one block each, the later ones
 // `parts` blocks.  Fused: one visit of each tile pair by the kv blocks, dQ added up in an fp32 accumulator.
@@ -159,6 +168,7 @@ struct AttnBwdScratch {
   void *kv_parts, *q_parts;
   unsigned *kv_counters, *q_counters;
   unsigned n_counters;    // of both, one after the other
+  void* go;               // a difference: what reaches each map, bf16 [B, H, N_Q, D]
   size_t bytes;
 };
 bool attn_bwd_has_fused(const AttnProblem& p);

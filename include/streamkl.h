@@ -378,6 +378,47 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
                                   void* dv, int bwd_mode, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Differential attention: the difference of two softmax maps over the same keys and
+ * values, with a learned weight,
+ *     O = softmax(scale Q1 K^T) V - lam softmax(scale Q2 K^T) V,
+ * and its backward, dlam included.
+ *
+ * s.maps describes both maps as streamkl_attn_fwd does its attention: H counts the query
+ *   heads of both, heads 2 i and 2 i + 1 of q are the maps of difference i, and H / 2 is a
+ *   multiple of HK; lengths, causal, scale and strides as there.  lse [B, H, N_Q] has both
+ *   maps' log-sum-exps.
+ * lam: fp32, element b lam_stride_b + i lam_stride_h + n lam_stride_n for difference i of row n
+ *   (strides may be 0: one weight for all).
+ * d, the difference: bf16 [B, H / 2, N_Q, D], strides d_stride_* (three zeros: contiguous).  It is
+ *   formed in fp32 and rounded once.  Rows that see no key are 0; lam is not used there.
+ * maps and s.maps.o_rest: NULL for the difference alone; both for a backward: each map's own
+ *   result and what its rounding left, bf16 [B, H, N_Q, D] with the strides o_stride_*.
+ * Backward: go = dLoss/dd with d's strides, dlse (or NULL) fp32 [B, H, N_Q]; maps and o_rest are
+ *   required.  dq, dk, dv as in streamkl_attn_bwd; dlam fp32 [B, H / 2, N_Q] contiguous, a value
+ *   for every row whatever lam's strides are.  What reaches the second map, -lam dO, enters the
+ *   products rounded to bf16.  bwd_mode as in streamkl_attn_bwd.
+ * Workspaces as in streamkl_attn_fwd and streamkl_attn_bwd; the backward's also has the maps' gradients,
+ *   2 D bytes per query row of both.  streamkl_diff_attn_fwd_plan: packed, splits and the workspace for any SM count
+ *   (num_sms <= 0: the current device; with num_sms > 0 a pure host rule).
+ */
+typedef struct {
+  streamkl_attn_shape maps;
+  const float* lam;
+  long long lam_stride_b, lam_stride_h, lam_stride_n;
+  long long d_stride_b, d_stride_h, d_stride_n;
+} streamkl_diff_attn_shape;
+streamkl_status streamkl_diff_attn_fwd_plan(streamkl_diff_attn_shape s, int num_sms, int* packed, int* splits,
+                                            size_t* workspace_bytes);
+streamkl_status streamkl_diff_attn_fwd_workspace(streamkl_diff_attn_shape s, size_t* bytes);
+streamkl_status streamkl_diff_attn_fwd(const void* q, const void* k, const void* v, streamkl_diff_attn_shape s, void* d,
+                                       void* maps, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+streamkl_status streamkl_diff_attn_bwd_workspace(streamkl_diff_attn_shape s, int bwd_mode, size_t* bytes);
+streamkl_status streamkl_diff_attn_bwd(const void* q, const void* k, const void* v, const void* maps, const float* lse,
+                                       const void* go, const float* dlse, streamkl_diff_attn_shape s, void* dq, void* dk,
+                                       void* dv, float* dlam, int bwd_mode, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/*
  * Log probabilities of given tokens, with entropy and top alternatives: the
  * output-layer companion of the attention loss (a student scored on the data's
  * tokens, or on its teacher's most likely ones).
