@@ -676,6 +676,9 @@ def diff_attn_fwd(q, k, v, lam, scale=None, causal=False, q_lens=None, k_lens=No
     [B, 2 H, N_Q] of both maps.  scale, causal and lengths as in attn_fwd.  return_maps adds what diff_attn_bwd reads: each
     map's own result and what its rounding left, two bf16 tensors like q.
     """
+    got = (_calls or calls()).diff_attn_fwd(q, k, v, lam, scale, causal, q_lens, k_lens, return_maps)
+    if got is not None:
+        return got
     (q, k, v), _, lam, q_lens, k_lens, sizes, dev, host = _diff_inputs((q, k, v), [], lam, q_lens, k_lens)
     (q, qs), (k, ks), (v, vs) = _layout(q), _layout(k), _layout(v)
     B, H, _, NQ, _, D = sizes
@@ -718,6 +721,9 @@ def diff_attn_bwd(q, k, v, lam, maps, lse, do, dlse=None, scale=None, causal=Fal
     """
     if bwd_mode == BWD_AUTO and torch.are_deterministic_algorithms_enabled():
         bwd_mode = BWD_SEPARATE
+    got = (_calls or calls()).diff_attn_bwd(q, k, v, lam, maps, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode, maps_rest)
+    if got is not None:
+        return got
     if maps_rest is None:
         raise ValueError("maps_rest is needed: diff_attn_fwd gives it with the maps (return_maps)")
     (q, k, v, maps, rest), (do,), lam, q_lens, k_lens, sizes, dev, host = _diff_inputs((q, k, v, maps, maps_rest), [do], lam,
@@ -835,6 +841,10 @@ def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0
 def _rotary(tensors, plan, positions, offset, interleaved, inverse, out):
     """Turns q and k (either may be None) by their positions; see rotary_fwd."""
     q, k = tensors
+    if out is None:
+        got = (_calls or calls()).rotary(q, k, plan.turns, plan.dim, plan.amplitude, positions, offset, interleaved, inverse)
+        if got is not None:
+            return got
     one = q if q is not None else k
     if one is None:
         raise ValueError("q or k is needed")
@@ -980,6 +990,9 @@ def vocab_xent_fwd(hidden, weight, tokens, scale=1.0):
     hidden: [..., C], weight: [V, C], both bf16 or both fp16, C a multiple of 8; tokens: [...], int64 or int32, a negative
     one is no token (its loss is 0), one past the vocabulary gives NaN.
     """
+    got = (_calls or calls()).vocab_xent_fwd(hidden, weight, tokens, scale)
+    if got is not None:
+        return got
     x, w, tok, s, lead, dev, host = _xent_inputs(hidden, weight, tokens, scale)
     nbytes = _workspace_bytes("streamkl_vocab_xent_fwd_workspace", dev, s)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -995,6 +1008,10 @@ def vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse=None, scale=1.0, w
 
     The same bits on every run.  Hidden states of rows without a gradient have to be finite all the same.
     """
+    if want_dhidden and want_dweight:
+        got = (_calls or calls()).vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse, scale)
+        if got is not None:
+            return got
     x, w, tok, s, lead, dev, host = _xent_inputs(hidden, weight, tokens, scale)
     lse, g_loss, g_lse = _rows(lse, dev, lead, "lse"), _rows(g_loss, dev, lead, "g_loss"), _rows(g_lse, dev, lead, "g_lse")
     if lse is None or g_loss is None:

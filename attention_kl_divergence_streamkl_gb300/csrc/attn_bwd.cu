@@ -265,9 +265,13 @@ __global__ void __launch_bounds__(256, KIND == kRowsShort ? 3 : 4)
 
 // ---------------------------------------------------------------------------
 // Row values of a difference of two maps, O = O1 - lam O2, for rows of both: what reaches the maps is dO and -lam dO.  The
-// second is rounded to bf16, half a step, as dO itself was where it came from, and goes to the workspace with dO beside it;
-// both deltas are taken from what is stored there and from both parts of the maps' results, dlam = -dO . O2 before the
-// rounding.  Bound by memory: five rows read, two written.
+// second row's size is taken into its weights, |lam| P2 = exp(S2 - (LSE2 - log |lam|)), which the products see as P2 and
+// round as they round P1, and its sign into dO, so that nothing is rounded for lam's sake (dO rounded times lam instead:
+// error of dV and dQ 2.6e-3 of their norm, 2.4e-3 so).  With a gradient of LSE2, which is then divided by |lam|, rows of
+// |lam| below 2^-6 multiply dO instead, rounded to bf16.  dO, signed, goes to the workspace for each map; both deltas are
+// taken from what is stored there and both parts of the maps' results, dlam = -dO . O2.  Bound by memory: five rows read, two
+// written.
+constexpr float kLeastWeight = 0.015625f;
 constexpr int kDiffRowsEach = 2;
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -304,16 +308,19 @@ __global__ void __launch_bounds__(256)
     }
     w[u] = there ? -lam[n * p.ls_n] : 0.f;
   }
+  auto in_weights = [&](float x) { return !in.dlse || !(fabsf(x) < kLeastWeight); };
 #pragma unroll
   for (int u = 0; u < kDiffRowsEach; ++u) {
     const int n = n0 + u * step;
     const bool there = seen(n);
     const uint32_t gs[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
     uint32_t hs[4];
+    const bool size_in_p = in_weights(w[u]);
+    const float by = size_in_p ? copysignf(1.f, w[u]) : w[u];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = from_bf16_pair(gs[i]);
-      hs[i] = there ? pack_bf16(v.x * w[u], v.y * w[u]) : 0u;
+      hs[i] = there ? pack_bf16(v.x * by, v.y * by) : 0u;
     }
     const uint4 h = make_uint4(hs[0], hs[1], hs[2], hs[3]);
     float sums[4] = {dot8(x[u][0], g[u], dot8(y[u][0], g[u], 0.f)), dot8(x[u][1], h, dot8(y[u][1], h, 0.f)),
@@ -323,8 +330,10 @@ __global__ void __launch_bounds__(256)
     if (lane < 4 && own < 2) {
       const long long bh = (long long)b * p.H + 2 * pair + own;
       const float l = there ? in.lse[bh * p.NQ + n] : kNegInf, dl = there && in.dlse ? in.dlse[bh * p.NQ + n] : 0.f;
-      row_s[bh * padded + n] = three_bf16(l == kNegInf ? kNoRow : -l * (1.f / p.scale));
-      row_d[bh * padded + n] = three_bf16(l == kNegInf ? 0.f : dl - sums[0]);
+      const bool scaled = own == 1 && size_in_p;
+      const bool none = l == kNegInf || (scaled && w[u] == 0.f);  // a weight of 0 leaves the map without a gradient
+      row_s[bh * padded + n] = three_bf16(none ? kNoRow : -(scaled ? l - logf(fabsf(w[u])) : l) * (1.f / p.scale));
+      row_d[bh * padded + n] = three_bf16(none ? 0.f : (scaled ? dl / fabsf(w[u]) : dl) - sums[0]);
     }
     if (lane < 4 && own == 2 && n < p.NQ) in.dlam[(long long)bp * p.NQ + n] = there ? -sums[0] : 0.f;
     const long long at = ((long long)b * p.H + 2 * pair) * p.NQ + n;

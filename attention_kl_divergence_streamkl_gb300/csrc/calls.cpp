@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
 #include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -210,6 +211,283 @@ PyObject* attn_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The difference's head count, weights and layout: H differences of two maps each in a.s.  lam is read with the strides that
+// broadcasting it gives.
+bool difference(const Attention& a, PyObject* lam, streamkl_diff_attn_shape* s) {
+  const at::Tensor* l = tensor(lam);
+  const int64_t size[3] = {a.s.B, a.s.H / 2, a.s.NQ};
+  if (!l || l->scalar_type() != at::kFloat || !on_device(*l, a.index) || l->dim() > 3 || l->dim() < 1 || a.s.H % 2 ||
+      a.s.H / 2 % a.s.HK)
+    return false;
+  long long stride[3] = {0, 0, 0};
+  for (int64_t i = 0; i < l->dim(); ++i) {
+    const int64_t to = 3 - l->dim() + i;
+    if (l->size(i) == size[to])
+      stride[to] = l->stride(i);
+    else if (l->size(i) != 1)
+      return false;
+  }
+  *s = streamkl_diff_attn_shape{a.s, l->const_data_ptr<float>(), stride[0], stride[1], stride[2], 0, 0, 0};
+  return true;
+}
+
+// diff_attn_fwd(q, k, v, lam, scale, causal, q_lens, k_lens, return_maps)
+PyObject* diff_attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Attention a;
+  streamkl_diff_attn_shape s;
+  if (n != 9 || !attention(args, 4, &a) || !difference(a, args[3], &s) || !PyBool_Check(args[8])) Py_RETURN_NONE;
+  const bool with_maps = args[8] == Py_True;
+  at::Tensor d, lse, maps, rest;
+  int status;
+  {
+    NoGil no_gil;
+    size_t bytes = 0;
+    if (with_maps) {
+      maps = like(*a.q, a.qs, a.index);
+      rest = like(*a.q, a.qs, a.index);
+      s.maps.o_rest = data(rest);
+    }
+    const auto bf16 = options(at::kBFloat16, a.index);
+    const long long B = a.s.B, H = a.s.H / 2, N = a.s.NQ, D = a.s.D;
+    if (H > 1 && a.qs.h < a.qs.n) {  // rows before heads, as q has them
+      d = at::empty_strided({B, H, N, D}, {N * H * D, D, H * D, 1}, bf16);
+      s.d_stride_b = N * H * D;
+      s.d_stride_h = D;
+      s.d_stride_n = H * D;
+    } else {
+      d = at::empty({B, H, N, D}, bf16);
+    }
+    status = streamkl_diff_attn_fwd_workspace(s, &bytes);
+    if (status == STREAMKL_OK) {
+      const at::Tensor ws = workspace(bytes, a.index);
+      lse = at::empty({a.s.B, a.s.H, a.s.NQ}, options(at::kFloat, a.index));
+      status = streamkl_diff_attn_fwd(a.q->const_data_ptr(), a.k->const_data_ptr(), a.v->const_data_ptr(), s, data(d), data(maps),
+                                      static_cast<float*>(data(lse)), data(ws), bytes, stream(a.index));
+    }
+  }
+  if (status != STREAMKL_OK) Py_RETURN_NONE;
+  return with_maps ? tuple({d, lse, maps, rest}) : tuple({d, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// diff_attn_bwd(q, k, v, lam, maps, lse, do, dlse, scale, causal, q_lens, k_lens, bwd_mode, maps_rest)
+PyObject* diff_attn_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Attention a;
+  streamkl_diff_attn_shape s;
+  if (n != 14 || !attention(args, 8, &a) || !difference(a, args[3], &s)) Py_RETURN_NONE;
+  const at::Tensor *maps = tensor(args[4]), *go = tensor(args[6]), *rest = tensor(args[13]);
+  Strides os, rs, gs;
+  if (!maps || !go || !rest || !on_device(*maps, a.index) || !on_device(*go, a.index) || !on_device(*rest, a.index) ||
+      maps->sizes() != a.q->sizes() || rest->sizes() != a.q->sizes() || !layout(*maps, &os) || !layout(*rest, &rs) ||
+      os.b != rs.b || os.h != rs.h || os.n != rs.n || !layout(*go, &gs))
+    Py_RETURN_NONE;
+  const int64_t d_sizes[4] = {a.s.B, a.s.H / 2, a.s.NQ, a.s.D};
+  if (go->sizes() != at::IntArrayRef(d_sizes, 4)) Py_RETURN_NONE;
+  s.maps.o_stride_b = os.b;
+  s.maps.o_stride_h = os.h;
+  s.maps.o_stride_n = os.n;
+  s.maps.o_rest = const_cast<void*>(rest->const_data_ptr());  // read only
+  s.d_stride_b = gs.b;
+  s.d_stride_h = gs.h;
+  s.d_stride_n = gs.n;
+  const float *lse, *dlse;
+  const auto row_sizes = a.q->sizes().slice(0, 3);
+  if (args[5] == Py_None || !rows(args[5], row_sizes, a.index, &lse) || !rows(args[7], row_sizes, a.index, &dlse) ||
+      !PyLong_Check(args[12]))
+    Py_RETURN_NONE;
+  const long mode = PyLong_AsLong(args[12]);
+  if (mode < 0 || mode > INT_MAX) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  at::Tensor dq, dk, dv, dlam;
+  int status;
+  {
+    NoGil no_gil;
+    size_t bytes = 0;
+    status = streamkl_diff_attn_bwd_workspace(s, (int)mode, &bytes);
+    if (status == STREAMKL_OK) {
+      const at::Tensor ws = workspace(bytes, a.index);
+      dq = like(*a.q, a.qs, a.index);
+      dk = like(*a.k, a.ks, a.index);
+      dv = like(*a.v, a.vs, a.index);
+      dlam = at::empty({a.s.B, a.s.H / 2, a.s.NQ}, options(at::kFloat, a.index));
+      status = streamkl_diff_attn_bwd(a.q->const_data_ptr(), a.k->const_data_ptr(), a.v->const_data_ptr(), maps->const_data_ptr(),
+                                      lse, go->const_data_ptr(), dlse, s, data(dq), data(dk), data(dv),
+                                      static_cast<float*>(data(dlam)), (int)mode, data(ws), bytes, stream(a.index));
+    }
+  }
+  if (status != STREAMKL_OK) Py_RETURN_NONE;
+  return tuple({dq, dk, dv, dlam});
+  END_HANDLE_TH_ERRORS
+}
+
+bool real_type(at::ScalarType type, int* out) {
+  *out = type == at::kBFloat16 ? STREAMKL_BF16 : type == at::kHalf ? STREAMKL_FP16 : STREAMKL_FP32;
+  return type == at::kBFloat16 || type == at::kHalf || type == at::kFloat;
+}
+
+// rotary(q, k, turns, dim, amplitude, positions, offset, interleaved, inverse), q and k both there
+PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 9) Py_RETURN_NONE;
+  const at::Tensor *x[2] = {tensor(args[0]), tensor(args[1])}, *turns = tensor(args[2]);
+  if (!x[0] || !x[1] || !turns || !x[0]->is_cuda()) Py_RETURN_NONE;
+  const int index = x[0]->get_device();
+  streamkl_rotary_shape s{};
+  if (index != c10::cuda::current_device() || !on_device(*x[1], index) || !on_device(*turns, index) ||
+      !real_type(x[0]->scalar_type(), &s.dtype) || x[1]->scalar_type() != x[0]->scalar_type() || turns->scalar_type() != at::kLong)
+    Py_RETURN_NONE;
+  for (const at::Tensor* t : x) {
+    if (t->dim() != 4 || t->numel() == 0 || t->stride(3) != 1) Py_RETURN_NONE;
+    for (int i = 0; i < 4; ++i)
+      if (t->size(i) > INT_MAX || t->stride(i) <= 0 || t->size(i) != (i == 1 ? t->size(i) : x[0]->size(i))) Py_RETURN_NONE;
+  }
+  if (!PyLong_Check(args[3]) || !PyFloat_Check(args[4]) || !PyLong_Check(args[6]) || !PyBool_Check(args[7]) || !PyBool_Check(args[8]))
+    Py_RETURN_NONE;
+  const long dim = PyLong_AsLong(args[3]);
+  const long long offset = PyLong_AsLongLong(args[6]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  s.B = (int)x[0]->size(0);
+  s.HQ = (int)x[0]->size(1);
+  s.HK = (int)x[1]->size(1);
+  s.N = (int)x[0]->size(2);
+  s.D = (int)x[0]->size(3);
+  if (dim <= 0 || dim > s.D || turns->numel() != dim / 2 || !turns->is_contiguous()) Py_RETURN_NONE;
+  s.dim = (int)dim;
+  s.interleaved = args[7] == Py_True;
+  s.amplitude = (float)PyFloat_AS_DOUBLE(args[4]);
+  s.offset = offset;
+  if (args[5] != Py_None) {
+    const at::Tensor* p = tensor(args[5]);
+    if (!p || offset || !on_device(*p, index) || (p->scalar_type() != at::kLong && p->scalar_type() != at::kInt) || p->dim() < 1 ||
+        p->dim() > 2 || p->size(p->dim() - 1) != s.N || (p->dim() == 2 && p->size(0) != s.B) ||
+        (s.N > 1 && p->stride(p->dim() - 1) != 1))
+      Py_RETURN_NONE;
+    s.positions = p->const_data_ptr();
+    s.positions_bytes = p->scalar_type() == at::kLong ? 8 : 4;
+    s.positions_stride = p->dim() == 2 && s.B > 1 ? p->stride(0) : 0;
+  }
+  at::Tensor out[2];
+  int status;
+  {
+    NoGil no_gil;
+    for (int i = 0; i < 2; ++i) out[i] = at::empty_like(*x[i]);
+    auto put = [](const at::Tensor& t, long long* b, long long* h, long long* r) {
+      *b = t.stride(0);
+      *h = t.stride(1);
+      *r = t.stride(2);
+    };
+    put(*x[0], &s.q_stride_b, &s.q_stride_h, &s.q_stride_n);
+    put(*x[1], &s.k_stride_b, &s.k_stride_h, &s.k_stride_n);
+    put(out[0], &s.q_out_stride_b, &s.q_out_stride_h, &s.q_out_stride_n);
+    put(out[1], &s.k_out_stride_b, &s.k_out_stride_h, &s.k_out_stride_n);
+    status = streamkl_rotary(x[0]->const_data_ptr(), x[1]->const_data_ptr(), s,
+                             reinterpret_cast<const unsigned long long*>(turns->const_data_ptr()), data(out[0]), data(out[1]),
+                             args[8] == Py_True, stream(index));
+  }
+  if (status != STREAMKL_OK) Py_RETURN_NONE;
+  return tuple({out[0], out[1]});
+  END_HANDLE_TH_ERRORS
+}
+
+struct Xent {
+  const at::Tensor *hidden, *weight;
+  const long long* tokens;
+  at::IntArrayRef lead;
+  int index;
+  streamkl_xent_shape s;
+};
+
+// hidden, weight, tokens at args[0..2], scale at args[`at`].
+bool xent(PyObject* const* args, int at, Xent* x) {
+  x->hidden = tensor(args[0]);
+  x->weight = tensor(args[1]);
+  const at::Tensor* t = tensor(args[2]);
+  if (!x->hidden || !x->weight || !t || !x->hidden->is_cuda() || x->hidden->numel() == 0 || x->hidden->dim() < 1) return false;
+  x->index = x->hidden->get_device();
+  const auto type = x->hidden->scalar_type();
+  if (x->index != c10::cuda::current_device() || !on_device(*x->weight, x->index) || !on_device(*t, x->index) ||
+      (type != at::kBFloat16 && type != at::kHalf) || x->weight->scalar_type() != type || x->weight->dim() != 2)
+    return false;
+  const auto size = x->hidden->sizes();
+  x->lead = size.slice(0, size.size() - 1);
+  const int64_t C = size.back();
+  if (x->weight->size(1) != C || x->weight->size(0) == 0 || C > INT_MAX || t->scalar_type() != at::kLong || t->sizes() != x->lead ||
+      !t->is_contiguous() || !PyFloat_Check(args[at]))
+    return false;
+  auto place = [](const at::Tensor& m) { return (reinterpret_cast<uintptr_t>(m.const_data_ptr()) & 15) == 0; };
+  long long hs = C;
+  if (!x->hidden->is_contiguous()) {
+    if (size.size() != 2 || x->hidden->stride(1) != 1 || x->hidden->stride(0) < C || x->hidden->stride(0) % 8) return false;
+    hs = x->hidden->stride(0);
+  }
+  const long long ws = x->weight->is_contiguous() ? C : x->weight->stride(0);
+  if (x->weight->stride(1) != 1 || ws < C || ws % 8 || C % 8 || !place(*x->hidden) || !place(*x->weight)) return false;
+  x->tokens = reinterpret_cast<const long long*>(t->const_data_ptr());
+  x->s = streamkl_xent_shape{x->hidden->numel() / C, x->weight->size(0), (int)C, type == at::kHalf ? STREAMKL_FP16 : STREAMKL_BF16,
+                             (float)PyFloat_AS_DOUBLE(args[at]), hs, ws};
+  return true;
+}
+
+// vocab_xent_fwd(hidden, weight, tokens, scale)
+PyObject* vocab_xent_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Xent x;
+  if (n != 4 || !xent(args, 3, &x)) Py_RETURN_NONE;
+  at::Tensor loss, lse;
+  int status;
+  {
+    NoGil no_gil;
+    size_t bytes = 0;
+    status = streamkl_vocab_xent_fwd_workspace(x.s, &bytes);
+    if (status == STREAMKL_OK) {
+      const at::Tensor ws = workspace(bytes, x.index);
+      loss = at::empty(x.lead, options(at::kFloat, x.index));
+      lse = at::empty(x.lead, options(at::kFloat, x.index));
+      status = streamkl_vocab_xent_fwd(x.hidden->const_data_ptr(), x.weight->const_data_ptr(), x.tokens, x.s,
+                                       static_cast<float*>(data(loss)), static_cast<float*>(data(lse)), data(ws), bytes,
+                                       stream(x.index));
+    }
+  }
+  if (status != STREAMKL_OK) Py_RETURN_NONE;
+  return tuple({loss, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse, scale), both gradients
+PyObject* vocab_xent_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Xent x;
+  if (n != 7 || !xent(args, 6, &x)) Py_RETURN_NONE;
+  const float *lse, *g, *gl;
+  if (args[3] == Py_None || args[4] == Py_None || !rows(args[3], x.lead, x.index, &lse) || !rows(args[4], x.lead, x.index, &g) ||
+      !rows(args[5], x.lead, x.index, &gl))
+    Py_RETURN_NONE;
+  at::Tensor dh, dw;
+  int status;
+  {
+    NoGil no_gil;
+    size_t bytes = 0;
+    status = streamkl_vocab_xent_bwd_workspace(x.s, 1, &bytes);
+    if (status == STREAMKL_OK) {
+      const at::Tensor ws = workspace(bytes, x.index);
+      dh = at::empty(x.hidden->sizes(), options(x.hidden->scalar_type(), x.index));
+      dw = at::empty(x.weight->sizes(), options(x.hidden->scalar_type(), x.index));
+      status = streamkl_vocab_xent_bwd(x.hidden->const_data_ptr(), x.weight->const_data_ptr(), x.tokens, lse, g, gl, x.s, data(dh),
+                                       data(dw), data(ws), bytes, stream(x.index));
+    }
+  }
+  if (status != STREAMKL_OK) Py_RETURN_NONE;
+  return tuple({dh, dw});
+  END_HANDLE_TH_ERRORS
+}
+
 struct Logits {
   const at::Tensor* x;
   int index, type;
@@ -320,6 +598,11 @@ PyCFunction fast() {
 
 PyMethodDef kMethods[] = {{"attn_fwd", fast<attn_fwd>(), METH_FASTCALL, nullptr},
                           {"attn_bwd", fast<attn_bwd>(), METH_FASTCALL, nullptr},
+                          {"diff_attn_fwd", fast<diff_attn_fwd>(), METH_FASTCALL, nullptr},
+                          {"diff_attn_bwd", fast<diff_attn_bwd>(), METH_FASTCALL, nullptr},
+                          {"rotary", fast<rotary>(), METH_FASTCALL, nullptr},
+                          {"vocab_xent_fwd", fast<vocab_xent_fwd>(), METH_FASTCALL, nullptr},
+                          {"vocab_xent_bwd", fast<vocab_xent_bwd>(), METH_FASTCALL, nullptr},
                           {"logprobs_fwd", fast<logprobs_fwd>(), METH_FASTCALL, nullptr},
                           {"logprobs_bwd", fast<logprobs_bwd>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

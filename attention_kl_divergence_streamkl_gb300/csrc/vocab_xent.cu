@@ -40,6 +40,11 @@ constexpr int OFF_BAR = OFF_OUT + EPILOGUE_WARPS * 4096;
 constexpr int BAR_SLOT = 8 * (2 * STAGES + 4);  // full, empty; tile there [2], tile free [2]; TMEM slot, abort flag
 static_assert(OFF_BAR + BAR_SLOT + 16 + 1024 <= kWholeSmSmem, "shared memory");
 
+// The tensor core's own additions cut off what does not fit, so a sum loses with every one of its C / 16 steps: 5e-7 of a
+// logit's terms for 32 of them, eight times that for 4096 channels in one go.  The forward, whose results are fp32, adds up
+// so many chunks at a time and then goes on in registers.  (8192 x 131072 x 4096 ... us in one go, ... with 8.)
+constexpr int kFlush = 8;
+
 enum Kind { kForward, kGradLogits, kGradients };
 
 // One matrix product: m_tiles x n_tiles tiles, each over `splits` ranges of the k_chunks 64-wide chunks.
@@ -48,10 +53,14 @@ struct Job {
   int m_group;       // forward and d: that many tiles along m share what they read of the other operand
   int a_mn, b_mn;    // the operand lies with its rows (m or n), not the summed index, along the 128-byte lines
   int rows, cols;    // of the output
+  int k;             // extent of the summed index
+  int a_box, b_box;  // rows of memory in a load's box
   __host__ __device__ long long tiles() const { return (long long)m_tiles * n_tiles * splits; }
 };
 struct Tile {
   int job, m, n, split, k0, k1;
+  // chunks of an accumulator: kForward starts a new one every kFlush chunks, whose values are added outside the tensor core
+  __device__ __forceinline__ int step(Kind kind) const { return kind == kForward ? kFlush : k1 - k0; }
 };
 
 struct XentParams {
@@ -131,6 +140,19 @@ struct Walk {
   }
 };
 
+// What a block loads of its half of an operand for a chunk: `loads` boxes and their bytes.  Rows that do not exist are
+// left out, by smaller boxes and fewer of them: TMA's zeros for them come at the price of loads, from one place of the L2
+// for all (8 x 131072 x 4096: 298 us with whole boxes, ... so).  What then lies in shared memory reaches only rows and
+// columns of the tile that nobody reads.
+struct Half {
+  int loads;
+  uint32_t bytes;
+};
+__device__ __forceinline__ Half half_of(int first, int extent, int mn, int box) {
+  const int loads = mn ? min(max((extent - first + 63) / 64, 0), 2) : first < extent;
+  return Half{loads, (uint32_t)(loads * box * 128)};
+}
+
 template <bool HALF>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if (HALF) {
@@ -201,22 +223,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const Job& j = p.job[t.job];
         const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
         const int m0 = t.m * TILE + (int)rank * BM, n0 = t.n * TILE + (int)rank * BM;
+        const Half a_half = half_of(m0, j.rows, j.a_mn, j.a_box), b_half = half_of(n0, j.cols, j.b_mn, j.b_box);
+        // the bytes of both blocks
+        const uint32_t bytes = half_of(t.m * TILE, j.rows, j.a_mn, j.a_box).bytes + half_of(t.m * TILE + BM, j.rows, j.a_mn, j.a_box).bytes +
+                               half_of(t.n * TILE, j.cols, j.b_mn, j.b_box).bytes + half_of(t.n * TILE + BM, j.cols, j.b_mn, j.b_box).bytes;
         for (int k = t.k0; k < t.k1; ++k) {
           if (lap && !(ok = mbar_wait(empty + 8 * s, (lap - 1) & 1, status, abort_flag))) break;
           const uint32_t a = sb + OFF_STAGE + s * 2 * HALF_STAGE, b = a + HALF_STAGE, done = full_even + 8 * s;
-          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 4 * HALF_STAGE);
-          if (j.a_mn) {
-            tma_load_2d_pair(a, ma, done, m0, k * BK);
-            tma_load_2d_pair(a + HALF_STAGE / 2, ma, done, m0 + 64, k * BK);
-          } else {
-            tma_load_2d_pair(a, ma, done, k * BK, m0);
-          }
-          if (j.b_mn) {
-            tma_load_2d_pair(b, mb, done, n0, k * BK);
-            tma_load_2d_pair(b + HALF_STAGE / 2, mb, done, n0 + 64, k * BK);
-          } else {
-            tma_load_2d_pair(b, mb, done, k * BK, n0);
-          }
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+          for (int h = 0; h < a_half.loads; ++h)
+            tma_load_2d_pair(a + h * (HALF_STAGE / 2), ma, done, j.a_mn ? m0 + 64 * h : k * BK, j.a_mn ? k * BK : m0);
+          for (int h = 0; h < b_half.loads; ++h)
+            tma_load_2d_pair(b + h * (HALF_STAGE / 2), mb, done, j.b_mn ? n0 + 64 * h : k * BK, j.b_mn ? k * BK : n0);
           if (++s == STAGES) {
             s = 0;
             ++lap;
@@ -238,32 +256,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == MMA_WARP) {
     if (rank == 0 && elect_one()) {
       int s = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, used = 0;  // used: accumulators begun
       bool ok = true;
       for (long long i = 0; ok && i < walk.n_all; ++i) {
         const Tile t = walk.tile(p, i);
         const Job& j = p.job[t.job];
-        const uint32_t buf = (uint32_t)i & 1;
-        if (i >= 2 && !(ok = mbar_wait(free_ + 8 * buf, (uint32_t)(i / 2 - 1) & 1, status, abort_flag))) break;
-        tc_fence_after();
         const uint32_t idesc = pair_idesc<HALF>(j.a_mn, j.b_mn);
         const uint32_t a_step = j.a_mn ? 2048 : 32, b_step = j.b_mn ? 2048 : 32;
         const uint32_t a_lbo = j.a_mn ? HALF_STAGE / 2 : 0, b_lbo = j.b_mn ? HALF_STAGE / 2 : 0;
-        for (int k = t.k0; k < t.k1; ++k) {
-          if (!(ok = mbar_wait(full + 8 * s, phase, status, abort_flag))) break;
+        for (int k0 = t.k0; ok && k0 < t.k1; k0 += t.step(KIND), ++used) {
+          const uint32_t buf = used & 1;
+          if (used >= 2 && !(ok = mbar_wait(free_ + 8 * buf, (used / 2 - 1) & 1, status, abort_flag))) break;
           tc_fence_after();
-          const uint32_t at = sb + OFF_STAGE + s * 2 * HALF_STAGE;
-          const uint64_t ad = sdesc_sw128(at, a_lbo, 1024), bd = sdesc_sw128(at + HALF_STAGE, b_lbo, 1024);
+          for (int k = k0; k < min(k0 + t.step(KIND), t.k1); ++k) {
+            if (!(ok = mbar_wait(full + 8 * s, phase, status, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t at = sb + OFF_STAGE + s * 2 * HALF_STAGE;
+            const uint64_t ad = sdesc_sw128(at, a_lbo, 1024), bd = sdesc_sw128(at + HALF_STAGE, b_lbo, 1024);
+            const int steps = min(BK / 16, (j.k - k * BK + 15) / 16);  // the last chunk may be short
 #pragma unroll
-          for (int ks = 0; ks < BK / 16; ++ks)
-            mma_pair(tmem + TILE * buf, sdesc_add(ad, ks * a_step), sdesc_add(bd, ks * b_step), idesc, k > t.k0 || ks > 0);
-          mma_commit_pair(empty + 8 * s);
-          if (++s == STAGES) {
-            s = 0;
-            phase ^= 1;
+            for (int ks = 0; ks < BK / 16; ++ks)
+              if (ks < steps)
+                mma_pair(tmem + TILE * buf, sdesc_add(ad, ks * a_step), sdesc_add(bd, ks * b_step), idesc, k > k0 || ks > 0);
+            mma_commit_pair(empty + 8 * s);
+            if (++s == STAGES) {
+              s = 0;
+              phase ^= 1;
+            }
           }
+          if (ok) mma_commit_pair(there + 8 * buf);
         }
-        if (ok) mma_commit_pair(there + 8 * buf);
       }
     }
     __syncwarp();
@@ -274,9 +296,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t stage = sb + OFF_OUT + warp * 4096;
     const uint32_t free_even = in_block(free_, 0);
     const float power = HALF && KIND != kForward ? p.power[KIND == kGradients] : 1.f;
+    uint32_t used = 0;  // accumulators taken
     for (long long i = 0; i < walk.n_all; ++i) {
       const Tile t = walk.tile(p, i);
-      const uint32_t buf = (uint32_t)i & 1;
+      const uint32_t buf = used & 1, parity = used / 2 & 1;
       const int row0 = t.m * TILE + (int)rank * BM + quarter * 32;  // the warp's first row
       const int col0 = t.n * TILE + half * 128;                     // and column
       const int row = row0 + lane;
@@ -284,20 +307,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if constexpr (KIND == kForward) {
         const bool real = row < p.R;
         const long long token = real ? p.tokens[row] : -1;
-        if (!mbar_wait_warp(there + 8 * buf, (uint32_t)(i / 2) & 1, status, abort_flag)) break;
-        tc_fence_after();
         uint32_t s0[32], s1[32], s2[32], s3[32];
-        tmem_ld32(ta, s0);
-        tmem_ld32(ta + 32, s1);
-        tmem_ld32(ta + 64, s2);
-        tmem_ld32(ta + 96, s3);
-        tmem_ld_wait();
-        reg_fence32(s0);
-        reg_fence32(s1);
-        reg_fence32(s2);
-        reg_fence32(s3);
-        tc_fence_before();
-        arrive_one_in(free_even + 8 * buf);
+        bool ok = true;
+        for (int k0 = t.k0; k0 < t.k1; k0 += kFlush, ++used) {
+          const uint32_t b = used & 1, from = tmem + lanes + TILE * b + 128 * half;
+          if (!(ok = mbar_wait_warp(there + 8 * b, used / 2 & 1, status, abort_flag))) break;
+          tc_fence_after();
+          if (k0 == t.k0) {
+            tmem_ld32(from, s0);
+            tmem_ld32(from + 32, s1);
+            tmem_ld32(from + 64, s2);
+            tmem_ld32(from + 96, s3);
+            tmem_ld_wait();
+            reg_fence32(s0);
+            reg_fence32(s1);
+            reg_fence32(s2);
+            reg_fence32(s3);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint32_t x[16];
+              tmem_ld16(from + 16 * q, x);
+              tmem_ld_wait();
+              reg_fence16(x);
+              uint32_t* to = (q < 2 ? s0 : q < 4 ? s1 : q < 6 ? s2 : s3) + 16 * (q & 1);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 y = fadd2(make_float2(__uint_as_float(to[k]), __uint_as_float(to[k + 1])),
+                                       make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                to[k] = __float_as_uint(y.x);
+                to[k + 1] = __float_as_uint(y.y);
+              }
+            }
+          }
+          tc_fence_before();
+          arrive_one_in(free_even + 8 * b);
+        }
+        if (!ok) break;
         const int seen = p.V - col0;
         const long long at = token - col0;
         if (__any_sync(0xffffffffu, at >= 0 && at < min(128, seen))) {
@@ -352,8 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           a = g + (p.g_lse ? p.g_lse[row] * p.scale * power : 0.f);
         }
         const int seen = real ? p.job[0].cols - col0 : 0;  // d is 0 past the piece; what is past the rows is not stored
-        bool ok = mbar_wait_warp(there + 8 * buf, (uint32_t)(i / 2) & 1, status, abort_flag);
-        if (!ok) break;
+        if (!mbar_wait_warp(there + 8 * buf, parity, status, abort_flag)) break;
+        ++used;
         tc_fence_after();
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
@@ -403,7 +449,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       } else {
         const Job& j = p.job[t.job];
         const bool sums = t.job == 0 && p.accumulate;
-        if (!mbar_wait_warp(there + 8 * buf, (uint32_t)(i / 2) & 1, status, abort_flag)) break;
+        if (!mbar_wait_warp(there + 8 * buf, parity, status, abort_flag)) break;
+        ++used;
         tc_fence_after();
         const bool rows_there = row0 < j.rows;
 #pragma unroll 1
@@ -470,33 +517,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins the tiles' maxima and sums: a warp's lanes are rows, the warps share the tiles.
-constexpr int kJoinWarps = 16;
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    xent_join_kernel(long long R, int V, int parts, long long part_rows, const float2* __restrict__ part,
+// Joins the tiles' maxima and sums.  A block has `each` rows (a power of two up to 32: neighbouring threads have
+// neighbouring rows) and deals the parts of a row out over its other threads, whose loads go out four at a time.
+constexpr int kJoinThreads = 512, kJoinAhead = 4;
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float to = fmaxf(a.x, b.x);
+  // (nothing but -inf on a side, and the sum's start, have a sum of 0 there; a NaN stays)
+  const float l = (a.x == to ? a.y : a.y * ex2(a.x - to)) + (b.x == to ? b.y : b.y * ex2(b.x - to));
+  return make_float2(to, l);
+}
+__global__ void __launch_bounds__(kJoinThreads)
+    xent_join_kernel(long long R, int V, int parts, int each, long long part_rows, const float2* __restrict__ part,
                      const float* __restrict__ given, const long long* __restrict__ tokens, float* __restrict__ loss,
                      float* __restrict__ lse) {
-  __shared__ float2 sums[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = (long long)blockIdx.x * 32 + lane;
+  __shared__ float2 sums[kJoinThreads];
+  const int mine = threadIdx.x & (each - 1), share = threadIdx.x / each, shares = kJoinThreads / each;
+  const long long row = (long long)blockIdx.x * each + mine;
   const bool real = row < R;
-  float m = kNegInf, l = 0.f;
-  auto join = [&](float2 x) {
-    if (x.x == kNegInf && x.y == 0.f) return;  // nothing but -inf there
-    const float to = fmaxf(m, x.x);
-    l = (m == kNegInf && l == 0.f ? 0.f : l * ex2(m - to)) + (x.x == to ? x.y : x.y * ex2(x.x - to));
-    m = to;
-  };
+  float2 x = make_float2(kNegInf, 0.f);
   if (real)
-    for (int i = warp; i < parts; i += kJoinWarps) join(part[(size_t)i * part_rows + row]);
-  sums[warp][lane] = make_float2(m, l);
-  __syncthreads();
-  if (warp || !real) return;
-#pragma unroll 1
-  for (int w = 1; w < kJoinWarps; ++w) join(sums[w][lane]);
-  const bool none = m == kNegInf && l == 0.f;
-  const float log_sum = logf(l);
-  lse[row] = none ? kNegInf : fmaf(m, kLn2, log_sum);
+    for (int i = share; i < parts; i += kJoinAhead * shares) {
+      float2 y[kJoinAhead];
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k)
+        y[k] = i + k * shares < parts ? part[(size_t)(i + k * shares) * part_rows + row] : make_float2(kNegInf, 0.f);
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k) x = join(x, y[k]);
+    }
+  sums[threadIdx.x] = x;
+  for (int half = shares / 2; half; half /= 2) {
+    __syncthreads();
+    if (share < half) sums[threadIdx.x] = x = join(x, sums[threadIdx.x + half * each]);
+  }
+  if (share || !real) return;
+  const float m = x.x, l = x.y, log_sum = logf(l);
+  lse[row] = m == kNegInf && l == 0.f ? kNegInf : fmaf(m, kLn2, log_sum);
   const long long token = tokens[row];
   // the differences first: a loss keeps its digits however far from 0 the logits lie
   loss[row] = token < 0 ? 0.f : token >= V ? __int_as_float(0x7fc00000) : fmaf(m - given[row], kLn2, log_sum);
@@ -564,8 +619,10 @@ cudaError_t launch(const XentParams& p, const Maps& maps, int pairs, int* status
 }
 
 // A matrix [rows, cols] of 2-byte values: an operand whose lines run along the summed index (k_major) or along its rows.
-bool operand_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, bool k_major) {
-  return encode_matrix_map(map, base, rows, cols, stride, k_major ? BM : BK, 64);
+// `box`: rows of a load, no more than there are (the summed index in whole steps of 16).
+bool operand_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, bool k_major, int* box) {
+  *box = k_major ? (int)std::min<long long>(BM, up(rows, 8)) : (int)std::min<long long>(BK, up(rows, 16));
+  return encode_matrix_map(map, base, rows, cols, stride, *box, 64);
 }
 
 }  // namespace
@@ -601,12 +658,12 @@ size_t xent_fwd_workspace(const XentProblem& p) {
 cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void* weight, const long long* tokens, float* loss,
                             float* lse, void* workspace, int num_sms, int* status, cudaStream_t st) {
   Maps maps{};
-  if (!operand_map(&maps.a[0], hidden, p.R, p.C, p.hidden_stride, true) ||
-      !operand_map(&maps.b[0], weight, p.V, p.C, p.weight_stride, true))
-    return cudaErrorInvalidValue;
   XentParams k{};
   const int m_tiles = tiles_of(p.R, TILE), n_tiles = tiles_of(p.V, TILE);
-  k.job[0] = Job{m_tiles, n_tiles, 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)p.V};
+  k.job[0] = Job{m_tiles, n_tiles, 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)p.V, p.C, 0, 0};
+  if (!operand_map(&maps.a[0], hidden, p.R, p.C, p.hidden_stride, true, &k.job[0].a_box) ||
+      !operand_map(&maps.b[0], weight, p.V, p.C, p.weight_stride, true, &k.job[0].b_box))
+    return cudaErrorInvalidValue;
   k.R = p.R;
   k.V = (int)p.V;
   k.scale = p.scale;
@@ -618,8 +675,10 @@ cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void
   const int pairs = pairs_for(k.job[0].tiles(), num_sms);
   cudaError_t e = p.half ? launch<kForward, true>(k, maps, pairs, status, st) : launch<kForward, false>(k, maps, pairs, status, st);
   if (e != cudaSuccess) return e;
-  xent_join_kernel<<<(unsigned)tiles_of(p.R, 32), kJoinWarps * 32, 0, st>>>(p.R, (int)p.V, 2 * n_tiles, k.part_rows, k.part,
-                                                                          k.given, tokens, loss, lse);
+  int each = 32;
+  while (each > 1 && each / 2 >= p.R) each /= 2;
+  xent_join_kernel<<<(unsigned)tiles_of(p.R, each), kJoinThreads, 0, st>>>(p.R, (int)p.V, 2 * n_tiles, each, k.part_rows, k.part,
+                                                                         k.given, tokens, loss, lse);
   return cudaGetLastError();
 }
 
@@ -652,11 +711,11 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     k.power = p.half ? power : nullptr;
     {
       Maps maps{};
-      if (!operand_map(&maps.a[0], in.hidden, p.R, p.C, p.hidden_stride, true) ||
-          !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, true) ||
+      k.job[0] = Job{m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)cols, p.C, 0, 0};
+      if (!operand_map(&maps.a[0], in.hidden, p.R, p.C, p.hidden_stride, true, &k.job[0].a_box) ||
+          !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, true, &k.job[0].b_box) ||
           !encode_matrix_map(&maps.out[0], d, p.R, cols, stride, 32, 64))
         return cudaErrorInvalidValue;
-      k.job[0] = Job{m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)cols};
       const int pairs = pairs_for(k.job[0].tiles(), num_sms);
       e = p.half ? launch<kGradLogits, true>(k, maps, pairs, status, st) : launch<kGradLogits, false>(k, maps, pairs, status, st);
       if (e != cudaSuccess) return e;
@@ -664,20 +723,21 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     Maps maps{};
     k.job[0] = k.job[1] = Job{};
     if (dhidden) {
-      if (!operand_map(&maps.a[0], d, p.R, cols, stride, true) || !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, false) ||
+      // (a last, short piece adds to the first sums only)
+      k.job[0] = Job{m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), 0, 0, 1, (int)p.R, p.C, (int)cols, 0, 0};
+      if (!operand_map(&maps.a[0], d, p.R, cols, stride, true, &k.job[0].a_box) ||
+          !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, false, &k.job[0].b_box) ||
           !encode_matrix_map(&maps.out[0], dhidden, p.R, p.C, p.C, 32, 64) ||
           (!g.direct && !encode_rows_f32_map(&maps.acc, acc, p.C, (int)p.R, g.splits, 32, 32)))
         return cudaErrorInvalidValue;
-      // (a last, short piece adds to the first sums only)
-      k.job[0] = Job{m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), 0, 0, 1, (int)p.R, p.C};
       k.accumulate = g.direct ? 0 : piece == 0 ? 1 : 2;
     }
     if (dweight) {
-      if (!operand_map(&maps.a[1], d, p.R, cols, stride, false) ||
-          !operand_map(&maps.b[1], in.hidden, p.R, p.C, p.hidden_stride, false) ||
+      k.job[1] = Job{tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, (int)cols, p.C, (int)p.R, 0, 0};
+      if (!operand_map(&maps.a[1], d, p.R, cols, stride, false, &k.job[1].a_box) ||
+          !operand_map(&maps.b[1], in.hidden, p.R, p.C, p.hidden_stride, false, &k.job[1].b_box) ||
           !encode_matrix_map(&maps.out[1], dweight, p.V, p.C, p.C, 32, 64))
         return cudaErrorInvalidValue;
-      k.job[1] = Job{tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, (int)cols, p.C};
     }
     const long long a = k.job[0].tiles(), b = k.job[1].tiles();
     const int pairs = pairs_for(a + b, num_sms);
