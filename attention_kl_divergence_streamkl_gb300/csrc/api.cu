@@ -918,6 +918,8 @@ static streamkl_status xent_problem(const streamkl_xent_shape& s, XentProblem* p
   if (s.rows > kMaxRows || s.vocab > kMaxRows || s.channels > (1 << 20) || s.hidden_stride >= (1ll << 38) ||
       s.weight_stride >= (1ll << 38) || s.rows * s.channels > (1ll << 40))
     return STREAMKL_ERR_UNSUPPORTED;
+  const long long r = s.rows / 256 + 1, v = s.vocab / 256 + 1, c = s.channels / 256 + 1;  // tiles
+  if (r * v >= (1ll << 31) || r * c >= (1ll << 24) || v * c >= (1ll << 30)) return STREAMKL_ERR_UNSUPPORTED;
   *p = XentProblem{s.rows, s.vocab, s.channels, s.dtype == STREAMKL_FP16, s.hidden_stride, s.weight_stride, s.scale};
   return STREAMKL_OK;
 }

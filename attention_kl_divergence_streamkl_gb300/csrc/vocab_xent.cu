@@ -32,11 +32,11 @@ constexpr int BM = 128, BK = 64;         // rows of either operand in a block, a
 constexpr int TILE = 256;                // a pair's tile: TILE x TILE
 constexpr int EPILOGUE_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int THREADS = 10 * 32;
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int HALF_STAGE = BM * BK * 2;  // one operand
 constexpr uint32_t kTmemCols = 512;
-constexpr int OFF_STAGE = 0, OFF_OUT = STAGES * 2 * HALF_STAGE;  // the epilogue warps' 4 KB each
-constexpr int OFF_BAR = OFF_OUT + EPILOGUE_WARPS * 4096;
+constexpr int OFF_STAGE = 0, OFF_OUT = STAGES * 2 * HALF_STAGE;  // 8 KB for each epilogue warp
+constexpr int OFF_BAR = OFF_OUT + EPILOGUE_WARPS * 8192;
 constexpr int BAR_SLOT = 8 * (2 * STAGES + 4);  // full, empty; tile there [2], tile free [2]; TMEM slot, abort flag
 static_assert(OFF_BAR + BAR_SLOT + 16 + 1024 <= kWholeSmSmem, "shared memory");
 
@@ -55,8 +55,22 @@ struct Job {
   int rows, cols;    // of the output
   int k;             // extent of the summed index
   int a_box, b_box;  // rows of memory in a load's box
+  // what a tile's number is divided by: the tiles of a split, of a group, and its rows or (gradients) columns of tiles
+  FastDiv by_split, by_group, by_m, by_last, by_n;
   __host__ __device__ long long tiles() const { return (long long)m_tiles * n_tiles * splits; }
 };
+Job make_job(int m_tiles, int n_tiles, int splits, int k_chunks, int m_group, int a_mn, int b_mn, long long rows, long long cols,
+             long long k) {
+  Job j{m_tiles, n_tiles, splits, k_chunks, m_group, a_mn, b_mn, (int)rows, (int)cols, (int)k, 0, 0, {}, {}, {}, {}, {}};
+  j.by_split = FastDiv((unsigned)((long long)m_tiles * n_tiles));
+  j.by_n = FastDiv((unsigned)n_tiles);
+  if (m_group) {
+    j.by_group = FastDiv((unsigned)((long long)m_group * n_tiles));
+    j.by_m = FastDiv((unsigned)m_group);
+    j.by_last = FastDiv((unsigned)(m_tiles % m_group ? m_tiles % m_group : m_group));
+  }
+  return j;
+}
 struct Tile {
   int job, m, n, split, k0, k1;
   // chunks of an accumulator: kForward starts a new one every kFlush chunks, whose values are added outside the tensor core
@@ -88,53 +102,54 @@ struct Maps {
 
 // The tiles of a pair, in its order.  One job: every pairs-th, the tiles along m first, in groups of m_group.
 // Two: the pair's share of the first job's tiles, then a run of the second's.
-__device__ __forceinline__ Tile job_tile(const Job& j, int job, long long i) {
+__device__ __forceinline__ Tile job_tile(const Job& j, int job, unsigned i) {
   Tile t;
   t.job = job;
-  const long long per = (long long)j.m_tiles * j.n_tiles;
-  t.split = j.splits == 1 ? 0 : (int)(i / per);
-  long long x = i - t.split * per;
-  if (job == 0 && j.m_group) {
-    const long long group = x / ((long long)j.m_group * j.n_tiles);
-    x -= group * j.m_group * j.n_tiles;
-    const int here = min(j.m_group, j.m_tiles - (int)group * j.m_group);
-    t.n = (int)(x / here);
-    t.m = (int)group * j.m_group + (int)(x - (long long)t.n * here);
+  t.split = j.splits == 1 ? 0 : (int)j.by_split.div(i);
+  unsigned x = i - (unsigned)t.split * j.by_split.d;
+  if (j.m_group) {
+    const unsigned group = j.by_group.div(x);
+    x -= group * j.by_group.d;
+    const FastDiv& here = (int)(group + 1) * j.m_group > j.m_tiles ? j.by_last : j.by_m;
+    t.n = (int)here.div(x);
+    t.m = (int)(group * j.by_m.d + (x - (unsigned)t.n * here.d));
   } else {
-    t.m = (int)(x / j.n_tiles);
-    t.n = (int)(x - (long long)t.m * j.n_tiles);
+    t.m = (int)j.by_n.div(x);
+    t.n = (int)(x - (unsigned)t.m * j.by_n.d);
   }
-  t.k0 = (int)((long long)j.k_chunks * t.split / j.splits);
-  t.k1 = (int)((long long)j.k_chunks * (t.split + 1) / j.splits);
+  t.k0 = 0;
+  t.k1 = j.k_chunks;
+  if (j.splits > 1) {  // (chunks below 2^24, splits at most 76: 32 bits)
+    t.k0 = (int)((unsigned)j.k_chunks * (unsigned)t.split / (unsigned)j.splits);
+    t.k1 = (int)((unsigned)j.k_chunks * (unsigned)(t.split + 1) / (unsigned)j.splits);
+  }
   return t;
 }
 struct Walk {
-  long long first, n_first, from, n_all;
-  int pairs;
+  unsigned first, n_first, from, n_all, pairs;
   template <Kind KIND>
-  __device__ __forceinline__ static Walk make(const XentParams& p, int pair, int pairs) {
+  __device__ __forceinline__ static Walk make(const XentParams& p, unsigned pair, unsigned pairs) {
     Walk w;
-    const long long a = p.job[0].tiles();
+    const unsigned a = (unsigned)p.job[0].tiles();
     w.first = pair;
     w.pairs = pairs;
     w.n_first = pair < a ? (a - pair + pairs - 1) / pairs : 0;
     w.from = 0;
     w.n_all = w.n_first;
     if (KIND == kGradients) {
-      const long long b = p.job[1].tiles(), few = (long long)p.few * p.more, rest = b - few, others = pairs - p.more;
-      long long to;
-      if (pair < p.more) {
-        w.from = (long long)p.few * pair;
-        to = w.from + p.few;
+      const unsigned more = (unsigned)p.more, few = (unsigned)p.few;
+      const unsigned b = (unsigned)p.job[1].tiles(), rest = b - few * more, others = pairs - more;
+      if (pair < more) {
+        w.from = few * pair;
+        w.n_all += few;
       } else {
-        w.from = few + rest * (pair - p.more) / others;
-        to = few + rest * (pair - p.more + 1) / others;
+        w.from = few * more + (unsigned)((unsigned long long)rest * (pair - more) / others);
+        w.n_all += few * more + (unsigned)((unsigned long long)rest * (pair - more + 1) / others) - w.from;
       }
-      w.n_all += to - w.from;
     }
     return w;
   }
-  __device__ __forceinline__ Tile tile(const XentParams& p, long long i) const {
+  __device__ __forceinline__ Tile tile(const XentParams& p, unsigned i) const {
     if (i < n_first) return job_tile(p.job[0], 0, first + i * pairs);
     return job_tile(p.job[1], 1, from + i - n_first);
   }
@@ -178,7 +193,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const Walk walk = Walk::make<KIND>(p, (int)(blockIdx.x >> 1), (int)(gridDim.x >> 1));
+  const Walk walk = Walk::make<KIND>(p, blockIdx.x >> 1, gridDim.x >> 1);
 
   const uint32_t bar = sb + OFF_BAR;
   const uint32_t full = bar, empty = full + 8 * STAGES, there = empty + 8 * STAGES, free_ = there + 16;
@@ -187,6 +202,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp == PRODUCER_WARP) {
     if (elect_one()) {
+      for (int t = 0; t < (KIND == kGradients ? 2 : 1); ++t) {
+        if (!p.job[t].m_tiles) continue;
+        prefetch_tensormap(&maps.a[t]);
+        prefetch_tensormap(&maps.b[t]);
+      }
       for (int s = 0; s < STAGES; ++s) {
         mbar_init(full + 8 * s, 1);   // the even block's: the bytes of both
         mbar_init(empty + 8 * s, 1);  // both blocks', by one commit
@@ -209,6 +229,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __syncthreads();
   cluster_sync();  // both blocks' barriers and TMEM are set up
   tc_fence_after();
+  let_next_begin();
+  if (KIND != kForward) wait_for_previous();
   whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + OFF_BAR + BAR_SLOT), status);
   constexpr uint32_t tmem = 0;
 
@@ -218,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int s = 0;          // the stage that is filled next
       uint32_t lap = 0;   // how often the ring has been round
       bool ok = true;
-      for (long long i = 0; ok && i < walk.n_all; ++i) {
+      for (unsigned i = 0; ok && i < walk.n_all; ++i) {
         const Tile t = walk.tile(p, i);
         const Job& j = p.job[t.job];
         const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
@@ -258,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int s = 0;
       uint32_t phase = 0, used = 0;  // used: accumulators begun
       bool ok = true;
-      for (long long i = 0; ok && i < walk.n_all; ++i) {
+      for (unsigned i = 0; ok && i < walk.n_all; ++i) {
         const Tile t = walk.tile(p, i);
         const Job& j = p.job[t.job];
         const uint32_t idesc = pair_idesc<HALF>(j.a_mn, j.b_mn);
@@ -293,11 +315,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t stage = sb + OFF_OUT + warp * 4096;
+    // A warp's 32 rows leave through 8 KB, 128 columns of 2 bytes or 64 of 4, as two boxes under one fence (a fence for each
+    // 64 columns: 4750 cycles a tile, ... so).
+    const uint32_t stage = sb + OFF_OUT + warp * 8192;
+    auto stage_free = [&]() {  // the stores before have read it
+      if (elect_one()) bulk_wait_read();
+      __syncwarp();
+    };
+    auto put = [&](int box, const uint32_t (&w)[32]) {  // the lane's row of a box, 128 bytes
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        st_shared16(stage + box * 4096 + lane * 128 + ((k ^ (lane & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+    };
     const uint32_t free_even = in_block(free_, 0);
     const float power = HALF && KIND != kForward ? p.power[KIND == kGradients] : 1.f;
     uint32_t used = 0;  // accumulators taken
-    for (long long i = 0; i < walk.n_all; ++i) {
+    for (unsigned i = 0; i < walk.n_all; ++i) {
       const Tile t = walk.tile(p, i);
       const uint32_t buf = used & 1, parity = used / 2 & 1;
       const int row0 = t.m * TILE + (int)rank * BM + quarter * 32;  // the warp's first row
@@ -433,19 +466,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             w[k / 2] = pack16<HALF>(d.x, d.y);
           }
-          if (elect_one()) bulk_wait_read();  // the warp's last store has read its 4 KB
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            st_shared16(stage + lane * 128 + ((k ^ (lane & 7)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
-          fence_async_smem();
-          __syncwarp();
-          if (elect_one()) {
-            if (row0 < p.R && col0 + 64 * q < p.job[0].cols) tma_store_2d(&maps.out[0], stage, col0 + 64 * q, row0);
-            bulk_commit();
-          }
-          __syncwarp();
+          if (q == 0) stage_free();
+          put(q, w);
         }
+        fence_async_smem();
+        __syncwarp();
+        if (elect_one()) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (row0 < p.R && col0 + 64 * q < p.job[0].cols) tma_store_2d(&maps.out[0], stage + 4096 * q, col0 + 64 * q, row0);
+          bulk_commit();
+        }
+        __syncwarp();
       } else {
         const Job& j = p.job[t.job];
         const bool sums = t.job == 0 && p.accumulate;
@@ -453,59 +485,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ++used;
         tc_fence_after();
         const bool rows_there = row0 < j.rows;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          tmem_ld32(ta + 32 * q, s);
-          tmem_ld_wait();
-          reg_fence32(s);
-          if (q == 3) {
-            tc_fence_before();
-            arrive_one_in(free_even + 8 * buf);
-          }
-          const int col = col0 + 32 * q;
-          if (sums || (q & 1) == 0) {
-            if (elect_one()) bulk_wait_read();
-            __syncwarp();
-          }
-          if (sums) {
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(ta, s0);
+        tmem_ld32(ta + 32, s1);
+        tmem_ld32(ta + 64, s2);
+        tmem_ld32(ta + 96, s3);
+        tmem_ld_wait();
+        reg_fence32(s0);
+        reg_fence32(s1);
+        reg_fence32(s2);
+        reg_fence32(s3);
+        tc_fence_before();
+        arrive_one_in(free_even + 8 * buf);
+        if (sums) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              st_shared16(stage + lane * 128 + ((k ^ (lane & 7)) << 4), make_uint4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack16<HALF>(__uint_as_float(s[8 * k + 2 * e]) * power, __uint_as_float(s[8 * k + 2 * e + 1]) * power);
-              st_shared16(stage + lane * 128 + (((4 * (q & 1) + k) ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-            }
-          }
-          if (sums || (q & 1)) {
+          for (int q = 0; q < 2; ++q) {
+            stage_free();
+            put(0, q ? s2 : s0);
+            put(1, q ? s3 : s1);
             fence_async_smem();
             __syncwarp();
             if (elect_one()) {
-              if (sums) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int col = col0 + 64 * q + 32 * h;
                 if (rows_there && col < j.cols) {
                   if (p.accumulate == 1)
-                    tma_store_3d(&maps.acc, stage, col, row0, t.split);
+                    tma_store_3d(&maps.acc, stage + 4096 * h, col, row0, t.split);
                   else
-                    tma_add_3d(&maps.acc, stage, col, row0, t.split);
+                    tma_add_3d(&maps.acc, stage + 4096 * h, col, row0, t.split);
                 }
-              } else if (rows_there && col - 32 < j.cols) {
-                tma_store_2d(&maps.out[t.job], stage, col - 32, row0 + (t.job ? p.v0 : 0));
               }
               bulk_commit();
             }
             __syncwarp();
           }
+        } else {
+          stage_free();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t* s = q ? (k < 16 ? s2 : s3) : (k < 16 ? s0 : s1);
+              w[k] = pack16<HALF>(__uint_as_float(s[2 * (k & 15)]) * power, __uint_as_float(s[2 * (k & 15) + 1]) * power);
+            }
+            put(q, w);
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              if (rows_there && col0 + 64 * q < j.cols)
+                tma_store_2d(&maps.out[t.job], stage + 4096 * q, col0 + 64 * q, row0 + (t.job ? p.v0 : 0));
+            bulk_commit();
+          }
+          __syncwarp();
         }
       }
     }
     if (KIND != kForward) {
-      if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-      __syncwarp();
+      stage_free();  // the block's memory is read until then; the grid's end waits for the writes
     }
   }
   tc_fence_before();
@@ -531,6 +572,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                      const float* __restrict__ given, const long long* __restrict__ tokens, float* __restrict__ loss,
                      float* __restrict__ lse) {
   __shared__ float2 sums[kJoinThreads];
+  wait_for_previous();
   const int mine = threadIdx.x & (each - 1), share = threadIdx.x / each, shares = kJoinThreads / each;
   const long long row = (long long)blockIdx.x * each + mine;
   const bool real = row < R;
@@ -561,6 +603,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 __global__ void __launch_bounds__(1024) xent_power_kernel(long long R, float scale, const float* __restrict__ g,
                                                           const float* __restrict__ g_lse, float* __restrict__ power) {
   __shared__ float warp_max[32];
+  let_next_begin();
   float mx = 0.f;
   for (long long i = threadIdx.x; i < R; i += 1024) mx = fmaxf(mx, scale * (fabsf(g[i]) + (g_lse ? fabsf(g_lse[i]) : 0.f)));
 #pragma unroll
@@ -584,14 +627,23 @@ __global__ void __launch_bounds__(256)
     xent_close_kernel(long long n, int splits, const float4* __restrict__ acc, const float* __restrict__ power,
                       uint2* __restrict__ out) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // four values
+  wait_for_previous();
   if (i >= n) return;
-  float4 s = __ldcg(acc + i);
-  for (int k = 1; k < splits; ++k) {
-    const float4 v = __ldcg(acc + k * n + i);
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  constexpr int AHEAD = 8;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < splits; k += AHEAD) {
+    float4 v[AHEAD];
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e)
+      if (k + e < splits) v[e] = __ldcg(acc + (k + e) * n + i);
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e) {
+      if (k + e >= splits) break;
+      s.x += v[e].x;
+      s.y += v[e].y;
+      s.z += v[e].z;
+      s.w += v[e].w;
+    }
   }
   const float f = HALF ? power[1] : 1.f;
   out[i] = make_uint2(pack16<HALF>(s.x * f, s.y * f), pack16<HALF>(s.z * f, s.w * f));
@@ -610,10 +662,11 @@ int m_group(const XentProblem& p, int m_tiles) {
 }
 
 template <Kind KIND, bool HALF>
-cudaError_t launch(const XentParams& p, const Maps& maps, int pairs, int* status, cudaStream_t st) {
+cudaError_t launch(const XentParams& p, const Maps& maps, int pairs, int* status, cudaStream_t st, bool behind = false) {
   const auto kern = xent_kernel<KIND, HALF>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kWholeSmSmem);
   if (e != cudaSuccess) return e;
+  if (KIND != kForward && behind) return launch_behind(kern, (unsigned)(2 * pairs), THREADS, kWholeSmSmem, st, p, status, maps);
   kern<<<(unsigned)(2 * pairs), THREADS, kWholeSmSmem, st>>>(p, status, maps);
   return cudaGetLastError();
 }
@@ -627,9 +680,11 @@ bool operand_map(CUtensorMap* map, const void* base, long long rows, long long c
 
 }  // namespace
 
+constexpr int kTileChunks = 6;
 // The vocabulary's pieces.  A piece's d lies in memory between the two launches: at most kPieceBytes of it, which is
 // near the L2's size, but at least kPieceColumns, so that the sums of dh, read and written once a piece (8 bytes for
 // 6 V/pieces operations), stay below a few hundredths of the products' time.
+constexpr long long kLine = 64;  // rows of d begin on whole lines: a box's row is then one request to the L2, not two
 constexpr long long kPieceBytes = 128ll << 20, kPieceColumns = 8192;
 XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms) {
   XentBwdPlan g{};
@@ -646,7 +701,7 @@ XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms) {
   }
   g.direct = g.pieces == 1 && g.splits == 1;
   g.off_d = 256;
-  g.off_acc = g.off_d + up((size_t)p.R * std::min<long long>(g.columns, (long long)up(p.V, 8)) * 2, 256);
+  g.off_acc = g.off_d + up((size_t)p.R * std::min<long long>(g.columns, (long long)up(p.V, kLine)) * 2, 256);
   g.bytes = g.off_acc + (want_dh && !g.direct ? (size_t)g.splits * p.R * p.C * 4 : 0);
   return g;
 }
@@ -660,7 +715,7 @@ cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void
   Maps maps{};
   XentParams k{};
   const int m_tiles = tiles_of(p.R, TILE), n_tiles = tiles_of(p.V, TILE);
-  k.job[0] = Job{m_tiles, n_tiles, 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)p.V, p.C, 0, 0};
+  k.job[0] = make_job(m_tiles, n_tiles, 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, p.R, p.V, p.C);
   if (!operand_map(&maps.a[0], hidden, p.R, p.C, p.hidden_stride, true, &k.job[0].a_box) ||
       !operand_map(&maps.b[0], weight, p.V, p.C, p.weight_stride, true, &k.job[0].b_box))
     return cudaErrorInvalidValue;
@@ -677,9 +732,8 @@ cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void
   if (e != cudaSuccess) return e;
   int each = 32;
   while (each > 1 && each / 2 >= p.R) each /= 2;
-  xent_join_kernel<<<(unsigned)tiles_of(p.R, each), kJoinThreads, 0, st>>>(p.R, (int)p.V, 2 * n_tiles, each, k.part_rows, k.part,
-                                                                         k.given, tokens, loss, lse);
-  return cudaGetLastError();
+  return launch_behind(xent_join_kernel, (unsigned)tiles_of(p.R, each), kJoinThreads, 0, st, p.R, (int)p.V, 2 * n_tiles, each,
+                       k.part_rows, k.part, k.given, tokens, loss, lse);
 }
 
 cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const XentBwdIn& in, void* dhidden, void* dweight,
@@ -696,7 +750,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
   const int m_tiles = tiles_of(p.R, TILE), c_tiles = tiles_of(p.C, TILE);
   for (int piece = 0; piece < g.pieces; ++piece) {
     const long long v0 = (long long)piece * g.columns, cols = std::min<long long>(g.columns, p.V - v0);
-    const long long stride = (long long)up(cols, 8);
+    const long long stride = (long long)up(cols, kLine);
     const uint8_t* w = static_cast<const uint8_t*>(in.weight) + v0 * p.weight_stride * 2;
     XentParams k{};
     k.R = p.R;
@@ -711,20 +765,21 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     k.power = p.half ? power : nullptr;
     {
       Maps maps{};
-      k.job[0] = Job{m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, (int)p.R, (int)cols, p.C, 0, 0};
+      k.job[0] = make_job(m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, p.R, cols, p.C);
       if (!operand_map(&maps.a[0], in.hidden, p.R, p.C, p.hidden_stride, true, &k.job[0].a_box) ||
           !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, true, &k.job[0].b_box) ||
           !encode_matrix_map(&maps.out[0], d, p.R, cols, stride, 32, 64))
         return cudaErrorInvalidValue;
       const int pairs = pairs_for(k.job[0].tiles(), num_sms);
-      e = p.half ? launch<kGradLogits, true>(k, maps, pairs, status, st) : launch<kGradLogits, false>(k, maps, pairs, status, st);
+      e = p.half ? launch<kGradLogits, true>(k, maps, pairs, status, st, true)
+                 : launch<kGradLogits, false>(k, maps, pairs, status, st, piece > 0);
       if (e != cudaSuccess) return e;
     }
     Maps maps{};
     k.job[0] = k.job[1] = Job{};
     if (dhidden) {
       // (a last, short piece adds to the first sums only)
-      k.job[0] = Job{m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), 0, 0, 1, (int)p.R, p.C, (int)cols, 0, 0};
+      k.job[0] = make_job(m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), 0, 0, 1, p.R, p.C, cols);
       if (!operand_map(&maps.a[0], d, p.R, cols, stride, true, &k.job[0].a_box) ||
           !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, false, &k.job[0].b_box) ||
           !encode_matrix_map(&maps.out[0], dhidden, p.R, p.C, p.C, 32, 64) ||
@@ -733,7 +788,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
       k.accumulate = g.direct ? 0 : piece == 0 ? 1 : 2;
     }
     if (dweight) {
-      k.job[1] = Job{tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, (int)cols, p.C, (int)p.R, 0, 0};
+      k.job[1] = make_job(tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, cols, p.C, p.R);
       if (!operand_map(&maps.a[1], d, p.R, cols, stride, false, &k.job[1].a_box) ||
           !operand_map(&maps.b[1], in.hidden, p.R, p.C, p.hidden_stride, false, &k.job[1].b_box) ||
           !encode_matrix_map(&maps.out[1], dweight, p.V, p.C, p.C, 32, 64))
@@ -743,20 +798,20 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     const int pairs = pairs_for(a + b, num_sms);
     // the pairs with one tile of dh more get so many tiles of dW that all end together
     k.more = (int)(a % pairs);
-    const double la = k.job[0].splits ? (double)k.job[0].k_chunks / k.job[0].splits + 2 : 0, lb = k.job[1].k_chunks + 2;
+    // (in chunks; a tile of dW takes kTileChunks at least, the time in which its 128 KB go out to memory at a pair's share)
+    const double la = k.job[0].splits ? (double)k.job[0].k_chunks / k.job[0].splits + 2 : 0;
+    const double lb = std::max(k.job[1].k_chunks, kTileChunks) + 1;
     const double each = (a * la + b * lb) / pairs, mine = (double)(a / pairs + 1) * la;
     k.few = k.more ? (int)std::max(0.0, std::min((each - mine) / lb + 0.5, (double)(b / k.more))) : 0;
-    e = p.half ? launch<kGradients, true>(k, maps, pairs, status, st) : launch<kGradients, false>(k, maps, pairs, status, st);
+    e = p.half ? launch<kGradients, true>(k, maps, pairs, status, st, true)
+               : launch<kGradients, false>(k, maps, pairs, status, st, true);
     if (e != cudaSuccess) return e;
   }
   if (dhidden && !g.direct) {
     const long long n = p.R * p.C / 4;
     const unsigned blocks = (unsigned)((n + 255) / 256);
-    if (p.half)
-      xent_close_kernel<true><<<blocks, 256, 0, st>>>(n, g.splits, reinterpret_cast<float4*>(acc), power, static_cast<uint2*>(dhidden));
-    else
-      xent_close_kernel<false><<<blocks, 256, 0, st>>>(n, g.splits, reinterpret_cast<float4*>(acc), power, static_cast<uint2*>(dhidden));
-    e = cudaGetLastError();
+    e = launch_behind(p.half ? xent_close_kernel<true> : xent_close_kernel<false>, blocks, 256, 0, st, n, g.splits,
+                      reinterpret_cast<float4*>(acc), power, static_cast<uint2*>(dhidden));
   }
   return e;
 }
