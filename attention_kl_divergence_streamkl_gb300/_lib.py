@@ -114,8 +114,8 @@ SIGNATURES = {
     "streamkl_rotary": (_I, [_P, _P, RotaryShape, _P, _P, _P, _I, _S]),
     "streamkl_vocab_xent_fwd_workspace": (_I, [XentShape, ctypes.POINTER(_SZ)]),
     "streamkl_vocab_xent_fwd": (_I, [_P, _P, _P, XentShape, _F, _F, _P, _SZ, _S]),
-    "streamkl_vocab_xent_bwd_plan": (_I, [XentShape, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
-    "streamkl_vocab_xent_bwd_workspace": (_I, [XentShape, _I, ctypes.POINTER(_SZ)]),
+    "streamkl_vocab_xent_bwd_plan": (_I, [XentShape, _I, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
+    "streamkl_vocab_xent_bwd_workspace": (_I, [XentShape, _I, _I, ctypes.POINTER(_SZ)]),
     "streamkl_vocab_xent_bwd": (_I, [_P, _P, _P, _F, _F, _F, XentShape, _P, _P, _P, _SZ, _S]),
     "streamkl_status_string": (ctypes.c_char_p, [_I]),
     "streamkl_check_device_status": (_I, [_S]),
@@ -975,11 +975,11 @@ def _xent_inputs(hidden, weight, tokens, scale):
     return x, w, tokens if tokens.is_contiguous() else tokens.contiguous(), s, lead, dev, host
 
 
-def vocab_xent_plan(rows, vocab, channels, num_sms, want_dhidden=True):
+def vocab_xent_plan(rows, vocab, channels, num_sms, want_dhidden=True, want_dweight=True):
     """(pieces of the vocabulary, splits of dhidden's sums, workspace bytes) of the backward on a device with num_sms SMs."""
     a, b, n = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_size_t(0)
     _check(lib().streamkl_vocab_xent_bwd_plan(make_xent_shape(rows, vocab, channels), int(num_sms), bool(want_dhidden),
-                                              *map(ctypes.byref, (a, b, n))), "streamkl_vocab_xent_bwd_plan")
+                                              bool(want_dweight), *map(ctypes.byref, (a, b, n))), "streamkl_vocab_xent_bwd_plan")
     return a.value, b.value, n.value
 
 
@@ -1006,7 +1006,7 @@ def vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse=None, scale=1.0, w
     """Gradients (dhidden, dweight) of vocab_xent_fwd's outputs, contiguous and of the inputs' type, for upstream
     gradients g_loss and g_lse (fp32 like tokens; g_lse may be None); lse is the forward's.  One that is not wanted is None.
 
-    The same bits on every run.  Hidden states of rows without a gradient have to be finite all the same.
+    The same bits on every run.  Rows without a gradient have none whatever they hold, NaN included; weight has to be finite.
     """
     if want_dhidden and want_dweight:
         got = (_calls or calls()).vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse, scale)
@@ -1018,7 +1018,7 @@ def vocab_xent_bwd(hidden, weight, tokens, lse, g_loss, g_lse=None, scale=1.0, w
         raise ValueError("lse and g_loss are needed")
     if not want_dhidden and not want_dweight:
         return None, None
-    nbytes = _workspace_bytes("streamkl_vocab_xent_bwd_workspace", dev, s, bool(want_dhidden))
+    nbytes = _workspace_bytes("streamkl_vocab_xent_bwd_workspace", dev, s, bool(want_dhidden), bool(want_dweight))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     dh = torch.empty(hidden.shape, dtype=x.dtype, device=dev) if want_dhidden else None
     dw = torch.empty(weight.shape, dtype=x.dtype, device=dev) if want_dweight else None

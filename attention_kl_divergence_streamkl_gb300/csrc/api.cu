@@ -947,23 +947,23 @@ streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, 
       launch_xent_fwd(p, hidden, weight, tokens, loss, lse, workspace, sms, status, static_cast<cudaStream_t>(stream)));
 }
 
-streamkl_status streamkl_vocab_xent_bwd_plan(streamkl_xent_shape s, int num_sms, int want_dhidden, int* pieces, int* splits,
-                                             size_t* bytes) {
+streamkl_status streamkl_vocab_xent_bwd_plan(streamkl_xent_shape s, int num_sms, int want_dhidden, int want_dweight, int* pieces,
+                                             int* splits, size_t* bytes) {
   XentProblem p;
   streamkl_status v = xent_problem(s, &p);
   if (v != STREAMKL_OK) return v;
   if (!pieces || !splits || !bytes) return STREAMKL_ERR_INVALID;
   if (num_sms <= 0 && (v = device_sms(&num_sms)) != STREAMKL_OK) return v;
-  const XentBwdPlan g = xent_bwd_plan(p, want_dhidden != 0, num_sms);
+  const XentBwdPlan g = xent_bwd_plan(p, want_dhidden != 0, want_dweight != 0, num_sms);
   *pieces = g.pieces;
   *splits = g.splits;
   *bytes = p.R ? g.bytes : 0;
   return STREAMKL_OK;
 }
 
-streamkl_status streamkl_vocab_xent_bwd_workspace(streamkl_xent_shape s, int want_dhidden, size_t* bytes) {
+streamkl_status streamkl_vocab_xent_bwd_workspace(streamkl_xent_shape s, int want_dhidden, int want_dweight, size_t* bytes) {
   int pieces, splits;
-  return streamkl_vocab_xent_bwd_plan(s, 0, want_dhidden, &pieces, &splits, bytes);
+  return streamkl_vocab_xent_bwd_plan(s, 0, want_dhidden, want_dweight, &pieces, &splits, bytes);
 }
 
 streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, const long long* tokens, const float* lse,
@@ -981,7 +981,7 @@ streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, 
     return STREAMKL_ERR_INVALID;
   int sms = 0, *status = nullptr;
   if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
-  const XentBwdPlan g = xent_bwd_plan(p, dhidden != nullptr, sms);
+  const XentBwdPlan g = xent_bwd_plan(p, dhidden != nullptr, dweight != nullptr, sms);
   if (!workspace || !aligned16(workspace) || workspace_bytes < g.bytes) return STREAMKL_ERR_WORKSPACE;
   if ((v = status_ptr(&status)) != STREAMKL_OK) return v;
   return from_cuda(launch_xent_bwd(p, g, XentBwdIn{hidden, weight, tokens, lse, g_loss, g_lse}, dhidden, dweight, workspace,

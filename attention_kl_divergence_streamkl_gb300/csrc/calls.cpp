@@ -474,7 +474,7 @@ PyObject* vocab_xent_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
   {
     NoGil no_gil;
     size_t bytes = 0;
-    status = streamkl_vocab_xent_bwd_workspace(x.s, 1, &bytes);
+    status = streamkl_vocab_xent_bwd_workspace(x.s, 1, 1, &bytes);
     if (status == STREAMKL_OK) {
       const at::Tensor ws = workspace(bytes, x.index);
       dh = at::empty(x.hidden->sizes(), options(x.hidden->scalar_type(), x.index));

@@ -208,9 +208,9 @@ struct XentBwdPlan {
   int pieces, splits;   // of the vocabulary; of dh's sums over a piece
   long long columns;    // of a piece
   bool direct;          // dh needs no sums between launches
-  size_t off_d, off_acc, bytes;
+  size_t off_d, off_acc, off_clean, bytes;
 };
-XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms);
+XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, bool want_dw, int num_sms);
 struct XentBwdIn {
   const void *hidden, *weight;
   const long long* tokens;

@@ -18,6 +18,9 @@
 // to piece in fp32.  d is rounded to the inputs' type, as the other operand of the products that it enters is: half a
 // step of each term.  In fp16 it is multiplied by a power of two that brings the largest upstream gradient to 2^14, for
 // p's small values would be lost below 2^-24 otherwise.
+// A row without a gradient has d = 0 whatever its logits are, but 0 * NaN would still reach dW through the product: the first
+// launch notes rows without a gradient whose logits are not finite, and where there are any, dW is formed with a copy of the
+// hidden states that has zeros there.
 #include "attn.cuh"
 #include "pair.cuh"
 
@@ -93,11 +96,13 @@ struct XentParams {
   const float *lse, *g, *g_lse;
   // fp16: the power of two on d and its inverse, else null
   const float* power;
+  int* not_finite;    // d of the first piece: [rows / 32], 32 rows have such hidden states without a gradient
+  const int* clean;   // gradients: dW reads the copy of the hidden states
   int accumulate;     // dh goes to the fp32 sums: 0 stored straight to the output, 1 written, 2 added
 };
 
 struct Maps {
-  CUtensorMap a[2], b[2], out[2], acc;
+  CUtensorMap a[2], b[2], out[2], acc, clean;
 };
 
 // The tiles of a pair, in its order.  One job: every pairs-th, the tiles along m first, in groups of m_group.
@@ -237,13 +242,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == PRODUCER_WARP) {
     if (elect_one()) {
       const uint32_t full_even = in_block(full, 0);
+      const bool clean = KIND == kGradients && p.job[1].m_tiles && *p.clean;
       int s = 0;          // the stage that is filled next
       uint32_t lap = 0;   // how often the ring has been round
       bool ok = true;
       for (unsigned i = 0; ok && i < walk.n_all; ++i) {
         const Tile t = walk.tile(p, i);
         const Job& j = p.job[t.job];
-        const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
+        const CUtensorMap *ma = &maps.a[t.job], *mb = KIND == kGradients && t.job && clean ? &maps.clean : &maps.b[t.job];
         const int m0 = t.m * TILE + (int)rank * BM, n0 = t.n * TILE + (int)rank * BM;
         const Half a_half = half_of(m0, j.rows, j.a_mn, j.a_box), b_half = half_of(n0, j.cols, j.b_mn, j.b_box);
         // the bytes of both blocks
@@ -446,6 +452,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tc_fence_before();
             arrive_one_in(free_even + 8 * buf);
           }
+          if (q == 0 && half == 0 && t.n == 0 && p.not_finite) {
+            const bool bad = __any_sync(0xffffffffu, real && a == 0.f && !(fabsf(__uint_as_float(s0[0])) <= 3.4e38f));
+            if (row0 < p.R && elect_one()) p.not_finite[row0 / 32] = bad;
+            __syncwarp();
+          }
           const long long here = at - 64 * q;
           const bool given = __any_sync(0xffffffffu, here >= 0 && here < 64);
           const bool edge = __any_sync(0xffffffffu, seen < 64 * (q + 1));
@@ -621,6 +632,26 @@ __global__ void __launch_bounds__(1024) xent_power_kernel(long long R, float sca
   power[1] = ldexpf(1.f, -e);
 }
 
+// The copy of the hidden states with zeros in rows without a gradient, where one of these is not finite; 16 bytes a thread.
+__global__ void __launch_bounds__(256)
+    xent_clean_kernel(long long R, int V, int C, long long stride, const uint4* __restrict__ hidden, const long long* __restrict__ tokens,
+                      const float* __restrict__ g, const float* __restrict__ g_lse, const int* __restrict__ not_finite,
+                      int* __restrict__ clean, uint4* __restrict__ out) {
+  let_next_begin();
+  wait_for_previous();
+  bool bad = false;
+  for (long long i = threadIdx.x; i < (R + 31) / 32; i += 256) bad |= __ldcg(not_finite + i) != 0;
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *clean = bad;
+  if (!bad) return;
+  for (long long r = blockIdx.x; r < R; r += gridDim.x) {
+    const long long token = tokens[r];
+    const float a = (token >= 0 && token < V ? g[r] : 0.f) + (g_lse ? g_lse[r] : 0.f);
+    for (int i = threadIdx.x; i < C / 8; i += 256)
+      out[r * (C / 8) + i] = a == 0.f ? make_uint4(0u, 0u, 0u, 0u) : hidden[r * (stride / 8) + i];
+  }
+}
+
 // dh from the splits' fp32 sums, added in their order.
 template <bool HALF>
 __global__ void __launch_bounds__(256)
@@ -686,7 +717,7 @@ constexpr int kTileChunks = 6;
 // 6 V/pieces operations), stay below a few hundredths of the products' time.
 constexpr long long kLine = 64;  // rows of d begin on whole lines: a box's row is then one request to the L2, not two
 constexpr long long kPieceBytes = 128ll << 20, kPieceColumns = 8192;
-XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms) {
+XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, bool want_dw, int num_sms) {
   XentBwdPlan g{};
   const long long most = std::max(kPieceColumns, kPieceBytes / (2 * std::max(p.R, 1ll)));
   g.pieces = (int)((p.V + most - 1) / most);
@@ -700,9 +731,10 @@ XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, int num_sms) {
     g.splits = (int)std::max(1ll, std::min((num_sms / 2) / tiles, chunks / 16));
   }
   g.direct = g.pieces == 1 && g.splits == 1;
-  g.off_d = 256;
+  g.off_d = up(256 + (size_t)tiles_of(p.R, 32) * sizeof(int), 256);
   g.off_acc = g.off_d + up((size_t)p.R * std::min<long long>(g.columns, (long long)up(p.V, kLine)) * 2, 256);
-  g.bytes = g.off_acc + (want_dh && !g.direct ? (size_t)g.splits * p.R * p.C * 4 : 0);
+  g.off_clean = g.off_acc + (want_dh && !g.direct ? up((size_t)g.splits * p.R * p.C * 4, 256) : 0);
+  g.bytes = g.off_clean + (want_dw ? (size_t)p.R * p.C * 2 : 0);
   return g;
 }
 
@@ -742,6 +774,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
   float* power = reinterpret_cast<float*>(ws);
   uint8_t* d = ws + g.off_d;
   float* acc = reinterpret_cast<float*>(ws + g.off_acc);
+  int *clean = reinterpret_cast<int*>(ws + 128), *not_finite = reinterpret_cast<int*>(ws + 256);
   cudaError_t e = cudaSuccess;
   if (p.half) {
     xent_power_kernel<<<1, 1024, 0, st>>>(p.R, p.scale, in.g, in.g_lse, power);
@@ -763,6 +796,8 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     k.g = in.g;
     k.g_lse = in.g_lse;
     k.power = p.half ? power : nullptr;
+    k.not_finite = dweight && piece == 0 ? not_finite : nullptr;
+    k.clean = clean;
     {
       Maps maps{};
       k.job[0] = make_job(m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, p.R, cols, p.C);
@@ -773,6 +808,12 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
       const int pairs = pairs_for(k.job[0].tiles(), num_sms);
       e = p.half ? launch<kGradLogits, true>(k, maps, pairs, status, st, true)
                  : launch<kGradLogits, false>(k, maps, pairs, status, st, piece > 0);
+      if (e != cudaSuccess) return e;
+    }
+    if (dweight && piece == 0) {
+      e = launch_behind(xent_clean_kernel, (unsigned)std::min<long long>(p.R, 2ll * num_sms), 256, 0, st, p.R, (int)p.V, p.C,
+                        p.hidden_stride, static_cast<const uint4*>(in.hidden), in.tokens, in.g, in.g_lse, not_finite, clean,
+                        reinterpret_cast<uint4*>(ws + g.off_clean));
       if (e != cudaSuccess) return e;
     }
     Maps maps{};
@@ -791,6 +832,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
       k.job[1] = make_job(tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, cols, p.C, p.R);
       if (!operand_map(&maps.a[1], d, p.R, cols, stride, false, &k.job[1].a_box) ||
           !operand_map(&maps.b[1], in.hidden, p.R, p.C, p.hidden_stride, false, &k.job[1].b_box) ||
+          !operand_map(&maps.clean, ws + g.off_clean, p.R, p.C, p.C, false, &k.job[1].b_box) ||
           !encode_matrix_map(&maps.out[1], dweight, p.V, p.C, p.C, 32, 64))
         return cudaErrorInvalidValue;
     }

@@ -483,11 +483,13 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  *   contiguous, of `dtype`; one of them may be NULL where it is not wanted.  d enters the
  *   products rounded to `dtype`; sums are fp32, dhidden and dweight are rounded once.  What
  *   several blocks add up is added in a fixed order: the same bits on every run.  A row whose
- *   gradients are 0 takes part in dweight's sum with zeros: its hidden states have to be finite.
+ *   gradients are 0 has dhidden 0 and no part in dweight, whatever its hidden states are, NaN
+ *   included; the weight has to be finite.
  * Workspaces (16-byte aligned): forward, 16 bytes per row and 256 columns; backward, a piece
- *   of d and fp32 sums of dhidden: streamkl_vocab_xent_bwd_plan gives the number of the
- *   vocabulary's pieces, the splits of dhidden's sums and the bytes for any SM count
- *   (num_sms <= 0: the current device; with num_sms > 0 a pure host rule).
+ *   of d, fp32 sums of dhidden and, for dweight, room for a copy of hidden:
+ *   streamkl_vocab_xent_bwd_plan gives the number of the vocabulary's pieces, the splits of
+ *   dhidden's sums and the bytes for any SM count (num_sms <= 0: the current device; with
+ *   num_sms > 0 a pure host rule).
  */
 typedef struct {
   long long rows, vocab;
@@ -498,9 +500,9 @@ typedef struct {
 streamkl_status streamkl_vocab_xent_fwd_workspace(streamkl_xent_shape s, size_t* bytes);
 streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, const long long* tokens, streamkl_xent_shape s,
                                         float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);
-streamkl_status streamkl_vocab_xent_bwd_plan(streamkl_xent_shape s, int num_sms, int want_dhidden, int* pieces, int* splits,
-                                             size_t* bytes);
-streamkl_status streamkl_vocab_xent_bwd_workspace(streamkl_xent_shape s, int want_dhidden, size_t* bytes);
+streamkl_status streamkl_vocab_xent_bwd_plan(streamkl_xent_shape s, int num_sms, int want_dhidden, int want_dweight, int* pieces,
+                                             int* splits, size_t* bytes);
+streamkl_status streamkl_vocab_xent_bwd_workspace(streamkl_xent_shape s, int want_dhidden, int want_dweight, size_t* bytes);
 streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, const long long* tokens, const float* lse,
                                         const float* g_loss, const float* g_lse, streamkl_xent_shape s, void* dhidden,
                                         void* dweight, void* workspace, size_t workspace_bytes, void* stream);

@@ -168,6 +168,36 @@ def test_rows_that_are_not_finite():
     check(h, w, t)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("R,V", [(40, 500), (300, 3000), (9000, 17000)])
+def test_rows_without_a_gradient_may_hold_anything(R, V, dtype):
+    """NaN and infinities in the hidden states of rows that have no token and no upstream gradient: nothing of them is seen."""
+    h, w, t = inputs(R, 72, V, dtype, 18, none=0.3)
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    g = torch.rand(R, generator=gen, device="cuda") / R
+    g[5] = 0.0
+    t[5], t[0] = 3, 1
+    _, lse = skl.vocab_xent_fwd(h, w, t)
+    off = (t < 0) | (g == 0)
+    for what in (float("nan"), float("inf"), -float("inf")):
+        bad = h.clone()
+        bad[off, 7] = what
+        bad[-1, 3] = h[-1, 3] if not bool(off[-1]) else what
+        loss, z = skl.vocab_xent_fwd(bad, w, t)
+        assert bool((loss[t < 0] == 0).all())
+        got = skl.vocab_xent_bwd(bad, w, t, z, g)
+        clean = torch.where(off[:, None], torch.zeros_like(h), h)
+        rh, rw, bh, bw = backward(clean, w, torch.where(off, -1, t), g, None, 1.0)
+        within(got[0], rh, bh, f"dhidden, {what}")
+        within(got[1], rw, bw, f"dweight, {what}")
+        assert not bool(got[0][off].any())
+        strided = torch.full((R, 80), float("nan"), device="cuda", dtype=h.dtype)
+        strided[:, :72] = bad
+        assert all(torch.equal(a, b) for a, b in zip(got, skl.vocab_xent_bwd(strided[:, :72], w, t, z, g)))
+    ref = skl.vocab_xent_bwd(h, w, t, lse, g)
+    within(ref[1], rw, bw, "dweight, finite")
+
+
 def test_logits_far_from_zero_keep_the_loss():
     """A vector that all rows of the weight share moves every logit by thousands, and the loss by nothing."""
     h, w, t = inputs(64, 64, 1000, "bf16", 8, none=0.0)
