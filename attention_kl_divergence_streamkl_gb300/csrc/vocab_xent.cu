@@ -436,6 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           a = g + (p.g_lse ? p.g_lse[row] * p.scale * power : 0.f);
         }
+        const bool none = g == 0.f && a == 0.f;
         const int seen = real ? p.job[0].cols - col0 : 0;  // d is 0 past the piece; what is past the rows is not stored
         if (!mbar_wait_warp(there + 8 * buf, parity, status, abort_flag)) break;
         ++used;
@@ -453,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             arrive_one_in(free_even + 8 * buf);
           }
           if (q == 0 && half == 0 && t.n == 0 && p.not_finite) {
-            const bool bad = __any_sync(0xffffffffu, real && a == 0.f && !(fabsf(__uint_as_float(s0[0])) <= 3.4e38f));
+            const bool bad = __any_sync(0xffffffffu, real && none && !(fabsf(__uint_as_float(s0[0])) <= 3.4e38f));
             if (row0 < p.R && elect_one()) p.not_finite[row0 / 32] = bad;
             __syncwarp();
           }
@@ -461,21 +462,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const bool given = __any_sync(0xffffffffu, here >= 0 && here < 64);
           const bool edge = __any_sync(0xffffffffu, seen < 64 * (q + 1));
           const float2 cc = make_float2(p.c, p.c), nl = make_float2(-lse2, -lse2), aa = make_float2(a, a);
-#pragma unroll
-          for (int k = 0; k < 64; k += 2) {
+          auto d_of = [&](int k) {
             const uint32_t* s = k < 32 ? s0 : s1;
             const float2 x = ffma2(make_float2(__uint_as_float(s[k & 31]), __uint_as_float(s[(k & 31) + 1])), cc, nl);
-            float2 d = fmul2(make_float2(ex2(x.x), ex2(x.y)), aa);
-            if (a == 0.f) d = make_float2(0.f, 0.f);  // no gradient is none, whatever the logits are
-            if (given) {
+            return fmul2(make_float2(ex2(x.x), ex2(x.y)), aa);
+          };
+          if (!given && !edge) {  // most tiles
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+              const float2 d = d_of(k);
+              w[k / 2] = pack16<HALF>(d.x, d.y);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 64; k += 2) {
+              float2 d = d_of(k);
               if (here == k) d.x -= g;
               if (here == k + 1) d.y -= g;
-            }
-            if (edge) {
               if (64 * q + k >= seen) d.x = 0.f;
               if (64 * q + k + 1 >= seen) d.y = 0.f;
+              w[k / 2] = pack16<HALF>(d.x, d.y);
             }
-            w[k / 2] = pack16<HALF>(d.x, d.y);
+          }
+          if (__any_sync(0xffffffffu, none)) {  // no gradient is none, whatever the logits are
+#pragma unroll
+            for (int k = 0; k < 32; ++k) w[k] = none ? 0u : w[k];
           }
           if (q == 0) stage_free();
           put(q, w);
@@ -646,9 +657,9 @@ __global__ void __launch_bounds__(256)
   if (!bad) return;
   for (long long r = blockIdx.x; r < R; r += gridDim.x) {
     const long long token = tokens[r];
-    const float a = (token >= 0 && token < V ? g[r] : 0.f) + (g_lse ? g_lse[r] : 0.f);
+    const bool none = (token < 0 || token >= V || g[r] == 0.f) && (!g_lse || g_lse[r] == 0.f);
     for (int i = threadIdx.x; i < C / 8; i += 256)
-      out[r * (C / 8) + i] = a == 0.f ? make_uint4(0u, 0u, 0u, 0u) : hidden[r * (stride / 8) + i];
+      out[r * (C / 8) + i] = none ? make_uint4(0u, 0u, 0u, 0u) : hidden[r * (stride / 8) + i];
   }
 }
 

@@ -232,6 +232,17 @@ def test_strides_shapes_and_types_of_tokens():
     assert none[0].shape == (0, 64) and not bool(none[1].any())
 
 
+def test_gradients_that_cancel():
+    """g' = -g: the probabilities have no gradient, the given token has."""
+    h, w, t = inputs(50, 64, 300, "bf16", 20, none=0.0)
+    _, lse = skl.vocab_xent_fwd(h, w, t)
+    g = torch.rand(50, device="cuda")
+    dh, dw = skl.vocab_xent_bwd(h, w, t, lse, g, -g)
+    rh, rw, bh, bw = backward(h, w, t, g, -g, 1.0)
+    within(dh, rh, bh, "dhidden")
+    within(dw, rw, bw, "dweight")
+
+
 def test_one_gradient_alone():
     h, w, t = inputs(400, 264, 900, "fp16", 10)
     _, lse = skl.vocab_xent_fwd(h, w, t)
