@@ -21,6 +21,14 @@
 // A row without a gradient has d = 0 whatever its logits are, but 0 * NaN would still reach dW through the product: the first
 // launch notes rows without a gradient whose logits are not finite, and where there are any, dW is formed with a copy of the
 // hidden states that has zeros there.
+//
+// Measured: forward of 8192 x 131072 x 4096 4.73 to 5.0 ms on different cards, 1.76 to 1.86 PFLOP/s, of 8 rows 178 to 195 us,
+// 5.5 to 6 TB/s; gradients of 4096 x 131072 x 2048 3.75 to 4.0 ms, 1.65 to 1.76 PFLOP/s: what the power limit leaves a plain matrix
+// product (1.71).  With few rows, pieces of W come from memory, and a chunk's products take 650 to 900 cycles where 606 are
+// what the tensor core needs; a launch's first 4 us (the ring's first filling) and last 3.5 us (the last tile's epilogue) stand
+// alone: gradients of 333 x 50021 x 1000 in fp16 135 us, floor 52.  Built and not kept: pieces of W brought to the L2 ahead of
+// their loads, by TMA or by a warp of its own (forward of 8 x 131072 x 4096 186 -> 213 and 287 us: requests to the L2 are what
+// it waits for), chunks of 128 in three stages (as fast), other orders of the summed index for each pair (slower).
 #include "attn.cuh"
 #include "pair.cuh"
 
@@ -45,7 +53,7 @@ static_assert(OFF_BAR + BAR_SLOT + 16 + 1024 <= kWholeSmSmem, "shared memory");
 
 // The tensor core's own additions cut off what does not fit, so a sum loses with every one of its C / 16 steps: 5e-7 of a
 // logit's terms for 32 of them, eight times that for 4096 channels in one go.  The forward, whose results are fp32, adds up
-// so many chunks at a time and then goes on in registers.  (8192 x 131072 x 4096 ... us in one go, ... with 8.)
+// so many chunks at a time and then goes on in registers.  (8192 x 131072 x 4096: 4727 us in one go, 4760 with 8 chunks.)
 constexpr int kFlush = 8;
 
 enum Kind { kForward, kGradLogits, kGradients };
@@ -82,8 +90,8 @@ struct Tile {
 
 struct XentParams {
   Job job[2];  // kGradients: dh, dW; else only the first
-  // kGradients: pairs below `more` take one tile of the first job more, and `few` of the second; the others share the rest
-  int more, few;
+  // kGradients: pairs below `more` take one tile of the first job more; meanwhile the others take `early` each of the second
+  int more, early;
   long long R;
   int V, v0;          // the vocabulary, and the first column of the piece
   float scale, c;     // c = scale log2(e)
@@ -106,7 +114,9 @@ struct Maps {
 };
 
 // The tiles of a pair, in its order.  One job: every pairs-th, the tiles along m first, in groups of m_group.
-// Two: the pair's share of the first job's tiles, then a run of the second's.
+// Two: the pair's share of the first job's tiles, then of the second's, in rounds too, so that the tiles at work at a time
+// are neighbours and read the same rows of d (a run of tiles to each pair read a piece of d from memory eight times,
+// 1.17 GB for 16384 columns, 4096 rows and 2048 channels: gradients of 4096 x 131072 x 2048 4320 us, 3860 in rounds).
 __device__ __forceinline__ Tile job_tile(const Job& j, int job, unsigned i) {
   Tile t;
   t.job = job;
@@ -131,38 +141,36 @@ __device__ __forceinline__ Tile job_tile(const Job& j, int job, unsigned i) {
   return t;
 }
 struct Walk {
-  unsigned first, n_first, from, n_all, pairs;
+  unsigned pair, pairs, n_first, n_all;
+  unsigned early, others, index;  // of the second job: tiles before the common rounds, who has such, the number among them
   template <Kind KIND>
   __device__ __forceinline__ static Walk make(const XentParams& p, unsigned pair, unsigned pairs) {
-    Walk w;
+    Walk w{};
     const unsigned a = (unsigned)p.job[0].tiles();
-    w.first = pair;
+    w.pair = pair;
     w.pairs = pairs;
-    w.n_first = pair < a ? (a - pair + pairs - 1) / pairs : 0;
-    w.from = 0;
-    w.n_all = w.n_first;
+    w.n_first = w.n_all = pair < a ? (a - pair + pairs - 1) / pairs : 0;
     if (KIND == kGradients) {
-      const unsigned more = (unsigned)p.more, few = (unsigned)p.few;
-      const unsigned b = (unsigned)p.job[1].tiles(), rest = b - few * more, others = pairs - more;
-      if (pair < more) {
-        w.from = few * pair;
-        w.n_all += few;
-      } else {
-        w.from = few * more + (unsigned)((unsigned long long)rest * (pair - more) / others);
-        w.n_all += few * more + (unsigned)((unsigned long long)rest * (pair - more + 1) / others) - w.from;
-      }
+      const unsigned more = (unsigned)p.more;
+      w.others = pairs - more;
+      w.index = pair - more;
+      w.early = pair < more ? 0 : (unsigned)p.early;
+      const unsigned common = (unsigned)p.job[1].tiles() - (unsigned)p.early * w.others;
+      w.n_all += w.early + (pair < common ? (common - pair + pairs - 1) / pairs : 0);
     }
     return w;
   }
   __device__ __forceinline__ Tile tile(const XentParams& p, unsigned i) const {
-    if (i < n_first) return job_tile(p.job[0], 0, first + i * pairs);
-    return job_tile(p.job[1], 1, from + i - n_first);
+    if (i < n_first) return job_tile(p.job[0], 0, pair + i * pairs);
+    const unsigned k = i - n_first;
+    if (k < early) return job_tile(p.job[1], 1, k * others + index);
+    return job_tile(p.job[1], 1, (unsigned)p.early * others + (k - early) * pairs + pair);
   }
 };
 
 // What a block loads of its half of an operand for a chunk: `loads` boxes and their bytes.  Rows that do not exist are
 // left out, by smaller boxes and fewer of them: TMA's zeros for them come at the price of loads, from one place of the L2
-// for all (8 x 131072 x 4096: 298 us with whole boxes, ... so).  What then lies in shared memory reaches only rows and
+// for all (8 x 131072 x 4096: 298 us with whole boxes, 186 so).  What then lies in shared memory reaches only rows and
 // columns of the tile that nobody reads.
 struct Half {
   int loads;
@@ -321,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    // A warp's 32 rows leave through 8 KB, 128 columns of 2 bytes or 64 of 4, as two boxes under one fence (a fence for each
-    // 64 columns: 4750 cycles a tile, ... so).
+    // A warp's 32 rows leave through 8 KB, 128 columns of 2 bytes or 64 of 4, as two boxes under one fence (a fence
+    // for each 64 columns: 4700 cycles a tile of dW where its sum is one chunk, 4100 so).
     const uint32_t stage = sb + OFF_OUT + warp * 8192;
     auto stage_free = [&]() {  // the stores before have read it
       if (elect_one()) bulk_wait_read();
@@ -722,12 +730,15 @@ bool operand_map(CUtensorMap* map, const void* base, long long rows, long long c
 
 }  // namespace
 
-constexpr int kTileChunks = 6;
-// The vocabulary's pieces.  A piece's d lies in memory between the two launches: at most kPieceBytes of it, which is
-// near the L2's size, but at least kPieceColumns, so that the sums of dh, read and written once a piece (8 bytes for
-// 6 V/pieces operations), stay below a few hundredths of the products' time.
+// What a tile takes, in the time of a chunk's products: its chunks and kMoreChunks for its epilogue, which the products
+// share the shared memory with; a tile of dW, whose 128 KB go out to memory at a pair's share of its rate, kTileChunks at least.
+constexpr int kTileChunks = 7, kMoreChunks = 4;
+// The vocabulary's pieces.  A piece's d lies in memory between the two launches: at most kPieceBytes of it, but at least
+// kPieceColumns, so that the sums of dh, read and written once a piece (8 bytes for 6 V / pieces operations), stay below
+// a few hundredths of the products' time.  Measured, gradients of 4096 x 131072 x 2048 and 8192 x 131072 x 4096, us: 64 MB
+// 3956, 15694; 128 MB 3864, 15723; 256 MB 3756, 15331; 512 MB 3745, 15367 -- each launch ends with a wave that is not full.
 constexpr long long kLine = 64;  // rows of d begin on whole lines: a box's row is then one request to the L2, not two
-constexpr long long kPieceBytes = 128ll << 20, kPieceColumns = 8192;
+constexpr long long kPieceBytes = 256ll << 20, kPieceColumns = 8192;
 XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, bool want_dw, int num_sms) {
   XentBwdPlan g{};
   const long long most = std::max(kPieceColumns, kPieceBytes / (2 * std::max(p.R, 1ll)));
@@ -849,13 +860,11 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     }
     const long long a = k.job[0].tiles(), b = k.job[1].tiles();
     const int pairs = pairs_for(a + b, num_sms);
-    // the pairs with one tile of dh more get so many tiles of dW that all end together
+    // while some pairs have one more tile of dh, the others take so many of dW
     k.more = (int)(a % pairs);
-    // (in chunks; a tile of dW takes kTileChunks at least, the time in which its 128 KB go out to memory at a pair's share)
-    const double la = k.job[0].splits ? (double)k.job[0].k_chunks / k.job[0].splits + 2 : 0;
-    const double lb = std::max(k.job[1].k_chunks, kTileChunks) + 1;
-    const double each = (a * la + b * lb) / pairs, mine = (double)(a / pairs + 1) * la;
-    k.few = k.more ? (int)std::max(0.0, std::min((each - mine) / lb + 0.5, (double)(b / k.more))) : 0;
+    const double la = k.job[0].splits ? (double)k.job[0].k_chunks / k.job[0].splits + kMoreChunks : 0;
+    const double lb = std::max(k.job[1].k_chunks + kMoreChunks, kTileChunks);
+    k.early = k.more ? (int)std::min(la / lb + 0.5, (double)(b / (pairs - k.more))) : 0;
     e = p.half ? launch<kGradients, true>(k, maps, pairs, status, st, true)
                : launch<kGradients, false>(k, maps, pairs, status, st, true);
     if (e != cudaSuccess) return e;
