@@ -29,7 +29,6 @@
 // not kept: Q and dO of the dQ block as operands in TMEM (64 KB less
 // shared-memory traffic a tile pair, and 3% slower).
 #include "attn.cuh"
-#include "pair.cuh"
 
 namespace skl {
 namespace {
@@ -281,7 +280,6 @@ __global__ void __launch_bounds__(256)
                           unsigned n_counters, int padded) {
   constexpr int LANES = D / 8, ROWS = 256 / LANES;
   static_assert(BT % (ROWS * kDiffRowsEach) == 0, "a block's rows are one head's");
-  let_next_begin();
   for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
   const int step = padded / kDiffRowsEach;
   const unsigned per_head = (unsigned)step / ROWS;
@@ -1019,7 +1017,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     int* status, const __grid_constant__ BwdMaps maps, const AttnBwdPlan plan,
                     float4* __restrict__ kv_parts, unsigned* __restrict__ kv_counters, float4* __restrict__ q_parts,
                     unsigned* __restrict__ q_counters) {
-  wait_for_previous();  // a difference's rows' kernel
   const unsigned x = blockIdx.x, first = plan.q_first ? plan.q_blocks : plan.kv_blocks;
   const bool is_q = plan.q_first ? x < first : x >= first;
   const unsigned blk = x < first ? x : x - first;
@@ -1074,9 +1071,6 @@ cudaError_t launch_d(const AttnProblem& p, const AttnBwdPlan& plan, AttnBwdIn in
   constexpr int smem = kWholeSmSmem;
   auto kern = attn_bwd_kernel<D>;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  if (p.diff)
-    return launch_behind(kern, plan.q_blocks + plan.kv_blocks, THREADS, smem, st, p, row_s, row_d, w.padded, status, m, plan,
-                         static_cast<float4*>(w.kv_parts), w.kv_counters, static_cast<float4*>(w.q_parts), w.q_counters);
   kern<<<plan.q_blocks + plan.kv_blocks, THREADS, smem, st>>>(
       p, row_s, row_d, w.padded, status, m, plan, static_cast<float4*>(w.kv_parts), w.kv_counters,
       static_cast<float4*>(w.q_parts), w.q_counters);

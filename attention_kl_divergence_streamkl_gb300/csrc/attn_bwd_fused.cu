@@ -26,7 +26,6 @@
 // 0.69 against 0.68 ms).  At D = 64: 8 heads, N8192, non-causal 0.31 against 0.43 ms; with red.add from registers instead of
 // staging and bulk reductions 0.39.
 #include "attn.cuh"
-#include "pair.cuh"
 
 namespace skl {
 namespace {
@@ -82,7 +81,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                           int* status, const __grid_constant__ Maps maps, const AttnBwdPlan plan, float4* __restrict__ part_acc,
                           unsigned* __restrict__ counters) {
   using L = Smem;
-  wait_for_previous();  // a difference's rows' kernel
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzled tiles' alignment; nothing lies before it
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -497,17 +495,10 @@ cudaError_t launch_attn_bwd_fused(const AttnProblem& p, const AttnBwdPlan& plan,
   constexpr int smem = kWholeSmSmem;
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_fused_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  if (p.diff) {
-    e = launch_behind(attn_bwd_fused_kernel, plan.kv_blocks, THREADS, smem, st, p, static_cast<const uint4*>(w.row_s),
-                      static_cast<const uint4*>(w.row_d), w.padded, status, m, plan, static_cast<float4*>(w.kv_parts),
-                      w.kv_counters);
-  } else {
-    attn_bwd_fused_kernel<<<plan.kv_blocks, THREADS, smem, st>>>(p, static_cast<const uint4*>(w.row_s),
-                                                                static_cast<const uint4*>(w.row_d), w.padded, status, m, plan,
-                                                                static_cast<float4*>(w.kv_parts), w.kv_counters);
-    e = cudaGetLastError();
-  }
-  if (e != cudaSuccess) return e;
+  attn_bwd_fused_kernel<<<plan.kv_blocks, THREADS, smem, st>>>(p, static_cast<const uint4*>(w.row_s),
+                                                              static_cast<const uint4*>(w.row_d), w.padded, status, m, plan,
+                                                              static_cast<float4*>(w.kv_parts), w.kv_counters);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   attn_dq_out_kernel<<<(unsigned)((p.rows * (D / 8) + 255) / 256), 256, 0, st>>>(p, w.acc, w.padded,
                                                                                static_cast<__nv_bfloat16*>(dq));
   return cudaGetLastError();

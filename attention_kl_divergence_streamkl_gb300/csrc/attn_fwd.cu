@@ -49,7 +49,6 @@
 // the whole group.  Few tiles: the keys are split over blocks, each writes its
 // (m, l, O) in fp32 and a second kernel merges them.
 #include "attn.cuh"
-#include "pair.cuh"
 
 namespace skl {
 namespace {
@@ -235,7 +234,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   whole_tmem(reinterpret_cast<volatile uint32_t*>(smem + L::OFF_BAR + L::BAR_SLOT), status);
   constexpr uint32_t tmem = 0;
-  if (DIFF) let_next_begin();  // the merge
 
   if (warp >= SOFTMAX_WARPS) {
     setmaxnreg_dec<kRegsOther>();
@@ -632,7 +630,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32 * (DIFF ? 2 : 1))
   const long long row = DIFF ? (2 * (blockIdx.x / (long long)p.NQ) + map) * p.NQ + n : blockIdx.x;
   float *weight = weights[map], *warp_m = warps_m[map], *warp_l = warps_l[map];
   Cols(*sums)[32] = all_sums[map];
-  if (DIFF) wait_for_previous();
   auto load = [&](int s) { return *(reinterpret_cast<const Cols*>(part_o + ((size_t)s * p.rows + row) * D) + lane); };
   Cols first[kMergeAhead];
 #pragma unroll
@@ -743,10 +740,8 @@ cudaError_t launch_d(const AttnProblem& p, const void* q, const void* k, const v
   const long long blocks = attn_fwd_items(p) * p.splits;
   kern<<<(unsigned)blocks, THREADS, smem, st>>>(p, lse, part_o, part_ml, status, mq, mk, mv, mo, mrest, mdiff);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  if (DIFF)
-    return launch_behind(attn_merge_kernel<D, DIFF>, (unsigned)(p.rows / 2), kMergeWarps * 64, 0, st, p, part_o, part_ml, out, lse,
-                         static_cast<__nv_bfloat16*>(diff));
-  attn_merge_kernel<D, DIFF><<<(unsigned)p.rows, kMergeWarps * 32, 0, st>>>(p, part_o, part_ml, out, lse, nullptr);
+  attn_merge_kernel<D, DIFF><<<(unsigned)(DIFF ? p.rows / 2 : p.rows), kMergeWarps * 32 * (DIFF ? 2 : 1), 0, st>>>(
+      p, part_o, part_ml, out, lse, static_cast<__nv_bfloat16*>(diff));
   return cudaGetLastError();
 }
 
