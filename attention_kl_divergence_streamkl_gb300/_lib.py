@@ -5,7 +5,8 @@ this module only checks tensor metadata, allocates outputs and workspaces
 through PyTorch's CUDA allocator, and passes raw pointers and the current CUDA
 stream to the C entry points of the same names.  There is no CPU fallback: if
 the library is missing, every call raises.  The entry points that a model calls
-per layer and per token (attn_fwd, attn_bwd, logprobs_fwd, logprobs_bwd) go to
+per layer and per token (attn_fwd, attn_bwd, diff_attn_fwd, diff_attn_bwd, rotary_fwd,
+rotary_bwd, logprobs_fwd, logprobs_bwd, vocab_xent_fwd, vocab_xent_bwd) go to
 the native caller first (csrc/calls.cpp, _calls.so), which does the same for
 tensors that need no copy in a third of the time, and come back here for the rest.
 
@@ -841,10 +842,6 @@ def logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None, scale=1.0
 def _rotary(tensors, plan, positions, offset, interleaved, inverse, out):
     """Turns q and k (either may be None) by their positions; see rotary_fwd."""
     q, k = tensors
-    if out is None:
-        got = (_calls or calls()).rotary(q, k, plan.turns, plan.dim, plan.amplitude, positions, offset, interleaved, inverse)
-        if got is not None:
-            return got
     one = q if q is not None else k
     if one is None:
         raise ValueError("q or k is needed")
@@ -924,11 +921,19 @@ def rotary_fwd(q, k, plan, positions=None, offset=0, interleaved=False, out=None
     with interleaved 2 i and 2 i + 1.  out: (q_out, k_out) to write to, for example q and k themselves or a cache's rows
     (it may overlap nothing else); an entry may be None.
     """
+    if out is None:
+        got = (_calls or calls()).rotary(q, k, plan.turns, plan.dim, plan.amplitude, positions, offset, interleaved, False)
+        if got is not None:
+            return got
     return _rotary((q, k), plan, positions, offset, interleaved, False, out)
 
 
 def rotary_bwd(dq, dk, plan, positions=None, offset=0, interleaved=False, out=None):
     """The gradients of rotary_fwd's q and k from those of its results: turned back by the same positions."""
+    if out is None:
+        got = (_calls or calls()).rotary(dq, dk, plan.turns, plan.dim, plan.amplitude, positions, offset, interleaved, True)
+        if got is not None:
+            return got
     return _rotary((dq, dk), plan, positions, offset, interleaved, True, out)
 
 

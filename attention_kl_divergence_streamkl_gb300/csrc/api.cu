@@ -295,7 +295,7 @@ using namespace skl;
 
 extern "C" {
 
-int streamkl_version(void) { return 200; }
+int streamkl_version(void) { return 300; }
 
 const char* streamkl_status_string(streamkl_status st) {
   switch (st) {

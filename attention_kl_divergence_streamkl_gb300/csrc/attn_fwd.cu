@@ -123,6 +123,8 @@ __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32
 // DIFF: heads 2 i and 2 i + 1 are the two maps of a difference.  A block's tiles are then the same 128 rows of both, so that
 // they share K and V and the difference is formed at the end, in fp32, from both accumulators (the second's through shared
 // memory); where heads are packed both maps' rows lie in the tile.  Without REST only the difference leaves the SM.
+// (B2 16 pairs HK8 N4096 D128 causal 222 us, attention of the 32 heads 232; one token over 65536 keys, B8 16 pairs HK8 367 us, 5.9
+// TB/s.)
 template <int D, bool FRESH, bool REST, bool DIFF>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_fwd_kernel(const AttnProblem p, float* __restrict__ out_lse,
