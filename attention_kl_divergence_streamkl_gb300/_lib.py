@@ -113,6 +113,7 @@ SIGNATURES = {
     "streamkl_diff_attn_bwd_workspace": (_I, [DiffAttnShape, _I, ctypes.POINTER(_SZ)]),
     "streamkl_diff_attn_bwd": (_I, [_P, _P, _P, _P, _F, _P, _F, DiffAttnShape, _P, _P, _P, _F, _I, _P, _SZ, _S]),
     "streamkl_rotary": (_I, [_P, _P, RotaryShape, _P, _P, _P, _I, _S]),
+    "streamkl_vocab_xent_fwd_plan": (_I, [XentShape, _I, ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
     "streamkl_vocab_xent_fwd_workspace": (_I, [XentShape, ctypes.POINTER(_SZ)]),
     "streamkl_vocab_xent_fwd": (_I, [_P, _P, _P, XentShape, _F, _F, _P, _SZ, _S]),
     "streamkl_vocab_xent_bwd_plan": (_I, [XentShape, _I, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_SZ)]),
@@ -978,6 +979,14 @@ def _xent_inputs(hidden, weight, tokens, scale):
     (x, xs), (w, ws) = _matrix(hidden if hidden.dim() == 2 else hidden.reshape(-1, C)), _matrix(weight)
     s = make_xent_shape(x.shape[0], V, C, DTYPES[x.dtype], scale, xs, ws)
     return x, w, tokens if tokens.is_contiguous() else tokens.contiguous(), s, lead, dev, host
+
+
+def vocab_xent_fwd_plan(rows, vocab, channels, num_sms):
+    """(columns of a tile, workspace bytes) of the forward on a device with num_sms SMs."""
+    w, n = ctypes.c_int(0), ctypes.c_size_t(0)
+    _check(lib().streamkl_vocab_xent_fwd_plan(make_xent_shape(rows, vocab, channels), int(num_sms), ctypes.byref(w), ctypes.byref(n)),
+           "streamkl_vocab_xent_fwd_plan")
+    return w.value, n.value
 
 
 def vocab_xent_plan(rows, vocab, channels, num_sms, want_dhidden=True, want_dweight=True):

@@ -280,7 +280,7 @@ bool encode_matrix_map(CUtensorMap* map, const void* base, long long rows, long 
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1u, 1u};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -924,13 +924,23 @@ static streamkl_status xent_problem(const streamkl_xent_shape& s, XentProblem* p
   return STREAMKL_OK;
 }
 
-streamkl_status streamkl_vocab_xent_fwd_workspace(streamkl_xent_shape s, size_t* bytes) {
+streamkl_status streamkl_vocab_xent_fwd_plan(streamkl_xent_shape s, int num_sms, int* width, size_t* bytes) {
   XentProblem p;
-  const streamkl_status v = xent_problem(s, &p);
+  streamkl_status v = xent_problem(s, &p);
   if (v != STREAMKL_OK) return v;
-  if (!bytes) return STREAMKL_ERR_INVALID;
-  *bytes = p.R ? xent_fwd_workspace(p) : 0;
+  if (!width || !bytes) return STREAMKL_ERR_INVALID;
+  *width = 0;
+  *bytes = 0;
+  if (p.R == 0) return STREAMKL_OK;
+  if (num_sms <= 0 && (v = device_sms(&num_sms)) != STREAMKL_OK) return v;
+  *width = xent_fwd_width(p, num_sms);
+  *bytes = xent_fwd_workspace(p, num_sms);
   return STREAMKL_OK;
+}
+
+streamkl_status streamkl_vocab_xent_fwd_workspace(streamkl_xent_shape s, size_t* bytes) {
+  int width;
+  return streamkl_vocab_xent_fwd_plan(s, 0, &width, bytes);
 }
 
 streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, const long long* tokens, streamkl_xent_shape s,
@@ -940,9 +950,12 @@ streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, 
   if (v != STREAMKL_OK || p.R == 0) return v;
   if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(tokens, 8) || !rows_ok(loss) || !rows_ok(lse))
     return STREAMKL_ERR_INVALID;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < xent_fwd_workspace(p)) return STREAMKL_ERR_WORKSPACE;
+  // no plan needs less than the rows' logits and a tile's partial sums
+  if (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)p.R * 20) return STREAMKL_ERR_WORKSPACE;
   int sms = 0, *status = nullptr;
-  if ((v = device_sms(&sms)) != STREAMKL_OK || (v = status_ptr(&status)) != STREAMKL_OK) return v;
+  if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
+  if (workspace_bytes < xent_fwd_workspace(p, sms)) return STREAMKL_ERR_WORKSPACE;
+  if ((v = status_ptr(&status)) != STREAMKL_OK) return v;
   return from_cuda(
       launch_xent_fwd(p, hidden, weight, tokens, loss, lse, workspace, sms, status, static_cast<cudaStream_t>(stream)));
 }

@@ -34,7 +34,7 @@ bool encode_tile_map(CUtensorMap* map, const void* base, int D, int N, int H, in
 // With box_cols 32 the box is {32, box_rows, 1} with the swizzle of its 128-byte rows.
 bool encode_rows_f32_map(CUtensorMap* map, float* base, int D, int rows, int BH, int box_rows, int box_cols = 0);
 // A 2-D TMA map {col, row} over a matrix of 2-byte values whose rows lie `stride` elements apart, a {box_cols, box_rows} box
-// with the swizzle of its 128-byte rows.
+// of 64 or 32 columns with the swizzle of its 128- or 64-byte rows.
 bool encode_matrix_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, int box_rows,
                        int box_cols);
 // The maps of Q1/Q2 and K1/K2 of a problem.
@@ -201,7 +201,8 @@ struct XentProblem {
   long long hidden_stride, weight_stride;
   float scale;
 };
-size_t xent_fwd_workspace(const XentProblem& p);
+int xent_fwd_width(const XentProblem& p, int num_sms);  // columns of a tile
+size_t xent_fwd_workspace(const XentProblem& p, int num_sms);
 cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void* weight, const long long* tokens, float* loss,
                             float* lse, void* workspace, int num_sms, int* status, cudaStream_t st);
 struct XentBwdPlan {

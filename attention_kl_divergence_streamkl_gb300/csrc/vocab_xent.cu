@@ -40,7 +40,7 @@ namespace skl {
 namespace {
 
 constexpr int BM = 128, BK = 64;         // rows of either operand in a block, and of the summed index, a stage
-constexpr int TILE = 256;                // a pair's tile: TILE x TILE
+constexpr int TILE = 256;                // a pair's tile: TILE rows x up to TILE columns
 constexpr int EPILOGUE_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int THREADS = 10 * 32;
 constexpr int STAGES = 5;
@@ -61,6 +61,7 @@ enum Kind { kForward, kGradLogits, kGradients };
 // One matrix product: m_tiles x n_tiles tiles, each over `splits` ranges of the k_chunks 64-wide chunks.
 struct Job {
   int m_tiles, n_tiles, splits, k_chunks;
+  int width;         // columns of a tile, and of its two blocks' halves together
   int m_group;       // forward and d: that many tiles along m share what they read of the other operand
   int a_mn, b_mn;    // the operand lies with its rows (m or n), not the summed index, along the 128-byte lines
   int rows, cols;    // of the output
@@ -70,9 +71,9 @@ struct Job {
   FastDiv by_split, by_group, by_m, by_last, by_n;
   __host__ __device__ long long tiles() const { return (long long)m_tiles * n_tiles * splits; }
 };
-Job make_job(int m_tiles, int n_tiles, int splits, int k_chunks, int m_group, int a_mn, int b_mn, long long rows, long long cols,
-             long long k) {
-  Job j{m_tiles, n_tiles, splits, k_chunks, m_group, a_mn, b_mn, (int)rows, (int)cols, (int)k, 0, 0, {}, {}, {}, {}, {}};
+Job make_job(int m_tiles, int n_tiles, int splits, int k_chunks, int width, int m_group, int a_mn, int b_mn, long long rows,
+             long long cols, long long k) {
+  Job j{m_tiles, n_tiles, splits, k_chunks, width, m_group, a_mn, b_mn, (int)rows, (int)cols, (int)k, 0, 0, {}, {}, {}, {}, {}};
   j.by_split = FastDiv((unsigned)((long long)m_tiles * n_tiles));
   j.by_n = FastDiv((unsigned)n_tiles);
   if (m_group) {
@@ -110,7 +111,7 @@ struct XentParams {
 };
 
 struct Maps {
-  CUtensorMap a[2], b[2], out[2], acc, clean;
+  CUtensorMap a[2], b[2], out[2], out32, acc, clean;  // out32: d's last 32 columns of a tile
 };
 
 // The tiles of a pair, in its order.  One job: every pairs-th, the tiles along m first, in groups of m_group.
@@ -190,12 +191,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return pack_bf16(lo, hi);
 }
 
-// instruction descriptor of a 256 x 256 tile of a pair
+// instruction descriptor of a pair's tile
 template <bool HALF>
-__device__ __forceinline__ uint32_t pair_idesc(bool a_mn, bool b_mn) {
+__device__ __forceinline__ uint32_t pair_idesc(bool a_mn, bool b_mn, int width) {
   const uint32_t type = HALF ? 0u : 1u;
   return (1u << 4) | (type << 7) | (type << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+         ((uint32_t)(width >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
 
 template <Kind KIND, bool HALF>
@@ -258,11 +259,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const Tile t = walk.tile(p, i);
         const Job& j = p.job[t.job];
         const CUtensorMap *ma = &maps.a[t.job], *mb = KIND == kGradients && t.job && clean ? &maps.clean : &maps.b[t.job];
-        const int m0 = t.m * TILE + (int)rank * BM, n0 = t.n * TILE + (int)rank * BM;
+        const int wide = j.width / 2, m0 = t.m * TILE + (int)rank * BM, n0 = t.n * j.width + (int)rank * wide;
         const Half a_half = half_of(m0, j.rows, j.a_mn, j.a_box), b_half = half_of(n0, j.cols, j.b_mn, j.b_box);
         // the bytes of both blocks
         const uint32_t bytes = half_of(t.m * TILE, j.rows, j.a_mn, j.a_box).bytes + half_of(t.m * TILE + BM, j.rows, j.a_mn, j.a_box).bytes +
-                               half_of(t.n * TILE, j.cols, j.b_mn, j.b_box).bytes + half_of(t.n * TILE + BM, j.cols, j.b_mn, j.b_box).bytes;
+                               half_of(t.n * j.width, j.cols, j.b_mn, j.b_box).bytes + half_of(t.n * j.width + wide, j.cols, j.b_mn, j.b_box).bytes;
         for (int k = t.k0; k < t.k1; ++k) {
           if (lap && !(ok = mbar_wait(empty + 8 * s, (lap - 1) & 1, status, abort_flag))) break;
           const uint32_t a = sb + OFF_STAGE + s * 2 * HALF_STAGE, b = a + HALF_STAGE, done = full_even + 8 * s;
@@ -297,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (unsigned i = 0; ok && i < walk.n_all; ++i) {
         const Tile t = walk.tile(p, i);
         const Job& j = p.job[t.job];
-        const uint32_t idesc = pair_idesc<HALF>(j.a_mn, j.b_mn);
+        const uint32_t idesc = pair_idesc<HALF>(j.a_mn, j.b_mn, j.width);
         const uint32_t a_step = j.a_mn ? 2048 : 32, b_step = j.b_mn ? 2048 : 32;
         const uint32_t a_lbo = j.a_mn ? HALF_STAGE / 2 : 0, b_lbo = j.b_mn ? HALF_STAGE / 2 : 0;
         for (int k0 = t.k0; ok && k0 < t.k1; k0 += t.step(KIND), ++used) {
@@ -348,7 +349,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Tile t = walk.tile(p, i);
       const uint32_t buf = used & 1, parity = used / 2 & 1;
       const int row0 = t.m * TILE + (int)rank * BM + quarter * 32;  // the warp's first row
-      const int col0 = t.n * TILE + half * 128;                     // and column
+      const int col0 = t.n * p.job[t.job].width + half * 128;       // and column
+      const int here_cols = min(128, p.job[t.job].width - half * 128);  // of the tile's
       const int row = row0 + lane;
       const uint32_t ta = tmem + lanes + TILE * buf + 128 * half;
       if constexpr (KIND == kForward) {
@@ -391,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           arrive_one_in(free_even + 8 * b);
         }
         if (!ok) break;
-        const int seen = p.V - col0;
+        const int seen = min(p.V - col0, here_cols);
         const long long at = token - col0;
         if (__any_sync(0xffffffffu, at >= 0 && at < min(128, seen))) {
 #pragma unroll
@@ -445,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           a = g + (p.g_lse ? p.g_lse[row] * p.scale * power : 0.f);
         }
         const bool none = g == 0.f && a == 0.f;
-        const int seen = real ? p.job[0].cols - col0 : 0;  // d is 0 past the piece; what is past the rows is not stored
+        const int seen = real ? min(p.job[0].cols - col0, here_cols) : 0;  // d is 0 past the piece; what is past the rows is not stored
         if (!mbar_wait_warp(there + 8 * buf, parity, status, abort_flag)) break;
         ++used;
         tc_fence_after();
@@ -497,14 +499,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int k = 0; k < 32; ++k) w[k] = none ? 0u : w[k];
           }
           if (q == 0) stage_free();
-          put(q, w);
+          if (64 * (q + 1) <= here_cols) {
+            put(q, w);
+          } else {  // 32 columns are left, rows of 64 bytes
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              st_shared16(stage + q * 4096 + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+          }
         }
         fence_async_smem();
         __syncwarp();
         if (elect_one()) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (row0 < p.R && col0 + 64 * q < p.job[0].cols) tma_store_2d(&maps.out[0], stage + 4096 * q, col0 + 64 * q, row0);
+          for (int q = 0; q < 2; ++q) {
+            const int left = here_cols - 64 * q, col = col0 + 64 * q;
+            if (row0 >= p.R || col >= p.job[0].cols || left <= 0) continue;
+            tma_store_2d(left >= 64 ? &maps.out[0] : &maps.out32, stage + 4096 * q, col, row0);
+          }
           bulk_commit();
         }
         __syncwarp();
@@ -699,6 +710,10 @@ __global__ void __launch_bounds__(256)
   out[i] = make_uint2(pack16<HALF>(s.x * f, s.y * f), pack16<HALF>(s.z * f, s.w * f));
 }
 
+// What a tile takes, in the time of a chunk's products: its chunks and kMoreChunks for its epilogue, which the products
+// share the shared memory with; a tile of dW, whose 128 KB go out to memory at a pair's share of its rate, kTileChunks at least.
+constexpr int kTileChunks = 7, kMoreChunks = 4;
+
 int tiles_of(long long n, int of) { return (int)((n + of - 1) / of); }
 size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
@@ -709,6 +724,26 @@ int pairs_for(long long tiles, int num_sms) { return (int)std::max<long long>(1,
 constexpr double kGroupBytes = 48e6;
 int m_group(const XentProblem& p, int m_tiles) {
   return std::max(1, std::min(m_tiles, (int)(kGroupBytes / (2.0 * TILE * p.C))));
+}
+
+// Columns of the forward's and d's tiles: 256, or fewer where the last wave of pairs would have few tiles.  A chunk's products
+// take as long as the tile is wide, its loads as long as both operands' rows; an epilogue kMoreChunks of the widest.  Narrower
+// tiles only for a tenth (forward of 100 x 20000 x 4096: 62 us with 79 tiles of 256, 57.8 with 125 of 160; 64 x 32000 x 512, two
+// waves either way: 21.0 with 256, 21.9 with 224).
+int tile_width(int m_tiles, long long rows, long long cols, int k_chunks, int num_sms) {
+  const int pairs = std::max(1, num_sms / 2);
+  int best = TILE;
+  double least = 0;
+  for (int w = TILE; w >= 160; w -= 32) {
+    const long long waves = (m_tiles * ((cols + w - 1) / w) + pairs - 1) / pairs;
+    const double loads = (double)(std::min<long long>(rows, TILE) + w) / (2 * TILE);
+    const double cost = waves * (k_chunks * std::max((double)w / TILE, loads) + kMoreChunks);
+    if (w == TILE || cost < least * 0.9) {
+      best = w;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 template <Kind KIND, bool HALF>
@@ -723,16 +758,14 @@ cudaError_t launch(const XentParams& p, const Maps& maps, int pairs, int* status
 
 // A matrix [rows, cols] of 2-byte values: an operand whose lines run along the summed index (k_major) or along its rows.
 // `box`: rows of a load, no more than there are (the summed index in whole steps of 16).
-bool operand_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, bool k_major, int* box) {
-  *box = k_major ? (int)std::min<long long>(BM, up(rows, 8)) : (int)std::min<long long>(BK, up(rows, 16));
+bool operand_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, bool k_major, int* box,
+                 int most = BM) {
+  *box = k_major ? (int)std::min<long long>(most, up(rows, 8)) : (int)std::min<long long>(BK, up(rows, 16));
   return encode_matrix_map(map, base, rows, cols, stride, *box, 64);
 }
 
 }  // namespace
 
-// What a tile takes, in the time of a chunk's products: its chunks and kMoreChunks for its epilogue, which the products
-// share the shared memory with; a tile of dW, whose 128 KB go out to memory at a pair's share of its rate, kTileChunks at least.
-constexpr int kTileChunks = 7, kMoreChunks = 4;
 // The vocabulary's pieces.  A piece's d lies in memory between the two launches: at most kPieceBytes of it, but at least
 // kPieceColumns, so that the sums of dh, read and written once a piece (8 bytes for 6 V / pieces operations), stay below
 // a few hundredths of the products' time.  Measured, gradients of 4096 x 131072 x 2048 and 8192 x 131072 x 4096, us: 64 MB
@@ -760,18 +793,22 @@ XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, bool want_dw, int 
   return g;
 }
 
-size_t xent_fwd_workspace(const XentProblem& p) {
-  return up((size_t)p.R * 4, 256) + (size_t)2 * tiles_of(p.V, TILE) * up(p.R, 32) * sizeof(float2);
+int xent_fwd_width(const XentProblem& p, int num_sms) {
+  return tile_width(tiles_of(p.R, TILE), p.R, p.V, tiles_of(p.C, BK), num_sms);
+}
+
+size_t xent_fwd_workspace(const XentProblem& p, int num_sms) {
+  return up((size_t)p.R * 4, 256) + (size_t)2 * tiles_of(p.V, xent_fwd_width(p, num_sms)) * up(p.R, 32) * sizeof(float2);
 }
 
 cudaError_t launch_xent_fwd(const XentProblem& p, const void* hidden, const void* weight, const long long* tokens, float* loss,
                             float* lse, void* workspace, int num_sms, int* status, cudaStream_t st) {
   Maps maps{};
   XentParams k{};
-  const int m_tiles = tiles_of(p.R, TILE), n_tiles = tiles_of(p.V, TILE);
-  k.job[0] = make_job(m_tiles, n_tiles, 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, p.R, p.V, p.C);
+  const int width = xent_fwd_width(p, num_sms), m_tiles = tiles_of(p.R, TILE), n_tiles = tiles_of(p.V, width);
+  k.job[0] = make_job(m_tiles, n_tiles, 1, tiles_of(p.C, BK), width, m_group(p, m_tiles), 0, 0, p.R, p.V, p.C);
   if (!operand_map(&maps.a[0], hidden, p.R, p.C, p.hidden_stride, true, &k.job[0].a_box) ||
-      !operand_map(&maps.b[0], weight, p.V, p.C, p.weight_stride, true, &k.job[0].b_box))
+      !operand_map(&maps.b[0], weight, p.V, p.C, p.weight_stride, true, &k.job[0].b_box, width / 2))
     return cudaErrorInvalidValue;
   k.R = p.R;
   k.V = (int)p.V;
@@ -822,10 +859,11 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     k.clean = clean;
     {
       Maps maps{};
-      k.job[0] = make_job(m_tiles, tiles_of(cols, TILE), 1, tiles_of(p.C, BK), m_group(p, m_tiles), 0, 0, p.R, cols, p.C);
+      const int width = tile_width(m_tiles, p.R, cols, tiles_of(p.C, BK), num_sms);
+      k.job[0] = make_job(m_tiles, tiles_of(cols, width), 1, tiles_of(p.C, BK), width, m_group(p, m_tiles), 0, 0, p.R, cols, p.C);
       if (!operand_map(&maps.a[0], in.hidden, p.R, p.C, p.hidden_stride, true, &k.job[0].a_box) ||
-          !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, true, &k.job[0].b_box) ||
-          !encode_matrix_map(&maps.out[0], d, p.R, cols, stride, 32, 64))
+          !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, true, &k.job[0].b_box, width / 2) ||
+          !encode_matrix_map(&maps.out[0], d, p.R, cols, stride, 32, 64) || !encode_matrix_map(&maps.out32, d, p.R, cols, stride, 32, 32))
         return cudaErrorInvalidValue;
       const int pairs = pairs_for(k.job[0].tiles(), num_sms);
       e = p.half ? launch<kGradLogits, true>(k, maps, pairs, status, st, true)
@@ -842,7 +880,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
     k.job[0] = k.job[1] = Job{};
     if (dhidden) {
       // (a last, short piece adds to the first sums only)
-      k.job[0] = make_job(m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), 0, 0, 1, p.R, p.C, cols);
+      k.job[0] = make_job(m_tiles, c_tiles, std::min(g.splits, tiles_of(cols, BK)), tiles_of(cols, BK), TILE, 0, 0, 1, p.R, p.C, cols);
       if (!operand_map(&maps.a[0], d, p.R, cols, stride, true, &k.job[0].a_box) ||
           !operand_map(&maps.b[0], w, cols, p.C, p.weight_stride, false, &k.job[0].b_box) ||
           !encode_matrix_map(&maps.out[0], dhidden, p.R, p.C, p.C, 32, 64) ||
@@ -851,7 +889,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
       k.accumulate = g.direct ? 0 : piece == 0 ? 1 : 2;
     }
     if (dweight) {
-      k.job[1] = make_job(tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), 0, 1, 1, cols, p.C, p.R);
+      k.job[1] = make_job(tiles_of(cols, TILE), c_tiles, 1, tiles_of(p.R, BK), TILE, 0, 1, 1, cols, p.C, p.R);
       if (!operand_map(&maps.a[1], d, p.R, cols, stride, false, &k.job[1].a_box) ||
           !operand_map(&maps.b[1], in.hidden, p.R, p.C, p.hidden_stride, false, &k.job[1].b_box) ||
           !operand_map(&maps.clean, ws + g.off_clean, p.R, p.C, p.C, false, &k.job[1].b_box) ||

@@ -485,11 +485,11 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  *   several blocks add up is added in a fixed order: the same bits on every run.  A row whose
  *   gradients are 0 has dhidden 0 and no part in dweight, whatever its hidden states are, NaN
  *   included; the weight has to be finite.
- * Workspaces (16-byte aligned): forward, 16 bytes per row and 256 columns; backward, a piece
+ * Workspaces (16-byte aligned): forward, 16 bytes per row and tile of 160 to 256 columns; backward, a piece
  *   of d, fp32 sums of dhidden and, for dweight, room for a copy of hidden:
  *   streamkl_vocab_xent_bwd_plan gives the number of the vocabulary's pieces, the splits of
- *   dhidden's sums and the bytes for any SM count (num_sms <= 0: the current device; with
- *   num_sms > 0 a pure host rule).
+ *   dhidden's sums and the bytes, streamkl_vocab_xent_fwd_plan the forward's tile and bytes,
+ *   for any SM count (num_sms <= 0: the current device; with num_sms > 0 a pure host rule).
  */
 typedef struct {
   long long rows, vocab;
@@ -497,6 +497,7 @@ typedef struct {
   float scale;
   long long hidden_stride, weight_stride;
 } streamkl_xent_shape;
+streamkl_status streamkl_vocab_xent_fwd_plan(streamkl_xent_shape s, int num_sms, int* tile_width, size_t* bytes);
 streamkl_status streamkl_vocab_xent_fwd_workspace(streamkl_xent_shape s, size_t* bytes);
 streamkl_status streamkl_vocab_xent_fwd(const void* hidden, const void* weight, const long long* tokens, streamkl_xent_shape s,
                                         float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -102,6 +102,28 @@ def test_large_vocabularies(R, C, V, dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("R,C,V", [(100, 512, 20000), (100, 1024, 28001), (300, 520, 12007), (64, 2000, 33000), (257, 1024, 12000)])
+def test_narrower_tiles(R, C, V, dtype):
+    """Vocabularies whose tiles of 256 columns would begin another wave; the last columns of a tile are 32 or 64."""
+    check(*inputs(R, C, V, dtype, R + V), gl=True)
+
+
+def test_every_width_of_a_tile_is_met():
+    assert {skl.vocab_xent_fwd_plan(R, V, C, 152)[0] for R, C, V in
+            [(300, 520, 12007), (100, 1024, 28001), (64, 2000, 33000), (8, 64, 300)]} == {160, 192, 224, 256}
+
+
+def test_a_forward_workspace_a_byte_short():
+    h, w, t = inputs(70, 64, 500, "bf16", 21)
+    _, n = skl.vocab_xent_fwd_plan(70, 500, 64, torch.cuda.get_device_properties(0).multi_processor_count)
+    out, ws = torch.empty(2, 70, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    args = (h.data_ptr(), w.data_ptr(), t.data_ptr(), K.make_xent_shape(70, 500, 64), out[0].data_ptr(), out[1].data_ptr(), ws.data_ptr())
+    assert skl.lib().streamkl_vocab_xent_fwd(*args, n - 1, None) == K.ERR_WORKSPACE
+    assert skl.lib().streamkl_vocab_xent_fwd(*args, n, None) == K.OK
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_pieces_of_the_vocabulary(dtype):
     """So many rows that d is written in three pieces; the last is no whole tile."""
     R, C, V = 17000, 72, 17001

@@ -45,6 +45,7 @@ def test_shapes_that_are_refused(lib, change, code):
     assert lib.streamkl_vocab_xent_fwd(*{**FWD, "shape": s}.values(), None) == code
     assert lib.streamkl_vocab_xent_bwd(*{**BWD, "shape": s}.values(), None) == code
     assert lib.streamkl_vocab_xent_fwd_workspace(s, ctypes.byref(n)) == code
+    assert lib.streamkl_vocab_xent_fwd_plan(s, 152, ctypes.byref(i), ctypes.byref(n)) == code
     assert lib.streamkl_vocab_xent_bwd_plan(s, 152, 1, 1, ctypes.byref(i), ctypes.byref(i), ctypes.byref(n)) == code
 
 
@@ -54,17 +55,26 @@ def test_forward_refuses_pointers(lib, change):
     assert lib.streamkl_vocab_xent_fwd(*{**FWD, "shape": shape(), **change}.values(), None) == K.ERR_INVALID
 
 
-@pytest.mark.parametrize("change", [dict(ws=None), dict(ws=ptr(8)), dict(nbytes=0)])
+@pytest.mark.parametrize("change", [dict(ws=None), dict(ws=ptr(8)), dict(nbytes=79)])
 def test_forward_refuses_workspaces(lib, change):
     assert lib.streamkl_vocab_xent_fwd(*{**FWD, "shape": shape(), **change}.values(), None) == K.ERR_WORKSPACE
 
 
-def test_forward_workspace_a_byte_short(lib):
-    n = ctypes.c_size_t(0)
-    assert lib.streamkl_vocab_xent_fwd_workspace(shape(), ctypes.byref(n)) == K.OK
-    assert n.value > 0
-    args = {**FWD, "shape": shape(), "nbytes": n.value - 1}
-    assert lib.streamkl_vocab_xent_fwd(*args.values(), None) == K.ERR_WORKSPACE
+@pytest.mark.parametrize("rows,vocab,channels", [(1, 1, 8), (8, 131072, 4096), (333, 50021, 1000), (8192, 131072, 4096), (100, 20000, 4096),
+                                                 (64, 32000, 4096), (5, 88, 496), (256, 19712, 512), (3000, 100, 64), (300, 12000, 520),
+                                                 (100, 28000, 1024)])
+def test_forward_plan(rows, vocab, channels):
+    """Tiles of 160 to 256 columns in steps of 32, narrower ones only where that saves a part of a wave of 76 pairs."""
+    B.build()
+    width, nbytes = skl.vocab_xent_fwd_plan(rows, vocab, channels, 152)
+    assert width in range(160, 257, 32)
+    tiles, m = -(-vocab // width), -(-rows // 256)
+    assert nbytes == -(-4 * rows // 256) * 256 + 2 * tiles * (-(-rows // 32) * 32) * 8
+
+    def waves(w):
+        return -(-m * -(-vocab // w) // 76)
+
+    assert width == 256 or waves(width) * width < waves(256) * 256
 
 
 @pytest.mark.parametrize("change", [dict(dh=None, dw=None), dict(dh=ptr(8)), dict(dw=ptr(8)), dict(hidden=None), dict(weight=None),
