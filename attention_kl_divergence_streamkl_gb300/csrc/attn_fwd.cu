@@ -121,10 +121,10 @@ __device__ __forceinline__ float row_exps(const uint32_t (&s0)[32], const uint32
 // 129 keys 7.3 -> 6.8; N8192 518 -> 542).
 // REST: the part of O that its rounding leaves is stored too.
 // DIFF: heads 2 i and 2 i + 1 are the two maps of a difference.  A block's tiles are then the same 128 rows of both, so that
-// they share K and V and the difference is formed at the end, in fp32, from both accumulators (the second's through shared
-// memory); where heads are packed both maps' rows lie in the tile.  Without REST only the difference leaves the SM.
-// (B2 16 pairs HK8 N4096 D128 causal 222 us, attention of the 32 heads 232; one token over 65536 keys, B8 16 pairs HK8 367 us, 5.9
-// TB/s.)
+// they share K and V and the difference is formed at the end, in fp32, from both accumulators; where heads are packed both
+// maps' rows lie in the tile.  Without REST only the difference leaves the SM.
+// (B2 16 pairs HK8 N4096 D128 causal 216 us, attention of the 32 heads 232, 222 with the second tile's rows through shared memory
+// too; one token over 65536 keys, B8 16 pairs HK8 367 us, 5.9 TB/s.)
 template <int D, bool FRESH, bool REST, bool DIFF>
 __global__ void __launch_bounds__(THREADS, 1)
     attn_fwd_kernel(const AttnProblem p, float* __restrict__ out_lse,
@@ -536,24 +536,54 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if constexpr (DIFF) {
-        // the second map's rows go through the ring's memory, whose tiles have all been used
+        // The difference: tiles of their own are both in TMEM, where a row's two threads read the same lanes, each a half of
+        // the columns; packed maps are rows of one tile, the second's go through the ring's memory, whose tiles have all been used.
         const int threads = p.packed ? SOFTMAX_WARPS / 2 * 32 : SOFTMAX_WARPS * 32;
+        const bool none = !(l > 0.f) && !nan;
+        float* factors = reinterpret_cast<float*>(smem + L::OFF_KV);  // of both tiles' rows, -1 for rows without keys
+        if (p.splits == 1 && !p.packed) factors[t * BM + r] = none ? -1.f : f;
+        tc_fence_before();
+        __syncwarp();
         if (p.splits == 1 && !named_bar_any(3, threads, !ok)) {
-          const bool none = !(l > 0.f) && !nan;
-          const bool second = p.packed ? g & 1 : t;
-          const uint32_t ring = sb + L::OFF_KV;
-          auto at = [&](int y, int v) { return ring + (uint32_t)(y * (D * 4) + ((v ^ (y & 7)) << 4)); };  // 16 bytes v of row y
-          auto load = [&](int d, uint32_t (&o)[32]) {
-            __syncwarp();
-            if (nt > 0) {
-              tmem_ld32(to + d, o);
-              tmem_ld_wait();
-              reg_fence32(o);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
+          tc_fence_after();
+          // (a row without keys is 0, whatever stands beside it)
+          auto weight = [&]() {
+            return p.lam[(long long)b * p.ls_b + (long long)(h / 2) * p.ls_h + (long long)qn * p.ls_n];
           };
-          if (p.packed || t == 1) {
+          if (!p.packed) {
+            const float f0 = factors[r], f1 = factors[BM + r], lam = real && f0 != -1.f ? weight() : 0.f;
+#pragma unroll 1
+            for (int d = t * (D / 2); d < (t + 1) * (D / 2); d += 32) {
+              uint32_t o[32], x[32];
+              __syncwarp();
+              if (nt > 0) {  // both tiles have as many
+                tmem_ld32(tmem + lanes + kColO + d, o);
+                tmem_ld32(tmem + lanes + kColO + D + d, x);
+                tmem_ld_wait();
+                reg_fence32(o);
+                reg_fence32(x);
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const float first = f0 == -1.f ? 0.f : __uint_as_float(o[k]) * f0, second = f1 == -1.f ? 0.f : __uint_as_float(x[k]) * f1;
+                o[k] = __float_as_uint(fmaf(-lam, second, first));
+              }
+              stage_row32(sb + L::OFF_Q, r, d, o, 1.f);
+            }
+          } else {
+            const bool second = g & 1;
+            const uint32_t ring = sb + L::OFF_KV;
+            auto at = [&](int y, int v) { return ring + (uint32_t)(y * (D * 4) + ((v ^ (y & 7)) << 4)); };  // 16 bytes v of row y
+            auto load = [&](int d, uint32_t (&o)[32]) {
+              __syncwarp();
+              if (nt > 0) {
+                tmem_ld32(to + d, o);
+                tmem_ld_wait();
+                reg_fence32(o);
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
+            };
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               uint32_t o[32];
@@ -564,14 +594,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                   st_shared16(at(r, d / 4 + k), make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
               }
             }
-          }
-          __syncwarp();
-          named_bar_sync(3, threads);
-          if (t == 0) {
+            __syncwarp();
+            named_bar_sync(3, threads);
             const bool mine = !second && real;
-            // (a row without keys is 0, whatever stands beside it)
-            const float lam = mine && !none ? p.lam[(long long)b * p.ls_b + (long long)(h / 2) * p.ls_h + (long long)qn * p.ls_n] : 0.f;
-            const int other = p.packed ? r + p.NQ : r, out_row = p.packed ? g / 2 * p.NQ + qn : r;
+            const float lam = mine && !none ? weight() : 0.f;
+            const int out_row = g / 2 * p.NQ + qn;
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               uint32_t o[32];
@@ -579,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (mine) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                  const uint4 x = ld_shared16(at(other, d / 4 + k));
+                  const uint4 x = ld_shared16(at(r + p.NQ, d / 4 + k));
                   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
@@ -588,14 +615,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 stage_row32(sb + L::OFF_Q, out_row, d, o, 1.f);
               }
             }
-            fence_async_smem();
+          }
+          fence_async_smem();
+          __syncwarp();
+          named_bar_sync(3, threads);
+          if (t == 0 && wq == 0) {
+            if (elect_one())
+              store_tile<D>(&mdiff, sb + L::OFF_Q, p.packed ? 0 : q0, p.packed ? hk * (p.G / 2) : hx, b);
             __syncwarp();
-            named_bar_sync(1, SOFTMAX_WARPS / 2 * 32);
-            if (wq == 0) {
-              if (elect_one())
-                store_tile<D>(&mdiff, sb + L::OFF_Q, p.packed ? 0 : q0, p.packed ? hk * (p.G / 2) : hx, b);
-              __syncwarp();
-            }
           }
         }
       }
