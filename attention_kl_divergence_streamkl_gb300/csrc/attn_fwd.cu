@@ -73,7 +73,8 @@ struct Smem {
   // q_full[2], kv_full[SLOTS], kv_empty[SLOTS], s_full[S_BUFS], p_ready[S_BUFS], o_done[S_BUFS], to_patch, patched; TMEM
   // slot, abort flag
   static constexpr int BAR_SLOT = 8 * (4 + 2 * SLOTS + 3 * S_BUFS);
-  static constexpr int BYTES = OFF_BAR + BAR_SLOT + 16 + 1024;
+  static constexpr int OFF_FACTORS = OFF_BAR + BAR_SLOT + 16;  // a difference's, of both tiles' rows
+  static constexpr int BYTES = OFF_FACTORS + 2 * BM * 4 + 1024;
 };
 static_assert(Smem<64>::BYTES <= kWholeSmSmem && Smem<128>::BYTES <= kWholeSmSmem, "shared memory");
 
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the columns; packed maps are rows of one tile, the second's go through the ring's memory, whose tiles have all been used.
         const int threads = p.packed ? SOFTMAX_WARPS / 2 * 32 : SOFTMAX_WARPS * 32;
         const bool none = !(l > 0.f) && !nan;
-        float* factors = reinterpret_cast<float*>(smem + L::OFF_KV);  // of both tiles' rows, -1 for rows without keys
+        // of both tiles' rows, -1 for rows without keys (not in the ring: the other tile's last product may still read V there)
+        float* factors = reinterpret_cast<float*>(smem + L::OFF_FACTORS);
         if (p.splits == 1 && !p.packed) factors[t * BM + r] = none ? -1.f : f;
         tc_fence_before();
         __syncwarp();

@@ -45,6 +45,29 @@ def test_forward_of_many_blocks(causal, padded, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("late", [0, 1])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4, 5, 8, 13])
+def test_one_map_is_done_before_the_other(tiles, late, D):
+    """The late map's logits grow by 22 in the last key tile, so that its reference moves there, while the other map's tile is
+    done; the last keys' values then lie in each place of the ring that a tile count leaves them in."""
+    B, H, HK, NQ, NK = 2, 40, 20, 200, 128 * tiles
+    assert skl.diff_attn_plan(B, H, HK, NQ, NK, D, sms())[:2] == (False, 1)
+    q, k, v, lam, _ = inputs(B, H, HK, NQ, NK, D, 7)
+    k[..., 0] = 0
+    k[:, :, -128:, 0] = 16 * (D / 128) ** 0.25
+    q[:, 1 - late::2, :, 0] = 0
+    q[:, late::2, :, 0] = 16 * (D / 128) ** 0.25
+    rd, rz, bd, bz, o, e = reference(q, k, v, lam)
+    for _ in range(4):
+        d, lse = skl.diff_attn_fwd(q, k, v, lam)
+        A.within(d, rd, bd, "d")
+        A.within(lse, rz, bz, "lse")
+        d, _, maps, rest = skl.diff_attn_fwd(q, k, v, lam, return_maps=True)
+        A.within(d, rd, bd, "d with the maps")
+        A.within(maps.double() + rest.double(), o, e + 2.0 ** -16 * o.abs() + 2.0 ** -126, "maps")
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_backward_of_many_blocks(D):
     """Every tile a block of its own, and for D 64 the path that visits each tile pair once."""
     B, H, HK, NQ, NK = 4, 24, 24, 300, 500
