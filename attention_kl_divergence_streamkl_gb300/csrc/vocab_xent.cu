@@ -418,7 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mx = fmax3(mx, __uint_as_float(s2[k]), __uint_as_float(s3[k]));
         }
         const float m = mx * p.c;
-        const float2 cc = make_float2(p.c, p.c), nm = mx == kNegInf ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+        // (m, not mx: a logit near the type's lowest value is -inf in these units)
+        const float2 cc = make_float2(p.c, p.c), nm = m == kNegInf ? make_float2(0.f, 0.f) : make_float2(-m, -m);
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {

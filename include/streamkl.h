@@ -474,7 +474,8 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  * tokens [rows], 64-bit.  loss_r = LSE_r - z[r, token], lse_r = LSE_r, fp32 [rows].  A
  *   negative token is no token: its loss is 0 and has no gradient (lse does).  A token
  *   >= vocab gives NaN and has no gradient.
- * A +inf or NaN logit makes its row's values NaN, -inf has probability 0.
+ * A +inf or NaN logit makes its row's values NaN, -inf has probability 0; |z| above 2.3e38, 2^128 in
+ *   units of log 2, counts as infinite.
  *
  * streamkl_vocab_xent_bwd: for upstream gradients g_loss [rows] and, unless NULL, g_lse
  *   [rows] of the two outputs, and the forward's lse:

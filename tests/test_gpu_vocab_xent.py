@@ -190,6 +190,26 @@ def test_rows_that_are_not_finite():
     check(h, w, t)
 
 
+@pytest.mark.parametrize("R", [1, 40, 300])
+@pytest.mark.parametrize("seen,V", [(200, 1024), (256, 700), (1, 20000)])
+def test_whole_tiles_of_the_lowest_value(seen, V, R):
+    """Columns behind `seen` are masked by a channel with the type's lowest value: some 128 columns hold nothing else."""
+    h, w, t = inputs(R, 64, V, "bf16", 11, none=0.0)
+    h[:, 0], w[:, 0] = 1.0, 0.0
+    w[seen:, 0] = torch.finfo(torch.bfloat16).min
+    t %= seen
+    ref, got = skl.vocab_xent_fwd(h, w[:seen], t), skl.vocab_xent_fwd(h, w, t)
+    F = forward(h, w[:seen], t, 1.0)
+    within(got[0], F[0], F[2], "loss")
+    within(got[1], F[1], F[3], "lse")
+    g = torch.rand(R, device="cuda")
+    (dh, dw), (rh, rw) = skl.vocab_xent_bwd(h, w, t, ref[1], g), skl.vocab_xent_bwd(h, w[:seen], t, ref[1], g)
+    assert bool((dh[:, 1:].isfinite()).all()) and not bool(dw[seen:].any())
+    _, _, bh, bw = backward(h, w[:seen], t, g, None, 1.0)
+    within(dh, rh.double(), 2 * bh, "dhidden")
+    within(dw[:seen], rw.double(), 2 * bw, "dweight")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("R,V", [(40, 500), (300, 3000), (17000, 17000)])
 def test_rows_without_a_gradient_may_hold_anything(R, V, dtype):
