@@ -24,7 +24,7 @@ namespace skl {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int kThreadsSm = 2048, kMostHeads = 4;
+constexpr int kThreadsSm = 2048;
 
 // Two neighbouring values of 2 bytes.
 template <typename T>
@@ -72,8 +72,8 @@ __device__ __forceinline__ void sincos_of_turn(unsigned long long turn, float* s
   *cos_out = (quarter + 1) & 2 ? -b : b;
 }
 
+constexpr int HEADS = 4;  // of a thread at most
 // V elements a vector: 16 bytes, or one pair alone where sizes or addresses do not allow that
-constexpr int HEADS = 4;  // whose loads are in flight together
 template <typename T, bool INTERLEAVED, int V>
 __global__ void __launch_bounds__(THREADS, INTERLEAVED ? 10 : 6) rotary_kernel(const RotaryProblem p) {
   constexpr int PAIRS = INTERLEAVED ? V / 2 : V, PARTS = INTERLEAVED ? 1 : 2;
@@ -97,18 +97,15 @@ __global__ void __launch_bounds__(THREADS, INTERLEAVED ? 10 : 6) rotary_kernel(c
   auto to = [&](int h) {
     return h < p.HQ ? static_cast<T*>(p.q_out) + out_q + h * p.qo.h : static_cast<T*>(p.k_out) + out_k + (h - p.HQ) * p.ko.h;
   };
-  Vec v[HEADS][PARTS];
-  auto load = [&](int h0) {
+  Vec v[HEADS][PARTS];  // on their way while the angles are formed
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      if (h0 + i < last) {
-        const T* src = from(h0 + i);
-        v[i][0] = *reinterpret_cast<const Vec*>(src);
-        if (PARTS == 2 && turns) v[i][PARTS - 1] = *reinterpret_cast<const Vec*>(src + p.dim / 2);
-      }
+  for (int i = 0; i < HEADS; ++i) {
+    if (first + i < last) {
+      const T* src = from(first + i);
+      v[i][0] = *reinterpret_cast<const Vec*>(src);
+      if (PARTS == 2 && turns) v[i][PARTS - 1] = *reinterpret_cast<const Vec*>(src + p.dim / 2);
     }
-  };
-  load(first);  // on their way while the angles are formed
+  }
   float c[PAIRS], s[PAIRS];
   if (turns) {
     long long pos = p.offset + n;
@@ -123,37 +120,34 @@ __global__ void __launch_bounds__(THREADS, INTERLEAVED ? 10 : 6) rotary_kernel(c
       s[k] *= p.sin_sign;
     }
   }
-  for (int h0 = first; h0 < last; h0 += HEADS) {
-    if (h0 != first) load(h0);
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      if (h0 + i < last) {
-        T* dst = to(h0 + i);
-        if (turns) {
+  for (int i = 0; i < HEADS; ++i) {
+    if (first + i < last) {
+      T* dst = to(first + i);
+      if (turns) {
 #pragma unroll
-          for (int k = 0; k < PAIRS; k += WIDE && !INTERLEAVED ? 2 : 1) {
-            if constexpr (WIDE && INTERLEAVED) {
-              uint32_t& w = reinterpret_cast<uint32_t*>(&v[i][0])[k];
-              const float2 z = unpack<T>(w);
-              w = pack<T>(make_float2(fmaf(z.x, c[k], -(z.y * s[k])), fmaf(z.y, c[k], z.x * s[k])));
-            } else if constexpr (WIDE) {
-              uint32_t &w0 = reinterpret_cast<uint32_t*>(&v[i][0])[k / 2], &w1 = reinterpret_cast<uint32_t*>(&v[i][PARTS - 1])[k / 2];
-              const float2 x = unpack<T>(w0), y = unpack<T>(w1);
-              const float2 cc = make_float2(c[k], c[(k + 1) % PAIRS]), ss = make_float2(s[k], s[(k + 1) % PAIRS]);
-              w0 = pack<T>(fsub2(fmul2(x, cc), fmul2(y, ss)));
-              w1 = pack<T>(ffma2(x, ss, fmul2(y, cc)));
-            } else {
-              T& first_of = INTERLEAVED ? v[i][0].x[(2 * k) % V] : v[i][0].x[k];
-              T& second_of = INTERLEAVED ? v[i][0].x[(2 * k + 1) % V] : v[i][PARTS - 1].x[k];
-              const float x = one(first_of), y = one(second_of);
-              first_of = one_of<T>(fmaf(x, c[k], -(y * s[k])));
-              second_of = one_of<T>(fmaf(y, c[k], x * s[k]));
-            }
+        for (int k = 0; k < PAIRS; k += WIDE && !INTERLEAVED ? 2 : 1) {
+          if constexpr (WIDE && INTERLEAVED) {
+            uint32_t& w = reinterpret_cast<uint32_t*>(&v[i][0])[k];
+            const float2 z = unpack<T>(w);
+            w = pack<T>(make_float2(fmaf(z.x, c[k], -(z.y * s[k])), fmaf(z.y, c[k], z.x * s[k])));
+          } else if constexpr (WIDE) {
+            uint32_t &w0 = reinterpret_cast<uint32_t*>(&v[i][0])[k / 2], &w1 = reinterpret_cast<uint32_t*>(&v[i][PARTS - 1])[k / 2];
+            const float2 x = unpack<T>(w0), y = unpack<T>(w1);
+            const float2 cc = make_float2(c[k], c[(k + 1) % PAIRS]), ss = make_float2(s[k], s[(k + 1) % PAIRS]);
+            w0 = pack<T>(fsub2(fmul2(x, cc), fmul2(y, ss)));
+            w1 = pack<T>(ffma2(x, ss, fmul2(y, cc)));
+          } else {
+            T& first_of = INTERLEAVED ? v[i][0].x[(2 * k) % V] : v[i][0].x[k];
+            T& second_of = INTERLEAVED ? v[i][0].x[(2 * k + 1) % V] : v[i][PARTS - 1].x[k];
+            const float x = one(first_of), y = one(second_of);
+            first_of = one_of<T>(fmaf(x, c[k], -(y * s[k])));
+            second_of = one_of<T>(fmaf(y, c[k], x * s[k]));
           }
-          if (PARTS == 2) *reinterpret_cast<Vec*>(dst + p.dim / 2) = v[i][PARTS - 1];
         }
-        *reinterpret_cast<Vec*>(dst) = v[i][0];
+        if (PARTS == 2) *reinterpret_cast<Vec*>(dst + p.dim / 2) = v[i][PARTS - 1];
       }
+      *reinterpret_cast<Vec*>(dst) = v[i][0];
     }
   }
 }
@@ -193,8 +187,8 @@ bool rotary_plan(RotaryProblem* p, int num_sms) {
   if (p->items > 0x7fffffffll - THREADS) return false;
   p->by_slots = FastDiv((unsigned)slots);
   p->by_rows = FastDiv((unsigned)p->N);
-  // heads a thread: as many as leave kThreadsSm threads an SM, between one and kMostHeads, and the same for all
-  const long long each = std::max(1ll, std::min<long long>({kMostHeads, heads, p->items * heads / ((long long)num_sms * kThreadsSm)}));
+  // heads a thread: as many as leave kThreadsSm threads an SM, between one and HEADS, and the same for all
+  const long long each = std::max(1ll, std::min<long long>({HEADS, heads, p->items * heads / ((long long)num_sms * kThreadsSm)}));
   const int shares = (int)((heads + each - 1) / each);
   p->heads_each = (heads + shares - 1) / shares;
   return true;
