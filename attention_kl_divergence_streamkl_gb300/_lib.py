@@ -894,6 +894,10 @@ def _rotary(tensors, plan, positions, offset, interleaved, inverse, out):
             outs[i] = torch.empty_like(t) if t.stride(3) == 1 and all(s > 0 for s in t.stride()) else t.new_empty(t.shape)
         elif o.shape != t.shape or o.dtype != dtype or o.device != dev or o.stride(3) != 1:
             raise ValueError("an output must have its input's shape, type and device, and contiguous channels")
+        elif o.requires_grad and torch.is_grad_enabled():
+            raise ValueError("out has no gradient: an output that requires one is not written to")
+        elif not o.is_inference():
+            torch.autograd.graph.increment_version(o)  # what was saved of it for a backward is no longer there
         ins.append(t)
     for t in (*ins, *outs):
         strides += [0, 0, 0] if t is None else t.stride()[:3]
@@ -920,7 +924,7 @@ def rotary_fwd(q, k, plan, positions=None, offset=0, interleaved=False, out=None
     q: [B, HQ, N, D], k: [B, HK, N, D], bf16, fp16 or fp32, either may be None; plan: rotary_plan's, on their device.
     positions: int64 or int32 [N] or [B, N]; without them row n is at offset + n.  Pairs are the channels i and dim / 2 + i,
     with interleaved 2 i and 2 i + 1.  out: (q_out, k_out) to write to, for example q and k themselves or a cache's rows
-    (it may overlap nothing else); an entry may be None.
+    (it may overlap nothing else, and require no gradient); an entry may be None.
     """
     if out is None:
         got = (_calls or calls()).rotary(q, k, plan.turns, plan.dim, plan.amplitude, positions, offset, interleaved, False)

@@ -171,6 +171,27 @@ def test_refusals_on_the_device():
         skl.rotary_fwd(x, None, plan, out=(x.transpose(1, 2), None))
 
 
+def test_outputs_and_gradients():
+    """An output that requires a gradient is refused; a backward that needs what stood in one says so."""
+    q, k = tensors(1, 2, 2, 8, 64, "fp32", 5)
+    plan = skl.rotary_plan(64)
+    leaf = q.clone().requires_grad_()
+    with pytest.raises(ValueError):
+        skl.rotary_fwd(leaf, k, plan, out=(leaf, k))
+    with torch.no_grad():
+        skl.rotary_fwd(leaf, k, plan, out=(leaf, None))
+    y = (leaf * k).sum()
+    skl.rotary_fwd(q, k, plan, out=(None, k))
+    with pytest.raises(RuntimeError):
+        y.backward()
+    ref = skl.rotary_fwd(q, k, plan)
+    with torch.inference_mode():
+        x = q.clone()
+        skl.rotary_fwd(x, k, plan, out=(x, k))
+        assert torch.equal(x, ref[0])
+    assert torch.equal(k, ref[1])
+
+
 def test_not_finite_values_stay_in_their_pairs():
     q, _ = tensors(1, 1, 0, 4, 64, "fp32", 4)
     plan = skl.rotary_plan(64)
