@@ -910,7 +910,7 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
 static streamkl_status xent_problem(const streamkl_xent_shape& s, XentProblem* p) {
   if (s.rows < 0 || s.vocab <= 0 || s.channels <= 0 || s.hidden_stride < s.channels || s.weight_stride < s.channels)
     return STREAMKL_ERR_INVALID;
-  if (!(s.scale > 0.f) || isinf(s.scale)) return STREAMKL_ERR_INVALID;
+  if (!(s.scale > 0.f) || isinf(s.scale * kLog2e)) return STREAMKL_ERR_INVALID;
   if (s.dtype != STREAMKL_BF16 && s.dtype != STREAMKL_FP16)
     return s.dtype == STREAMKL_FP32 ? STREAMKL_ERR_UNSUPPORTED : STREAMKL_ERR_INVALID;
   // rows of 16-byte granules for TMA; rows, columns and their tiles in 32 bits
@@ -992,6 +992,10 @@ streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, 
   if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(tokens, 8) || !rows_ok(lse) || !rows_ok(g_loss) ||
       !aligned_to_or_null(g_lse, 4))
     return STREAMKL_ERR_INVALID;
+  // both are read until the end
+  for (const void* to : {dhidden, dweight})
+    if (to && (to == hidden || to == weight)) return STREAMKL_ERR_INVALID;
+  if (dhidden == dweight) return STREAMKL_ERR_INVALID;
   int sms = 0, *status = nullptr;
   if ((v = device_sms(&sms)) != STREAMKL_OK) return v;
   const XentBwdPlan g = xent_bwd_plan(p, dhidden != nullptr, dweight != nullptr, sms);
@@ -1038,6 +1042,8 @@ streamkl_status streamkl_rotary(const void* q, const void* k, streamkl_rotary_sh
     return STREAMKL_ERR_INVALID;
   if (s.HK && (!aligned_to(k, size) || !aligned_to(k_out, size) || !rows_disjoint(k_to, s.B, s.HK, s.N, s.D)))
     return STREAMKL_ERR_INVALID;
+  // an output on the other's place is read by other blocks
+  if (s.HQ && s.HK && (q_out == k_out || q_out == k || k_out == q)) return STREAMKL_ERR_INVALID;
   // in place: every row on itself
   auto moved = [&](const RotaryStrides& a, const RotaryStrides& b, int heads) {
     return (s.B > 1 && a.b != b.b) || (heads > 1 && a.h != b.h) || (s.N > 1 && a.n != b.n);

@@ -481,7 +481,7 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  *   [rows] of the two outputs, and the forward's lse:
  *     d = scale (g_loss (p - [v = token]) + g_lse p),  p = exp(z - lse)
  *     dhidden = d weight [rows, channels],  dweight = d^T hidden [vocab, channels]
- *   contiguous, of `dtype`; one of them may be NULL where it is not wanted.  d enters the
+ *   contiguous, of `dtype`, overlapping nothing; one of them may be NULL where it is not wanted.  d enters the
  *   products rounded to `dtype`; sums are fp32, dhidden and dweight are rounded once.  What
  *   several blocks add up is added in a fixed order: the same bits on every run.  A row whose
  *   gradients are 0 has dhidden 0 and no part in dweight, whatever its hidden states are, NaN

@@ -43,6 +43,7 @@ def call(lib, q=ptr(), k=ptr(16), turns=ptr(32), q_out=ptr(64), k_out=ptr(128), 
     (dict(dtype=2, q=ptr(2)), K.ERR_INVALID),
     (dict(qoh=0), K.ERR_INVALID), (dict(qon=32), K.ERR_INVALID), (dict(kob=512), K.ERR_INVALID),  # rows on one another
     (dict(q_out=ptr(), qoh=64, qon=256), K.ERR_INVALID),  # in place, rows on other rows
+    (dict(k_out=ptr(64)), K.ERR_INVALID), (dict(q_out=ptr(16)), K.ERR_INVALID), (dict(k_out=ptr()), K.ERR_INVALID),  # on the other
 ])
 def test_refuses(lib, change, code):
     assert call(lib, **change) == code

@@ -27,6 +27,7 @@ BAD_SHAPES = [
     (dict(rows=-1), K.ERR_INVALID), (dict(vocab=0), K.ERR_INVALID), (dict(channels=0), K.ERR_INVALID),
     (dict(hidden_stride=56), K.ERR_INVALID), (dict(weight_stride=0), K.ERR_INVALID), (dict(scale=0.0), K.ERR_INVALID),
     (dict(scale=-1.0), K.ERR_INVALID), (dict(scale=float("nan")), K.ERR_INVALID), (dict(scale=float("inf")), K.ERR_INVALID),
+    (dict(scale=3e38), K.ERR_INVALID),
     (dict(dtype=3), K.ERR_INVALID), (dict(dtype=-1), K.ERR_INVALID), (dict(dtype=2), K.ERR_UNSUPPORTED),
     (dict(channels=60), K.ERR_UNSUPPORTED), (dict(hidden_stride=68), K.ERR_UNSUPPORTED),
     (dict(weight_stride=68), K.ERR_UNSUPPORTED), (dict(rows=2**31), K.ERR_UNSUPPORTED), (dict(vocab=2**31), K.ERR_UNSUPPORTED),
@@ -78,7 +79,8 @@ def test_forward_plan(rows, vocab, channels):
 
 
 @pytest.mark.parametrize("change", [dict(dh=None, dw=None), dict(dh=ptr(8)), dict(dw=ptr(8)), dict(hidden=None), dict(weight=None),
-                                    dict(tokens=None), dict(lse=None), dict(g=None), dict(gl=ptr(2))])
+                                    dict(tokens=None), dict(lse=None), dict(g=None), dict(gl=ptr(2)),
+                                    dict(dh=ptr()), dict(dw=ptr(16)), dict(dw=ptr()), dict(dh=ptr(16)), dict(dw=ptr(128))])
 def test_backward_refuses_pointers(lib, change):
     assert lib.streamkl_vocab_xent_bwd(*{**BWD, "shape": shape(), **change}.values(), None) == K.ERR_INVALID
 
