@@ -191,6 +191,25 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return pack_bf16(lo, hi);
 }
 
+// Element `at` of 32 registers, or of 64: one select each, by the index's bits.
+__device__ __forceinline__ float pick(const uint32_t (&s)[32], int at) {
+  uint32_t t[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) t[k] = at & 16 ? s[k + 16] : s[k];
+#pragma unroll
+  for (int half = 8; half; half /= 2) {
+#pragma unroll
+    for (int k = 0; k < half; ++k) t[k] = at & half ? t[k + half] : t[k];
+  }
+  return __uint_as_float(t[0]);
+}
+__device__ __forceinline__ float pick(const uint32_t (&s0)[32], const uint32_t (&s1)[32], int at) {
+  uint32_t t[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) t[k] = at & 32 ? s1[k] : s0[k];
+  return pick(t, at);
+}
+
 // instruction descriptor of a pair's tile
 template <bool HALF>
 __device__ __forceinline__ uint32_t pair_idesc(bool a_mn, bool b_mn, int width) {
@@ -396,11 +415,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int seen = min(p.V - col0, here_cols);
         const long long at = token - col0;
         if (__any_sync(0xffffffffu, at >= 0 && at < min(128, seen))) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const uint32_t z = at == k ? s0[k] : at == k + 32 ? s1[k] : at == k + 64 ? s2[k] : s3[k];
-            if (at >= 0 && at < seen && (at & 31) == k && at < 128) p.given[row] = __uint_as_float(z) * p.c;
-          }
+          const float z = at & 64 ? pick(s2, s3, (int)at) : pick(s0, s1, (int)at);
+          if (at >= 0 && at < min(128, seen)) p.given[row] = z * p.c;
         }
         if (seen < 128) {
 #pragma unroll
@@ -411,29 +427,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (k + 96 >= seen) s3[k] = __float_as_uint(kNegInf);
           }
         }
-        float mx = kNegInf;
+        // Four chains of maxima and of sums, and the given token's logit by selects (a test of each of 128 for it held one tile in
+        // two up): 4096 x 32000 x 256 88 -> 68 us, x 512 98 -> 81, 4096 x 50257 x 1024 244 -> 226; with less than 8 chunks a
+        // tile the exponentials, 2048 cycles, and the way from tile to tile bound it.  (A quarter of them as polynomials: slower.)
+        float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          mx = fmax3(mx, __uint_as_float(s0[k]), __uint_as_float(s1[k]));
-          mx = fmax3(mx, __uint_as_float(s2[k]), __uint_as_float(s3[k]));
+        for (int k = 0; k < 32; k += 2) {
+          top[0] = fmax3(top[0], __uint_as_float(s0[k]), __uint_as_float(s0[k + 1]));
+          top[1] = fmax3(top[1], __uint_as_float(s1[k]), __uint_as_float(s1[k + 1]));
+          top[2] = fmax3(top[2], __uint_as_float(s2[k]), __uint_as_float(s2[k + 1]));
+          top[3] = fmax3(top[3], __uint_as_float(s3[k]), __uint_as_float(s3[k + 1]));
         }
+        const float mx = fmax3(fmaxf(top[0], top[1]), top[2], top[3]);
         const float m = mx * p.c;
         // (m, not mx: a logit near the type's lowest value is -inf in these units)
         const float2 cc = make_float2(p.c, p.c), nm = m == kNegInf ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0, l2 = l0, l3 = l0;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const uint32_t* s = h == 0 ? s0 : h == 1 ? s1 : h == 2 ? s2 : s3;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float2 x0 = ffma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
-            const float2 x1 = ffma2(make_float2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), cc, nm);
-            l0 = fadd2(l0, make_float2(ex2(x0.x), ex2(x0.y)));
-            l1 = fadd2(l1, make_float2(ex2(x1.x), ex2(x1.y)));
-          }
+        for (int k = 0; k < 32; k += 2) {
+          auto two = [&](const uint32_t (&s)[32]) { return ffma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm); };
+          const float2 x0 = two(s0), x1 = two(s1), x2 = two(s2), x3 = two(s3);
+          l0 = fadd2(l0, make_float2(ex2(x0.x), ex2(x0.y)));
+          l1 = fadd2(l1, make_float2(ex2(x1.x), ex2(x1.y)));
+          l2 = fadd2(l2, make_float2(ex2(x2.x), ex2(x2.y)));
+          l3 = fadd2(l3, make_float2(ex2(x3.x), ex2(x3.y)));
         }
-        l0 = fadd2(l0, l1);
-        if (real) p.part[(size_t)(2 * t.n + half) * p.part_rows + row] = make_float2(m, l0.x + l0.y);
+        const float2 l = fadd2(fadd2(l0, l1), fadd2(l2, l3));
+        if (real) p.part[(size_t)(2 * t.n + half) * p.part_rows + row] = make_float2(m, l.x + l.y);
       } else if constexpr (KIND == kGradLogits) {
         const bool real = row < p.R;
         long long at = -1;
