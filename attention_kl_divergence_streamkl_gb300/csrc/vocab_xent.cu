@@ -789,10 +789,12 @@ bool operand_map(CUtensorMap* map, const void* base, long long rows, long long c
 
 // The vocabulary's pieces.  A piece's d lies in memory between the two launches: at most kPieceBytes of it, but at least
 // kPieceColumns, so that the sums of dh, read and written once a piece (8 bytes for 6 V / pieces operations), stay below
-// a few hundredths of the products' time.  Measured, gradients of 4096 x 131072 x 2048 and 8192 x 131072 x 4096, us: 64 MB
-// 3956, 15694; 128 MB 3864, 15723; 256 MB 3756, 15331; 512 MB 3745, 15367 -- each launch ends with a wave that is not full.
+// a few hundredths of the products' time.  Each launch ends with a wave that is not full, and no piece that is worth its
+// launches stays in the L2.  Measured, us, gradients of 4096 x 131072 x 2048 and 8192 x 131072 x 4096: 64 MB 3956, 15694; 128 MB
+// 3864, 15723; 256 MB 3756, 15331; 512 MB 3745, 15367; of 4096 x 65536 x 256 and 16384 x 50257 x 1024: 256 MB 407, 3440; 512 MB
+// 369, 3145; 1 GB 369, 3117.
 constexpr long long kLine = 64;  // rows of d begin on whole lines: a box's row is then one request to the L2, not two
-constexpr long long kPieceBytes = 256ll << 20, kPieceColumns = 8192;
+constexpr long long kPieceBytes = 512ll << 20, kPieceColumns = 8192;
 XentBwdPlan xent_bwd_plan(const XentProblem& p, bool want_dh, bool want_dw, int num_sms) {
   XentBwdPlan g{};
   const long long most = std::max(kPieceColumns, kPieceBytes / (2 * std::max(p.R, 1ll)));

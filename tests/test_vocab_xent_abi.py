@@ -94,12 +94,12 @@ def test_no_rows_is_no_work(lib):
 @pytest.mark.parametrize("rows,vocab,channels", [(1, 1, 8), (8, 131072, 4096), (333, 50021, 1000), (8192, 131072, 4096),
                                                  (1 << 20, 131072, 4096), (9000, 17001, 64), (4096, 1 << 20, 8192)])
 def test_plan(rows, vocab, channels):
-    """A piece of d is at most 256 MB or 8192 columns, the pieces cover the vocabulary, and the sums of dhidden are split
+    """A piece of d is at most 512 MB or 8192 columns, the pieces cover the vocabulary, and the sums of dhidden are split
     only where its tiles are too few."""
     B.build()
     pieces, splits, nbytes = skl.vocab_xent_plan(rows, vocab, channels, 152)
     columns = -(-vocab // pieces)
-    assert pieces >= 1 and (columns <= 8192 or 2 * rows * columns <= 1 << 28)
+    assert pieces >= 1 and (columns <= 8192 or 2 * rows * columns <= 1 << 29)
     tiles = -(-rows // 256) * -(-channels // 256)
     assert splits == 1 or splits * tiles <= 76
     _, _, without = skl.vocab_xent_plan(rows, vocab, channels, 152, want_dhidden=False)
