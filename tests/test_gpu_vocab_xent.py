@@ -151,6 +151,20 @@ def test_tokens_that_are_none():
     assert not bool(dh.any()) and not bool(dw.any())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_column_may_be_the_given_one(dtype):
+    """Each column of the vocabulary is some row's token, at every place of a tile, whole and narrower ones."""
+    V = 771
+    h, w, _ = inputs(V, 64, V, dtype, 21)
+    check(h, w, torch.arange(V, device="cuda"), gl=True)
+    check(h, w, torch.arange(V, device="cuda").flip(0))
+    R, C, V = 100, 1024, 20000
+    assert skl.vocab_xent_fwd_plan(R, V, C, 152)[0] < 256
+    h, w, _ = inputs(R, C, V, dtype, 22)
+    for first in (0, 100, 200, 300, 19900):
+        check(h, w, torch.arange(first, first + R, device="cuda"))
+
+
 def test_tokens_past_the_vocabulary():
     h, w, t = inputs(70, 64, 300, "bf16", 6, none=0.0)
     t[7], t[9] = 300, 2 ** 40
