@@ -16,7 +16,7 @@
 // Backward: the vocabulary goes by in pieces.  A piece's d (2 bytes, rows x columns) is written once by the first
 // launch; the second reads it for both gradients: a piece's rows of dW are complete, the sum for dh goes on from piece
 // to piece in fp32.  d is rounded to the inputs' type, as the other operand of the products that it enters is: half a
-// step of each term.  In fp16 it is multiplied by a power of two that brings the largest upstream gradient to 2^14, for
+// step of each term.  In fp16 it is multiplied by a power of two that brings the largest upstream gradient in use to 2^14, for
 // p's small values would be lost below 2^-24 otherwise.
 // A row without a gradient has d = 0 whatever its logits are, but 0 * NaN would still reach dW through the product: the first
 // launch notes rows without a gradient whose logits are not finite, and where there are any, dW is formed with a copy of the
@@ -661,13 +661,20 @@ __global__ void __launch_bounds__(kJoinThreads)
   loss[row] = token < 0 ? 0.f : token >= V ? __int_as_float(0x7fc00000) : fmaf(m - given[row], kLn2, log_sum);
 }
 
-// fp16: the power of two that brings the largest |scale g| to [2^13, 2^14), and its inverse.
-__global__ void __launch_bounds__(1024) xent_power_kernel(long long R, float scale, const float* __restrict__ g,
-                                                          const float* __restrict__ g_lse, float* __restrict__ power) {
+// fp16: the power of two that brings the largest scale (|g| + |g'|) to [2^13, 2^14), and its inverse.  Of what d is made of: g
+// only where the row has a token, and only finite values (one that is not leaves the other rows' digits alone).
+__global__ void __launch_bounds__(1024)
+    xent_power_kernel(long long R, int V, float scale, const long long* __restrict__ tokens, const float* __restrict__ g,
+                      const float* __restrict__ g_lse, float* __restrict__ power) {
   __shared__ float warp_max[32];
   let_next_begin();
   float mx = 0.f;
-  for (long long i = threadIdx.x; i < R; i += 1024) mx = fmaxf(mx, scale * (fabsf(g[i]) + (g_lse ? fabsf(g_lse[i]) : 0.f)));
+  for (long long i = threadIdx.x; i < R; i += 1024) {
+    const long long token = tokens[i];
+    const float of_loss = fabsf(g[i]), of_lse = g_lse ? fabsf(g_lse[i]) : 0.f;
+    const float x = scale * ((token >= 0 && token < V ? of_loss : 0.f) + of_lse);
+    if (x < __int_as_float(0x7f800000)) mx = fmaxf(mx, x);
+  }
 #pragma unroll
   for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = mx;
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(1024) xent_power_kernel(long long R, float sca
   if (threadIdx.x) return;
   for (int w = 1; w < 32; ++w) mx = fmaxf(mx, warp_max[w]);
   int e = 0;
-  if (mx > 0.f && mx < __int_as_float(0x7f800000)) {
+  if (mx > 0.f) {
     frexpf(mx, &e);  // mx = f 2^e, f in [1/2, 1)
     e = min(max(14 - e, -100), 100);
   }
@@ -859,7 +866,7 @@ cudaError_t launch_xent_bwd(const XentProblem& p, const XentBwdPlan& g, const Xe
   int *clean = reinterpret_cast<int*>(ws + 128), *not_finite = reinterpret_cast<int*>(ws + 256);
   cudaError_t e = cudaSuccess;
   if (p.half) {
-    xent_power_kernel<<<1, 1024, 0, st>>>(p.R, p.scale, in.g, in.g_lse, power);
+    xent_power_kernel<<<1, 1024, 0, st>>>(p.R, (int)p.V, p.scale, in.tokens, in.g, in.g_lse, power);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int m_tiles = tiles_of(p.R, TILE), c_tiles = tiles_of(p.C, TILE);

@@ -482,7 +482,9 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  *     d = scale (g_loss (p - [v = token]) + g_lse p),  p = exp(z - lse)
  *     dhidden = d weight [rows, channels],  dweight = d^T hidden [vocab, channels]
  *   contiguous, of `dtype`, overlapping nothing; one of them may be NULL where it is not wanted.  d enters the
- *   products rounded to `dtype`; sums are fp32, dhidden and dweight are rounded once.  What
+ *   products rounded to `dtype`, in fp16 times one power of two for all rows, which brings the largest finite
+ *   scale (|g_loss| + |g_lse|) to [2^13, 2^14), g_loss counted where the row has a token: entries of d below 2^-38 of
+ *   the largest row's gradient are lost then.  Sums are fp32, dhidden and dweight are rounded once.  What
  *   several blocks add up is added in a fixed order: the same bits on every run.  A row whose
  *   gradients are 0 has dhidden 0 and no part in dweight, whatever its hidden states are, NaN
  *   included; the weight has to be finite.
