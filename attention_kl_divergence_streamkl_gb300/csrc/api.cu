@@ -985,10 +985,11 @@ streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, 
   XentProblem p;
   streamkl_status v = xent_problem(s, &p);
   if (v != STREAMKL_OK) return v;
-  if ((!dhidden && !dweight) || !aligned_to_or_null(dhidden, 16) || !aligned_to_or_null(dweight, 16)) return STREAMKL_ERR_INVALID;
+  if (!aligned_to_or_null(dhidden, 16) || !aligned_to_or_null(dweight, 16)) return STREAMKL_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (p.R == 0)  // an empty sum
+  if (p.R == 0)  // an empty sum, and a dhidden of no rows, which may have no address
     return dweight ? from_cuda(cudaMemsetAsync(dweight, 0, (size_t)p.V * p.C * 2, st)) : STREAMKL_OK;
+  if (!dhidden && !dweight) return STREAMKL_ERR_INVALID;
   if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(tokens, 8) || !rows_ok(lse) || !rows_ok(g_loss) ||
       !aligned_to_or_null(g_lse, 4))
     return STREAMKL_ERR_INVALID;

@@ -481,7 +481,8 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  *   [rows] of the two outputs, and the forward's lse:
  *     d = scale (g_loss (p - [v = token]) + g_lse p),  p = exp(z - lse)
  *     dhidden = d weight [rows, channels],  dweight = d^T hidden [vocab, channels]
- *   contiguous, of `dtype`, overlapping nothing; one of them may be NULL where it is not wanted.  d enters the
+ *   contiguous, of `dtype`, overlapping nothing; one of them may be NULL where it is not wanted (with no rows
+ *   dhidden is empty and may be NULL too; dweight is 0).  d enters the
  *   products rounded to `dtype`, in fp16 times one power of two for all rows, which brings the largest finite
  *   scale (|g_loss| + |g_lse|) to [2^13, 2^14), g_loss counted where the row has a token: entries of d below 2^-38 of
  *   the largest row's gradient are lost then.  Sums are fp32, dhidden and dweight are rounded once.  What
