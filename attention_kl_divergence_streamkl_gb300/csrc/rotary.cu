@@ -4,9 +4,10 @@
 // back: -sin for sin.
 //
 // The angle is kept as a fraction of a turn in 64 bits of fixed point: turns_i = 2^64 f_i / 2 pi, so p turns_i mod 2^64 is
-// the angle mod a turn, for any 64-bit position, to p 2^-64 of a turn -- where p f_i in fp32 would be off by 0.06 at
-// a position of a million.  The two highest bits, rounded, are the quadrant; the rest, at most an eighth of a turn, goes
-// through the Taylor series of sin and cos, whose first left-out terms are below 2^-28 and 2^-32.
+// the angle mod a turn, for any 64-bit position, to the |p| 2^-65 of a turn that rounding f_i to 2^-64 leaves -- where p f_i in
+// fp32 would be off by 0.06 radians at a position of a million.  Sine and cosine are taken of the product's upper 32 bits, so of an
+// angle that is less than 2^-32 of a turn too small.  The two highest bits, rounded, are the quadrant; the rest, at most an eighth
+// of a turn, goes through the Taylor series of sin and cos, whose first left-out terms are below 2^-28 and 2^-32.
 //
 // A thread has one 16-byte vector of a row's pairs (HALF: one of either half) at one position, takes its sines and
 // cosines once, and then goes through up to four heads of q and k, all of them loaded before the first angle is known.
@@ -52,7 +53,8 @@ __device__ __forceinline__ T one_of(float x) {
   if constexpr (std::is_same<T, float>::value) return x;
 }
 
-// sin and cos of `turn` / 2^64 of a turn.  The angle's highest 32 bits are enough: 2^-32 of a turn is 1.5e-9.
+// sin and cos of `turn` / 2^64 of a turn.  The angle's highest 32 bits are enough: 2^-32 of a turn is 1.5e-9 radians, a twentieth of
+// fp32's half step at 1.
 __device__ __forceinline__ void sincos_of_turn(unsigned long long turn, float* sin_out, float* cos_out) {
   const unsigned t = (unsigned)(turn >> 32), quarter = (t + (1u << 29)) >> 30;  // the nearest
   const int rest = (int)(t - (quarter << 30));                                  // within 2^29

@@ -522,7 +522,8 @@ streamkl_status streamkl_vocab_xent_bwd(const void* hidden, const void* weight, 
  *   copied.  Pair i is the channels i and dim / 2 + i, with `interleaved` 2 i and 2 i + 1.
  * A row at position p: (x, y) -> amplitude (x cos a - y sin a, y cos a + x sin a), a = p turns[i]
  *   2^-64 of a turn: turns [dim / 2], device, 2^64 f_i / 2 pi mod 2^64 for a frequency of f_i radians
- *   a position.  The angle is exact to |p| 2^-64 turns for any 64-bit p, negative ones too.
+ *   a position.  For any 64-bit p, negative ones too, the angle is within 2^-32 turns (1.5e-9 radians) of p turns[i], whose
+ *   own rounding is |p| 2^-65 turns.
  *   Arithmetic is fp32, results are rounded once.
  * positions: device, 32-bit or 64-bit integers (positions_bytes), sequence b's N of them from element
  *   b positions_stride on (stride 0: the same for all); NULL: row n is at offset + n.
