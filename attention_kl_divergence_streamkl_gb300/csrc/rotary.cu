@@ -13,6 +13,7 @@
 // cosines once, and then goes through up to four heads of q and k, all of them loaded before the first angle is known.
 // Bound by HBM's latency and rate for many rows, by the launch for few.  Measured: B2 H32 HK8 N4096 D128 bf16 29.5 us, 5.7
 // TB/s of 6.8 (37 with eight heads a thread, two at a time, and 43 with values taken apart one by one); fp32 52.5 us, 6.4 TB/s.
+// Without 16-byte granules one element (a pair, interleaved) is moved at a time: D80 with 20 that turn 56 us, 1.9 TB/s (36).
 #include "common.cuh"
 #include "kernels.h"
 

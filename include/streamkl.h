@@ -485,7 +485,9 @@ streamkl_status streamkl_logprobs_bwd(const void* logits, int dtype, long long r
  *   dhidden is empty and may be NULL too; dweight is 0).  d enters the
  *   products rounded to `dtype`, in fp16 times one power of two for all rows, which brings the largest finite
  *   scale (|g_loss| + |g_lse|) to [2^13, 2^14), g_loss counted where the row has a token: entries of d below 2^-38 of
- *   the largest row's gradient are lost then.  Sums are fp32, dhidden and dweight are rounded once.  What
+ *   the largest row's gradient are lost then.  p is formed from lse as it is stored: far from 0 the roundings of
+ *   lse, and of z and lse in units of log 2, move it by up to 8 max(|z|, |lse|) 2^-24 of itself.  Sums are fp32,
+ *   dhidden and dweight are rounded once.  What
  *   several blocks add up is added in a fixed order: the same bits on every run.  A row whose
  *   gradients are 0 has dhidden 0 and no part in dweight, whatever its hidden states are, NaN
  *   included; the weight has to be finite.
