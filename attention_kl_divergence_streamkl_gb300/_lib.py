@@ -718,8 +718,8 @@ def diff_attn_bwd(q, k, v, lam, maps, lse, do, dlse=None, scale=None, causal=Fal
     """Differential attention's gradients (dq, dk, dv, dlam): bf16 with the layouts of q, k, v, and fp32 [B, H, N_Q], a value
     for each row whatever shape lam has.
 
-    maps, lse, maps_rest: diff_attn_fwd's for the same inputs (return_maps); do: dLoss/dd like d; dlse: dLoss/dlse fp32
-    [B, 2 H, N_Q] or None.  bwd_mode as in attn_bwd.
+    maps, lse, maps_rest: diff_attn_fwd's for the same inputs (return_maps), whose 16 bits dlam is as exact as; do: dLoss/dd
+    like d; dlse: dLoss/dlse fp32 [B, 2 H, N_Q] or None.  bwd_mode as in attn_bwd.
     """
     if bwd_mode == BWD_AUTO and torch.are_deterministic_algorithms_enabled():
         bwd_mode = BWD_SEPARATE

@@ -395,9 +395,10 @@ streamkl_status streamkl_attn_bwd(const void* q, const void* k, const void* v, c
  *   result and what its rounding left, bf16 [B, H, N_Q, D] with the strides o_stride_*.
  * Backward: go = dLoss/dd with d's strides, dlse (or NULL) fp32 [B, H, N_Q]; maps and o_rest are
  *   required.  dq, dk, dv as in streamkl_attn_bwd; dlam fp32 [B, H / 2, N_Q] contiguous, a value
- *   for every row whatever lam's strides are.  |lam| is part of the second map's weights, which enter
- *   the products rounded to bf16 as the first's do; with dlse, where |lam| is below 1/64, it multiplies
- *   dO instead, rounded to bf16.  bwd_mode as in streamkl_attn_bwd.
+ *   for every row whatever lam's strides are, as exact as the second map's two parts: each term dO O2 to 2^-16 of
+ *   itself.  |lam| is part of the second map's weights, which enter the products rounded to bf16 as the
+ *   first's do; with dlse, where |lam| is below 1/64, it multiplies dO instead, rounded to bf16.
+ *   bwd_mode as in streamkl_attn_bwd.
  * Workspaces as in streamkl_attn_fwd and streamkl_attn_bwd; the backward's also has the maps' gradients,
  *   2 D bytes per query row of both.  streamkl_diff_attn_fwd_plan: packed, splits and the workspace for any SM count
  *   (num_sms <= 0: the current device; with num_sms > 0 a pure host rule).
